@@ -531,7 +531,7 @@ def _exact_evict(raw, c):
             blocks = sorted(fixed | set(rest[: max(0, keep - len(fixed))]))
             rows, at = [], []
             for i, j in enumerate(blocks):
-                left = t - BLOCK * j if i + 1 == len(blocks) else 4 * BLOCK
+                left = t - BLOCK * (n - len(blocks)) - BLOCK * i
                 for w in range(4):
                     if 16 * w + 32 <= left:
                         rows.append((4 * j + w, i, w < 3 or (i + 1 < len(blocks) and blocks[i + 1] == j + 1)))
