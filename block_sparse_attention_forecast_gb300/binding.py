@@ -28,6 +28,9 @@ __all__ = [
     "sparda_prefill_forecast_select", "sparda_prefill_multihead_select", "sparda_prefill_attn",
     "sparda_prefetch_blocks_cached", "sparda_sparse_decode_attn_cached", "BlockCache",
     "sparda_prefetch_blocks_copy_engine",
+    "LayerKV4", "sparda_kv4_quantize", "sparda_kv4_dequantize", "sparda_kv4_append", "sparda_kv4_decode_attn",
+    "sparda_sparse_decode_attn_mass", "sparda_evict_blocks", "sparda_kv4_evict_blocks", "KV4_BLOCK_BYTES",
+    "WS_ATTN_MASS", "WS_KV4_ATTN", "WS_KV4_ATTN_MASS",
     "OK", "ERR_INVALID_ARG", "ERR_UNSUPPORTED_SHAPE", "ERR_MISALIGNED", "ERR_NOT_MAPPED_HOST",
     "ERR_WORKSPACE_TOO_SMALL", "ERR_CUDA", "ERR_STATIC_SCRATCH_LIMIT", "DEV_WAIT_TIMEOUT", "DEV_BAD_SEQ_LEN", "DEV_BAD_INDEX",
     "WS_SELECT", "WS_ATTN", "WS_MULTIHEAD", "WS_PREFILL", "BLOCK", "WIN_KERNEL", "WIN_STRIDE",
@@ -55,6 +58,11 @@ WS_SELECT = 1
 WS_ATTN = 2
 WS_MULTIHEAD = 3
 WS_PREFILL = 4
+WS_ATTN_MASS = 5
+WS_KV4_ATTN = 6
+WS_KV4_ATTN_MASS = 7
+
+KV4_BLOCK_BYTES = 10240     # one 64-token block of the 4-bit cache, keys and values
 
 BLOCK = 64
 WIN_KERNEL = 32
@@ -79,6 +87,10 @@ class c_layer_kv(ctypes.Structure):
                 ("on_host", ctypes.c_int32), ("reserved", ctypes.c_int32)]
 
 
+class c_layer_kv4(ctypes.Structure):
+    _fields_ = [("kv", ctypes.c_void_p), ("ck", ctypes.c_void_p)]
+
+
 def _load():
     if not os.path.exists(LIB_PATH):
         raise ImportError(
@@ -87,6 +99,7 @@ def _load():
     lib = ctypes.CDLL(LIB_PATH)
     P, I32, SZ = ctypes.c_void_p, ctypes.c_int32, ctypes.c_size_t
     SH, LY = ctypes.POINTER(c_shape), ctypes.POINTER(c_layer_kv)
+    L4 = ctypes.POINTER(c_layer_kv4)
     sig = {
         "sparda_abi_version": (I32, []),
         "sparda_status_string": (ctypes.c_char_p, [I32]),
@@ -115,6 +128,13 @@ def _load():
         "sparda_prefetch_blocks_cached": (I32, [SH, LY, P, P, P, I32, P, P, P, I32, P, P, P, I32, P]),
         "sparda_prefetch_blocks_copy_engine": (I32, [SH, LY, P, P, P, I32, P, P, P, P]),
         "sparda_sparse_decode_attn_cached": (I32, [SH, LY, P, P, I32, P, P, P, P, P, I32, P, P, SZ, P]),
+        "sparda_kv4_quantize": (I32, [SH, L4, P, P, P, I32, P]),
+        "sparda_kv4_dequantize": (I32, [SH, L4, P, P, P, I32, P, P, P]),
+        "sparda_kv4_append": (I32, [SH, L4, P, P, P, I32, P]),
+        "sparda_kv4_decode_attn": (I32, [SH, L4, P, P, P, P, I32, P, P, P, SZ, P]),
+        "sparda_sparse_decode_attn_mass": (I32, [SH, LY, P, P, P, P, I32, P, P, P, SZ, P]),
+        "sparda_evict_blocks": (I32, [SH, LY, P, P, SH, LY, P, P, I32, I32, I32, P, P]),
+        "sparda_kv4_evict_blocks": (I32, [SH, L4, P, P, SH, L4, P, P, I32, I32, I32, P, P]),
     }
     for name, (res, args) in sig.items():
         fn = getattr(lib, name)
@@ -222,6 +242,26 @@ class LayerKV:
             hk = hv = None
         ck = torch.zeros((shape.max_batch, G, shape.w_cap, d), dtype=torch.bfloat16, device=device)
         return LayerKV(k, v, ck, hk, hv, on_host)
+
+
+@dataclass
+class LayerKV4:
+    """One layer's cache in 4 bits (sparda_layer_kv4), as torch tensors on the device.
+
+    kv: uint8 [max_batch, G, max_ctx / 64, KV4_BLOCK_BYTES]. ck: bf16 [max_batch, G, w_cap, d].
+    """
+    kv: torch.Tensor
+    ck: torch.Tensor
+
+    def c(self):
+        return c_layer_kv4(self.kv.data_ptr(), self.ck.data_ptr())
+
+    @staticmethod
+    def empty(shape, device="cuda"):
+        B, G = shape.max_batch, shape.n_groups
+        kv = torch.empty((B, G, shape.max_ctx // shape.block, KV4_BLOCK_BYTES), dtype=torch.uint8, device=device)
+        ck = torch.zeros((B, G, shape.w_cap, shape.head_dim), dtype=torch.bfloat16, device=device)
+        return LayerKV4(kv, ck)
 
 
 def hot_slot(j):
@@ -462,3 +502,144 @@ def sparda_prefetch_blocks_copy_engine(shape, layer, idx_host, cnt_host, seq_len
         ctypes.c_void_p(cnt_host.data_ptr()), ctypes.c_void_p(seq_len_host.data_ptr()), int(batch),
         _ptr(staging_k), _ptr(staging_v), ctypes.byref(n), _stream(stream)))
     return n.value
+
+
+# ------------------------------------------------------------------ the 4-bit cache, block mass, eviction
+def _checked(what, t, dtype, n, device):
+    """t's address, if it is a contiguous tensor of `dtype` on `device` with at least n elements."""
+    if t.dtype != dtype or t.device != device or t.numel() < n or not t.is_contiguous():
+        raise ValueError("%s: a contiguous %s tensor of at least %d elements on %s is wanted, got %s %s on %s%s" % (
+            what, dtype, n, device, t.dtype, tuple(t.shape), t.device, "" if t.is_contiguous() else ", strided"))
+    return t.data_ptr()
+
+
+def _cache_device(t):
+    """The device of a layer's cache, which has to be the current one (the call's stream and the
+    library's device state are its)."""
+    if t.device.type != "cuda" or t.device.index != torch.cuda.current_device():
+        raise ValueError("the layer's cache is on %s; the current device is cuda:%d" % (t.device, torch.cuda.current_device()))
+    return t.device
+
+
+def _kv4_dims(shape, layer, batch):
+    """(device, B, G, d, ctx, c_layer) of a call on a 4-bit cache, its tensors checked."""
+    dev = _cache_device(layer.kv)
+    B, G, d, ctx = int(batch), shape.n_groups, shape.head_dim, shape.max_ctx
+    c = c_layer_kv4(
+        _checked("kv", layer.kv, torch.uint8, shape.max_batch * G * (ctx // BLOCK) * KV4_BLOCK_BYTES, dev),
+        _checked("ck", layer.ck, torch.bfloat16, shape.max_batch * G * shape.w_cap * d, dev))
+    return dev, B, G, d, ctx, c
+
+
+def _selection_ptrs(shape, idx, cnt, B, G, dev):
+    if idx is None and cnt is None:
+        return None, None
+    if idx is None or cnt is None:
+        raise ValueError("idx and cnt come together")
+    return _checked("idx", idx, torch.int32, B * G * shape.kslots, dev), _checked("cnt", cnt, torch.int32, B * G, dev)
+
+
+def sparda_kv4_quantize(shape, layer, k, v, seq_len, batch, stream=None):
+    """Tokens 0 .. seq_len[b]-1 of k and v (bf16 [max_batch, G, max_ctx, d]) into a LayerKV4."""
+    dev, B, G, d, ctx, lc = _kv4_dims(shape, layer, batch)
+    n = shape.max_batch * G * ctx * d
+    _check("sparda_kv4_quantize", lib.sparda_kv4_quantize(
+        ctypes.byref(shape.c()), ctypes.byref(lc), _checked("k", k, torch.bfloat16, n, dev),
+        _checked("v", v, torch.bfloat16, n, dev), _checked("seq_len", seq_len, torch.int32, B, dev), B, _stream(stream)))
+
+
+def sparda_kv4_dequantize(shape, layer, seq_len, batch, k, v, idx=None, cnt=None, stream=None):
+    """The values of a LayerKV4 as bf16: every token's rows into k and v [max_batch, G, max_ctx, d], or
+    with idx and cnt the selected blocks' into staging buffers [max_batch, G, topk+2, 64, d]."""
+    dev, B, G, d, ctx, lc = _kv4_dims(shape, layer, batch)
+    pi, pc = _selection_ptrs(shape, idx, cnt, B, G, dev)
+    n = shape.max_batch * G * (ctx if pi is None else shape.kslots * BLOCK) * d
+    _check("sparda_kv4_dequantize", lib.sparda_kv4_dequantize(
+        ctypes.byref(shape.c()), ctypes.byref(lc), pi, pc, _checked("seq_len", seq_len, torch.int32, B, dev), B,
+        _checked("k", k, torch.bfloat16, n, dev), _checked("v", v, torch.bfloat16, n, dev), _stream(stream)))
+
+
+def sparda_kv4_append(shape, layer, k_new, v_new, seq_len, batch, stream=None):
+    """The current token's key and value (bf16 [B, G, d]) into a LayerKV4, with its compressed key."""
+    dev, B, G, d, _, lc = _kv4_dims(shape, layer, batch)
+    _check("sparda_kv4_append", lib.sparda_kv4_append(
+        ctypes.byref(shape.c()), ctypes.byref(lc), _checked("k_new", k_new, torch.bfloat16, B * G * d, dev),
+        _checked("v_new", v_new, torch.bfloat16, B * G * d, dev), _checked("seq_len", seq_len, torch.int32, B, dev), B,
+        _stream(stream)))
+
+
+def sparda_kv4_decode_attn(shape, layer, q, idx, cnt, seq_len, batch, out, ws, mass=None, stream=None):
+    """Decode attention over a LayerKV4: the selected blocks, or with idx = cnt = None every token.
+    mass (float32 [max_batch, G, max_ctx / 64]): the block weights to add to; ws is then a
+    WS_KV4_ATTN_MASS workspace, else a WS_KV4_ATTN one."""
+    dev, B, G, d, ctx, lc = _kv4_dims(shape, layer, batch)
+    n = B * G * shape.heads_per_group * d
+    pi, pc = _selection_ptrs(shape, idx, cnt, B, G, dev)
+    pm = None if mass is None else _checked("mass", mass, torch.float32, B * G * (ctx // BLOCK), dev)
+    _check("sparda_kv4_decode_attn", lib.sparda_kv4_decode_attn(
+        ctypes.byref(shape.c()), ctypes.byref(lc), _checked("q", q, torch.bfloat16, n, dev), pi, pc,
+        _checked("seq_len", seq_len, torch.int32, B, dev), B, _checked("out", out, torch.bfloat16, n, dev), pm,
+        _checked("ws", ws, torch.uint8, 1, dev), ws.numel(), _stream(stream)))
+
+
+def _layer_ptrs(shape, layer):
+    """A resident LayerKV's c struct, its tensors checked."""
+    if layer.on_host:
+        raise ValueError("a resident layer is wanted")
+    dev = _cache_device(layer.k)
+    rows = shape.max_batch * shape.n_groups
+    n = rows * shape.max_ctx * shape.head_dim
+    return dev, c_layer_kv(
+        _checked("k", layer.k, torch.bfloat16, n, dev), _checked("v", layer.v, torch.bfloat16, n, dev),
+        _checked("ck", layer.ck, torch.bfloat16, rows * shape.w_cap * shape.head_dim, dev), None, None, 0, 0)
+
+
+def sparda_sparse_decode_attn_mass(shape, layer, q, idx, cnt, seq_len, batch, out, ws, mass, stream=None):
+    """sparda_sparse_decode_attn of a resident layer that also adds to mass (float32 [max_batch, G,
+    max_ctx / 64]) the attention weight each selected block received. ws: WS_ATTN_MASS."""
+    dev, lc = _layer_ptrs(shape, layer)
+    B, G = int(batch), shape.n_groups
+    n = B * G * shape.heads_per_group * shape.head_dim
+    pi, pc = _selection_ptrs(shape, idx, cnt, B, G, dev)
+    _check("sparda_sparse_decode_attn_mass", lib.sparda_sparse_decode_attn_mass(
+        ctypes.byref(shape.c()), ctypes.byref(lc), _checked("q", q, torch.bfloat16, n, dev), pi, pc,
+        _checked("seq_len", seq_len, torch.int32, B, dev), B, _checked("out", out, torch.bfloat16, n, dev),
+        _checked("mass", mass, torch.float32, B * G * (shape.max_ctx // BLOCK), dev),
+        _checked("ws", ws, torch.uint8, 1, dev), ws.numel(), _stream(stream)))
+
+
+def _evict(fn, ptrs, shape, layer, mass, seq_len, batch, keep, recent, kept, dst_shape, dst, dst_mass, dst_seq_len, stream):
+    dev, lc = ptrs(shape, layer)
+    B, G = int(batch), shape.n_groups
+    ds = dc = pm = pl = None
+    if dst is not None:
+        if dst_shape is None or dst_mass is None or dst_seq_len is None:
+            raise ValueError("dst_shape, dst, dst_mass and dst_seq_len come together")
+        ds, dc = ctypes.byref(dst_shape.c()), ctypes.byref(ptrs(dst_shape, dst)[1])
+        pm = _checked("dst_mass", dst_mass, torch.float32, B * G * (dst_shape.max_ctx // BLOCK), dev)
+        pl = _checked("dst_seq_len", dst_seq_len, torch.int32, B, dev)
+    elif dst_shape is not None or dst_mass is not None or dst_seq_len is not None:
+        raise ValueError("dst_shape, dst, dst_mass and dst_seq_len come together")
+    _check(fn.__name__, fn(
+        ctypes.byref(shape.c()), ctypes.byref(lc), _checked("mass", mass, torch.float32, B * G * (shape.max_ctx // BLOCK), dev),
+        _checked("seq_len", seq_len, torch.int32, B, dev), ds, dc, pm, pl, B, int(keep), int(recent),
+        _checked("kept", kept, torch.int32, B * G * max(0, int(keep)), dev), _stream(stream)))
+
+
+def sparda_evict_blocks(shape, layer, mass, seq_len, batch, keep, recent, kept, dst_shape=None, dst=None,
+                        dst_mass=None, dst_seq_len=None, stream=None):
+    """Cut every sequence of a resident LayerKV to `keep` blocks: block 0, the `recent` newest and those
+    with the largest mass. In place, or into the cache dst with its dst_mass and dst_seq_len. kept
+    (int32 [B, G, keep]) receives the old block numbers."""
+    _evict(lib.sparda_evict_blocks, _layer_ptrs, shape, layer, mass, seq_len, batch, keep, recent, kept, dst_shape, dst,
+           dst_mass, dst_seq_len, stream)
+
+
+def sparda_kv4_evict_blocks(shape, layer, mass, seq_len, batch, keep, recent, kept, dst_shape=None, dst=None,
+                            dst_mass=None, dst_seq_len=None, stream=None):
+    """sparda_evict_blocks of a LayerKV4."""
+    def ptrs(sh, lay):
+        dev, _, _, _, _, lc = _kv4_dims(sh, lay, 1)
+        return dev, lc
+    _evict(lib.sparda_kv4_evict_blocks, ptrs, shape, layer, mass, seq_len, batch, keep, recent, kept, dst_shape, dst,
+           dst_mass, dst_seq_len, stream)

@@ -123,6 +123,15 @@ size_t attn_ml_bytes(const sparda_shape* s) {
 }
 
 
+// Block mass: the attention's statistics of `slots` blocks per (sequence, group), then the final
+// maximum and sum of each head.
+size_t mass_stats_bytes(const sparda_shape* s, int slots) {
+  return round256((size_t)s->max_batch * s->n_groups * slots * 4 * kHeads * sizeof(float2));
+}
+size_t mass_ml_bytes(const sparda_shape* s) {
+  return round256((size_t)s->max_batch * s->n_groups * 2 * kHeads * sizeof(float));
+}
+
 int32_t cuda_status(cudaError_t e) {
   if (e == cudaSuccess) return SPARDA_OK;
   std::fprintf(stderr, "sparda: CUDA error %s\n", cudaGetErrorString(e));
@@ -204,6 +213,23 @@ int32_t layer_status(const sparda_layer_kv* L, bool need_kv) {
   return SPARDA_OK;
 }
 
+// The shape rules of the 4-bit cache: sparda_check_shape's, with 1 to 16 heads per group.
+int32_t kv4_shape_status(const sparda_shape* s) {
+  if (!s) return SPARDA_ERR_INVALID_ARG;
+  if (s->heads_per_group < 1 || s->heads_per_group > kHeads) return SPARDA_ERR_UNSUPPORTED_SHAPE;
+  sparda_shape full = *s;
+  full.heads_per_group = kHeads;
+  return shape_status(&full);
+}
+
+size_t kv4_part_bytes() { return (size_t)kKv4MaxCtas * 2 * (kHeads * kHeadDim + 2 * kHeads) * sizeof(float); }
+int kv4_mass_slots(const sparda_shape* s) { return kslots(s) > nb_cap(s) ? kslots(s) : nb_cap(s); }
+size_t kv4_workspace_bytes(const sparda_shape* s, int32_t batch, int32_t kind) {
+  if (kv4_shape_status(s) != SPARDA_OK || batch < 1 || batch > s->max_batch) return 0;
+  const size_t base = counters_bytes(s) + kv4_part_bytes();
+  return kind == SPARDA_WS_KV4_ATTN ? base : base + mass_stats_bytes(s, kv4_mass_slots(s)) + mass_ml_bytes(s);
+}
+
 #define SPARDA_TRY(x)                     \
   do {                                    \
     const int32_t st_ = (x);              \
@@ -236,10 +262,13 @@ const char* sparda_status_string(int32_t status) {
 int32_t sparda_check_shape(const sparda_shape* shape) { return shape_status(shape); }
 
 size_t sparda_workspace_bytes(const sparda_shape* s, int32_t batch, int32_t kind) {
+  if (kind == SPARDA_WS_KV4_ATTN || kind == SPARDA_WS_KV4_ATTN_MASS) return kv4_workspace_bytes(s, batch, kind);
   if (shape_status(s) != SPARDA_OK || batch < 1 || batch > s->max_batch) return 0;
   switch (kind) {
     case SPARDA_WS_SELECT: return kQueueBytes + counters_bytes(s) + select_data_bytes(s);
     case SPARDA_WS_ATTN: return counters_bytes(s) + attn_o_bytes(s) + attn_ml_bytes(s);
+    case SPARDA_WS_ATTN_MASS:
+      return sparda_workspace_bytes(s, batch, SPARDA_WS_ATTN) + mass_stats_bytes(s, kslots(s)) + mass_ml_bytes(s);
     case SPARDA_WS_MULTIHEAD: return select_data_bytes(s);
     case SPARDA_WS_PREFILL: return round256((size_t)s->max_batch * s->n_groups * nb_cap(s) * nb_cap(s) * sizeof(float));
     default: return 0;
@@ -731,6 +760,229 @@ int32_t sparda_prefetch_blocks_copy_engine(const sparda_shape* s, const sparda_l
   }
   if (n_copies) *n_copies = copies;
   return SPARDA_OK;
+}
+
+}  // extern "C"
+
+// ------------------------------------------------------------------ the 4-bit KV cache
+namespace {
+
+int32_t kv4_layer_status(const sparda_layer_kv4* L, bool need_ck) {
+  if (!L || !L->kv || (need_ck && !L->ck)) return SPARDA_ERR_INVALID_ARG;
+  return aligned(L->kv, 16) && aligned(L->ck, 16) ? SPARDA_OK : SPARDA_ERR_MISALIGNED;
+}
+
+// The checks and arguments that the calls writing or reading the 4-bit cache share.
+int32_t prepare_kv4_cache(const sparda_shape* s, const sparda_layer_kv4* L, bool need_ck, const void* k, const void* v,
+                          const int32_t* seq_len, int32_t batch, Kv4CacheArgs* a) {
+  SPARDA_TRY(kv4_shape_status(s));
+  SPARDA_TRY(batch_status(s, batch));
+  SPARDA_TRY(kv4_layer_status(L, need_ck));
+  if (!k || !v || !seq_len) return SPARDA_ERR_INVALID_ARG;
+  if (!aligned(k, 16) || !aligned(v, 16) || !aligned(seq_len, 4)) return SPARDA_ERR_MISALIGNED;
+  int* err = dev_error_ptr();
+  if (!err) return SPARDA_ERR_CUDA;
+  *a = Kv4CacheArgs{};
+  a->kv = static_cast<uint8_t*>(L->kv);
+  a->ck = static_cast<__nv_bfloat16*>(L->ck);
+  a->seq_len = seq_len;
+  a->err = err;
+  a->G = s->n_groups;
+  a->max_ctx = s->max_ctx;
+  a->nb_cap = nb_cap(s);
+  a->W_cap = w_cap(s);
+  a->kslots = kslots(s);
+  return SPARDA_OK;
+}
+
+}  // namespace
+
+extern "C" {
+
+int32_t sparda_kv4_quantize(const sparda_shape* s, const sparda_layer_kv4* L, const void* k, const void* v,
+                            const int32_t* seq_len, int32_t batch, void* stream) {
+  Kv4CacheArgs a;
+  SPARDA_TRY(prepare_kv4_cache(s, L, false, k, v, seq_len, batch, &a));
+  a.k = static_cast<const __nv_bfloat16*>(k);
+  a.v = static_cast<const __nv_bfloat16*>(v);
+  launch_kv4_quantize(a, batch * s->n_groups, static_cast<cudaStream_t>(stream));
+  return cuda_status(cudaGetLastError());
+}
+
+int32_t sparda_kv4_dequantize(const sparda_shape* s, const sparda_layer_kv4* L, const int32_t* idx, const int32_t* cnt,
+                              const int32_t* seq_len, int32_t batch, void* k, void* v, void* stream) {
+  if ((idx == nullptr) != (cnt == nullptr)) return SPARDA_ERR_INVALID_ARG;
+  if (!aligned(idx, 4) || !aligned(cnt, 4)) return SPARDA_ERR_MISALIGNED;
+  Kv4CacheArgs a;
+  SPARDA_TRY(prepare_kv4_cache(s, L, false, k, v, seq_len, batch, &a));
+  a.idx = idx;
+  a.cnt = cnt;
+  a.k_out = static_cast<__nv_bfloat16*>(k);
+  a.v_out = static_cast<__nv_bfloat16*>(v);
+  launch_kv4_dequantize(a, batch * s->n_groups, static_cast<cudaStream_t>(stream));
+  return cuda_status(cudaGetLastError());
+}
+
+int32_t sparda_kv4_append(const sparda_shape* s, const sparda_layer_kv4* L, const void* k_new, const void* v_new,
+                          const int32_t* seq_len, int32_t batch, void* stream) {
+  Kv4CacheArgs a;
+  SPARDA_TRY(prepare_kv4_cache(s, L, true, k_new, v_new, seq_len, batch, &a));
+  a.k = static_cast<const __nv_bfloat16*>(k_new);
+  a.v = static_cast<const __nv_bfloat16*>(v_new);
+  launch_kv4_append(a, batch * s->n_groups, static_cast<cudaStream_t>(stream));
+  return cuda_status(cudaGetLastError());
+}
+
+int32_t sparda_kv4_decode_attn(const sparda_shape* s, const sparda_layer_kv4* L, const void* q, const int32_t* idx,
+                               const int32_t* cnt, const int32_t* seq_len, int32_t batch, void* out, float* mass,
+                               void* ws, size_t ws_bytes, void* stream) {
+  SPARDA_TRY(kv4_shape_status(s));
+  SPARDA_TRY(batch_status(s, batch));
+  SPARDA_TRY(kv4_layer_status(L, false));
+  if (!q || !seq_len || !out || !ws || (idx == nullptr) != (cnt == nullptr)) return SPARDA_ERR_INVALID_ARG;
+  if (!aligned(q, 16) || !aligned(out, 16) || !aligned(ws, 16) || !aligned(idx, 4) || !aligned(cnt, 4) ||
+      !aligned(seq_len, 4) || !aligned(mass, 4))
+    return SPARDA_ERR_MISALIGNED;
+  if (ws_bytes < kv4_workspace_bytes(s, batch, mass ? SPARDA_WS_KV4_ATTN_MASS : SPARDA_WS_KV4_ATTN))
+    return SPARDA_ERR_WORKSPACE_TOO_SMALL;
+  int* err = dev_error_ptr();
+  if (!err) return SPARDA_ERR_CUDA;
+  const cudaStream_t st = static_cast<cudaStream_t>(stream);
+  uint8_t* w = static_cast<uint8_t*>(ws);
+  float* part = reinterpret_cast<float*>(w + counters_bytes(s));
+  uint8_t* stats = w + counters_bytes(s) + kv4_part_bytes();
+  const int slots = idx ? kslots(s) : nb_cap(s);
+  Kv4AttnArgs a{static_cast<const uint8_t*>(L->kv), static_cast<const __nv_bfloat16*>(q), idx, cnt, seq_len,
+                static_cast<__nv_bfloat16*>(out), part, part + (size_t)kKv4MaxCtas * 2 * kHeads * kHeadDim,
+                reinterpret_cast<unsigned*>(w), nullptr, nullptr, err, s->n_groups, s->heads_per_group, s->max_ctx,
+                nb_cap(s), kslots(s), batch * s->n_groups};
+  if (mass) {
+    a.stats = reinterpret_cast<float2*>(stats);
+    a.ml = reinterpret_cast<float*>(stats + mass_stats_bytes(s, kv4_mass_slots(s)));
+  }
+  launch_kv4_attn(a, st);
+  if (mass) {
+    BlockMassArgs m{a.stats, a.ml, mass, idx, cnt, seq_len, s->n_groups, s->heads_per_group, s->max_ctx, nb_cap(s), slots};
+    launch_block_mass(m, batch * s->n_groups, st);
+  }
+  return cuda_status(cudaGetLastError());
+}
+
+// ------------------------------------------------------------------ block mass and eviction
+int32_t sparda_sparse_decode_attn_mass(const sparda_shape* s, const sparda_layer_kv* L, const void* q, const int32_t* idx,
+                                       const int32_t* cnt, const int32_t* seq_len, int32_t batch, void* out, float* mass,
+                                       void* ws, size_t ws_bytes, void* stream) {
+  if (!L || L->on_host || !mass) return SPARDA_ERR_INVALID_ARG;
+  if (!aligned(mass, 4) || !aligned(seq_len, 4)) return SPARDA_ERR_MISALIGNED;
+  if (ws_bytes < sparda_workspace_bytes(s, batch, SPARDA_WS_ATTN_MASS)) return SPARDA_ERR_WORKSPACE_TOO_SMALL;
+  AttnArgs a;
+  CUtensorMap mk, mv, hk, hv;
+  SPARDA_TRY(prepare_attn(s, L, nullptr, nullptr, q, idx, cnt, seq_len, batch, out, ws, ws_bytes, &a, &mk, &mv, &hk, &hv));
+  uint8_t* stats = static_cast<uint8_t*>(ws) + sparda_workspace_bytes(s, batch, SPARDA_WS_ATTN);
+  a.stats = reinterpret_cast<float2*>(stats);
+  a.ml = reinterpret_cast<float*>(stats + mass_stats_bytes(s, kslots(s)));
+  const cudaStream_t st = static_cast<cudaStream_t>(stream);
+  launch_sparse_attn(a, mk, mv, hk, hv, batch * s->n_groups, st);
+  BlockMassArgs m{a.stats, a.ml, mass, idx, cnt, seq_len, s->n_groups, kHeads, s->max_ctx, nb_cap(s), kslots(s)};
+  launch_block_mass(m, batch * s->n_groups, st);
+  return cuda_status(cudaGetLastError());
+}
+
+}  // extern "C"
+
+namespace {
+
+// What both evictions check and hand on beside their cache planes. `in_place`: no dst argument.
+int32_t prepare_evict(const sparda_shape* s, const sparda_shape* d, const void* ck, void* dst_ck, float* mass,
+                      int32_t* seq_len, float* dst_mass, int32_t* dst_seq_len, int32_t batch, int32_t keep,
+                      int32_t recent, int32_t* kept, bool in_place, EvictArgs* a) {
+  SPARDA_TRY(batch_status(s, batch));
+  if (!mass || !seq_len || !kept || recent < 1 || keep <= recent) return SPARDA_ERR_INVALID_ARG;
+  if (keep > kMaxCtx / kBlock) return SPARDA_ERR_UNSUPPORTED_SHAPE;
+  if (in_place) {
+    if (d || dst_mass || dst_seq_len) return SPARDA_ERR_INVALID_ARG;
+    d = s;
+    dst_ck = const_cast<void*>(ck);
+    dst_mass = mass;
+    dst_seq_len = seq_len;
+  } else {
+    if (!d || !dst_mass || !dst_seq_len || dst_mass == mass || dst_seq_len == seq_len || dst_ck == ck)
+      return SPARDA_ERR_INVALID_ARG;
+    if (d->n_groups != s->n_groups || d->max_batch < batch || d->max_ctx / kBlock < keep)
+      return SPARDA_ERR_UNSUPPORTED_SHAPE;
+  }
+  if (!aligned(mass, 4) || !aligned(seq_len, 4) || !aligned(dst_mass, 4) || !aligned(dst_seq_len, 4) || !aligned(kept, 4))
+    return SPARDA_ERR_MISALIGNED;
+  int* err = dev_error_ptr();
+  if (!err) return SPARDA_ERR_CUDA;
+  a->src_ck = static_cast<const __nv_bfloat16*>(ck);
+  a->dst_ck = static_cast<__nv_bfloat16*>(dst_ck);
+  a->src_mass = mass;
+  a->dst_mass = dst_mass;
+  a->src_len = seq_len;
+  a->dst_len = dst_seq_len;
+  a->kept = kept;
+  a->err = err;
+  a->B = batch;
+  a->G = s->n_groups;
+  a->src_nb = nb_cap(s);
+  a->dst_nb = nb_cap(d);
+  a->keep = keep;
+  a->recent = recent;
+  a->in_place = in_place ? 1 : 0;
+  return SPARDA_OK;
+}
+
+}  // namespace
+
+extern "C" {
+
+int32_t sparda_evict_blocks(const sparda_shape* s, const sparda_layer_kv* L, float* mass, int32_t* seq_len,
+                            const sparda_shape* d, const sparda_layer_kv* dst, float* dst_mass, int32_t* dst_seq_len,
+                            int32_t batch, int32_t keep, int32_t recent, int32_t* kept, void* stream) {
+  SPARDA_TRY(shape_status(s));
+  if (!L || L->on_host) return SPARDA_ERR_INVALID_ARG;
+  SPARDA_TRY(layer_status(L, true));
+  if (d) SPARDA_TRY(shape_status(d));
+  if (dst) {
+    if (dst->on_host) return SPARDA_ERR_INVALID_ARG;
+    SPARDA_TRY(layer_status(dst, true));
+    if (dst->k == L->k || dst->v == L->v) return SPARDA_ERR_INVALID_ARG;
+  }
+  EvictArgs a{};
+  SPARDA_TRY(prepare_evict(s, d, L->ck, dst ? dst->ck : nullptr, mass, seq_len, dst_mass, dst_seq_len, batch, keep, recent,
+                           kept, dst == nullptr, &a));
+  a.src[0] = static_cast<const uint8_t*>(L->k);
+  a.src[1] = static_cast<const uint8_t*>(L->v);
+  a.dst[0] = static_cast<uint8_t*>(dst ? dst->k : L->k);
+  a.dst[1] = static_cast<uint8_t*>(dst ? dst->v : L->v);
+  a.planes = 2;
+  a.block_bytes = kBlockBytes;
+  launch_evict(a, static_cast<cudaStream_t>(stream));
+  return cuda_status(cudaGetLastError());
+}
+
+int32_t sparda_kv4_evict_blocks(const sparda_shape* s, const sparda_layer_kv4* L, float* mass, int32_t* seq_len,
+                                const sparda_shape* d, const sparda_layer_kv4* dst, float* dst_mass,
+                                int32_t* dst_seq_len, int32_t batch, int32_t keep, int32_t recent, int32_t* kept,
+                                void* stream) {
+  SPARDA_TRY(kv4_shape_status(s));
+  SPARDA_TRY(kv4_layer_status(L, true));
+  if (d) SPARDA_TRY(kv4_shape_status(d));
+  if (dst) {
+    SPARDA_TRY(kv4_layer_status(dst, true));
+    if (dst->kv == L->kv) return SPARDA_ERR_INVALID_ARG;
+  }
+  EvictArgs a{};
+  SPARDA_TRY(prepare_evict(s, d, L->ck, dst ? dst->ck : nullptr, mass, seq_len, dst_mass, dst_seq_len, batch, keep, recent,
+                           kept, dst == nullptr, &a));
+  a.src[0] = static_cast<const uint8_t*>(L->kv);
+  a.dst[0] = static_cast<uint8_t*>(dst ? dst->kv : L->kv);
+  a.planes = 1;
+  a.block_bytes = SPARDA_KV4_BLOCK_BYTES;
+  a.kv4 = 1;
+  launch_evict(a, static_cast<cudaStream_t>(stream));
+  return cuda_status(cudaGetLastError());
 }
 
 }  // extern "C"

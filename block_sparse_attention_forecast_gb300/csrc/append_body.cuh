@@ -71,6 +71,27 @@ __device__ __forceinline__ uint16_t fixed_mean_to_bf16(long long S) {
   return (uint16_t)(sign + ((uint32_t)(p + 75) << 7) + (m - 128u));
 }
 
+// The mean of 32 bf16 pairs, per half-word, rounded once to bf16: a compression window's
+// compressed key for two channels.
+__device__ __forceinline__ uint32_t window_mean(const uint32_t (&xs)[kWinKernel]) {
+  bool in_range = true;
+  long long S0 = 0, S1 = 0;
+#pragma unroll
+  for (int u = 0; u < kWinKernel; ++u) {
+    S0 += bf16_to_fixed(xs[u] & 0xffffu, in_range);
+    S1 += bf16_to_fixed(xs[u] >> 16, in_range);
+  }
+  if (in_range) return (uint32_t)fixed_mean_to_bf16(S0) | ((uint32_t)fixed_mean_to_bf16(S1) << 16);
+  double s0 = 0.0, s1 = 0.0;
+#pragma unroll
+  for (int u = 0; u < kWinKernel; ++u) {
+    s0 += bf16_lo(xs[u]);
+    s1 += bf16_hi(xs[u]);
+  }
+  const __nv_bfloat16 b0 = f64_to_bf16_rn(s0 / kWinKernel), b1 = f64_to_bf16_rn(s1 / kWinKernel);
+  return (uint32_t)__bfloat16_as_ushort(b0) | ((uint32_t)__bfloat16_as_ushort(b1) << 16);
+}
+
 // The append of sequence-group `bg` by 64 threads; thread t (0..63) owns dims 2t and 2t+1.
 __device__ __forceinline__ void append_token(const AppendArgs& a, int bg, int t) {
   const int b = bg / a.G;

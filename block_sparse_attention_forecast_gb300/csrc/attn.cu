@@ -15,23 +15,25 @@ namespace sparda {
 
 int attn_blocks_per_cta() { return 1; }   // workspace holds up to topk+2 partials per group
 
+template <bool kStats>
 __global__ void __launch_bounds__(kAttnThreads, 1) sparse_attn_kernel(
     const AttnArgs a, const __grid_constant__ CUtensorMap mk, const __grid_constant__ CUtensorMap mv,
     const __grid_constant__ CUtensorMap hk, const __grid_constant__ CUtensorMap hv) {
   SPARDA_TL_ENTRY();
   grid_dep_launch();
   unsigned long long tl_first = 0;
-  attn_cta(a, &mk, &mv, &hk, &hv, blockIdx.x, gridDim.x, &tl_first);
+  attn_cta<false, kStats>(a, &mk, &mv, &hk, &hv, blockIdx.x, gridDim.x, &tl_first);
   SPARDA_TL_EXIT(a.tl_buf, a.tl_launch, kTlAttention, tl_first);
 }
 
+template <bool kStats>
 __global__ void __launch_bounds__(kAttnThreads, 1) sparse_attn_cluster_kernel(
     const AttnArgs a, const __grid_constant__ CUtensorMap mk, const __grid_constant__ CUtensorMap mv,
     const __grid_constant__ CUtensorMap hk, const __grid_constant__ CUtensorMap hv) {
   SPARDA_TL_ENTRY();
   grid_dep_launch();
   unsigned long long tl_first = 0;
-  attn_cta<true>(a, &mk, &mv, &hk, &hv, blockIdx.x, gridDim.x, &tl_first);
+  attn_cta<true, kStats>(a, &mk, &mv, &hk, &hv, blockIdx.x, gridDim.x, &tl_first);
   SPARDA_TL_EXIT(a.tl_buf, a.tl_launch, kTlAttention, tl_first);
 }
 
@@ -73,7 +75,8 @@ void launch_sparse_attn(const AttnArgs& a, const CUtensorMap& mk, const CUtensor
   }
   b.tl_launch = timeline_next_launch();
   b.tl_buf = timeline_buffer();
-  auto kern = cluster ? sparse_attn_cluster_kernel : sparse_attn_kernel;
+  auto kern = a.stats ? (cluster ? sparse_attn_cluster_kernel<true> : sparse_attn_kernel<true>)
+                      : (cluster ? sparse_attn_cluster_kernel<false> : sparse_attn_kernel<false>);
   const int smem = cluster ? kAttnClusterSmem : kAttnSmem;
   cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
   // Programmatic serialization: the barrier set-up overlaps the kernel before it in the

@@ -97,7 +97,9 @@ __device__ __forceinline__ GroupInfo group_info(const AttnArgs& a, int bg) {
 // cluster of seg_per_group CTAs that covers group c / seg_per_group (seg_per_group >= 2), and
 // every thread of the CTA reaches the merge's one cluster barrier. tl_first (timeline
 // build only): thread 0 stores there the time its first block arrived.
-template <bool kClusterMerge = false>
+// kStats: every quarter block's softmax statistics of each head and the final ones are stored
+// too, for the block mass.
+template <bool kClusterMerge = false, bool kStats = false>
 __device__ __forceinline__ void attn_cta(const AttnArgs& a, const CUtensorMap* mk, const CUtensorMap* mv,
                                          const CUtensorMap* hk, const CUtensorMap* hv, int c, int grid,
                                          unsigned long long* tl_first = nullptr) {
@@ -312,6 +314,13 @@ __device__ __forceinline__ void attn_cta(const AttnArgs& a, const CUtensorMap* m
         ps1 += __shfl_xor_sync(0xffffffffu, ps1, 1);
         ps0 += __shfl_xor_sync(0xffffffffu, ps0, 2);
         ps1 += __shfl_xor_sync(0xffffffffu, ps1, 2);
+        if constexpr (kStats) {
+          if (cq == 0) {
+            float2* st = a.stats + (((size_t)bg * a.kslots + s) * kGroupWarps + wq) * kHeads;
+            st[g] = make_float2(m0, ps0);
+            st[g + 8] = make_float2(m1, ps1);
+          }
+        }
         l0 = l0 * al0 + ps0;
         l1 = l1 * al1 + ps1;
 #pragma unroll
@@ -414,6 +423,12 @@ __device__ __forceinline__ void attn_cta(const AttnArgs& a, const CUtensorMap* m
           acc[0] += wt * x0.x; acc[1] += wt * x0.y; acc[2] += wt * x0.z; acc[3] += wt * x0.w;
           acc[4] += wt * x1.x; acc[5] += wt * x1.y; acc[6] += wt * x1.z; acc[7] += wt * x1.w;
         }
+        if constexpr (kStats) {
+          if ((t & 15) == 0) {
+            a.ml[bg * 2 * kHeads + h] = Mx;
+            a.ml[bg * 2 * kHeads + kHeads + h] = L;
+          }
+        }
         uint32_t pk[4];
 #pragma unroll
         for (int e = 0; e < 4; ++e)
@@ -428,6 +443,12 @@ __device__ __forceinline__ void attn_cta(const AttnArgs& a, const CUtensorMap* m
     const int n_seg = sg > 0 ? sg : cta_of_unit(last, grid, U) - c_first + 1;
     uint4* outp = reinterpret_cast<uint4*>(a.out + ((size_t)bg * kHeads + h) * kHeadDim + d0);
     if (n_seg == 1) {
+      if constexpr (kStats) {
+        if ((t & 15) == 0) {
+          a.ml[bg * 2 * kHeads + h] = Mh;
+          a.ml[bg * 2 * kHeads + kHeads + h] = Lh;
+        }
+      }
       uint32_t pk[4];
 #pragma unroll
       for (int e = 0; e < 4; ++e)
@@ -494,6 +515,12 @@ __device__ __forceinline__ void attn_cta(const AttnArgs& a, const CUtensorMap* m
         acc[6] += wt * px[q][1].z; acc[7] += wt * px[q][1].w;
       }
       M = Mn;
+    }
+    if constexpr (kStats) {
+      if ((t & 15) == 0) {
+        a.ml[bg * 2 * kHeads + h] = M;
+        a.ml[bg * 2 * kHeads + kHeads + h] = L;
+      }
     }
     uint32_t pk[4];
 #pragma unroll

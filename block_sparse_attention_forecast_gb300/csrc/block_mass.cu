@@ -1,0 +1,49 @@
+// The attention weight that each attended block received, summed over the group's heads and added
+// to the sequence's running totals: mass[b, g, j] += sum_h sum_{t in block j} softmax_h(t).
+//
+// The attention kernels leave, for every quarter (16 tokens) of an attended block and every head,
+// the maximum m and the sum l of exp2(s - m), and for every head the final maximum M and sum L
+// over all blocks; the weight of the quarter is l exp2(m - M) / L. So no score is stored or
+// computed twice: 512 bytes per block beside the block's 10 to 32 KiB. One warp per attended
+// block; a block's weights are added in a fixed order and once, by one atomic addition (a block
+// named twice in idx adds the same number twice, in either order).
+#include "kernels.h"
+
+#include "common.cuh"
+
+namespace sparda {
+
+constexpr int kMassWarps = 8;
+
+__global__ void __launch_bounds__(kMassWarps * 32) block_mass_kernel(const BlockMassArgs a) {
+  grid_dep_wait();
+  grid_dep_launch();
+  const int per = (a.slots + kMassWarps - 1) / kMassWarps;
+  const int bg = blockIdx.x / per, s = (blockIdx.x % per) * kMassWarps + (int)threadIdx.x / 32, lane = threadIdx.x & 31;
+  const int T = a.seq_len[bg / a.G];
+  if (s >= a.slots || T < 1 || T > a.max_ctx) return;
+  const int tb = (T - 1) / kBlock;
+  int j = s;
+  if (a.idx) {
+    if (s >= a.cnt[bg]) return;
+    j = a.idx[(size_t)bg * a.slots + s];
+  }
+  if (j < 0 || j > tb) return;                     // reported by the attention
+  const int h = lane & 15;
+  const float M = a.ml[bg * 2 * kHeads + h], L = a.ml[bg * 2 * kHeads + kHeads + h];
+  const float2* st = a.stats + ((size_t)bg * a.slots + s) * 4 * kHeads;
+  const float2 x = st[lane], y = st[lane + 32];
+  // a quarter without tokens has l = 0
+  float w = (x.y == 0.f ? 0.f : x.y * fast_exp2(x.x - M)) + (y.y == 0.f ? 0.f : y.y * fast_exp2(y.x - M));
+  w = h < a.H && L != 0.f ? w / L : 0.f;
+#pragma unroll
+  for (int d = 16; d; d >>= 1) w += __shfl_xor_sync(0xffffffffu, w, d);
+  if (lane == 0) atomicAdd(a.mass + (size_t)bg * a.nb_cap + j, w);
+}
+
+void launch_block_mass(const BlockMassArgs& a, int bg_count, cudaStream_t s) {
+  const unsigned per = (unsigned)(a.slots + kMassWarps - 1) / kMassWarps;
+  launch_pdl(block_mass_kernel, dim3(per * (unsigned)bg_count), dim3(kMassWarps * 32), 0, s, a);
+}
+
+}  // namespace sparda

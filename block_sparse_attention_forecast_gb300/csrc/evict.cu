@@ -1,0 +1,368 @@
+// Eviction: every (sequence, group) keeps block 0, its `recent` newest blocks and, of the others,
+// the ones with the largest accumulated attention weight, `keep` blocks in all; kept blocks move
+// together to the front in their order, with their compressed keys and weights, in the cache itself
+// or into another (smaller) one, and the sequence's length drops by the blocks lost.
+//
+//   evict_select_kernel   one CTA per (sequence, group): the kept list. The weights stay in
+//                         registers as order-preserving integers; the (keep - forced)-th largest
+//                         is found bit by bit, 32 counts over the CTA at most, which does not
+//                         depend on how the weights are spread (many blocks tie at 0).
+//   evict_move_kernel     into another cache: one CTA per kept block. Bytes in, bytes out.
+//   evict_shift_kernel    in the cache itself: block n moves from kept[n] >= n, so a block may be
+//                         overwritten only once it has been read. One thread-block cluster per
+//                         (sequence, group) takes the kept blocks in rounds of a few blocks per CTA:
+//                         all of a round is read into shared memory, a cluster barrier, then it is
+//                         written. A round writes blocks below its end and later rounds read blocks
+//                         at or above it, so the next round's reads start before the barrier.
+//   evict_join_kernel     after the shift: the compressed keys of windows that span two blocks
+//                         which were not neighbours before (the move kernel does its own).
+//   evict_length_kernel   after the shift: the new lengths, once nothing reads the old ones.
+//
+// A moved block's windows 4n .. 4n+2 lie inside it and move with it; window 4n+3 takes its last 16
+// keys and the first 16 of the next block.
+#include "append_body.cuh"
+#include "kernels.h"
+#include "kv4.cuh"
+
+namespace sparda {
+
+namespace {
+
+constexpr int kSelThreads = 512;
+constexpr int kSelPer = kMaxCtx / kBlock / kSelThreads;         // weights per thread: 8
+constexpr int kMoveThreads = 256;
+constexpr int kShiftSmem = 220 * 1024;                          // two rounds of a CTA's blocks
+constexpr int kCkRow = kHeadDim * 2;                            // bytes of a compressed key
+
+__device__ __forceinline__ bool valid_len(int T, int nb) { return T >= 1 && T <= nb * kBlock; }
+__device__ __forceinline__ int blocks_of(int T) { return (T - 1) / kBlock + 1; }
+// The length after the eviction of a sequence of T tokens.
+__device__ __forceinline__ int kept_len(int T, int keep) {
+  const int n = blocks_of(T);
+  return T - kBlock * (n - min(n, keep));
+}
+
+// Weight -> integer in the weights' order: a NaN above every number, -0 equal to +0, 0 unused.
+__device__ __forceinline__ uint32_t weight_key(float w) {
+  if (w != w) return 0xffffffffu;
+  return ordered_key(w == 0.f ? 0.f : w);
+}
+
+// Two channels of the key of token `tok` of block j of (sequence, group) bg.
+__device__ __forceinline__ uint32_t cache_key2(const uint8_t* plane, int kv4, size_t block, int tok, int t) {
+  if (!kv4) return reinterpret_cast<const uint32_t*>(plane + block * kBlockBytes + tok * kRowBytes)[t];
+  const uint8_t* b = plane + block * kv4::kBlockBytes4;
+  const uint32_t w = *reinterpret_cast<const uint32_t*>(b + kv4::kKCodes + tok * 64 + (t >> 2) * 4);
+  const uint32_t sz = *reinterpret_cast<const uint32_t*>(b + kv4::kKScales + tok * 16 + (t >> 4) * 4);
+  return kv4::key_pair(w, t & 3, kv4::as_bf2(kv4::dup_lo(sz)), kv4::as_bf2(kv4::dup_hi(sz)));
+}
+
+// The compressed key of a window made of the last 16 keys of block ja and the first 16 of jb, by 64 threads.
+__device__ __forceinline__ uint32_t joined_window(const uint8_t* plane, int kv4, size_t ja, size_t jb, int t) {
+  uint32_t xs[kWinKernel];
+#pragma unroll
+  for (int u = 0; u < kWinKernel / 2; ++u) {
+    xs[u] = cache_key2(plane, kv4, ja, kBlock - kWinKernel / 2 + u, t);
+    xs[u + kWinKernel / 2] = cache_key2(plane, kv4, jb, u, t);
+  }
+  return window_mean(xs);
+}
+
+// Bytes of compressed keys that move with kept block n of `count` (T tokens afterwards): its windows
+// that are complete, its last only beside its old neighbour.
+__device__ __forceinline__ int window_bytes(int n, int count, int T, bool neighbour) {
+  const int complete = num_windows(T) - 4 * n;
+  const int own = n + 1 < count && neighbour ? 4 : 3;
+  return min(max(complete, 0), own) * kCkRow;
+}
+// Whether window 4n+3 has to be formed anew.
+__device__ __forceinline__ bool joins(int n, int count, int T, bool neighbour) {
+  return n + 1 < count && !neighbour && num_windows(T) > 4 * n + 3;
+}
+
+}  // namespace
+
+__global__ void __launch_bounds__(kSelThreads) evict_select_kernel(const EvictArgs a) {
+  __shared__ int s_cnt[32];
+  __shared__ int s_warp[2][kSelThreads / 32];
+  grid_dep_wait();
+  grid_dep_launch();
+  const int bg = blockIdx.x, b = bg / a.G, tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  const int T = a.src_len[b];
+  const bool valid = valid_len(T, a.src_nb);
+  const int n = valid ? blocks_of(T) : 0, count = min(n, a.keep);
+  if (!valid && tid == 0) atomicOr(a.err, SPARDA_DEV_BAD_SEQ_LEN);
+  const float* src = a.src_mass + (size_t)bg * a.src_nb;
+  float w[kSelPer];
+  uint32_t key[kSelPer];
+#pragma unroll
+  for (int i = 0; i < kSelPer; ++i) {
+    const int j = tid * kSelPer + i;
+    w[i] = j < n ? src[j] : 0.f;
+  }
+#pragma unroll
+  for (int i = 0; i < kSelPer; ++i) {
+    const int j = tid * kSelPer + i;
+    key[i] = j >= 1 && j < n - a.recent ? weight_key(w[i]) : 0u;     // candidates only
+  }
+  if (tid < 32) s_cnt[tid] = 0;
+  __syncthreads();                                 // in place: every weight is read before one is written
+  uint32_t sel = 0;                                // bit i: block tid * kSelPer + i is kept
+  if (n <= a.keep) {
+#pragma unroll
+    for (int i = 0; i < kSelPer; ++i) sel |= (tid * kSelPer + i < n ? 1u : 0u) << i;
+  } else {
+    const int want = a.keep - 1 - a.recent;        // candidates to keep; more of them exist
+    uint32_t thr = 0xffffffffu;                    // the want-th largest key
+    int above = 0;                                 // candidates above it
+    if (want > 0) {
+      thr = 0u;
+      for (int bit = 31; bit >= 0; --bit) {
+        const uint32_t tryk = thr | (1u << bit);
+        int c = 0;
+#pragma unroll
+        for (int i = 0; i < kSelPer; ++i) c += key[i] >= tryk;
+        c = __reduce_add_sync(0xffffffffu, c);
+        if (lane == 0 && c) atomicAdd(&s_cnt[bit], c);
+        __syncthreads();
+        const int total = s_cnt[bit];
+        if (total >= want) {
+          thr = tryk;
+          if (total == want) break;                // exactly the keys at or above thr
+        }
+      }
+      // keys above thr, for the share of the ties
+      __syncthreads();
+      if (tid == 0) s_cnt[0] = 0;
+      __syncthreads();
+      int c = 0;
+#pragma unroll
+      for (int i = 0; i < kSelPer; ++i) c += key[i] > thr;
+      c = __reduce_add_sync(0xffffffffu, c);
+      if (lane == 0 && c) atomicAdd(&s_cnt[0], c);
+      __syncthreads();
+      above = s_cnt[0];
+    }
+    // ties go to the lowest blocks: the rank of each key equal to thr
+    int ties = 0;
+#pragma unroll
+    for (int i = 0; i < kSelPer; ++i) ties += want > 0 && key[i] == thr && key[i] != 0u;
+    int scan = ties;
+#pragma unroll
+    for (int d = 1; d < 32; d <<= 1) {
+      const int o = __shfl_up_sync(0xffffffffu, scan, d);
+      if (lane >= d) scan += o;
+    }
+    if (lane == 31) s_warp[0][warp] = scan;
+    __syncthreads();
+    int rank = scan - ties;
+    for (int q = 0; q < warp; ++q) rank += s_warp[0][q];
+#pragma unroll
+    for (int i = 0; i < kSelPer; ++i) {
+      const int j = tid * kSelPer + i;
+      bool in = j == 0 || (j >= n - a.recent && j < n);
+      if (want > 0 && key[i] != 0u) {
+        in = in || key[i] > thr;
+        if (key[i] == thr) in = in || rank++ < want - above;
+      }
+      sel |= (in ? 1u : 0u) << i;
+    }
+  }
+  // places: an exclusive scan of the kept flags in block order
+  const int mine = __popc(sel);
+  int scan = mine;
+#pragma unroll
+  for (int d = 1; d < 32; d <<= 1) {
+    const int o = __shfl_up_sync(0xffffffffu, scan, d);
+    if (lane >= d) scan += o;
+  }
+  if (lane == 31) s_warp[1][warp] = scan;
+  __syncthreads();
+  int at = scan - mine;
+  for (int q = 0; q < warp; ++q) at += s_warp[1][q];
+  int32_t* kept = a.kept + (size_t)bg * a.keep;
+  float* dst = a.dst_mass + (size_t)bg * a.dst_nb;
+#pragma unroll
+  for (int i = 0; i < kSelPer; ++i)
+    if (sel >> i & 1u) {
+      kept[at] = tid * kSelPer + i;
+      dst[at] = w[i];
+      ++at;
+    }
+  for (int i = count + tid; i < a.keep; i += kSelThreads) kept[i] = -1;
+  if (valid)
+    for (int i = count + tid; i < a.dst_nb; i += kSelThreads) dst[i] = 0.f;
+  if (!a.in_place && tid == 0 && bg % a.G == 0) a.dst_len[b] = valid ? kept_len(T, a.keep) : T;
+}
+
+// Grid: (sequence, group) x kept block.
+__global__ void __launch_bounds__(kMoveThreads) evict_move_kernel(const EvictArgs a) {
+  grid_dep_wait();
+  grid_dep_launch();
+  const int bg = blockIdx.x / a.keep, n = blockIdx.x % a.keep, tid = threadIdx.x;
+  const int32_t* kept = a.kept + (size_t)bg * a.keep;
+  const int j = kept[n], nxt = n + 1 < a.keep ? kept[n + 1] : -1;
+  if (j < 0) return;
+  const int T0 = a.src_len[bg / a.G];
+  const int T = kept_len(T0, a.keep), count = min(blocks_of(T0), a.keep);
+  const size_t from = (size_t)bg * a.src_nb + j, to = (size_t)bg * a.dst_nb + n;
+  const int vecs = a.block_bytes / 16;
+  for (int p = 0; p < a.planes; ++p) {
+    const uint4* s = reinterpret_cast<const uint4*>(a.src[p] + from * a.block_bytes);
+    uint4* d = reinterpret_cast<uint4*>(a.dst[p] + to * a.block_bytes);
+    uint4 r[4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+      if (tid + i * kMoveThreads < vecs) r[i] = __ldcs(s + tid + i * kMoveThreads);
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+      if (tid + i * kMoveThreads < vecs) d[tid + i * kMoveThreads] = r[i];
+  }
+  const size_t src_row = (size_t)bg * (4 * a.src_nb - 1) + 4 * j, dst_row = (size_t)bg * (4 * a.dst_nb - 1) + 4 * n;
+  const bool neighbour = nxt == j + 1;
+  if (tid < window_bytes(n, count, T, neighbour) / 16)
+    reinterpret_cast<uint4*>(a.dst_ck + dst_row * kHeadDim)[tid] =
+        reinterpret_cast<const uint4*>(a.src_ck + src_row * kHeadDim)[tid];
+  if (tid >= 64 && tid < 128 && joins(n, count, T, neighbour))
+    reinterpret_cast<uint32_t*>(a.dst_ck + (dst_row + 3) * kHeadDim)[tid - 64] =
+        joined_window(a.src[0], a.kv4, from, (size_t)bg * a.src_nb + nxt, tid - 64);
+}
+static_assert(kBlockBytes / 16 <= 4 * kMoveThreads, "a plane's block is at most four vectors per thread");
+
+// One cluster of gridDim.x / (B*G) CTAs per (sequence, group), one warp each; lane 0 issues the
+// bulk copies. Shared memory: two rounds of `slots` blocks with their compressed keys.
+__global__ void __launch_bounds__(32) evict_shift_kernel(const EvictArgs a, int ctas, int slots) {
+  extern __shared__ uint8_t smem_shift[];
+  __shared__ alignas(8) uint64_t bar[2];
+  const int lane = threadIdx.x;
+  if (lane == 0) {
+    mbar_init(&bar[0], 1);
+    mbar_init(&bar[1], 1);
+    fence_mbar_init();
+  }
+  __syncwarp();
+  grid_dep_wait();
+  grid_dep_launch();
+  const int bg = blockIdx.x / ctas, rank = blockIdx.x % ctas;
+  const int T0 = a.src_len[bg / a.G];
+  const bool valid = valid_len(T0, a.src_nb);
+  const int count = valid ? min(blocks_of(T0), a.keep) : 0, T = valid ? kept_len(T0, a.keep) : 0;
+  const int32_t* kept = a.kept + (size_t)bg * a.keep;
+  uint8_t* base = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_shift) + 127) & ~static_cast<uintptr_t>(127));
+  const int slot_bytes = a.planes * a.block_bytes + 4 * kCkRow;
+  const int round = ctas * slots, rounds = (count + round - 1) / round;
+  // the block, its old place and its compressed-key bytes of slot i of this CTA in round r
+  struct Item { int n, j, ck; };
+  const auto item = [&](int r, int i) {
+    Item it{r * round + rank * slots + i, -1, 0};
+    if (it.n < count) {
+      it.j = kept[it.n];
+      const bool neighbour = it.n + 1 < count && kept[it.n + 1] == it.j + 1;
+      it.ck = window_bytes(it.n, count, T, neighbour);
+      if (it.j == it.n) it.j = -1;                 // already in place, with its windows
+    }
+    return it;
+  };
+  const auto load = [&](int r) {
+    uint32_t bytes = 0;
+    for (int i = 0; i < slots; ++i) {
+      const Item it = item(r, i);
+      if (it.j >= 0) bytes += a.planes * a.block_bytes + it.ck;
+    }
+    mbar_arrive_expect_tx(&bar[r & 1], bytes);
+    for (int i = 0; i < slots; ++i) {
+      const Item it = item(r, i);
+      if (it.j < 0) continue;
+      uint8_t* s = base + ((r & 1) * slots + i) * slot_bytes;
+      for (int p = 0; p < a.planes; ++p)
+        bulk_load(s + p * a.block_bytes, a.dst[p] + ((size_t)bg * a.dst_nb + it.j) * a.block_bytes, a.block_bytes, &bar[r & 1]);
+      if (it.ck) bulk_load(s + a.planes * a.block_bytes, a.dst_ck + ((size_t)bg * (4 * a.dst_nb - 1) + 4 * it.j) * kHeadDim,
+                           it.ck, &bar[r & 1]);
+    }
+  };
+  bool ok = true;                                  // a wait that ran out: nothing more is written
+  if (lane == 0 && rounds > 0) load(0);
+  for (int r = 0; r < rounds; ++r) {
+    if (lane == 0) {
+      if (ok) ok = mbar_wait(&bar[r & 1], (r >> 1) & 1, a.err);
+      if (ok && r + 1 < rounds) {
+        bulk_wait_read<0>();                       // the other buffer's stores have left it
+        load(r + 1);
+      }
+    }
+    cluster_sync();                                // the round is in shared memory, everywhere
+    if (lane == 0 && ok) {
+      for (int i = 0; i < slots; ++i) {
+        const Item it = item(r, i);
+        if (it.j < 0) continue;
+        const uint8_t* s = base + ((r & 1) * slots + i) * slot_bytes;
+        for (int p = 0; p < a.planes; ++p)
+          bulk_store(a.dst[p] + ((size_t)bg * a.dst_nb + it.n) * a.block_bytes, s + p * a.block_bytes, a.block_bytes);
+        if (it.ck) bulk_store(a.dst_ck + ((size_t)bg * (4 * a.dst_nb - 1) + 4 * it.n) * kHeadDim, s + a.planes * a.block_bytes,
+                              it.ck);
+      }
+      bulk_commit();
+    }
+  }
+  if (lane == 0) bulk_wait_all();
+}
+
+// Grid: (sequence, group) x groups of kept blocks, 64 threads per kept block.
+__global__ void __launch_bounds__(kMoveThreads) evict_join_kernel(const EvictArgs a) {
+  grid_dep_wait();
+  grid_dep_launch();
+  constexpr int per = kMoveThreads / 64;
+  const int pieces = (a.keep + per - 1) / per;
+  const int bg = blockIdx.x / pieces, n = (blockIdx.x % pieces) * per + (int)threadIdx.x / 64, t = threadIdx.x % 64;
+  const int T0 = a.src_len[bg / a.G];
+  if (n + 1 >= a.keep || !valid_len(T0, a.src_nb)) return;
+  const int32_t* kept = a.kept + (size_t)bg * a.keep;
+  if (!joins(n, min(blocks_of(T0), a.keep), kept_len(T0, a.keep), kept[n + 1] == kept[n] + 1)) return;
+  const size_t block = (size_t)bg * a.dst_nb + n;
+  reinterpret_cast<uint32_t*>(a.dst_ck + ((size_t)bg * (4 * a.dst_nb - 1) + 4 * n + 3) * kHeadDim)[t] =
+      joined_window(a.dst[0], a.kv4, block, block + 1, t);
+}
+
+__global__ void evict_length_kernel(const EvictArgs a) {
+  grid_dep_wait();
+  grid_dep_launch();
+  for (int b = threadIdx.x; b < a.B; b += blockDim.x) {
+    const int T = a.src_len[b];
+    if (valid_len(T, a.src_nb)) a.dst_len[b] = kept_len(T, a.keep);
+  }
+}
+
+void launch_evict(const EvictArgs& a, cudaStream_t s) {
+  const unsigned bg = (unsigned)a.B * a.G;
+  launch_pdl(evict_select_kernel, dim3(bg), dim3(kSelThreads), 0, s, a);
+  if (!a.in_place) {
+    launch_pdl(evict_move_kernel, dim3(bg * (unsigned)a.keep), dim3(kMoveThreads), 0, s, a);
+    return;
+  }
+  // as many CTAs per (sequence, group) as fill the SMs, up to a portable cluster of 8
+  int ctas = 1;
+  while (ctas < 8 && 2 * ctas * (int)bg <= sm_count()) ctas *= 2;
+  const int slot_bytes = a.planes * a.block_bytes + 4 * kCkRow;
+  const int slots = kShiftSmem / (2 * slot_bytes);
+  const size_t smem = 128 + 2 * (size_t)slots * slot_bytes;
+  cudaFuncSetAttribute(evict_shift_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(bg * ctas);
+  cfg.blockDim = dim3(32);
+  cfg.dynamicSmemBytes = smem;
+  cfg.stream = s;
+  cudaLaunchAttribute attr[2];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  attr[1].id = cudaLaunchAttributeClusterDimension;
+  attr[1].val.clusterDim.x = ctas;
+  attr[1].val.clusterDim.y = 1;
+  attr[1].val.clusterDim.z = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 2;
+  cudaLaunchKernelEx(&cfg, evict_shift_kernel, a, ctas, slots);
+  launch_pdl(evict_join_kernel, dim3(bg * (unsigned)((a.keep + 3) / 4)), dim3(kMoveThreads), 0, s, a);
+  launch_pdl(evict_length_kernel, dim3(1), dim3(256), 0, s, a);
+}
+
+}  // namespace sparda

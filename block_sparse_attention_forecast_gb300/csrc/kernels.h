@@ -86,6 +86,10 @@ struct AttnArgs {
   int stage_slots = 0;
   uint32_t tl_launch = 0;        // launch number for the timeline build's records
   void* tl_buf = nullptr;        // the timeline build's record store
+  // block mass (the standalone launch): (max, sum) [B*G, kslots, 4, 16] and the final max and
+  // sum [B*G, 2, 16]; nullptr: not wanted
+  float2* stats = nullptr;
+  float* ml = nullptr;
 };
 
 struct MultiheadArgs {
@@ -183,6 +187,72 @@ void launch_prefill_attn_tc(const PrefillArgs& a, const CUtensorMap& mq, const C
 int multihead_tiles(int w_cap);
 int multihead_cluster_size(int n_tiles_cap, int bg_count);
 
+// The 4-bit cache (kv4_cache.cu): writing it, one token or a whole prompt, and reading it back.
+struct Kv4CacheArgs {
+  uint8_t* kv;                   // [max_batch, G, nb_cap, SPARDA_KV4_BLOCK_BYTES]
+  __nv_bfloat16* ck;             // [max_batch, G, W_cap, d] (append)
+  const __nv_bfloat16* k;        // quantize: [max_batch, G, max_ctx, d]; append: [B, G, d]
+  const __nv_bfloat16* v;
+  __nv_bfloat16* k_out;          // dequantize: [max_batch, G, max_ctx, d] or [max_batch, G, kslots, 64, d]
+  __nv_bfloat16* v_out;
+  const int32_t* idx;            // dequantize of selected blocks: [B, G, kslots]; nullptr: all blocks
+  const int32_t* cnt;
+  const int32_t* seq_len;
+  int* err;
+  int G, max_ctx, nb_cap, W_cap, kslots;
+};
+void launch_kv4_quantize(const Kv4CacheArgs& a, int bg_count, cudaStream_t s);
+void launch_kv4_dequantize(const Kv4CacheArgs& a, int bg_count, cudaStream_t s);
+void launch_kv4_append(const Kv4CacheArgs& a, int bg_count, cudaStream_t s);
+
+// Decode attention over the 4-bit cache (kv4_attn.cu).
+constexpr int kKv4MaxCtas = 160;                  // at most this many CTAs share the blocks
+struct Kv4AttnArgs {
+  const uint8_t* kv;
+  const __nv_bfloat16* q;        // [B, G*H, d]
+  const int32_t* idx;            // [B, G, kslots]; nullptr: every block of the sequence
+  const int32_t* cnt;
+  const int32_t* seq_len;
+  __nv_bfloat16* out;            // [B, G*H, d]
+  float* part_o;                 // workspace [kKv4MaxCtas, 2, 16, d]
+  float* part_ml;                // workspace [kKv4MaxCtas, 2, 2, 16]
+  unsigned* counters;            // workspace [max_batch*G], zero between calls
+  float2* stats;                 // block mass: (max, sum) [B*G, slots, 4, 16]; nullptr: not wanted
+  float* ml;                     // block mass: final max and sum [B*G, 2, 16]
+  int* err;
+  int G, H, max_ctx, nb_cap, kslots, bg_count;
+};
+void launch_kv4_attn(const Kv4AttnArgs& a, cudaStream_t s);
+
+// Accumulates the attention weight of each attended block (block_mass.cu).
+struct BlockMassArgs {
+  const float2* stats;           // [B*G, slots, 4, 16] (max, sum) per quarter block and head
+  const float* ml;               // [B*G, 2, 16]
+  float* mass;                   // [max_batch, G, nb_cap]
+  const int32_t* idx;            // [B, G, kslots]; nullptr: slot j is block j
+  const int32_t* cnt;
+  const int32_t* seq_len;
+  int G, H, max_ctx, nb_cap, slots;
+};
+void launch_block_mass(const BlockMassArgs& a, int bg_count, cudaStream_t s);
+
+// Eviction (evict.cu). A cache is one or two planes of fixed bytes per block.
+struct EvictArgs {
+  const uint8_t* src[2];         // [max_batch*G, src_nb, block_bytes]
+  uint8_t* dst[2];               // [max_batch*G, dst_nb, block_bytes]
+  const __nv_bfloat16* src_ck;   // [max_batch*G, 4*src_nb-1, d]
+  __nv_bfloat16* dst_ck;
+  const float* src_mass;         // [max_batch*G, src_nb]
+  float* dst_mass;
+  const int32_t* src_len;        // [B]
+  int32_t* dst_len;
+  int32_t* kept;                 // [B*G, keep]
+  int* err;
+  int planes, block_bytes, kv4;  // kv4: one plane in the 4-bit layout; else K and V planes of bf16
+  int B, G, src_nb, dst_nb, keep, recent, in_place;
+};
+void launch_evict(const EvictArgs& a, cudaStream_t s);
+
 // Device address of the library's device error word on the current device (api.cu).
 int* dev_error_word();
 
@@ -190,5 +260,23 @@ int* dev_error_word();
 int select_chunk_blocks(int nb_cap, int bg_count);
 int attn_blocks_per_cta();
 size_t smem_select_bytes(int chunk_blocks);
+int sm_count();                                   // of the current device (attn.cu)
+
+// A launch that may begin while the kernel before it in the stream still runs (programmatic
+// dependent launch); the kernel waits for that one with grid_dep_wait().
+template <typename... P, typename... A>
+inline void launch_pdl(void (*kern)(P...), dim3 grid, dim3 block, size_t smem, cudaStream_t s, A&&... args) {
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = grid;
+  cfg.blockDim = block;
+  cfg.dynamicSmemBytes = smem;
+  cfg.stream = s;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  cudaLaunchKernelEx(&cfg, kern, static_cast<P>(args)...);
+}
 
 }  // namespace sparda

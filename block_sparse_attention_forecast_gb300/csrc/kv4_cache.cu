@@ -1,0 +1,259 @@
+// Writing and reading back the 4-bit KV cache (layout and grid: kv4.cuh): a prompt's keys and
+// values at once, one decode token, and blocks back to bf16. All three move bytes: a prompt token
+// is 512 bytes read and 160 written per KV group, its arithmetic (one exact division per value)
+// hides behind that.
+#include "append_body.cuh"
+#include "kernels.h"
+#include "kv4.cuh"
+
+namespace sparda {
+using namespace kv4;
+
+constexpr int kQThreads = 256;
+constexpr int kQRounds = kBlock * 16 / kQThreads;      // (token, 8 channels) items per thread: 4
+
+__device__ __forceinline__ float bf_at(const uint4& x, int i) {
+  const uint32_t u = i < 2 ? x.x : i < 4 ? x.y : i < 6 ? x.z : x.w;
+  return (i & 1) ? bf16_hi(u) : bf16_lo(u);
+}
+
+// The grid of a 32-channel group from the 8 channels of each of its four lanes (xor 1, 2).
+template <bool kKey>
+__device__ __forceinline__ Grid group_grid(const uint4& x) {
+  float lo = bf_at(x, 0), hi = lo;
+  bool fin = true;
+#pragma unroll
+  for (int i = 0; i < 8; ++i) {
+    const float v = bf_at(x, i);
+    fin = fin && fabsf(v) < INFINITY;
+    lo = fminf(lo, v);
+    hi = fmaxf(hi, v);
+  }
+#pragma unroll
+  for (int d = 1; d <= 2; d <<= 1) {
+    lo = fminf(lo, __shfl_xor_sync(0xffffffffu, lo, d));
+    hi = fmaxf(hi, __shfl_xor_sync(0xffffffffu, hi, d));
+    fin = __shfl_xor_sync(0xffffffffu, (int)fin, d) && fin;
+  }
+  return make_grid<kKey>(lo, hi, fin);
+}
+
+// One CTA per (sequence-group, block). 16 lanes hold a row, 8 channels each, so loads are whole
+// lines and a group's extremes take two shuffles. The block is put together in shared memory and
+// leaves as one bulk copy: written directly, the value codes would leave as 16-byte pieces 64
+// bytes apart.
+__global__ void __launch_bounds__(kQThreads) kv4_quantize_kernel(const Kv4CacheArgs a) {
+  __shared__ alignas(128) uint8_t blk[kBlockBytes4];
+  grid_dep_wait();
+  grid_dep_launch();
+  const int j = blockIdx.x % a.nb_cap, bg = blockIdx.x / a.nb_cap, b = bg / a.G;
+  const int T = a.seq_len[b];
+  if (T < 1 || T > a.max_ctx) {
+    if (threadIdx.x == 0 && j == 0) atomicOr(a.err, SPARDA_DEV_BAD_SEQ_LEN);
+    return;
+  }
+  if (j * kBlock >= T) return;
+  const int l16 = threadIdx.x & 15, row0 = threadIdx.x >> 4;
+  const uint4* k = reinterpret_cast<const uint4*>(a.k) + ((size_t)bg * a.max_ctx + (size_t)j * kBlock) * 16 + l16;
+  const uint4* v = reinterpret_cast<const uint4*>(a.v) + ((size_t)bg * a.max_ctx + (size_t)j * kBlock) * 16 + l16;
+  const int live = min(kBlock, T - j * kBlock);
+  uint4 xk[kQRounds], xv[kQRounds];
+#pragma unroll
+  for (int r = 0; r < kQRounds; ++r) {
+    const int t = row0 + r * (kQThreads / 16);
+    const bool in = t < live;                      // rows past the prompt are stored as zeros
+    xk[r] = in ? __ldcs(k + (size_t)t * 16) : make_uint4(0, 0, 0, 0);
+    xv[r] = in ? __ldcs(v + (size_t)t * 16) : make_uint4(0, 0, 0, 0);
+  }
+#pragma unroll
+  for (int r = 0; r < kQRounds; ++r) {
+    const int t = row0 + r * (kQThreads / 16);
+    {
+      const Grid g = group_grid<true>(xk[r]);
+      uint32_t w = 0;
+#pragma unroll
+      for (int i = 0; i < 8; ++i) w |= code_of(bf_at(xk[r], i), g) << (4 * (i >> 1) + 16 * (i & 1));
+      *reinterpret_cast<uint32_t*>(blk + kKCodes + t * 64 + l16 * 4) = rol(w, 3);
+      if ((l16 & 3) == 0) *reinterpret_cast<uint32_t*>(blk + kKScales + t * 16 + l16) = g.s16 | (g.z16 << 16);
+    }
+    {
+      const Grid g = group_grid<false>(xv[r]);
+      // channels 8 l16 + 0..3 in the low half, + 4..7 in the high half
+      uint32_t w = 0;
+#pragma unroll
+      for (int i = 0; i < 8; ++i) w |= code_of(bf_at(xv[r], i), g) << (4 * i);
+      // the even token's lane takes the first four channels of both tokens, the odd one's the rest
+      const uint32_t other = __shfl_xor_sync(0xffffffffu, w, 16);
+      const uint32_t both = (t & 1) ? __byte_perm(other, w, 0x7632) : __byte_perm(w, other, 0x5410);
+      *reinterpret_cast<uint32_t*>(blk + value_chunk(t >> 1, l16 >> 1) + ((l16 & 1) * 2 + (t & 1)) * 4) = rol(both, 6);
+      const uint32_t so = __shfl_xor_sync(0xffffffffu, g.s16, 16), zo = __shfl_xor_sync(0xffffffffu, g.z16, 16);
+      if ((l16 & 3) == 0 && !(t & 1))
+        *reinterpret_cast<uint2*>(blk + value_scale(t >> 1, l16 >> 2)) = make_uint2(g.s16 | (so << 16), g.z16 | (zo << 16));
+    }
+  }
+  fence_proxy_async_shared();
+  __syncthreads();
+  if (threadIdx.x == 0) {
+    uint8_t* dst = a.kv + ((size_t)bg * a.nb_cap + j) * kBlockBytes4;
+    bulk_store(dst, blk, kBlockBytes4);
+    bulk_commit();
+    bulk_wait_all();
+  }
+}
+
+// One CTA per (sequence-group, slot): the block's values back as bf16, rows of the sequence only.
+// idx == nullptr: slot j is block j and rows go to a cache [.., max_ctx, 128]; otherwise the slot's
+// block is idx[slot] and rows go to a staging buffer [.., kslots, 64, 128].
+__global__ void __launch_bounds__(kQThreads) kv4_dequantize_kernel(const Kv4CacheArgs a) {
+  __shared__ alignas(16) uint8_t blk[kBlockBytes4];
+  grid_dep_wait();
+  grid_dep_launch();
+  const int n_slots = a.idx ? a.kslots : a.nb_cap;
+  const int s = blockIdx.x % n_slots, bg = blockIdx.x / n_slots, b = bg / a.G;
+  const int T = a.seq_len[b];
+  if (T < 1 || T > a.max_ctx) {
+    if (threadIdx.x == 0 && s == 0) atomicOr(a.err, SPARDA_DEV_BAD_SEQ_LEN);
+    return;
+  }
+  int j = s;
+  if (a.idx) {
+    if (s >= a.cnt[bg]) return;
+    j = a.idx[(size_t)bg * a.kslots + s];
+    if (j < 0 || j > (T - 1) / kBlock) {
+      if (threadIdx.x == 0) atomicOr(a.err, SPARDA_DEV_BAD_INDEX);
+      return;
+    }
+  } else if (j * kBlock >= T) {
+    return;
+  }
+  const uint4* src = reinterpret_cast<const uint4*>(a.kv + ((size_t)bg * a.nb_cap + j) * kBlockBytes4);
+  for (int i = threadIdx.x; i < kBlockBytes4 / 16; i += kQThreads) reinterpret_cast<uint4*>(blk)[i] = __ldcs(src + i);
+  __syncthreads();
+  const size_t row = a.idx ? ((size_t)bg * a.kslots + s) * kBlock : (size_t)bg * a.max_ctx + (size_t)j * kBlock;
+  uint4* k = reinterpret_cast<uint4*>(a.k_out) + row * 16;
+  uint4* v = reinterpret_cast<uint4*>(a.v_out) + row * 16;
+  const int live = min(kBlock, T - j * kBlock);
+  const int l16 = threadIdx.x & 15;
+#pragma unroll
+  for (int r = 0; r < kQRounds; ++r) {
+    const int t = (threadIdx.x >> 4) + r * (kQThreads / 16);
+    if (t >= live) break;
+    const uint32_t w = *reinterpret_cast<const uint32_t*>(blk + kKCodes + t * 64 + l16 * 4);
+    const uint32_t sz = *reinterpret_cast<const uint32_t*>(blk + kKScales + t * 16 + (l16 >> 2) * 4);
+    const __nv_bfloat162 s2 = as_bf2(dup_lo(sz)), z2 = as_bf2(dup_hi(sz));
+    k[t * 16 + l16] = make_uint4(key_pair(w, 0, s2, z2), key_pair(w, 1, s2, z2), key_pair(w, 2, s2, z2),
+                                 key_pair(w, 3, s2, z2));
+  }
+#pragma unroll
+  for (int r = 0; r < kQRounds / 2; ++r) {         // a token pair of 8 channels per thread
+    const int pair = (threadIdx.x >> 4) + r * (kQThreads / 16);
+    if (2 * pair >= live) break;
+    const uint2 w = *reinterpret_cast<const uint2*>(blk + value_chunk(pair, l16 >> 1) + (l16 & 1) * 8);
+    const uint2 sz = *reinterpret_cast<const uint2*>(blk + value_scale(pair, l16 >> 2));
+    uint32_t lo[4], hi[4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const uint32_t word = i < 2 ? w.x : w.y;
+      const float2 c0 = __half22float2(as_h2(value_pair(word, (2 * i) & 3, as_h2(sz.x), as_h2(sz.y))));
+      const float2 c1 = __half22float2(as_h2(value_pair(word, (2 * i + 1) & 3, as_h2(sz.x), as_h2(sz.y))));
+      lo[i] = pack_bf16(c0.x, c1.x);
+      hi[i] = pack_bf16(c0.y, c1.y);
+    }
+    v[(2 * pair) * 16 + l16] = make_uint4(lo[0], lo[1], lo[2], lo[3]);
+    if (2 * pair + 1 < live) v[(2 * pair + 1) * 16 + l16] = make_uint4(hi[0], hi[1], hi[2], hi[3]);
+  }
+}
+
+// One decode token: 64 threads per (sequence, group), thread t owns channels 2t and 2t+1 of the
+// key and of the value. When the token completes a compression window the same threads sum the
+// window's 32 stored keys exactly (fixed point, as the bf16 cache's append does).
+constexpr int kAppendPerCta4 = 4;
+
+__global__ void __launch_bounds__(64 * kAppendPerCta4) kv4_append_kernel(const Kv4CacheArgs a, int bg_count) {
+  grid_dep_wait();
+  grid_dep_launch();
+  const int bg = blockIdx.x * kAppendPerCta4 + (int)threadIdx.x / 64, t = threadIdx.x % 64;
+  if (bg >= bg_count) return;                      // whole warps
+  const int b = bg / a.G;
+  const int T = a.seq_len[b];
+  if (T < 1 || T > a.max_ctx) {
+    if (t == 0) atomicOr(a.err, SPARDA_DEV_BAD_SEQ_LEN);
+    return;
+  }
+  const int p = T - 1, tok = p % kBlock;
+  uint8_t* blk = a.kv + ((size_t)bg * a.nb_cap + p / kBlock) * kBlockBytes4;
+  const bool window = T >= kWinKernel && (T - kWinKernel) % kWinStride == 0;
+  // the window's 31 older keys: their words and scales, issued before anything waits
+  uint32_t ww[kWinKernel - 1], ws[kWinKernel - 1];
+  if (window) {
+#pragma unroll
+    for (int u = 0; u < kWinKernel - 1; ++u) {
+      const int pos = T - kWinKernel + u;
+      const uint8_t* src = a.kv + ((size_t)bg * a.nb_cap + pos / kBlock) * kBlockBytes4;
+      ww[u] = *reinterpret_cast<const uint32_t*>(src + kKCodes + (pos % kBlock) * 64 + (t >> 2) * 4);
+      ws[u] = *reinterpret_cast<const uint32_t*>(src + kKScales + (pos % kBlock) * 16 + (t >> 4) * 4);
+    }
+  }
+  const uint32_t kn = reinterpret_cast<const uint32_t*>(a.k + (size_t)bg * kHeadDim)[t];
+  const uint32_t vn = reinterpret_cast<const uint32_t*>(a.v + (size_t)bg * kHeadDim)[t];
+  Grid gk, gv;
+#pragma unroll
+  for (int which = 0; which < 2; ++which) {
+    const uint32_t x = which ? vn : kn;
+    float lo = fminf(bf16_lo(x), bf16_hi(x)), hi = fmaxf(bf16_lo(x), bf16_hi(x));
+    int fin = fabsf(bf16_lo(x)) < INFINITY && fabsf(bf16_hi(x)) < INFINITY;
+#pragma unroll
+    for (int d = 1; d <= 8; d <<= 1) {
+      lo = fminf(lo, __shfl_xor_sync(0xffffffffu, lo, d));
+      hi = fmaxf(hi, __shfl_xor_sync(0xffffffffu, hi, d));
+      fin &= __shfl_xor_sync(0xffffffffu, fin, d);
+    }
+    if (which) gv = make_grid<false>(lo, hi, fin);
+    else gk = make_grid<true>(lo, hi, fin);
+  }
+  // key: four threads make a word
+  const uint32_t ck0 = code_of(bf16_lo(kn), gk), ck1 = code_of(bf16_hi(kn), gk);
+  uint32_t w = (ck0 | (ck1 << 16)) << (4 * (t & 3));
+  w |= __shfl_xor_sync(0xffffffffu, w, 1);
+  w |= __shfl_xor_sync(0xffffffffu, w, 2);
+  w = rol(w, 3);
+  if ((t & 3) == 0) *reinterpret_cast<uint32_t*>(blk + kKCodes + tok * 64 + (t >> 2) * 4) = w;
+  if ((t & 15) == 0) *reinterpret_cast<uint32_t*>(blk + kKScales + tok * 16 + (t >> 4) * 4) = gk.s16 | (gk.z16 << 16);
+  // value: two threads make the half-word of four channels; the other half belongs to the pair's
+  // other token and is kept
+  uint32_t hw = (code_of(bf16_lo(vn), gv) | (code_of(bf16_hi(vn), gv) << 4)) << (8 * (t & 1));
+  hw |= __shfl_xor_sync(0xffffffffu, hw, 1);
+  const int pair = tok >> 1;
+  if ((t & 1) == 0) {
+    uint32_t* word = reinterpret_cast<uint32_t*>(blk + value_chunk(pair, t >> 3) + ((t >> 1) & 3) * 4);
+    *word = rol((tok & 1) ? ((ror(*word, 6) & 0xffffu) | (hw << 16)) : hw, 6);
+  }
+  if ((t & 15) == 0) {
+    uint16_t* sz = reinterpret_cast<uint16_t*>(blk + value_scale(pair, t >> 4)) + (tok & 1);
+    sz[0] = (uint16_t)gv.s16;
+    sz[2] = (uint16_t)gv.z16;
+    if (!(tok & 1)) sz[1] = sz[3] = 0;             // the pair's other token is not there yet
+  }
+  if (!window) return;
+  uint32_t xs[kWinKernel];
+#pragma unroll
+  for (int u = 0; u < kWinKernel - 1; ++u)
+    xs[u] = key_pair(ww[u], t & 3, as_bf2(dup_lo(ws[u])), as_bf2(dup_hi(ws[u])));
+  const uint32_t sz = gk.s16 | (gk.z16 << 16);
+  xs[kWinKernel - 1] = key_pair(w, t & 3, as_bf2(dup_lo(sz)), as_bf2(dup_hi(sz)));
+  reinterpret_cast<uint32_t*>(a.ck + ((size_t)bg * a.W_cap + (T - kWinKernel) / kWinStride) * kHeadDim)[t] =
+      window_mean(xs);
+}
+
+void launch_kv4_quantize(const Kv4CacheArgs& a, int bg_count, cudaStream_t s) {
+  launch_pdl(kv4_quantize_kernel, dim3((unsigned)bg_count * a.nb_cap), dim3(kQThreads), 0, s, a);
+}
+void launch_kv4_dequantize(const Kv4CacheArgs& a, int bg_count, cudaStream_t s) {
+  launch_pdl(kv4_dequantize_kernel, dim3((unsigned)bg_count * (a.idx ? a.kslots : a.nb_cap)), dim3(kQThreads), 0, s, a);
+}
+void launch_kv4_append(const Kv4CacheArgs& a, int bg_count, cudaStream_t s) {
+  launch_pdl(kv4_append_kernel, dim3((bg_count + kAppendPerCta4 - 1) / kAppendPerCta4), dim3(64 * kAppendPerCta4), 0, s, a,
+             bg_count);
+}
+
+}  // namespace sparda

@@ -16,6 +16,8 @@
  *   sparda_sparse_decode_attn  block-sparse GQA decode attention over the selection
  *   sparda_prefetch_blocks     gather of selected blocks from pinned host memory (UVA)
  *   sparda_multihead_select    the baseline query-driven selector, for comparison
+ *   sparda_kv4_*               a layer's cache held in 4 bits: fill, append, attend, read back
+ *   sparda_evict_blocks        eviction of blocks by the attention weight they received
  *
  * Conventions shared by every call
  *   - All tensors are caller-owned. The library never allocates, frees or synchronises on
@@ -75,6 +77,9 @@ extern "C" {
 #define SPARDA_WS_ATTN        2
 #define SPARDA_WS_MULTIHEAD   3
 #define SPARDA_WS_PREFILL     4
+#define SPARDA_WS_ATTN_MASS     5  /* sparda_sparse_decode_attn_mass                       */
+#define SPARDA_WS_KV4_ATTN      6  /* sparda_kv4_decode_attn without mass                  */
+#define SPARDA_WS_KV4_ATTN_MASS 7  /* sparda_kv4_decode_attn with mass                     */
 
 /* ---------------------------------------------------------------- shapes */
 /*
@@ -566,6 +571,144 @@ int32_t sparda_prefill_multihead_select(const sparda_shape* shape, const void* c
 int32_t sparda_prefill_attn(const sparda_shape* shape, const sparda_layer_kv* layer, const void* q,
                             const int32_t* idx, const int32_t* cnt, const int32_t* seq_len, int32_t batch,
                             void* out, void* stream);
+
+/* ---------------------------------------------------------------- the 4-bit KV cache */
+/*
+ * A resident layer's keys and values held in 4 bits: 160 bytes per token and KV group instead of
+ * 512. An extension beyond the pages.
+ *
+ * Every row (one token's key or value of one group, 128 channels) is four groups of 32 channels,
+ * each with its own grid of 16 levels, a scale s and an offset z of 16 bits each:
+ *   s = T((hi - lo) / 15)     z = T(lo - 16 s)     code = clamp(rint((x - z) / s - 16), 0, 15)
+ *   value(code) = T(s (16 + code) + z)
+ * lo and hi are the group's smallest and largest value, T() rounds to bf16 for keys and to fp16
+ * for values (to nearest even), the subtractions and divisions before T are float32 operations,
+ * each rounded once, rint rounds halves to even, and s (16 + code) + z is rounded once. A group
+ * whose s is 0 has codes 0. A group that holds an infinity or a NaN, or whose s or z overflows T
+ * (values beyond about 60000 in magnitude), stands for NaN in all 32 channels. A value differs
+ * from x by at most s/2 plus the roundings of z and of the value itself.
+ *
+ *   kv     uint8 [max_batch, G, max_ctx/64, SPARDA_KV4_BLOCK_BYTES], device memory: the 64-token
+ *          blocks, keys and values of a block together (the layout inside a block is the
+ *          library's own; blocks may be copied whole).
+ *   ck     bf16 [max_batch, G, W_cap, d]: compressed keys, as in sparda_layer_kv. After a prefill
+ *          they come from the bf16 keys (sparda_compress_keys); tokens appended later form them
+ *          from the stored values.
+ *
+ * The calls take any heads_per_group from 1 to 16 (the other shape rules are sparda_check_shape's).
+ * They begin while the kernel before them in the stream still runs (programmatic dependent
+ * launch), wait for it to complete before they read or write anything, and let the next launch
+ * begin only then. All pointers 16-byte aligned, index and length arrays 4-byte.
+ */
+#define SPARDA_KV4_BLOCK_BYTES 10240
+
+typedef struct sparda_layer_kv4 {
+  void* kv;
+  void* ck;
+} sparda_layer_kv4;
+
+/*
+ * sparda_kv4_quantize -- a prompt into the 4-bit cache: tokens 0 .. seq_len[b]-1 of k and v (bf16
+ * [max_batch, G, max_ctx, d], as a resident sparda_layer_kv holds them, so that one bf16 cache can
+ * serve every layer's prefill in turn). Rows of the last block past the prompt become zeros;
+ * later blocks, and sequences at and past batch, stay as they were. ck is not touched.
+ */
+int32_t sparda_kv4_quantize(const sparda_shape* shape, const sparda_layer_kv4* layer, const void* k, const void* v,
+                            const int32_t* seq_len, int32_t batch, void* stream);
+
+/*
+ * sparda_kv4_dequantize -- the values back as bf16 (value rows rounded once more, from fp16), for
+ * the entry points that read bf16 caches, such as the prefill of a conversation's next turn.
+ * idx and cnt NULL: the rows of every token, into k and v bf16 [max_batch, G, max_ctx, d].
+ * Otherwise the blocks idx[b, g, 0 .. cnt[b,g]-1] (int32 [B, G, topk+2]), slot s into rows
+ * [b, g, s, 0 .. 63] of k and v bf16 [max_batch, G, topk+2, 64, d], the layout of
+ * sparda_prefetch_blocks' staging buffers. Rows at and past seq_len[b] are left as they were. A
+ * block index outside 0 .. (seq_len[b]-1)/64 sets SPARDA_DEV_BAD_INDEX and its slot is left.
+ */
+int32_t sparda_kv4_dequantize(const sparda_shape* shape, const sparda_layer_kv4* layer, const int32_t* idx,
+                              const int32_t* cnt, const int32_t* seq_len, int32_t batch, void* k, void* v, void* stream);
+
+/*
+ * sparda_kv4_append -- the current token's key and value (k_new, v_new: bf16 [B, G, d]) at position
+ * seq_len[b]-1 of the 4-bit cache, and the compressed key of the window it completes: the mean of
+ * the window's 32 stored key values, exact, rounded once to bf16. The counterpart of
+ * sparda_append_kv; the same ordering rule holds for a selection right behind it (it writes only
+ * the window that the selection does not score yet).
+ */
+int32_t sparda_kv4_append(const sparda_shape* shape, const sparda_layer_kv4* layer, const void* k_new,
+                          const void* v_new, const int32_t* seq_len, int32_t batch, void* stream);
+
+/*
+ * sparda_kv4_decode_attn -- sparda_sparse_decode_attn over the 4-bit cache, with the stored values as
+ * keys and values: for every query head h of group g (q, out: bf16 [B, G*H, d], H = 1 .. 16)
+ *   out[b, g*H + h, :] = sum_t softmax_t(q . k_t / sqrt(d)) v_t
+ * over the tokens t < seq_len[b] of the blocks idx[b, g, 0 .. cnt[b,g]-1], or, with idx and cnt
+ * NULL, over all tokens t < seq_len[b]. A block named twice counts twice; an index outside the
+ * sequence's blocks sets SPARDA_DEV_BAD_INDEX and is skipped; with nothing to attend (cnt 0, a bad
+ * seq_len) the output is zero. mass: NULL, or the block weights to add to (as
+ * sparda_sparse_decode_attn_mass); with mass the call is two launches.
+ * workspace: SPARDA_WS_KV4_ATTN, with mass SPARDA_WS_KV4_ATTN_MASS.
+ */
+int32_t sparda_kv4_decode_attn(const sparda_shape* shape, const sparda_layer_kv4* layer, const void* q,
+                               const int32_t* idx, const int32_t* cnt, const int32_t* seq_len, int32_t batch,
+                               void* out, float* mass, void* workspace, size_t workspace_bytes, void* stream);
+
+/* ---------------------------------------------------------------- block mass and eviction */
+/*
+ * An extension beyond the pages, for caches that must not grow with the conversation: attention
+ * calls add up the weight that each 64-token block receives, and the blocks with the least of it
+ * are evicted. mass: float32 [max_batch, G, max_ctx/64], zeroed by the caller at the start.
+ */
+
+/*
+ * sparda_sparse_decode_attn_mass -- sparda_sparse_decode_attn of a resident layer (the same output,
+ * bit for bit) that also adds to mass[b, g, j], for every block j = idx[b, g, s], s < cnt[b,g],
+ *   sum over the group's heads h and the block's tokens t < T of softmax_t(q_h . k_t / sqrt(d)).
+ * A block named twice in idx is added twice; an index outside the sequence's blocks adds nothing.
+ * Two launches; mass is added to in place, in an order that does not change the result. Two calls
+ * that may run at the same time must not share mass. workspace: SPARDA_WS_ATTN_MASS.
+ * SPARDA_ERR_INVALID_ARG for an offloaded layer.
+ */
+int32_t sparda_sparse_decode_attn_mass(const sparda_shape* shape, const sparda_layer_kv* layer, const void* q,
+                                       const int32_t* idx, const int32_t* cnt, const int32_t* seq_len, int32_t batch,
+                                       void* out, float* mass, void* workspace, size_t workspace_bytes, void* stream);
+
+/*
+ * sparda_evict_blocks -- every sequence of more than `keep` blocks is cut to `keep`: block 0, its
+ * `recent` newest blocks (the partly filled last one among them) and, of the rest, each group's
+ * blocks with the largest mass (ties to the lower block; a NaN ranks above every number). The
+ * kept blocks move to the front in their order, so block n of the result was block
+ * kept[b, g, n], and
+ *   dst_seq_len[b] = seq_len[b] - 64 (blocks - min(blocks, keep)).
+ * Keys carry their positions with them (rotary embeddings are applied before they are cached).
+ * Compressed keys: windows inside one block move with it; a window across two blocks that were
+ * not neighbours is formed anew (the exact mean of its 32 keys rounded to bf16, for a 4-bit cache
+ * of their stored values); rows past the result's complete windows are left as they were.
+ * dst_mass[b, g, n] = mass[b, g, kept[b, g, n]], and 0 from there to the end of the row.
+ *
+ * In place: dst_shape and dst NULL (dst_mass and dst_seq_len too): layer, mass and seq_len are
+ * updated. Otherwise dst is another resident cache of dst_shape (n_groups equal, max_batch >= batch,
+ * max_ctx >= 64 keep, smaller or larger than the source's) that shares no memory with the source,
+ * dst_mass float32 [max_batch, G, max_ctx/64] of dst_shape, dst_seq_len int32 [B], and the source
+ * stays as it was. kept: int32 [B, G, keep], written: the old block numbers, ascending, -1 behind.
+ * A sequence with a seq_len out of range keeps everything as it is (kept -1; into another cache,
+ * its length is copied) and sets SPARDA_DEV_BAD_SEQ_LEN. Sequences at and past batch stay as they were.
+ *
+ * SPARDA_ERR_INVALID_ARG: an offloaded layer, recent < 1, keep <= recent, only some of the dst
+ * arguments NULL, a dst buffer that is the source's. SPARDA_ERR_UNSUPPORTED_SHAPE: dst_shape too
+ * small, other groups, or keep above 4096. Ordering: as sparda_compress_keys, the call must not be
+ * the kernel just before a selection that scores this cache.
+ */
+int32_t sparda_evict_blocks(const sparda_shape* shape, const sparda_layer_kv* layer, float* mass, int32_t* seq_len,
+                            const sparda_shape* dst_shape, const sparda_layer_kv* dst, float* dst_mass,
+                            int32_t* dst_seq_len, int32_t batch, int32_t keep, int32_t recent, int32_t* kept,
+                            void* stream);
+
+/* sparda_kv4_evict_blocks -- the same of a 4-bit cache (heads_per_group 1 to 16). */
+int32_t sparda_kv4_evict_blocks(const sparda_shape* shape, const sparda_layer_kv4* layer, float* mass,
+                                int32_t* seq_len, const sparda_shape* dst_shape, const sparda_layer_kv4* dst,
+                                float* dst_mass, int32_t* dst_seq_len, int32_t batch, int32_t keep, int32_t recent,
+                                int32_t* kept, void* stream);
 
 #ifdef __cplusplus
 }

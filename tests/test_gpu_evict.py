@@ -1,0 +1,227 @@
+"""Eviction of cache blocks by accumulated attention weight, bf16 and 4-bit caches, in place and into
+another cache, against a plain restatement (tests/kv4_reference.py). Moves are compared byte for
+byte, compressed keys with the exact means of the moved keys."""
+import numpy as np
+import pytest
+import torch
+
+import synth
+from oracle import sparda_oracle as O
+from tests import kv4_reference as R
+from tests.parity import to64
+
+pytestmark = pytest.mark.gpu
+
+
+@pytest.fixture(scope="module")
+def sb(cuda_ok):
+    from block_sparse_attention_forecast_gb300 import build
+    build.build()
+    import block_sparse_attention_forecast_gb300.binding as b
+    b.sparda_device_error(clear=True)
+    return b
+
+
+def _i32(x):
+    return torch.tensor(x, dtype=torch.int32, device="cuda")
+
+
+def _mass(B, G, nb, kind, seed):
+    rng = np.random.default_rng(seed)
+    if kind == "ties":
+        m = rng.integers(0, 3, size=(B, G, nb)).astype(np.float32)
+    elif kind == "zero":
+        m = np.zeros((B, G, nb), dtype=np.float32)
+        m[:, :, ::3] = -0.0
+    else:
+        m = np.exp(1.5 * rng.standard_normal((B, G, nb))).astype(np.float32)
+        m[rng.random((B, G, nb)) < 0.3] = 0
+    if kind == "special":
+        m.reshape(-1)[::7] = np.nan
+        m.reshape(-1)[3::11] = np.inf
+        m.reshape(-1)[4::13] = -1.0
+    return torch.from_numpy(m)
+
+
+def _case(sb, kv4, T_list, G, ctx, mass_kind, seed):
+    """(shape, layer, K as stored, mass) with one sequence behind the batch."""
+    B = len(T_list) + 1
+    shape = sb.Shape(n_groups=G, max_ctx=ctx, max_batch=B)
+    K, V = synth.normal_bf16((B, G, ctx, 128), seed, 1), synth.normal_bf16((B, G, ctx, 128), seed, 2)
+    bf = sb.LayerKV.empty(shape)
+    bf.k.copy_(K.cuda())
+    bf.v.copy_(V.cuda())
+    full = _i32([min(max(t, 1), ctx) for t in T_list] + [ctx])
+    sb.sparda_compress_keys(shape, bf, full, B)
+    if not kv4:
+        return shape, bf, K, _mass(B, G, ctx // 64, mass_kind, seed)
+    layer = sb.LayerKV4.empty(shape)
+    layer.kv.fill_(0x5a)
+    sb.sparda_kv4_quantize(shape, layer, bf.k, bf.v, full, B)
+    layer.ck.copy_(bf.ck)
+    return shape, layer, torch.from_numpy(R.grid_values(K, True)), _mass(B, G, ctx // 64, mass_kind, seed)
+
+
+def _planes(layer):
+    """The cache's planes as byte tensors [B, G, nb, bytes per block]."""
+    if hasattr(layer, "kv"):
+        return [layer.kv]
+    return [x.view(torch.uint8).view(*x.shape[:2], -1, 64 * 256) for x in (layer.k, layer.v)]
+
+
+def _check(shape, before, after, K, mass, m_after, T_list, lens, kept, keep, recent, ck_before, dst_nb, untouched_ck):
+    G = shape.n_groups
+    for b, T in enumerate(T_list):
+        n = (T - 1) // 64 + 1
+        count = min(n, keep)
+        assert int(lens[b]) == T - 64 * (n - count)
+        W = O.num_windows(int(lens[b]))
+        for g in range(G):
+            m = mass[b, g].numpy()
+            blocks = R.kept_blocks(m.astype(np.float64), n, keep, recent)
+            assert [int(x) for x in kept[b, g]] == blocks + [-1] * (keep - count), (b, g)
+            for x, y in zip(before, after):
+                assert torch.equal(y[b, g, :count], x[b, g, blocks])
+            got = m_after[b, g].numpy()
+            assert np.array_equal(got[:count], m[blocks], equal_nan=True) and (got[count:dst_nb] == 0).all()
+            want = untouched_ck[b, g].clone()
+            for i, j in enumerate(blocks):
+                for w in range(4):
+                    if 4 * i + w >= W:
+                        continue
+                    if w < 3 or blocks[i + 1] == j + 1:
+                        want[4 * i + w] = ck_before[b, g, 4 * j + w]
+                    else:
+                        span = np.concatenate([to64(K[b, g, 64 * j + 48:64 * j + 64]),
+                                               to64(K[b, g, 64 * blocks[i + 1]:64 * blocks[i + 1] + 16])])
+                        want[4 * i + w] = torch.from_numpy(O.compress_keys(span, 1)[0]).to(torch.bfloat16)
+            yield b, g, want
+
+
+CASES = [
+    # T_list, G, ctx, keep, recent, weights
+    ([1000, 64, 1, 640, 65], 2, 1024, 4, 1, "plain"),
+    ([4096, 4095, 4033, 4032, 3000], 3, 4096, 17, 5, "plain"),
+    ([4096, 2000], 1, 4096, 33, 32, "plain"),
+    ([4000, 4096], 2, 4096, 40, 1, "ties"),
+    ([4096], 2, 4096, 63, 2, "zero"),
+    ([4096, 100], 2, 4096, 64, 2, "plain"),
+    ([8000, 8192, 5000], 2, 8192, 21, 3, "special"),
+    ([16384], 1, 16384, 200, 8, "plain"),
+    ([2048] * 40, 4, 2048, 9, 2, "ties"),
+]
+
+
+@pytest.mark.parametrize("in_place", [False, True])
+@pytest.mark.parametrize("kv4", [False, True])
+@pytest.mark.parametrize("case", range(len(CASES)))
+def test_evict(sb, case, kv4, in_place):
+    T_list, G, ctx, keep, recent, kind = CASES[case]
+    B, nb = len(T_list), ctx // 64
+    shape, layer, K, mass = _case(sb, kv4, T_list, G, ctx, kind, 200 + case)
+    before = [x.cpu().clone() for x in _planes(layer)]
+    ck_before = layer.ck.cpu().clone()
+    m = mass.cuda()
+    seq = _i32(T_list)
+    kept = torch.full((B + 1, G, keep), -7, dtype=torch.int32, device="cuda")
+    evict = sb.sparda_kv4_evict_blocks if kv4 else sb.sparda_evict_blocks
+    if in_place:
+        evict(shape, layer, m, seq, B, keep, recent, kept)
+        after, m_after, lens, dst_nb, ck_after, untouched = layer, m, seq, nb, layer.ck, ck_before
+    else:
+        dshape = sb.Shape(n_groups=G, max_ctx=64 * (keep + 3), max_batch=B + 2)
+        after = (sb.LayerKV4 if kv4 else sb.LayerKV).empty(dshape)
+        for x in _planes(after):
+            x.fill_(0x33)
+        after.ck.fill_(5)
+        untouched = after.ck.cpu().clone()
+        dst_nb = keep + 3
+        m_after = torch.full((B + 2, G, dst_nb), 11.0, device="cuda")
+        lens = _i32([-1] * B)
+        evict(shape, layer, m, seq, B, keep, recent, kept, dst_shape=dshape, dst=after, dst_mass=m_after, dst_seq_len=lens)
+        ck_after = after.ck
+    torch.cuda.synchronize()
+    assert sb.sparda_device_error(clear=True) == 0
+    planes = [x.cpu() for x in _planes(after)]
+    got_ck = ck_after.cpu()
+    seen = 0
+    for b, g, want in _check(shape, before, planes, K, mass, m_after.cpu(), T_list, lens.cpu(), kept.cpu(), keep, recent,
+                             ck_before, dst_nb, untouched):
+        W = O.num_windows(int(lens[b]))
+        assert torch.equal(got_ck[b, g, :W], want[:W]), (b, g)
+        if not in_place:
+            assert (got_ck[b, g, W:] == 5).all()
+        seen += 1
+    assert seen == B * G
+    # the sequence behind the batch
+    assert (kept[B] == -7).all()
+    if in_place:
+        for x, y in zip(before, planes):
+            assert torch.equal(y[B], x[B])
+        assert torch.equal(got_ck[B], ck_before[B])
+        assert np.array_equal(m[B].cpu().numpy(), mass[B].numpy(), equal_nan=True)
+    else:
+        for x, y in zip(before, _planes(layer)):
+            assert torch.equal(y.cpu(), x)                     # the source stays
+        assert torch.equal(seq.cpu(), torch.tensor(T_list, dtype=torch.int32))
+        assert (m_after[B:] == 11).all()
+        for y in planes:
+            assert (y[B:] == 0x33).all()
+
+
+@pytest.mark.parametrize("in_place", [False, True])
+def test_evict_reports_bad_lengths(sb, in_place):
+    shape, layer, _, mass = _case(sb, True, [1024, 1024, 1024], 2, 1024, "plain", 300)
+    m, seq = mass.cuda(), _i32([0, 1024, 1025])
+    kept = torch.zeros((3, 2, 4), dtype=torch.int32, device="cuda")
+    before = layer.kv.clone()
+    if in_place:
+        sb.sparda_kv4_evict_blocks(shape, layer, m, seq, 3, 4, 1, kept)
+        lens, after = seq, layer.kv
+        same = before
+    else:
+        dshape = sb.Shape(n_groups=2, max_ctx=256, max_batch=3)
+        dst = sb.LayerKV4.empty(dshape)
+        dst.kv.fill_(0x33)
+        same = dst.kv.clone()
+        lens = _i32([9, 9, 9])
+        sb.sparda_kv4_evict_blocks(shape, layer, m, seq, 3, 4, 1, kept, dst_shape=dshape, dst=dst,
+                                   dst_mass=torch.zeros((3, 2, 4), device="cuda"), dst_seq_len=lens)
+        after = dst.kv
+    torch.cuda.synchronize()
+    assert sb.sparda_device_error(clear=True) == sb.DEV_BAD_SEQ_LEN
+    assert lens.tolist() == [0, 256, 1025]
+    assert (kept[0] == -1).all() and (kept[2] == -1).all() and (kept[1] >= 0).all()
+    assert torch.equal(after[0], same[0]) and torch.equal(after[2], same[2])
+
+
+def test_evict_then_compress_agrees(sb):
+    """After an in-place eviction of a bf16 cache the compressed keys are what sparda_compress_keys
+    builds from the moved keys, and a second eviction continues from there (in a graph)."""
+    T_list, G, ctx, keep = [4000, 3000], 2, 4096, 20
+    shape, layer, _, mass = _case(sb, False, T_list, G, ctx, "plain", 400)
+    m, seq = mass.cuda(), _i32(T_list)
+    kept = torch.zeros((2, G, keep), dtype=torch.int32, device="cuda")
+    sb.sparda_evict_blocks(shape, layer, m, seq, 2, keep, 4, kept)
+    fresh = sb.LayerKV(layer.k, layer.v, torch.zeros_like(layer.ck))
+    sb.sparda_compress_keys(shape, fresh, seq, 2)
+    torch.cuda.synchronize()
+    for b in range(2):
+        W = O.num_windows(int(seq[b]))
+        assert torch.equal(layer.ck[b, :, :W], fresh.ck[b, :, :W])
+    graph = torch.cuda.CUDAGraph()
+    k2 = torch.zeros((2, G, 9), dtype=torch.int32, device="cuda")
+    with torch.cuda.graph(graph):
+        sb.sparda_evict_blocks(shape, layer, m, seq, 2, 9, 2, k2)
+    want = [R.kept_blocks(m[b, g, :].double().cpu().numpy(), (int(seq[b]) - 1) // 64 + 1, 9, 2) for b in range(2) for g in range(G)]
+    kb = layer.k.clone()
+    graph.replay()
+    torch.cuda.synchronize()
+    assert sb.sparda_device_error(clear=True) == 0
+    for i, blocks in enumerate(want):
+        b, g = divmod(i, G)
+        assert k2[b, g].tolist() == blocks
+        assert torch.equal(layer.k[b, g].view(-1, 64, 128)[:9], kb[b, g].view(-1, 64, 128)[blocks])
+    graph.replay()                                             # nothing left to evict
+    torch.cuda.synchronize()
+    assert [int((t - 1) // 64 + 1) for t in seq.tolist()] == [9, 9] and k2[0, 0].tolist() == list(range(9))

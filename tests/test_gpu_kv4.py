@@ -1,0 +1,434 @@
+"""The 4-bit KV cache on the GPU against the 64-bit reference (tests/kv4_reference.py)."""
+import numpy as np
+import pytest
+import torch
+
+import synth
+from oracle import sparda_oracle as O
+from tests import kv4_reference as R
+from tests.parity import to64
+
+pytestmark = pytest.mark.gpu
+
+W16 = 2.0 ** -11                  # an attention weight as an fp16 operand
+
+
+@pytest.fixture(scope="module")
+def sb(cuda_ok):
+    from block_sparse_attention_forecast_gb300 import build
+    build.build()
+    import block_sparse_attention_forecast_gb300.binding as b
+    b.sparda_device_error(clear=True)
+    return b
+
+
+def _i32(x):
+    return torch.tensor(x, dtype=torch.int32, device="cuda")
+
+
+def _kv(shape, seed):
+    dims = (shape.max_batch, shape.n_groups, shape.max_ctx, 128)
+    K = synth.normal_bf16(dims, seed, 1)
+    K[..., 5] *= 6                                        # a strong channel and an offset, as keys have
+    K = (K.float() + 0.5 * synth.normal_bf16((1, shape.n_groups, 1, 128), seed, 2).float()).to(torch.bfloat16)
+    return K, synth.normal_bf16(dims, seed, 3)
+
+
+def _filled(sb, shape, K, V, T_list):
+    """A LayerKV4 whose memory held garbage (0xff: NaN scales) before the prompt was written."""
+    layer = sb.LayerKV4.empty(shape)
+    layer.kv.fill_(0xff)
+    sb.sparda_kv4_quantize(shape, layer, K.cuda(), V.cuda(), _i32(T_list), len(T_list))
+    return layer
+
+
+def _read(sb, shape, layer, T_list, fill=7.0):
+    k = torch.full((shape.max_batch, shape.n_groups, shape.max_ctx, 128), fill, dtype=torch.bfloat16, device="cuda")
+    v = torch.full_like(k, fill)
+    sb.sparda_kv4_dequantize(shape, layer, _i32(T_list), len(T_list), k, v)
+    torch.cuda.synchronize()
+    assert sb.sparda_device_error(clear=True) == 0
+    return k.cpu(), v.cpu()
+
+
+def _v16(V):
+    """The value rows as the attention reads them (fp16), float64."""
+    return R.grid_values(V, key=False)
+
+
+def _bf(x):
+    return torch.from_numpy(x).to(torch.bfloat16)
+
+
+# ------------------------------------------------------------------ quantize / dequantize
+@pytest.mark.parametrize("T_list,G,ctx", [([1, 2, 31, 32, 33, 63, 64], 1, 64), ([65, 127, 128, 129, 200], 3, 256),
+                                          ([1000, 1, 4096], 2, 4096)])
+def test_prompt_values_exact(sb, T_list, G, ctx):
+    shape = sb.Shape(n_groups=G, heads_per_group=3, max_ctx=ctx, max_batch=len(T_list) + 1)
+    K, V = _kv(shape, 11)
+    layer = _filled(sb, shape, K, V, T_list)
+    k, v = _read(sb, shape, layer, T_list)
+    kr, vr = R.grid_values(K, True), _v16(V)
+    for b, T in enumerate(T_list):
+        assert torch.equal(k[b, :, :T], _bf(kr[b, :, :T])), T
+        assert torch.equal(v[b, :, :T], _bf(vr[b, :, :T])), T
+        assert (k[b, :, T:] == 7).all() and (v[b, :, T:] == 7).all()
+    assert (k[len(T_list):] == 7).all()
+    assert (layer.kv[len(T_list):] == 0xff).all()         # the sequence behind the batch
+    # the grid's own promise: within half a step, plus the roundings of z (2^-8 / 2^-11 of |z|) and
+    # of the value (the same of |x|)
+    for X, ref, r in ((K, kr, 2.0 ** -8), (V, vr, 2.0 ** -11)):
+        x = to64(X).reshape(-1, 32)
+        y = ref.reshape(-1, 32)
+        lo, hi = x.min(1, keepdims=True), x.max(1, keepdims=True)
+        s = (hi - lo) / 15 * (1 + r)
+        bound = s / 2 + r * (np.abs(lo) + 16 * s) * 1.01 + 15 * r * s + r * np.abs(x).max(1, keepdims=True) + 1e-30
+        assert (np.abs(x - y) <= bound).all()
+
+
+def test_prompt_special_groups(sb):
+    shape = sb.Shape(n_groups=1, max_ctx=64, max_batch=1)
+    K, V = _kv(shape, 12)
+    rows = [torch.zeros(128), torch.full((128,), 3.0), torch.full((128,), -1e-30), torch.full((128,), 1e38),
+            torch.cat([torch.full((32,), x) for x in (float("inf"), float("nan"), float("-inf"), 2.0)]),
+            torch.linspace(-3e38, 3e38, 128), torch.linspace(-7e4, 7e4, 128), torch.linspace(100, 100.5, 128),
+            torch.linspace(-1e-39, 1e-39, 128), torch.linspace(1e-6, 3e-6, 128), -torch.zeros(128)]
+    for r, x in enumerate(rows):
+        K[0, 0, r] = x.to(torch.bfloat16)
+        V[0, 0, r] = x.to(torch.bfloat16)
+    K[0, 0, 20, 7] = float("nan")
+    V[0, 0, 21, 100] = float("inf")
+    layer = _filled(sb, shape, K, V, [64])
+    k, v = _read(sb, shape, layer, [64])
+    assert np.array_equal(to64(k), to64(_bf(R.grid_values(K, True))), equal_nan=True)
+    assert np.array_equal(to64(v), to64(_bf(_v16(V))), equal_nan=True)
+    assert torch.isnan(k[0, 0, 20, :32]).all() and not torch.isnan(k[0, 0, 20, 32:]).any()
+    assert torch.isnan(k[0, 0, 4, :96]).all() and (k[0, 0, 4, 96:] == 2).all()
+
+
+def test_dequantize_selected_blocks(sb):
+    T_list = [300, 64, 700]
+    shape = sb.Shape(n_groups=2, max_ctx=704, max_batch=4, topk=3)
+    K, V = _kv(shape, 13)
+    layer = _filled(sb, shape, K, V, T_list)
+    full_k, full_v = _read(sb, shape, layer, T_list)
+    idx = _i32([[[0, 4, 2, -1, -1], [4, 0, 0, 1, 3]], [[0, -1, -1, -1, -1]] * 2, [[10, 5, 3, 1, 0], [7, 9, -1, -1, -1]]])
+    cnt = _i32([[3, 5], [1, 0], [5, 2]])
+    st = torch.full((4, 2, 5, 64, 128), 9.0, dtype=torch.bfloat16, device="cuda")
+    sv = st.clone()
+    sb.sparda_kv4_dequantize(shape, layer, _i32(T_list), 3, st, sv, idx=idx, cnt=cnt)
+    torch.cuda.synchronize()
+    assert sb.sparda_device_error(clear=True) == 0
+    for b, T in enumerate(T_list):
+        for g in range(2):
+            for s in range(5):
+                j = int(idx[b, g, s])
+                live = max(0, min(64, T - 64 * j)) if s < int(cnt[b, g]) else 0
+                assert torch.equal(st[b, g, s, :live].cpu(), full_k[b, g, 64 * j:64 * j + live])
+                assert torch.equal(sv[b, g, s, :live].cpu(), full_v[b, g, 64 * j:64 * j + live])
+                assert (st[b, g, s, live:] == 9).all() and (sv[b, g, s, live:] == 9).all()
+    assert (st[3] == 9).all()
+    # an index outside the sequence: reported, its slot left
+    bad = idx.clone()
+    bad[1, 0, 0] = 1
+    st.fill_(9)
+    sb.sparda_kv4_dequantize(shape, layer, _i32(T_list), 3, st, sv, idx=bad, cnt=cnt)
+    torch.cuda.synchronize()
+    assert sb.sparda_device_error(clear=True) == sb.DEV_BAD_INDEX
+    assert (st[1, 0] == 9).all() and torch.equal(st[0, 0, 1, :44].cpu(), full_k[0, 0, 256:300])
+
+
+# ------------------------------------------------------------------ append
+def test_append_equals_prompt_token_by_token(sb):
+    """From an empty cache of garbage, 150 tokens one at a time: the stored bytes of the values are
+    those of a prompt, and every completed window's compressed key is the exact mean of its stored
+    keys rounded to bf16."""
+    n = 150
+    shape = sb.Shape(n_groups=3, heads_per_group=1, max_ctx=192, max_batch=3)
+    K, V = _kv(shape, 21)
+    layer = sb.LayerKV4.empty(shape)
+    layer.kv.fill_(0xff)
+    layer.ck.fill_(5)
+    seq = _i32([0, 30])                                        # the second sequence starts behind 30 tokens
+    pre = _filled(sb, shape, K, V, [1, 30])
+    layer.kv[1] = pre.kv[1]
+    for step in range(n):
+        seq += 1
+        T = seq.tolist()
+        kn = torch.stack([K[b, :, T[b] - 1] for b in range(2)]).cuda()
+        vn = torch.stack([V[b, :, T[b] - 1] for b in range(2)]).cuda()
+        sb.sparda_kv4_append(shape, layer, kn, vn, seq, 2)
+        if step in (0, 1, 31, 63, 64, 65, n - 1):
+            k, v = _read(sb, shape, layer, T)
+            for b in range(2):
+                assert torch.equal(k[b, :, :T[b]], _bf(R.grid_values(K[b, :, :T[b]], True))), (step, b)
+                assert torch.equal(v[b, :, :T[b]], _bf(_v16(V[b, :, :T[b]]))), (step, b)
+    kr = R.grid_values(K, True)
+    for b in range(2):
+        W = O.num_windows(T[b])
+        for g in range(3):
+            want = O.compress_keys(kr[b, g, :T[b]], W)
+            # the second sequence's first 30 tokens came as a prompt, which leaves ck alone; every
+            # window completes by a later append, so all are written
+            assert np.array_equal(to64(layer.ck[b, g, :W]), want), (b, g)
+    assert (layer.ck[:2, :, O.num_windows(180):] == 5).all() and (layer.ck[2] == 5).all()
+    assert (layer.kv[2] == 0xff).all()
+
+
+def test_append_reports_bad_lengths(sb):
+    shape = sb.Shape(n_groups=1, max_ctx=128, max_batch=3)
+    layer = sb.LayerKV4.empty(shape)
+    layer.kv.fill_(0xaa)
+    x = torch.ones((3, 1, 128), dtype=torch.bfloat16, device="cuda")
+    sb.sparda_kv4_append(shape, layer, x, x, _i32([0, 129, -5]), 3)
+    torch.cuda.synchronize()
+    assert sb.sparda_device_error(clear=True) == sb.DEV_BAD_SEQ_LEN
+    assert (layer.kv == 0xaa).all()
+
+
+# ------------------------------------------------------------------ attention
+def _check_attention(sb, shape, layer, K, V, T_list, q, idx, cnt, mass=False, ws=None):
+    B, G, H = len(T_list), shape.n_groups, shape.heads_per_group
+    out = torch.full((shape.max_batch, G * H, 128), 3.0, dtype=torch.bfloat16, device="cuda")
+    ws = ws if ws is not None else sb.workspace(shape, B, sb.WS_KV4_ATTN_MASS if mass else sb.WS_KV4_ATTN)
+    m0 = m = None
+    if mass:
+        m = synth.normal_bf16((shape.max_batch, G, shape.max_ctx // 64), 99).float().abs().cuda()
+        m0 = to64(m)
+    sb.sparda_kv4_decode_attn(shape, layer, q.cuda(), idx, cnt, _i32(T_list), B, out, ws, mass=m)
+    torch.cuda.synchronize()
+    assert sb.sparda_device_error(clear=True) == 0
+    assert (out[B:] == 3).all()
+    o = to64(out)
+    for b, T in enumerate(T_list):
+        nb = (T - 1) // 64 + 1
+        for g in range(G):
+            blocks = None if idx is None else [int(x) for x in idx[b, g, :int(cnt[b, g])]]
+            k = R.grid_values(K[b, g, :64 * nb], True)
+            v = _v16(V[b, g, :64 * nb])
+            ref, tol, w, wtol = R.attention(to64(q[b, g * H:(g + 1) * H]), k, v, blocks, T, W16)
+            err = np.abs(o[b, g * H:(g + 1) * H] - ref)
+            assert (err <= tol).all(), (b, g, T, float((err - tol).max()))
+            if mass:
+                want = m0[b, g].copy()
+                per = np.zeros(shape.max_ctx // 64)
+                for j, x in zip(blocks if blocks is not None else range(nb), w):
+                    per[j] += x
+                want += per
+                err = np.abs(to64(m[b, g]) - want)
+                assert (err <= wtol * per + 2.0 ** -22 * np.abs(want)).all(), (b, g, float(err.max()))
+    if mass:
+        assert np.array_equal(to64(m[B:]), m0[B:])
+    return out
+
+
+def _select(rng, T_list, G, topk):
+    """Block 0, the tail block and up to topk others, ascending, -1 padded."""
+    idx = -np.ones((len(T_list), G, topk + 2), dtype=np.int32)
+    cnt = np.zeros((len(T_list), G), dtype=np.int32)
+    for b, T in enumerate(T_list):
+        tb = (T - 1) // 64
+        for g in range(G):
+            pool = np.arange(1, tb)
+            pick = rng.choice(pool, size=min(topk, len(pool)), replace=False) if len(pool) else []
+            sel = sorted({0, tb} | set(int(x) for x in pick))
+            idx[b, g, :len(sel)] = sel
+            cnt[b, g] = len(sel)
+    return torch.from_numpy(idx).cuda(), torch.from_numpy(cnt).cuda()
+
+
+CASES = [
+    # T_list, G, H, ctx, topk (0: all blocks)
+    ([1], 1, 1, 64, 0),
+    ([1, 2, 15, 16, 17, 63, 64, 65], 2, 16, 128, 0),
+    ([64, 128, 129, 1000], 3, 5, 1024, 0),
+    ([5000], 2, 16, 5056, 0),
+    ([33, 4097, 700], 1, 9, 4160, 0),
+    ([1, 64, 65, 130], 2, 16, 192, 8),
+    ([4096, 3000, 2500], 2, 16, 4096, 8),
+    ([4096], 1, 8, 4096, 62),
+    ([777] * 20, 2, 2, 832, 4),
+    ([640, 100] * 40, 2, 4, 640, 0),
+]
+
+
+@pytest.mark.parametrize("mass", [False, True])
+@pytest.mark.parametrize("case", range(len(CASES)))
+def test_attention(sb, case, mass):
+    T_list, G, H, ctx, topk = CASES[case]
+    B = len(T_list)
+    shape = sb.Shape(n_groups=G, heads_per_group=H, max_ctx=ctx, max_batch=B + 1, topk=max(1, topk))
+    K, V = _kv(shape, 31 + case)
+    layer = _filled(sb, shape, K, V, T_list)
+    q = synth.normal_bf16((B, G * H, 128), 32, case)
+    idx, cnt = _select(np.random.default_rng(case), T_list, G, topk) if topk else (None, None)
+    _check_attention(sb, shape, layer, K, V, T_list, q, idx, cnt, mass)
+
+
+def test_attention_peaked_and_flat(sb):
+    """Scores of a few units around and, scaled up, hundreds apart (the running maximum moves often
+    and most weights vanish); and equal scores."""
+    T_list = [3000]
+    shape = sb.Shape(n_groups=1, heads_per_group=16, max_ctx=3008, max_batch=1)
+    K, V = _kv(shape, 41)
+    layer = _filled(sb, shape, K, V, T_list)
+    q = synth.normal_bf16((1, 16, 128), 42)
+    q[0, 4:8] = 0                                              # flat
+    q[0, 8:] = (q[0, 8:].float() * 60).to(torch.bfloat16)      # peaked
+    _check_attention(sb, shape, layer, K, V, T_list, q, None, None, mass=True)
+
+
+def test_attention_selection_edges(sb):
+    """cnt 0, a block named twice, unsorted blocks, cnt above topk+2 (clamped)."""
+    T_list = [500, 500, 500, 500]
+    shape = sb.Shape(n_groups=1, heads_per_group=4, max_ctx=512, max_batch=4, topk=2)
+    K, V = _kv(shape, 51)
+    layer = _filled(sb, shape, K, V, T_list)
+    q = synth.normal_bf16((4, 4, 128), 52)
+    idx = _i32([[[3, 3, 0, -1]], [[7, 0, 5, 2]], [[1, -1, -1, -1]], [[0, 1, 2, 7]]])
+    cnt = _i32([[3], [4], [0], [4]])
+    _check_attention(sb, shape, layer, K, V, T_list, q, idx, cnt, mass=True)
+    out = torch.ones((4, 4, 128), dtype=torch.bfloat16, device="cuda")
+    ws = sb.workspace(shape, 4, sb.WS_KV4_ATTN)
+    sb.sparda_kv4_decode_attn(shape, layer, q.cuda(), idx, cnt, _i32(T_list), 4, out, ws)
+    ref = out.clone()
+    assert (out[2] == 0).all()
+    over = cnt.clone()
+    over[3] = 9
+    sb.sparda_kv4_decode_attn(shape, layer, q.cuda(), idx, over, _i32(T_list), 4, out, ws)
+    assert torch.equal(out, ref)
+    # an index outside the sequence is reported and skipped: sequence 1 without its block 5
+    bad, less = idx.clone(), idx.clone()
+    bad[1, 0, 2] = 8
+    less[1, 0] = torch.tensor([7, 0, 2, -1], dtype=torch.int32)
+    c3 = cnt.clone()
+    c3[1] = 3
+    mass = torch.zeros((4, 1, 8), device="cuda")
+    wm = sb.workspace(shape, 4, sb.WS_KV4_ATTN_MASS)
+    sb.sparda_kv4_decode_attn(shape, layer, q.cuda(), bad, cnt, _i32(T_list), 4, out, wm, mass=mass)
+    torch.cuda.synchronize()
+    assert sb.sparda_device_error(clear=True) == sb.DEV_BAD_INDEX
+    sb.sparda_kv4_decode_attn(shape, layer, q.cuda(), less, c3, _i32(T_list), 4, ref, ws)
+    assert (out.float() - ref.float()).abs().max() <= 2.0 ** -7 * ref.float().abs().max()
+    assert abs(float(mass[1].sum()) - 4) < 1e-3                # four heads, one each
+    # lengths out of range: zero output, reported; the others are unaffected
+    sb.sparda_kv4_decode_attn(shape, layer, q.cuda(), idx, cnt, _i32([500, 0, 500, 513]), 4, out, ws)
+    torch.cuda.synchronize()
+    assert sb.sparda_device_error(clear=True) == sb.DEV_BAD_SEQ_LEN
+    assert (out[1] == 0).all() and (out[3] == 0).all()
+    assert (out[0] != 0).any()
+
+
+def test_attention_nan_rows(sb):
+    """A NaN key group reaches only its own group's heads; masked garbage reaches nothing."""
+    T_list = [100]
+    shape = sb.Shape(n_groups=2, heads_per_group=2, max_ctx=128, max_batch=1)
+    K, V = _kv(shape, 61)
+    K[0, 1, 50, 3] = float("nan")
+    layer = _filled(sb, shape, K, V, T_list)
+    q = synth.normal_bf16((1, 4, 128), 62).cuda()
+    out = torch.zeros((1, 4, 128), dtype=torch.bfloat16, device="cuda")
+    sb.sparda_kv4_decode_attn(shape, layer, q, None, None, _i32(T_list), 1, out, sb.workspace(shape, 1, sb.WS_KV4_ATTN))
+    assert not torch.isnan(out[0, :2]).any() and torch.isnan(out[0, 2:]).all()
+
+
+def test_attention_many_groups(sb):
+    """More (sequence, group)s than the balanced plan holds: whole groups per CTA."""
+    B = 530
+    T_list = [1 + (37 * b) % 190 for b in range(B)]
+    shape = sb.Shape(n_groups=2, heads_per_group=2, max_ctx=192, max_batch=B, topk=1)
+    K, V = _kv(shape, 71)
+    layer = _filled(sb, shape, K, V, T_list)
+    q = synth.normal_bf16((B, 4, 128), 72)
+    _check_attention(sb, shape, layer, K, V, T_list, q, None, None, mass=True)
+    idx, cnt = _select(np.random.default_rng(7), T_list, 2, 1)
+    _check_attention(sb, shape, layer, K, V, T_list, q, idx, cnt)
+
+
+def test_attention_offsets_past_32_bits(sb):
+    """The last sequence of a cache of 5.4 GB, read and written beyond byte 2^32."""
+    B, ctx = 64, 262144
+    shape = sb.Shape(n_groups=2, heads_per_group=16, max_ctx=ctx, max_batch=B)
+    layer = sb.LayerKV4.empty(shape)
+    assert layer.kv.numel() > 1 << 32
+    T_list = [70] * (B - 1) + [2000]
+    K = torch.zeros((B, 2, ctx, 128), dtype=torch.bfloat16, device="cuda")
+    V = torch.zeros_like(K)
+    Ks, Vs = synth.normal_bf16((2, 2048, 128), 81, 1), synth.normal_bf16((2, 2048, 128), 81, 2)
+    K[-1, :, :2048], V[-1, :, :2048] = Ks.cuda(), Vs.cuda()
+    sb.sparda_kv4_quantize(shape, layer, K, V, _i32(T_list), B)
+    q = synth.normal_bf16((B, 32, 128), 82)
+    out = torch.zeros((B, 32, 128), dtype=torch.bfloat16, device="cuda")
+    sb.sparda_kv4_decode_attn(shape, layer, q.cuda(), None, None, _i32(T_list), B, out, sb.workspace(shape, B, sb.WS_KV4_ATTN))
+    torch.cuda.synchronize()
+    assert sb.sparda_device_error(clear=True) == 0
+    for g in range(2):
+        ref, tol, _, _ = R.attention(to64(q[-1, 16 * g:16 * g + 16]), R.grid_values(Ks[g], True), _v16(Vs[g]), None, 2000, W16)
+        assert (np.abs(to64(out[-1, 16 * g:16 * g + 16]) - ref) <= tol).all()
+
+
+def test_attention_repeats_and_leaves_the_workspace(sb):
+    """Calls back to back on one workspace, in a graph and on a side stream give the same bits."""
+    T_list = [9000, 77, 5000]
+    shape = sb.Shape(n_groups=2, heads_per_group=8, max_ctx=9024, max_batch=3)
+    K, V = _kv(shape, 91)
+    layer = _filled(sb, shape, K, V, T_list)
+    q = synth.normal_bf16((3, 16, 128), 92).cuda()
+    seq = _i32(T_list)
+    ws = sb.workspace(shape, 3, sb.WS_KV4_ATTN_MASS)
+    outs, masses = [], []
+    for _ in range(3):
+        outs.append(torch.zeros((3, 16, 128), dtype=torch.bfloat16, device="cuda"))
+        masses.append(torch.zeros((3, 2, 141), device="cuda"))
+        sb.sparda_kv4_decode_attn(shape, layer, q, None, None, seq, 3, outs[-1], ws, mass=masses[-1])
+    torch.cuda.synchronize()
+    side = torch.cuda.Stream()
+    o2, m2 = torch.zeros_like(outs[0]), torch.zeros_like(masses[0])
+    side.wait_stream(torch.cuda.current_stream())
+    sb.sparda_kv4_decode_attn(shape, layer, q, None, None, seq, 3, o2, ws, mass=m2, stream=side)
+    side.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    o3, m3 = torch.zeros_like(outs[0]), torch.zeros_like(masses[0])
+    with torch.cuda.graph(graph):
+        sb.sparda_kv4_decode_attn(shape, layer, q, None, None, seq, 3, o3, ws, mass=m3)
+    graph.replay()
+    graph.replay()
+    torch.cuda.synchronize()
+    for o, m in zip(outs[1:] + [o2], masses[1:] + [m2]):
+        # which CTA joins a group's partial results may differ, their order does not
+        assert torch.equal(o, outs[0]) and torch.equal(m, masses[0])
+    assert torch.equal(o3, outs[0])
+    assert (m3 - 2 * masses[0]).abs().max() <= 2.0 ** -22 * m3.max()
+    counters = ws[:3 * 2 * 4].view(torch.int32)
+    assert (counters == 0).all()
+    assert sb.sparda_device_error(clear=True) == 0
+
+
+# ------------------------------------------------------------------ mass of the bf16 cache
+@pytest.mark.parametrize("T_list,topk", [([4096, 3000, 65, 1], 8), ([2500] * 20, 8), ([4000], 62), ([300] * 90, 2)])
+def test_bf16_attention_with_mass(sb, T_list, topk):
+    B, G, ctx = len(T_list), 2, 4096
+    shape = sb.Shape(n_groups=G, max_ctx=ctx, max_batch=B, topk=topk)
+    layer = sb.LayerKV.empty(shape)
+    K, V = synth.normal_bf16((B, G, ctx, 128), 101, 1), synth.normal_bf16((B, G, ctx, 128), 101, 2)
+    layer.k.copy_(K.cuda())
+    layer.v.copy_(V.cuda())
+    q = synth.normal_bf16((B, 32, 128), 102)
+    idx, cnt = _select(np.random.default_rng(3), T_list, G, topk)
+    out, plain = (torch.zeros((B, 32, 128), dtype=torch.bfloat16, device="cuda") for _ in range(2))
+    mass = torch.zeros((B, G, ctx // 64), device="cuda")
+    ws = sb.workspace(shape, B, sb.WS_ATTN_MASS)
+    sb.sparda_sparse_decode_attn(shape, layer, q.cuda(), idx, cnt, _i32(T_list), B, plain, ws)
+    sb.sparda_sparse_decode_attn_mass(shape, layer, q.cuda(), idx, cnt, _i32(T_list), B, out, ws, mass)
+    torch.cuda.synchronize()
+    assert sb.sparda_device_error(clear=True) == 0
+    assert torch.equal(out, plain)
+    for b in range(0, B, max(1, B // 5)):
+        for g in range(G):
+            blocks = [int(x) for x in idx[b, g, :int(cnt[b, g])]]
+            _, _, w, wtol = R.attention(to64(q[b, 16 * g:16 * g + 16]), to64(K[b, g]), to64(V[b, g]), blocks, T_list[b], 0)
+            want = np.zeros(ctx // 64)
+            want[blocks] = w
+            got = to64(mass[b, g])
+            assert (np.abs(got - want) <= (wtol + 2.0 ** -22) * want).all()
+            assert abs(got.sum() - 16) < 1e-3

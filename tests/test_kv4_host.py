@@ -1,0 +1,153 @@
+"""Host-side checks of the 4-bit cache, block-mass and eviction entry points: workspace sizes and
+every refusal, all before any launch (no GPU needed)."""
+import ctypes
+
+import pytest
+import torch
+
+from block_sparse_attention_forecast_gb300 import build as _build
+
+_build.build()
+
+import block_sparse_attention_forecast_gb300.binding as sb  # noqa: E402
+
+P = ctypes.c_void_p
+FAKE, FAKE2, ODD = P(1 << 20), P(1 << 24), P((1 << 20) + 8)
+BIG = 1 << 40
+
+
+def _shape(**kw):
+    return sb.Shape(**{**dict(max_batch=2, max_ctx=4096, topk=8), **kw})
+
+
+def _ref(s):
+    return ctypes.byref(s.c())
+
+
+def _l4(kv=1 << 20, ck=1 << 20):
+    return ctypes.byref(sb.c_layer_kv4(kv, ck))
+
+
+def _lk(k=1 << 20, v=1 << 20, ck=1 << 20, on_host=0):
+    return ctypes.byref(sb.c_layer_kv(k, v, ck, None, None, on_host, 0))
+
+
+def test_workspace_sizes():
+    for H in (1, 5, 16):
+        s = _shape(heads_per_group=H)
+        plain = sb.sparda_workspace_bytes(s, 2, sb.WS_KV4_ATTN)
+        mass = sb.sparda_workspace_bytes(s, 2, sb.WS_KV4_ATTN_MASS)
+        # counters, then two partial results for each of at least 152 CTAs
+        assert plain >= 2 * 2 * 4 + 152 * 2 * (16 * 128 + 32) * 4
+        # statistics of every block (64 of them here, more than the 10 selectable ones)
+        assert mass >= plain + 2 * 2 * 64 * 4 * 16 * 8 + 2 * 2 * 2 * 16 * 4
+    assert sb.sparda_workspace_bytes(_shape(heads_per_group=17), 2, sb.WS_KV4_ATTN) == 0
+    assert sb.sparda_workspace_bytes(_shape(heads_per_group=0), 2, sb.WS_KV4_ATTN) == 0
+    assert sb.sparda_workspace_bytes(_shape(), 3, sb.WS_KV4_ATTN) == 0
+    attn = sb.sparda_workspace_bytes(_shape(), 2, sb.WS_ATTN)
+    assert sb.sparda_workspace_bytes(_shape(), 2, sb.WS_ATTN_MASS) >= attn + 2 * 2 * 10 * 4 * 16 * 8
+    assert sb.sparda_workspace_bytes(_shape(heads_per_group=8), 2, sb.WS_ATTN_MASS) == 0
+
+
+def test_cache_calls_reject_bad_arguments():
+    s = _ref(_shape())
+    for fn in (sb.lib.sparda_kv4_quantize, sb.lib.sparda_kv4_append):
+        assert fn(None, _l4(), FAKE, FAKE, FAKE, 1, None) == sb.ERR_INVALID_ARG
+        assert fn(_ref(_shape(heads_per_group=17)), _l4(), FAKE, FAKE, FAKE, 1, None) == sb.ERR_UNSUPPORTED_SHAPE
+        assert fn(_ref(_shape(head_dim=64)), _l4(), FAKE, FAKE, FAKE, 1, None) == sb.ERR_UNSUPPORTED_SHAPE
+        assert fn(s, None, FAKE, FAKE, FAKE, 1, None) == sb.ERR_INVALID_ARG
+        assert fn(s, _l4(kv=None), FAKE, FAKE, FAKE, 1, None) == sb.ERR_INVALID_ARG
+        assert fn(s, _l4(kv=(1 << 20) + 8), FAKE, FAKE, FAKE, 1, None) == sb.ERR_MISALIGNED
+        assert fn(s, _l4(), None, FAKE, FAKE, 1, None) == sb.ERR_INVALID_ARG
+        assert fn(s, _l4(), FAKE, None, FAKE, 1, None) == sb.ERR_INVALID_ARG
+        assert fn(s, _l4(), FAKE, FAKE, None, 1, None) == sb.ERR_INVALID_ARG
+        assert fn(s, _l4(), ODD, FAKE, FAKE, 1, None) == sb.ERR_MISALIGNED
+        assert fn(s, _l4(), FAKE, ODD, FAKE, 1, None) == sb.ERR_MISALIGNED
+        assert fn(s, _l4(), FAKE, FAKE, FAKE, 0, None) == sb.ERR_INVALID_ARG
+        assert fn(s, _l4(), FAKE, FAKE, FAKE, 3, None) == sb.ERR_INVALID_ARG
+    # only the append needs the compressed keys
+    assert sb.lib.sparda_kv4_append(s, _l4(ck=None), FAKE, FAKE, FAKE, 1, None) == sb.ERR_INVALID_ARG
+    deq = sb.lib.sparda_kv4_dequantize
+    assert deq(s, _l4(), FAKE, None, FAKE, 1, FAKE, FAKE, None) == sb.ERR_INVALID_ARG       # idx without cnt
+    assert deq(s, _l4(), None, FAKE, FAKE, 1, FAKE, FAKE, None) == sb.ERR_INVALID_ARG
+    assert deq(s, _l4(), P(2), FAKE, FAKE, 1, FAKE, FAKE, None) == sb.ERR_MISALIGNED
+    assert deq(s, _l4(), None, None, FAKE, 1, None, FAKE, None) == sb.ERR_INVALID_ARG
+
+
+def test_attention_rejects_bad_arguments():
+    s = _shape()
+    need, need_mass = (sb.sparda_workspace_bytes(s, 2, k) for k in (sb.WS_KV4_ATTN, sb.WS_KV4_ATTN_MASS))
+
+    def call(shape=s, layer=None, q=FAKE, idx=FAKE, cnt=FAKE, seq=FAKE, batch=1, out=FAKE, mass=None, ws=FAKE, n=BIG):
+        return sb.lib.sparda_kv4_decode_attn(_ref(shape), layer or _l4(ck=None), q, idx, cnt, seq, batch, out, mass, ws,
+                                             n, None)
+    assert call(shape=_shape(heads_per_group=17)) == sb.ERR_UNSUPPORTED_SHAPE
+    assert call(shape=_shape(topk=63)) == sb.ERR_UNSUPPORTED_SHAPE
+    assert call(layer=_l4(kv=None)) == sb.ERR_INVALID_ARG
+    for name in ("q", "seq", "out", "ws"):
+        assert call(**{name: None}) == sb.ERR_INVALID_ARG, name
+    assert call(idx=None) == sb.ERR_INVALID_ARG and call(cnt=None) == sb.ERR_INVALID_ARG
+    for name in ("q", "out", "ws"):
+        assert call(**{name: ODD}) == sb.ERR_MISALIGNED, name
+    assert call(mass=P(2)) == sb.ERR_MISALIGNED
+    assert call(batch=3) == sb.ERR_INVALID_ARG
+    assert call(n=need - 1) == sb.ERR_WORKSPACE_TOO_SMALL
+    assert call(mass=FAKE, n=need_mass - 1) == sb.ERR_WORKSPACE_TOO_SMALL
+    m = sb.lib.sparda_sparse_decode_attn_mass
+    assert m(_ref(s), _lk(), FAKE, FAKE, FAKE, FAKE, 1, FAKE, None, FAKE, BIG, None) == sb.ERR_INVALID_ARG
+    assert m(_ref(s), _lk(on_host=1), FAKE, FAKE, FAKE, FAKE, 1, FAKE, FAKE, FAKE, BIG, None) == sb.ERR_INVALID_ARG
+    assert m(_ref(s), _lk(), FAKE, FAKE, FAKE, FAKE, 1, FAKE, P(2), FAKE, BIG, None) == sb.ERR_MISALIGNED
+    assert m(_ref(_shape(heads_per_group=8)), _lk(), FAKE, FAKE, FAKE, FAKE, 1, FAKE, FAKE, FAKE, BIG,
+             None) == sb.ERR_UNSUPPORTED_SHAPE
+
+
+@pytest.mark.parametrize("kv4", [False, True])
+def test_eviction_rejects_bad_arguments(kv4):
+    s = _shape()
+    fn = sb.lib.sparda_kv4_evict_blocks if kv4 else sb.lib.sparda_evict_blocks
+    layer = _l4 if kv4 else _lk
+    other = (lambda **k: _l4(**{**dict(kv=1 << 24, ck=1 << 24), **k})) if kv4 else \
+            (lambda **k: _lk(**{**dict(k=1 << 24, v=1 << 24, ck=1 << 24), **k}))
+
+    def call(shape=s, L=None, mass=FAKE, seq=FAKE, ds=None, dl=None, dm=None, dq=None, batch=1, keep=8, recent=2, kept=FAKE):
+        return fn(_ref(shape), L or layer(), mass, seq, None if ds is None else _ref(ds), dl, dm, dq, batch, keep, recent,
+                  kept, None)
+    assert call(mass=None) == sb.ERR_INVALID_ARG and call(seq=None) == sb.ERR_INVALID_ARG
+    assert call(kept=None) == sb.ERR_INVALID_ARG and call(batch=3) == sb.ERR_INVALID_ARG
+    assert call(recent=0) == sb.ERR_INVALID_ARG and call(keep=2, recent=2) == sb.ERR_INVALID_ARG
+    assert call(keep=4097) == sb.ERR_UNSUPPORTED_SHAPE
+    assert call(L=layer(ck=None)) == sb.ERR_INVALID_ARG
+    assert call(mass=P(2)) == sb.ERR_MISALIGNED and call(kept=P(2)) == sb.ERR_MISALIGNED
+    full = dict(ds=s, dl=other(), dm=FAKE2, dq=FAKE2)
+    for name in full:
+        assert call(**{**full, name: None}) == sb.ERR_INVALID_ARG, name
+    assert call(**{**full, "dl": layer()}) == sb.ERR_INVALID_ARG                    # the source itself
+    assert call(**{**full, "dm": FAKE}) == sb.ERR_INVALID_ARG
+    assert call(**{**full, "dq": FAKE}) == sb.ERR_INVALID_ARG
+    assert call(**{**full, "dl": other(ck=1 << 20)}) == sb.ERR_INVALID_ARG
+    assert call(**{**full, "ds": _shape(max_ctx=256)}) == sb.ERR_UNSUPPORTED_SHAPE  # 4 blocks for 8
+    assert call(**{**full, "ds": _shape(n_groups=1)}) == sb.ERR_UNSUPPORTED_SHAPE
+    assert call(**{**full, "ds": _shape(max_batch=1)}, batch=2) == sb.ERR_UNSUPPORTED_SHAPE
+    assert call(**{**full, "dl": other(ck=(1 << 24) + 8)}) == sb.ERR_MISALIGNED
+    if not kv4:
+        assert call(L=_lk(on_host=1)) in (sb.ERR_INVALID_ARG, sb.ERR_NOT_MAPPED_HOST)
+        assert call(shape=_shape(heads_per_group=8)) == sb.ERR_UNSUPPORTED_SHAPE
+
+
+def test_binding_refuses_tensors_on_another_device():
+    s = _shape()
+    cpu = sb.LayerKV4.empty(s, device="cpu")
+    assert cpu.kv.shape == (2, 2, 64, sb.KV4_BLOCK_BYTES) and cpu.ck.shape == (2, 2, 255, 128)
+    seq = torch.ones(2, dtype=torch.int32)
+    x = torch.zeros((2, 2, 128), dtype=torch.bfloat16)
+    with pytest.raises((ValueError, RuntimeError)):
+        sb.sparda_kv4_append(s, cpu, x, x, seq, 2)
+
+
+def test_binding_checks_types_sizes_and_strides():
+    dev = torch.device("cpu")
+    ok = torch.zeros((4, 8), dtype=torch.bfloat16)
+    assert sb._checked("x", ok, torch.bfloat16, 32, dev) == ok.data_ptr()
+    for bad in (ok.float(), ok[:3], ok.t()):
+        with pytest.raises(ValueError):
+            sb._checked("x", bad, torch.bfloat16, 32, dev)
