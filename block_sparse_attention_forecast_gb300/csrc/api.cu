@@ -860,9 +860,10 @@ int32_t sparda_kv4_decode_attn(const sparda_shape* s, const sparda_layer_kv4* L,
     a.stats = reinterpret_cast<float2*>(stats);
     a.ml = reinterpret_cast<float*>(stats + mass_stats_bytes(s, kv4_mass_slots(s)));
   }
-  launch_kv4_attn(a, st);
+  const int parts = launch_kv4_attn(a, st);
+  if (!parts) return SPARDA_ERR_CUDA;
   if (mass) {
-    BlockMassArgs m{a.stats, a.ml, mass, idx, cnt, seq_len, s->n_groups, s->heads_per_group, s->max_ctx, nb_cap(s), slots};
+    BlockMassArgs m{a.stats, a.ml, mass, idx, cnt, seq_len, s->n_groups, s->heads_per_group, s->max_ctx, nb_cap(s), slots, parts};
     launch_block_mass(m, batch * s->n_groups, st);
   }
   return cuda_status(cudaGetLastError());
@@ -883,7 +884,7 @@ int32_t sparda_sparse_decode_attn_mass(const sparda_shape* s, const sparda_layer
   a.ml = reinterpret_cast<float*>(stats + mass_stats_bytes(s, kslots(s)));
   const cudaStream_t st = static_cast<cudaStream_t>(stream);
   launch_sparse_attn(a, mk, mv, hk, hv, batch * s->n_groups, st);
-  BlockMassArgs m{a.stats, a.ml, mass, idx, cnt, seq_len, s->n_groups, kHeads, s->max_ctx, nb_cap(s), kslots(s)};
+  BlockMassArgs m{a.stats, a.ml, mass, idx, cnt, seq_len, s->n_groups, kHeads, s->max_ctx, nb_cap(s), kslots(s), 4};
   launch_block_mass(m, batch * s->n_groups, st);
   return cuda_status(cudaGetLastError());
 }

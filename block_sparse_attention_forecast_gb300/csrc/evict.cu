@@ -54,7 +54,7 @@ __device__ __forceinline__ uint32_t cache_key2(const uint8_t* plane, int kv4, si
   const uint8_t* b = plane + block * kv4::kBlockBytes4;
   const uint32_t w = *reinterpret_cast<const uint32_t*>(b + kv4::kKCodes + tok * 64 + (t >> 2) * 4);
   const uint32_t sz = *reinterpret_cast<const uint32_t*>(b + kv4::kKScales + tok * 16 + (t >> 4) * 4);
-  return kv4::key_pair(w, t & 3, kv4::as_bf2(kv4::dup_lo(sz)), kv4::as_bf2(kv4::dup_hi(sz)));
+  return kv4::key_pair(w, t & 3, kv4::dup_lo(sz), kv4::dup_hi(sz));
 }
 
 // The compressed key of a window made of the last 16 keys of block ja and the first 16 of jb, by 64 threads.

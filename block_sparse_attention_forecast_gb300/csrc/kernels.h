@@ -217,22 +217,22 @@ struct Kv4AttnArgs {
   float* part_o;                 // workspace [kKv4MaxCtas, 2, 16, d]
   float* part_ml;                // workspace [kKv4MaxCtas, 2, 2, 16]
   unsigned* counters;            // workspace [max_batch*G], zero between calls
-  float2* stats;                 // block mass: (max, sum) [B*G, slots, 4, 16]; nullptr: not wanted
+  float2* stats;                 // block mass: (max, sum) [B*G, slots, parts, 16]; nullptr: not wanted
   float* ml;                     // block mass: final max and sum [B*G, 2, 16]
   int* err;
   int G, H, max_ctx, nb_cap, kslots, bg_count;
 };
-void launch_kv4_attn(const Kv4AttnArgs& a, cudaStream_t s);
+int launch_kv4_attn(const Kv4AttnArgs& a, cudaStream_t s);   // the stats' parts per block (2 or 4); 0: not launched
 
 // Accumulates the attention weight of each attended block (block_mass.cu).
 struct BlockMassArgs {
-  const float2* stats;           // [B*G, slots, 4, 16] (max, sum) per quarter block and head
+  const float2* stats;           // [B*G, slots, parts, 16] (max, sum) per part of a block and head
   const float* ml;               // [B*G, 2, 16]
   float* mass;                   // [max_batch, G, nb_cap]
   const int32_t* idx;            // [B, G, kslots]; nullptr: slot j is block j
   const int32_t* cnt;
   const int32_t* seq_len;
-  int G, H, max_ctx, nb_cap, slots;
+  int G, H, max_ctx, nb_cap, slots, parts;   // parts: 2 or 4 per block
 };
 void launch_block_mass(const BlockMassArgs& a, int bg_count, cudaStream_t s);
 

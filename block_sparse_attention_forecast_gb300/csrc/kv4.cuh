@@ -12,7 +12,7 @@
 // Why this form: 16 + code is a bit pattern. The upper mantissa bits of 16.0 (bf16 0x4180, fp16
 // 0x4c00) count units, so a code placed there is 16 + code with one AND-OR, and one packed fused
 // multiply-add turns two codes into two values in the type the tensor cores read: 11
-// instructions for 8 values. z carries the rounding of 24 s at most (half of 0.125 s in bf16),
+// instructions for 8 values, 5 to 7 of them on the half-rate logic pipe. z carries the rounding of 24 s at most (half of 0.125 s in bf16),
 // which only moves the grid, since codes are taken against the rounded z. Keys are bf16 because
 // the queries are; values are fp16 so that the attention weights, its other operand, keep 11
 // bits instead of 8.
@@ -30,7 +30,9 @@
 //   * value pair (tokens t0 = 16 step + 8 half + 2 cq and t0 + 1): 16 bytes for each octet g of
 //     16 channels, at ((step * 2 + half) * 32 + 4 g + cq) * 16; word w of it holds channels
 //     16 g + 4 w + p in nibble p, t0 in the low half-word and t0 + 1 in the high one, rotated
-//     left by 6.
+//     left by 2: channels 0 and 1 (and, after a rotation by 8, 2 and 3) can then be taken where they
+//     lie, as 256 + code and as 16 + code; the 240 too many come off in one addition, on the
+//     multiply-add pipe, which has room where the logic pipe has none.
 #pragma once
 
 #include <cuda_fp16.h>
@@ -52,22 +54,53 @@ static_assert(kBlockBytes4 == 10240, "block layout");
 __device__ __forceinline__ uint32_t ror(uint32_t x, int n) { return __funnelshift_r(x, x, n); }
 __device__ __forceinline__ uint32_t rol(uint32_t x, int n) { return __funnelshift_l(x, x, n); }
 
+// Two values at a time, packed in 32 bits; each result is rounded once.
+__device__ __forceinline__ uint32_t fma_bf2(uint32_t x, uint32_t y, uint32_t z) {
+  uint32_t r;
+  asm("fma.rn.bf16x2 %0, %1, %2, %3;" : "=r"(r) : "r"(x), "r"(y), "r"(z));
+  return r;
+}
+__device__ __forceinline__ uint32_t fma_h2(uint32_t x, uint32_t y, uint32_t z) {
+  uint32_t r;
+  asm("fma.rn.f16x2 %0, %1, %2, %3;" : "=r"(r) : "r"(x), "r"(y), "r"(z));
+  return r;
+}
+__device__ __forceinline__ uint32_t add_h2(uint32_t x, uint32_t y) {
+  uint32_t r;
+  asm("add.rn.f16x2 %0, %1, %2;" : "=r"(r) : "r"(x), "r"(y));
+  return r;
+}
+__device__ __forceinline__ float2 floats_h2(uint32_t x) { return __half22float2(*reinterpret_cast<const __half2*>(&x)); }
+
+// The code masks. A kernel in which the unpacking counts holds them in vector registers (read from
+// shared memory): an AND-OR with the mask and the pattern both constants, or both uniform
+// registers, costs a second instruction, a move.
+struct Masks {
+  uint32_t key = 0x00780078u;       // bits 3..6 of each half
+  uint32_t lo = 0x003c003cu;        // bits 2..5
+  uint32_t hi = 0x03c003c0u;        // bits 6..9
+};
+
+template <uint32_t kPattern>
+__device__ __forceinline__ uint32_t and_or(uint32_t x, uint32_t mask) {
+  uint32_t r;
+  asm("lop3.b32 %0, %1, %2, %3, 0xea;" : "=r"(r) : "r"(x), "r"(mask), "n"(kPattern));
+  return r;
+}
+
 // Channel pair p of a key word -> two bf16 values (s2, z2: the group's scale and offset twice).
-__device__ __forceinline__ uint32_t key_pair(uint32_t word, int p, __nv_bfloat162 s2, __nv_bfloat162 z2) {
-  const uint32_t u = (ror(word, 4 * p) & 0x00780078u) | 0x41804180u;
-  const __nv_bfloat162 v = __hfma2(*reinterpret_cast<const __nv_bfloat162*>(&u), s2, z2);
-  return *reinterpret_cast<const uint32_t*>(&v);
+__device__ __forceinline__ uint32_t key_pair(uint32_t word, int p, uint32_t s2, uint32_t z2, const Masks& m = Masks()) {
+  return fma_bf2(and_or<0x41804180u>(ror(word, 4 * p), m.key), s2, z2);
 }
 
 // Channel p of a value word -> the values of its two tokens as fp16 (s2, z2: per token).
-__device__ __forceinline__ uint32_t value_pair(uint32_t word, int p, __half2 s2, __half2 z2) {
-  const uint32_t u = (ror(word, 4 * p) & 0x03c003c0u) | 0x4c004c00u;
-  const __half2 v = __hfma2(*reinterpret_cast<const __half2*>(&u), s2, z2);
-  return *reinterpret_cast<const uint32_t*>(&v);
+__device__ __forceinline__ uint32_t value_pair(uint32_t word, int p, uint32_t s2, uint32_t z2, const Masks& m = Masks()) {
+  const uint32_t u = p < 2 ? word : ror(word, 8);
+  // 16 + code, from 256 + code for even p
+  const uint32_t c = p & 1 ? and_or<0x4c004c00u>(u, m.hi) : add_h2(and_or<0x5c005c00u>(u, m.lo), 0xdb80db80u);
+  return fma_h2(c, s2, z2);
 }
 
-__device__ __forceinline__ __nv_bfloat162 as_bf2(uint32_t u) { return *reinterpret_cast<const __nv_bfloat162*>(&u); }
-__device__ __forceinline__ __half2 as_h2(uint32_t u) { return *reinterpret_cast<const __half2*>(&u); }
 // The low / high half-word of u in both halves.
 __device__ __forceinline__ uint32_t dup_lo(uint32_t u) { return __byte_perm(u, u, 0x1010); }
 __device__ __forceinline__ uint32_t dup_hi(uint32_t u) { return __byte_perm(u, u, 0x3232); }

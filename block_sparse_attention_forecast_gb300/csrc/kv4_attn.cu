@@ -16,9 +16,11 @@
 // consumer warps form groups of four that take blocks in turn, a warp 16 tokens of each.
 //
 // Numbers: S in float32 from exact products (keys and queries are bf16); softmax in float32, base
-// 2; weights are rounded to fp16 against the running maximum, scaled by 2^14 so that everything
-// down to 2^-28 of the largest weight keeps fp16's 11 bits; sums in float32. The accumulator is
-// rescaled only when a warp's running maximum moves.
+// 2; sums in float32. A weight is a power of two of its score's distance to a reference, which
+// follows the running maximum of its head only when that has risen by more than 2^8: with 16 heads
+// some maximum rises in most steps of 16 tokens, and the rescaling (64 multiplications) with it. The
+// weights are operands in fp16, scaled by 2^6: at most 2^14, at full precision (2^-11) down to 2^-20 of
+// the reference, and below that off by at most 2^-31 of it each.
 #include <cuda_fp16.h>
 
 #include "kernels.h"
@@ -29,25 +31,54 @@ using namespace kv4;
 
 namespace {
 
-constexpr int kWarpsPerBlock = 4;
-constexpr int kBlockGroups = 2;                             // groups of four consumer warps
-constexpr int kCWarps = kBlockGroups * kWarpsPerBlock;
+constexpr int kCWarps = 8;
 constexpr int kCThreads = kCWarps * 32;
-constexpr int kThreads4 = kCThreads + 32;
-constexpr int kRing = 12;
-static_assert(kRing % kBlockGroups == 0, "each ring stage must belong to one consumer group");
+// The producer has a warpgroup to itself, of which one warp works: registers are moved from it to the
+// consumers, which would otherwise be held to 168 each and spill.
+constexpr int kThreads4 = kCThreads + 128;
+constexpr int kLaunchRegs = 168, kProducerRegs = 40, kConsumerRegs = 208;
+static_assert(128 * kProducerRegs + kCThreads * kConsumerRegs <= kThreads4 * kLaunchRegs, "registers the launch holds");
+constexpr int kRing = 16;                                   // at most a warp's lanes
 constexpr int kPlanMax = 1024;                              // (sequence, group)s the balanced plan holds
 constexpr int kRow = 144;                                   // merge-buffer row: 128 + 4 per 32, no bank conflicts
-constexpr int kMergeFloats4 = kCWarps * (kHeads * kRow + 2 * kHeads);
+constexpr int kMergeWarps = kCWarps / 2;                    // the others' results are folded in first
+constexpr int kMergeFloats4 = kMergeWarps * (kHeads * kRow + 2 * kHeads);
+constexpr int kQBytes = 8 * 512;                            // the queries as A fragments
 constexpr int kHeader4 = 1024 + (kPlanMax + 32) * 4;
-constexpr int kSmem4 = 128 + kHeader4 + kRing * kBlockBytes4 + kMergeFloats4 * 4;
+constexpr int kSmem4 = 128 + kHeader4 + kRing * kBlockBytes4 + kQBytes + kMergeFloats4 * 4;
+// The cluster form's receive area: of each head that a CTA owns (rank h % cluster), the partial
+// result of every CTA at entry (h / cluster) * cluster + source rank.
+constexpr int kMaxCluster4 = 8;
+constexpr int kRecv4 = kHeads + kMaxCluster4 - 1;
+constexpr int kClusterSmem4 = kSmem4 + kRecv4 * (kHeadDim + 2) * 4;
+constexpr int kWholeBlocks = 2;                             // blocks per warp from which a warp takes whole ones
+constexpr int kClusterBlocks = 24;                          // blocks per CTA up to which groups get clusters
 constexpr int kMinUnits = 2;                                // blocks per CTA below which fewer CTAs work
-constexpr float kPShift = 14.f;                             // weights are scaled by 2^kPShift
+constexpr float kPShift = 6.f;                              // weights are scaled by 2^kPShift
+constexpr float kRise = 8.f;                                // rise of a maximum (base 2) that is let pass
+constexpr uint32_t kProducerPolls = 1u << 25;               // bounds a lane's wait to seconds
 constexpr float kNegInf = -INFINITY;
+// The running maximum before any token: finite, so that no difference of maxima is a NaN.
+constexpr float kLowest = -3.0e38f;
 
 __device__ __forceinline__ void sync_consumers() { asm volatile("bar.sync 1, %0;" ::"n"(kCThreads) : "memory"); }
 __device__ __forceinline__ void arrive(uint64_t* bar) {
   asm volatile("mbarrier.arrive.shared::cta.b64 _, [%0];" ::"r"(smem_addr(bar)) : "memory");
+}
+// D += A B (m16n8k16, fp16 or bf16 operands). Not volatile: the compiler may interleave products with
+// the unpacking of later operands.
+template <bool kHalf>
+__device__ __forceinline__ void product(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0,
+                                        uint32_t b1) {
+  if constexpr (kHalf) {
+    asm("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
+        : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
+        : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
+  } else {
+    asm("mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
+        : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
+        : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
+  }
 }
 // Channel c of a merge-buffer row.
 __device__ __forceinline__ int mcol(int c) { return c + 4 * (c >> 5); }
@@ -59,7 +90,23 @@ __device__ __forceinline__ int group_blocks(const Kv4AttnArgs& a, int bg, int T)
   return a.idx ? min(max(a.cnt[bg], 0), a.kslots) : tb + 1;
 }
 
-__device__ __forceinline__ uint4 lds128(const uint8_t* p) { return *reinterpret_cast<const uint4*>(p); }
+// Shared-memory loads by 32-bit address: through pointers into the aligned ring the compiler
+// would make them generic loads.
+__device__ __forceinline__ uint4 lds128(uint32_t p) {
+  uint4 v;
+  asm volatile("ld.shared.v4.u32 {%0, %1, %2, %3}, [%4];" : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "r"(p) : "memory");
+  return v;
+}
+__device__ __forceinline__ uint2 lds64(uint32_t p) {
+  uint2 v;
+  asm volatile("ld.shared.v2.u32 {%0, %1}, [%2];" : "=r"(v.x), "=r"(v.y) : "r"(p) : "memory");
+  return v;
+}
+__device__ __forceinline__ uint32_t lds32(uint32_t p) {
+  uint32_t v;
+  asm volatile("ld.shared.u32 %0, [%1];" : "=r"(v) : "r"(p) : "memory");
+  return v;
+}
 
 // The pieces of the unit range that a CTA owns, one (sequence, group) at a time.
 struct Piece {
@@ -71,8 +118,13 @@ struct Piece {
 
 // kStats: also store every quarter block's softmax statistics (max, sum of each head) and the
 // final ones, for the block mass.
-template <bool kStats>
-__global__ void __launch_bounds__(kThreads4, 1) kv4_attn_kernel(const Kv4AttnArgs a) {
+//
+// kW: warps that share a block. 1: a warp takes whole blocks, 32 tokens at a time; 4: a warp takes 16
+// tokens of each block, for short ranges, where the time to the first result counts.
+// kCluster: the n_cta CTAs of a (sequence, group) form a thread-block cluster, one piece each, and
+// join their results in distributed shared memory; no plan, no workspace.
+template <int kW, bool kStats, bool kCluster>
+__global__ void __launch_bounds__(kThreads4, 1) kv4_attn_kernel(const Kv4AttnArgs a, int cluster) {
   extern __shared__ uint8_t smem_raw4[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw4) + 127) & ~static_cast<uintptr_t>(127));
   uint64_t* full = reinterpret_cast<uint64_t*>(smem);
@@ -81,25 +133,42 @@ __global__ void __launch_bounds__(kThreads4, 1) kv4_attn_kernel(const Kv4AttnArg
   int* s_flag = stage_live + kRing;
   int* s_pre = reinterpret_cast<int*>(smem + 1024);
   uint8_t* ring = smem + kHeader4;
-  float* mO = reinterpret_cast<float*>(ring + kRing * kBlockBytes4);
-  float* mM = mO + kCWarps * kHeads * kRow;
-  float* mL = mM + kCWarps * kHeads;
+  uint4* s_q = reinterpret_cast<uint4*>(ring + kRing * kBlockBytes4);
+  float* mO = reinterpret_cast<float*>(ring + kRing * kBlockBytes4 + kQBytes);
+  float* mM = mO + kMergeWarps * kHeads * kRow;
+  float* mL = mM + kMergeWarps * kHeads;
+  constexpr int kBlockGroups = kCWarps / kW;     // blocks in the consumers' hands at a time
+  constexpr int kTiles = kW == 1 ? 4 : 2;        // 8-token tiles of a step
+  constexpr int kSteps = 8 / kW / kTiles;        // steps of a warp per block
+  static_assert(kRing % kBlockGroups == 0, "each ring stage must belong to one group of consumers");
 
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   if (tid == 0) {
     for (int i = 0; i < kRing; ++i) {
       mbar_init(&full[i], 1);
-      mbar_init(&empty[i], kWarpsPerBlock);
+      mbar_init(&empty[i], kW);
     }
     fence_mbar_init();
+    const Masks m;
+    s_flag[1] = (int)m.key;
+    s_flag[2] = (int)m.lo;
+    s_flag[3] = (int)m.hi;
   }
   grid_dep_wait();
   grid_dep_launch();
 
   // ------------------------------------------------------------ the plan
-  const bool balanced = a.bg_count <= kPlanMax;
-  int U = 0, ctas = gridDim.x, u0 = 0, u1 = 0;
-  if (balanced) {
+  const bool balanced = !kCluster && a.bg_count <= kPlanMax;
+  int U = 0, ctas = gridDim.x, u0 = 0, u1 = 0, n0 = 0;
+  if constexpr (kCluster) {
+    const int bg = blockIdx.x / cluster, rank = blockIdx.x % cluster;
+    const int T = a.seq_len[bg / a.G];
+    n0 = group_blocks(a, bg, T);
+    u0 = n0 * rank / cluster;
+    u1 = n0 * (rank + 1) / cluster;
+    if ((T < 1 || T > a.max_ctx) && rank == 0 && tid == 0) atomicOr(a.err, SPARDA_DEV_BAD_SEQ_LEN);
+    __syncthreads();                               // the barriers are initialised
+  } else if (balanced) {
     for (int bg = tid; bg < a.bg_count; bg += kThreads4) {
       const int T = a.seq_len[bg / a.G];
       if ((T < 1 || T > a.max_ctx) && blockIdx.x == 0) atomicOr(a.err, SPARDA_DEV_BAD_SEQ_LEN);
@@ -133,7 +202,8 @@ __global__ void __launch_bounds__(kThreads4, 1) kv4_attn_kernel(const Kv4AttnArg
   const int c = blockIdx.x;
   const auto cta_of = [&](long long unit) { return (int)(((unit + 1) * ctas - 1) / U); };
 
-  // Walks the CTA's pieces: balanced, the groups its unit range meets; else whole groups c, c + grid, ...
+  // Walks the CTA's pieces: balanced, the groups its unit range meets; in a cluster, its share of the
+  // one group; else whole groups c, c + grid, ...
   int w_u = u0, w_bg = 0;
   if (balanced && u0 < u1) {
     int lo = 0, hi = a.bg_count - 1;                 // the group with pre[bg] <= u0 < pre[bg + 1]
@@ -144,7 +214,7 @@ __global__ void __launch_bounds__(kThreads4, 1) kv4_attn_kernel(const Kv4AttnArg
     }
     w_bg = lo;
   } else if (!balanced) {
-    w_bg = c;
+    w_bg = kCluster ? c / cluster : c;
   }
   const auto next_piece = [&](Piece& p) -> bool {
     if (balanced) {
@@ -161,6 +231,14 @@ __global__ void __launch_bounds__(kThreads4, 1) kv4_attn_kernel(const Kv4AttnArg
     }
     if (w_bg >= a.bg_count) return false;
     p.bg = w_bg;
+    if constexpr (kCluster) {
+      p.s0 = u0;
+      p.s1 = u1;
+      p.first = c;
+      p.n_cta = 1;
+      w_bg = a.bg_count;
+      return true;
+    }
     p.s0 = 0;
     const int T = a.seq_len[w_bg / a.G];
     if ((T < 1 || T > a.max_ctx) && tid == 0) atomicOr(a.err, SPARDA_DEV_BAD_SEQ_LEN);
@@ -171,171 +249,242 @@ __global__ void __launch_bounds__(kThreads4, 1) kv4_attn_kernel(const Kv4AttnArg
     return true;
   };
 
-  if (warp == kCWarps) {
+  if (warp >= kCWarps) {
     // ------------------------------------------------------------ producer
-    int it = 0;
-    Piece p;
-    while (next_piece(p)) {
-      const int T = a.seq_len[p.bg / a.G];
-      const int tb = (T - 1) / kBlock;
-      for (int base = p.s0; base < p.s1; base += 32) {
-        const int s = base + lane;
-        int j = s, live = 0;
-        if (s < p.s1) {
-          if (a.idx) j = a.idx[(size_t)p.bg * a.kslots + s];
-          if (j < 0 || j > tb) {
-            atomicOr(a.err, SPARDA_DEV_BAD_INDEX);   // skipped: block 0 is staged with no live token
-            j = 0;
-          } else {
-            live = min(kBlock, T - j * kBlock);
-          }
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kProducerRegs));
+    // Lane l < kRing fills ring stage l: the CTA's units l, l + kRing, ... Each pass over the lanes
+    // polls every stage at once and refills those that are free.
+    if (warp == kCWarps && lane < kRing) {
+      int left = u1 - u0 - lane;                     // balanced or cluster: units from this lane's next on
+      int bg = w_bg, n = 0, s = lane;                // its next unit: slot s of the n of group bg
+      if (kCluster) {
+        s += u0;
+        n = n0;
+      } else if (balanced) {
+        if (left > 0) {
+          s += u0 - s_pre[bg];
+          n = s_pre[bg + 1] - s_pre[bg];
         }
-        const int n = min(32, p.s1 - base);
-        for (int i = 0; i < n; ++i, ++it) {
-          const int jj = __shfl_sync(0xffffffffu, j, i), ll = __shfl_sync(0xffffffffu, live, i);
-          const int stage = it % kRing;
-          int ok = 1;
-          if (lane == 0) {
-            if (it >= kRing) ok = mbar_wait(&empty[stage], ((it / kRing) & 1) ^ 1, a.err);
-            if (ok) {
-              stage_live[stage] = ll;
-              mbar_arrive_expect_tx(&full[stage], kBlockBytes4);
-              bulk_load(ring + stage * kBlockBytes4, a.kv + ((size_t)p.bg * a.nb_cap + jj) * kBlockBytes4, kBlockBytes4,
-                        &full[stage]);
-            }
-          }
-          if (!__shfl_sync(0xffffffffu, ok, 0)) return;
+      } else if (bg < a.bg_count) {
+        n = group_blocks(a, bg, a.seq_len[bg / a.G]);
+      }
+      uint32_t round = 0, polls = 0;
+      const uint8_t* src = nullptr;
+      int live = 0;
+      // the lane's next unit, looked up ahead of the wait for its stage; false behind the last
+      const auto look_up = [&]() -> bool {
+        if (kCluster || balanced ? left <= 0 : bg >= a.bg_count) return false;
+        while (s >= n) {
+          s -= n;
+          bg += balanced ? 1 : (int)gridDim.x;
+          if (!balanced && bg >= a.bg_count) return false;
+          n = balanced ? s_pre[bg + 1] - s_pre[bg] : group_blocks(a, bg, a.seq_len[bg / a.G]);
+        }
+        int j = a.idx ? a.idx[(size_t)bg * a.kslots + s] : s;
+        const int T = a.seq_len[bg / a.G];
+        if ((unsigned)j > (unsigned)((T - 1) / kBlock)) {
+          atomicOr(a.err, SPARDA_DEV_BAD_INDEX);     // skipped: block 0 is staged with no live token
+          j = 0;
+          live = 0;
+        } else {
+          live = min(kBlock, T - j * kBlock);
+        }
+        src = a.kv + ((size_t)bg * a.nb_cap + j) * kBlockBytes4;
+        s += kRing;
+        left -= kRing;
+        return true;
+      };
+      bool more = look_up();
+      while (more) {
+        if (round == 0 || mbar_test_wait(&empty[lane], (round & 1) ^ 1)) {
+          stage_live[lane] = live;
+          mbar_arrive_expect_tx(&full[lane], kBlockBytes4);
+          bulk_load(ring + lane * kBlockBytes4, src, kBlockBytes4, &full[lane]);
+          ++round;
+          polls = 0;
+          more = look_up();
+        } else if (++polls > kProducerPolls) {
+          atomicOr(a.err, SPARDA_DEV_WAIT_TIMEOUT);
+          more = false;
         }
       }
     }
+    if constexpr (kCluster) cluster_sync();          // the consumers' barrier
     return;
   }
 
   // -------------------------------------------------------------- consumers
-  const int grp = warp / kWarpsPerBlock, wq = warp % kWarpsPerBlock;
+  asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kConsumerRegs));
+  const int grp = warp / kW, wq = warp % kW;
   const int g = lane >> 2, cq = lane & 3;
   const float sl2 = 1.4426950408889634f * 0.08838834764831845f;   // log2(e) / sqrt(128)
   int it = 0;
   bool ok = true;             // a wait that ran out: no further compute, the barriers stay matched
   bool first_piece = true;
+  const uint32_t masks_at = smem_addr(s_flag) + 4;
+  const Masks mk{lds32(masks_at), lds32(masks_at + 4), lds32(masks_at + 8)};
+  const uint32_t ring_at = smem_addr(ring), live_at = smem_addr(stage_live);
   Piece p;
   while (next_piece(p)) {
-    float m0 = kNegInf, m1 = kNegInf, l0 = 0.f, l1 = 0.f;
+    // the references, raw scores, and the exponents' offsets: p = 2^(sl2 (s - m) + kPShift)
+    float m0 = kLowest, m1 = kLowest, l0 = 0.f, l1 = 0.f;
+    float nb0 = kPShift - m0 * sl2, nb1 = kPShift - m1 * sl2;
+    float up0 = kLowest, up1 = kLowest;        // a score above it moves the reference
     float o[16][4];
 #pragma unroll
     for (int n = 0; n < 16; ++n) o[n][0] = o[n][1] = o[n][2] = o[n][3] = 0.f;
-    uint4 qa[4], qb[4];       // rows g and g + 8, channels 32 cq + 8 w ..
+    // A fragments, rows g and g + 8: K step 2 w + i takes channels 32 cq + 8 w + 4 i .. They are put
+    // together in shared memory and loaded as quadruples: built in registers, they would be moved
+    // into place again in every step. Every warp writes the same values before it reads them.
+    uint4 qf[8];
     {
       const uint4* q0 = reinterpret_cast<const uint4*>(a.q + ((size_t)p.bg * a.H + g) * kHeadDim + 32 * cq);
       const uint4 none = make_uint4(0, 0, 0, 0);
 #pragma unroll
       for (int w = 0; w < 4; ++w) {
-        qa[w] = g < a.H ? q0[w] : none;
-        qb[w] = g + 8 < a.H ? q0[w + 8 * (kHeadDim / 8)] : none;
+        const uint4 x = g < a.H ? q0[w] : none, y = g + 8 < a.H ? q0[w + 8 * (kHeadDim / 8)] : none;
+        s_q[(2 * w) * 32 + lane] = make_uint4(x.x, y.x, x.y, y.y);
+        s_q[(2 * w + 1) * 32 + lane] = make_uint4(x.z, y.z, x.w, y.w);
       }
+#pragma unroll
+      for (int w = 0; w < 8; ++w) qf[w] = lds128(smem_addr(s_q + w * 32 + lane));
     }
-    for (int s = p.s0; s < p.s1; ++s, ++it) {
-      if (it % kBlockGroups != grp) continue;
-      const int stage = it % kRing;
-      if (ok) ok = __all_sync(0xffffffffu, mbar_wait(&full[stage], (it / kRing) & 1, a.err));
-      if (!ok) continue;
-      const uint8_t* blk = ring + stage * kBlockBytes4;
-      const int live = stage_live[stage] - 16 * wq;              // tokens of this warp's 16 that exist
-
-      float sc[2][4];
+    // this group's blocks of the piece: its ring stages come round every kBlockGroups
+    int skip = grp - it % kBlockGroups;
+    if (skip < 0) skip += kBlockGroups;
+    int stage = (it + skip) % kRing, phase = ((it + skip) / kRing) & 1;
+    it += p.s1 - p.s0;
+    for (int s = p.s0 + skip; ok && s < p.s1; s += kBlockGroups) {
+      ok = __all_sync(0xffffffffu, mbar_wait(&full[stage], phase, a.err));
+      if (!ok) break;
+      const int block_live = (int)lds32(live_at + 4 * stage);
+#pragma unroll 1
+      for (int step = 0; step < kSteps; ++step) {
+        const int tile0 = (wq * kSteps + step) * kTiles;         // the step's first 8-token tile of the block
+        const int live = block_live - 8 * tile0;                 // tokens of the step that exist
+        const uint32_t blk = ring_at + stage * kBlockBytes4;
+        const uint32_t kc = blk + kKCodes + tile0 * 512 + lane * 16, ks = blk + kKScales + tile0 * 128 + lane * 4;
+        const uint32_t vc = blk + kVCodes + tile0 * 512 + lane * 16;
+        const uint32_t vs = blk + kVScales + (tile0 * 4 + cq) * 32 + (g >> 1) * 8;
+        // raw scores, heads g and g + 8
+        float sc[kTiles][4];
+        uint4 kw[kTiles];
+        uint32_t s2[kTiles], z2[kTiles];
 #pragma unroll
-      for (int r = 0; r < 2; ++r) {
-        const uint4 kw = lds128(blk + kKCodes + wq * 1024 + r * 512 + lane * 16);
-        const uint32_t sz = *reinterpret_cast<const uint32_t*>(blk + kKScales + wq * 256 + r * 128 + lane * 4);
-        const __nv_bfloat162 s2 = as_bf2(dup_lo(sz)), z2 = as_bf2(dup_hi(sz));
-        float x[4] = {0.f, 0.f, 0.f, 0.f}, y[4] = {0.f, 0.f, 0.f, 0.f};
-#pragma unroll
-        for (int w = 0; w < 4; ++w) {
-          const uint32_t word = w == 0 ? kw.x : w == 1 ? kw.y : w == 2 ? kw.z : kw.w;
-          mma_16816(x, qa[w].x, qb[w].x, qa[w].y, qb[w].y, key_pair(word, 0, s2, z2), key_pair(word, 1, s2, z2));
-          mma_16816(y, qa[w].z, qb[w].z, qa[w].w, qb[w].w, key_pair(word, 2, s2, z2), key_pair(word, 3, s2, z2));
+        for (int r = 0; r < kTiles; ++r) {
+          kw[r] = lds128(kc + r * 512);
+          const uint32_t sz = lds32(ks + r * 128);
+          s2[r] = dup_lo(sz);
+          z2[r] = dup_hi(sz);
+          sc[r][0] = sc[r][1] = sc[r][2] = sc[r][3] = 0.f;
         }
+        // the tiles side by side, so that consecutive products do not wait for one another
 #pragma unroll
-        for (int e = 0; e < 4; ++e) sc[r][e] = (x[e] + y[e]) * sl2;
-      }
-      if (live < 16) {
+        for (int k = 0; k < 8; ++k) {
 #pragma unroll
-        for (int r = 0; r < 2; ++r)
-#pragma unroll
-          for (int e = 0; e < 4; ++e)
-            if (8 * r + 2 * cq + (e & 1) >= live) sc[r][e] = kNegInf;
-      }
-      float mx0 = fmaxf(fmaxf(sc[0][0], sc[0][1]), fmaxf(sc[1][0], sc[1][1]));
-      float mx1 = fmaxf(fmaxf(sc[0][2], sc[0][3]), fmaxf(sc[1][2], sc[1][3]));
-      mx0 = fmaxf(mx0, __shfl_xor_sync(0xffffffffu, mx0, 1));
-      mx1 = fmaxf(mx1, __shfl_xor_sync(0xffffffffu, mx1, 1));
-      mx0 = fmaxf(mx0, __shfl_xor_sync(0xffffffffu, mx0, 2));
-      mx1 = fmaxf(mx1, __shfl_xor_sync(0xffffffffu, mx1, 2));
-      if (__any_sync(0xffffffffu, mx0 > m0 || mx1 > m1)) {
-        const float n0 = fmaxf(m0, mx0), n1 = fmaxf(m1, mx1);
-        const float al0 = m0 == kNegInf ? 0.f : fast_exp2(m0 - n0), al1 = m1 == kNegInf ? 0.f : fast_exp2(m1 - n1);
-        m0 = n0;
-        m1 = n1;
-        l0 *= al0;
-        l1 *= al1;
-#pragma unroll
-        for (int n = 0; n < 16; ++n) {
-          o[n][0] *= al0;
-          o[n][1] *= al0;
-          o[n][2] *= al1;
-          o[n][3] *= al1;
+          for (int r = 0; r < kTiles; ++r) {
+            const uint32_t word = k < 2 ? kw[r].x : k < 4 ? kw[r].y : k < 6 ? kw[r].z : kw[r].w;
+            product<false>(sc[r], qf[k].x, qf[k].y, qf[k].z, qf[k].w, key_pair(word, 2 * (k & 1), s2[r], z2[r], mk),
+                           key_pair(word, 2 * (k & 1) + 1, s2[r], z2[r], mk));
+          }
         }
-      }
-      const float base0 = (m0 == kNegInf ? 0.f : m0) - kPShift, base1 = (m1 == kNegInf ? 0.f : m1) - kPShift;
-      float pr[2][4];
+        // scales and offsets of the value tiles
+        uint2 z[kTiles];
 #pragma unroll
-      for (int r = 0; r < 2; ++r) {
-        pr[r][0] = fast_exp2(sc[r][0] - base0);
-        pr[r][1] = fast_exp2(sc[r][1] - base0);
-        pr[r][2] = fast_exp2(sc[r][2] - base1);
-        pr[r][3] = fast_exp2(sc[r][3] - base1);
-      }
-      float ps0 = (pr[0][0] + pr[0][1]) + (pr[1][0] + pr[1][1]);
-      float ps1 = (pr[0][2] + pr[0][3]) + (pr[1][2] + pr[1][3]);
-      if constexpr (kStats) {
-        ps0 += __shfl_xor_sync(0xffffffffu, ps0, 1);
-        ps1 += __shfl_xor_sync(0xffffffffu, ps1, 1);
-        ps0 += __shfl_xor_sync(0xffffffffu, ps0, 2);
-        ps1 += __shfl_xor_sync(0xffffffffu, ps1, 2);
-        if (cq == 0) {
-          const int slots = a.idx ? a.kslots : a.nb_cap;
-          float2* st = a.stats + (((size_t)p.bg * slots + s) * kWarpsPerBlock + wq) * kHeads;
-          st[g] = make_float2(m0, ps0);
-          st[g + 8] = make_float2(m1, ps1);
+        for (int r = 0; r < kTiles; ++r) z[r] = lds64(vs + r * 128);
+        if (live < 8 * kTiles) {
+          // tokens that do not exist hold anything: no weight, and values of 0
+#pragma unroll
+          for (int r = 0; r < kTiles; ++r) {
+            const bool in0 = 8 * r + 2 * cq < live, in1 = 8 * r + 2 * cq + 1 < live;
+            sc[r][0] = in0 ? sc[r][0] : kNegInf;
+            sc[r][1] = in1 ? sc[r][1] : kNegInf;
+            sc[r][2] = in0 ? sc[r][2] : kNegInf;
+            sc[r][3] = in1 ? sc[r][3] : kNegInf;
+            const uint32_t keep = (in0 ? 0xffffu : 0u) | (in1 ? 0xffff0000u : 0u);
+            z[r].x &= keep;
+            z[r].y &= keep;
+          }
         }
-      }
-      l0 += ps0;              // without kStats: this lane's share, summed over the four lanes at the end
-      l1 += ps1;
-      const __half2 h0 = __floats2half2_rn(pr[0][0], pr[0][1]), h1 = __floats2half2_rn(pr[0][2], pr[0][3]);
-      const __half2 h2 = __floats2half2_rn(pr[1][0], pr[1][1]), h3 = __floats2half2_rn(pr[1][2], pr[1][3]);
-      const uint32_t pa0 = *reinterpret_cast<const uint32_t*>(&h0), pa1 = *reinterpret_cast<const uint32_t*>(&h1);
-      const uint32_t pa2 = *reinterpret_cast<const uint32_t*>(&h2), pa3 = *reinterpret_cast<const uint32_t*>(&h3);
-      const uint4 v0 = lds128(blk + kVCodes + wq * 1024 + lane * 16), v1 = lds128(blk + kVCodes + wq * 1024 + 512 + lane * 16);
-      uint2 z0 = *reinterpret_cast<const uint2*>(blk + kVScales + ((wq * 2) * 4 + cq) * 32 + (g >> 1) * 8);
-      uint2 z1 = *reinterpret_cast<const uint2*>(blk + kVScales + ((wq * 2 + 1) * 4 + cq) * 32 + (g >> 1) * 8);
-      if (live < 16) {        // tokens that do not exist hold anything: their values become 0
-        const uint32_t k0 = (2 * cq < live ? 0xffffu : 0u) | (2 * cq + 1 < live ? 0xffff0000u : 0u);
-        const uint32_t k1 = (8 + 2 * cq < live ? 0xffffu : 0u) | (9 + 2 * cq < live ? 0xffff0000u : 0u);
-        z0.x &= k0;
-        z0.y &= k0;
-        z1.x &= k1;
-        z1.y &= k1;
-      }
+        float mx0 = fmaxf(sc[0][0], sc[0][1]), mx1 = fmaxf(sc[0][2], sc[0][3]);
 #pragma unroll
-      for (int n = 0; n < 16; ++n) {
-        const uint32_t wa = n < 4 ? v0.x : n < 8 ? v0.y : n < 12 ? v0.z : v0.w;
-        const uint32_t wb = n < 4 ? v1.x : n < 8 ? v1.y : n < 12 ? v1.z : v1.w;
-        mma_16816_f16(o[n], pa0, pa1, pa2, pa3, value_pair(wa, n & 3, as_h2(z0.x), as_h2(z0.y)),
-                      value_pair(wb, n & 3, as_h2(z1.x), as_h2(z1.y)));
+        for (int r = 1; r < kTiles; ++r) {
+          mx0 = fmaxf(mx0, fmaxf(sc[r][0], sc[r][1]));
+          mx1 = fmaxf(mx1, fmaxf(sc[r][2], sc[r][3]));
+        }
+        if (__any_sync(0xffffffffu, mx0 > up0 || mx1 > up1)) {     // move the references
+          mx0 = fmaxf(mx0, __shfl_xor_sync(0xffffffffu, mx0, 1));
+          mx1 = fmaxf(mx1, __shfl_xor_sync(0xffffffffu, mx1, 1));
+          mx0 = fmaxf(mx0, __shfl_xor_sync(0xffffffffu, mx0, 2));
+          mx1 = fmaxf(mx1, __shfl_xor_sync(0xffffffffu, mx1, 2));
+          const float n0 = fmaxf(m0, mx0), n1 = fmaxf(m1, mx1);
+          const float al0 = fast_exp2((m0 - n0) * sl2), al1 = fast_exp2((m1 - n1) * sl2);
+          m0 = n0;
+          m1 = n1;
+          nb0 = kPShift - m0 * sl2;
+          nb1 = kPShift - m1 * sl2;
+          up0 = m0 + kRise / sl2;
+          up1 = m1 + kRise / sl2;
+          l0 *= al0;
+          l1 *= al1;
+#pragma unroll
+          for (int n = 0; n < 16; ++n) {
+            o[n][0] *= al0;
+            o[n][1] *= al0;
+            o[n][2] *= al1;
+            o[n][3] *= al1;
+          }
+        }
+        // weights, as A fragments of 16 tokens
+        uint32_t pa[kTiles][2];
+        float ps0 = 0.f, ps1 = 0.f;
+#pragma unroll
+        for (int r = 0; r < kTiles; ++r) {
+          const float p0 = fast_exp2(fmaf(sc[r][0], sl2, nb0)), p1 = fast_exp2(fmaf(sc[r][1], sl2, nb0));
+          const float p2 = fast_exp2(fmaf(sc[r][2], sl2, nb1)), p3 = fast_exp2(fmaf(sc[r][3], sl2, nb1));
+          ps0 += p0 + p1;
+          ps1 += p2 + p3;
+          const __half2 x = __floats2half2_rn(p0, p1), y = __floats2half2_rn(p2, p3);
+          pa[r][0] = *reinterpret_cast<const uint32_t*>(&x);
+          pa[r][1] = *reinterpret_cast<const uint32_t*>(&y);
+        }
+        if constexpr (kStats) {
+          ps0 += __shfl_xor_sync(0xffffffffu, ps0, 1);
+          ps1 += __shfl_xor_sync(0xffffffffu, ps1, 1);
+          ps0 += __shfl_xor_sync(0xffffffffu, ps0, 2);
+          ps1 += __shfl_xor_sync(0xffffffffu, ps1, 2);
+          if (cq == 0) {
+            const int slots = a.idx ? a.kslots : a.nb_cap;
+            float2* st = a.stats + (((size_t)p.bg * slots + s) * (8 / kTiles) + tile0 / kTiles) * kHeads;
+            st[g] = make_float2(m0 * sl2, ps0);
+            st[g + 8] = make_float2(m1 * sl2, ps1);
+          }
+        }
+        l0 += ps0;            // without kStats: this lane's share, summed over the four lanes at the end
+        l1 += ps1;
+        // o += weights . values
+#pragma unroll
+        for (int r = 0; r < kTiles; r += 2) {
+          const uint4 v0 = lds128(vc + r * 512), v1 = lds128(vc + r * 512 + 512);
+#pragma unroll
+          for (int n = 0; n < 16; ++n) {
+            const uint32_t wa = n < 4 ? v0.x : n < 8 ? v0.y : n < 12 ? v0.z : v0.w;
+            const uint32_t wb = n < 4 ? v1.x : n < 8 ? v1.y : n < 12 ? v1.z : v1.w;
+            product<true>(o[n], pa[r][0], pa[r][1], pa[r + 1][0], pa[r + 1][1], value_pair(wa, n & 3, z[r].x, z[r].y, mk),
+                          value_pair(wb, n & 3, z[r + 1].x, z[r + 1].y, mk));
+          }
+        }
       }
       __syncwarp();
       if (lane == 0) arrive(&empty[stage]);
+      stage += kBlockGroups;
+      if (stage >= kRing) {
+        stage -= kRing;
+        phase ^= 1;
+      }
     }
+    m0 *= sl2;
+    m1 *= sl2;
     if constexpr (!kStats) {
       l0 += __shfl_xor_sync(0xffffffffu, l0, 1);
       l1 += __shfl_xor_sync(0xffffffffu, l1, 1);
@@ -344,9 +493,32 @@ __global__ void __launch_bounds__(kThreads4, 1) kv4_attn_kernel(const Kv4AttnArg
     }
 
     // ---------------------------------------------------------- merge the warps
-    sync_consumers();                          // the merge buffer is free again
-    {
-      float* r0 = mO + (warp * kHeads + g) * kRow;
+    // The upper half of the warps hand their results to the lower half, lane for lane.
+    if (warp >= kMergeWarps) {
+      float4* give = reinterpret_cast<float4*>(mO + (warp - kMergeWarps) * kHeads * kRow) + lane;
+#pragma unroll
+      for (int n = 0; n < 16; ++n) give[n * 32] = make_float4(o[n][0], o[n][1], o[n][2], o[n][3]);
+      give[16 * 32] = make_float4(m0, m1, l0, l1);
+    }
+    sync_consumers();
+    if (warp < kMergeWarps) {
+      float* mine = mO + warp * kHeads * kRow;
+      const float4* take = reinterpret_cast<const float4*>(mine) + lane;
+      const float4 ml = take[16 * 32];
+      const float n0 = fmaxf(m0, ml.x), n1 = fmaxf(m1, ml.y);
+      const float wa0 = fast_exp2(m0 - n0), wa1 = fast_exp2(m1 - n1), wb0 = fast_exp2(ml.x - n0), wb1 = fast_exp2(ml.y - n1);
+      l0 = l0 * wa0 + ml.z * wb0;
+      l1 = l1 * wa1 + ml.w * wb1;
+#pragma unroll
+      for (int n = 0; n < 16; ++n) {
+        const float4 x = take[n * 32];
+        o[n][0] = o[n][0] * wa0 + x.x * wb0;
+        o[n][1] = o[n][1] * wa0 + x.y * wb0;
+        o[n][2] = o[n][2] * wa1 + x.z * wb1;
+        o[n][3] = o[n][3] * wa1 + x.w * wb1;
+      }
+      __syncwarp();
+      float* r0 = mine + g * kRow;
       float* r1 = r0 + 8 * kRow;
 #pragma unroll
       for (int i = 0; i < 4; ++i) {            // o[n][0]: channel 32 cq + n; o[n][1]: 32 cq + 16 + n
@@ -356,26 +528,24 @@ __global__ void __launch_bounds__(kThreads4, 1) kv4_attn_kernel(const Kv4AttnArg
         *reinterpret_cast<float4*>(r1 + 36 * cq + 16 + 4 * i) = make_float4(o[4 * i][3], o[4 * i + 1][3], o[4 * i + 2][3], o[4 * i + 3][3]);
       }
       if (cq == 0) {
-        mM[warp * kHeads + g] = m0;
-        mM[warp * kHeads + g + 8] = m1;
+        mM[warp * kHeads + g] = n0;
+        mM[warp * kHeads + g + 8] = n1;
         mL[warp * kHeads + g] = l0;
         mL[warp * kHeads + g + 8] = l1;
       }
     }
     sync_consumers();
-    // thread t < 256: head h = t / 16, channels d0 .. d0 + 7
-    const int t = tid, h = (t >> 4) & 15, d0 = (t & 15) * 8;
-    float M = kNegInf, L = 0.f, acc[8];
+    // thread t: head h = t / 16, channels d0 .. d0 + 7
+    const int t = tid, h = t >> 4, d0 = (t & 15) * 8;
+    float M = kLowest, L = 0.f, acc[8];
 #pragma unroll
     for (int e = 0; e < 8; ++e) acc[e] = 0.f;
-    const bool active = t < 256;
-    if (active) {
+    {
 #pragma unroll
-      for (int w = 0; w < kCWarps; ++w) M = fmaxf(M, mM[w * kHeads + h]);
-      const float base = M == kNegInf ? 0.f : M;
+      for (int w = 0; w < kMergeWarps; ++w) M = fmaxf(M, mM[w * kHeads + h]);
 #pragma unroll
-      for (int w = 0; w < kCWarps; ++w) {
-        const float wt = fast_exp2(mM[w * kHeads + h] - base);
+      for (int w = 0; w < kMergeWarps; ++w) {
+        const float wt = fast_exp2(mM[w * kHeads + h] - M);
         L += wt * mL[w * kHeads + h];
         const float* row = mO + (w * kHeads + h) * kRow + mcol(d0);
         const float4 x = *reinterpret_cast<const float4*>(row), y = *reinterpret_cast<const float4*>(row + 4);
@@ -383,12 +553,42 @@ __global__ void __launch_bounds__(kThreads4, 1) kv4_attn_kernel(const Kv4AttnArg
         acc[4] += wt * y.x; acc[5] += wt * y.y; acc[6] += wt * y.z; acc[7] += wt * y.w;
       }
     }
-    bool write = active;
-    if (p.n_cta > 1) {
+    bool write = true;
+    if constexpr (kCluster) {
+      // pushed to the CTA that owns the head; behind the one cluster barrier no CTA reads another's
+      // memory, so none has to stay for the others
+      float* rO = mL + kMergeWarps * kHeads;
+      float* rM = rO + kRecv4 * kHeadDim;
+      float* rL = rM + kRecv4;
+      const uint32_t rank = cluster_rank(), owner = (uint32_t)(h % cluster);
+      const int e0 = (h / cluster) * cluster, entry = e0 + (int)rank;
+      st_cluster_f4(rO + entry * kHeadDim + d0, owner, make_float4(acc[0], acc[1], acc[2], acc[3]));
+      st_cluster_f4(rO + entry * kHeadDim + d0 + 4, owner, make_float4(acc[4], acc[5], acc[6], acc[7]));
+      if ((t & 15) == 0) {
+        st_cluster_f(rM + entry, owner, M);
+        st_cluster_f(rL + entry, owner, L);
+      }
+      cluster_sync();
+      write = owner == rank;
+      if (write) {
+        for (int q = 0; q < cluster; ++q) M = fmaxf(M, rM[e0 + q]);
+        L = 0.f;
+#pragma unroll
+        for (int e = 0; e < 8; ++e) acc[e] = 0.f;
+        for (int q = 0; q < cluster; ++q) {
+          const float wt = fast_exp2(rM[e0 + q] - M);
+          L += wt * rL[e0 + q];
+          const float4* src = reinterpret_cast<const float4*>(rO + (e0 + q) * kHeadDim + d0);
+          const float4 x = src[0], y = src[1];
+          acc[0] += wt * x.x; acc[1] += wt * x.y; acc[2] += wt * x.z; acc[3] += wt * x.w;
+          acc[4] += wt * y.x; acc[5] += wt * y.y; acc[6] += wt * y.z; acc[7] += wt * y.w;
+        }
+      }
+    } else if (p.n_cta > 1) {
       // a CTA's partial of its first piece lies in slot 0, of its last in slot 1; a piece that is
       // neither covers its group alone
       const int slot = c * 2 + (first_piece ? 0 : 1);
-      if (active) {
+      {
         float4* po = reinterpret_cast<float4*>(a.part_o + ((size_t)slot * kHeads + h) * kHeadDim + d0);
         po[0] = make_float4(acc[0], acc[1], acc[2], acc[3]);
         po[1] = make_float4(acc[4], acc[5], acc[6], acc[7]);
@@ -405,13 +605,13 @@ __global__ void __launch_bounds__(kThreads4, 1) kv4_attn_kernel(const Kv4AttnArg
         if (*s_flag) a.counters[p.bg] = 0u;
       }
       sync_consumers();
-      write = write && *s_flag != 0;
+      write = *s_flag != 0;
       if (write) {
         // the last CTA of the group joins the partials. The group's first CTA left its partial in
         // slot 1 unless the group begins that CTA's range; all others in slot 0.
         const int g0 = s_pre[p.bg];
         const int first_slot = p.first * 2 + ((int)((long long)U * p.first / ctas) == g0 ? 0 : 1);
-        M = kNegInf;
+        M = kLowest;
         L = 0.f;
 #pragma unroll
         for (int e = 0; e < 8; ++e) acc[e] = 0.f;
@@ -423,7 +623,7 @@ __global__ void __launch_bounds__(kThreads4, 1) kv4_attn_kernel(const Kv4AttnArg
           for (int q = 0; q < kFlight; ++q) {
             const bool in = q0 + q < p.n_cta;
             const int sl = q0 + q == 0 || !in ? first_slot : (p.first + q0 + q) * 2;
-            pm[q] = in ? __ldcg(a.part_ml + sl * 2 * kHeads + h) : kNegInf;
+            pm[q] = in ? __ldcg(a.part_ml + sl * 2 * kHeads + h) : kLowest;
             pl[q] = __ldcg(a.part_ml + sl * 2 * kHeads + kHeads + h);
             const float4* src = reinterpret_cast<const float4*>(a.part_o + ((size_t)sl * kHeads + h) * kHeadDim + d0);
             px[q][0] = __ldcg(src);
@@ -432,14 +632,13 @@ __global__ void __launch_bounds__(kThreads4, 1) kv4_attn_kernel(const Kv4AttnArg
           float Mn = M;
 #pragma unroll
           for (int q = 0; q < kFlight; ++q) Mn = fmaxf(Mn, pm[q]);
-          const float base = Mn == kNegInf ? 0.f : Mn;
-          const float old = fast_exp2(M - base);
+          const float old = fast_exp2(M - Mn);
           L *= old;
 #pragma unroll
           for (int e = 0; e < 8; ++e) acc[e] *= old;
 #pragma unroll
           for (int q = 0; q < kFlight; ++q) {
-            const float wt = fast_exp2(pm[q] - base);
+            const float wt = fast_exp2(pm[q] - Mn);
             if (q0 + q < p.n_cta) {
               L += wt * pl[q];
               acc[0] += wt * px[q][0].x; acc[1] += wt * px[q][0].y; acc[2] += wt * px[q][0].z; acc[3] += wt * px[q][0].w;
@@ -465,6 +664,8 @@ __global__ void __launch_bounds__(kThreads4, 1) kv4_attn_kernel(const Kv4AttnArg
       }
     }
     first_piece = false;
+    if constexpr (kCluster) return;
+    sync_consumers();                          // the merge buffer is free again
   }
   // groups without a block belong to no range: their output is zero
   if (balanced) {
@@ -476,14 +677,63 @@ __global__ void __launch_bounds__(kThreads4, 1) kv4_attn_kernel(const Kv4AttnArg
   }
 }
 
-void launch_kv4_attn(const Kv4AttnArgs& a, cudaStream_t s) {
-  const long long bound = (long long)a.bg_count * (a.idx ? a.kslots : a.nb_cap);
-  int grid = sm_count() < kKv4MaxCtas ? sm_count() : kKv4MaxCtas;
+namespace {
+
+template <int kW, bool kStats, bool kCluster>
+int launch_form(const Kv4AttnArgs& a, int grid, int cluster, cudaStream_t s) {
+  auto kern = kv4_attn_kernel<kW, kStats, kCluster>;
+  constexpr int smem = kCluster ? kClusterSmem4 : kSmem4;
+  static_assert(smem <= 232448, "shared memory of a CTA");
+  // the register split needs the registers that it counts on; a build with fewer must not run
+  static const bool fits = [&] {
+    cudaFuncAttributes at;
+    return cudaFuncGetAttributes(&at, kern) == cudaSuccess &&
+           at.numRegs * kThreads4 >= 128 * kProducerRegs + kCThreads * kConsumerRegs;
+  }();
+  if (!fits) return 0;
+  cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(grid);
+  cfg.blockDim = dim3(kThreads4);
+  cfg.dynamicSmemBytes = smem;
+  cfg.stream = s;
+  cudaLaunchAttribute attr[2];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  attr[1].id = cudaLaunchAttributeClusterDimension;
+  attr[1].val.clusterDim.x = cluster;
+  attr[1].val.clusterDim.y = 1;
+  attr[1].val.clusterDim.z = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = kCluster ? 2 : 1;
+  cudaLaunchKernelEx(&cfg, kern, a, cluster);
+  return kW == 1 ? 2 : 4;
+}
+
+template <int kW, bool kCluster>
+int launch_form(const Kv4AttnArgs& a, int grid, int cluster, cudaStream_t s) {
+  return a.stats ? launch_form<kW, true, kCluster>(a, grid, cluster, s) : launch_form<kW, false, kCluster>(a, grid, cluster, s);
+}
+
+}  // namespace
+
+int launch_kv4_attn(const Kv4AttnArgs& a, cudaStream_t s) {
+  const int sms = sm_count() < kKv4MaxCtas ? sm_count() : kKv4MaxCtas;
+  const int slots = a.idx ? a.kslots : a.nb_cap;
+  const long long bound = (long long)a.bg_count * slots;
+  // Few blocks per (sequence, group): one cluster each, when the clusters reach most SMs or have no
+  // use for more. Clusters stay within the SMs, so that they all run at once.
+  int cluster = a.bg_count <= sms ? sms / a.bg_count : 0;
+  if (cluster > kMaxCluster4) cluster = kMaxCluster4;
+  const int useful = (slots + kMinUnits - 1) / kMinUnits;
+  if (cluster > useful) cluster = useful;
+  if (cluster >= 1 && slots <= kClusterBlocks * cluster) return launch_form<4, true>(a, cluster * a.bg_count, cluster, s);
+  int grid = sms;
   const long long want = a.bg_count <= kPlanMax ? (bound + kMinUnits - 1) / kMinUnits : a.bg_count;
   if (want < grid) grid = (int)want;
-  auto kern = a.stats ? kv4_attn_kernel<true> : kv4_attn_kernel<false>;
-  cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmem4);
-  launch_pdl(kern, dim3(grid), dim3(kThreads4), kSmem4, s, a);
+  // whole blocks per warp once a warp has several
+  return bound >= (long long)kWholeBlocks * kCWarps * grid ? launch_form<1, false>(a, grid, 1, s)
+                                                           : launch_form<4, false>(a, grid, 1, s);
 }
 
 }  // namespace sparda

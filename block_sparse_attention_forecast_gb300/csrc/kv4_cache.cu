@@ -85,7 +85,7 @@ __global__ void __launch_bounds__(kQThreads) kv4_quantize_kernel(const Kv4CacheA
       // the even token's lane takes the first four channels of both tokens, the odd one's the rest
       const uint32_t other = __shfl_xor_sync(0xffffffffu, w, 16);
       const uint32_t both = (t & 1) ? __byte_perm(other, w, 0x7632) : __byte_perm(w, other, 0x5410);
-      *reinterpret_cast<uint32_t*>(blk + value_chunk(t >> 1, l16 >> 1) + ((l16 & 1) * 2 + (t & 1)) * 4) = rol(both, 6);
+      *reinterpret_cast<uint32_t*>(blk + value_chunk(t >> 1, l16 >> 1) + ((l16 & 1) * 2 + (t & 1)) * 4) = rol(both, 2);
       const uint32_t so = __shfl_xor_sync(0xffffffffu, g.s16, 16), zo = __shfl_xor_sync(0xffffffffu, g.z16, 16);
       if ((l16 & 3) == 0 && !(t & 1))
         *reinterpret_cast<uint2*>(blk + value_scale(t >> 1, l16 >> 2)) = make_uint2(g.s16 | (so << 16), g.z16 | (zo << 16));
@@ -140,7 +140,7 @@ __global__ void __launch_bounds__(kQThreads) kv4_dequantize_kernel(const Kv4Cach
     if (t >= live) break;
     const uint32_t w = *reinterpret_cast<const uint32_t*>(blk + kKCodes + t * 64 + l16 * 4);
     const uint32_t sz = *reinterpret_cast<const uint32_t*>(blk + kKScales + t * 16 + (l16 >> 2) * 4);
-    const __nv_bfloat162 s2 = as_bf2(dup_lo(sz)), z2 = as_bf2(dup_hi(sz));
+    const uint32_t s2 = dup_lo(sz), z2 = dup_hi(sz);
     k[t * 16 + l16] = make_uint4(key_pair(w, 0, s2, z2), key_pair(w, 1, s2, z2), key_pair(w, 2, s2, z2),
                                  key_pair(w, 3, s2, z2));
   }
@@ -154,8 +154,8 @@ __global__ void __launch_bounds__(kQThreads) kv4_dequantize_kernel(const Kv4Cach
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
       const uint32_t word = i < 2 ? w.x : w.y;
-      const float2 c0 = __half22float2(as_h2(value_pair(word, (2 * i) & 3, as_h2(sz.x), as_h2(sz.y))));
-      const float2 c1 = __half22float2(as_h2(value_pair(word, (2 * i + 1) & 3, as_h2(sz.x), as_h2(sz.y))));
+      const float2 c0 = floats_h2(value_pair(word, (2 * i) & 3, sz.x, sz.y));
+      const float2 c1 = floats_h2(value_pair(word, (2 * i + 1) & 3, sz.x, sz.y));
       lo[i] = pack_bf16(c0.x, c1.x);
       hi[i] = pack_bf16(c0.y, c1.y);
     }
@@ -226,7 +226,7 @@ __global__ void __launch_bounds__(64 * kAppendPerCta4) kv4_append_kernel(const K
   const int pair = tok >> 1;
   if ((t & 1) == 0) {
     uint32_t* word = reinterpret_cast<uint32_t*>(blk + value_chunk(pair, t >> 3) + ((t >> 1) & 3) * 4);
-    *word = rol((tok & 1) ? ((ror(*word, 6) & 0xffffu) | (hw << 16)) : hw, 6);
+    *word = rol((tok & 1) ? ((ror(*word, 2) & 0xffffu) | (hw << 16)) : hw, 2);
   }
   if ((t & 15) == 0) {
     uint16_t* sz = reinterpret_cast<uint16_t*>(blk + value_scale(pair, t >> 4)) + (tok & 1);
@@ -238,9 +238,9 @@ __global__ void __launch_bounds__(64 * kAppendPerCta4) kv4_append_kernel(const K
   uint32_t xs[kWinKernel];
 #pragma unroll
   for (int u = 0; u < kWinKernel - 1; ++u)
-    xs[u] = key_pair(ww[u], t & 3, as_bf2(dup_lo(ws[u])), as_bf2(dup_hi(ws[u])));
+    xs[u] = key_pair(ww[u], t & 3, dup_lo(ws[u]), dup_hi(ws[u]));
   const uint32_t sz = gk.s16 | (gk.z16 << 16);
-  xs[kWinKernel - 1] = key_pair(w, t & 3, as_bf2(dup_lo(sz)), as_bf2(dup_hi(sz)));
+  xs[kWinKernel - 1] = key_pair(w, t & 3, dup_lo(sz), dup_hi(sz));
   reinterpret_cast<uint32_t*>(a.ck + ((size_t)bg * a.W_cap + (T - kWinKernel) / kWinStride) * kHeadDim)[t] =
       window_mean(xs);
 }
