@@ -196,6 +196,20 @@ class Shape:
         return c_shape(self.n_groups, self.heads_per_group, self.head_dim, self.block,
                        self.win_kernel, self.win_stride, self.topk, self.max_ctx, self.max_batch)
 
+    def __setattr__(self, name, value):
+        self.__dict__[name] = value
+        self.__dict__.pop("_ref", None)
+
+    def __getstate__(self):
+        return {k: v for k, v in self.__dict__.items() if k != "_ref"}
+
+    def ref(self):
+        """A pointer to c(), kept until a field changes."""
+        r = self.__dict__.get("_ref")
+        if r is None:
+            r = self.__dict__["_ref"] = ctypes.byref(self.c())
+        return r
+
     @property
     def w_cap(self):
         return num_windows(self.max_ctx)
@@ -505,38 +519,50 @@ def sparda_prefetch_blocks_copy_engine(shape, layer, idx_host, cnt_host, seq_len
 
 
 # ------------------------------------------------------------------ the 4-bit cache, block mass, eviction
-def _checked(what, t, dtype, n, device):
-    """t's address, if it is a contiguous tensor of `dtype` on `device` with at least n elements."""
-    if t.dtype != dtype or t.device != device or t.numel() < n or not t.is_contiguous():
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+
+
+def _stream_handle(stream, dev):
+    """The stream's handle as an integer: `stream`, or the current one of device `dev`."""
+    if stream is not None:
+        return stream.cuda_stream
+    return _raw_stream(dev) if _raw_stream is not None else torch.cuda.current_stream(dev).cuda_stream
+
+
+def _checked(what, t, dtype, n, dev):
+    """t's address, if it is a contiguous tensor of `dtype` on CUDA device `dev` (-1: the CPU) with at
+    least n elements."""
+    if t.dtype is not dtype or t.get_device() != dev or t.numel() < n or not t.is_contiguous():
         raise ValueError("%s: a contiguous %s tensor of at least %d elements on %s is wanted, got %s %s on %s%s" % (
-            what, dtype, n, device, t.dtype, tuple(t.shape), t.device, "" if t.is_contiguous() else ", strided"))
+            what, dtype, n, "the CPU" if dev < 0 else "cuda:%d" % dev, t.dtype, tuple(t.shape), t.device,
+            "" if t.is_contiguous() else ", strided"))
     return t.data_ptr()
 
 
 def _cache_device(t):
-    """The device of a layer's cache, which has to be the current one (the call's stream and the
-    library's device state are its)."""
-    if t.device.type != "cuda" or t.device.index != torch.cuda.current_device():
-        raise ValueError("the layer's cache is on %s; the current device is cuda:%d" % (t.device, torch.cuda.current_device()))
-    return t.device
+    """The index of the device that holds a layer's cache, which has to be the current one (the call's
+    stream and the library's device state are its)."""
+    dev = t.get_device()
+    if dev < 0 or dev != torch.cuda.current_device():
+        raise ValueError("the layer's cache is on %s; it has to be on the current CUDA device" % t.device)
+    return dev
 
 
 def _kv4_dims(shape, layer, batch):
-    """(device, B, G, d, ctx, c_layer) of a call on a 4-bit cache, its tensors checked."""
+    """(device, B, G, d, ctx, pointer to the C layer) of a call on a 4-bit cache, its tensors checked."""
     dev = _cache_device(layer.kv)
-    B, G, d, ctx = int(batch), shape.n_groups, shape.head_dim, shape.max_ctx
-    c = c_layer_kv4(
-        _checked("kv", layer.kv, torch.uint8, shape.max_batch * G * (ctx // BLOCK) * KV4_BLOCK_BYTES, dev),
-        _checked("ck", layer.ck, torch.bfloat16, shape.max_batch * G * shape.w_cap * d, dev))
-    return dev, B, G, d, ctx, c
+    G, d, ctx, rows = shape.n_groups, shape.head_dim, shape.max_ctx, shape.max_batch * shape.n_groups
+    c = c_layer_kv4(_checked("kv", layer.kv, torch.uint8, rows * (ctx // BLOCK) * KV4_BLOCK_BYTES, dev),
+                    _checked("ck", layer.ck, torch.bfloat16, rows * num_windows(ctx) * d, dev))
+    return dev, int(batch), G, d, ctx, ctypes.byref(c)
 
 
-def _selection_ptrs(shape, idx, cnt, B, G, dev):
+def _selection_ptrs(shape, idx, cnt, bg, dev):
     if idx is None and cnt is None:
         return None, None
     if idx is None or cnt is None:
         raise ValueError("idx and cnt come together")
-    return _checked("idx", idx, torch.int32, B * G * shape.kslots, dev), _checked("cnt", cnt, torch.int32, B * G, dev)
+    return _checked("idx", idx, torch.int32, bg * (shape.topk + 2), dev), _checked("cnt", cnt, torch.int32, bg, dev)
 
 
 def sparda_kv4_quantize(shape, layer, k, v, seq_len, batch, stream=None):
@@ -544,28 +570,28 @@ def sparda_kv4_quantize(shape, layer, k, v, seq_len, batch, stream=None):
     dev, B, G, d, ctx, lc = _kv4_dims(shape, layer, batch)
     n = shape.max_batch * G * ctx * d
     _check("sparda_kv4_quantize", lib.sparda_kv4_quantize(
-        ctypes.byref(shape.c()), ctypes.byref(lc), _checked("k", k, torch.bfloat16, n, dev),
-        _checked("v", v, torch.bfloat16, n, dev), _checked("seq_len", seq_len, torch.int32, B, dev), B, _stream(stream)))
+        shape.ref(), lc, _checked("k", k, torch.bfloat16, n, dev), _checked("v", v, torch.bfloat16, n, dev),
+        _checked("seq_len", seq_len, torch.int32, B, dev), B, _stream_handle(stream, dev)))
 
 
 def sparda_kv4_dequantize(shape, layer, seq_len, batch, k, v, idx=None, cnt=None, stream=None):
     """The values of a LayerKV4 as bf16: every token's rows into k and v [max_batch, G, max_ctx, d], or
     with idx and cnt the selected blocks' into staging buffers [max_batch, G, topk+2, 64, d]."""
     dev, B, G, d, ctx, lc = _kv4_dims(shape, layer, batch)
-    pi, pc = _selection_ptrs(shape, idx, cnt, B, G, dev)
-    n = shape.max_batch * G * (ctx if pi is None else shape.kslots * BLOCK) * d
+    pi, pc = _selection_ptrs(shape, idx, cnt, B * G, dev)
+    n = shape.max_batch * G * (ctx if pi is None else (shape.topk + 2) * BLOCK) * d
     _check("sparda_kv4_dequantize", lib.sparda_kv4_dequantize(
-        ctypes.byref(shape.c()), ctypes.byref(lc), pi, pc, _checked("seq_len", seq_len, torch.int32, B, dev), B,
-        _checked("k", k, torch.bfloat16, n, dev), _checked("v", v, torch.bfloat16, n, dev), _stream(stream)))
+        shape.ref(), lc, pi, pc, _checked("seq_len", seq_len, torch.int32, B, dev), B,
+        _checked("k", k, torch.bfloat16, n, dev), _checked("v", v, torch.bfloat16, n, dev), _stream_handle(stream, dev)))
 
 
 def sparda_kv4_append(shape, layer, k_new, v_new, seq_len, batch, stream=None):
     """The current token's key and value (bf16 [B, G, d]) into a LayerKV4, with its compressed key."""
     dev, B, G, d, _, lc = _kv4_dims(shape, layer, batch)
     _check("sparda_kv4_append", lib.sparda_kv4_append(
-        ctypes.byref(shape.c()), ctypes.byref(lc), _checked("k_new", k_new, torch.bfloat16, B * G * d, dev),
+        shape.ref(), lc, _checked("k_new", k_new, torch.bfloat16, B * G * d, dev),
         _checked("v_new", v_new, torch.bfloat16, B * G * d, dev), _checked("seq_len", seq_len, torch.int32, B, dev), B,
-        _stream(stream)))
+        _stream_handle(stream, dev)))
 
 
 def sparda_kv4_decode_attn(shape, layer, q, idx, cnt, seq_len, batch, out, ws, mass=None, stream=None):
@@ -574,24 +600,24 @@ def sparda_kv4_decode_attn(shape, layer, q, idx, cnt, seq_len, batch, out, ws, m
     WS_KV4_ATTN_MASS workspace, else a WS_KV4_ATTN one."""
     dev, B, G, d, ctx, lc = _kv4_dims(shape, layer, batch)
     n = B * G * shape.heads_per_group * d
-    pi, pc = _selection_ptrs(shape, idx, cnt, B, G, dev)
+    pi, pc = _selection_ptrs(shape, idx, cnt, B * G, dev)
     pm = None if mass is None else _checked("mass", mass, torch.float32, B * G * (ctx // BLOCK), dev)
     _check("sparda_kv4_decode_attn", lib.sparda_kv4_decode_attn(
-        ctypes.byref(shape.c()), ctypes.byref(lc), _checked("q", q, torch.bfloat16, n, dev), pi, pc,
+        shape.ref(), lc, _checked("q", q, torch.bfloat16, n, dev), pi, pc,
         _checked("seq_len", seq_len, torch.int32, B, dev), B, _checked("out", out, torch.bfloat16, n, dev), pm,
-        _checked("ws", ws, torch.uint8, 1, dev), ws.numel(), _stream(stream)))
+        _checked("ws", ws, torch.uint8, 1, dev), ws.numel(), _stream_handle(stream, dev)))
 
 
 def _layer_ptrs(shape, layer):
-    """A resident LayerKV's c struct, its tensors checked."""
+    """(device, pointer to the C layer) of a resident LayerKV, its tensors checked."""
     if layer.on_host:
         raise ValueError("a resident layer is wanted")
     dev = _cache_device(layer.k)
-    rows = shape.max_batch * shape.n_groups
-    n = rows * shape.max_ctx * shape.head_dim
-    return dev, c_layer_kv(
+    rows, d = shape.max_batch * shape.n_groups, shape.head_dim
+    n = rows * shape.max_ctx * d
+    return dev, ctypes.byref(c_layer_kv(
         _checked("k", layer.k, torch.bfloat16, n, dev), _checked("v", layer.v, torch.bfloat16, n, dev),
-        _checked("ck", layer.ck, torch.bfloat16, rows * shape.w_cap * shape.head_dim, dev), None, None, 0, 0)
+        _checked("ck", layer.ck, torch.bfloat16, rows * num_windows(shape.max_ctx) * d, dev), None, None, 0, 0))
 
 
 def sparda_sparse_decode_attn_mass(shape, layer, q, idx, cnt, seq_len, batch, out, ws, mass, stream=None):
@@ -600,30 +626,30 @@ def sparda_sparse_decode_attn_mass(shape, layer, q, idx, cnt, seq_len, batch, ou
     dev, lc = _layer_ptrs(shape, layer)
     B, G = int(batch), shape.n_groups
     n = B * G * shape.heads_per_group * shape.head_dim
-    pi, pc = _selection_ptrs(shape, idx, cnt, B, G, dev)
+    pi, pc = _selection_ptrs(shape, idx, cnt, B * G, dev)
     _check("sparda_sparse_decode_attn_mass", lib.sparda_sparse_decode_attn_mass(
-        ctypes.byref(shape.c()), ctypes.byref(lc), _checked("q", q, torch.bfloat16, n, dev), pi, pc,
+        shape.ref(), lc, _checked("q", q, torch.bfloat16, n, dev), pi, pc,
         _checked("seq_len", seq_len, torch.int32, B, dev), B, _checked("out", out, torch.bfloat16, n, dev),
         _checked("mass", mass, torch.float32, B * G * (shape.max_ctx // BLOCK), dev),
-        _checked("ws", ws, torch.uint8, 1, dev), ws.numel(), _stream(stream)))
+        _checked("ws", ws, torch.uint8, 1, dev), ws.numel(), _stream_handle(stream, dev)))
 
 
-def _evict(fn, ptrs, shape, layer, mass, seq_len, batch, keep, recent, kept, dst_shape, dst, dst_mass, dst_seq_len, stream):
+def _evict(name, fn, ptrs, shape, layer, mass, seq_len, batch, keep, recent, kept, dst_shape, dst, dst_mass, dst_seq_len,
+           stream):
     dev, lc = ptrs(shape, layer)
     B, G = int(batch), shape.n_groups
     ds = dc = pm = pl = None
-    if dst is not None:
-        if dst_shape is None or dst_mass is None or dst_seq_len is None:
+    given = [x is not None for x in (dst_shape, dst, dst_mass, dst_seq_len)]
+    if any(given):
+        if not all(given):
             raise ValueError("dst_shape, dst, dst_mass and dst_seq_len come together")
-        ds, dc = ctypes.byref(dst_shape.c()), ctypes.byref(ptrs(dst_shape, dst)[1])
+        ds, dc = dst_shape.ref(), ptrs(dst_shape, dst)[1]
         pm = _checked("dst_mass", dst_mass, torch.float32, B * G * (dst_shape.max_ctx // BLOCK), dev)
         pl = _checked("dst_seq_len", dst_seq_len, torch.int32, B, dev)
-    elif dst_shape is not None or dst_mass is not None or dst_seq_len is not None:
-        raise ValueError("dst_shape, dst, dst_mass and dst_seq_len come together")
-    _check(fn.__name__, fn(
-        ctypes.byref(shape.c()), ctypes.byref(lc), _checked("mass", mass, torch.float32, B * G * (shape.max_ctx // BLOCK), dev),
+    _check(name, fn(
+        shape.ref(), lc, _checked("mass", mass, torch.float32, B * G * (shape.max_ctx // BLOCK), dev),
         _checked("seq_len", seq_len, torch.int32, B, dev), ds, dc, pm, pl, B, int(keep), int(recent),
-        _checked("kept", kept, torch.int32, B * G * max(0, int(keep)), dev), _stream(stream)))
+        _checked("kept", kept, torch.int32, B * G * max(0, int(keep)), dev), _stream_handle(stream, dev)))
 
 
 def sparda_evict_blocks(shape, layer, mass, seq_len, batch, keep, recent, kept, dst_shape=None, dst=None,
@@ -631,15 +657,17 @@ def sparda_evict_blocks(shape, layer, mass, seq_len, batch, keep, recent, kept, 
     """Cut every sequence of a resident LayerKV to `keep` blocks: block 0, the `recent` newest and those
     with the largest mass. In place, or into the cache dst with its dst_mass and dst_seq_len. kept
     (int32 [B, G, keep]) receives the old block numbers."""
-    _evict(lib.sparda_evict_blocks, _layer_ptrs, shape, layer, mass, seq_len, batch, keep, recent, kept, dst_shape, dst,
-           dst_mass, dst_seq_len, stream)
+    _evict("sparda_evict_blocks", lib.sparda_evict_blocks, _layer_ptrs, shape, layer, mass, seq_len, batch, keep, recent,
+           kept, dst_shape, dst, dst_mass, dst_seq_len, stream)
+
+
+def _kv4_ptrs(shape, layer):
+    dev, _, _, _, _, lc = _kv4_dims(shape, layer, 1)
+    return dev, lc
 
 
 def sparda_kv4_evict_blocks(shape, layer, mass, seq_len, batch, keep, recent, kept, dst_shape=None, dst=None,
                             dst_mass=None, dst_seq_len=None, stream=None):
     """sparda_evict_blocks of a LayerKV4."""
-    def ptrs(sh, lay):
-        dev, _, _, _, _, lc = _kv4_dims(sh, lay, 1)
-        return dev, lc
-    _evict(lib.sparda_kv4_evict_blocks, ptrs, shape, layer, mass, seq_len, batch, keep, recent, kept, dst_shape, dst,
-           dst_mass, dst_seq_len, stream)
+    _evict("sparda_kv4_evict_blocks", lib.sparda_kv4_evict_blocks, _kv4_ptrs, shape, layer, mass, seq_len, batch, keep,
+           recent, kept, dst_shape, dst, dst_mass, dst_seq_len, stream)

@@ -8,6 +8,8 @@
 #include <stddef.h>
 #include <stdint.h>
 
+#include <atomic>
+
 namespace sparda {
 
 // The scores-only selection of the fused launch hands out its work dynamically for up to this
@@ -261,6 +263,21 @@ int select_chunk_blocks(int nb_cap, int bg_count);
 int attn_blocks_per_cta();
 size_t smem_select_bytes(int chunk_blocks);
 int sm_count();                                   // of the current device (attn.cu)
+
+// A kernel's opt-in to more than 48 KB of shared memory, once per device (each call of the runtime for
+// it costs as much as a small check).
+struct SmemOptIn {
+  std::atomic<bool> done[64] = {};
+  template <typename K>
+  bool set(K kern, int bytes) {
+    int dev = 0;
+    if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= 64) return false;
+    if (done[dev].load(std::memory_order_acquire)) return true;
+    if (cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes) != cudaSuccess) return false;
+    done[dev].store(true, std::memory_order_release);
+    return true;
+  }
+};
 
 // A launch that may begin while the kernel before it in the stream still runs (programmatic
 // dependent launch); the kernel waits for that one with grid_dep_wait().

@@ -105,43 +105,63 @@ __device__ __forceinline__ uint32_t value_pair(uint32_t word, int p, uint32_t s2
 __device__ __forceinline__ uint32_t dup_lo(uint32_t u) { return __byte_perm(u, u, 0x1010); }
 __device__ __forceinline__ uint32_t dup_hi(uint32_t u) { return __byte_perm(u, u, 0x3232); }
 
-// A group's grid. s and z as stored (16 bits each) and as float.
+// A group's grid: s and z as stored (16 bits each) and as float, and 1 / s for the first guess.
 struct Grid {
   uint32_t s16, z16;
-  float s, z;
+  float s, z, r;
 };
 
+// lo or hi is a NaN or an infinity if the group holds one.
 template <bool kKey>
-__device__ __forceinline__ Grid make_grid(float lo, float hi, bool finite) {
-  Grid r;
-  const float range = __fdiv_rn(__fsub_rn(hi, lo), 15.0f);
+__device__ __forceinline__ Grid make_grid(float lo, float hi) {
+  Grid g;
+  const float step = __fdiv_rn(__fsub_rn(hi, lo), 15.0f);
   if (kKey) {
-    const __nv_bfloat16 s = __float2bfloat16_rn(range);
-    r.s = __bfloat162float(s);
-    __nv_bfloat16 z = __float2bfloat16_rn(__fsub_rn(lo, 16.0f * r.s));
-    r.z = __bfloat162float(z);
-    r.s16 = __bfloat16_as_ushort(s);
-    r.z16 = __bfloat16_as_ushort(z);
+    const __nv_bfloat16 s = __float2bfloat16_rn(step);
+    g.s = __bfloat162float(s);
+    const __nv_bfloat16 z = __float2bfloat16_rn(__fsub_rn(lo, 16.0f * g.s));
+    g.z = __bfloat162float(z);
+    g.s16 = __bfloat16_as_ushort(s);
+    g.z16 = __bfloat16_as_ushort(z);
   } else {
-    const __half s = __float2half_rn(range);
-    r.s = __half2float(s);
-    __half z = __float2half_rn(__fsub_rn(lo, 16.0f * r.s));
-    r.z = __half2float(z);
-    r.s16 = __half_as_ushort(s);
-    r.z16 = __half_as_ushort(z);
+    const __half s = __float2half_rn(step);
+    g.s = __half2float(s);
+    const __half z = __float2half_rn(__fsub_rn(lo, 16.0f * g.s));
+    g.z = __half2float(z);
+    g.s16 = __half_as_ushort(s);
+    g.z16 = __half_as_ushort(z);
   }
-  if (!finite || !(fabsf(r.z) < INFINITY) || !(r.s < INFINITY)) {
-    r.s = r.z = 0.f;                               // codes 0; the offset makes every value NaN
-    r.s16 = 0u;
-    r.z16 = 0x7fffu;                               // NaN in bf16 and in fp16
+  if (!(fabsf(g.z) < INFINITY) || !(g.s < INFINITY)) {
+    g.s = g.z = 0.f;                               // codes 0; the offset makes every value NaN
+    g.s16 = 0u;
+    g.z16 = 0x7fffu;                               // NaN in bf16 and in fp16
   }
-  return r;
+  g.r = __frcp_rn(g.s);
+  return g;
 }
 
-__device__ __forceinline__ uint32_t code_of(float x, const Grid& g) {
-  if (!(g.s > 0.f)) return 0u;
-  const float c = rintf(__fsub_rn(__fdiv_rn(__fsub_rn(x, g.z), g.s), 16.0f));
-  return (uint32_t)fminf(fmaxf(c, 0.f), 15.f);
+// clamp(rint((x - z) / s - 16), 0, 15) for a finite x, as a float. Without the division: c is the
+// nearest whole number to (x - z) / s up to the error of the guess, and e = (x - z) - c s is exact
+// (c s has at most 17 bits, and the difference is no larger than s), so comparing e with s / 2 decides
+// at and near the borders, ties to even. (A quotient that is not exactly halfway does not round to
+// halfway either: x - z and the border times s are at least one unit of x - z apart.)
+__device__ __forceinline__ float code_of(float x, const Grid& g) {
+  constexpr float kWhole = 12582912.f;             // 1.5 * 2^23: adding it rounds to whole numbers
+  const float d = __fsub_rn(x, g.z);
+  float c = __fsub_rn(__fadd_rn(__fmul_rn(d, g.r), kWhole), kWhole);
+  const float e = fmaf(-c, g.s, d), half = 0.5f * g.s;
+  if (fabsf(e) >= half) {
+    if (!(g.s >= 1e-30f))                          // 1 / s may overflow, and half of s lose a bit
+      c = g.s > 0.f ? rintf(__fsub_rn(__fdiv_rn(d, g.s), 16.0f)) + 16.0f : 16.0f;
+    else if (fabsf(e) > half || ((int)c & 1))
+      c += e > 0.f ? 1.f : -1.f;
+  }
+  return fminf(fmaxf(c, 16.f), 31.f) - 16.f;
+}
+
+// Four codes (whole floats) as four nibbles, the first lowest.
+__device__ __forceinline__ uint32_t nibbles(float c0, float c1, float c2, float c3) {
+  return __float_as_uint(fmaf(fmaf(fmaf(c3, 16.f, c2), 16.f, c1), 16.f, c0) + 8388608.f) & 0xffffu;
 }
 
 // Byte offset in a block of the 16 bytes of value codes of token pair `pair` (token / 2) and

@@ -154,6 +154,7 @@ __global__ void __launch_bounds__(kThreads4, 1) kv4_attn_kernel(const Kv4AttnArg
     s_flag[2] = (int)m.lo;
     s_flag[3] = (int)m.hi;
   }
+  if constexpr (kCluster) cluster_arrive();       // waited for before the first write to another CTA's memory
   grid_dep_wait();
   grid_dep_launch();
 
@@ -309,7 +310,10 @@ __global__ void __launch_bounds__(kThreads4, 1) kv4_attn_kernel(const Kv4AttnArg
         }
       }
     }
-    if constexpr (kCluster) cluster_sync();          // the consumers' barrier
+    if constexpr (kCluster) {                        // the consumers' two barriers
+      cluster_wait();
+      cluster_sync();
+    }
     return;
   }
 
@@ -562,6 +566,7 @@ __global__ void __launch_bounds__(kThreads4, 1) kv4_attn_kernel(const Kv4AttnArg
       float* rL = rM + kRecv4;
       const uint32_t rank = cluster_rank(), owner = (uint32_t)(h % cluster);
       const int e0 = (h / cluster) * cluster, entry = e0 + (int)rank;
+      cluster_wait();                          // every CTA of the cluster has started
       st_cluster_f4(rO + entry * kHeadDim + d0, owner, make_float4(acc[0], acc[1], acc[2], acc[3]));
       st_cluster_f4(rO + entry * kHeadDim + d0 + 4, owner, make_float4(acc[4], acc[5], acc[6], acc[7]));
       if ((t & 15) == 0) {
@@ -690,8 +695,8 @@ int launch_form(const Kv4AttnArgs& a, int grid, int cluster, cudaStream_t s) {
     return cudaFuncGetAttributes(&at, kern) == cudaSuccess &&
            at.numRegs * kThreads4 >= 128 * kProducerRegs + kCThreads * kConsumerRegs;
   }();
-  if (!fits) return 0;
-  cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+  static SmemOptIn opt_in;
+  if (!fits || !opt_in.set(kern, smem)) return 0;
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3(grid);
   cfg.blockDim = dim3(kThreads4);

@@ -17,25 +17,31 @@ __device__ __forceinline__ float bf_at(const uint4& x, int i) {
   return (i & 1) ? bf16_hi(u) : bf16_lo(u);
 }
 
-// The grid of a 32-channel group from the 8 channels of each of its four lanes (xor 1, 2).
+// (smallest, -largest) of packed bf16 pairs; a NaN takes over.
+__device__ __forceinline__ uint32_t min_bf2(uint32_t x, uint32_t y) {
+  uint32_t r;
+  asm("min.NaN.bf16x2 %0, %1, %2;" : "=r"(r) : "r"(x), "r"(y));
+  return r;
+}
+__device__ __forceinline__ uint32_t max_bf2(uint32_t x, uint32_t y) {
+  uint32_t r;
+  asm("max.NaN.bf16x2 %0, %1, %2;" : "=r"(r) : "r"(x), "r"(y));
+  return r;
+}
+// The grid of a 32-channel group, its extremes reduced over `kLanes` neighbouring lanes. lo, hi: this
+// lane's smallest and largest values, in pairs.
+template <bool kKey, int kLanes>
+__device__ __forceinline__ Grid group_grid(uint32_t lo, uint32_t hi) {
+  lo = min_bf2(lo, dup_hi(lo));                    // the low half is the smaller of the pair
+  hi = max_bf2(hi, dup_hi(hi));
+  uint32_t v = __byte_perm(lo, hi ^ 0x8000u, 0x5410);    // (lo, -hi): one minimum for both
+#pragma unroll
+  for (int d = 1; d < kLanes; d <<= 1) v = min_bf2(v, __shfl_xor_sync(0xffffffffu, v, d));
+  return make_grid<kKey>(bf16_lo(v), -bf16_hi(v));
+}
 template <bool kKey>
 __device__ __forceinline__ Grid group_grid(const uint4& x) {
-  float lo = bf_at(x, 0), hi = lo;
-  bool fin = true;
-#pragma unroll
-  for (int i = 0; i < 8; ++i) {
-    const float v = bf_at(x, i);
-    fin = fin && fabsf(v) < INFINITY;
-    lo = fminf(lo, v);
-    hi = fmaxf(hi, v);
-  }
-#pragma unroll
-  for (int d = 1; d <= 2; d <<= 1) {
-    lo = fminf(lo, __shfl_xor_sync(0xffffffffu, lo, d));
-    hi = fmaxf(hi, __shfl_xor_sync(0xffffffffu, hi, d));
-    fin = __shfl_xor_sync(0xffffffffu, (int)fin, d) && fin;
-  }
-  return make_grid<kKey>(lo, hi, fin);
+  return group_grid<kKey, 4>(min_bf2(min_bf2(x.x, x.y), min_bf2(x.z, x.w)), max_bf2(max_bf2(x.x, x.y), max_bf2(x.z, x.w)));
 }
 
 // One CTA per (sequence-group, block). 16 lanes hold a row, 8 channels each, so loads are whole
@@ -70,18 +76,20 @@ __global__ void __launch_bounds__(kQThreads) kv4_quantize_kernel(const Kv4CacheA
     const int t = row0 + r * (kQThreads / 16);
     {
       const Grid g = group_grid<true>(xk[r]);
-      uint32_t w = 0;
+      float c[8];
 #pragma unroll
-      for (int i = 0; i < 8; ++i) w |= code_of(bf_at(xk[r], i), g) << (4 * (i >> 1) + 16 * (i & 1));
+      for (int i = 0; i < 8; ++i) c[i] = code_of(bf_at(xk[r], i), g);
+      const uint32_t w = nibbles(c[0], c[2], c[4], c[6]) | nibbles(c[1], c[3], c[5], c[7]) << 16;
       *reinterpret_cast<uint32_t*>(blk + kKCodes + t * 64 + l16 * 4) = rol(w, 3);
       if ((l16 & 3) == 0) *reinterpret_cast<uint32_t*>(blk + kKScales + t * 16 + l16) = g.s16 | (g.z16 << 16);
     }
     {
       const Grid g = group_grid<false>(xv[r]);
       // channels 8 l16 + 0..3 in the low half, + 4..7 in the high half
-      uint32_t w = 0;
+      float c[8];
 #pragma unroll
-      for (int i = 0; i < 8; ++i) w |= code_of(bf_at(xv[r], i), g) << (4 * i);
+      for (int i = 0; i < 8; ++i) c[i] = code_of(bf_at(xv[r], i), g);
+      const uint32_t w = nibbles(c[0], c[1], c[2], c[3]) | nibbles(c[4], c[5], c[6], c[7]) << 16;
       // the even token's lane takes the first four channels of both tokens, the odd one's the rest
       const uint32_t other = __shfl_xor_sync(0xffffffffu, w, 16);
       const uint32_t both = (t & 1) ? __byte_perm(other, w, 0x7632) : __byte_perm(w, other, 0x5410);
@@ -196,23 +204,9 @@ __global__ void __launch_bounds__(64 * kAppendPerCta4) kv4_append_kernel(const K
   }
   const uint32_t kn = reinterpret_cast<const uint32_t*>(a.k + (size_t)bg * kHeadDim)[t];
   const uint32_t vn = reinterpret_cast<const uint32_t*>(a.v + (size_t)bg * kHeadDim)[t];
-  Grid gk, gv;
-#pragma unroll
-  for (int which = 0; which < 2; ++which) {
-    const uint32_t x = which ? vn : kn;
-    float lo = fminf(bf16_lo(x), bf16_hi(x)), hi = fmaxf(bf16_lo(x), bf16_hi(x));
-    int fin = fabsf(bf16_lo(x)) < INFINITY && fabsf(bf16_hi(x)) < INFINITY;
-#pragma unroll
-    for (int d = 1; d <= 8; d <<= 1) {
-      lo = fminf(lo, __shfl_xor_sync(0xffffffffu, lo, d));
-      hi = fmaxf(hi, __shfl_xor_sync(0xffffffffu, hi, d));
-      fin &= __shfl_xor_sync(0xffffffffu, fin, d);
-    }
-    if (which) gv = make_grid<false>(lo, hi, fin);
-    else gk = make_grid<true>(lo, hi, fin);
-  }
+  const Grid gk = group_grid<true, 16>(kn, kn), gv = group_grid<false, 16>(vn, vn);
   // key: four threads make a word
-  const uint32_t ck0 = code_of(bf16_lo(kn), gk), ck1 = code_of(bf16_hi(kn), gk);
+  const uint32_t ck0 = (uint32_t)code_of(bf16_lo(kn), gk), ck1 = (uint32_t)code_of(bf16_hi(kn), gk);
   uint32_t w = (ck0 | (ck1 << 16)) << (4 * (t & 3));
   w |= __shfl_xor_sync(0xffffffffu, w, 1);
   w |= __shfl_xor_sync(0xffffffffu, w, 2);
@@ -221,7 +215,7 @@ __global__ void __launch_bounds__(64 * kAppendPerCta4) kv4_append_kernel(const K
   if ((t & 15) == 0) *reinterpret_cast<uint32_t*>(blk + kKScales + tok * 16 + (t >> 4) * 4) = gk.s16 | (gk.z16 << 16);
   // value: two threads make the half-word of four channels; the other half belongs to the pair's
   // other token and is kept
-  uint32_t hw = (code_of(bf16_lo(vn), gv) | (code_of(bf16_hi(vn), gv) << 4)) << (8 * (t & 1));
+  uint32_t hw = ((uint32_t)code_of(bf16_lo(vn), gv) | ((uint32_t)code_of(bf16_hi(vn), gv) << 4)) << (8 * (t & 1));
   hw |= __shfl_xor_sync(0xffffffffu, hw, 1);
   const int pair = tok >> 1;
   if ((t & 1) == 0) {

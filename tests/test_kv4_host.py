@@ -145,7 +145,7 @@ def test_binding_refuses_tensors_on_another_device():
 
 
 def test_binding_checks_types_sizes_and_strides():
-    dev = torch.device("cpu")
+    dev = -1
     ok = torch.zeros((4, 8), dtype=torch.bfloat16)
     assert sb._checked("x", ok, torch.bfloat16, 32, dev) == ok.data_ptr()
     for bad in (ok.float(), ok[:3], ok.t()):
