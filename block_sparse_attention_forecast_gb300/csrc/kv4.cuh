@@ -105,17 +105,31 @@ __device__ __forceinline__ uint32_t value_pair(uint32_t word, int p, uint32_t s2
 __device__ __forceinline__ uint32_t dup_lo(uint32_t u) { return __byte_perm(u, u, 0x1010); }
 __device__ __forceinline__ uint32_t dup_hi(uint32_t u) { return __byte_perm(u, u, 0x3232); }
 
-// A group's grid: s and z as stored (16 bits each) and as float, and 1 / s for the first guess.
+// A group's grid: s and z as stored (16 bits each), and what the codes are found with, in units of
+// 2^-64, 1 or 2^64 so that neither s nor 1 / s leaves float32's range.
 struct Grid {
   uint32_t s16, z16;
-  float s, z, r;
+  float unit, s, z, r;          // s and z times the unit, and 1 / s
+  bool clamp;                   // whether a code may leave 0 .. 15
 };
+
+// x / 15 rounded to float32 and then to the storage type, given as float: by a multiplication, except
+// beside the storage type's rounding borders (the dropped bits within 2 units of halfway), where the
+// division decides.
+template <bool kKey>
+__device__ __forceinline__ float fifteenth(float x) {
+  float q = x * (1.0f / 15.0f);
+  constexpr uint32_t kDropped = kKey ? 0xffffu : 0x1fffu, kHalf = (kDropped + 1) / 2;
+  const bool plain = kKey ? q >= 1e-30f : q >= 6.2e-5f;      // above the storage type's subnormals
+  if (!plain || (__float_as_uint(q) & kDropped) - (kHalf - 3u) <= 6u) q = __fdiv_rn(x, 15.0f);
+  return q;
+}
 
 // lo or hi is a NaN or an infinity if the group holds one.
 template <bool kKey>
 __device__ __forceinline__ Grid make_grid(float lo, float hi) {
   Grid g;
-  const float step = __fdiv_rn(__fsub_rn(hi, lo), 15.0f);
+  const float step = fifteenth<kKey>(__fsub_rn(hi, lo));
   if (kKey) {
     const __nv_bfloat16 s = __float2bfloat16_rn(step);
     g.s = __bfloat162float(s);
@@ -131,37 +145,58 @@ __device__ __forceinline__ Grid make_grid(float lo, float hi) {
     g.s16 = __half_as_ushort(s);
     g.z16 = __half_as_ushort(z);
   }
-  if (!(fabsf(g.z) < INFINITY) || !(g.s < INFINITY)) {
-    g.s = g.z = 0.f;                               // codes 0; the offset makes every value NaN
-    g.s16 = 0u;
-    g.z16 = 0x7fffu;                               // NaN in bf16 and in fp16
+  g.unit = 1.f;
+  if (!(fabsf(g.z) < INFINITY && g.s >= 1e-30f && g.s <= 1e30f)) {
+    if (!(fabsf(g.z) < INFINITY) || !(g.s < INFINITY)) {
+      g.s = g.z = 0.f;                             // the offset makes every value NaN
+      g.s16 = 0u;
+      g.z16 = 0x7fffu;                             // NaN in bf16 and in fp16
+    }
+    if (g.s > 0.f) g.unit = g.s > 1.f ? 5.421010862427522e-20f : 18446744073709551616.f;
+    g.s *= g.unit;
+    g.z *= g.unit;
   }
-  g.r = __frcp_rn(g.s);
+  asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(g.r) : "f"(g.s));
+  // only where the offset's rounding moved the grid past lo or hi; s = 0 (a NaN here) too
+  g.clamp = !(fmaf(lo, g.unit, -g.z) * g.r > 15.6f && fmaf(hi, g.unit, -g.z) * g.r < 31.4f);
   return g;
 }
 
-// clamp(rint((x - z) / s - 16), 0, 15) for a finite x, as a float. Without the division: c is the
-// nearest whole number to (x - z) / s up to the error of the guess, and e = (x - z) - c s is exact
-// (c s has at most 17 bits, and the difference is no larger than s), so comparing e with s / 2 decides
-// at and near the borders, ties to even. (A quotient that is not exactly halfway does not round to
-// halfway either: x - z and the border times s are at least one unit of x - z apart.)
-__device__ __forceinline__ float code_of(float x, const Grid& g) {
+// c[i] = 16 + clamp(rint((x[i] - z) / s - 16), 0, 15) for finite x, as floats. Without the division:
+// c is the nearest whole number to (x - z) / s up to the error of the guess, and e = (x - z) - c s is
+// exact (c s has at most 17 bits, and the difference is no larger than s), so comparing e with s / 2
+// decides at and near the borders, ties to even. (A quotient that is not exactly halfway does not
+// round to halfway either: x - z and the border times s are at least one unit of x - z apart.) The
+// borders are met by one value in 500, so they are looked after once for all the values.
+template <int kN>
+__device__ __forceinline__ void codes_of(const float (&x)[kN], const Grid& g, float (&c)[kN]) {
   constexpr float kWhole = 12582912.f;             // 1.5 * 2^23: adding it rounds to whole numbers
-  const float d = __fsub_rn(x, g.z);
-  float c = __fsub_rn(__fadd_rn(__fmul_rn(d, g.r), kWhole), kWhole);
-  const float e = fmaf(-c, g.s, d), half = 0.5f * g.s;
-  if (fabsf(e) >= half) {
-    if (!(g.s >= 1e-30f))                          // 1 / s may overflow, and half of s lose a bit
-      c = g.s > 0.f ? rintf(__fsub_rn(__fdiv_rn(d, g.s), 16.0f)) + 16.0f : 16.0f;
-    else if (fabsf(e) > half || ((int)c & 1))
-      c += e > 0.f ? 1.f : -1.f;
+  const float half = 0.5f * g.s;
+  float e[kN];
+  bool border = false;
+#pragma unroll
+  for (int i = 0; i < kN; ++i) {
+    const float d = fmaf(x[i], g.unit, -g.z);
+    c[i] = fmaf(d, g.r, kWhole) - kWhole;
+    e[i] = fmaf(-c[i], g.s, d);
+    border = border || !(fabsf(e[i]) < half);
   }
-  return fminf(fmaxf(c, 16.f), 31.f) - 16.f;
+  if (border) {
+#pragma unroll
+    for (int i = 0; i < kN; ++i)
+      if (fabsf(e[i]) > half || (fabsf(e[i]) == half && (__float_as_uint(c[i] + kWhole) & 1u)))
+        c[i] += e[i] > 0.f ? 1.f : -1.f;
+  }
+  if (g.clamp) {
+#pragma unroll
+    for (int i = 0; i < kN; ++i) c[i] = fminf(fmaxf(c[i], 16.f), 31.f);
+  }
 }
 
-// Four codes (whole floats) as four nibbles, the first lowest.
+// Four results of codes_of as four nibbles, the first lowest.
 __device__ __forceinline__ uint32_t nibbles(float c0, float c1, float c2, float c3) {
-  return __float_as_uint(fmaf(fmaf(fmaf(c3, 16.f, c2), 16.f, c1), 16.f, c0) + 8388608.f) & 0xffffu;
+  constexpr float kBase = 8388608.f - 16.f * 0x1111;
+  return __float_as_uint(fmaf(fmaf(fmaf(c3, 16.f, c2), 16.f, c1), 16.f, c0) + kBase) & 0xffffu;
 }
 
 // Byte offset in a block of the 16 bytes of value codes of token pair `pair` (token / 2) and

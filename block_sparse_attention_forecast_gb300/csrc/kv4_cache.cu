@@ -12,11 +12,6 @@ using namespace kv4;
 constexpr int kQThreads = 256;
 constexpr int kQRounds = kBlock * 16 / kQThreads;      // (token, 8 channels) items per thread: 4
 
-__device__ __forceinline__ float bf_at(const uint4& x, int i) {
-  const uint32_t u = i < 2 ? x.x : i < 4 ? x.y : i < 6 ? x.z : x.w;
-  return (i & 1) ? bf16_hi(u) : bf16_lo(u);
-}
-
 // (smallest, -largest) of packed bf16 pairs; a NaN takes over.
 __device__ __forceinline__ uint32_t min_bf2(uint32_t x, uint32_t y) {
   uint32_t r;
@@ -28,10 +23,15 @@ __device__ __forceinline__ uint32_t max_bf2(uint32_t x, uint32_t y) {
   asm("max.NaN.bf16x2 %0, %1, %2;" : "=r"(r) : "r"(x), "r"(y));
   return r;
 }
-// The grid of a 32-channel group, its extremes reduced over `kLanes` neighbouring lanes. lo, hi: this
-// lane's smallest and largest values, in pairs.
+// The grid of a 32-channel group spread over kLanes neighbouring lanes; x: the lane's values, in pairs.
 template <bool kKey, int kLanes>
-__device__ __forceinline__ Grid group_grid(uint32_t lo, uint32_t hi) {
+__device__ __forceinline__ Grid group_grid(const uint32_t (&x)[16 / kLanes]) {
+  uint32_t lo = x[0], hi = x[0];
+#pragma unroll
+  for (int i = 1; i < 16 / kLanes; ++i) {
+    lo = min_bf2(lo, x[i]);
+    hi = max_bf2(hi, x[i]);
+  }
   lo = min_bf2(lo, dup_hi(lo));                    // the low half is the smaller of the pair
   hi = max_bf2(hi, dup_hi(hi));
   uint32_t v = __byte_perm(lo, hi ^ 0x8000u, 0x5410);    // (lo, -hi): one minimum for both
@@ -39,15 +39,16 @@ __device__ __forceinline__ Grid group_grid(uint32_t lo, uint32_t hi) {
   for (int d = 1; d < kLanes; d <<= 1) v = min_bf2(v, __shfl_xor_sync(0xffffffffu, v, d));
   return make_grid<kKey>(bf16_lo(v), -bf16_hi(v));
 }
-template <bool kKey>
-__device__ __forceinline__ Grid group_grid(const uint4& x) {
-  return group_grid<kKey, 4>(min_bf2(min_bf2(x.x, x.y), min_bf2(x.z, x.w)), max_bf2(max_bf2(x.x, x.y), max_bf2(x.z, x.w)));
+// The codes, plus 16, of four pairs of values.
+__device__ __forceinline__ void codes8(uint32_t x0, uint32_t x1, uint32_t x2, uint32_t x3, const Grid& g, float (&c)[8]) {
+  const float f[8] = {bf16_lo(x0), bf16_hi(x0), bf16_lo(x1), bf16_hi(x1), bf16_lo(x2), bf16_hi(x2), bf16_lo(x3), bf16_hi(x3)};
+  codes_of(f, g, c);
 }
 
-// One CTA per (sequence-group, block). 16 lanes hold a row, 8 channels each, so loads are whole
-// lines and a group's extremes take two shuffles. The block is put together in shared memory and
-// leaves as one bulk copy: written directly, the value codes would leave as 16-byte pieces 64
-// bytes apart.
+// One CTA per (sequence-group, block), one thread per (token, group of 32 channels) of the keys and of
+// the values: a group's extremes and grid are found once, by the thread that needs them. Its 64 bytes
+// are four loads that the lanes' lines share. The block is put together in shared memory and leaves
+// as one bulk copy.
 __global__ void __launch_bounds__(kQThreads) kv4_quantize_kernel(const Kv4CacheArgs a) {
   __shared__ alignas(128) uint8_t blk[kBlockBytes4];
   grid_dep_wait();
@@ -59,45 +60,56 @@ __global__ void __launch_bounds__(kQThreads) kv4_quantize_kernel(const Kv4CacheA
     return;
   }
   if (j * kBlock >= T) return;
-  const int l16 = threadIdx.x & 15, row0 = threadIdx.x >> 4;
-  const uint4* k = reinterpret_cast<const uint4*>(a.k) + ((size_t)bg * a.max_ctx + (size_t)j * kBlock) * 16 + l16;
-  const uint4* v = reinterpret_cast<const uint4*>(a.v) + ((size_t)bg * a.max_ctx + (size_t)j * kBlock) * 16 + l16;
-  const int live = min(kBlock, T - j * kBlock);
-  uint4 xk[kQRounds], xv[kQRounds];
+  const int t = threadIdx.x >> 2, grp = threadIdx.x & 3;
+  const size_t row = (size_t)bg * a.max_ctx + (size_t)j * kBlock + t;
+  const bool live = j * kBlock + t < T;            // rows past the prompt are stored as zeros
+  uint32_t xk[16], xv[16];
 #pragma unroll
-  for (int r = 0; r < kQRounds; ++r) {
-    const int t = row0 + r * (kQThreads / 16);
-    const bool in = t < live;                      // rows past the prompt are stored as zeros
-    xk[r] = in ? __ldcs(k + (size_t)t * 16) : make_uint4(0, 0, 0, 0);
-    xv[r] = in ? __ldcs(v + (size_t)t * 16) : make_uint4(0, 0, 0, 0);
+  for (int i = 0; i < 4; ++i) {
+    const uint4 none = make_uint4(0, 0, 0, 0);
+    const uint4 k = live ? __ldcs(reinterpret_cast<const uint4*>(a.k) + row * 16 + grp * 4 + i) : none;
+    const uint4 v = live ? __ldcs(reinterpret_cast<const uint4*>(a.v) + row * 16 + grp * 4 + i) : none;
+    xk[4 * i] = k.x, xk[4 * i + 1] = k.y, xk[4 * i + 2] = k.z, xk[4 * i + 3] = k.w;
+    xv[4 * i] = v.x, xv[4 * i + 1] = v.y, xv[4 * i + 2] = v.z, xv[4 * i + 3] = v.w;
   }
+  {
+    const Grid g = group_grid<true, 1>(xk);
+    uint32_t w[4];
 #pragma unroll
-  for (int r = 0; r < kQRounds; ++r) {
-    const int t = row0 + r * (kQThreads / 16);
-    {
-      const Grid g = group_grid<true>(xk[r]);
+    for (int i = 0; i < 4; ++i) {
       float c[8];
-#pragma unroll
-      for (int i = 0; i < 8; ++i) c[i] = code_of(bf_at(xk[r], i), g);
-      const uint32_t w = nibbles(c[0], c[2], c[4], c[6]) | nibbles(c[1], c[3], c[5], c[7]) << 16;
-      *reinterpret_cast<uint32_t*>(blk + kKCodes + t * 64 + l16 * 4) = rol(w, 3);
-      if ((l16 & 3) == 0) *reinterpret_cast<uint32_t*>(blk + kKScales + t * 16 + l16) = g.s16 | (g.z16 << 16);
+      codes8(xk[4 * i], xk[4 * i + 1], xk[4 * i + 2], xk[4 * i + 3], g, c);
+      w[i] = rol(nibbles(c[0], c[2], c[4], c[6]) | nibbles(c[1], c[3], c[5], c[7]) << 16, 3);
     }
-    {
-      const Grid g = group_grid<false>(xv[r]);
-      // channels 8 l16 + 0..3 in the low half, + 4..7 in the high half
+    *reinterpret_cast<uint4*>(blk + kKCodes + threadIdx.x * 16) = make_uint4(w[0], w[1], w[2], w[3]);
+    *reinterpret_cast<uint32_t*>(blk + kKScales + threadIdx.x * 4) = g.s16 | (g.z16 << 16);
+  }
+  {
+    const Grid g = group_grid<false, 1>(xv);
+    uint32_t h[8];                                 // four channels each, in the low half
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
       float c[8];
-#pragma unroll
-      for (int i = 0; i < 8; ++i) c[i] = code_of(bf_at(xv[r], i), g);
-      const uint32_t w = nibbles(c[0], c[1], c[2], c[3]) | nibbles(c[4], c[5], c[6], c[7]) << 16;
-      // the even token's lane takes the first four channels of both tokens, the odd one's the rest
-      const uint32_t other = __shfl_xor_sync(0xffffffffu, w, 16);
-      const uint32_t both = (t & 1) ? __byte_perm(other, w, 0x7632) : __byte_perm(w, other, 0x5410);
-      *reinterpret_cast<uint32_t*>(blk + value_chunk(t >> 1, l16 >> 1) + ((l16 & 1) * 2 + (t & 1)) * 4) = rol(both, 2);
-      const uint32_t so = __shfl_xor_sync(0xffffffffu, g.s16, 16), zo = __shfl_xor_sync(0xffffffffu, g.z16, 16);
-      if ((l16 & 3) == 0 && !(t & 1))
-        *reinterpret_cast<uint2*>(blk + value_scale(t >> 1, l16 >> 2)) = make_uint2(g.s16 | (so << 16), g.z16 | (zo << 16));
+      codes8(xv[4 * i], xv[4 * i + 1], xv[4 * i + 2], xv[4 * i + 3], g, c);
+      h[2 * i] = nibbles(c[0], c[1], c[2], c[3]);
+      h[2 * i + 1] = nibbles(c[4], c[5], c[6], c[7]);
     }
+    // the even token's thread takes the first octet of 16 channels of both tokens, the odd one's the other
+    const bool odd = t & 1;
+    uint32_t w[4];
+#pragma unroll
+    for (int i = 0; i < 4; i += 2) {
+      const uint32_t give = odd ? h[i] | h[i + 1] << 16 : h[4 + i] | h[5 + i] << 16;
+      const uint32_t take = __shfl_xor_sync(0xffffffffu, give, 4);
+      const uint32_t own0 = odd ? h[4 + i] : h[i], own1 = odd ? h[5 + i] : h[i + 1];
+      w[i] = rol(odd ? __byte_perm(take, own0, 0x5410) : __byte_perm(own0, take, 0x5410), 2);
+      w[i + 1] = rol(odd ? __byte_perm(take, own1, 0x5432) : __byte_perm(own1, take, 0x7610), 2);
+    }
+    *reinterpret_cast<uint4*>(blk + value_chunk(t >> 1, 2 * grp + (t & 1))) = make_uint4(w[0], w[1], w[2], w[3]);
+    const uint32_t sz = g.s16 | (g.z16 << 16), so = __shfl_xor_sync(0xffffffffu, sz, 4);
+    if (!odd)
+      *reinterpret_cast<uint2*>(blk + value_scale(t >> 1, grp)) =
+          make_uint2(__byte_perm(sz, so, 0x5410), __byte_perm(sz, so, 0x7632));
   }
   fence_proxy_async_shared();
   __syncthreads();
@@ -204,10 +216,12 @@ __global__ void __launch_bounds__(64 * kAppendPerCta4) kv4_append_kernel(const K
   }
   const uint32_t kn = reinterpret_cast<const uint32_t*>(a.k + (size_t)bg * kHeadDim)[t];
   const uint32_t vn = reinterpret_cast<const uint32_t*>(a.v + (size_t)bg * kHeadDim)[t];
-  const Grid gk = group_grid<true, 16>(kn, kn), gv = group_grid<false, 16>(vn, vn);
+  const Grid gk = group_grid<true, 16>({kn}), gv = group_grid<false, 16>({vn});
+  float ck[2], cv[2];
+  codes_of({bf16_lo(kn), bf16_hi(kn)}, gk, ck);
+  codes_of({bf16_lo(vn), bf16_hi(vn)}, gv, cv);
   // key: four threads make a word
-  const uint32_t ck0 = (uint32_t)code_of(bf16_lo(kn), gk), ck1 = (uint32_t)code_of(bf16_hi(kn), gk);
-  uint32_t w = (ck0 | (ck1 << 16)) << (4 * (t & 3));
+  uint32_t w = (((uint32_t)ck[0] - 16u) | (((uint32_t)ck[1] - 16u) << 16)) << (4 * (t & 3));
   w |= __shfl_xor_sync(0xffffffffu, w, 1);
   w |= __shfl_xor_sync(0xffffffffu, w, 2);
   w = rol(w, 3);
@@ -215,7 +229,7 @@ __global__ void __launch_bounds__(64 * kAppendPerCta4) kv4_append_kernel(const K
   if ((t & 15) == 0) *reinterpret_cast<uint32_t*>(blk + kKScales + tok * 16 + (t >> 4) * 4) = gk.s16 | (gk.z16 << 16);
   // value: two threads make the half-word of four channels; the other half belongs to the pair's
   // other token and is kept
-  uint32_t hw = ((uint32_t)code_of(bf16_lo(vn), gv) | ((uint32_t)code_of(bf16_hi(vn), gv) << 4)) << (8 * (t & 1));
+  uint32_t hw = (((uint32_t)cv[0] - 16u) | (((uint32_t)cv[1] - 16u) << 4)) << (8 * (t & 1));
   hw |= __shfl_xor_sync(0xffffffffu, hw, 1);
   const int pair = tok >> 1;
   if ((t & 1) == 0) {
