@@ -5,8 +5,8 @@
 //
 //   evict_select_kernel   one CTA per (sequence, group): the kept list. The weights stay in
 //                         registers as order-preserving integers; the (keep - forced)-th largest
-//                         is found bit by bit, 32 counts over the CTA at most, which does not
-//                         depend on how the weights are spread (many blocks tie at 0).
+//                         is found digit by digit, three histograms at most, whatever the
+//                         weights' spread; of the keys tied there the lowest blocks are taken.
 //   evict_move_kernel     into another cache: one CTA per kept block. Bytes in, bytes out.
 //   evict_shift_kernel    in the cache itself: block n moves from kept[n] >= n, so a block may be
 //                         overwritten only once it has been read. One thread-block cluster per
@@ -30,6 +30,7 @@ namespace {
 
 constexpr int kSelThreads = 512;
 constexpr int kSelPer = kMaxCtx / kBlock / kSelThreads;         // weights per thread: 8
+constexpr int kBins = 2048;
 constexpr int kMoveThreads = 256;
 constexpr int kShiftSmem = 220 * 1024;                          // two rounds of a CTA's blocks
 constexpr int kCkRow = kHeadDim * 2;                            // bytes of a compressed key
@@ -83,8 +84,8 @@ __device__ __forceinline__ bool joins(int n, int count, int T, bool neighbour) {
 }  // namespace
 
 __global__ void __launch_bounds__(kSelThreads) evict_select_kernel(const EvictArgs a) {
-  __shared__ int s_cnt[32];
-  __shared__ int s_warp[2][kSelThreads / 32];
+  __shared__ int s_bin[kBins], s_found[3];
+  __shared__ int s_warp[3][kSelThreads / 32];
   grid_dep_wait();
   grid_dep_launch();
   const int bg = blockIdx.x, b = bg / a.G, tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
@@ -105,7 +106,6 @@ __global__ void __launch_bounds__(kSelThreads) evict_select_kernel(const EvictAr
     const int j = tid * kSelPer + i;
     key[i] = j >= 1 && j < n - a.recent ? weight_key(w[i]) : 0u;     // candidates only
   }
-  if (tid < 32) s_cnt[tid] = 0;
   __syncthreads();                                 // in place: every weight is read before one is written
   uint32_t sel = 0;                                // bit i: block tid * kSelPer + i is kept
   if (n <= a.keep) {
@@ -113,57 +113,79 @@ __global__ void __launch_bounds__(kSelThreads) evict_select_kernel(const EvictAr
     for (int i = 0; i < kSelPer; ++i) sel |= (tid * kSelPer + i < n ? 1u : 0u) << i;
   } else {
     const int want = a.keep - 1 - a.recent;        // candidates to keep; more of them exist
-    uint32_t thr = 0xffffffffu;                    // the want-th largest key
-    int above = 0;                                 // candidates above it
+    uint32_t thr = 0xffffffffu;                    // the want-th largest key (its leading bits)
+    int share = 0, low = 0;                        // of the keys whose bits above `low` are thr's, the share kept
     if (want > 0) {
+      // digits of 11, 11 and 10 bits: a histogram of the keys that agree so far, and the digit at
+      // which the counts from the top reach the share
       thr = 0u;
-      for (int bit = 31; bit >= 0; --bit) {
-        const uint32_t tryk = thr | (1u << bit);
-        int c = 0;
-#pragma unroll
-        for (int i = 0; i < kSelPer; ++i) c += key[i] >= tryk;
-        c = __reduce_add_sync(0xffffffffu, c);
-        if (lane == 0 && c) atomicAdd(&s_cnt[bit], c);
+      share = want;
+#pragma unroll 1
+      for (int pass = 0; pass < 3; ++pass) {
+        const int bits = pass < 2 ? 11 : 10, above = pass == 0 ? 32 : pass == 1 ? 21 : 10;
+        low = above - bits;
+        for (int i = tid; i < kBins; i += kSelThreads) s_bin[i] = 0;
         __syncthreads();
-        const int total = s_cnt[bit];
-        if (total >= want) {
-          thr = tryk;
-          if (total == want) break;                // exactly the keys at or above thr
-        }
-      }
-      // keys above thr, for the share of the ties
-      __syncthreads();
-      if (tid == 0) s_cnt[0] = 0;
-      __syncthreads();
-      int c = 0;
 #pragma unroll
-      for (int i = 0; i < kSelPer; ++i) c += key[i] > thr;
-      c = __reduce_add_sync(0xffffffffu, c);
-      if (lane == 0 && c) atomicAdd(&s_cnt[0], c);
-      __syncthreads();
-      above = s_cnt[0];
+        for (int i = 0; i < kSelPer; ++i)
+          if (key[i] != 0u && (pass == 0 || (key[i] ^ thr) >> above == 0u))
+            atomicAdd(&s_bin[(key[i] >> low) & ((1u << bits) - 1u)], 1);
+        __syncthreads();
+        // this thread's bins are the highest kBins / kSelThreads not yet taken: thread 0 the top ones
+        constexpr int kPer = kBins / kSelThreads;
+        int n_bin[kPer], mine = 0;
+#pragma unroll
+        for (int i = 0; i < kPer; ++i) {
+          n_bin[i] = s_bin[kBins - 1 - tid * kPer - i];
+          mine += n_bin[i];
+        }
+        int sum = mine;
+#pragma unroll
+        for (int d = 1; d < 32; d <<= 1) {
+          const int o = __shfl_up_sync(0xffffffffu, sum, d);
+          if (lane >= d) sum += o;
+        }
+        if (lane == 31) s_warp[0][warp] = sum;
+        __syncthreads();
+        for (int q = 0; q < warp; ++q) sum += s_warp[0][q];
+        int before = sum - mine;
+#pragma unroll
+        for (int i = 0; i < kPer; ++i) {
+          if (before < share && before + n_bin[i] >= share) {
+            s_found[0] = kBins - 1 - tid * kPer - i;
+            s_found[1] = share - before;
+            s_found[2] = n_bin[i];
+          }
+          before += n_bin[i];
+        }
+        __syncthreads();
+        thr |= (uint32_t)s_found[0] << low;
+        share = s_found[1];
+        if (s_found[2] == share) break;            // all of them are kept
+      }
     }
+    const uint32_t lead = thr >> low;              // keys are ranked by their bits from `low` on
     // ties go to the lowest blocks: the rank of each key equal to thr
     int ties = 0;
 #pragma unroll
-    for (int i = 0; i < kSelPer; ++i) ties += want > 0 && key[i] == thr && key[i] != 0u;
+    for (int i = 0; i < kSelPer; ++i) ties += want > 0 && key[i] != 0u && key[i] >> low == lead;
     int scan = ties;
 #pragma unroll
     for (int d = 1; d < 32; d <<= 1) {
       const int o = __shfl_up_sync(0xffffffffu, scan, d);
       if (lane >= d) scan += o;
     }
-    if (lane == 31) s_warp[0][warp] = scan;
+    if (lane == 31) s_warp[1][warp] = scan;
     __syncthreads();
     int rank = scan - ties;
-    for (int q = 0; q < warp; ++q) rank += s_warp[0][q];
+    for (int q = 0; q < warp; ++q) rank += s_warp[1][q];
 #pragma unroll
     for (int i = 0; i < kSelPer; ++i) {
       const int j = tid * kSelPer + i;
       bool in = j == 0 || (j >= n - a.recent && j < n);
       if (want > 0 && key[i] != 0u) {
-        in = in || key[i] > thr;
-        if (key[i] == thr) in = in || rank++ < want - above;
+        in = in || key[i] >> low > lead;
+        if (key[i] >> low == lead) in = in || rank++ < share;
       }
       sel |= (in ? 1u : 0u) << i;
     }
@@ -176,10 +198,10 @@ __global__ void __launch_bounds__(kSelThreads) evict_select_kernel(const EvictAr
     const int o = __shfl_up_sync(0xffffffffu, scan, d);
     if (lane >= d) scan += o;
   }
-  if (lane == 31) s_warp[1][warp] = scan;
+  if (lane == 31) s_warp[2][warp] = scan;
   __syncthreads();
   int at = scan - mine;
-  for (int q = 0; q < warp; ++q) at += s_warp[1][q];
+  for (int q = 0; q < warp; ++q) at += s_warp[2][q];
   int32_t* kept = a.kept + (size_t)bg * a.keep;
   float* dst = a.dst_mass + (size_t)bg * a.dst_nb;
 #pragma unroll
@@ -206,17 +228,22 @@ __global__ void __launch_bounds__(kMoveThreads) evict_move_kernel(const EvictArg
   const int T0 = a.src_len[bg / a.G];
   const int T = kept_len(T0, a.keep), count = min(blocks_of(T0), a.keep);
   const size_t from = (size_t)bg * a.src_nb + j, to = (size_t)bg * a.dst_nb + n;
+  // all of the block's loads are in flight before the first store
   const int vecs = a.block_bytes / 16;
-  for (int p = 0; p < a.planes; ++p) {
+  uint4 r[2][4];
+#pragma unroll
+  for (int p = 0; p < 2; ++p) {
     const uint4* s = reinterpret_cast<const uint4*>(a.src[p] + from * a.block_bytes);
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+      if (p < a.planes && tid + i * kMoveThreads < vecs) r[p][i] = __ldcs(s + tid + i * kMoveThreads);
+  }
+#pragma unroll
+  for (int p = 0; p < 2; ++p) {
     uint4* d = reinterpret_cast<uint4*>(a.dst[p] + to * a.block_bytes);
-    uint4 r[4];
 #pragma unroll
     for (int i = 0; i < 4; ++i)
-      if (tid + i * kMoveThreads < vecs) r[i] = __ldcs(s + tid + i * kMoveThreads);
-#pragma unroll
-    for (int i = 0; i < 4; ++i)
-      if (tid + i * kMoveThreads < vecs) d[tid + i * kMoveThreads] = r[i];
+      if (p < a.planes && tid + i * kMoveThreads < vecs) d[tid + i * kMoveThreads] = r[p][i];
   }
   const size_t src_row = (size_t)bg * (4 * a.src_nb - 1) + 4 * j, dst_row = (size_t)bg * (4 * a.dst_nb - 1) + 4 * n;
   const bool neighbour = nxt == j + 1;
