@@ -267,8 +267,17 @@ class LayerKV4:
     kv: torch.Tensor
     ck: torch.Tensor
 
+    on_host = False                # a 4-bit cache is resident
+
     def c(self):
         return c_layer_kv4(self.kv.data_ptr(), self.ck.data_ptr())
+
+    def __setattr__(self, name, value):
+        self.__dict__[name] = value
+        self.__dict__.pop("_args", None)
+
+    def __getstate__(self):
+        return {k: v for k, v in self.__dict__.items() if k != "_args"}
 
     @staticmethod
     def empty(shape, device="cuda"):
@@ -520,6 +529,7 @@ def sparda_prefetch_blocks_copy_engine(shape, layer, idx_host, cnt_host, seq_len
 
 # ------------------------------------------------------------------ the 4-bit cache, block mass, eviction
 _raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+_current_device = getattr(torch._C, "_cuda_getDevice", None) or torch.cuda.current_device
 
 
 def _stream_handle(stream, dev):
@@ -543,18 +553,25 @@ def _cache_device(t):
     """The index of the device that holds a layer's cache, which has to be the current one (the call's
     stream and the library's device state are its)."""
     dev = t.get_device()
-    if dev < 0 or dev != torch.cuda.current_device():
+    if dev < 0 or dev != _current_device():
         raise ValueError("the layer's cache is on %s; it has to be on the current CUDA device" % t.device)
     return dev
 
 
-def _kv4_dims(shape, layer, batch):
-    """(device, B, G, d, ctx, pointer to the C layer) of a call on a 4-bit cache, its tensors checked."""
-    dev = _cache_device(layer.kv)
-    G, d, ctx, rows = shape.n_groups, shape.head_dim, shape.max_ctx, shape.max_batch * shape.n_groups
-    c = c_layer_kv4(_checked("kv", layer.kv, torch.uint8, rows * (ctx // BLOCK) * KV4_BLOCK_BYTES, dev),
-                    _checked("ck", layer.ck, torch.bfloat16, rows * num_windows(ctx) * d, dev))
-    return dev, int(batch), G, d, ctx, ctypes.byref(c)
+def _kv4_layer(shape, layer):
+    """(device, pointer to the C layer) of a LayerKV4, its tensors checked. The C struct is kept with the
+    layer until one of its fields is set; the tensors' sizes and addresses are checked in every call."""
+    kv, ck = layer.kv, layer.ck
+    dev = _cache_device(kv)
+    rows = shape.max_batch * shape.n_groups
+    n_kv, n_ck = rows * (shape.max_ctx // BLOCK) * KV4_BLOCK_BYTES, rows * num_windows(shape.max_ctx) * shape.head_dim
+    args = layer.__dict__.get("_args")
+    if args is not None and args[0] == (kv.data_ptr(), ck.data_ptr()) and kv.numel() >= n_kv and ck.numel() >= n_ck:
+        return dev, args[1]
+    c = c_layer_kv4(_checked("kv", kv, torch.uint8, n_kv, dev), _checked("ck", ck, torch.bfloat16, n_ck, dev))
+    ref = ctypes.byref(c)
+    layer.__dict__["_args"] = ((c.kv, c.ck), ref)
+    return dev, ref
 
 
 def _selection_ptrs(shape, idx, cnt, bg, dev):
@@ -567,7 +584,8 @@ def _selection_ptrs(shape, idx, cnt, bg, dev):
 
 def sparda_kv4_quantize(shape, layer, k, v, seq_len, batch, stream=None):
     """Tokens 0 .. seq_len[b]-1 of k and v (bf16 [max_batch, G, max_ctx, d]) into a LayerKV4."""
-    dev, B, G, d, ctx, lc = _kv4_dims(shape, layer, batch)
+    dev, lc = _kv4_layer(shape, layer)
+    B, G, d, ctx = int(batch), shape.n_groups, shape.head_dim, shape.max_ctx
     n = shape.max_batch * G * ctx * d
     _check("sparda_kv4_quantize", lib.sparda_kv4_quantize(
         shape.ref(), lc, _checked("k", k, torch.bfloat16, n, dev), _checked("v", v, torch.bfloat16, n, dev),
@@ -577,7 +595,8 @@ def sparda_kv4_quantize(shape, layer, k, v, seq_len, batch, stream=None):
 def sparda_kv4_dequantize(shape, layer, seq_len, batch, k, v, idx=None, cnt=None, stream=None):
     """The values of a LayerKV4 as bf16: every token's rows into k and v [max_batch, G, max_ctx, d], or
     with idx and cnt the selected blocks' into staging buffers [max_batch, G, topk+2, 64, d]."""
-    dev, B, G, d, ctx, lc = _kv4_dims(shape, layer, batch)
+    dev, lc = _kv4_layer(shape, layer)
+    B, G, d, ctx = int(batch), shape.n_groups, shape.head_dim, shape.max_ctx
     pi, pc = _selection_ptrs(shape, idx, cnt, B * G, dev)
     n = shape.max_batch * G * (ctx if pi is None else (shape.topk + 2) * BLOCK) * d
     _check("sparda_kv4_dequantize", lib.sparda_kv4_dequantize(
@@ -587,7 +606,8 @@ def sparda_kv4_dequantize(shape, layer, seq_len, batch, k, v, idx=None, cnt=None
 
 def sparda_kv4_append(shape, layer, k_new, v_new, seq_len, batch, stream=None):
     """The current token's key and value (bf16 [B, G, d]) into a LayerKV4, with its compressed key."""
-    dev, B, G, d, _, lc = _kv4_dims(shape, layer, batch)
+    dev, lc = _kv4_layer(shape, layer)
+    B, G, d = int(batch), shape.n_groups, shape.head_dim
     _check("sparda_kv4_append", lib.sparda_kv4_append(
         shape.ref(), lc, _checked("k_new", k_new, torch.bfloat16, B * G * d, dev),
         _checked("v_new", v_new, torch.bfloat16, B * G * d, dev), _checked("seq_len", seq_len, torch.int32, B, dev), B,
@@ -598,7 +618,8 @@ def sparda_kv4_decode_attn(shape, layer, q, idx, cnt, seq_len, batch, out, ws, m
     """Decode attention over a LayerKV4: the selected blocks, or with idx = cnt = None every token.
     mass (float32 [max_batch, G, max_ctx / 64]): the block weights to add to; ws is then a
     WS_KV4_ATTN_MASS workspace, else a WS_KV4_ATTN one."""
-    dev, B, G, d, ctx, lc = _kv4_dims(shape, layer, batch)
+    dev, lc = _kv4_layer(shape, layer)
+    B, G, d, ctx = int(batch), shape.n_groups, shape.head_dim, shape.max_ctx
     n = B * G * shape.heads_per_group * d
     pi, pc = _selection_ptrs(shape, idx, cnt, B * G, dev)
     pm = None if mass is None else _checked("mass", mass, torch.float32, B * G * (ctx // BLOCK), dev)
@@ -661,13 +682,8 @@ def sparda_evict_blocks(shape, layer, mass, seq_len, batch, keep, recent, kept, 
            kept, dst_shape, dst, dst_mass, dst_seq_len, stream)
 
 
-def _kv4_ptrs(shape, layer):
-    dev, _, _, _, _, lc = _kv4_dims(shape, layer, 1)
-    return dev, lc
-
-
 def sparda_kv4_evict_blocks(shape, layer, mass, seq_len, batch, keep, recent, kept, dst_shape=None, dst=None,
                             dst_mass=None, dst_seq_len=None, stream=None):
     """sparda_evict_blocks of a LayerKV4."""
-    _evict("sparda_kv4_evict_blocks", lib.sparda_kv4_evict_blocks, _kv4_ptrs, shape, layer, mass, seq_len, batch, keep,
+    _evict("sparda_kv4_evict_blocks", lib.sparda_kv4_evict_blocks, _kv4_layer, shape, layer, mass, seq_len, batch, keep,
            recent, kept, dst_shape, dst, dst_mass, dst_seq_len, stream)
