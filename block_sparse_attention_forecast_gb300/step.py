@@ -21,6 +21,11 @@ and selects its own blocks with a same-layer forecast), three ways to launch the
     gathered blocks in an HBM cache of its own across steps, and the gather copies only the
     selected blocks the cache lacks (an extension beyond the pages).
 
+A layer may also keep its cache in 4 bits (LayerKV4, resident); its append and attention are then
+sparda_kv4_append and sparda_kv4_decode_attn. With block_mass, every attention also adds up the weight
+each block received, and evict() cuts the caches to the blocks with the most of it, in place (both are
+extensions beyond the pages, and run in "streams" mode).
+
 Every mode computes the same results bit for bit. Everything here is host-side orchestration
 of libsparda calls (no arithmetic); the whole step can be captured once into a CUDA graph and
 replayed. With host I/O attached (attach_host_io), every step also brings its inputs from
@@ -36,7 +41,9 @@ from . import binding as sb
 class DecodeStack:
     """Buffers and streams of an n_layers decode stack with forecast lookahead.
 
-    layers: list of sb.LayerKV (resident or offloaded; layer 0 must be resident).
+    layers: list of sb.LayerKV (resident or offloaded; layer 0 must be resident) or sb.LayerKV4.
+    block_mass: keep mass [n_layers, max_batch, G, max_ctx / 64], the attention weight that every
+    block of every layer received (no layer offloaded).
     W_self0: bf16 [G*d, hidden] (layer 0's same-layer forecast head); W_next[L]: bf16
     [G*d, hidden] for L < n_layers - 1 (layer L's head that forecasts layer L+1).
     Per-step inputs live in static device buffers h, q, k_new, v_new, seq_len; outputs in
@@ -46,7 +53,8 @@ class DecodeStack:
     MODES = ("pipelined", "fused", "streams")
 
     def __init__(self, shape, layers, W_self0, W_next, batch, device="cuda", gather_ctas=0,
-                 overlap=True, advance=False, after_attention=None, mode="pipelined", block_cache=None):
+                 overlap=True, advance=False, after_attention=None, mode="pipelined", block_cache=None,
+                 block_mass=False):
         self.shape = shape
         self.layers = layers
         self.n_layers = len(layers)
@@ -66,7 +74,11 @@ class DecodeStack:
         # Offloaded stacks keep them apart: layer L+1's selection must finish early so that
         # its gather overlaps layer L.
         assert mode in self.MODES, mode
-        self.mode = "streams" if self.any_offload else mode
+        self.kv4 = [isinstance(l, sb.LayerKV4) for l in layers]
+        if block_mass and self.any_offload:
+            raise ValueError("block_mass needs every layer resident")
+        # the fused launches read bf16 caches and leave no statistics
+        self.mode = "streams" if self.any_offload or any(self.kv4) or block_mass else mode
         G, H, d = shape.n_groups, shape.heads_per_group, shape.head_dim
         hidden = W_self0.shape[1]
         n, B = self.n_layers, batch
@@ -90,7 +102,14 @@ class DecodeStack:
         self.cnt = torch.zeros((n, B, G), dtype=torch.int32, device=device)
         self.seq_len = torch.ones(B, dtype=torch.int32, device=device)
         self.ws_sel = sb.workspace(shape, B, sb.WS_SELECT, device)
-        self.ws_attn = sb.workspace(shape, B, sb.WS_ATTN, device)
+        self.ws_attn = sb.workspace(shape, B, sb.WS_ATTN_MASS if block_mass else sb.WS_ATTN, device)
+        self.ws_attn4 = None
+        if any(self.kv4):
+            self.ws_attn4 = sb.workspace(shape, B, sb.WS_KV4_ATTN_MASS if block_mass else sb.WS_KV4_ATTN, device)
+        self.mass = None
+        if block_mass:
+            self.mass = torch.zeros((n, shape.max_batch, G, shape.max_ctx // shape.block), dtype=torch.float32,
+                                    device=device)
         self.ws_sel2 = sb.workspace(shape, B, sb.WS_SELECT, device) if self.mode != "streams" else None
         # block_cache = n_cache slots per (sequence, group): every offloaded layer keeps the
         # blocks it gathered in HBM across steps and gathers only the ones it lacks (an
@@ -304,8 +323,16 @@ class DecodeStack:
                     gather_done[L + 1].record(self.gather)
                     if not self.overlap:
                         main.wait_event(gather_done[L + 1])
-            sb.sparda_append_kv(sh, layer, self.k_new[L], self.v_new[L], self.seq_len, B, stream=main)
-            if layer.on_host and self.caches is not None:
+            append = sb.sparda_kv4_append if self.kv4[L] else sb.sparda_append_kv
+            append(sh, layer, self.k_new[L], self.v_new[L], self.seq_len, B, stream=main)
+            mass = None if self.mass is None else self.mass[L]
+            if self.kv4[L]:
+                sb.sparda_kv4_decode_attn(sh, layer, self.q[L], self.idx[L], self.cnt[L], self.seq_len, B, self.out[L],
+                                          self.ws_attn4, mass=mass, stream=main)
+            elif mass is not None:
+                sb.sparda_sparse_decode_attn_mass(sh, layer, self.q[L], self.idx[L], self.cnt[L], self.seq_len, B,
+                                                  self.out[L], self.ws_attn, mass, stream=main)
+            elif layer.on_host and self.caches is not None:
                 main.wait_event(gather_done[L])
                 sb.sparda_sparse_decode_attn_cached(sh, layer, self.caches[L], self.q[L], self.idx[L], self.cnt[L],
                                                     self.seq_len, B, self.out[L], self.ws_attn, stream=main)
@@ -417,17 +444,35 @@ class DecodeStack:
         else:
             self.enqueue()
 
+    def evict(self, keep, recent=1):
+        """Between two steps, with seq_len already counting the next step's token (as advance leaves it):
+        cut every sequence's cached tokens to `keep` blocks -- block 0, the `recent` newest and, per layer
+        and group, those with the largest mass -- in place, and seq_len with them. Returns kept, int32
+        [n_layers, B, G, keep]: the old block numbers. In place, so a captured step goes on."""
+        if self.mass is None:
+            raise ValueError("evict needs a stack with block_mass")
+        B = self.batch
+        kept = torch.full((self.n_layers, B, self.shape.n_groups, int(keep)), -1, dtype=torch.int32, device=self.device)
+        cached = (self.seq_len - 1).clamp_(min=1)     # an empty sequence has nothing to move either way
+        for L, layer in enumerate(self.layers):
+            lens = cached.clone()                     # every layer is cut from the same length
+            cut = sb.sparda_kv4_evict_blocks if self.kv4[L] else sb.sparda_evict_blocks
+            cut(self.shape, layer, self.mass[L], lens, B, keep, recent, kept[L])
+        self.seq_len.sub_(cached - lens)
+        return kept
+
     def kernel_launches_per_step(self):
         """Kernels of libsparda one step launches. All modes start with layer 0's own
         projection and selection. Pipelined: then per layer a prologue, per layer but the
         last an attend-and-score, the last layer's attention alone. Fused: per layer an
         append, per layer but the last a projection and an attend-and-select, the last
         layer's attention. Streams: per layer append and attention, per layer but the last a
-        projection and a selection, one gather per offloaded layer."""
+        projection and a selection, one gather per offloaded layer, one block-mass launch per
+        layer where that is kept."""
         n = self.n_layers
         if self.mode == "pipelined":
             return 2 + n + (n - 1) + 1
         if self.mode == "fused":
             return 2 + n + 2 * (n - 1) + 1
         gathers = sum(1 for l in self.layers[1:] if l.on_host) * (2 if self.caches is not None else 1)
-        return 2 + n * 2 + (n - 1) * 2 + gathers
+        return 2 + n * 2 + (n - 1) * 2 + gathers + (n if self.mass is not None else 0)
