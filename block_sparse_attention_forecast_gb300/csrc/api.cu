@@ -854,15 +854,15 @@ int32_t sparda_kv4_decode_attn(const sparda_shape* s, const sparda_layer_kv4* L,
   const int slots = idx ? kslots(s) : nb_cap(s);
   Kv4AttnArgs a{static_cast<const uint8_t*>(L->kv), static_cast<const __nv_bfloat16*>(q), idx, cnt, seq_len,
                 static_cast<__nv_bfloat16*>(out), part, part + (size_t)kKv4MaxCtas * 2 * kHeads * kHeadDim,
-                reinterpret_cast<unsigned*>(w), nullptr, nullptr, err, s->n_groups, s->heads_per_group, s->max_ctx,
+                reinterpret_cast<unsigned*>(w), nullptr, nullptr, mass, err, s->n_groups, s->heads_per_group, s->max_ctx,
                 nb_cap(s), kslots(s), batch * s->n_groups};
   if (mass) {
     a.stats = reinterpret_cast<float2*>(stats);
     a.ml = reinterpret_cast<float*>(stats + mass_stats_bytes(s, kv4_mass_slots(s)));
   }
   const int parts = launch_kv4_attn(a, st);
-  if (!parts) return SPARDA_ERR_CUDA;
-  if (mass) {
+  if (parts < 0) return SPARDA_ERR_CUDA;
+  if (parts > 0) {
     BlockMassArgs m{a.stats, a.ml, mass, idx, cnt, seq_len, s->n_groups, s->heads_per_group, s->max_ctx, nb_cap(s), slots, parts};
     launch_block_mass(m, batch * s->n_groups, st);
   }
@@ -882,10 +882,12 @@ int32_t sparda_sparse_decode_attn_mass(const sparda_shape* s, const sparda_layer
   uint8_t* stats = static_cast<uint8_t*>(ws) + sparda_workspace_bytes(s, batch, SPARDA_WS_ATTN);
   a.stats = reinterpret_cast<float2*>(stats);
   a.ml = reinterpret_cast<float*>(stats + mass_stats_bytes(s, kslots(s)));
+  a.mass = mass;
   const cudaStream_t st = static_cast<cudaStream_t>(stream);
-  launch_sparse_attn(a, mk, mv, hk, hv, batch * s->n_groups, st);
-  BlockMassArgs m{a.stats, a.ml, mass, idx, cnt, seq_len, s->n_groups, kHeads, s->max_ctx, nb_cap(s), kslots(s), 4};
-  launch_block_mass(m, batch * s->n_groups, st);
+  if (launch_sparse_attn(a, mk, mv, hk, hv, batch * s->n_groups, st)) {
+    BlockMassArgs m{a.stats, a.ml, mass, idx, cnt, seq_len, s->n_groups, kHeads, s->max_ctx, nb_cap(s), kslots(s), 4};
+    launch_block_mass(m, batch * s->n_groups, st);
+  }
   return cuda_status(cudaGetLastError());
 }
 

@@ -51,7 +51,7 @@ int sm_count() {
 }
 
 
-void launch_sparse_attn(const AttnArgs& a, const CUtensorMap& mk, const CUtensorMap& mv,
+bool launch_sparse_attn(const AttnArgs& a, const CUtensorMap& mk, const CUtensorMap& mv,
                         const CUtensorMap& hk, const CUtensorMap& hv, int bg_count,
                         cudaStream_t s) {
   AttnArgs b = a;
@@ -97,6 +97,7 @@ void launch_sparse_attn(const AttnArgs& a, const CUtensorMap& mk, const CUtensor
   cfg.attrs = attr;
   cfg.numAttrs = cluster ? 2 : 1;
   cudaLaunchKernelEx(&cfg, kern, b, mk, mv, hk, hv);
+  return !cluster;
 }
 
 }  // namespace sparda

@@ -210,6 +210,7 @@ __device__ __forceinline__ void attn_cta(const AttnArgs& a, const CUtensorMap* m
       }
     }
     if constexpr (kClusterMerge) cluster_sync();   // the consumers' merge barrier
+    if constexpr (kClusterMerge && kStats) cluster_sync();
     return;
   }
 
@@ -424,10 +425,11 @@ __device__ __forceinline__ void attn_cta(const AttnArgs& a, const CUtensorMap* m
           acc[4] += wt * x1.x; acc[5] += wt * x1.y; acc[6] += wt * x1.z; acc[7] += wt * x1.w;
         }
         if constexpr (kStats) {
-          if ((t & 15) == 0) {
-            a.ml[bg * 2 * kHeads + h] = Mx;
-            a.ml[bg * 2 * kHeads + kHeads + h] = L;
-          }
+          if ((t & 15) == 0)                       // every CTA of the cluster learns the head's maximum and sum
+            for (int q = 0; q < sg; ++q) {
+              st_cluster_f(mM + h, (uint32_t)q, Mx);
+              st_cluster_f(mL + h, (uint32_t)q, L);
+            }
         }
         uint32_t pk[4];
 #pragma unroll
@@ -435,6 +437,17 @@ __device__ __forceinline__ void attn_cta(const AttnArgs& a, const CUtensorMap* m
           pk[e] = pack_bf16(L > 0.f ? acc[2 * e] / L : 0.f, L > 0.f ? acc[2 * e + 1] / L : 0.f);
         *reinterpret_cast<uint4*>(a.out + ((size_t)bg * kHeads + h) * kHeadDim + d0) =
             make_uint4(pk[0], pk[1], pk[2], pk[3]);
+      }
+      if constexpr (kStats) {
+        cluster_sync();                        // (the merge buffers mM, mL were last read before the first one)
+        const float Mh0 = mM[lane & 15], Lh0 = mL[lane & 15];
+        const int nb = a.max_ctx / kBlock;
+        for (int s = s_begin + warp; s < s_stop; s += kConsumerWarps) {
+          const int j = a.idx[(size_t)bg * a.kslots + s];
+          if (j >= 0 && j <= gi.tb)
+            add_block_mass(a.stats + ((size_t)bg * a.kslots + s) * kGroupWarps * kHeads, kGroupWarps, kHeads, Mh0, Lh0,
+                           a.mass + (size_t)bg * nb + j);
+        }
       }
       continue;
     }

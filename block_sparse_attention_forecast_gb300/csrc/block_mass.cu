@@ -4,8 +4,9 @@
 // The attention kernels leave, for every quarter or half (16 or 32 tokens) of an attended block and
 // every head, a reference m and the sum l of exp2(s - m), and for every head the final reference M
 // and sum L over all blocks; the weight of the part is l exp2(m - M) / L. So no score is stored or
-// computed twice: 256 or 512 bytes per block beside the block's 10 to 32 KiB. One warp per attended
-// block; a block's weights are added in a fixed order and once, by one atomic addition (a block
+// computed twice: 256 or 512 bytes per block beside the block's 10 to 32 KiB. Where a (sequence,
+// group) is one thread-block cluster, the attention adds the weights itself (its CTAs tell each other
+// M and L); this kernel serves the other forms. One warp per attended block; a block's weights are added in a fixed order and once, by one atomic addition (a block
 // named twice in idx adds the same number twice, in either order).
 #include "kernels.h"
 
@@ -31,14 +32,8 @@ __global__ void __launch_bounds__(kMassWarps * 32) block_mass_kernel(const Block
   if (j < 0 || j > tb) return;                     // reported by the attention
   const int h = lane & 15;
   const float M = a.ml[bg * 2 * kHeads + h], L = a.ml[bg * 2 * kHeads + kHeads + h];
-  const float2* st = a.stats + ((size_t)bg * a.slots + s) * a.parts * kHeads;
-  const float2 x = st[lane], y = a.parts == 4 ? st[lane + 32] : make_float2(0.f, 0.f);
-  // a part without tokens has l = 0
-  float w = (x.y == 0.f ? 0.f : x.y * fast_exp2(x.x - M)) + (y.y == 0.f ? 0.f : y.y * fast_exp2(y.x - M));
-  w = h < a.H && L != 0.f ? w / L : 0.f;
-#pragma unroll
-  for (int d = 16; d; d >>= 1) w += __shfl_xor_sync(0xffffffffu, w, d);
-  if (lane == 0) atomicAdd(a.mass + (size_t)bg * a.nb_cap + j, w);
+  add_block_mass(a.stats + ((size_t)bg * a.slots + s) * a.parts * kHeads, a.parts, a.H, M, L,
+                 a.mass + (size_t)bg * a.nb_cap + j);
 }
 
 void launch_block_mass(const BlockMassArgs& a, int bg_count, cudaStream_t s) {

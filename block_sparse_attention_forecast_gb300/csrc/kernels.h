@@ -92,6 +92,7 @@ struct AttnArgs {
   // sum [B*G, 2, 16]; nullptr: not wanted
   float2* stats = nullptr;
   float* ml = nullptr;
+  float* mass = nullptr;         // [max_batch, G, max_ctx/64]: added to by the cluster form itself
 };
 
 struct MultiheadArgs {
@@ -141,7 +142,8 @@ void launch_compress_keys(const CompressArgs& a, int bg_count, cudaStream_t s);
 void launch_forecast_project(const ProjectArgs& a, cudaStream_t s);
 void launch_forecast_select(const SelectArgs& a, int bg_count, cudaStream_t s);
 // maps: K and V of the resident cache or of the staging buffer, then hot K and V (offload).
-void launch_sparse_attn(const AttnArgs& a, const CUtensorMap& mk, const CUtensorMap& mv,
+// Returns whether the block mass (where wanted) is still to be added, by launch_block_mass.
+bool launch_sparse_attn(const AttnArgs& a, const CUtensorMap& mk, const CUtensorMap& mv,
                         const CUtensorMap& hk, const CUtensorMap& hv, int bg_count,
                         cudaStream_t s);
 void launch_prefetch(const PrefetchArgs& a, int n_ctas, cudaStream_t s);
@@ -221,10 +223,13 @@ struct Kv4AttnArgs {
   unsigned* counters;            // workspace [max_batch*G], zero between calls
   float2* stats;                 // block mass: (max, sum) [B*G, slots, parts, 16]; nullptr: not wanted
   float* ml;                     // block mass: final max and sum [B*G, 2, 16]
+  float* mass;                   // [max_batch, G, nb_cap]: added to by the cluster form itself
   int* err;
   int G, H, max_ctx, nb_cap, kslots, bg_count;
 };
-int launch_kv4_attn(const Kv4AttnArgs& a, cudaStream_t s);   // the stats' parts per block (2 or 4); 0: not launched
+// The stats' parts per block (2 or 4) where the block mass is still to be added by launch_block_mass,
+// 0 where there is nothing left to do, -1 if nothing was launched.
+int launch_kv4_attn(const Kv4AttnArgs& a, cudaStream_t s);
 
 // Accumulates the attention weight of each attended block (block_mass.cu).
 struct BlockMassArgs {
@@ -237,6 +242,22 @@ struct BlockMassArgs {
   int G, H, max_ctx, nb_cap, slots, parts;   // parts: 2 or 4 per block
 };
 void launch_block_mass(const BlockMassArgs& a, int bg_count, cudaStream_t s);
+
+#ifdef __CUDACC__
+// The weight of one attended block from its statistics, added to *mass by one warp: l exp2(m - M) / L
+// over its parts and heads (M, L: the final maximum and sum of head lane % 16).
+__device__ __forceinline__ void add_block_mass(const float2* st, int parts, int H, float M, float L, float* mass) {
+  const int lane = threadIdx.x & 31;
+  const float2 x = st[lane], y = parts == 4 ? st[lane + 32] : make_float2(0.f, 0.f);
+  float w = 0.f;                                   // a part without tokens has l = 0
+  if (x.y != 0.f) w += x.y * exp2f(x.x - M);
+  if (y.y != 0.f) w += y.y * exp2f(y.x - M);
+  w = (lane & 15) < H && L != 0.f ? w / L : 0.f;
+#pragma unroll
+  for (int d = 16; d; d >>= 1) w += __shfl_xor_sync(0xffffffffu, w, d);
+  if (lane == 0) atomicAdd(mass, w);
+}
+#endif
 
 // Eviction (evict.cu). A cache is one or two planes of fixed bytes per block.
 struct EvictArgs {

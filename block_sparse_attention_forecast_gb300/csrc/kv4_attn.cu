@@ -310,9 +310,10 @@ __global__ void __launch_bounds__(kThreads4, 1) kv4_attn_kernel(const Kv4AttnArg
         }
       }
     }
-    if constexpr (kCluster) {                        // the consumers' two barriers
+    if constexpr (kCluster) {                        // the consumers' barriers
       cluster_wait();
       cluster_sync();
+      if constexpr (kStats) cluster_sync();
     }
     return;
   }
@@ -655,7 +656,13 @@ __global__ void __launch_bounds__(kThreads4, 1) kv4_attn_kernel(const Kv4AttnArg
       }
     }
     if (write) {
-      if constexpr (kStats) {
+      if constexpr (kStats && kCluster) {
+        if ((t & 15) == 0)                     // every CTA of the cluster learns the head's reference and sum
+          for (int q = 0; q < cluster; ++q) {
+            st_cluster_f(mM + h, (uint32_t)q, M);
+            st_cluster_f(mL + h, (uint32_t)q, L);
+          }
+      } else if constexpr (kStats) {
         if ((t & 15) == 0) {
           a.ml[p.bg * 2 * kHeads + h] = M;
           a.ml[p.bg * 2 * kHeads + kHeads + h] = L;
@@ -669,6 +676,18 @@ __global__ void __launch_bounds__(kThreads4, 1) kv4_attn_kernel(const Kv4AttnArg
       }
     }
     first_piece = false;
+    if constexpr (kCluster && kStats) {
+      cluster_sync();                          // (mM and mL were last read before the first one)
+      const float Mh = mM[lane & 15], Lh = mL[lane & 15];
+      const int tb = (a.seq_len[p.bg / a.G] - 1) / kBlock;
+      const int slots = a.idx ? a.kslots : a.nb_cap;
+      for (int s = p.s0 + warp; s < p.s1; s += kCWarps) {
+        const int j = a.idx ? a.idx[(size_t)p.bg * a.kslots + s] : s;
+        if (j >= 0 && j <= tb)
+          add_block_mass(a.stats + ((size_t)p.bg * slots + s) * (8 / kTiles) * kHeads, 8 / kTiles, a.H, Mh, Lh,
+                         a.mass + (size_t)p.bg * a.nb_cap + j);
+      }
+    }
     if constexpr (kCluster) return;
     sync_consumers();                          // the merge buffer is free again
   }
@@ -696,7 +715,7 @@ int launch_form(const Kv4AttnArgs& a, int grid, int cluster, cudaStream_t s) {
            at.numRegs * kThreads4 >= 128 * kProducerRegs + kCThreads * kConsumerRegs;
   }();
   static SmemOptIn opt_in;
-  if (!fits || !opt_in.set(kern, smem)) return 0;
+  if (!fits || !opt_in.set(kern, smem)) return -1;
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3(grid);
   cfg.blockDim = dim3(kThreads4);
@@ -712,7 +731,7 @@ int launch_form(const Kv4AttnArgs& a, int grid, int cluster, cudaStream_t s) {
   cfg.attrs = attr;
   cfg.numAttrs = kCluster ? 2 : 1;
   cudaLaunchKernelEx(&cfg, kern, a, cluster);
-  return kW == 1 ? 2 : 4;
+  return !kStats || kCluster ? 0 : kW == 1 ? 2 : 4;
 }
 
 template <int kW, bool kCluster>

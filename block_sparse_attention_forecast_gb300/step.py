@@ -467,8 +467,8 @@ class DecodeStack:
         last an attend-and-score, the last layer's attention alone. Fused: per layer an
         append, per layer but the last a projection and an attend-and-select, the last
         layer's attention. Streams: per layer append and attention, per layer but the last a
-        projection and a selection, one gather per offloaded layer, one block-mass launch per
-        layer where that is kept."""
+        projection and a selection, one gather per offloaded layer, and at most one block-mass launch per
+        layer where that is kept (counted here)."""
         n = self.n_layers
         if self.mode == "pipelined":
             return 2 + n + (n - 1) + 1

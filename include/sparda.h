@@ -646,7 +646,7 @@ int32_t sparda_kv4_append(const sparda_shape* shape, const sparda_layer_kv4* lay
  * NULL, over all tokens t < seq_len[b]. A block named twice counts twice; an index outside the
  * sequence's blocks sets SPARDA_DEV_BAD_INDEX and is skipped; with nothing to attend (cnt 0, a bad
  * seq_len) the output is zero. mass: NULL, or the block weights to add to (as
- * sparda_sparse_decode_attn_mass); with mass the call is two launches.
+ * sparda_sparse_decode_attn_mass); with mass the call is one or two launches.
  * workspace: SPARDA_WS_KV4_ATTN, with mass SPARDA_WS_KV4_ATTN_MASS.
  */
 int32_t sparda_kv4_decode_attn(const sparda_shape* shape, const sparda_layer_kv4* layer, const void* q,
@@ -665,7 +665,7 @@ int32_t sparda_kv4_decode_attn(const sparda_shape* shape, const sparda_layer_kv4
  * bit for bit) that also adds to mass[b, g, j], for every block j = idx[b, g, s], s < cnt[b,g],
  *   sum over the group's heads h and the block's tokens t < T of softmax_t(q_h . k_t / sqrt(d)).
  * A block named twice in idx is added twice; an index outside the sequence's blocks adds nothing.
- * Two launches; mass is added to in place, in an order that does not change the result. Two calls
+ * One or two launches; mass is added to in place, in an order that does not change the result. Two calls
  * that may run at the same time must not share mass. workspace: SPARDA_WS_ATTN_MASS.
  * SPARDA_ERR_INVALID_ARG for an offloaded layer.
  */
