@@ -230,7 +230,6 @@ struct Kv4AttnArgs {
 // The stats' parts per block (2 or 4) where the block mass is still to be added by launch_block_mass,
 // 0 where there is nothing left to do, -1 if nothing was launched.
 int launch_kv4_attn(const Kv4AttnArgs& a, cudaStream_t s);
-bool launch_kv4_attn_tc(const Kv4AttnArgs& a, int grid, cudaStream_t s);   // many blocks (kv4_attn_tc.cu)
 
 // Accumulates the attention weight of each attended block (block_mass.cu).
 struct BlockMassArgs {

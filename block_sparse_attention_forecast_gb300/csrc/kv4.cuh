@@ -19,7 +19,7 @@
 //
 // One block (64 tokens, keys and values) is kKv4BlockBytes contiguous bytes, one bulk copy:
 //   [0, 4096)      key codes    [token 64][word 16] u32, word w = channels 8w .. 8w+7
-//   [4096, 8192)   value codes  [8-token tile 8] of 512 bytes, below
+//   [4096, 8192)   value codes  [token pair 32 as (step 4, half 2, cq 4)] interleaved, below
 //   [8192, 9216)   key scales   [token 64][group 4] u32: s low, z high
 //   [9216, 10240)  value scales [pair 32][group 4] 2 x u32: s of both tokens, z of both tokens
 // They are laid out as the attention's tensor-core fragments need them, so that a warp's
@@ -27,10 +27,9 @@
 //   * key word w: channel pair p (8w+2p, 8w+2p+1) in nibble p of the low / high half-word, then
 //     the word rotated left by 3, which puts pair 0 where the bf16 pattern wants it; a right
 //     rotation by 4p brings pair p there.
-//   * value pair (tokens t0 = 8 tile + 2 cq and t0 + 1), octet g of 16 channels: four words, word w
-//     with channels 16 g + 4 w + p, in two places: words 0 and 2 at tile * 512 + (4 g + cq) * 8,
-//     words 1 and 3 256 bytes behind them (each is what two of the four warps of a tcgen05 operand
-//     read). A word holds channel p in nibble p, t0 in the low half-word and t0 + 1 in the high one, rotated
+//   * value pair (tokens t0 = 16 step + 8 half + 2 cq and t0 + 1): 16 bytes for each octet g of
+//     16 channels, at ((step * 2 + half) * 32 + 4 g + cq) * 16; word w of it holds channels
+//     16 g + 4 w + p in nibble p, t0 in the low half-word and t0 + 1 in the high one, rotated
 //     left by 2: channels 0 and 1 (and, after a rotation by 8, 2 and 3) can then be taken where they
 //     lie, as 256 + code and as 16 + code; the 240 too many come off in one addition, on the
 //     multiply-add pipe, which has room where the logic pipe has none.
@@ -200,10 +199,10 @@ __device__ __forceinline__ uint32_t nibbles(float c0, float c1, float c2, float 
   return __float_as_uint(fmaf(fmaf(fmaf(c3, 16.f, c2), 16.f, c1), 16.f, c0) + kBase) & 0xffffu;
 }
 
-// Byte offset in a block of word w of the value codes of token pair `pair` (token / 2) and channel
-// octet g (channels 16 g ..): pairs are numbered (tile, cq) = (bits 2.., 1..0).
-__device__ __forceinline__ int value_word(int pair, int g, int w) {
-  return kVCodes + (pair >> 2) * 512 + (w & 1) * 256 + (4 * g + (pair & 3)) * 8 + (w >> 1) * 4;
+// Byte offset in a block of the 16 bytes of value codes of token pair `pair` (token / 2) and
+// channel octet g (channels 16 g ..): pairs are numbered (step, half, cq) = (bits 3.., 2, 1..0).
+__device__ __forceinline__ int value_chunk(int pair, int g) {
+  return kVCodes + ((pair >> 2) * 32 + 4 * g + (pair & 3)) * 16;
 }
 // Byte offset of the (s pair, z pair) of token pair `pair` and channel group `grp`.
 __device__ __forceinline__ int value_scale(int pair, int grp) { return kVScales + (pair * 4 + grp) * 8; }

@@ -23,7 +23,8 @@
 // the reference, and below that off by at most 2^-31 of it each.
 #include <cuda_fp16.h>
 
-#include "kv4_attn.cuh"
+#include "kernels.h"
+#include "kv4.cuh"
 
 namespace sparda {
 using namespace kv4;
@@ -38,6 +39,7 @@ constexpr int kThreads4 = kCThreads + 128;
 constexpr int kLaunchRegs = 168, kProducerRegs = 40, kConsumerRegs = 208;
 static_assert(128 * kProducerRegs + kCThreads * kConsumerRegs <= kThreads4 * kLaunchRegs, "registers the launch holds");
 constexpr int kRing = 16;                                   // at most a warp's lanes
+constexpr int kPlanMax = 1024;                              // (sequence, group)s the balanced plan holds
 constexpr int kRow = 144;                                   // merge-buffer row: 128 + 4 per 32, no bank conflicts
 constexpr int kMergeWarps = kCWarps / 2;                    // the others' results are folded in first
 constexpr int kMergeFloats4 = kMergeWarps * (kHeads * kRow + 2 * kHeads);
@@ -49,11 +51,20 @@ constexpr int kSmem4 = 128 + kHeader4 + kRing * kBlockBytes4 + kQBytes + kMergeF
 constexpr int kMaxCluster4 = 8;
 constexpr int kRecv4 = kHeads + kMaxCluster4 - 1;
 constexpr int kClusterSmem4 = kSmem4 + kRecv4 * (kHeadDim + 2) * 4;
-constexpr int kTensorBlocks = 24;                           // blocks per CTA from which the tensor-memory form is used
 constexpr int kWholeBlocks = 2;                             // blocks per warp from which a warp takes whole ones
 constexpr int kClusterBlocks = 24;                          // blocks per CTA up to which groups get clusters
+constexpr int kMinUnits = 2;                                // blocks per CTA below which fewer CTAs work
+constexpr float kPShift = 6.f;                              // weights are scaled by 2^kPShift
+constexpr float kRise = 8.f;                                // rise of a maximum (base 2) that is let pass
+constexpr uint32_t kProducerPolls = 1u << 25;               // bounds a lane's wait to seconds
+constexpr float kNegInf = -INFINITY;
+// The running maximum before any token: finite, so that no difference of maxima is a NaN.
+constexpr float kLowest = -3.0e38f;
 
 __device__ __forceinline__ void sync_consumers() { asm volatile("bar.sync 1, %0;" ::"n"(kCThreads) : "memory"); }
+__device__ __forceinline__ void arrive(uint64_t* bar) {
+  asm volatile("mbarrier.arrive.shared::cta.b64 _, [%0];" ::"r"(smem_addr(bar)) : "memory");
+}
 // D += A B (m16n8k16, fp16 or bf16 operands). Not volatile: the compiler may interleave products with
 // the unpacking of later operands.
 template <bool kHalf>
@@ -71,6 +82,37 @@ __device__ __forceinline__ void product(float (&d)[4], uint32_t a0, uint32_t a1,
 }
 // Channel c of a merge-buffer row.
 __device__ __forceinline__ int mcol(int c) { return c + 4 * (c >> 5); }
+
+// Blocks of (sequence, group) bg.
+__device__ __forceinline__ int group_blocks(const Kv4AttnArgs& a, int bg, int T) {
+  if (T < 1 || T > a.max_ctx) return 0;
+  const int tb = (T - 1) / kBlock;
+  return a.idx ? min(max(a.cnt[bg], 0), a.kslots) : tb + 1;
+}
+
+// Shared-memory loads by 32-bit address: through pointers into the aligned ring the compiler
+// would make them generic loads.
+__device__ __forceinline__ uint4 lds128(uint32_t p) {
+  uint4 v;
+  asm volatile("ld.shared.v4.u32 {%0, %1, %2, %3}, [%4];" : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "r"(p) : "memory");
+  return v;
+}
+__device__ __forceinline__ uint2 lds64(uint32_t p) {
+  uint2 v;
+  asm volatile("ld.shared.v2.u32 {%0, %1}, [%2];" : "=r"(v.x), "=r"(v.y) : "r"(p) : "memory");
+  return v;
+}
+__device__ __forceinline__ uint32_t lds32(uint32_t p) {
+  uint32_t v;
+  asm volatile("ld.shared.u32 %0, [%1];" : "=r"(v) : "r"(p) : "memory");
+  return v;
+}
+
+// The pieces of the unit range that a CTA owns, one (sequence, group) at a time.
+struct Piece {
+  int bg, s0, s1;       // slots s0 .. s1-1 of group bg
+  int first, n_cta;     // the group's first CTA and how many share it
+};
 
 }  // namespace
 
@@ -116,39 +158,85 @@ __global__ void __launch_bounds__(kThreads4, 1) kv4_attn_kernel(const Kv4AttnArg
   grid_dep_wait();
   grid_dep_launch();
 
-  // The CTA's blocks: in a cluster its share of the one group; else, balanced, a range that may meet
-  // several groups, or whole groups c, c + grid, ...
+  // ------------------------------------------------------------ the plan
   const bool balanced = !kCluster && a.bg_count <= kPlanMax;
-  const int c = blockIdx.x;
-  Plan plan{};
-  int u0 = 0, u1 = 0, n0 = 0, w_bg = c;
+  int U = 0, ctas = gridDim.x, u0 = 0, u1 = 0, n0 = 0;
   if constexpr (kCluster) {
-    w_bg = c / cluster;
-    const int rank = c % cluster, T = a.seq_len[w_bg / a.G];
-    n0 = group_blocks(a, w_bg, T);
+    const int bg = blockIdx.x / cluster, rank = blockIdx.x % cluster;
+    const int T = a.seq_len[bg / a.G];
+    n0 = group_blocks(a, bg, T);
     u0 = n0 * rank / cluster;
     u1 = n0 * (rank + 1) / cluster;
     if ((T < 1 || T > a.max_ctx) && rank == 0 && tid == 0) atomicOr(a.err, SPARDA_DEV_BAD_SEQ_LEN);
     __syncthreads();                               // the barriers are initialised
   } else if (balanced) {
-    plan = make_plan(a, s_pre);
-    if (c >= plan.ctas) return;
-    u0 = plan.u0;
-    u1 = plan.u1;
-    w_bg = u0 < u1 ? plan.group_of(u0) : 0;
+    for (int bg = tid; bg < a.bg_count; bg += kThreads4) {
+      const int T = a.seq_len[bg / a.G];
+      if ((T < 1 || T > a.max_ctx) && blockIdx.x == 0) atomicOr(a.err, SPARDA_DEV_BAD_SEQ_LEN);
+      s_pre[bg + 1] = group_blocks(a, bg, T);
+    }
+    __syncthreads();
+    if (warp == 0) {
+      if (lane == 0) s_pre[0] = 0;
+      int carry = 0;
+      for (int base = 0; base < a.bg_count; base += 32) {
+        int v = base + lane < a.bg_count ? s_pre[base + lane + 1] : 0;
+#pragma unroll
+        for (int d = 1; d < 32; d <<= 1) {
+          const int o = __shfl_up_sync(0xffffffffu, v, d);
+          if (lane >= d) v += o;
+        }
+        v += carry;
+        if (base + lane < a.bg_count) s_pre[base + lane + 1] = v;
+        carry = __shfl_sync(0xffffffffu, v, 31);
+      }
+    }
+    __syncthreads();
+    U = s_pre[a.bg_count];
+    ctas = min((int)gridDim.x, max(1, (U + kMinUnits - 1) / kMinUnits));
+    if ((int)blockIdx.x >= ctas) return;
+    u0 = (int)((long long)U * blockIdx.x / ctas);
+    u1 = (int)((long long)U * (blockIdx.x + 1) / ctas);
   } else {
     __syncthreads();
   }
-  int w_u = u0;
+  const int c = blockIdx.x;
+  const auto cta_of = [&](long long unit) { return (int)(((unit + 1) * ctas - 1) / U); };
+
+  // Walks the CTA's pieces: balanced, the groups its unit range meets; in a cluster, its share of the
+  // one group; else whole groups c, c + grid, ...
+  int w_u = u0, w_bg = 0;
+  if (balanced && u0 < u1) {
+    int lo = 0, hi = a.bg_count - 1;                 // the group with pre[bg] <= u0 < pre[bg + 1]
+    while (lo < hi) {
+      const int mid = (lo + hi) >> 1;
+      if (s_pre[mid + 1] > u0) hi = mid;
+      else lo = mid + 1;
+    }
+    w_bg = lo;
+  } else if (!balanced) {
+    w_bg = kCluster ? c / cluster : c;
+  }
   const auto next_piece = [&](Piece& p) -> bool {
-    if (balanced) return plan.next(p, w_u, w_bg);
+    if (balanced) {
+      if (w_u >= u1) return false;
+      while (s_pre[w_bg + 1] <= w_u) ++w_bg;
+      const int g0 = s_pre[w_bg], g1 = s_pre[w_bg + 1];
+      p.bg = w_bg;
+      p.s0 = w_u - g0;
+      p.s1 = min(u1, g1) - g0;
+      p.first = cta_of(g0);
+      p.n_cta = cta_of(g1 - 1) - p.first + 1;
+      w_u = min(u1, g1);
+      return true;
+    }
     if (w_bg >= a.bg_count) return false;
     p.bg = w_bg;
-    p.first = c;
-    p.n_cta = 1;
     if constexpr (kCluster) {
       p.s0 = u0;
       p.s1 = u1;
+      p.first = c;
+      p.n_cta = 1;
       w_bg = a.bg_count;
       return true;
     }
@@ -156,6 +244,8 @@ __global__ void __launch_bounds__(kThreads4, 1) kv4_attn_kernel(const Kv4AttnArg
     const int T = a.seq_len[w_bg / a.G];
     if ((T < 1 || T > a.max_ctx) && tid == 0) atomicOr(a.err, SPARDA_DEV_BAD_SEQ_LEN);
     p.s1 = group_blocks(a, w_bg, T);
+    p.first = c;
+    p.n_cta = 1;
     w_bg += gridDim.x;
     return true;
   };
@@ -173,8 +263,8 @@ __global__ void __launch_bounds__(kThreads4, 1) kv4_attn_kernel(const Kv4AttnArg
         n = n0;
       } else if (balanced) {
         if (left > 0) {
-          s += u0 - plan.pre[bg];
-          n = plan.pre[bg + 1] - plan.pre[bg];
+          s += u0 - s_pre[bg];
+          n = s_pre[bg + 1] - s_pre[bg];
         }
       } else if (bg < a.bg_count) {
         n = group_blocks(a, bg, a.seq_len[bg / a.G]);
@@ -189,7 +279,7 @@ __global__ void __launch_bounds__(kThreads4, 1) kv4_attn_kernel(const Kv4AttnArg
           s -= n;
           bg += balanced ? 1 : (int)gridDim.x;
           if (!balanced && bg >= a.bg_count) return false;
-          n = balanced ? plan.pre[bg + 1] - plan.pre[bg] : group_blocks(a, bg, a.seq_len[bg / a.G]);
+          n = balanced ? s_pre[bg + 1] - s_pre[bg] : group_blocks(a, bg, a.seq_len[bg / a.G]);
         }
         int j = a.idx ? a.idx[(size_t)bg * a.kslots + s] : s;
         const int T = a.seq_len[bg / a.G];
@@ -232,7 +322,7 @@ __global__ void __launch_bounds__(kThreads4, 1) kv4_attn_kernel(const Kv4AttnArg
   asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kConsumerRegs));
   const int grp = warp / kW, wq = warp % kW;
   const int g = lane >> 2, cq = lane & 3;
-  const float sl2 = kScale2;
+  const float sl2 = 1.4426950408889634f * 0.08838834764831845f;   // log2(e) / sqrt(128)
   int it = 0;
   bool ok = true;             // a wait that ran out: no further compute, the barriers stay matched
   bool first_piece = true;
@@ -279,7 +369,7 @@ __global__ void __launch_bounds__(kThreads4, 1) kv4_attn_kernel(const Kv4AttnArg
         const int live = block_live - 8 * tile0;                 // tokens of the step that exist
         const uint32_t blk = ring_at + stage * kBlockBytes4;
         const uint32_t kc = blk + kKCodes + tile0 * 512 + lane * 16, ks = blk + kKScales + tile0 * 128 + lane * 4;
-        const uint32_t vc = blk + kVCodes + tile0 * 512 + lane * 8;
+        const uint32_t vc = blk + kVCodes + tile0 * 512 + lane * 16;
         const uint32_t vs = blk + kVScales + (tile0 * 4 + cq) * 32 + (g >> 1) * 8;
         // raw scores, heads g and g + 8
         float sc[kTiles][4];
@@ -380,12 +470,11 @@ __global__ void __launch_bounds__(kThreads4, 1) kv4_attn_kernel(const Kv4AttnArg
         // o += weights . values
 #pragma unroll
         for (int r = 0; r < kTiles; r += 2) {
-          const uint2 v0 = lds64(vc + r * 512), v0b = lds64(vc + r * 512 + 256);
-          const uint2 v1 = lds64(vc + r * 512 + 512), v1b = lds64(vc + r * 512 + 768);
+          const uint4 v0 = lds128(vc + r * 512), v1 = lds128(vc + r * 512 + 512);
 #pragma unroll
           for (int n = 0; n < 16; ++n) {
-            const uint32_t wa = n < 4 ? v0.x : n < 8 ? v0b.x : n < 12 ? v0.y : v0b.y;
-            const uint32_t wb = n < 4 ? v1.x : n < 8 ? v1b.x : n < 12 ? v1.y : v1b.y;
+            const uint32_t wa = n < 4 ? v0.x : n < 8 ? v0.y : n < 12 ? v0.z : v0.w;
+            const uint32_t wb = n < 4 ? v1.x : n < 8 ? v1.y : n < 12 ? v1.z : v1.w;
             product<true>(o[n], pa[r][0], pa[r][1], pa[r + 1][0], pa[r + 1][1], value_pair(wa, n & 3, z[r].x, z[r].y, mk),
                           value_pair(wb, n & 3, z[r + 1].x, z[r + 1].y, mk));
           }
@@ -502,7 +591,9 @@ __global__ void __launch_bounds__(kThreads4, 1) kv4_attn_kernel(const Kv4AttnArg
         }
       }
     } else if (p.n_cta > 1) {
-      const int slot = plan.own_place(c, first_piece);
+      // a CTA's partial of its first piece lies in slot 0, of its last in slot 1; a piece that is
+      // neither covers its group alone
+      const int slot = c * 2 + (first_piece ? 0 : 1);
       {
         float4* po = reinterpret_cast<float4*>(a.part_o + ((size_t)slot * kHeads + h) * kHeadDim + d0);
         po[0] = make_float4(acc[0], acc[1], acc[2], acc[3]);
@@ -522,7 +613,10 @@ __global__ void __launch_bounds__(kThreads4, 1) kv4_attn_kernel(const Kv4AttnArg
       sync_consumers();
       write = *s_flag != 0;
       if (write) {
-        // the last CTA of the group to get here joins the partial results
+        // the last CTA of the group joins the partials. The group's first CTA left its partial in
+        // slot 1 unless the group begins that CTA's range; all others in slot 0.
+        const int g0 = s_pre[p.bg];
+        const int first_slot = p.first * 2 + ((int)((long long)U * p.first / ctas) == g0 ? 0 : 1);
         M = kLowest;
         L = 0.f;
 #pragma unroll
@@ -534,7 +628,7 @@ __global__ void __launch_bounds__(kThreads4, 1) kv4_attn_kernel(const Kv4AttnArg
 #pragma unroll
           for (int q = 0; q < kFlight; ++q) {
             const bool in = q0 + q < p.n_cta;
-            const int sl = plan.place_of(p, in ? q0 + q : 0);
+            const int sl = q0 + q == 0 || !in ? first_slot : (p.first + q0 + q) * 2;
             pm[q] = in ? __ldcg(a.part_ml + sl * 2 * kHeads + h) : kLowest;
             pl[q] = __ldcg(a.part_ml + sl * 2 * kHeads + kHeads + h);
             const float4* src = reinterpret_cast<const float4*>(a.part_o + ((size_t)sl * kHeads + h) * kHeadDim + d0);
@@ -597,7 +691,14 @@ __global__ void __launch_bounds__(kThreads4, 1) kv4_attn_kernel(const Kv4AttnArg
     if constexpr (kCluster) return;
     sync_consumers();                          // the merge buffer is free again
   }
-  if (balanced) zero_empty_groups(a, plan, tid, kCThreads);
+  // groups without a block belong to no range: their output is zero
+  if (balanced) {
+    for (int bg = c; bg < a.bg_count; bg += ctas) {
+      if (s_pre[bg + 1] != s_pre[bg]) continue;
+      uint32_t* out = reinterpret_cast<uint32_t*>(a.out + (size_t)bg * a.H * kHeadDim);
+      for (int i = tid; i < a.H * kHeadDim / 2; i += kCThreads) out[i] = 0u;
+    }
+  }
 }
 
 namespace {
@@ -654,9 +755,6 @@ int launch_kv4_attn(const Kv4AttnArgs& a, cudaStream_t s) {
   int grid = sms;
   const long long want = a.bg_count <= kPlanMax ? (bound + kMinUnits - 1) / kMinUnits : a.bg_count;
   if (want < grid) grid = (int)want;
-  // many blocks: the tensor-memory form (it leaves no statistics)
-  if (a.bg_count <= kPlanMax && !a.stats && bound >= (long long)kTensorBlocks * grid)
-    return launch_kv4_attn_tc(a, grid, s) ? 0 : -1;
   // whole blocks per warp once a warp has several
   return bound >= (long long)kWholeBlocks * kCWarps * grid ? launch_form<1, false>(a, grid, 1, s)
                                                            : launch_form<4, false>(a, grid, 1, s);

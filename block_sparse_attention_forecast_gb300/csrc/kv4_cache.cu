@@ -105,9 +105,7 @@ __global__ void __launch_bounds__(kQThreads) kv4_quantize_kernel(const Kv4CacheA
       w[i] = rol(odd ? __byte_perm(take, own0, 0x5410) : __byte_perm(own0, take, 0x5410), 2);
       w[i + 1] = rol(odd ? __byte_perm(take, own1, 0x5432) : __byte_perm(own1, take, 0x7610), 2);
     }
-    const int g16 = 2 * grp + (t & 1);
-    *reinterpret_cast<uint2*>(blk + value_word(t >> 1, g16, 0)) = make_uint2(w[0], w[2]);
-    *reinterpret_cast<uint2*>(blk + value_word(t >> 1, g16, 1)) = make_uint2(w[1], w[3]);
+    *reinterpret_cast<uint4*>(blk + value_chunk(t >> 1, 2 * grp + (t & 1))) = make_uint4(w[0], w[1], w[2], w[3]);
     const uint32_t sz = g.s16 | (g.z16 << 16), so = __shfl_xor_sync(0xffffffffu, sz, 4);
     if (!odd)
       *reinterpret_cast<uint2*>(blk + value_scale(t >> 1, grp)) =
@@ -170,8 +168,7 @@ __global__ void __launch_bounds__(kQThreads) kv4_dequantize_kernel(const Kv4Cach
   for (int r = 0; r < kQRounds / 2; ++r) {         // a token pair of 8 channels per thread
     const int pair = (threadIdx.x >> 4) + r * (kQThreads / 16);
     if (2 * pair >= live) break;
-    const uint2 w = make_uint2(*reinterpret_cast<const uint32_t*>(blk + value_word(pair, l16 >> 1, 2 * (l16 & 1))),
-                               *reinterpret_cast<const uint32_t*>(blk + value_word(pair, l16 >> 1, 2 * (l16 & 1) + 1)));
+    const uint2 w = *reinterpret_cast<const uint2*>(blk + value_chunk(pair, l16 >> 1) + (l16 & 1) * 8);
     const uint2 sz = *reinterpret_cast<const uint2*>(blk + value_scale(pair, l16 >> 2));
     uint32_t lo[4], hi[4];
 #pragma unroll
@@ -236,7 +233,7 @@ __global__ void __launch_bounds__(64 * kAppendPerCta4) kv4_append_kernel(const K
   hw |= __shfl_xor_sync(0xffffffffu, hw, 1);
   const int pair = tok >> 1;
   if ((t & 1) == 0) {
-    uint32_t* word = reinterpret_cast<uint32_t*>(blk + value_word(pair, t >> 3, (t >> 1) & 3));
+    uint32_t* word = reinterpret_cast<uint32_t*>(blk + value_chunk(pair, t >> 3) + ((t >> 1) & 3) * 4);
     *word = rol((tok & 1) ? ((ror(*word, 2) & 0xffffu) | (hw << 16)) : hw, 2);
   }
   if ((t & 15) == 0) {

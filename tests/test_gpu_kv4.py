@@ -432,3 +432,71 @@ def test_bf16_attention_with_mass(sb, T_list, topk):
             got = to64(mass[b, g])
             assert (np.abs(got - want) <= (wtol + 2.0 ** -22) * want).all()
             assert abs(got.sum() - 16) < 1e-3
+
+
+# ------------------------------------------------------------------ many blocks (tensor-memory form)
+@pytest.mark.parametrize("T_list,G,H,ctx", [
+    ([16384, 1, 64, 65, 8191, 4000, 127, 12345], 2, 16, 16384),
+    ([16320] * 5, 3, 3, 16384),
+    ([1 + (53 * b) % 512 for b in range(400)], 2, 8, 512),       # several short groups per CTA
+    ([70000], 4, 11, 70016),
+])
+def test_attention_many_blocks(sb, T_list, G, H, ctx):
+    B = len(T_list)
+    shape = sb.Shape(n_groups=G, heads_per_group=H, max_ctx=ctx, max_batch=B + 1)
+    K, V = _kv(shape, 110 + B)
+    layer = _filled(sb, shape, K, V, T_list)
+    q = synth.normal_bf16((B, G * H, 128), 111, B)
+    q[:, 0] = (q[:, 0].float() * 40).to(torch.bfloat16)          # peaked: the references move
+    q[:, 1] = 0
+    _check_attention(sb, shape, layer, K, V, T_list, q, None, None)
+
+
+def test_attention_many_selected_blocks(sb):
+    """Selections of up to 64 blocks in a large batch; empty ones, bad lengths and indices among them."""
+    B, G, ctx, topk = 70, 1, 4096, 62
+    T_list = [1 + (977 * b) % 4096 for b in range(B)]
+    shape = sb.Shape(n_groups=G, heads_per_group=16, max_ctx=ctx, max_batch=B, topk=topk)
+    K, V = _kv(shape, 121)
+    layer = _filled(sb, shape, K, V, T_list)
+    q = synth.normal_bf16((B, 16, 128), 122)
+    idx, cnt = _select(np.random.default_rng(5), T_list, G, topk)
+    cnt[3] = cnt[40] = 0
+    good = _check_attention(sb, shape, layer, K, V, T_list, q, idx, cnt)
+    bad, lens = idx.clone(), list(T_list)
+    bad[7, 0, 0] = 64
+    bad[8, 0, 0] = -2147483648
+    bad[9, 0, 0] = 2147483647
+    lens[20], lens[21] = 0, 4097
+    out = torch.ones_like(good)
+    sb.sparda_kv4_decode_attn(shape, layer, q.cuda(), bad, cnt, _i32(lens), B, out, sb.workspace(shape, B, sb.WS_KV4_ATTN))
+    torch.cuda.synchronize()
+    assert sb.sparda_device_error(clear=True) == sb.DEV_BAD_INDEX | sb.DEV_BAD_SEQ_LEN
+    assert (out[20:22] == 0).all()
+    same = [b for b in range(B) if b not in (7, 8, 9, 20, 21)]
+    # the ranges per CTA moved with the lengths, and the order of the sums with them
+    assert (out[same].float() - good[same].float()).abs().max() <= 2.0 ** -7 * good.float().abs().max()
+    assert not torch.isnan(out).any()
+
+
+def test_attention_many_blocks_nan_and_repeats(sb):
+    T_list = [9000, 16000, 77, 16384, 333, 5000, 16384, 2]
+    shape = sb.Shape(n_groups=2, heads_per_group=4, max_ctx=16384, max_batch=8)
+    K, V = _kv(shape, 131)
+    K[1, 1, 15990, 3] = float("nan")
+    V[3, 0, 100, 64] = float("inf")
+    layer = _filled(sb, shape, K, V, T_list)
+    q = synth.normal_bf16((8, 8, 128), 132).cuda()
+    ws = sb.workspace(shape, 8, sb.WS_KV4_ATTN)
+    outs = []
+    for _ in range(4):
+        outs.append(torch.zeros((8, 8, 128), dtype=torch.bfloat16, device="cuda"))
+        sb.sparda_kv4_decode_attn(shape, layer, q, None, None, _i32(T_list), 8, outs[-1], ws)
+    torch.cuda.synchronize()
+    assert sb.sparda_device_error(clear=True) == 0
+    for o in outs[1:]:
+        assert torch.equal(o.view(torch.int16), outs[0].view(torch.int16))
+    nan = torch.isnan(outs[0])
+    assert nan[1, 4:].all() and not nan[1, :4].any()
+    assert nan[3, :4, 64:96].all() and not nan[3, :4, :64].any() and not nan[3, 4:].any()
+    assert not nan[[0, 2, 4, 5, 6, 7]].any()
