@@ -52,6 +52,7 @@ constexpr int kMaxCluster4 = 8;
 constexpr int kRecv4 = kHeads + kMaxCluster4 - 1;
 constexpr int kClusterSmem4 = kSmem4 + kRecv4 * (kHeadDim + 2) * 4;
 constexpr int kWholeBlocks = 2;                             // blocks per warp from which a warp takes whole ones
+constexpr int kPairBlocks = 6;                              // blocks per CTA above which pairs of warps share a block
 constexpr int kClusterBlocks = 24;                          // blocks per CTA up to which groups get clusters
 constexpr int kMinUnits = 2;                                // blocks per CTA below which fewer CTAs work
 constexpr float kPShift = 6.f;                              // weights are scaled by 2^kPShift
@@ -119,8 +120,8 @@ struct Piece {
 // kStats: also store every quarter block's softmax statistics (max, sum of each head) and the
 // final ones, for the block mass.
 //
-// kW: warps that share a block. 1: a warp takes whole blocks, 32 tokens at a time; 4: a warp takes 16
-// tokens of each block, for short ranges, where the time to the first result counts.
+// kW: warps that share a block. 1: a warp takes whole blocks, 32 tokens at a time; 2 and 4: a warp takes
+// 32 or 16 tokens of each block, for short ranges, where the time to the first result counts.
 // kCluster: the n_cta CTAs of a (sequence, group) form a thread-block cluster, one piece each, and
 // join their results in distributed shared memory; no plan, no workspace.
 template <int kW, bool kStats, bool kCluster>
@@ -138,7 +139,7 @@ __global__ void __launch_bounds__(kThreads4, 1) kv4_attn_kernel(const Kv4AttnArg
   float* mM = mO + kMergeWarps * kHeads * kRow;
   float* mL = mM + kMergeWarps * kHeads;
   constexpr int kBlockGroups = kCWarps / kW;     // blocks in the consumers' hands at a time
-  constexpr int kTiles = kW == 1 ? 4 : 2;        // 8-token tiles of a step
+  constexpr int kTiles = kW == 4 ? 2 : 4;        // 8-token tiles of a step
   constexpr int kSteps = 8 / kW / kTiles;        // steps of a warp per block
   static_assert(kRing % kBlockGroups == 0, "each ring stage must belong to one group of consumers");
 
@@ -621,7 +622,7 @@ __global__ void __launch_bounds__(kThreads4, 1) kv4_attn_kernel(const Kv4AttnArg
         L = 0.f;
 #pragma unroll
         for (int e = 0; e < 8; ++e) acc[e] = 0.f;
-        constexpr int kFlight = 8;
+        constexpr int kFlight = 4;
         for (int q0 = 0; q0 < p.n_cta; q0 += kFlight) {
           float pm[kFlight], pl[kFlight];
           float4 px[kFlight][2];
@@ -731,7 +732,7 @@ int launch_form(const Kv4AttnArgs& a, int grid, int cluster, cudaStream_t s) {
   cfg.attrs = attr;
   cfg.numAttrs = kCluster ? 2 : 1;
   cudaLaunchKernelEx(&cfg, kern, a, cluster);
-  return !kStats || kCluster ? 0 : kW == 1 ? 2 : 4;
+  return !kStats || kCluster ? 0 : kW == 4 ? 4 : 2;
 }
 
 template <int kW, bool kCluster>
@@ -751,7 +752,9 @@ int launch_kv4_attn(const Kv4AttnArgs& a, cudaStream_t s) {
   if (cluster > kMaxCluster4) cluster = kMaxCluster4;
   const int useful = (slots + kMinUnits - 1) / kMinUnits;
   if (cluster > useful) cluster = useful;
-  if (cluster >= 1 && slots <= kClusterBlocks * cluster) return launch_form<4, true>(a, cluster * a.bg_count, cluster, s);
+  if (cluster >= 1 && slots <= kClusterBlocks * cluster)
+    return slots > kPairBlocks * cluster ? launch_form<2, true>(a, cluster * a.bg_count, cluster, s)
+                                         : launch_form<4, true>(a, cluster * a.bg_count, cluster, s);
   int grid = sms;
   const long long want = a.bg_count <= kPlanMax ? (bound + kMinUnits - 1) / kMinUnits : a.bg_count;
   if (want < grid) grid = (int)want;
