@@ -71,9 +71,58 @@ __device__ __forceinline__ uint16_t fixed_mean_to_bf16(long long S) {
   return (uint16_t)(sign + ((uint32_t)(p + 75) << 7) + (m - 128u));
 }
 
+// The exact sum of 32 bf16 values, as two float32 numbers hi + lo. amax: their largest magnitude,
+// in [2^-64, 2^64). Each value is cut at u = 2^-12 of amax's power of two (adding and taking off 1.5 * 2^23 u
+// rounds to multiples of u): the upper parts are multiples of u below 2^19 u in sum, the lower parts
+// multiples of the smallest value's last bit and below 16 u in sum, so neither sum is ever rounded
+// while no nonzero value is below 2^-24 amax.
+__device__ __forceinline__ float2 exact_sum(const float (&x)[kWinKernel], float amax) {
+  const float u = __uint_as_float((__float_as_uint(amax) & 0x7f800000u) - (12u << 23)), cut = 12582912.f * u;
+  float hi = 0.f, lo = 0.f;
+#pragma unroll
+  for (int i = 0; i < kWinKernel; ++i) {
+    const float h = __fsub_rn(__fadd_rn(x[i], cut), cut);
+    hi += h;
+    lo += __fsub_rn(x[i], h);
+  }
+  return make_float2(hi, lo);
+}
+
 // The mean of 32 bf16 pairs, per half-word, rounded once to bf16: a compression window's
-// compressed key for two channels.
+// compressed key for two channels. A window of ordinary values is summed in float32 (exact_sum), at
+// 8 instructions per value; any other through the fixed-point or the float64 sum of the append.
 __device__ __forceinline__ uint32_t window_mean(const uint32_t (&xs)[kWinKernel]) {
+  uint32_t top = 0u, low = 0xffffffffu;            // per half: largest magnitude, smallest nonzero one less 1
+#pragma unroll
+  for (int u = 0; u < kWinKernel; ++u) {
+    const uint32_t m = xs[u] & 0x7fff7fffu;
+    top = __vmaxu2(top, m);
+    low = __vminu2(low, __vsub2(m, 0x00010001u));
+  }
+  const uint32_t t0 = top & 0xffffu, t1 = top >> 16, l0 = low & 0xffffu, l1 = low >> 16;
+  // bf16 codes of 2^-64 and 2^64; a magnitude 24 powers of two down is a code 24 * 128 down
+  const auto plain = [](uint32_t t, uint32_t l) { return t >= 0x1f80u && t < 0x5f80u && l + 24u * 128u >= t; };
+  if (plain(t0, l0) && plain(t1, l1)) {
+    uint32_t r[2];
+#pragma unroll
+    for (int half = 0; half < 2; ++half) {
+      float x[kWinKernel];
+#pragma unroll
+      for (int u = 0; u < kWinKernel; ++u) x[u] = half ? bf16_hi(xs[u]) : bf16_lo(xs[u]);
+      const float2 s = exact_sum(x, __uint_as_float((half ? t1 : t0) << 16));
+      // hi + lo rounded to odd, then to bf16: one rounding in all
+      const float f = __fadd_rn(s.x, s.y);
+      const float e = __fadd_rn(__fsub_rn(s.x, __fsub_rn(f, __fsub_rn(f, s.x))), __fsub_rn(s.y, __fsub_rn(f, s.x)));
+      uint32_t bits = __float_as_uint(f);
+      if (e != 0.f) {
+        if ((e < 0.f) == (f > 0.f)) --bits;        // towards zero
+        bits |= 1u;
+      }
+      r[half] = __bfloat16_as_ushort(__float2bfloat16_rn(__uint_as_float(bits) * (1.f / kWinKernel)));
+      if (f == 0.f && e == 0.f) r[half] = 0u;
+    }
+    return r[0] | (r[1] << 16);
+  }
   bool in_range = true;
   long long S0 = 0, S1 = 0;
 #pragma unroll

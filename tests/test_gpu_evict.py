@@ -225,3 +225,55 @@ def test_evict_then_compress_agrees(sb):
     graph.replay()                                             # nothing left to evict
     torch.cuda.synchronize()
     assert [int((t - 1) // 64 + 1) for t in seq.tolist()] == [9, 9] and k2[0, 0].tolist() == list(range(9))
+
+
+def _bf16_mean(values):
+    """The mean of 32 bf16 values (floats), exact, rounded once to bf16 (nearest even), as a float."""
+    from fractions import Fraction
+    s = sum((Fraction(float(v)) for v in values), Fraction(0)) / 32
+    if s == 0:
+        return 0.0
+    a, e = abs(s), 0
+    while a >= 2 ** (e + 1):
+        e += 1
+    while a < Fraction(2) ** e:
+        e -= 1
+    unit = Fraction(2) ** (max(e, -126) - 7)
+    n = a / unit
+    k = int(n)
+    if n - k > Fraction(1, 2) or (n - k == Fraction(1, 2) and k & 1):
+        k += 1
+    return float(k * unit) * (1 if s > 0 else -1)
+
+
+@pytest.mark.parametrize("spread", [0, 6, 20, 30, 60])
+def test_joined_windows_are_exact_means(sb, spread):
+    """Keys whose magnitudes spread over 2^+-spread, with zeros, cancellation and halfway sums: every
+    joined window is the exact mean rounded once."""
+    ctx, keep, seed = 1024, 5, 500 + spread
+    shape = sb.Shape(n_groups=1, max_ctx=ctx, max_batch=1)
+    rng = np.random.default_rng(seed)
+    x = rng.standard_normal((ctx, 128)) * 2.0 ** rng.integers(-spread, spread + 1, size=(ctx, 128))
+    x[rng.random((ctx, 128)) < 0.05] = 0
+    x[:, 1] = np.where(np.arange(ctx) % 2, 3.0, -3.0)                 # sums to nothing
+    x[:, 2] = 0.0
+    x[:, 3] = np.where(np.arange(ctx) % 32 == 5, 2.0 ** -3, 1.0 + 2.0 ** -7)  # sums near halfway
+    x[:, 4] = 1.0
+    x[:, 4][::16] = 1.0 + 2.0 ** -3                                   # 32 + 1/4: halfway in bf16 terms of the mean
+    K = torch.from_numpy(x).to(torch.bfloat16)
+    layer = sb.LayerKV.empty(shape)
+    layer.k.copy_(K.cuda()[None, None])
+    layer.v.zero_()
+    mass = torch.zeros((1, 1, 16), device="cuda")
+    mass[0, 0, [3, 6, 9]] = 1
+    kept = torch.zeros((1, 1, keep), dtype=torch.int32, device="cuda")
+    seq = _i32([ctx])
+    sb.sparda_evict_blocks(shape, layer, mass, seq, 1, keep, 1, kept)
+    torch.cuda.synchronize()
+    blocks = [0, 3, 6, 9, 15]
+    assert kept[0, 0].tolist() == blocks
+    Kf = K.double().numpy()
+    for i in range(keep - 1):
+        span = np.concatenate([Kf[64 * blocks[i] + 48:64 * blocks[i] + 64], Kf[64 * blocks[i + 1]:64 * blocks[i + 1] + 16]])
+        want = [_bf16_mean(span[:, c]) for c in range(128)]
+        assert to64(layer.ck[0, 0, 4 * i + 3]).tolist() == want, i
