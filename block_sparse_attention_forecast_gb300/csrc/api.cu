@@ -961,7 +961,7 @@ int32_t sparda_evict_blocks(const sparda_shape* s, const sparda_layer_kv* L, flo
   a.dst[1] = static_cast<uint8_t*>(dst ? dst->v : L->v);
   a.planes = 2;
   a.block_bytes = kBlockBytes;
-  launch_evict(a, static_cast<cudaStream_t>(stream));
+  if (!launch_evict(a, static_cast<cudaStream_t>(stream))) return SPARDA_ERR_CUDA;
   return cuda_status(cudaGetLastError());
 }
 
@@ -984,7 +984,7 @@ int32_t sparda_kv4_evict_blocks(const sparda_shape* s, const sparda_layer_kv4* L
   a.planes = 1;
   a.block_bytes = SPARDA_KV4_BLOCK_BYTES;
   a.kv4 = 1;
-  launch_evict(a, static_cast<cudaStream_t>(stream));
+  if (!launch_evict(a, static_cast<cudaStream_t>(stream))) return SPARDA_ERR_CUDA;
   return cuda_status(cudaGetLastError());
 }
 

@@ -7,7 +7,7 @@
 //                         registers as order-preserving integers; the (keep - forced)-th largest
 //                         is found digit by digit, three histograms at most, whatever the
 //                         weights' spread; of the keys tied there the lowest blocks are taken.
-//   evict_move_kernel     into another cache: one CTA per kept block. Bytes in, bytes out.
+//   evict_move_kernel     into another cache: bytes in, bytes out.
 //   evict_shift_kernel    in the cache itself: block n moves from kept[n] >= n, so a block may be
 //                         overwritten only once it has been read. One thread-block cluster per
 //                         (sequence, group) takes the kept blocks in rounds of a few blocks per CTA:
@@ -29,9 +29,12 @@ namespace sparda {
 namespace {
 
 constexpr int kSelThreads = 512;
+static_assert(kSelThreads / 32 <= 32, "a warp's lanes hold the warps' totals");
 constexpr int kSelPer = kMaxCtx / kBlock / kSelThreads;         // weights per thread: 8
 constexpr int kBins = 2048;
 constexpr int kMoveThreads = 256;
+constexpr int kMoveSmem = 96 * 1024;                            // a CTA's ring: 9 blocks of 10 KiB, 6 of 16 KiB
+constexpr uint32_t kMovePolls = 1u << 25;                       // bounds a lane's wait to seconds
 constexpr int kShiftSmem = 220 * 1024;                          // two rounds of a CTA's blocks
 constexpr int kCkRow = kHeadDim * 2;                            // bytes of a compressed key
 
@@ -89,18 +92,22 @@ __global__ void __launch_bounds__(kSelThreads) evict_select_kernel(const EvictAr
   grid_dep_wait();
   grid_dep_launch();
   const int bg = blockIdx.x, b = bg / a.G, tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
-  const int T = a.src_len[b];
-  const bool valid = valid_len(T, a.src_nb);
-  const int n = valid ? blocks_of(T) : 0, count = min(n, a.keep);
-  if (!valid && tid == 0) atomicOr(a.err, SPARDA_DEV_BAD_SEQ_LEN);
   const float* src = a.src_mass + (size_t)bg * a.src_nb;
   float w[kSelPer];
   uint32_t key[kSelPer];
 #pragma unroll
-  for (int i = 0; i < kSelPer; ++i) {
+  for (int i = 0; i < kSelPer; ++i) {              // beside the length's load, not behind it
     const int j = tid * kSelPer + i;
-    w[i] = j < n ? src[j] : 0.f;
+    w[i] = j < a.src_nb ? src[j] : 0.f;
   }
+  const int T = a.src_len[b];
+  const bool valid = valid_len(T, a.src_nb);
+  const int n = valid ? blocks_of(T) : 0, count = min(n, a.keep);
+  if (!valid && tid == 0) atomicOr(a.err, SPARDA_DEV_BAD_SEQ_LEN);
+  // the sum of the earlier warps' totals
+  const auto earlier = [&](const int (&totals)[kSelThreads / 32]) {
+    return (int)__reduce_add_sync(0xffffffffu, lane < warp ? totals[lane] : 0);
+  };
 #pragma unroll
   for (int i = 0; i < kSelPer; ++i) {
     const int j = tid * kSelPer + i;
@@ -147,8 +154,7 @@ __global__ void __launch_bounds__(kSelThreads) evict_select_kernel(const EvictAr
         }
         if (lane == 31) s_warp[0][warp] = sum;
         __syncthreads();
-        for (int q = 0; q < warp; ++q) sum += s_warp[0][q];
-        int before = sum - mine;
+        int before = sum - mine + earlier(s_warp[0]);
 #pragma unroll
         for (int i = 0; i < kPer; ++i) {
           if (before < share && before + n_bin[i] >= share) {
@@ -177,8 +183,7 @@ __global__ void __launch_bounds__(kSelThreads) evict_select_kernel(const EvictAr
     }
     if (lane == 31) s_warp[1][warp] = scan;
     __syncthreads();
-    int rank = scan - ties;
-    for (int q = 0; q < warp; ++q) rank += s_warp[1][q];
+    int rank = scan - ties + earlier(s_warp[1]);
 #pragma unroll
     for (int i = 0; i < kSelPer; ++i) {
       const int j = tid * kSelPer + i;
@@ -200,8 +205,7 @@ __global__ void __launch_bounds__(kSelThreads) evict_select_kernel(const EvictAr
   }
   if (lane == 31) s_warp[2][warp] = scan;
   __syncthreads();
-  int at = scan - mine;
-  for (int q = 0; q < warp; ++q) at += s_warp[2][q];
+  int at = scan - mine + earlier(s_warp[2]);
   int32_t* kept = a.kept + (size_t)bg * a.keep;
   float* dst = a.dst_mass + (size_t)bg * a.dst_nb;
 #pragma unroll
@@ -217,44 +221,79 @@ __global__ void __launch_bounds__(kSelThreads) evict_select_kernel(const EvictAr
   if (!a.in_place && tid == 0 && bg % a.G == 0) a.dst_len[b] = valid ? kept_len(T, a.keep) : T;
 }
 
-// Grid: (sequence, group) x kept block.
-__global__ void __launch_bounds__(kMoveThreads) evict_move_kernel(const EvictArgs a) {
+// A fixed grid. Warp 0 moves whole blocks by bulk copies through a ring in shared memory: lane l owns a
+// slot of it and every (slots x CTAs)-th block, so a CTA has all its slots' reads in flight whatever its
+// registers. The other warps, 64 threads per kept block, move the compressed keys and form those of
+// windows that join blocks. (One CTA per kept block, its bytes through registers: 22 us instead of 14 for
+// 4096 blocks of a 4-bit cache.)
+__global__ void __launch_bounds__(kMoveThreads + 32) evict_move_kernel(const EvictArgs a, int slots) {
+  extern __shared__ uint8_t smem_move[];
+  __shared__ alignas(8) uint64_t full[32];
+  const int tid = threadIdx.x, lane = tid & 31;
+  const int n_kept = a.B * a.G * a.keep;
+  if (tid < 32) {
+    if (lane < slots) mbar_init(&full[lane], 1);
+    fence_mbar_init();
+    __syncwarp();
+  }
   grid_dep_wait();
   grid_dep_launch();
-  const int bg = blockIdx.x / a.keep, n = blockIdx.x % a.keep, tid = threadIdx.x;
-  const int32_t* kept = a.kept + (size_t)bg * a.keep;
-  const int j = kept[n], nxt = n + 1 < a.keep ? kept[n + 1] : -1;
-  if (j < 0) return;
-  const int T0 = a.src_len[bg / a.G];
-  const int T = kept_len(T0, a.keep), count = min(blocks_of(T0), a.keep);
-  const size_t from = (size_t)bg * a.src_nb + j, to = (size_t)bg * a.dst_nb + n;
-  // all of the block's loads are in flight before the first store
-  const int vecs = a.block_bytes / 16;
-  uint4 r[2][4];
-#pragma unroll
-  for (int p = 0; p < 2; ++p) {
-    const uint4* s = reinterpret_cast<const uint4*>(a.src[p] + from * a.block_bytes);
-#pragma unroll
-    for (int i = 0; i < 4; ++i)
-      if (p < a.planes && tid + i * kMoveThreads < vecs) r[p][i] = __ldcs(s + tid + i * kMoveThreads);
+  if (tid < 32) {
+    if (lane >= slots) return;
+    uint8_t* slot = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_move) + 127) & ~static_cast<uintptr_t>(127)) +
+                    (size_t)lane * a.block_bytes;
+    int item = (int)blockIdx.x * slots + lane;     // (kept block, plane)
+    const int step = (int)gridDim.x * slots, items = n_kept * a.planes;
+    uint8_t* dst = nullptr;
+    // issues the read of the lane's next block, if there is one
+    const auto read_next = [&]() -> bool {
+      for (; item < items; item += step) {
+        const int k = item / a.planes, p = item % a.planes, bg = k / a.keep, n = k % a.keep;
+        const int j = a.kept[k];
+        if (j < 0) continue;
+        dst = a.dst[p] + ((size_t)bg * a.dst_nb + n) * a.block_bytes;
+        mbar_arrive_expect_tx(&full[lane], a.block_bytes);
+        bulk_load(slot, a.src[p] + ((size_t)bg * a.src_nb + j) * a.block_bytes, a.block_bytes, &full[lane]);
+        item += step;
+        return true;
+      }
+      return false;
+    };
+    uint32_t phase = 0, polls = 0;
+    bool reading = read_next();
+    while (reading) {
+      if (mbar_test_wait(&full[lane], phase)) {
+        bulk_store(dst, slot, a.block_bytes);
+        bulk_commit();
+        bulk_wait_read<0>();                       // the slot may be filled again
+        phase ^= 1;
+        polls = 0;
+        reading = read_next();
+      } else if (++polls > kMovePolls) {
+        atomicOr(a.err, SPARDA_DEV_WAIT_TIMEOUT);
+        reading = false;
+      }
+    }
+    bulk_wait_all();
+    return;
   }
-#pragma unroll
-  for (int p = 0; p < 2; ++p) {
-    uint4* d = reinterpret_cast<uint4*>(a.dst[p] + to * a.block_bytes);
-#pragma unroll
-    for (int i = 0; i < 4; ++i)
-      if (p < a.planes && tid + i * kMoveThreads < vecs) d[tid + i * kMoveThreads] = r[p][i];
+  const int t = (tid - 32) % 64;
+  for (int k = (int)blockIdx.x * (kMoveThreads / 64) + (tid - 32) / 64; k < n_kept; k += (int)gridDim.x * (kMoveThreads / 64)) {
+    const int bg = k / a.keep, n = k % a.keep;
+    const int j = a.kept[k], nxt = n + 1 < a.keep ? a.kept[k + 1] : -1;
+    if (j < 0) continue;
+    const int T0 = a.src_len[bg / a.G];
+    const int T = kept_len(T0, a.keep), count = min(blocks_of(T0), a.keep);
+    const size_t from = (size_t)bg * a.src_nb + j;
+    const size_t src_row = (size_t)bg * (4 * a.src_nb - 1) + 4 * j, dst_row = (size_t)bg * (4 * a.dst_nb - 1) + 4 * n;
+    const bool neighbour = nxt == j + 1;
+    if (t < window_bytes(n, count, T, neighbour) / 16)
+      reinterpret_cast<uint4*>(a.dst_ck + dst_row * kHeadDim)[t] = reinterpret_cast<const uint4*>(a.src_ck + src_row * kHeadDim)[t];
+    if (joins(n, count, T, neighbour))
+      reinterpret_cast<uint32_t*>(a.dst_ck + (dst_row + 3) * kHeadDim)[t] =
+          joined_window(a.src[0], a.kv4, from, (size_t)bg * a.src_nb + nxt, t);
   }
-  const size_t src_row = (size_t)bg * (4 * a.src_nb - 1) + 4 * j, dst_row = (size_t)bg * (4 * a.dst_nb - 1) + 4 * n;
-  const bool neighbour = nxt == j + 1;
-  if (tid < window_bytes(n, count, T, neighbour) / 16)
-    reinterpret_cast<uint4*>(a.dst_ck + dst_row * kHeadDim)[tid] =
-        reinterpret_cast<const uint4*>(a.src_ck + src_row * kHeadDim)[tid];
-  if (tid >= 64 && tid < 128 && joins(n, count, T, neighbour))
-    reinterpret_cast<uint32_t*>(a.dst_ck + (dst_row + 3) * kHeadDim)[tid - 64] =
-        joined_window(a.src[0], a.kv4, from, (size_t)bg * a.src_nb + nxt, tid - 64);
 }
-static_assert(kBlockBytes / 16 <= 4 * kMoveThreads, "a plane's block is at most four vectors per thread");
 
 // One cluster of gridDim.x / (B*G) CTAs per (sequence, group), one warp each; lane 0 issues the
 // bulk copies. Shared memory: two rounds of `slots` blocks with their compressed keys.
@@ -359,12 +398,18 @@ __global__ void evict_length_kernel(const EvictArgs a) {
   }
 }
 
-void launch_evict(const EvictArgs& a, cudaStream_t s) {
+bool launch_evict(const EvictArgs& a, cudaStream_t s) {
   const unsigned bg = (unsigned)a.B * a.G;
   launch_pdl(evict_select_kernel, dim3(bg), dim3(kSelThreads), 0, s, a);
   if (!a.in_place) {
-    launch_pdl(evict_move_kernel, dim3(bg * (unsigned)a.keep), dim3(kMoveThreads), 0, s, a);
-    return;
+    // two CTAs per SM
+    const int slots = kMoveSmem / a.block_bytes;
+    static SmemOptIn opt_in;
+    if (!opt_in.set(evict_move_kernel, kMoveSmem + 128)) return false;
+    const long long items = (long long)bg * a.keep * a.planes, ctas = (items + slots - 1) / slots;
+    const int grid = (int)(ctas < 2 * sm_count() ? ctas : 2 * sm_count());
+    launch_pdl(evict_move_kernel, dim3(grid), dim3(kMoveThreads + 32), (size_t)slots * a.block_bytes + 128, s, a, slots);
+    return true;
   }
   // as many CTAs per (sequence, group) as fill the SMs, up to a portable cluster of 8
   int ctas = 1;
@@ -372,7 +417,8 @@ void launch_evict(const EvictArgs& a, cudaStream_t s) {
   const int slot_bytes = a.planes * a.block_bytes + 4 * kCkRow;
   const int slots = kShiftSmem / (2 * slot_bytes);
   const size_t smem = 128 + 2 * (size_t)slots * slot_bytes;
-  cudaFuncSetAttribute(evict_shift_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+  static SmemOptIn opt_in;
+  if (!opt_in.set(evict_shift_kernel, 128 + kShiftSmem)) return false;
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3(bg * ctas);
   cfg.blockDim = dim3(32);
@@ -390,6 +436,7 @@ void launch_evict(const EvictArgs& a, cudaStream_t s) {
   cudaLaunchKernelEx(&cfg, evict_shift_kernel, a, ctas, slots);
   launch_pdl(evict_join_kernel, dim3(bg * (unsigned)((a.keep + 3) / 4)), dim3(kMoveThreads), 0, s, a);
   launch_pdl(evict_length_kernel, dim3(1), dim3(256), 0, s, a);
+  return true;
 }
 
 }  // namespace sparda

@@ -274,7 +274,7 @@ struct EvictArgs {
   int planes, block_bytes, kv4;  // kv4: one plane in the 4-bit layout; else K and V planes of bf16
   int B, G, src_nb, dst_nb, keep, recent, in_place;
 };
-void launch_evict(const EvictArgs& a, cudaStream_t s);
+bool launch_evict(const EvictArgs& a, cudaStream_t s);   // false: a launch could not be prepared
 
 // Device address of the library's device error word on the current device (api.cu).
 int* dev_error_word();
