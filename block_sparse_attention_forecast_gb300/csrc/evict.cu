@@ -224,8 +224,8 @@ __global__ void __launch_bounds__(kSelThreads) evict_select_kernel(const EvictAr
 // A fixed grid. Warp 0 moves whole blocks by bulk copies through a ring in shared memory: lane l owns a
 // slot of it and every (slots x CTAs)-th block, so a CTA has all its slots' reads in flight whatever its
 // registers. The other warps, 64 threads per kept block, move the compressed keys and form those of
-// windows that join blocks. (One CTA per kept block, its bytes through registers: 22 us instead of 14 for
-// 4096 blocks of a 4-bit cache.)
+// windows that join blocks. (One CTA per kept block, its bytes through registers: 21.0 us instead of
+// 19.4 for 4096 blocks of a 4-bit cache, 41.5 instead of 40.1 for 4096 of bf16 keys and values.)
 __global__ void __launch_bounds__(kMoveThreads + 32) evict_move_kernel(const EvictArgs a, int slots) {
   extern __shared__ uint8_t smem_move[];
   __shared__ alignas(8) uint64_t full[32];

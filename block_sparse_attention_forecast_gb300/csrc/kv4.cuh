@@ -109,7 +109,7 @@ __device__ __forceinline__ uint32_t dup_hi(uint32_t u) { return __byte_perm(u, u
 // 2^-64, 1 or 2^64 so that neither s nor 1 / s leaves float32's range.
 struct Grid {
   uint32_t s16, z16;
-  float unit, s, z, r;          // s and z times the unit, and 1 / s
+  float unit, s, z, r;          // s and z times the unit, and 1 / s, approximately
   bool clamp;                   // whether a code may leave 0 .. 15
 };
 
@@ -157,46 +157,72 @@ __device__ __forceinline__ Grid make_grid(float lo, float hi) {
     g.z *= g.unit;
   }
   asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(g.r) : "f"(g.s));
-  // only where the offset's rounding moved the grid past lo or hi; s = 0 (a NaN here) too
-  g.clamp = !(fmaf(lo, g.unit, -g.z) * g.r > 15.6f && fmaf(hi, g.unit, -g.z) * g.r < 31.4f);
+  // only where the offset's rounding moved the grid past lo or hi; s = 0 (a NaN here) and huge s too
+  g.clamp = !(g.unit >= 1.f && fmaf(lo, g.unit, -g.z) * g.r > 15.6f && fmaf(hi, g.unit, -g.z) * g.r < 31.4f);
   return g;
 }
 
-// c[i] = 16 + clamp(rint((x[i] - z) / s - 16), 0, 15) for finite x, as floats. Without the division:
-// c is the nearest whole number to (x - z) / s up to the error of the guess, and e = (x - z) - c s is
-// exact (c s has at most 17 bits, and the difference is no larger than s), so comparing e with s / 2
-// decides at and near the borders, ties to even. (A quotient that is not exactly halfway does not
-// round to halfway either: x - z and the border times s are at least one unit of x - z apart.) The
-// borders are met by one value in 500, so they are looked after once for all the values.
+// Two float32 operations at a time, each rounded once.
+struct Pair {
+  float x, y;
+};
+__device__ __forceinline__ Pair fma2(Pair a, Pair b, Pair c) {
+  Pair d;
+  asm("{\n\t.reg .b64 a, b, c;\n\tmov.b64 a, {%2, %3};\n\tmov.b64 b, {%4, %5};\n\tmov.b64 c, {%6, %7};\n\t"
+      "fma.rn.f32x2 a, a, b, c;\n\tmov.b64 {%0, %1}, a;\n\t}"
+      : "=f"(d.x), "=f"(d.y)
+      : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y), "f"(c.x), "f"(c.y));
+  return d;
+}
+__device__ __forceinline__ Pair add2(Pair a, Pair b) {
+  Pair d;
+  asm("{\n\t.reg .b64 a, b;\n\tmov.b64 a, {%2, %3};\n\tmov.b64 b, {%4, %5};\n\tadd.rn.f32x2 a, a, b;\n\t"
+      "mov.b64 {%0, %1}, a;\n\t}"
+      : "=f"(d.x), "=f"(d.y)
+      : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y));
+  return d;
+}
+
+// Low 16 bits of c[i]: the code of x[i], clamp(rint((x[i] - z) / s - 16), 0, 15), for finite x; the upper
+// bits are constant. Without a division and without a branch on a border between two codes. With
+// d = x - z (one rounding) and n the even number nearest to d / s, or the other one when d / s is
+// nearly odd, e = d - n s is exact: n s has at most 16 bits, d and n s are multiples of d's last bit, and
+// |e| < 2 s. The quotient is n + e / s, and since n is even a tie goes to n: it is n + rint(e r') with
+// r' = (1 - 2^-21) / s up to 2^-22.4 of it. At a tie e r' is below 1/2; past a tie |e| is at least s / 2 plus one
+// last bit of d, more than 2^-20.1 s as d >= 15.5 s, and e r' above 1/2. (Below 15.5 s, or above 31.5 s, the
+// code is clamped.) Both sums with a large constant round to whole numbers, the first to even ones.
 template <int kN>
-__device__ __forceinline__ void codes_of(const float (&x)[kN], const Grid& g, float (&c)[kN]) {
-  constexpr float kWhole = 12582912.f;             // 1.5 * 2^23: adding it rounds to whole numbers
-  const float half = 0.5f * g.s;
-  float e[kN];
-  bool border = false;
+__device__ __forceinline__ void codes_of(const float (&x)[kN], const Grid& g, uint32_t (&c)[kN]) {
+  static_assert(kN % 2 == 0, "pairs of values");
+  constexpr float kEven = 25165824.f;              // 1.5 * 2^24
+  constexpr float kWhole = 12582912.f;             // 1.5 * 2^23
+  constexpr float kBack = -(kEven - kWhole + 16.f);
+  const float r1 = g.r * (1.f - 1.f / 2097152.f);
 #pragma unroll
-  for (int i = 0; i < kN; ++i) {
-    const float d = fmaf(x[i], g.unit, -g.z);
-    c[i] = fmaf(d, g.r, kWhole) - kWhole;
-    e[i] = fmaf(-c[i], g.s, d);
-    border = border || !(fabsf(e[i]) < half);
-  }
-  if (border) {
-#pragma unroll
-    for (int i = 0; i < kN; ++i)
-      if (fabsf(e[i]) > half || (fabsf(e[i]) == half && (__float_as_uint(c[i] + kWhole) & 1u)))
-        c[i] += e[i] > 0.f ? 1.f : -1.f;
+  for (int i = 0; i < kN; i += 2) {
+    const Pair d = fma2({x[i], x[i + 1]}, {g.unit, g.unit}, {-g.z, -g.z});
+    const Pair w = fma2(d, {g.r, g.r}, {kEven, kEven});
+    const Pair n = add2(w, {-kEven, -kEven});
+    const Pair e = fma2(n, {-g.s, -g.s}, d);
+    const Pair q = fma2(e, {r1, r1}, add2(w, {kBack, kBack}));
+    c[i] = __float_as_uint(q.x);
+    c[i + 1] = __float_as_uint(q.y);
   }
   if (g.clamp) {
 #pragma unroll
-    for (int i = 0; i < kN; ++i) c[i] = fminf(fmaxf(c[i], 16.f), 31.f);
+    for (int i = 0; i < kN; ++i)
+      c[i] = __float_as_uint(fminf(fmaxf(__uint_as_float(c[i]), kWhole), kWhole + 15.f));
+    if (g.unit < 1.f) {                            // x - z may be infinite: the last code
+#pragma unroll
+      for (int i = 0; i < kN; ++i)
+        if (__fsub_rn(x[i], g.z / g.unit) == INFINITY) c[i] = __float_as_uint(kWhole + 15.f);
+    }
   }
 }
 
-// Four results of codes_of as four nibbles, the first lowest.
-__device__ __forceinline__ uint32_t nibbles(float c0, float c1, float c2, float c3) {
-  constexpr float kBase = 8388608.f - 16.f * 0x1111;
-  return __float_as_uint(fmaf(fmaf(fmaf(c3, 16.f, c2), 16.f, c1), 16.f, c0) + kBase) & 0xffffu;
+// Four results of codes_of as four nibbles in the low half, the first lowest; the high half is anything.
+__device__ __forceinline__ uint32_t nibbles(uint32_t c0, uint32_t c1, uint32_t c2, uint32_t c3) {
+  return (c0 + (c1 << 4)) + ((c2 + (c3 << 4)) << 8);
 }
 
 // Byte offset in a block of the 16 bytes of value codes of token pair `pair` (token / 2) and

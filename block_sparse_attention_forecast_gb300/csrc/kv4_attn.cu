@@ -2,23 +2,31 @@
 // query heads of each (sequence, group), over the tokens of the selected blocks or of all blocks.
 //
 // What bounds it: a token is 160 bytes of cache for 4 * 16 * 128 multiply-adds and 256 codes to
-// expand, so at the memory's rate one SM has about 7 cycles per token. The expansion (1.4
-// instructions per code, kv4.cuh) and the tensor instructions (two m16n8k16 per token) both have
-// to fit under that. The heads are the M dimension of warp-level MMAs: the cache is the B operand,
-// expanded in registers straight into B fragments. A tcgen05 form would have to write the
-// expanded 512 bytes per token to shared or tensor memory first, as much traffic again as the
-// tensor cores then read.
+// expand. The heads are the M dimension of warp-level MMAs (m16n8k16), and the cache is the B operand,
+// expanded in registers straight into B fragments (1.4 instructions per code, kv4.cuh). Per 16 tokens
+// a warp issues 293 instructions, 32 of them products. A product occupies the tensor pipe for 8.2
+// cycles and its operands' expansion the issue port for 8.7, but the two only half overlap (13.5
+// cycles together), so the instructions bound a long cache, not the memory: batch 16 of 131072 tokens
+// (671 MB) takes 147 us, and 137 us when every copy hits the same block in L2. A tcgen05 form, whose
+// expanded operands go through tensor memory, took 240 us.
 //
-// Work: the blocks of all (sequence, group)s in a row, U of them, are cut into one contiguous
-// range per CTA, balanced to one block, whatever the lengths; every CTA finds its range itself
-// from seq_len or cnt (a prefix sum over the groups), since the lengths live on the device. One
-// producer thread brings whole blocks (10 KiB, one bulk copy each) into a shared-memory ring; the
-// consumer warps form groups of four that take blocks in turn, a warp 16 tokens of each.
+// Work, three forms chosen by launch_kv4_attn:
+//   - few blocks per (sequence, group): one thread-block cluster each, the blocks split evenly over
+//     its CTAs, results joined in distributed shared memory; no plan, no workspace;
+//   - else the blocks of all (sequence, group)s in a row, U of them, cut into one contiguous range
+//     per CTA, balanced to one block whatever the lengths. Every CTA finds its range itself from seq_len
+//     or cnt (a prefix sum over the groups), since the lengths live on the device. A group's CTAs
+//     leave partial results in a workspace, and the last to arrive joins them;
+//   - with more (sequence, group)s than the prefix sums hold, whole groups per CTA, in turn.
+// Whole blocks (10 KiB, one bulk copy each) go through a ring of 16 stages in shared memory: lane l of the
+// producer warp fills stage l whenever it is free, so all stages are polled at once and no free one
+// waits for another. The consumer warps take blocks in turn, kW warps per block.
 //
 // Numbers: S in float32 from exact products (keys and queries are bf16); softmax in float32, base
 // 2; sums in float32. A weight is a power of two of its score's distance to a reference, which
 // follows the running maximum of its head only when that has risen by more than 2^8: with 16 heads
-// some maximum rises in most steps of 16 tokens, and the rescaling (64 multiplications) with it. The
+// some maximum rises in most steps of 16 tokens, and the rescaling (64 multiplications) with it
+// (batch 16 of 131072 tokens: 192 us with a rescaling at every rise, 186 us at that stage without). The
 // weights are operands in fp16, scaled by 2^6: at most 2^14, at full precision (2^-11) down to 2^-20 of
 // the reference, and below that off by at most 2^-31 of it each.
 #include <cuda_fp16.h>
@@ -34,12 +42,13 @@ namespace {
 constexpr int kCWarps = 8;
 constexpr int kCThreads = kCWarps * 32;
 // The producer has a warpgroup to itself, of which one warp works: registers are moved from it to the
-// consumers, which would otherwise be held to 168 each and spill.
+// consumers, which would otherwise be held to 168 each and spill (162 us instead of 147 for batch 16 of
+// 131072 tokens; twelve consumer warps of fewer registers also 162).
 constexpr int kThreads4 = kCThreads + 128;
 constexpr int kLaunchRegs = 168, kProducerRegs = 40, kConsumerRegs = 208;
 static_assert(128 * kProducerRegs + kCThreads * kConsumerRegs <= kThreads4 * kLaunchRegs, "registers the launch holds");
 constexpr int kRing = 16;                                   // at most a warp's lanes
-constexpr int kPlanMax = 1024;                              // (sequence, group)s the balanced plan holds
+constexpr int kPlanMax = 1024;
 constexpr int kRow = 144;                                   // merge-buffer row: 128 + 4 per 32, no bank conflicts
 constexpr int kMergeWarps = kCWarps / 2;                    // the others' results are folded in first
 constexpr int kMergeFloats4 = kMergeWarps * (kHeads * kRow + 2 * kHeads);
@@ -51,10 +60,22 @@ constexpr int kSmem4 = 128 + kHeader4 + kRing * kBlockBytes4 + kQBytes + kMergeF
 constexpr int kMaxCluster4 = 8;
 constexpr int kRecv4 = kHeads + kMaxCluster4 - 1;
 constexpr int kClusterSmem4 = kSmem4 + kRecv4 * (kHeadDim + 2) * 4;
-constexpr int kWholeBlocks = 2;                             // blocks per warp from which a warp takes whole ones
-constexpr int kPairBlocks = 6;                              // blocks per CTA above which pairs of warps share a block
-constexpr int kClusterBlocks = 24;                          // blocks per CTA up to which groups get clusters
-constexpr int kMinUnits = 2;                                // blocks per CTA below which fewer CTAs work
+// The rules' limits, with both sides measured (kW = warps that share a block):
+//   kWholeBlocks    blocks per warp from which a warp takes whole ones. Batch 16 of 131072 tokens (215
+//                   blocks per CTA): kW 1 147 us, 2 150, 4 174. A ragged batch of 64 with 3 to 24576
+//                   tokens (21 per CTA): 27.5, 27.4, 28.7.
+//   kPairBlocks     blocks per CTA of a cluster above which two warps share a block, not four. 34 blocks in
+//                   clusters of 4 (8.5 per CTA): kW 2 8.4 us, 4 8.75; clusters of 8 (4 per CTA): 7.04, 6.95.
+//   kClusterBlocks  blocks per CTA up to which groups get clusters. Against the planned form, 34 blocks of one
+//                   sequence: 6.8 us instead of 12.5; of 16 sequences: 8.4 instead of 14.8.
+//   kMinUnits       blocks per CTA below which fewer CTAs work; 1, 2 and 4 measured alike, and 2 halves
+//                   the CTAs that a small call occupies.
+//   kPlanMax        (sequence, group)s of the balanced plan, held in 4 KiB of shared memory; beyond it there
+//                   are at least six per SM, and whole groups balance well enough.
+constexpr int kWholeBlocks = 2;
+constexpr int kPairBlocks = 6;
+constexpr int kClusterBlocks = 24;
+constexpr int kMinUnits = 2;
 constexpr float kPShift = 6.f;                              // weights are scaled by 2^kPShift
 constexpr float kRise = 8.f;                                // rise of a maximum (base 2) that is let pass
 constexpr uint32_t kProducerPolls = 1u << 25;               // bounds a lane's wait to seconds

@@ -39,8 +39,8 @@ __device__ __forceinline__ Grid group_grid(const uint32_t (&x)[16 / kLanes]) {
   for (int d = 1; d < kLanes; d <<= 1) v = min_bf2(v, __shfl_xor_sync(0xffffffffu, v, d));
   return make_grid<kKey>(bf16_lo(v), -bf16_hi(v));
 }
-// The codes, plus 16, of four pairs of values.
-__device__ __forceinline__ void codes8(uint32_t x0, uint32_t x1, uint32_t x2, uint32_t x3, const Grid& g, float (&c)[8]) {
+// The codes of four pairs of values, as codes_of leaves them.
+__device__ __forceinline__ void codes8(uint32_t x0, uint32_t x1, uint32_t x2, uint32_t x3, const Grid& g, uint32_t (&c)[8]) {
   const float f[8] = {bf16_lo(x0), bf16_hi(x0), bf16_lo(x1), bf16_hi(x1), bf16_lo(x2), bf16_hi(x2), bf16_lo(x3), bf16_hi(x3)};
   codes_of(f, g, c);
 }
@@ -77,9 +77,9 @@ __global__ void __launch_bounds__(kQThreads) kv4_quantize_kernel(const Kv4CacheA
     uint32_t w[4];
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
-      float c[8];
+      uint32_t c[8];
       codes8(xk[4 * i], xk[4 * i + 1], xk[4 * i + 2], xk[4 * i + 3], g, c);
-      w[i] = rol(nibbles(c[0], c[2], c[4], c[6]) | nibbles(c[1], c[3], c[5], c[7]) << 16, 3);
+      w[i] = rol(__byte_perm(nibbles(c[0], c[2], c[4], c[6]), nibbles(c[1], c[3], c[5], c[7]), 0x5410), 3);
     }
     *reinterpret_cast<uint4*>(blk + kKCodes + threadIdx.x * 16) = make_uint4(w[0], w[1], w[2], w[3]);
     *reinterpret_cast<uint32_t*>(blk + kKScales + threadIdx.x * 4) = g.s16 | (g.z16 << 16);
@@ -89,7 +89,7 @@ __global__ void __launch_bounds__(kQThreads) kv4_quantize_kernel(const Kv4CacheA
     uint32_t h[8];                                 // four channels each, in the low half
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
-      float c[8];
+      uint32_t c[8];
       codes8(xv[4 * i], xv[4 * i + 1], xv[4 * i + 2], xv[4 * i + 3], g, c);
       h[2 * i] = nibbles(c[0], c[1], c[2], c[3]);
       h[2 * i + 1] = nibbles(c[4], c[5], c[6], c[7]);
@@ -99,7 +99,7 @@ __global__ void __launch_bounds__(kQThreads) kv4_quantize_kernel(const Kv4CacheA
     uint32_t w[4];
 #pragma unroll
     for (int i = 0; i < 4; i += 2) {
-      const uint32_t give = odd ? h[i] | h[i + 1] << 16 : h[4 + i] | h[5 + i] << 16;
+      const uint32_t give = __byte_perm(odd ? h[i] : h[4 + i], odd ? h[i + 1] : h[5 + i], 0x5410);
       const uint32_t take = __shfl_xor_sync(0xffffffffu, give, 4);
       const uint32_t own0 = odd ? h[4 + i] : h[i], own1 = odd ? h[5 + i] : h[i + 1];
       w[i] = rol(odd ? __byte_perm(take, own0, 0x5410) : __byte_perm(own0, take, 0x5410), 2);
@@ -217,11 +217,11 @@ __global__ void __launch_bounds__(64 * kAppendPerCta4) kv4_append_kernel(const K
   const uint32_t kn = reinterpret_cast<const uint32_t*>(a.k + (size_t)bg * kHeadDim)[t];
   const uint32_t vn = reinterpret_cast<const uint32_t*>(a.v + (size_t)bg * kHeadDim)[t];
   const Grid gk = group_grid<true, 16>({kn}), gv = group_grid<false, 16>({vn});
-  float ck[2], cv[2];
+  uint32_t ck[2], cv[2];
   codes_of({bf16_lo(kn), bf16_hi(kn)}, gk, ck);
   codes_of({bf16_lo(vn), bf16_hi(vn)}, gv, cv);
   // key: four threads make a word
-  uint32_t w = (((uint32_t)ck[0] - 16u) | (((uint32_t)ck[1] - 16u) << 16)) << (4 * (t & 3));
+  uint32_t w = ((ck[0] & 15u) | ((ck[1] & 15u) << 16)) << (4 * (t & 3));
   w |= __shfl_xor_sync(0xffffffffu, w, 1);
   w |= __shfl_xor_sync(0xffffffffu, w, 2);
   w = rol(w, 3);
@@ -229,7 +229,7 @@ __global__ void __launch_bounds__(64 * kAppendPerCta4) kv4_append_kernel(const K
   if ((t & 15) == 0) *reinterpret_cast<uint32_t*>(blk + kKScales + tok * 16 + (t >> 4) * 4) = gk.s16 | (gk.z16 << 16);
   // value: two threads make the half-word of four channels; the other half belongs to the pair's
   // other token and is kept
-  uint32_t hw = (((uint32_t)cv[0] - 16u) | (((uint32_t)cv[1] - 16u) << 4)) << (8 * (t & 1));
+  uint32_t hw = ((cv[0] & 15u) | ((cv[1] & 15u) << 4)) << (8 * (t & 1));
   hw |= __shfl_xor_sync(0xffffffffu, hw, 1);
   const int pair = tok >> 1;
   if ((t & 1) == 0) {

@@ -86,6 +86,36 @@ def test_prompt_values_exact(sb, T_list, G, ctx):
         assert (np.abs(x - y) <= bound).all()
 
 
+def test_prompt_codes_at_borders(sb):
+    """Codes halfway between two levels or beside it, over all scales: exact at every one."""
+    T, G = 8192, 4
+    shape = sb.Shape(n_groups=G, max_ctx=T, max_batch=1)
+    gen = torch.Generator().manual_seed(17)
+    groups = (1, G, T, 4)                                  # 32 channels each
+
+    def draw(lo, hi):
+        return lo + (hi - lo) * torch.rand(groups + (1,), generator=gen, dtype=torch.float64)
+
+    def rows(kind, lo, hi):
+        """kind: 0 halves of a step (ties), 1 whole numbers of any range, 2 normal with an offset, 3 halves
+        of a step with a few last bits; scaled by 2^lo .. 2^hi."""
+        noise = torch.randn(groups + (32,), generator=gen, dtype=torch.float64)
+        whole = torch.randint(0, 31, groups + (32,), generator=gen).double() / 2
+        whole[..., 0], whole[..., 1] = 0, 15                # the step is 1, and every half is a tie
+        wide = torch.floor(whole * draw(0.2, 12))
+        shift = torch.floor(draw(-24, 24))
+        x = torch.stack([whole + shift, wide + shift, noise + shift * draw(0, 4), whole * (1 + noise * 2.0 ** -7) + shift])[kind]
+        return (x * 2.0 ** torch.floor(draw(lo, hi))).reshape(1, G, T, 128).to(torch.bfloat16)
+
+    for kind in range(4):
+        for lo, hi in ((-3, 3), (-40, 40), (-135, 127)):
+            K, V = rows(kind, lo, hi), rows(kind, max(lo, -28), min(hi, 12))
+            layer = _filled(sb, shape, K, V, [T])
+            k, v = _read(sb, shape, layer, [T])
+            assert np.array_equal(to64(k), to64(_bf(R.grid_values(K, True))), equal_nan=True), (kind, lo, hi)
+            assert np.array_equal(to64(v), to64(_bf(_v16(V))), equal_nan=True), (kind, lo, hi)
+
+
 def test_prompt_special_groups(sb):
     shape = sb.Shape(n_groups=1, max_ctx=64, max_batch=1)
     K, V = _kv(shape, 12)
