@@ -1,7 +1,7 @@
 // Writing and reading back the 4-bit KV cache (layout and grid: kv4.cuh): a prompt's keys and
 // values at once, one decode token, and blocks back to bf16. All three move bytes: a prompt token
-// is 512 bytes read and 160 written per KV group, its arithmetic (one exact division per value)
-// hides behind that.
+// is 512 bytes read and 160 written per KV group, or the reverse. Storing a prompt, some 9 instructions
+// per value, hides behind that; read back, a value is one and a half.
 #include "append_body.cuh"
 #include "kernels.h"
 #include "kv4.cuh"
@@ -45,12 +45,28 @@ __device__ __forceinline__ void codes8(uint32_t x0, uint32_t x1, uint32_t x2, ui
   codes_of(f, g, c);
 }
 
+// 16 bytes into shared memory, zeros beyond the first `bytes` of them.
+__device__ __forceinline__ void copy16(uint4* dst, const uint4* src, uint32_t bytes) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(smem_addr(dst)), "l"(src), "r"(bytes) : "memory");
+}
+__device__ __forceinline__ void copy_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+template <int kLeft>
+__device__ __forceinline__ void copy_wait() {
+  asm volatile("cp.async.wait_group %0;" ::"n"(kLeft) : "memory");
+}
+// Where 16-byte chunk q of a warp's 8 rows lies: neither its 32 lanes' consecutive chunks nor every fourth
+// one meet in a bank.
+__device__ __forceinline__ int swizzled(int q) { return q ^ ((q >> 3) & 3); }
+
 // One CTA per (sequence-group, block), one thread per (token, group of 32 channels) of the keys and of
-// the values: a group's extremes and grid are found once, by the thread that needs them. Its 64 bytes
-// are four loads that the lanes' lines share. The block is put together in shared memory and leaves
-// as one bulk copy.
-__global__ void __launch_bounds__(kQThreads) kv4_quantize_kernel(const Kv4CacheArgs a) {
-  __shared__ alignas(128) uint8_t blk[kBlockBytes4];
+// the values: a group's extremes and grid are found once, by the thread that needs them. A warp
+// fetches its own 8 tokens, whole lines at a time, through shared memory: loaded straight into registers, a
+// group's 64 bytes are four loads that share lines with the neighbours', and the cache they share them in
+// is too small for the CTAs in flight (a round trip that moves 1.0 GB takes 184 us that way with four CTAs per
+// SM and 213 with five, 179.5 like this). The layout of a block puts every warp's codes side by side, so they
+// are stored from registers, without a barrier.
+__global__ void __launch_bounds__(kQThreads, 5) kv4_quantize_kernel(const Kv4CacheArgs a) {
+  __shared__ uint4 rows[kQThreads / 32 * 256];
   grid_dep_wait();
   grid_dep_launch();
   const int j = blockIdx.x % a.nb_cap, bg = blockIdx.x / a.nb_cap, b = bg / a.G;
@@ -60,37 +76,57 @@ __global__ void __launch_bounds__(kQThreads) kv4_quantize_kernel(const Kv4CacheA
     return;
   }
   if (j * kBlock >= T) return;
-  const int t = threadIdx.x >> 2, grp = threadIdx.x & 3;
-  const size_t row = (size_t)bg * a.max_ctx + (size_t)j * kBlock + t;
-  const bool live = j * kBlock + t < T;            // rows past the prompt are stored as zeros
-  uint32_t xk[16], xv[16];
+  uint8_t* blk = a.kv + ((size_t)bg * a.nb_cap + j) * kBlockBytes4;
+  // the warp's 8 tokens of the keys, then of the values
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const size_t row = (size_t)bg * a.max_ctx + (size_t)j * kBlock + warp * 8;
+  uint4* mine = rows + warp * 256;
 #pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    const uint4 none = make_uint4(0, 0, 0, 0);
-    const uint4 k = live ? __ldcs(reinterpret_cast<const uint4*>(a.k) + row * 16 + grp * 4 + i) : none;
-    const uint4 v = live ? __ldcs(reinterpret_cast<const uint4*>(a.v) + row * 16 + grp * 4 + i) : none;
-    xk[4 * i] = k.x, xk[4 * i + 1] = k.y, xk[4 * i + 2] = k.z, xk[4 * i + 3] = k.w;
-    xv[4 * i] = v.x, xv[4 * i + 1] = v.y, xv[4 * i + 2] = v.z, xv[4 * i + 3] = v.w;
+  for (int m = 0; m < 2; ++m) {
+    const uint4* src = reinterpret_cast<const uint4*>(m ? a.v : a.k) + row * 16;
+#pragma unroll
+    for (int r = 0; r < 4; ++r) {
+      const int q = r * 32 + lane;
+      // rows past the prompt are stored as zeros
+      const uint32_t bytes = j * kBlock + warp * 8 + (q >> 4) < T ? 16u : 0u;
+      copy16(mine + m * 128 + swizzled(q), bytes ? src + q : src, bytes);
+    }
+    copy_commit();
   }
+  const int t = threadIdx.x >> 2, grp = threadIdx.x & 3;
+  uint32_t x[16];
+  const auto take_group = [&](int m) {
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const uint4 y = mine[m * 128 + swizzled(lane * 4 + i)];
+      x[4 * i] = y.x, x[4 * i + 1] = y.y, x[4 * i + 2] = y.z, x[4 * i + 3] = y.w;
+    }
+  };
+  copy_wait<1>();
+  __syncwarp();
+  take_group(0);
   {
-    const Grid g = group_grid<true, 1>(xk);
+    const Grid g = group_grid<true, 1>(x);
     uint32_t w[4];
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
       uint32_t c[8];
-      codes8(xk[4 * i], xk[4 * i + 1], xk[4 * i + 2], xk[4 * i + 3], g, c);
+      codes8(x[4 * i], x[4 * i + 1], x[4 * i + 2], x[4 * i + 3], g, c);
       w[i] = rol(__byte_perm(nibbles(c[0], c[2], c[4], c[6]), nibbles(c[1], c[3], c[5], c[7]), 0x5410), 3);
     }
     *reinterpret_cast<uint4*>(blk + kKCodes + threadIdx.x * 16) = make_uint4(w[0], w[1], w[2], w[3]);
     *reinterpret_cast<uint32_t*>(blk + kKScales + threadIdx.x * 4) = g.s16 | (g.z16 << 16);
   }
+  copy_wait<0>();
+  __syncwarp();
+  take_group(1);
   {
-    const Grid g = group_grid<false, 1>(xv);
+    const Grid g = group_grid<false, 1>(x);
     uint32_t h[8];                                 // four channels each, in the low half
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
       uint32_t c[8];
-      codes8(xv[4 * i], xv[4 * i + 1], xv[4 * i + 2], xv[4 * i + 3], g, c);
+      codes8(x[4 * i], x[4 * i + 1], x[4 * i + 2], x[4 * i + 3], g, c);
       h[2 * i] = nibbles(c[0], c[1], c[2], c[3]);
       h[2 * i + 1] = nibbles(c[4], c[5], c[6], c[7]);
     }
@@ -110,14 +146,6 @@ __global__ void __launch_bounds__(kQThreads) kv4_quantize_kernel(const Kv4CacheA
     if (!odd)
       *reinterpret_cast<uint2*>(blk + value_scale(t >> 1, grp)) =
           make_uint2(__byte_perm(sz, so, 0x5410), __byte_perm(sz, so, 0x7632));
-  }
-  fence_proxy_async_shared();
-  __syncthreads();
-  if (threadIdx.x == 0) {
-    uint8_t* dst = a.kv + ((size_t)bg * a.nb_cap + j) * kBlockBytes4;
-    bulk_store(dst, blk, kBlockBytes4);
-    bulk_commit();
-    bulk_wait_all();
   }
 }
 
