@@ -102,6 +102,19 @@ __device__ __forceinline__ void product(float (&d)[4], uint32_t a0, uint32_t a1,
         : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
   }
 }
+// x of all the lanes that hold the same heads: the four of a quad, or with kEight one of each quad.
+template <bool kEight, typename Op>
+__device__ __forceinline__ float over_lanes(float x, Op op) {
+#pragma unroll
+  for (int d = kEight ? 4 : 1; d <= (kEight ? 16 : 2); d <<= 1) x = op(x, __shfl_xor_sync(0xffffffffu, x, d));
+  return x;
+}
+// An 8 x 8 matrix of 16-bit values, two per lane, transposed.
+__device__ __forceinline__ uint32_t transposed(uint32_t x) {
+  uint32_t y;
+  asm volatile("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(y) : "r"(x));
+  return y;
+}
 // Channel c of a merge-buffer row.
 __device__ __forceinline__ int mcol(int c) { return c + 4 * (c >> 5); }
 
@@ -145,7 +158,8 @@ struct Piece {
 // 32 or 16 tokens of each block, for short ranges, where the time to the first result counts.
 // kCluster: the n_cta CTAs of a (sequence, group) form a thread-block cluster, one piece each, and
 // join their results in distributed shared memory; no plan, no workspace.
-template <int kW, bool kStats, bool kCluster>
+// kEight: at most 8 heads.
+template <int kW, bool kStats, bool kCluster, bool kEight>
 __global__ void __launch_bounds__(kThreads4, 1) kv4_attn_kernel(const Kv4AttnArgs a, int cluster) {
   extern __shared__ uint8_t smem_raw4[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw4) + 127) & ~static_cast<uintptr_t>(127));
@@ -162,6 +176,7 @@ __global__ void __launch_bounds__(kThreads4, 1) kv4_attn_kernel(const Kv4AttnArg
   constexpr int kBlockGroups = kCWarps / kW;     // blocks in the consumers' hands at a time
   constexpr int kTiles = kW == 4 ? 2 : 4;        // 8-token tiles of a step
   constexpr int kSteps = 8 / kW / kTiles;        // steps of a warp per block
+  constexpr int kAcc = kEight ? 8 : 16;          // accumulators of 16 heads x 8 channels, or of 16 channels x 8 heads
   static_assert(kRing % kBlockGroups == 0, "each ring stage must belong to one group of consumers");
 
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
@@ -357,9 +372,9 @@ __global__ void __launch_bounds__(kThreads4, 1) kv4_attn_kernel(const Kv4AttnArg
     float m0 = kLowest, m1 = kLowest, l0 = 0.f, l1 = 0.f;
     float nb0 = kPShift - m0 * sl2, nb1 = kPShift - m1 * sl2;
     float up0 = kLowest, up1 = kLowest;        // a score above it moves the reference
-    float o[16][4];
+    float o[kAcc][4];
 #pragma unroll
-    for (int n = 0; n < 16; ++n) o[n][0] = o[n][1] = o[n][2] = o[n][3] = 0.f;
+    for (int n = 0; n < kAcc; ++n) o[n][0] = o[n][1] = o[n][2] = o[n][3] = 0.f;
     // A fragments, rows g and g + 8: K step 2 w + i takes channels 32 cq + 8 w + 4 i .. They are put
     // together in shared memory and loaded as quadruples: built in registers, they would be moved
     // into place again in every step. Every warp writes the same values before it reads them.
@@ -393,8 +408,10 @@ __global__ void __launch_bounds__(kThreads4, 1) kv4_attn_kernel(const Kv4AttnArg
         const uint32_t kc = blk + kKCodes + tile0 * 512 + lane * 16, ks = blk + kKScales + tile0 * 128 + lane * 4;
         const uint32_t vc = blk + kVCodes + tile0 * 512 + lane * 16;
         const uint32_t vs = blk + kVScales + (tile0 * 4 + cq) * 32 + (g >> 1) * 8;
-        // raw scores, heads g and g + 8
-        float sc[kTiles][4];
+        // raw scores: tokens 2 cq and 2 cq + 1 of tile r, heads g and g + 8; kEight: of a pair of tiles,
+        // token g of either, heads 2 cq and 2 cq + 1
+        constexpr int kScores = kEight ? kTiles / 2 : kTiles;
+        float sc[kScores][4];
         uint4 kw[kTiles];
         uint32_t s2[kTiles], z2[kTiles];
 #pragma unroll
@@ -403,16 +420,22 @@ __global__ void __launch_bounds__(kThreads4, 1) kv4_attn_kernel(const Kv4AttnArg
           const uint32_t sz = lds32(ks + r * 128);
           s2[r] = dup_lo(sz);
           z2[r] = dup_hi(sz);
-          sc[r][0] = sc[r][1] = sc[r][2] = sc[r][3] = 0.f;
         }
+#pragma unroll
+        for (int r = 0; r < kScores; ++r) sc[r][0] = sc[r][1] = sc[r][2] = sc[r][3] = 0.f;
         // the tiles side by side, so that consecutive products do not wait for one another
 #pragma unroll
         for (int k = 0; k < 8; ++k) {
-#pragma unroll
-          for (int r = 0; r < kTiles; ++r) {
+          const auto keys = [&](int r, int half) {
             const uint32_t word = k < 2 ? kw[r].x : k < 4 ? kw[r].y : k < 6 ? kw[r].z : kw[r].w;
-            product<false>(sc[r], qf[k].x, qf[k].y, qf[k].z, qf[k].w, key_pair(word, 2 * (k & 1), s2[r], z2[r], mk),
-                           key_pair(word, 2 * (k & 1) + 1, s2[r], z2[r], mk));
+            return key_pair(word, 2 * (k & 1) + half, s2[r], z2[r], mk);
+          };
+#pragma unroll
+          for (int r = 0; r < kScores; ++r) {
+            if constexpr (kEight)
+              product<false>(sc[r], keys(2 * r, 0), keys(2 * r + 1, 0), keys(2 * r, 1), keys(2 * r + 1, 1), qf[k].x, qf[k].z);
+            else
+              product<false>(sc[r], qf[k].x, qf[k].y, qf[k].z, qf[k].w, keys(r, 0), keys(r, 1));
           }
         }
         // scales and offsets of the value tiles
@@ -424,26 +447,29 @@ __global__ void __launch_bounds__(kThreads4, 1) kv4_attn_kernel(const Kv4AttnArg
 #pragma unroll
           for (int r = 0; r < kTiles; ++r) {
             const bool in0 = 8 * r + 2 * cq < live, in1 = 8 * r + 2 * cq + 1 < live;
-            sc[r][0] = in0 ? sc[r][0] : kNegInf;
-            sc[r][1] = in1 ? sc[r][1] : kNegInf;
-            sc[r][2] = in0 ? sc[r][2] : kNegInf;
-            sc[r][3] = in1 ? sc[r][3] : kNegInf;
+            if constexpr (kEight) {
+              if (8 * r + g >= live) sc[r / 2][2 * (r & 1)] = sc[r / 2][2 * (r & 1) + 1] = kNegInf;
+            } else {
+              sc[r][0] = in0 ? sc[r][0] : kNegInf;
+              sc[r][1] = in1 ? sc[r][1] : kNegInf;
+              sc[r][2] = in0 ? sc[r][2] : kNegInf;
+              sc[r][3] = in1 ? sc[r][3] : kNegInf;
+            }
             const uint32_t keep = (in0 ? 0xffffu : 0u) | (in1 ? 0xffff0000u : 0u);
             z[r].x &= keep;
             z[r].y &= keep;
           }
         }
-        float mx0 = fmaxf(sc[0][0], sc[0][1]), mx1 = fmaxf(sc[0][2], sc[0][3]);
+        // a lane's two heads are its scores 0, 1 and 2, 3; kEight: 0, 2 and 1, 3
+        float mx0 = fmaxf(sc[0][0], sc[0][kEight ? 2 : 1]), mx1 = fmaxf(sc[0][kEight ? 1 : 2], sc[0][3]);
 #pragma unroll
-        for (int r = 1; r < kTiles; ++r) {
-          mx0 = fmaxf(mx0, fmaxf(sc[r][0], sc[r][1]));
-          mx1 = fmaxf(mx1, fmaxf(sc[r][2], sc[r][3]));
+        for (int r = 1; r < kScores; ++r) {
+          mx0 = fmaxf(mx0, fmaxf(sc[r][0], sc[r][kEight ? 2 : 1]));
+          mx1 = fmaxf(mx1, fmaxf(sc[r][kEight ? 1 : 2], sc[r][3]));
         }
         if (__any_sync(0xffffffffu, mx0 > up0 || mx1 > up1)) {     // move the references
-          mx0 = fmaxf(mx0, __shfl_xor_sync(0xffffffffu, mx0, 1));
-          mx1 = fmaxf(mx1, __shfl_xor_sync(0xffffffffu, mx1, 1));
-          mx0 = fmaxf(mx0, __shfl_xor_sync(0xffffffffu, mx0, 2));
-          mx1 = fmaxf(mx1, __shfl_xor_sync(0xffffffffu, mx1, 2));
+          mx0 = over_lanes<kEight>(mx0, [](float x, float y) { return fmaxf(x, y); });
+          mx1 = over_lanes<kEight>(mx1, [](float x, float y) { return fmaxf(x, y); });
           const float n0 = fmaxf(m0, mx0), n1 = fmaxf(m1, mx1);
           const float al0 = fast_exp2((m0 - n0) * sl2), al1 = fast_exp2((m1 - n1) * sl2);
           m0 = n0;
@@ -455,50 +481,59 @@ __global__ void __launch_bounds__(kThreads4, 1) kv4_attn_kernel(const Kv4AttnArg
           l0 *= al0;
           l1 *= al1;
 #pragma unroll
-          for (int n = 0; n < 16; ++n) {
+          for (int n = 0; n < kAcc; ++n) {
             o[n][0] *= al0;
-            o[n][1] *= al0;
-            o[n][2] *= al1;
+            o[n][1] *= kEight ? al1 : al0;
+            o[n][2] *= kEight ? al0 : al1;
             o[n][3] *= al1;
           }
         }
-        // weights, as A fragments of 16 tokens
+        // weights, as A fragments of 16 tokens; kEight: as B fragments, a tile's 8 x 8 transposed
         uint32_t pa[kTiles][2];
         float ps0 = 0.f, ps1 = 0.f;
 #pragma unroll
-        for (int r = 0; r < kTiles; ++r) {
-          const float p0 = fast_exp2(fmaf(sc[r][0], sl2, nb0)), p1 = fast_exp2(fmaf(sc[r][1], sl2, nb0));
-          const float p2 = fast_exp2(fmaf(sc[r][2], sl2, nb1)), p3 = fast_exp2(fmaf(sc[r][3], sl2, nb1));
-          ps0 += p0 + p1;
-          ps1 += p2 + p3;
+        for (int r = 0; r < kScores; ++r) {
+          const float nb01 = kEight ? nb1 : nb0, nb10 = kEight ? nb0 : nb1;
+          const float p0 = fast_exp2(fmaf(sc[r][0], sl2, nb0)), p1 = fast_exp2(fmaf(sc[r][1], sl2, nb01));
+          const float p2 = fast_exp2(fmaf(sc[r][2], sl2, nb10)), p3 = fast_exp2(fmaf(sc[r][3], sl2, nb1));
+          ps0 += p0 + (kEight ? p2 : p1);
+          ps1 += (kEight ? p1 : p2) + p3;
           const __half2 x = __floats2half2_rn(p0, p1), y = __floats2half2_rn(p2, p3);
-          pa[r][0] = *reinterpret_cast<const uint32_t*>(&x);
-          pa[r][1] = *reinterpret_cast<const uint32_t*>(&y);
-        }
-        if constexpr (kStats) {
-          ps0 += __shfl_xor_sync(0xffffffffu, ps0, 1);
-          ps1 += __shfl_xor_sync(0xffffffffu, ps1, 1);
-          ps0 += __shfl_xor_sync(0xffffffffu, ps0, 2);
-          ps1 += __shfl_xor_sync(0xffffffffu, ps1, 2);
-          if (cq == 0) {
-            const int slots = a.idx ? a.kslots : a.nb_cap;
-            float2* st = a.stats + (((size_t)p.bg * slots + s) * (8 / kTiles) + tile0 / kTiles) * kHeads;
-            st[g] = make_float2(m0 * sl2, ps0);
-            st[g + 8] = make_float2(m1 * sl2, ps1);
+          const uint32_t xb = *reinterpret_cast<const uint32_t*>(&x), yb = *reinterpret_cast<const uint32_t*>(&y);
+          if constexpr (kEight) {
+            pa[2 * r][0] = transposed(xb);
+            pa[2 * r + 1][0] = transposed(yb);
+          } else {
+            pa[r][0] = xb;
+            pa[r][1] = yb;
           }
         }
-        l0 += ps0;            // without kStats: this lane's share, summed over the four lanes at the end
+        if constexpr (kStats) {
+          ps0 = over_lanes<kEight>(ps0, [](float x, float y) { return x + y; });
+          ps1 = over_lanes<kEight>(ps1, [](float x, float y) { return x + y; });
+          const int slots = a.idx ? a.kslots : a.nb_cap;
+          float2* st = a.stats + (((size_t)p.bg * slots + s) * (8 / kTiles) + tile0 / kTiles) * kHeads;
+          if (kEight ? g == 0 : cq == 0) {
+            st[kEight ? 2 * cq : g] = make_float2(m0 * sl2, ps0);
+            st[kEight ? 2 * cq + 1 : g + 8] = make_float2(m1 * sl2, ps1);
+          }
+        }
+        l0 += ps0;            // without kStats: this lane's share, summed over the lanes at the end
         l1 += ps1;
         // o += weights . values
 #pragma unroll
         for (int r = 0; r < kTiles; r += 2) {
           const uint4 v0 = lds128(vc + r * 512), v1 = lds128(vc + r * 512 + 512);
+          const auto values = [&](const uint4& v, int n, const uint2& sz) {
+            return value_pair(n < 4 ? v.x : n < 8 ? v.y : n < 12 ? v.z : v.w, n & 3, sz.x, sz.y, mk);
+          };
 #pragma unroll
-          for (int n = 0; n < 16; ++n) {
-            const uint32_t wa = n < 4 ? v0.x : n < 8 ? v0.y : n < 12 ? v0.z : v0.w;
-            const uint32_t wb = n < 4 ? v1.x : n < 8 ? v1.y : n < 12 ? v1.z : v1.w;
-            product<true>(o[n], pa[r][0], pa[r][1], pa[r + 1][0], pa[r + 1][1], value_pair(wa, n & 3, z[r].x, z[r].y, mk),
-                          value_pair(wb, n & 3, z[r + 1].x, z[r + 1].y, mk));
+          for (int n = 0; n < kAcc; ++n) {
+            if constexpr (kEight)
+              product<true>(o[n], values(v0, 2 * n, z[r]), values(v0, 2 * n + 1, z[r]), values(v1, 2 * n, z[r + 1]),
+                            values(v1, 2 * n + 1, z[r + 1]), pa[r][0], pa[r + 1][0]);
+            else
+              product<true>(o[n], pa[r][0], pa[r][1], pa[r + 1][0], pa[r + 1][1], values(v0, n, z[r]), values(v1, n, z[r + 1]));
           }
         }
       }
@@ -513,52 +548,57 @@ __global__ void __launch_bounds__(kThreads4, 1) kv4_attn_kernel(const Kv4AttnArg
     m0 *= sl2;
     m1 *= sl2;
     if constexpr (!kStats) {
-      l0 += __shfl_xor_sync(0xffffffffu, l0, 1);
-      l1 += __shfl_xor_sync(0xffffffffu, l1, 1);
-      l0 += __shfl_xor_sync(0xffffffffu, l0, 2);
-      l1 += __shfl_xor_sync(0xffffffffu, l1, 2);
+      l0 = over_lanes<kEight>(l0, [](float x, float y) { return x + y; });
+      l1 = over_lanes<kEight>(l1, [](float x, float y) { return x + y; });
     }
-
     // ---------------------------------------------------------- merge the warps
     // The upper half of the warps hand their results to the lower half, lane for lane.
     if (warp >= kMergeWarps) {
       float4* give = reinterpret_cast<float4*>(mO + (warp - kMergeWarps) * kHeads * kRow) + lane;
 #pragma unroll
-      for (int n = 0; n < 16; ++n) give[n * 32] = make_float4(o[n][0], o[n][1], o[n][2], o[n][3]);
-      give[16 * 32] = make_float4(m0, m1, l0, l1);
+      for (int n = 0; n < kAcc; ++n) give[n * 32] = make_float4(o[n][0], o[n][1], o[n][2], o[n][3]);
+      give[kAcc * 32] = make_float4(m0, m1, l0, l1);
     }
     sync_consumers();
     if (warp < kMergeWarps) {
       float* mine = mO + warp * kHeads * kRow;
       const float4* take = reinterpret_cast<const float4*>(mine) + lane;
-      const float4 ml = take[16 * 32];
+      const float4 ml = take[kAcc * 32];
       const float n0 = fmaxf(m0, ml.x), n1 = fmaxf(m1, ml.y);
       const float wa0 = fast_exp2(m0 - n0), wa1 = fast_exp2(m1 - n1), wb0 = fast_exp2(ml.x - n0), wb1 = fast_exp2(ml.y - n1);
       l0 = l0 * wa0 + ml.z * wb0;
       l1 = l1 * wa1 + ml.w * wb1;
 #pragma unroll
-      for (int n = 0; n < 16; ++n) {
+      for (int n = 0; n < kAcc; ++n) {
         const float4 x = take[n * 32];
         o[n][0] = o[n][0] * wa0 + x.x * wb0;
-        o[n][1] = o[n][1] * wa0 + x.y * wb0;
-        o[n][2] = o[n][2] * wa1 + x.z * wb1;
+        o[n][1] = o[n][1] * (kEight ? wa1 : wa0) + x.y * (kEight ? wb1 : wb0);
+        o[n][2] = o[n][2] * (kEight ? wa0 : wa1) + x.z * (kEight ? wb0 : wb1);
         o[n][3] = o[n][3] * wa1 + x.w * wb1;
       }
       __syncwarp();
-      float* r0 = mine + g * kRow;
-      float* r1 = r0 + 8 * kRow;
+      const int h0 = kEight ? 2 * cq : g, h1 = kEight ? 2 * cq + 1 : g + 8;      // the lane's heads
+      float* r0 = mine + h0 * kRow;
+      float* r1 = mine + h1 * kRow;
 #pragma unroll
-      for (int i = 0; i < 4; ++i) {            // o[n][0]: channel 32 cq + n; o[n][1]: 32 cq + 16 + n
-        *reinterpret_cast<float4*>(r0 + 36 * cq + 4 * i) = make_float4(o[4 * i][0], o[4 * i + 1][0], o[4 * i + 2][0], o[4 * i + 3][0]);
-        *reinterpret_cast<float4*>(r0 + 36 * cq + 16 + 4 * i) = make_float4(o[4 * i][1], o[4 * i + 1][1], o[4 * i + 2][1], o[4 * i + 3][1]);
-        *reinterpret_cast<float4*>(r1 + 36 * cq + 4 * i) = make_float4(o[4 * i][2], o[4 * i + 1][2], o[4 * i + 2][2], o[4 * i + 3][2]);
-        *reinterpret_cast<float4*>(r1 + 36 * cq + 16 + 4 * i) = make_float4(o[4 * i][3], o[4 * i + 1][3], o[4 * i + 2][3], o[4 * i + 3][3]);
+      for (int i = 0; i < 4; ++i) {
+        if constexpr (kEight) {                // o[n][0]: channel 16 g + 2 n; o[n][2]: 16 g + 2 n + 1
+          const int at = mcol(16 * g) + 4 * i;
+          *reinterpret_cast<float4*>(r0 + at) = make_float4(o[2 * i][0], o[2 * i][2], o[2 * i + 1][0], o[2 * i + 1][2]);
+          *reinterpret_cast<float4*>(r1 + at) = make_float4(o[2 * i][1], o[2 * i][3], o[2 * i + 1][1], o[2 * i + 1][3]);
+        } else {                               // o[n][0]: channel 32 cq + n; o[n][1]: 32 cq + 16 + n
+          const int at = mcol(32 * cq) + 4 * i;
+          *reinterpret_cast<float4*>(r0 + at) = make_float4(o[4 * i][0], o[4 * i + 1][0], o[4 * i + 2][0], o[4 * i + 3][0]);
+          *reinterpret_cast<float4*>(r0 + at + 16) = make_float4(o[4 * i][1], o[4 * i + 1][1], o[4 * i + 2][1], o[4 * i + 3][1]);
+          *reinterpret_cast<float4*>(r1 + at) = make_float4(o[4 * i][2], o[4 * i + 1][2], o[4 * i + 2][2], o[4 * i + 3][2]);
+          *reinterpret_cast<float4*>(r1 + at + 16) = make_float4(o[4 * i][3], o[4 * i + 1][3], o[4 * i + 2][3], o[4 * i + 3][3]);
+        }
       }
-      if (cq == 0) {
-        mM[warp * kHeads + g] = n0;
-        mM[warp * kHeads + g + 8] = n1;
-        mL[warp * kHeads + g] = l0;
-        mL[warp * kHeads + g + 8] = l1;
+      if (kEight ? g == 0 : cq == 0) {
+        mM[warp * kHeads + h0] = n0;
+        mM[warp * kHeads + h1] = n1;
+        mL[warp * kHeads + h0] = l0;
+        mL[warp * kHeads + h1] = l1;
       }
     }
     sync_consumers();
@@ -725,9 +765,9 @@ __global__ void __launch_bounds__(kThreads4, 1) kv4_attn_kernel(const Kv4AttnArg
 
 namespace {
 
-template <int kW, bool kStats, bool kCluster>
+template <int kW, bool kStats, bool kCluster, bool kEight>
 int launch_form(const Kv4AttnArgs& a, int grid, int cluster, cudaStream_t s) {
-  auto kern = kv4_attn_kernel<kW, kStats, kCluster>;
+  auto kern = kv4_attn_kernel<kW, kStats, kCluster, kEight>;
   constexpr int smem = kCluster ? kClusterSmem4 : kSmem4;
   static_assert(smem <= 232448, "shared memory of a CTA");
   // the register split needs the registers that it counts on; a build with fewer must not run
@@ -758,7 +798,11 @@ int launch_form(const Kv4AttnArgs& a, int grid, int cluster, cudaStream_t s) {
 
 template <int kW, bool kCluster>
 int launch_form(const Kv4AttnArgs& a, int grid, int cluster, cudaStream_t s) {
-  return a.stats ? launch_form<kW, true, kCluster>(a, grid, cluster, s) : launch_form<kW, false, kCluster>(a, grid, cluster, s);
+  if (a.H <= 8)
+    return a.stats ? launch_form<kW, true, kCluster, true>(a, grid, cluster, s)
+                   : launch_form<kW, false, kCluster, true>(a, grid, cluster, s);
+  return a.stats ? launch_form<kW, true, kCluster, false>(a, grid, cluster, s)
+                 : launch_form<kW, false, kCluster, false>(a, grid, cluster, s);
 }
 
 }  // namespace
