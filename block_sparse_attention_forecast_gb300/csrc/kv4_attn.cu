@@ -8,7 +8,10 @@
 // cycles and its operands' expansion the issue port for 8.7, but the two only half overlap (13.5
 // cycles together), so the instructions bound a long cache, not the memory: batch 16 of 131072 tokens
 // (671 MB) takes 147 us, and 137 us when every copy hits the same block in L2. A tcgen05 form, whose
-// expanded operands go through tensor memory, took 240 us.
+// expanded operands go through tensor memory, took 240 us. With at most 8 heads (kEight) the roles
+// change: the cache is the A operand, 16 tokens or 16 channels of it, the heads are the N dimension,
+// and half the products do: the same batch with 8 heads takes 117 us, 0.84 of the memory's rate
+// (147 with the heads as M). A score tile's 8 x 8 weights are transposed between lanes on the way.
 //
 // Work, three forms chosen by launch_kv4_attn:
 //   - few blocks per (sequence, group): one thread-block cluster each, the blocks split evenly over
@@ -61,11 +64,12 @@ constexpr int kMaxCluster4 = 8;
 constexpr int kRecv4 = kHeads + kMaxCluster4 - 1;
 constexpr int kClusterSmem4 = kSmem4 + kRecv4 * (kHeadDim + 2) * 4;
 // The rules' limits, with both sides measured (kW = warps that share a block):
-//   kWholeBlocks    blocks per warp from which a warp takes whole ones. Batch 16 of 131072 tokens (215
-//                   blocks per CTA): kW 1 147 us, 2 150, 4 174. A ragged batch of 64 with 3 to 24576
-//                   tokens (21 per CTA): 27.5, 27.4, 28.7.
+//   kWholeBlocks    blocks per warp from which a warp takes whole ones. Batch 16 of 131072 tokens (431
+//                   blocks per CTA), 16 heads: kW 1 148 us, 2 151, 4 177; 8 heads: 117, 121, 144. A ragged
+//                   batch of 8 x 8 groups of 4096 to 8191 tokens (41 per CTA), 4 heads: 24.6, 24.3, 25.6.
 //   kPairBlocks     blocks per CTA of a cluster above which two warps share a block, not four. 34 blocks in
-//                   clusters of 4 (8.5 per CTA): kW 2 8.4 us, 4 8.75; clusters of 8 (4 per CTA): 7.04, 6.95.
+//                   clusters of 4 (8.5 per CTA): kW 2 8.45 us, 4 8.8, with 8 heads 7.4, 7.57; clusters
+//                   of 8 (4.25 per CTA): 7.04, 6.95.
 //   kClusterBlocks  blocks per CTA up to which groups get clusters. Against the planned form, 34 blocks of one
 //                   sequence: 6.8 us instead of 12.5; of 16 sequences: 8.4 instead of 14.8.
 //   kMinUnits       blocks per CTA below which fewer CTAs work; 1, 2 and 4 measured alike, and 2 halves
