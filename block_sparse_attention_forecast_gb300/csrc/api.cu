@@ -895,7 +895,29 @@ int32_t sparda_sparse_decode_attn_mass(const sparda_shape* s, const sparda_layer
 
 namespace {
 
-// What both evictions check and hand on beside their cache planes. `in_place`: no dst argument.
+bool overlap(const void* p, size_t n, const void* q, size_t m) {
+  const uintptr_t a = reinterpret_cast<uintptr_t>(p), b = reinterpret_cast<uintptr_t>(q);
+  return a < b + m && b < a + n;
+}
+
+// Whether a cache of shape d shares memory with the source of shape s (planes and compressed keys), or
+// its weights and lengths with the source's.
+bool evict_overlap(const EvictArgs& a, const sparda_shape* s, const sparda_shape* d, int32_t batch) {
+  const size_t ns = (size_t)s->max_batch * s->n_groups, nd = (size_t)d->max_batch * d->n_groups;
+  const void* from[3] = {a.src_ck, a.src[0], a.src[1]};
+  const void* to[3] = {a.dst_ck, a.dst[0], a.dst[1]};
+  const size_t ck = kHeadDim * 2;
+  const size_t n_from[2] = {ns * w_cap(s) * ck, ns * a.src_nb * a.block_bytes};
+  const size_t n_to[2] = {nd * w_cap(d) * ck, nd * a.dst_nb * a.block_bytes};
+  for (int i = 0; i <= a.planes; ++i)
+    for (int j = 0; j <= a.planes; ++j)
+      if (overlap(from[i], n_from[i > 0], to[j], n_to[j > 0])) return true;
+  return overlap(a.src_mass, ns * a.src_nb * 4, a.dst_mass, nd * a.dst_nb * 4) ||
+         overlap(a.src_len, (size_t)batch * 4, a.dst_len, (size_t)batch * 4);
+}
+
+// What both evictions check and hand on beside their cache planes, which *a holds already.
+// `in_place`: no dst argument.
 int32_t prepare_evict(const sparda_shape* s, const sparda_shape* d, const void* ck, void* dst_ck, float* mass,
                       int32_t* seq_len, float* dst_mass, int32_t* dst_seq_len, int32_t batch, int32_t keep,
                       int32_t recent, int32_t* kept, bool in_place, EvictArgs* a) {
@@ -909,15 +931,12 @@ int32_t prepare_evict(const sparda_shape* s, const sparda_shape* d, const void* 
     dst_mass = mass;
     dst_seq_len = seq_len;
   } else {
-    if (!d || !dst_mass || !dst_seq_len || dst_mass == mass || dst_seq_len == seq_len || dst_ck == ck)
-      return SPARDA_ERR_INVALID_ARG;
+    if (!d || !dst_mass || !dst_seq_len) return SPARDA_ERR_INVALID_ARG;
     if (d->n_groups != s->n_groups || d->max_batch < batch || d->max_ctx / kBlock < keep)
       return SPARDA_ERR_UNSUPPORTED_SHAPE;
   }
   if (!aligned(mass, 4) || !aligned(seq_len, 4) || !aligned(dst_mass, 4) || !aligned(dst_seq_len, 4) || !aligned(kept, 4))
     return SPARDA_ERR_MISALIGNED;
-  int* err = dev_error_ptr();
-  if (!err) return SPARDA_ERR_CUDA;
   a->src_ck = static_cast<const __nv_bfloat16*>(ck);
   a->dst_ck = static_cast<__nv_bfloat16*>(dst_ck);
   a->src_mass = mass;
@@ -925,7 +944,6 @@ int32_t prepare_evict(const sparda_shape* s, const sparda_shape* d, const void* 
   a->src_len = seq_len;
   a->dst_len = dst_seq_len;
   a->kept = kept;
-  a->err = err;
   a->B = batch;
   a->G = s->n_groups;
   a->src_nb = nb_cap(s);
@@ -933,7 +951,9 @@ int32_t prepare_evict(const sparda_shape* s, const sparda_shape* d, const void* 
   a->keep = keep;
   a->recent = recent;
   a->in_place = in_place ? 1 : 0;
-  return SPARDA_OK;
+  if (!in_place && evict_overlap(*a, s, d, batch)) return SPARDA_ERR_INVALID_ARG;
+  a->err = dev_error_ptr();
+  return a->err ? SPARDA_OK : SPARDA_ERR_CUDA;
 }
 
 }  // namespace
@@ -950,17 +970,16 @@ int32_t sparda_evict_blocks(const sparda_shape* s, const sparda_layer_kv* L, flo
   if (dst) {
     if (dst->on_host) return SPARDA_ERR_INVALID_ARG;
     SPARDA_TRY(layer_status(dst, true));
-    if (dst->k == L->k || dst->v == L->v) return SPARDA_ERR_INVALID_ARG;
   }
   EvictArgs a{};
-  SPARDA_TRY(prepare_evict(s, d, L->ck, dst ? dst->ck : nullptr, mass, seq_len, dst_mass, dst_seq_len, batch, keep, recent,
-                           kept, dst == nullptr, &a));
   a.src[0] = static_cast<const uint8_t*>(L->k);
   a.src[1] = static_cast<const uint8_t*>(L->v);
   a.dst[0] = static_cast<uint8_t*>(dst ? dst->k : L->k);
   a.dst[1] = static_cast<uint8_t*>(dst ? dst->v : L->v);
   a.planes = 2;
   a.block_bytes = kBlockBytes;
+  SPARDA_TRY(prepare_evict(s, d, L->ck, dst ? dst->ck : nullptr, mass, seq_len, dst_mass, dst_seq_len, batch, keep, recent,
+                           kept, dst == nullptr, &a));
   if (!launch_evict(a, static_cast<cudaStream_t>(stream))) return SPARDA_ERR_CUDA;
   return cuda_status(cudaGetLastError());
 }
@@ -972,18 +991,15 @@ int32_t sparda_kv4_evict_blocks(const sparda_shape* s, const sparda_layer_kv4* L
   SPARDA_TRY(kv4_shape_status(s));
   SPARDA_TRY(kv4_layer_status(L, true));
   if (d) SPARDA_TRY(kv4_shape_status(d));
-  if (dst) {
-    SPARDA_TRY(kv4_layer_status(dst, true));
-    if (dst->kv == L->kv) return SPARDA_ERR_INVALID_ARG;
-  }
+  if (dst) SPARDA_TRY(kv4_layer_status(dst, true));
   EvictArgs a{};
-  SPARDA_TRY(prepare_evict(s, d, L->ck, dst ? dst->ck : nullptr, mass, seq_len, dst_mass, dst_seq_len, batch, keep, recent,
-                           kept, dst == nullptr, &a));
   a.src[0] = static_cast<const uint8_t*>(L->kv);
   a.dst[0] = static_cast<uint8_t*>(dst ? dst->kv : L->kv);
   a.planes = 1;
   a.block_bytes = SPARDA_KV4_BLOCK_BYTES;
   a.kv4 = 1;
+  SPARDA_TRY(prepare_evict(s, d, L->ck, dst ? dst->ck : nullptr, mass, seq_len, dst_mass, dst_seq_len, batch, keep, recent,
+                           kept, dst == nullptr, &a));
   if (!launch_evict(a, static_cast<cudaStream_t>(stream))) return SPARDA_ERR_CUDA;
   return cuda_status(cudaGetLastError());
 }

@@ -151,3 +151,33 @@ def test_binding_checks_types_sizes_and_strides():
     for bad in (ok.float(), ok[:3], ok.t()):
         with pytest.raises(ValueError):
             sb._checked("x", bad, torch.bfloat16, 32, dev)
+
+
+@pytest.mark.parametrize("kv4", [False, True])
+def test_eviction_refuses_a_destination_inside_the_source(kv4):
+    """A destination that shares any memory with the source, not its first byte only."""
+    s, base = _shape(max_batch=2, n_groups=2, max_ctx=1024), 1 << 30
+    fn = sb.lib.sparda_kv4_evict_blocks if kv4 else sb.lib.sparda_evict_blocks
+    plane = 4 * (16 * 10240 if kv4 else 1024 * 256)
+    ck = 4 * sb.num_windows(1024) * 256
+    if kv4:
+        make = lambda k, v, c: _l4(kv=k, ck=c)
+    else:
+        make = lambda k, v, c: _lk(k=k, v=v, ck=c)
+    far = base << 4
+    src = make(base, base + plane, base + 2 * plane)
+
+    def call(k=far, v=far + plane, c=far + 2 * plane, mass=1 << 20, dm=1 << 21, seq=1 << 22, dq=1 << 23, batch=2, keep=8):
+        return fn(_ref(s), src, P(mass), P(seq), _ref(s), make(k, v, c), P(dm), P(dq), batch, keep, 2, P(1 << 25), None)
+    bad = sb.ERR_INVALID_ARG
+    assert call(k=base + 16) == bad and call(k=base + plane - 16) == bad and call(k=base - plane + 16) == bad
+    assert call(c=base + 2 * plane + ck - 16) == bad                       # compressed keys
+    assert call(c=base + 16) == bad and call(k=base + 2 * plane + 16) == bad      # of different kinds
+    assert call(dm=(1 << 20) + 4) == bad and call(dq=(1 << 22) + 4) == bad
+    if not kv4:
+        assert call(v=base + 32) == bad and call(k=base + plane + 64) == bad
+    # side by side is apart: no refusal of the arguments
+    for ok in (dict(), dict(c=base + 2 * plane + ck), dict(dq=(1 << 22) + 8), dict(dm=(1 << 20) + 4 * 64)):
+        assert call(**ok, keep=4097) == sb.ERR_UNSUPPORTED_SHAPE
+        if not torch.cuda.is_available():
+            assert call(**ok) != bad
