@@ -28,6 +28,7 @@
 // for the next group.
 #pragma once
 
+#include "block_mass.cuh"
 #include "common.cuh"
 #include "kernels.h"
 #include "timeline.cuh"
@@ -439,15 +440,12 @@ __device__ __forceinline__ void attn_cta(const AttnArgs& a, const CUtensorMap* m
             make_uint4(pk[0], pk[1], pk[2], pk[3]);
       }
       if constexpr (kStats) {
+        const SlotBlocks list = slot_blocks(a.idx + (size_t)bg * a.kslots, gi.n_sel);
         cluster_sync();                        // (the merge buffers mM, mL were last read before the first one)
         const float Mh0 = mM[lane & 15], Lh0 = mL[lane & 15];
-        const int nb = a.max_ctx / kBlock;
-        for (int s = s_begin + warp; s < s_stop; s += kConsumerWarps) {
-          const int j = a.idx[(size_t)bg * a.kslots + s];
-          if (j >= 0 && j <= gi.tb)
-            add_block_mass(a.stats + ((size_t)bg * a.kslots + s) * kGroupWarps * kHeads, kGroupWarps, kHeads, Mh0, Lh0,
-                           a.mass + (size_t)bg * nb + j);
-        }
+        for (int s = s_begin + warp; s < s_stop; s += kConsumerWarps)
+          add_block_mass(a.stats + (size_t)bg * a.kslots * kGroupWarps * kHeads, kGroupWarps, kHeads, Mh0, Lh0, list, s, gi.tb,
+                         a.mass + (size_t)bg * (a.max_ctx / kBlock));
       }
       continue;
     }

@@ -243,22 +243,6 @@ struct BlockMassArgs {
 };
 void launch_block_mass(const BlockMassArgs& a, int bg_count, cudaStream_t s);
 
-#ifdef __CUDACC__
-// The weight of one attended block from its statistics, added to *mass by one warp: l exp2(m - M) / L
-// over its parts and heads (M, L: the final maximum and sum of head lane % 16).
-__device__ __forceinline__ void add_block_mass(const float2* st, int parts, int H, float M, float L, float* mass) {
-  const int lane = threadIdx.x & 31;
-  const float2 x = st[lane], y = parts == 4 ? st[lane + 32] : make_float2(0.f, 0.f);
-  float w = 0.f;                                   // a part without tokens has l = 0
-  if (x.y != 0.f) w += x.y * exp2f(x.x - M);
-  if (y.y != 0.f) w += y.y * exp2f(y.x - M);
-  w = (lane & 15) < H && L != 0.f ? w / L : 0.f;
-#pragma unroll
-  for (int d = 16; d; d >>= 1) w += __shfl_xor_sync(0xffffffffu, w, d);
-  if (lane == 0) atomicAdd(mass, w);
-}
-#endif
-
 // Eviction (evict.cu). A cache is one or two planes of fixed bytes per block.
 struct EvictArgs {
   const uint8_t* src[2];         // [max_batch*G, src_nb, block_bytes]

@@ -34,6 +34,7 @@
 // the reference, and below that off by at most 2^-31 of it each.
 #include <cuda_fp16.h>
 
+#include "block_mass.cuh"
 #include "kernels.h"
 #include "kv4.cuh"
 
@@ -743,16 +744,14 @@ __global__ void __launch_bounds__(kThreads4, 1) kv4_attn_kernel(const Kv4AttnArg
     }
     first_piece = false;
     if constexpr (kCluster && kStats) {
-      cluster_sync();                          // (mM and mL were last read before the first one)
-      const float Mh = mM[lane & 15], Lh = mL[lane & 15];
+      const SlotBlocks list = slot_blocks(a.idx ? a.idx + (size_t)p.bg * a.kslots : nullptr, n0);
       const int tb = (a.seq_len[p.bg / a.G] - 1) / kBlock;
       const int slots = a.idx ? a.kslots : a.nb_cap;
-      for (int s = p.s0 + warp; s < p.s1; s += kCWarps) {
-        const int j = a.idx ? a.idx[(size_t)p.bg * a.kslots + s] : s;
-        if (j >= 0 && j <= tb)
-          add_block_mass(a.stats + ((size_t)p.bg * slots + s) * (8 / kTiles) * kHeads, 8 / kTiles, a.H, Mh, Lh,
-                         a.mass + (size_t)p.bg * a.nb_cap + j);
-      }
+      cluster_sync();                          // (mM and mL were last read before the first one)
+      const float Mh = mM[lane & 15], Lh = mL[lane & 15];
+      for (int s = p.s0 + warp; s < p.s1; s += kCWarps)
+        add_block_mass(a.stats + (size_t)p.bg * slots * (8 / kTiles) * kHeads, 8 / kTiles, a.H, Mh, Lh, list, s, tb,
+                       a.mass + (size_t)p.bg * a.nb_cap);
     }
     if constexpr (kCluster) return;
     sync_consumers();                          // the merge buffer is free again

@@ -530,3 +530,46 @@ def test_attention_many_blocks_nan_and_repeats(sb):
     assert nan[1, 4:].all() and not nan[1, :4].any()
     assert nan[3, :4, 64:96].all() and not nan[3, :4, :64].any() and not nan[3, 4:].any()
     assert not nan[[0, 2, 4, 5, 6, 7]].any()
+
+
+@pytest.mark.parametrize("fmt", ["kv4", "bf16"])
+@pytest.mark.parametrize("B,topk", [(1, 62), (20, 30), (90, 14)])
+def test_mass_of_repeated_blocks_is_reproducible(sb, fmt, B, topk):
+    """Lists that name few blocks many times, over the CTAs of a cluster or of the planned form: the same
+    bits in every call, and what the list's 64-bit reference adds up."""
+    T, n = 1900, topk + 2
+    shape = sb.Shape(n_groups=2, heads_per_group=16, max_ctx=1920, max_batch=B, topk=topk)
+    K, V = _kv(shape, 81)
+    T_list = [T] * B
+    layer = _filled(sb, shape, K, V, T_list)
+    if fmt == "bf16":
+        layer = sb.LayerKV(K.cuda(), V.cuda(), torch.zeros_like(layer.ck))
+    q = synth.normal_bf16((B, 32, 128), 82) * 2
+    gen = torch.Generator().manual_seed(83)
+    idx = torch.randint(0, 5, (B, 2, n), generator=gen, dtype=torch.int32) * 7
+    cnt = torch.randint(1, n + 1, (B, 2), generator=gen, dtype=torch.int32)
+    cnt[0] = n
+    out = torch.empty((B, 32, 128), dtype=torch.bfloat16, device="cuda")
+    kind, call = (sb.WS_KV4_ATTN_MASS, sb.sparda_kv4_decode_attn) if fmt == "kv4" else (
+        sb.WS_ATTN_MASS, sb.sparda_sparse_decode_attn_mass)
+    ws, seq, qd, di, dc = sb.workspace(shape, B, kind), _i32(T_list), q.cuda(), idx.cuda(), cnt.cuda()
+    start = torch.rand((B, 2, 30), generator=gen).cuda()
+    masses = []
+    for _ in range(12):
+        masses.append(start.clone())
+        call(shape, layer, qd, di, dc, seq, B, out, ws, mass=masses[-1])
+    torch.cuda.synchronize()
+    assert sb.sparda_device_error(clear=True) == 0
+    assert all(torch.equal(m, masses[0]) for m in masses[1:])
+    k64 = R.grid_values(K, True) if fmt == "kv4" else to64(K)
+    v64 = _v16(V) if fmt == "kv4" else to64(V)
+    for b in (0, B - 1):
+        for g in range(2):
+            blocks = idx[b, g, :cnt[b, g]].tolist()
+            _, _, w, tol = R.attention(to64(q)[b, 16 * g:16 * g + 16], k64[b, g], v64[b, g], blocks, T, W16)
+            want = start[b, g].cpu().double().numpy()
+            bound = 2.0 ** -22 * want
+            for j, x in zip(blocks, w):
+                want[j] += x
+                bound[j] += tol * x + 2.0 ** -22 * want[j]
+            assert (np.abs(masses[0][b, g].cpu().double().numpy() - want) <= bound).all()
