@@ -53,6 +53,7 @@ constexpr int kLaunchRegs = 168, kProducerRegs = 40, kConsumerRegs = 208;
 static_assert(128 * kProducerRegs + kCThreads * kConsumerRegs <= kThreads4 * kLaunchRegs, "registers the launch holds");
 constexpr int kRing = 16;                                   // at most a warp's lanes
 constexpr int kPlanMax = 1024;
+static_assert(kPlanMax <= 32 * 32, "two steps of a warp find a group");
 constexpr int kRow = 144;                                   // merge-buffer row: 128 + 4 per 32, no bank conflicts
 constexpr int kMergeWarps = kCWarps / 2;                    // the others' results are folded in first
 constexpr int kMergeFloats4 = kMergeWarps * (kHeads * kRow + 2 * kHeads);
@@ -78,6 +79,7 @@ constexpr int kClusterSmem4 = kSmem4 + kRecv4 * (kHeadDim + 2) * 4;
 //   kPlanMax        (sequence, group)s of the balanced plan, held in 4 KiB of shared memory; beyond it there
 //                   are at least six per SM, and whole groups balance well enough.
 constexpr int kWholeBlocks = 2;
+constexpr int kPieceWhole = 10, kPieceSplit = 4;
 constexpr int kPairBlocks = 6;
 constexpr int kClusterBlocks = 24;
 constexpr int kMinUnits = 2;
@@ -181,6 +183,7 @@ __global__ void __launch_bounds__(kThreads4, 1) kv4_attn_kernel(const Kv4AttnArg
   constexpr int kBlockGroups = kCWarps / kW;     // blocks in the consumers' hands at a time
   constexpr int kTiles = kW == 4 ? 2 : 4;        // 8-token tiles of a step
   constexpr int kSteps = 8 / kW / kTiles;        // steps of a warp per block
+  constexpr int kPiece = kW == 1 ? kPieceWhole : kPieceSplit;
   constexpr int kAcc = kEight ? 8 : 16;          // accumulators of 16 heads x 8 channels, or of 16 channels x 8 heads
   static_assert(kRing % kBlockGroups == 0, "each ring stage must belong to one group of consumers");
 
@@ -202,7 +205,26 @@ __global__ void __launch_bounds__(kThreads4, 1) kv4_attn_kernel(const Kv4AttnArg
 
   // ------------------------------------------------------------ the plan
   const bool balanced = !kCluster && a.bg_count <= kPlanMax;
-  int U = 0, ctas = gridDim.x, u0 = 0, u1 = 0, n0 = 0;
+  // The CTAs' ranges are equal in cost: a block counts 1, a group's beginning kPiece more. Block u of the
+  // row, of group bg, then begins at cost u + kPiece (bg + 1).
+  int U = 0, V = 0, ctas = gridDim.x, u0 = 0, u1 = 0, n0 = 0, w_bg = 0;
+  // the first block of CTA i's range, and (bg) a group at or before its
+  const auto cut = [&](int i, int& bg) {
+    const int v = (int)((long long)V * i / ctas);
+    // the last group that begins at or before cost v, by a warp, in two steps of 32 candidates
+    const int stride = (a.bg_count + 31) >> 5;
+    int at = lane * stride;
+    unsigned m = __ballot_sync(0xffffffffu, at < a.bg_count && s_pre[at] + kPiece * at <= v);
+    int lo = (31 - __clz(m)) * stride;
+    at = lo + lane;
+    m = __ballot_sync(0xffffffffu, lane < stride && at < a.bg_count && s_pre[at] + kPiece * at <= v);
+    lo += 31 - __clz(m);
+    bg = lo;
+    return min(s_pre[lo] + max(v - (s_pre[lo] + kPiece * (lo + 1)), 0), s_pre[lo + 1]);
+  };
+  const auto cta_of = [&](int unit, int bg) {
+    return (int)(((long long)(unit + kPiece * (bg + 1) + 1) * ctas - 1) / V);
+  };
   if constexpr (kCluster) {
     const int bg = blockIdx.x / cluster, rank = blockIdx.x % cluster;
     const int T = a.seq_len[bg / a.G];
@@ -237,28 +259,19 @@ __global__ void __launch_bounds__(kThreads4, 1) kv4_attn_kernel(const Kv4AttnArg
     U = s_pre[a.bg_count];
     ctas = min((int)gridDim.x, max(1, (U + kMinUnits - 1) / kMinUnits));
     if ((int)blockIdx.x >= ctas) return;
-    u0 = (int)((long long)U * blockIdx.x / ctas);
-    u1 = (int)((long long)U * (blockIdx.x + 1) / ctas);
+    V = U + kPiece * a.bg_count;
+    u0 = cut(blockIdx.x, w_bg);
+    int end_bg;
+    u1 = cut(blockIdx.x + 1, end_bg);
   } else {
     __syncthreads();
   }
   const int c = blockIdx.x;
-  const auto cta_of = [&](long long unit) { return (int)(((unit + 1) * ctas - 1) / U); };
 
   // Walks the CTA's pieces: balanced, the groups its unit range meets; in a cluster, its share of the
   // one group; else whole groups c, c + grid, ...
-  int w_u = u0, w_bg = 0;
-  if (balanced && u0 < u1) {
-    int lo = 0, hi = a.bg_count - 1;                 // the group with pre[bg] <= u0 < pre[bg + 1]
-    while (lo < hi) {
-      const int mid = (lo + hi) >> 1;
-      if (s_pre[mid + 1] > u0) hi = mid;
-      else lo = mid + 1;
-    }
-    w_bg = lo;
-  } else if (!balanced) {
-    w_bg = kCluster ? c / cluster : c;
-  }
+  int w_u = u0;
+  if (!balanced) w_bg = kCluster ? c / cluster : c;
   const auto next_piece = [&](Piece& p) -> bool {
     if (balanced) {
       if (w_u >= u1) return false;
@@ -267,8 +280,8 @@ __global__ void __launch_bounds__(kThreads4, 1) kv4_attn_kernel(const Kv4AttnArg
       p.bg = w_bg;
       p.s0 = w_u - g0;
       p.s1 = min(u1, g1) - g0;
-      p.first = cta_of(g0);
-      p.n_cta = cta_of(g1 - 1) - p.first + 1;
+      p.first = cta_of(g0, w_bg);
+      p.n_cta = cta_of(g1 - 1, w_bg) - p.first + 1;
       w_u = min(u1, g1);
       return true;
     }
@@ -683,7 +696,8 @@ __global__ void __launch_bounds__(kThreads4, 1) kv4_attn_kernel(const Kv4AttnArg
         // the last CTA of the group joins the partials. The group's first CTA left its partial in
         // slot 1 unless the group begins that CTA's range; all others in slot 0.
         const int g0 = s_pre[p.bg];
-        const int first_slot = p.first * 2 + ((int)((long long)U * p.first / ctas) == g0 ? 0 : 1);
+        int at;
+        const int first_slot = p.first * 2 + (cut(p.first, at) == g0 ? 0 : 1);
         M = kLowest;
         L = 0.f;
 #pragma unroll
