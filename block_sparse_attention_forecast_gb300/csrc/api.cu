@@ -222,11 +222,12 @@ int32_t kv4_shape_status(const sparda_shape* s) {
   return shape_status(&full);
 }
 
+constexpr size_t kKv4JoinBytes = (kKv4MaxCtas * 2 * sizeof(unsigned) + 255) / 256 * 256;
 size_t kv4_part_bytes() { return (size_t)kKv4MaxCtas * 2 * (kHeads * kHeadDim + 2 * kHeads) * sizeof(float); }
 int kv4_mass_slots(const sparda_shape* s) { return kslots(s) > nb_cap(s) ? kslots(s) : nb_cap(s); }
 size_t kv4_workspace_bytes(const sparda_shape* s, int32_t batch, int32_t kind) {
   if (kv4_shape_status(s) != SPARDA_OK || batch < 1 || batch > s->max_batch) return 0;
-  const size_t base = counters_bytes(s) + kv4_part_bytes();
+  const size_t base = counters_bytes(s) + kKv4JoinBytes + kv4_part_bytes();
   return kind == SPARDA_WS_KV4_ATTN ? base : base + mass_stats_bytes(s, kv4_mass_slots(s)) + mass_ml_bytes(s);
 }
 
@@ -849,12 +850,13 @@ int32_t sparda_kv4_decode_attn(const sparda_shape* s, const sparda_layer_kv4* L,
   if (!err) return SPARDA_ERR_CUDA;
   const cudaStream_t st = static_cast<cudaStream_t>(stream);
   uint8_t* w = static_cast<uint8_t*>(ws);
-  float* part = reinterpret_cast<float*>(w + counters_bytes(s));
-  uint8_t* stats = w + counters_bytes(s) + kv4_part_bytes();
+  unsigned* joins = reinterpret_cast<unsigned*>(w + counters_bytes(s));
+  float* part = reinterpret_cast<float*>(w + counters_bytes(s) + kKv4JoinBytes);
+  uint8_t* stats = reinterpret_cast<uint8_t*>(part) + kv4_part_bytes();
   const int slots = idx ? kslots(s) : nb_cap(s);
   Kv4AttnArgs a{static_cast<const uint8_t*>(L->kv), static_cast<const __nv_bfloat16*>(q), idx, cnt, seq_len,
                 static_cast<__nv_bfloat16*>(out), part, part + (size_t)kKv4MaxCtas * 2 * kHeads * kHeadDim,
-                reinterpret_cast<unsigned*>(w), nullptr, nullptr, mass, err, s->n_groups, s->heads_per_group, s->max_ctx,
+                reinterpret_cast<unsigned*>(w), joins, nullptr, nullptr, mass, err, s->n_groups, s->heads_per_group, s->max_ctx,
                 nb_cap(s), kslots(s), batch * s->n_groups};
   if (mass) {
     a.stats = reinterpret_cast<float2*>(stats);

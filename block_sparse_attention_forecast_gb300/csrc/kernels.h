@@ -221,6 +221,7 @@ struct Kv4AttnArgs {
   float* part_o;                 // workspace [kKv4MaxCtas, 2, 16, d]
   float* part_ml;                // workspace [kKv4MaxCtas, 2, 2, 16]
   unsigned* counters;            // workspace [max_batch*G], zero between calls
+  unsigned* join_counters;       // workspace [kKv4MaxCtas, 2], zero between calls
   float2* stats;                 // block mass: (max, sum) [B*G, slots, parts, 16]; nullptr: not wanted
   float* ml;                     // block mass: final max and sum [B*G, 2, 16]
   float* mass;                   // [max_batch, G, nb_cap]: added to by the cluster form itself

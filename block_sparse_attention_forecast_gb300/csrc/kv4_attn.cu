@@ -7,19 +7,19 @@
 // a warp issues 293 instructions, 32 of them products. A product occupies the tensor pipe for 8.2
 // cycles and its operands' expansion the issue port for 8.7, but the two only half overlap (13.5
 // cycles together), so the instructions bound a long cache, not the memory: batch 16 of 131072 tokens
-// (671 MB) takes 147 us, and 137 us when every copy hits the same block in L2. A tcgen05 form, whose
+// (671 MB) takes 144 us, and 137 us when every copy hits the same block in L2. A tcgen05 form, whose
 // expanded operands go through tensor memory, took 240 us. With at most 8 heads (kEight) the roles
 // change: the cache is the A operand, 16 tokens or 16 channels of it, the heads are the N dimension,
-// and half the products do: the same batch with 8 heads takes 117 us, 0.84 of the memory's rate
+// and half the products do: the same batch with 8 heads takes 116 us, 0.85 of the memory's rate
 // (147 with the heads as M). A score tile's 8 x 8 weights are transposed between lanes on the way.
 //
 // Work, three forms chosen by launch_kv4_attn:
 //   - few blocks per (sequence, group): one thread-block cluster each, the blocks split evenly over
 //     its CTAs, results joined in distributed shared memory; no plan, no workspace;
 //   - else the blocks of all (sequence, group)s in a row, U of them, cut into one contiguous range
-//     per CTA, balanced to one block whatever the lengths. Every CTA finds its range itself from seq_len
+//     per CTA, of equal cost whatever the lengths. Every CTA finds its range itself from seq_len
 //     or cnt (a prefix sum over the groups), since the lengths live on the device. A group's CTAs
-//     leave partial results in a workspace, and the last to arrive joins them;
+//     leave partial results in a workspace, and the last to arrive joins them, always in the same order;
 //   - with more (sequence, group)s than the prefix sums hold, whole groups per CTA, in turn.
 // Whole blocks (10 KiB, one bulk copy each) go through a ring of 16 stages in shared memory: lane l of the
 // producer warp fills stage l whenever it is free, so all stages are polled at once and no free one
@@ -76,10 +76,17 @@ constexpr int kClusterSmem4 = kSmem4 + kRecv4 * (kHeadDim + 2) * 4;
 //                   sequence: 6.8 us instead of 12.5; of 16 sequences: 8.4 instead of 14.8.
 //   kMinUnits       blocks per CTA below which fewer CTAs work; 1, 2 and 4 measured alike, and 2 halves
 //                   the CTAs that a small call occupies.
+//   kPieceWhole     what beginning a group costs a CTA of the planned form (its warps drain, join and start
+//   kPieceSplit     again), in blocks, with whole blocks per warp and with four warps per block. 8 x 8
+//                   groups of 64 to 128 blocks, 4 heads: 24.5 us at 0, 22.6 at 14, 23.5 at 28; 400 groups of 6
+//                   blocks: 24.9 at 0, 21.3 at 7, 21.0 at 14.
+//   kJoin           CTAs that join their results at once; those of a longer group join in two levels. One sequence
+//                   of 131072 tokens (76 CTAs per group): 24.3 us at 4, 23.7 at 8, 24.2 at 16, 32.4 at once.
 //   kPlanMax        (sequence, group)s of the balanced plan, held in 4 KiB of shared memory; beyond it there
 //                   are at least six per SM, and whole groups balance well enough.
 constexpr int kWholeBlocks = 2;
-constexpr int kPieceWhole = 10, kPieceSplit = 4;
+constexpr int kPieceWhole = 14, kPieceSplit = 8;
+constexpr int kJoin = 8;
 constexpr int kPairBlocks = 6;
 constexpr int kClusterBlocks = 24;
 constexpr int kMinUnits = 2;
@@ -380,7 +387,6 @@ __global__ void __launch_bounds__(kThreads4, 1) kv4_attn_kernel(const Kv4AttnArg
   const float sl2 = 1.4426950408889634f * 0.08838834764831845f;   // log2(e) / sqrt(128)
   int it = 0;
   bool ok = true;             // a wait that ran out: no further compute, the barriers stay matched
-  bool first_piece = true;
   const uint32_t masks_at = smem_addr(s_flag) + 4;
   const Masks mk{lds32(masks_at), lds32(masks_at + 4), lds32(masks_at + 8)};
   const uint32_t ring_at = smem_addr(ring), live_at = smem_addr(stage_live);
@@ -671,10 +677,10 @@ __global__ void __launch_bounds__(kThreads4, 1) kv4_attn_kernel(const Kv4AttnArg
         }
       }
     } else if (p.n_cta > 1) {
-      // a CTA's partial of its first piece lies in slot 0, of its last in slot 1; a piece that is
-      // neither covers its group alone
-      const int slot = c * 2 + (first_piece ? 0 : 1);
-      {
+      // A CTA's partial of its first piece lies in slot 0, of its last in slot 1; a piece that is
+      // neither covers its group alone. The group's first CTA left its partial in slot 1 unless the
+      // group begins that CTA's range; all others in slot 0.
+      const auto store_partial = [&](int slot) {
         float4* po = reinterpret_cast<float4*>(a.part_o + ((size_t)slot * kHeads + h) * kHeadDim + d0);
         po[0] = make_float4(acc[0], acc[1], acc[2], acc[3]);
         po[1] = make_float4(acc[4], acc[5], acc[6], acc[7]);
@@ -682,34 +688,34 @@ __global__ void __launch_bounds__(kThreads4, 1) kv4_attn_kernel(const Kv4AttnArg
           a.part_ml[slot * 2 * kHeads + h] = M;
           a.part_ml[slot * 2 * kHeads + kHeads + h] = L;
         }
-      }
-      sync_consumers();                        // every consumer's partial stores are issued
-      if (t == 0) {
-        unsigned prev;
-        asm volatile("atom.acq_rel.gpu.global.add.u32 %0, [%1], 1;" : "=r"(prev) : "l"(a.counters + p.bg) : "memory");
-        *s_flag = prev == (unsigned)(p.n_cta - 1);
-        if (*s_flag) a.counters[p.bg] = 0u;
-      }
-      sync_consumers();
-      write = *s_flag != 0;
-      if (write) {
-        // the last CTA of the group joins the partials. The group's first CTA left its partial in
-        // slot 1 unless the group begins that CTA's range; all others in slot 0.
-        const int g0 = s_pre[p.bg];
-        int at;
-        const int first_slot = p.first * 2 + (cut(p.first, at) == g0 ? 0 : 1);
+      };
+      int at;
+      const int first_slot = p.first * 2 + (cut(p.first, at) == s_pre[p.bg] ? 0 : 1);
+      const auto slot_of = [&](int k) { return k == 0 ? first_slot : (p.first + k) * 2; };
+      // Counts this CTA in; the last of n joins the partials of the group's CTAs k0, k0 + step, ... (n of
+      // them, always in this order) into (M, L, acc) and returns true.
+      const auto join = [&](unsigned* counter, int n, int k0, int step) -> bool {
+        sync_consumers();                      // every consumer's partial stores are issued
+        if (t == 0) {
+          unsigned prev;
+          asm volatile("atom.acq_rel.gpu.global.add.u32 %0, [%1], 1;" : "=r"(prev) : "l"(counter) : "memory");
+          *s_flag = prev == (unsigned)(n - 1);
+          if (*s_flag) *counter = 0u;
+        }
+        sync_consumers();
+        if (*s_flag == 0) return false;
         M = kLowest;
         L = 0.f;
 #pragma unroll
         for (int e = 0; e < 8; ++e) acc[e] = 0.f;
         constexpr int kFlight = 4;
-        for (int q0 = 0; q0 < p.n_cta; q0 += kFlight) {
+        for (int q0 = 0; q0 < n; q0 += kFlight) {
           float pm[kFlight], pl[kFlight];
           float4 px[kFlight][2];
 #pragma unroll
           for (int q = 0; q < kFlight; ++q) {
-            const bool in = q0 + q < p.n_cta;
-            const int sl = q0 + q == 0 || !in ? first_slot : (p.first + q0 + q) * 2;
+            const bool in = q0 + q < n;
+            const int sl = slot_of(in ? k0 + (q0 + q) * step : k0);
             pm[q] = in ? __ldcg(a.part_ml + sl * 2 * kHeads + h) : kLowest;
             pl[q] = __ldcg(a.part_ml + sl * 2 * kHeads + kHeads + h);
             const float4* src = reinterpret_cast<const float4*>(a.part_o + ((size_t)sl * kHeads + h) * kHeadDim + d0);
@@ -726,7 +732,7 @@ __global__ void __launch_bounds__(kThreads4, 1) kv4_attn_kernel(const Kv4AttnArg
 #pragma unroll
           for (int q = 0; q < kFlight; ++q) {
             const float wt = fast_exp2(pm[q] - Mn);
-            if (q0 + q < p.n_cta) {
+            if (q0 + q < n) {
               L += wt * pl[q];
               acc[0] += wt * px[q][0].x; acc[1] += wt * px[q][0].y; acc[2] += wt * px[q][0].z; acc[3] += wt * px[q][0].w;
               acc[4] += wt * px[q][1].x; acc[5] += wt * px[q][1].y; acc[6] += wt * px[q][1].z; acc[7] += wt * px[q][1].w;
@@ -734,6 +740,17 @@ __global__ void __launch_bounds__(kThreads4, 1) kv4_attn_kernel(const Kv4AttnArg
           }
           M = Mn;
         }
+        return true;
+      };
+      // Up to kJoin CTAs join at once; a group of more in two levels, kJoin neighbours first, whose result takes
+      // the first one's slot.
+      const int k = c - p.first, lead = k - k % kJoin;
+      store_partial(slot_of(k));
+      write = join(a.join_counters + slot_of(lead), min(kJoin, p.n_cta - lead), lead, 1);
+      if (write && p.n_cta > kJoin) {
+        __syncwarp();                          // the head's M and L have been read by its 16 threads
+        store_partial(slot_of(lead));
+        write = join(a.counters + p.bg, (p.n_cta + kJoin - 1) / kJoin, 0, kJoin);
       }
     }
     if (write) {
@@ -756,7 +773,6 @@ __global__ void __launch_bounds__(kThreads4, 1) kv4_attn_kernel(const Kv4AttnArg
         *reinterpret_cast<uint4*>(a.out + ((size_t)p.bg * a.H + h) * kHeadDim + d0) = make_uint4(pk[0], pk[1], pk[2], pk[3]);
       }
     }
-    first_piece = false;
     if constexpr (kCluster && kStats) {
       const SlotBlocks list = slot_blocks(a.idx ? a.idx + (size_t)p.bg * a.kslots : nullptr, n0);
       const int tb = (a.seq_len[p.bg / a.G] - 1) / kBlock;

@@ -573,3 +573,23 @@ def test_mass_of_repeated_blocks_is_reproducible(sb, fmt, B, topk):
                 want[j] += x
                 bound[j] += tol * x + 2.0 ** -22 * want[j]
             assert (np.abs(masses[0][b, g].cpu().double().numpy() - want) <= bound).all()
+
+
+def test_attention_joins_of_many_ctas(sb):
+    """Groups that spread over more CTAs than join at once, beside short ones: exact, the same bits in every
+    call, and every counter of the workspace left at zero."""
+    T_list = [40000, 64, 1, 20000]
+    shape = sb.Shape(n_groups=1, heads_per_group=7, max_ctx=40000, max_batch=4)
+    K, V = _kv(shape, 95)
+    layer = _filled(sb, shape, K, V, T_list)
+    q = synth.normal_bf16((4, 7, 128), 96)
+    _check_attention(sb, shape, layer, K, V, T_list, q, None, None, mass=True)
+    ws = sb.workspace(shape, 4, sb.WS_KV4_ATTN)
+    outs = []
+    for _ in range(8):
+        outs.append(torch.zeros((4, 7, 128), dtype=torch.bfloat16, device="cuda"))
+        sb.sparda_kv4_decode_attn(shape, layer, q.cuda(), None, None, _i32(T_list), 4, outs[-1], ws)
+    torch.cuda.synchronize()
+    assert all(torch.equal(o, outs[0]) for o in outs[1:])
+    assert (ws[:256 + 1280] == 0).all()              # the counters lie before the partial results
+    assert sb.sparda_device_error(clear=True) == 0
