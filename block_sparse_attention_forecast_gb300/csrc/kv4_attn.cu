@@ -134,9 +134,8 @@ __device__ __forceinline__ int mcol(int c) { return c + 4 * (c >> 5); }
 
 // Blocks of (sequence, group) bg.
 __device__ __forceinline__ int group_blocks(const Kv4AttnArgs& a, int bg, int T) {
-  if (T < 1 || T > a.max_ctx) return 0;
-  const int tb = (T - 1) / kBlock;
-  return a.idx ? min(max(a.cnt[bg], 0), a.kslots) : tb + 1;
+  const int n = a.idx ? min(max(a.cnt[bg], 0), a.kslots) : (T - 1) / kBlock + 1;    // loaded beside T
+  return T < 1 || T > a.max_ctx ? 0 : n;
 }
 
 // Shared-memory loads by 32-bit address: through pointers into the aligned ring the compiler
@@ -206,6 +205,17 @@ __global__ void __launch_bounds__(kThreads4, 1) kv4_attn_kernel(const Kv4AttnArg
     s_flag[2] = (int)m.lo;
     s_flag[3] = (int)m.hi;
   }
+  // A group's queries as A fragments, rows g and g + 8: K step 2 w + i takes channels 32 cq + 8 w + 4 i ..
+  // They are put together in shared memory and loaded as quadruples: built in registers, they would be
+  // moved into place again in every step.
+  const auto stage_queries = [&](int bg, int w) {
+    const int g = lane >> 2, cq = lane & 3;
+    const uint4* q0 = reinterpret_cast<const uint4*>(a.q + ((size_t)bg * a.H + g) * kHeadDim + 32 * cq);
+    const uint4 none = make_uint4(0, 0, 0, 0);
+    const uint4 x = g < a.H ? q0[w] : none, y = g + 8 < a.H ? q0[w + 8 * (kHeadDim / 8)] : none;
+    s_q[(2 * w) * 32 + lane] = make_uint4(x.x, y.x, x.y, y.y);
+    s_q[(2 * w + 1) * 32 + lane] = make_uint4(x.z, y.z, x.w, y.w);
+  };
   if constexpr (kCluster) cluster_arrive();       // waited for before the first write to another CTA's memory
   grid_dep_wait();
   grid_dep_launch();
@@ -214,7 +224,7 @@ __global__ void __launch_bounds__(kThreads4, 1) kv4_attn_kernel(const Kv4AttnArg
   const bool balanced = !kCluster && a.bg_count <= kPlanMax;
   // The CTAs' ranges are equal in cost: a block counts 1, a group's beginning kPiece more. Block u of the
   // row, of group bg, then begins at cost u + kPiece (bg + 1).
-  int U = 0, V = 0, ctas = gridDim.x, u0 = 0, u1 = 0, n0 = 0, w_bg = 0;
+  int U = 0, V = 0, ctas = gridDim.x, u0 = 0, u1 = 0, n0 = 0, w_bg = 0, T0 = 0;
   // the first block of CTA i's range, and (bg) a group at or before its
   const auto cut = [&](int i, int& bg) {
     const int v = (int)((long long)V * i / ctas);
@@ -234,10 +244,15 @@ __global__ void __launch_bounds__(kThreads4, 1) kv4_attn_kernel(const Kv4AttnArg
   };
   if constexpr (kCluster) {
     const int bg = blockIdx.x / cluster, rank = blockIdx.x % cluster;
+    // the length, the list and the queries at once: one round trip to memory
     const int T = a.seq_len[bg / a.G];
+    const int j = a.idx && tid < a.kslots ? a.idx[(size_t)bg * a.kslots + tid] : 0;
+    if (warp < 4) stage_queries(bg, warp);
     n0 = group_blocks(a, bg, T);
+    s_pre[tid] = j;
     u0 = n0 * rank / cluster;
     u1 = n0 * (rank + 1) / cluster;
+    T0 = T;
     if ((T < 1 || T > a.max_ctx) && rank == 0 && tid == 0) atomicOr(a.err, SPARDA_DEV_BAD_SEQ_LEN);
     __syncthreads();                               // the barriers are initialised
   } else if (balanced) {
@@ -343,8 +358,8 @@ __global__ void __launch_bounds__(kThreads4, 1) kv4_attn_kernel(const Kv4AttnArg
           if (!balanced && bg >= a.bg_count) return false;
           n = balanced ? s_pre[bg + 1] - s_pre[bg] : group_blocks(a, bg, a.seq_len[bg / a.G]);
         }
-        int j = a.idx ? a.idx[(size_t)bg * a.kslots + s] : s;
-        const int T = a.seq_len[bg / a.G];
+        int j = !a.idx ? s : kCluster ? s_pre[s] : a.idx[(size_t)bg * a.kslots + s];
+        const int T = kCluster ? T0 : a.seq_len[bg / a.G];
         if ((unsigned)j > (unsigned)((T - 1) / kBlock)) {
           atomicOr(a.err, SPARDA_DEV_BAD_INDEX);     // skipped: block 0 is staged with no live token
           j = 0;
@@ -399,22 +414,13 @@ __global__ void __launch_bounds__(kThreads4, 1) kv4_attn_kernel(const Kv4AttnArg
     float o[kAcc][4];
 #pragma unroll
     for (int n = 0; n < kAcc; ++n) o[n][0] = o[n][1] = o[n][2] = o[n][3] = 0.f;
-    // A fragments, rows g and g + 8: K step 2 w + i takes channels 32 cq + 8 w + 4 i .. They are put
-    // together in shared memory and loaded as quadruples: built in registers, they would be moved
-    // into place again in every step. Every warp writes the same values before it reads them.
     uint4 qf[8];
-    {
-      const uint4* q0 = reinterpret_cast<const uint4*>(a.q + ((size_t)p.bg * a.H + g) * kHeadDim + 32 * cq);
-      const uint4 none = make_uint4(0, 0, 0, 0);
+    if constexpr (!kCluster) {                     // every warp writes the same values before it reads them
 #pragma unroll
-      for (int w = 0; w < 4; ++w) {
-        const uint4 x = g < a.H ? q0[w] : none, y = g + 8 < a.H ? q0[w + 8 * (kHeadDim / 8)] : none;
-        s_q[(2 * w) * 32 + lane] = make_uint4(x.x, y.x, x.y, y.y);
-        s_q[(2 * w + 1) * 32 + lane] = make_uint4(x.z, y.z, x.w, y.w);
-      }
-#pragma unroll
-      for (int w = 0; w < 8; ++w) qf[w] = lds128(smem_addr(s_q + w * 32 + lane));
+      for (int w = 0; w < 4; ++w) stage_queries(p.bg, w);
     }
+#pragma unroll
+    for (int w = 0; w < 8; ++w) qf[w] = lds128(smem_addr(s_q + w * 32 + lane));
     // this group's blocks of the piece: its ring stages come round every kBlockGroups
     int skip = grp - it % kBlockGroups;
     if (skip < 0) skip += kBlockGroups;
@@ -774,8 +780,8 @@ __global__ void __launch_bounds__(kThreads4, 1) kv4_attn_kernel(const Kv4AttnArg
       }
     }
     if constexpr (kCluster && kStats) {
-      const SlotBlocks list = slot_blocks(a.idx ? a.idx + (size_t)p.bg * a.kslots : nullptr, n0);
-      const int tb = (a.seq_len[p.bg / a.G] - 1) / kBlock;
+      const SlotBlocks list = slot_blocks(a.idx ? s_pre : nullptr, n0);
+      const int tb = (T0 - 1) / kBlock;
       const int slots = a.idx ? a.kslots : a.nb_cap;
       cluster_sync();                          // (mM and mL were last read before the first one)
       const float Mh = mM[lane & 15], Lh = mL[lane & 15];
