@@ -14,8 +14,9 @@
 // (147 with the heads as M). A score tile's 8 x 8 weights are transposed between lanes on the way.
 //
 // Work, three forms chosen by launch_kv4_attn:
-//   - few blocks per (sequence, group): one thread-block cluster each, the blocks split evenly over
-//     its CTAs, results joined in distributed shared memory; no plan, no workspace;
+//   - few blocks per (sequence, group): one thread-block cluster each (of one CTA where there are more
+//     groups than SMs), the blocks split evenly over its CTAs, results joined in distributed shared
+//     memory; no plan, no workspace;
 //   - else the blocks of all (sequence, group)s in a row, U of them, cut into one contiguous range
 //     per CTA, of equal cost whatever the lengths. Every CTA finds its range itself from seq_len
 //     or cnt (a prefix sum over the groups), since the lengths live on the device. A group's CTAs
@@ -72,22 +73,28 @@ constexpr int kClusterSmem4 = kSmem4 + kRecv4 * (kHeadDim + 2) * 4;
 //   kPairBlocks     blocks per CTA of a cluster above which two warps share a block, not four. 34 blocks in
 //                   clusters of 4 (8.5 per CTA): kW 2 8.45 us, 4 8.8, with 8 heads 7.4, 7.57; clusters
 //                   of 8 (4.25 per CTA): 7.04, 6.95.
-//   kClusterBlocks  blocks per CTA up to which groups get clusters. Against the planned form, 34 blocks of one
-//                   sequence: 6.8 us instead of 12.5; of 16 sequences: 8.4 instead of 14.8.
+//   kCtaCost        what a CTA of the cluster form costs beside its blocks, and the planned form beside its
+//   kPlanCost       share of blocks and beginnings, in blocks. With them the cheaper form is the one measured
+//                   faster at (groups, blocks, clusters vs plan in us, 16 heads): (2, 34) 6.8, 12.5; (32, 34)
+//                   8.4, 14.8; (140, 34) 17.5, 26.2; (160, 16) 17.9, 19.0; (160, 34) 30.2, 27.8; (200, 24)
+//                   24.6, 27.5; (200, 34) 31.2, 31.3; (200, 64) 49, 44; (400, 6) 18.7, 20.8; (600, 34) 64, 71;
+//                   (600, 64) 95, 104.
+//   kClusterBlocks  blocks per CTA up to which groups get clusters where no list bounds them: above, the
+//                   plan's balance over ragged lengths counts for more.
 //   kMinUnits       blocks per CTA below which fewer CTAs work; 1, 2 and 4 measured alike, and 2 halves
 //                   the CTAs that a small call occupies.
-//   kPieceWhole     what beginning a group costs a CTA of the planned form (its warps drain, join and start
-//   kPieceSplit     again), in blocks, with whole blocks per warp and with four warps per block. 8 x 8
-//                   groups of 64 to 128 blocks, 4 heads: 24.5 us at 0, 22.6 at 14, 23.5 at 28; 400 groups of 6
-//                   blocks: 24.9 at 0, 21.3 at 7, 21.0 at 14.
+//   kPiece          what beginning a group costs a CTA of the planned form (its warps drain, join and start
+//                   again), in blocks. 8 x 8 groups of 64 to 128 blocks, 4 heads: 24.5 us at 0, 22.6 at 14,
+//                   23.5 at 28; 200 groups of 34 blocks: 34.5, 30.6, 31.8.
 //   kJoin           CTAs that join their results at once; those of a longer group join in two levels. One sequence
 //                   of 131072 tokens (76 CTAs per group): 24.3 us at 4, 23.7 at 8, 24.2 at 16, 32.4 at once.
 //   kPlanMax        (sequence, group)s of the balanced plan, held in 4 KiB of shared memory; beyond it there
 //                   are at least six per SM, and whole groups balance well enough.
 constexpr int kWholeBlocks = 2;
-constexpr int kPieceWhole = 14, kPieceSplit = 8;
+constexpr int kPiece = 14;
 constexpr int kJoin = 8;
 constexpr int kPairBlocks = 6;
+constexpr int kCtaCost = 8, kPlanCost = 20;
 constexpr int kClusterBlocks = 24;
 constexpr int kMinUnits = 2;
 constexpr float kPShift = 6.f;                              // weights are scaled by 2^kPShift
@@ -189,7 +196,6 @@ __global__ void __launch_bounds__(kThreads4, 1) kv4_attn_kernel(const Kv4AttnArg
   constexpr int kBlockGroups = kCWarps / kW;     // blocks in the consumers' hands at a time
   constexpr int kTiles = kW == 4 ? 2 : 4;        // 8-token tiles of a step
   constexpr int kSteps = 8 / kW / kTiles;        // steps of a warp per block
-  constexpr int kPiece = kW == 1 ? kPieceWhole : kPieceSplit;
   constexpr int kAcc = kEight ? 8 : 16;          // accumulators of 16 heads x 8 channels, or of 16 channels x 8 heads
   static_assert(kRing % kBlockGroups == 0, "each ring stage must belong to one group of consumers");
 
@@ -850,15 +856,22 @@ int launch_kv4_attn(const Kv4AttnArgs& a, cudaStream_t s) {
   const int sms = sm_count() < kKv4MaxCtas ? sm_count() : kKv4MaxCtas;
   const int slots = a.idx ? a.kslots : a.nb_cap;
   const long long bound = (long long)a.bg_count * slots;
-  // Few blocks per (sequence, group): one cluster each, when the clusters reach most SMs or have no
-  // use for more. Clusters stay within the SMs, so that they all run at once.
-  int cluster = a.bg_count <= sms ? sms / a.bg_count : 0;
+  // One cluster per (sequence, group), or the plan: whichever the costs below favour. Clusters fill the SMs
+  // at most once, or are single CTAs that come in waves.
+  int cluster = a.bg_count <= sms ? sms / a.bg_count : 1;
   if (cluster > kMaxCluster4) cluster = kMaxCluster4;
   const int useful = (slots + kMinUnits - 1) / kMinUnits;
   if (cluster > useful) cluster = useful;
-  if (cluster >= 1 && slots <= kClusterBlocks * cluster)
-    return slots > kPairBlocks * cluster ? launch_form<2, true>(a, cluster * a.bg_count, cluster, s)
-                                         : launch_form<4, true>(a, cluster * a.bg_count, cluster, s);
+  const int share = (slots + cluster - 1) / cluster;
+  const long long waves = ((long long)a.bg_count * cluster + sms - 1) / sms;
+  const long long planned = (long long)a.bg_count * (slots + kPiece) / sms + kPlanCost;
+  // Without a list, slots is the capacity: sequences may be far shorter, which the plan takes into account.
+  if ((a.idx || share <= kClusterBlocks) && waves * (share + kCtaCost) <= planned) {
+    const int ctas = cluster * a.bg_count;
+    return share > kWholeBlocks * kCWarps ? launch_form<1, true>(a, ctas, cluster, s)
+           : share > kPairBlocks          ? launch_form<2, true>(a, ctas, cluster, s)
+                                          : launch_form<4, true>(a, ctas, cluster, s);
+  }
   int grid = sms;
   const long long want = a.bg_count <= kPlanMax ? (bound + kMinUnits - 1) / kMinUnits : a.bg_count;
   if (want < grid) grid = (int)want;

@@ -593,3 +593,50 @@ def test_attention_joins_of_many_ctas(sb):
     assert all(torch.equal(o, outs[0]) for o in outs[1:])
     assert (ws[:256 + 1280] == 0).all()              # the counters lie before the partial results
     assert sb.sparda_device_error(clear=True) == 0
+
+
+@pytest.mark.parametrize("mass", [False, True])
+@pytest.mark.parametrize("T_list,G,H,ctx,topk", [
+    ([2200] * 70, 2, 16, 2240, 32),                # one CTA per group, whole blocks per warp
+    ([1500, 90] * 40, 2, 5, 1536, 32),             # more groups than SMs, many blocks each: ranges over groups
+    ([1400] * 100, 2, 8, 1408, 9),                 # more groups than SMs, few blocks each
+    ([20000, 13000], 1, 16, 20032, 0),             # few groups, several warps per block
+    ([20000, 13000], 1, 6, 20032, 0),
+])
+def test_attention_forms(sb, T_list, G, H, ctx, topk, mass):
+    B = len(T_list)
+    shape = sb.Shape(n_groups=G, heads_per_group=H, max_ctx=ctx, max_batch=B + 1, topk=max(1, topk))
+    K, V = _kv(shape, 97)
+    layer = _filled(sb, shape, K, V, T_list)
+    q = synth.normal_bf16((B, G * H, 128), 98)
+    idx = cnt = None
+    if topk:
+        idx, cnt = _select(np.random.default_rng(99), T_list, G, topk)
+    _check_attention(sb, shape, layer, K, V, T_list, q, idx, cnt, mass=mass)
+
+
+def test_attention_whole_groups_of_long_caches(sb):
+    """More groups than the plan holds, in caches of more blocks than a cluster takes: whole groups per CTA."""
+    B, ctx = 530, 1600
+    shape = sb.Shape(n_groups=2, heads_per_group=9, max_ctx=ctx, max_batch=B)
+    small = sb.Shape(n_groups=2, heads_per_group=9, max_ctx=ctx, max_batch=5)
+    K, V = _kv(small, 101)
+    T_list = [ctx if b % 97 == 0 else 1 + (37 * b) % 300 for b in range(B)]
+    rep = [b % 5 for b in range(B)]
+    layer = sb.LayerKV4.empty(shape)
+    layer.kv.fill_(0xff)
+    sb.sparda_kv4_quantize(shape, layer, K.cuda()[rep], V.cuda()[rep], _i32(T_list), B)
+    q = synth.normal_bf16((B, 18, 128), 102)
+    out = torch.empty((B, 18, 128), dtype=torch.bfloat16, device="cuda")
+    mass = torch.zeros((B, 2, ctx // 64), device="cuda")
+    ws = sb.workspace(shape, B, sb.WS_KV4_ATTN_MASS)
+    sb.sparda_kv4_decode_attn(shape, layer, q.cuda(), None, None, _i32(T_list), B, out, ws, mass=mass)
+    torch.cuda.synchronize()
+    assert sb.sparda_device_error(clear=True) == 0
+    k64, v64 = R.grid_values(K, True), _v16(V)
+    for b in list(range(0, B, 23)) + [97, 194, B - 1]:
+        for g in range(2):
+            ref, tol, w, wtol = R.attention(to64(q)[b, 9 * g:9 * g + 9], k64[rep[b], g], v64[rep[b], g], None, T_list[b], W16)
+            assert (np.abs(to64(out)[b, 9 * g:9 * g + 9] - ref) <= tol).all(), b
+            got = mass[b, g].cpu().double().numpy()
+            assert (np.abs(got[:len(w)] - w) <= wtol * w + 2.0 ** -22 * w).all() and (got[len(w):] == 0).all()
