@@ -199,9 +199,19 @@ class Shape:
     def __setattr__(self, name, value):
         self.__dict__[name] = value
         self.__dict__.pop("_ref", None)
+        self.__dict__.pop("_kv4_sizes", None)
 
     def __getstate__(self):
-        return {k: v for k, v in self.__dict__.items() if k != "_ref"}
+        return {k: v for k, v in self.__dict__.items() if k not in ("_ref", "_kv4_sizes")}
+
+    def kv4_sizes(self):
+        """(bytes of a LayerKV4's kv, elements of its ck), kept until a field changes."""
+        r = self.__dict__.get("_kv4_sizes")
+        if r is None:
+            rows = self.max_batch * self.n_groups
+            r = self.__dict__["_kv4_sizes"] = (rows * (self.max_ctx // BLOCK) * KV4_BLOCK_BYTES,
+                                               rows * num_windows(self.max_ctx) * self.head_dim)
+        return r
 
     def ref(self):
         """A pointer to c(), kept until a field changes."""
@@ -562,15 +572,17 @@ def _kv4_layer(shape, layer):
     """(device, pointer to the C layer) of a LayerKV4, its tensors checked. The C struct is kept with the
     layer until one of its fields is set; the tensors' sizes and addresses are checked in every call."""
     kv, ck = layer.kv, layer.ck
-    dev = _cache_device(kv)
-    rows = shape.max_batch * shape.n_groups
-    n_kv, n_ck = rows * (shape.max_ctx // BLOCK) * KV4_BLOCK_BYTES, rows * num_windows(shape.max_ctx) * shape.head_dim
+    dev = kv.get_device()
+    if dev < 0 or dev != _current_device():
+        _cache_device(kv)                            # raises
+    n_kv, n_ck = shape.kv4_sizes()
     args = layer.__dict__.get("_args")
-    if args is not None and args[0] == (kv.data_ptr(), ck.data_ptr()) and kv.numel() >= n_kv and ck.numel() >= n_ck:
-        return dev, args[1]
+    if (args is not None and args[0] == kv.data_ptr() and args[1] == ck.data_ptr() and kv.numel() >= n_kv and
+            ck.numel() >= n_ck):
+        return dev, args[2]
     c = c_layer_kv4(_checked("kv", kv, torch.uint8, n_kv, dev), _checked("ck", ck, torch.bfloat16, n_ck, dev))
     ref = ctypes.byref(c)
-    layer.__dict__["_args"] = ((c.kv, c.ck), ref)
+    layer.__dict__["_args"] = (c.kv, c.ck, ref)
     return dev, ref
 
 

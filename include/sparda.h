@@ -695,7 +695,7 @@ int32_t sparda_sparse_decode_attn_mass(const sparda_shape* shape, const sparda_l
  * its length is copied) and sets SPARDA_DEV_BAD_SEQ_LEN. Sequences at and past batch stay as they were.
  *
  * SPARDA_ERR_INVALID_ARG: an offloaded layer, recent < 1, keep <= recent, only some of the dst
- * arguments NULL, a dst buffer that is the source's. SPARDA_ERR_UNSUPPORTED_SHAPE: dst_shape too
+ * arguments NULL, dst memory that overlaps the source's. SPARDA_ERR_UNSUPPORTED_SHAPE: dst_shape too
  * small, other groups, or keep above 4096. Ordering: as sparda_compress_keys, the call must not be
  * the kernel just before a selection that scores this cache.
  */
