@@ -33,7 +33,13 @@ static_assert(kSelThreads / 32 <= 32, "a warp's lanes hold the warps' totals");
 constexpr int kSelPer = kMaxCtx / kBlock / kSelThreads;         // weights per thread: 8
 constexpr int kBins = 2048;
 constexpr int kMoveThreads = 256;
-constexpr int kMoveSmem = 96 * 1024;                            // a CTA's ring: 9 blocks of 10 KiB, 6 of 16 KiB
+// The move's ring slots per CTA, and the bytes of all CTAs' slots on an SM. Twice 32 KiB (bf16) or three times
+// 20 (4 bits) per SM is the fastest of rings from 16 to 192 KiB: more or fewer bytes in flight cost up to a
+// quarter, as DRAM switches between reading and writing.
+//   4096 blocks of bf16 keys and values, with the selection: 49.1 us; 54.4 with twice 96 KiB, 63 with once 32
+//   4096 blocks in 4 bits, with the selection and the reading back: 43.6 us; 45.1 with twice 32, 49.3 with twice 96
+constexpr int kMoveSlots = 2;
+constexpr int kMoveBytes = 64 * 1024;
 constexpr uint32_t kMovePolls = 1u << 25;                       // bounds a lane's wait to seconds
 constexpr int kShiftSmem = 220 * 1024;                          // two rounds of a CTA's blocks
 constexpr int kCkRow = kHeadDim * 2;                            // bytes of a compressed key
@@ -222,33 +228,31 @@ __global__ void __launch_bounds__(kSelThreads) evict_select_kernel(const EvictAr
 }
 
 // A fixed grid. Warp 0 moves whole blocks by bulk copies through a ring in shared memory: lane l owns a
-// slot of it and every (slots x CTAs)-th block, so a CTA has all its slots' reads in flight whatever its
-// registers. The other warps, 64 threads per kept block, move the compressed keys and form those of
-// windows that join blocks. (One CTA per kept block, its bytes through registers: 21.0 us instead of
-// 19.4 for 4096 blocks of a 4-bit cache, 41.5 instead of 40.1 for 4096 of bf16 keys and values.)
-__global__ void __launch_bounds__(kMoveThreads + 32) evict_move_kernel(const EvictArgs a, int slots) {
+// slot of it and every (slots x CTAs)-th block, so the reads in flight do not depend on registers. The
+// other warps, 64 threads per kept block, move the compressed keys and form those of windows that join blocks.
+__global__ void __launch_bounds__(kMoveThreads + 32) evict_move_kernel(const EvictArgs a) {
   extern __shared__ uint8_t smem_move[];
-  __shared__ alignas(8) uint64_t full[32];
+  __shared__ alignas(8) uint64_t full[kMoveSlots];
   const int tid = threadIdx.x, lane = tid & 31;
   const int n_kept = a.B * a.G * a.keep;
   if (tid < 32) {
-    if (lane < slots) mbar_init(&full[lane], 1);
+    if (lane < kMoveSlots) mbar_init(&full[lane], 1);
     fence_mbar_init();
     __syncwarp();
   }
   grid_dep_wait();
   grid_dep_launch();
   if (tid < 32) {
-    if (lane >= slots) return;
+    if (lane >= kMoveSlots) return;
     uint8_t* slot = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_move) + 127) & ~static_cast<uintptr_t>(127)) +
                     (size_t)lane * a.block_bytes;
-    int item = (int)blockIdx.x * slots + lane;     // (kept block, plane)
-    const int step = (int)gridDim.x * slots, items = n_kept * a.planes;
+    int item = (int)blockIdx.x * kMoveSlots + lane;     // one plane's kept blocks, then the other's
+    const int step = (int)gridDim.x * kMoveSlots, items = n_kept * a.planes;
     uint8_t* dst = nullptr;
     // issues the read of the lane's next block, if there is one
     const auto read_next = [&]() -> bool {
       for (; item < items; item += step) {
-        const int k = item / a.planes, p = item % a.planes, bg = k / a.keep, n = k % a.keep;
+        const int k = item % n_kept, p = item / n_kept, bg = k / a.keep, n = k % a.keep;
         const int j = a.kept[k];
         if (j < 0) continue;
         dst = a.dst[p] + ((size_t)bg * a.dst_nb + n) * a.block_bytes;
@@ -402,13 +406,10 @@ bool launch_evict(const EvictArgs& a, cudaStream_t s) {
   const unsigned bg = (unsigned)a.B * a.G;
   launch_pdl(evict_select_kernel, dim3(bg), dim3(kSelThreads), 0, s, a);
   if (!a.in_place) {
-    // two CTAs per SM
-    const int slots = kMoveSmem / a.block_bytes;
-    static SmemOptIn opt_in;
-    if (!opt_in.set(evict_move_kernel, kMoveSmem + 128)) return false;
-    const long long items = (long long)bg * a.keep * a.planes, ctas = (items + slots - 1) / slots;
-    const int grid = (int)(ctas < 2 * sm_count() ? ctas : 2 * sm_count());
-    launch_pdl(evict_move_kernel, dim3(grid), dim3(kMoveThreads + 32), (size_t)slots * a.block_bytes + 128, s, a, slots);
+    const int ring = kMoveSlots * a.block_bytes;
+    const long long items = (long long)bg * a.keep * a.planes, ctas = (items + kMoveSlots - 1) / kMoveSlots;
+    const int most = kMoveBytes / ring * sm_count(), grid = (int)(ctas < most ? ctas : most);
+    launch_pdl(evict_move_kernel, dim3(grid), dim3(kMoveThreads + 32), (size_t)ring + 128, s, a);
     return true;
   }
   // as many CTAs per (sequence, group) as fill the SMs, up to a portable cluster of 8

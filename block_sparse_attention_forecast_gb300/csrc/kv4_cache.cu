@@ -151,7 +151,9 @@ __global__ void __launch_bounds__(kQThreads, 5) kv4_quantize_kernel(const Kv4Cac
 
 // One CTA per (sequence-group, slot): the block's values back as bf16, rows of the sequence only.
 // idx == nullptr: slot j is block j and rows go to a cache [.., max_ctx, 128]; otherwise the slot's
-// block is idx[slot] and rows go to a staging buffer [.., kslots, 64, 128].
+// block is idx[slot] and rows go to a staging buffer [.., kslots, 64, 128]. The rows, 3.2 times the
+// bytes read, are stored to be evicted first, so that they do not push out a cache that was just
+// written (128 blocks of 32 groups after their eviction: 49.0 us instead of 52.1, both calls).
 __global__ void __launch_bounds__(kQThreads) kv4_dequantize_kernel(const Kv4CacheArgs a) {
   __shared__ alignas(16) uint8_t blk[kBlockBytes4];
   grid_dep_wait();
@@ -189,8 +191,8 @@ __global__ void __launch_bounds__(kQThreads) kv4_dequantize_kernel(const Kv4Cach
     const uint32_t w = *reinterpret_cast<const uint32_t*>(blk + kKCodes + t * 64 + l16 * 4);
     const uint32_t sz = *reinterpret_cast<const uint32_t*>(blk + kKScales + t * 16 + (l16 >> 2) * 4);
     const uint32_t s2 = dup_lo(sz), z2 = dup_hi(sz);
-    k[t * 16 + l16] = make_uint4(key_pair(w, 0, s2, z2), key_pair(w, 1, s2, z2), key_pair(w, 2, s2, z2),
-                                 key_pair(w, 3, s2, z2));
+    __stcs(k + t * 16 + l16, make_uint4(key_pair(w, 0, s2, z2), key_pair(w, 1, s2, z2), key_pair(w, 2, s2, z2),
+                                        key_pair(w, 3, s2, z2)));
   }
 #pragma unroll
   for (int r = 0; r < kQRounds / 2; ++r) {         // a token pair of 8 channels per thread
@@ -207,8 +209,8 @@ __global__ void __launch_bounds__(kQThreads) kv4_dequantize_kernel(const Kv4Cach
       lo[i] = pack_bf16(c0.x, c1.x);
       hi[i] = pack_bf16(c0.y, c1.y);
     }
-    v[(2 * pair) * 16 + l16] = make_uint4(lo[0], lo[1], lo[2], lo[3]);
-    if (2 * pair + 1 < live) v[(2 * pair + 1) * 16 + l16] = make_uint4(hi[0], hi[1], hi[2], hi[3]);
+    __stcs(v + (2 * pair) * 16 + l16, make_uint4(lo[0], lo[1], lo[2], lo[3]));
+    if (2 * pair + 1 < live) __stcs(v + (2 * pair + 1) * 16 + l16, make_uint4(hi[0], hi[1], hi[2], hi[3]));
   }
 }
 
