@@ -8,12 +8,12 @@
 //                         is found digit by digit, three histograms at most, whatever the
 //                         weights' spread; of the keys tied there the lowest blocks are taken.
 //   evict_move_kernel     into another cache: bytes in, bytes out.
-//   evict_shift_kernel    in the cache itself: block n moves from kept[n] >= n, so a block may be
-//                         overwritten only once it has been read. One thread-block cluster per
-//                         (sequence, group) takes the kept blocks in rounds of a few blocks per CTA:
-//                         all of a round is read into shared memory, a cluster barrier, then it is
-//                         written. A round writes blocks below its end and later rounds read blocks
-//                         at or above it, so the next round's reads start before the barrier.
+//   evict_shift_kernel    in the cache itself: block n moves from kept[n] >= n, so its place may be
+//                         written only once the block that lay there, if it is kept, has been read.
+//                         That block is kept[m] == n for an m < n: the kept list carries a mark on
+//                         every block still to be read, whoever has read it clears the mark, and
+//                         block n's write waits for m's. One cooperative launch, blocks in the order
+//                         of n: the lowest one in flight never waits, so every wait ends.
 //   evict_join_kernel     after the shift: the compressed keys of windows that span two blocks
 //                         which were not neighbours before (the move kernel does its own).
 //   evict_length_kernel   after the shift: the new lengths, once nothing reads the old ones.
@@ -41,7 +41,9 @@ constexpr int kMoveThreads = 256;
 constexpr int kMoveSlots = 2;
 constexpr int kMoveBytes = 64 * 1024;
 constexpr uint32_t kMovePolls = 1u << 25;                       // bounds a lane's wait to seconds
-constexpr int kShiftSmem = 220 * 1024;                          // two rounds of a CTA's blocks
+constexpr uint32_t kShiftPolls = 1u << 22;                      // the same, each a round trip to L2
+constexpr int kShiftBytes = 72 * 1024;                          // shared memory of the shift's CTAs on an SM
+constexpr int kUnread = 1 << 30;                                // kept: a block that moves and has not been read
 constexpr int kCkRow = kHeadDim * 2;                            // bytes of a compressed key
 
 __device__ __forceinline__ bool valid_len(int T, int nb) { return T >= 1 && T <= nb * kBlock; }
@@ -217,7 +219,8 @@ __global__ void __launch_bounds__(kSelThreads) evict_select_kernel(const EvictAr
 #pragma unroll
   for (int i = 0; i < kSelPer; ++i)
     if (sel >> i & 1u) {
-      kept[at] = tid * kSelPer + i;
+      const int j = tid * kSelPer + i;
+      kept[at] = a.in_place && j != at ? j | kUnread : j;
       dst[at] = w[i];
       ++at;
     }
@@ -299,82 +302,69 @@ __global__ void __launch_bounds__(kMoveThreads + 32) evict_move_kernel(const Evi
   }
 }
 
-// One cluster of gridDim.x / (B*G) CTAs per (sequence, group), one warp each; lane 0 issues the
-// bulk copies. Shared memory: two rounds of `slots` blocks with their compressed keys.
-__global__ void __launch_bounds__(32) evict_shift_kernel(const EvictArgs a, int ctas, int slots) {
+// One warp per CTA, whose first lane moves one block at a time, with its compressed keys: its read, the mark, the
+// wait, its write. All CTAs are resident (a cooperative launch). Reads and writes of a block are each
+// whole before the next thing happens to its place, so no write meets a read of the same bytes.
+__global__ void __launch_bounds__(32) evict_shift_kernel(const EvictArgs a) {
   extern __shared__ uint8_t smem_shift[];
-  __shared__ alignas(8) uint64_t bar[2];
-  const int lane = threadIdx.x;
-  if (lane == 0) {
-    mbar_init(&bar[0], 1);
-    mbar_init(&bar[1], 1);
-    fence_mbar_init();
-  }
-  __syncwarp();
-  grid_dep_wait();
-  grid_dep_launch();
-  const int bg = blockIdx.x / ctas, rank = blockIdx.x % ctas;
-  const int T0 = a.src_len[bg / a.G];
-  const bool valid = valid_len(T0, a.src_nb);
-  const int count = valid ? min(blocks_of(T0), a.keep) : 0, T = valid ? kept_len(T0, a.keep) : 0;
-  const int32_t* kept = a.kept + (size_t)bg * a.keep;
-  uint8_t* base = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_shift) + 127) & ~static_cast<uintptr_t>(127));
-  const int slot_bytes = a.planes * a.block_bytes + 4 * kCkRow;
-  const int round = ctas * slots, rounds = (count + round - 1) / round;
-  // the block, its old place and its compressed-key bytes of slot i of this CTA in round r
-  struct Item { int n, j, ck; };
-  const auto item = [&](int r, int i) {
-    Item it{r * round + rank * slots + i, -1, 0};
-    if (it.n < count) {
-      it.j = kept[it.n];
-      const bool neighbour = it.n + 1 < count && kept[it.n + 1] == it.j + 1;
-      it.ck = window_bytes(it.n, count, T, neighbour);
-      if (it.j == it.n) it.j = -1;                 // already in place, with its windows
+  __shared__ alignas(8) uint64_t full;
+  if (threadIdx.x) return;
+  mbar_init(&full, 1);
+  fence_mbar_init();
+  uint8_t* slot = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_shift) + 127) & ~static_cast<uintptr_t>(127));
+  const int groups = a.B * a.G, items = groups * a.keep;
+  uint32_t phase = 0;
+  bool ok = true;                                  // until a wait runs out: then nothing more is moved, but
+  for (int item = blockIdx.x; item < items; item += gridDim.x) {
+    const int bg = item % groups, n = item / groups;
+    int32_t* kept = a.kept + (size_t)bg * a.keep;
+    const int v = kept[n];
+    if (v < 0 || !(v & kUnread)) continue;         // behind the last block, or already in place with its windows
+    const int j = v ^ kUnread;
+    if (!ok) {                                     // the marks go on being cleared, so that nobody waits for them
+      asm volatile("st.release.gpu.global.s32 [%0], %1;" ::"l"(kept + n), "r"(j) : "memory");
+      continue;
     }
-    return it;
-  };
-  const auto load = [&](int r) {
-    uint32_t bytes = 0;
-    for (int i = 0; i < slots; ++i) {
-      const Item it = item(r, i);
-      if (it.j >= 0) bytes += a.planes * a.block_bytes + it.ck;
+    const int T0 = a.src_len[bg / a.G];
+    const int T = kept_len(T0, a.keep), count = min(blocks_of(T0), a.keep);
+    const bool neighbour = n + 1 < count && (kept[n + 1] & ~kUnread) == j + 1;
+    const int ck = window_bytes(n, count, T, neighbour);
+    const size_t row = (size_t)bg * (4 * a.dst_nb - 1);
+    mbar_arrive_expect_tx(&full, a.planes * a.block_bytes + ck);
+    for (int p = 0; p < a.planes; ++p)
+      bulk_load(slot + p * a.block_bytes, a.dst[p] + ((size_t)bg * a.dst_nb + j) * a.block_bytes, a.block_bytes, &full);
+    if (ck) bulk_load(slot + a.planes * a.block_bytes, a.dst_ck + (row + 4 * j) * kHeadDim, ck, &full);
+    // meanwhile: the kept block that lies at n, kept[m] for an m < n (the list ascends, and kept[i] >= i)
+    int lo = 0, hi = n;
+    while (lo < hi) {
+      const int mid = (lo + hi) >> 1;
+      if ((kept[mid] & ~kUnread) < n) lo = mid + 1;
+      else hi = mid;
     }
-    mbar_arrive_expect_tx(&bar[r & 1], bytes);
-    for (int i = 0; i < slots; ++i) {
-      const Item it = item(r, i);
-      if (it.j < 0) continue;
-      uint8_t* s = base + ((r & 1) * slots + i) * slot_bytes;
-      for (int p = 0; p < a.planes; ++p)
-        bulk_load(s + p * a.block_bytes, a.dst[p] + ((size_t)bg * a.dst_nb + it.j) * a.block_bytes, a.block_bytes, &bar[r & 1]);
-      if (it.ck) bulk_load(s + a.planes * a.block_bytes, a.dst_ck + ((size_t)bg * (4 * a.dst_nb - 1) + 4 * it.j) * kHeadDim,
-                           it.ck, &bar[r & 1]);
-    }
-  };
-  bool ok = true;                                  // a wait that ran out: nothing more is written
-  if (lane == 0 && rounds > 0) load(0);
-  for (int r = 0; r < rounds; ++r) {
-    if (lane == 0) {
-      if (ok) ok = mbar_wait(&bar[r & 1], (r >> 1) & 1, a.err);
-      if (ok && r + 1 < rounds) {
-        bulk_wait_read<0>();                       // the other buffer's stores have left it
-        load(r + 1);
+    ok = mbar_wait(&full, phase, a.err);
+    phase ^= 1;
+    asm volatile("st.release.gpu.global.s32 [%0], %1;" ::"l"(kept + n), "r"(j) : "memory");
+    if (ok && lo < n && (kept[lo] & ~kUnread) == n) {
+      uint32_t polls = 0;
+      for (;;) {
+        int at;
+        asm volatile("ld.acquire.gpu.global.s32 %0, [%1];" : "=r"(at) : "l"(kept + lo) : "memory");
+        if (!(at & kUnread)) break;
+        if (++polls > kShiftPolls) {
+          atomicOr(a.err, SPARDA_DEV_WAIT_TIMEOUT);
+          ok = false;
+          break;
+        }
       }
     }
-    cluster_sync();                                // the round is in shared memory, everywhere
-    if (lane == 0 && ok) {
-      for (int i = 0; i < slots; ++i) {
-        const Item it = item(r, i);
-        if (it.j < 0) continue;
-        const uint8_t* s = base + ((r & 1) * slots + i) * slot_bytes;
-        for (int p = 0; p < a.planes; ++p)
-          bulk_store(a.dst[p] + ((size_t)bg * a.dst_nb + it.n) * a.block_bytes, s + p * a.block_bytes, a.block_bytes);
-        if (it.ck) bulk_store(a.dst_ck + ((size_t)bg * (4 * a.dst_nb - 1) + 4 * it.n) * kHeadDim, s + a.planes * a.block_bytes,
-                              it.ck);
-      }
-      bulk_commit();
-    }
+    if (!ok) continue;
+    for (int p = 0; p < a.planes; ++p)
+      bulk_store(a.dst[p] + ((size_t)bg * a.dst_nb + n) * a.block_bytes, slot + p * a.block_bytes, a.block_bytes);
+    if (ck) bulk_store(a.dst_ck + (row + 4 * n) * kHeadDim, slot + a.planes * a.block_bytes, ck);
+    bulk_commit();
+    bulk_wait_read<0>();                           // the slot may be filled again
   }
-  if (lane == 0) bulk_wait_all();
+  bulk_wait_all();
 }
 
 // Grid: (sequence, group) x groups of kept blocks, 64 threads per kept block.
@@ -412,29 +402,19 @@ bool launch_evict(const EvictArgs& a, cudaStream_t s) {
     launch_pdl(evict_move_kernel, dim3(grid), dim3(kMoveThreads + 32), (size_t)ring + 128, s, a);
     return true;
   }
-  // as many CTAs per (sequence, group) as fill the SMs, up to a portable cluster of 8
-  int ctas = 1;
-  while (ctas < 8 && 2 * ctas * (int)bg <= sm_count()) ctas *= 2;
-  const int slot_bytes = a.planes * a.block_bytes + 4 * kCkRow;
-  const int slots = kShiftSmem / (2 * slot_bytes);
-  const size_t smem = 128 + 2 * (size_t)slots * slot_bytes;
-  static SmemOptIn opt_in;
-  if (!opt_in.set(evict_shift_kernel, 128 + kShiftSmem)) return false;
+  const int smem = 128 + a.planes * a.block_bytes + 4 * kCkRow;
+  const long long items = (long long)bg * a.keep, most = kShiftBytes / smem * sm_count();
   cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3(bg * ctas);
+  cfg.gridDim = dim3((unsigned)(items < most ? items : most));
   cfg.blockDim = dim3(32);
   cfg.dynamicSmemBytes = smem;
   cfg.stream = s;
-  cudaLaunchAttribute attr[2];
-  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-  attr[0].val.programmaticStreamSerializationAllowed = 1;
-  attr[1].id = cudaLaunchAttributeClusterDimension;
-  attr[1].val.clusterDim.x = ctas;
-  attr[1].val.clusterDim.y = 1;
-  attr[1].val.clusterDim.z = 1;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeCooperative;
+  attr[0].val.cooperative = 1;
   cfg.attrs = attr;
-  cfg.numAttrs = 2;
-  cudaLaunchKernelEx(&cfg, evict_shift_kernel, a, ctas, slots);
+  cfg.numAttrs = 1;
+  if (cudaLaunchKernelEx(&cfg, evict_shift_kernel, a) != cudaSuccess) return false;
   launch_pdl(evict_join_kernel, dim3(bg * (unsigned)((a.keep + 3) / 4)), dim3(kMoveThreads), 0, s, a);
   launch_pdl(evict_length_kernel, dim3(1), dim3(256), 0, s, a);
   return true;
