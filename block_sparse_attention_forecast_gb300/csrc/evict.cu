@@ -42,7 +42,10 @@ constexpr int kMoveSlots = 2;
 constexpr int kMoveBytes = 64 * 1024;
 constexpr uint32_t kMovePolls = 1u << 25;                       // bounds a lane's wait to seconds
 constexpr uint32_t kShiftPolls = 1u << 22;                      // the same, each a round trip to L2
-constexpr int kShiftBytes = 72 * 1024;                          // shared memory of the shift's CTAs on an SM
+// Shared memory of the shift's CTAs on an SM, a block each. With the selection, 4 sequences of bf16 blocks to 512:
+// 81 us at 72 KiB, 70 at 140, 68 at 175, 67 at 210; 16 sequences in 4 bits to 512: 129, 112, 110, 108. (A cluster
+// per group that reads a round of blocks before it writes it: 125 and 146; of one sequence 103, this 23.)
+constexpr int kShiftBytes = 175 * 1024;
 constexpr int kUnread = 1 << 30;                                // kept: a block that moves and has not been read
 constexpr int kCkRow = kHeadDim * 2;                            // bytes of a compressed key
 
