@@ -277,3 +277,67 @@ def test_joined_windows_are_exact_means(sb, spread):
         span = np.concatenate([Kf[64 * blocks[i] + 48:64 * blocks[i] + 64], Kf[64 * blocks[i + 1]:64 * blocks[i + 1] + 16]])
         want = [_bf16_mean(span[:, c]) for c in range(128)]
         assert to64(layer.ck[0, 0, 4 * i + 3]).tolist() == want, i
+
+
+@pytest.mark.parametrize("kv4", [False, True])
+@pytest.mark.parametrize("lost", [1, 3, 200])
+def test_evict_in_place_of_long_shifts(sb, kv4, lost):
+    """Nearly every block moves by a few places, each onto one that moves too: the bytes of the old cache, the
+    same in every run and in a replayed graph."""
+    B, G, n = 2, 2, 1100
+    keep, T = n - lost, 64 * n - 5
+    shape = sb.Shape(n_groups=G, max_ctx=64 * n, max_batch=B)
+    gen = torch.Generator(device="cuda").manual_seed(31)
+    raw = torch.randint(0, 256, (B, G, n, 10240 if kv4 else 32768), generator=gen, dtype=torch.uint8, device="cuda")
+    ck0 = torch.randint(-2 ** 14, 2 ** 14, (B, G, shape.w_cap, 128), generator=gen, dtype=torch.int16, device="cuda")
+
+    def fresh():
+        if kv4:
+            return sb.LayerKV4(raw.clone(), ck0.clone().view(torch.bfloat16))
+        k, v = (raw[..., i:i + 16384].contiguous().view(torch.bfloat16).view(B, G, 64 * n, 128) for i in (0, 16384))
+        return sb.LayerKV(k, v, ck0.clone().view(torch.bfloat16))
+
+    def held(layer):
+        if kv4:
+            return layer.kv
+        return torch.cat([x.view(torch.uint8).view(B, G, n, 16384) for x in (layer.k, layer.v)], dim=-1)
+    mass0 = torch.rand((B, G, n), generator=gen, device="cuda") + 1
+    mass0[:, :, 1:1 + lost] = 0                            # the oldest go
+    mass0[1, 1] = 1
+    mass0[1, 1, torch.randperm(n - 2, generator=gen, device="cuda")[:lost] + 1] = 0
+    want = []
+    for b in range(B):
+        for g in range(G):
+            gone = set(torch.nonzero(mass0[b, g] == 0).flatten().tolist())
+            want.append([j for j in range(n) if j not in gone])
+    want = torch.tensor(want, device="cuda").view(B, G, keep)
+    fn = sb.sparda_kv4_evict_blocks if kv4 else sb.sparda_evict_blocks
+    kept = torch.empty((B, G, keep), dtype=torch.int32, device="cuda")
+    layer, mass, seq = fresh(), mass0.clone(), torch.full((B,), T, dtype=torch.int32, device="cuda")
+    graph = torch.cuda.CUDAGraph()
+    for run in range(4):
+        if run == 2:
+            with torch.cuda.graph(graph):
+                fn(shape, layer, mass, seq, B, keep, 1, kept)
+        if run:
+            again = fresh()
+            for name in ("kv", "ck") if kv4 else ("k", "v", "ck"):
+                getattr(layer, name).copy_(getattr(again, name))
+            mass.copy_(mass0)
+            seq.fill_(T)
+        if run < 2:
+            fn(shape, layer, mass, seq, B, keep, 1, kept)
+        else:
+            graph.replay()
+        torch.cuda.synchronize()
+        assert sb.sparda_device_error(clear=True) == 0
+        assert torch.equal(kept.long(), want)
+        assert (seq == T - 64 * lost).all()
+        got = held(layer)
+        for b in range(B):
+            for g in range(G):
+                assert torch.equal(got[b, g, :keep], raw[b, g][want[b, g]]), (run, b, g)
+                inner = torch.stack([ck0[b, g][4 * want[b, g] + i] for i in range(3)], dim=1)
+                assert torch.equal(layer.ck[b, g].view(torch.int16)[:4 * keep - 1].view(-1, 128)[
+                    (4 * torch.arange(keep, device="cuda")[:, None] + torch.arange(3, device="cuda")).flatten()].view(keep, 3, 128)
+                    [:-1], inner[:-1]), (run, b, g)
