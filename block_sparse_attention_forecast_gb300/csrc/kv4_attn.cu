@@ -7,7 +7,7 @@
 // a warp issues 293 instructions, 32 of them products. A product occupies the tensor pipe for 8.2
 // cycles and its operands' expansion the issue port for 8.7, but the two only half overlap (13.5
 // cycles together), so the instructions bound a long cache, not the memory: batch 16 of 131072 tokens
-// (671 MB) takes 144 us, and 137 us when every copy hits the same block in L2. A tcgen05 form, whose
+// (671 MB) takes 143 us, and 137 us when every copy hits the same block in L2. A tcgen05 form, whose
 // expanded operands go through tensor memory, took 240 us. With at most 8 heads (kEight) the roles
 // change: the cache is the A operand, 16 tokens or 16 channels of it, the heads are the N dimension,
 // and half the products do: the same batch with 8 heads takes 116 us, 0.85 of the memory's rate
