@@ -77,8 +77,9 @@ bool launch_sparse_attn(const AttnArgs& a, const CUtensorMap& mk, const CUtensor
   b.tl_buf = timeline_buffer();
   auto kern = a.stats ? (cluster ? sparse_attn_cluster_kernel<true> : sparse_attn_kernel<true>)
                       : (cluster ? sparse_attn_cluster_kernel<false> : sparse_attn_kernel<false>);
-  const int smem = cluster ? kAttnClusterSmem : kAttnSmem;
-  cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+  const int smem = !cluster ? kAttnSmem : a.stats ? kAttnMassSmem : kAttnClusterSmem;
+  static SmemOptIn opt_in[4];
+  opt_in[(a.stats ? 2 : 0) + (cluster ? 1 : 0)].set(kern, smem);      // (a launch without it reports the error)
   // Programmatic serialization: the barrier set-up overlaps the kernel before it in the
   // stream; the producer waits for it before it reads the unit metadata, the consumers before
   // they write anything.

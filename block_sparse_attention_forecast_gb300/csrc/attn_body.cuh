@@ -58,6 +58,9 @@ constexpr int kMaxClusterCtas = 8;
 constexpr int kRecvEntries = kHeads + kMaxClusterCtas - 1;
 constexpr int kRecvFloats = kRecvEntries * kHeadDim + 2 * kRecvEntries;
 constexpr int kAttnClusterSmem = kAttnSmem + kRecvFloats * 4;
+// With the block mass: every CTA's (max, sum) of every head.
+constexpr int kAttnMassSmem = kAttnClusterSmem + kMaxClusterCtas * 2 * kHeads * 4;
+static_assert(kAttnMassSmem <= 232448, "shared memory of a CTA");
 
 // Shared-memory address of 16-byte chunk `chunk` (0..15 over the 128 dims) of row `r` of a
 // K or V block staged as two 64-row x 128-byte halves with the 128-byte TMA swizzle.
@@ -211,7 +214,6 @@ __device__ __forceinline__ void attn_cta(const AttnArgs& a, const CUtensorMap* m
       }
     }
     if constexpr (kClusterMerge) cluster_sync();   // the consumers' merge barrier
-    if constexpr (kClusterMerge && kStats) cluster_sync();
     return;
   }
 
@@ -407,7 +409,16 @@ __device__ __forceinline__ void attn_cta(const AttnArgs& a, const CUtensorMap* m
       if ((t & 15) == 0) {
         st_cluster_f(rM + entry, owner, Mh);
         st_cluster_f(rL + entry, owner, Lh);
+        if constexpr (kStats) {
+          // for the block mass every CTA learns everyone's: it then needs no second barrier
+          for (int q = 0; q < sg; ++q) {
+            st_cluster_f(rL + kRecvEntries + (rank * 2) * kHeads + h, (uint32_t)q, Mh);
+            st_cluster_f(rL + kRecvEntries + (rank * 2 + 1) * kHeads + h, (uint32_t)q, Lh);
+          }
+        }
       }
+      SlotBlocks list{};
+      if constexpr (kStats) list = slot_blocks(a.idx + (size_t)bg * a.kslots, gi.n_sel);
       cluster_sync();                          // every partial of the cluster's heads is in place
       if (h % sg == (int)rank) {
         const int e0 = (h / sg) * sg;
@@ -425,13 +436,6 @@ __device__ __forceinline__ void attn_cta(const AttnArgs& a, const CUtensorMap* m
           acc[0] += wt * x0.x; acc[1] += wt * x0.y; acc[2] += wt * x0.z; acc[3] += wt * x0.w;
           acc[4] += wt * x1.x; acc[5] += wt * x1.y; acc[6] += wt * x1.z; acc[7] += wt * x1.w;
         }
-        if constexpr (kStats) {
-          if ((t & 15) == 0)                       // every CTA of the cluster learns the head's maximum and sum
-            for (int q = 0; q < sg; ++q) {
-              st_cluster_f(mM + h, (uint32_t)q, Mx);
-              st_cluster_f(mL + h, (uint32_t)q, L);
-            }
-        }
         uint32_t pk[4];
 #pragma unroll
         for (int e = 0; e < 4; ++e)
@@ -440,9 +444,11 @@ __device__ __forceinline__ void attn_cta(const AttnArgs& a, const CUtensorMap* m
             make_uint4(pk[0], pk[1], pk[2], pk[3]);
       }
       if constexpr (kStats) {
-        const SlotBlocks list = slot_blocks(a.idx + (size_t)bg * a.kslots, gi.n_sel);
-        cluster_sync();                        // (the merge buffers mM, mL were last read before the first one)
-        const float Mh0 = mM[lane & 15], Lh0 = mL[lane & 15];
+        const float* every = rL + kRecvEntries + (lane & 15);
+        float Mh0 = -INFINITY, Lh0 = 0.f;
+        for (int q = 0; q < sg; ++q) Mh0 = fmaxf(Mh0, every[2 * q * kHeads]);
+        const float base0 = (Mh0 == -INFINITY) ? 0.f : Mh0;
+        for (int q = 0; q < sg; ++q) Lh0 += exp2f(every[2 * q * kHeads] - base0) * every[(2 * q + 1) * kHeads];
         for (int s = s_begin + warp; s < s_stop; s += kConsumerWarps)
           add_block_mass(a.stats + (size_t)bg * a.kslots * kGroupWarps * kHeads, kGroupWarps, kHeads, Mh0, Lh0, list, s, gi.tb,
                          a.mass + (size_t)bg * (a.max_ctx / kBlock));

@@ -66,6 +66,7 @@ constexpr int kSmem4 = 128 + kHeader4 + kRing * kBlockBytes4 + kQBytes + kMergeF
 constexpr int kMaxCluster4 = 8;
 constexpr int kRecv4 = kHeads + kMaxCluster4 - 1;
 constexpr int kClusterSmem4 = kSmem4 + kRecv4 * (kHeadDim + 2) * 4;
+constexpr int kMassSmem4 = kClusterSmem4 + kMaxCluster4 * 2 * kHeads * 4;      // and every CTA's references and sums
 // The rules' limits, with both sides measured (kW = warps that share a block):
 //   kWholeBlocks    blocks per warp from which a warp takes whole ones. Batch 16 of 131072 tokens (431
 //                   blocks per CTA), 16 heads: kW 1 148 us, 2 151, 4 177; 8 heads: 117, 121, 144. A ragged
@@ -396,7 +397,6 @@ __global__ void __launch_bounds__(kThreads4, 1) kv4_attn_kernel(const Kv4AttnArg
     if constexpr (kCluster) {                        // the consumers' barriers
       cluster_wait();
       cluster_sync();
-      if constexpr (kStats) cluster_sync();
     }
     return;
   }
@@ -671,6 +671,13 @@ __global__ void __launch_bounds__(kThreads4, 1) kv4_attn_kernel(const Kv4AttnArg
       if ((t & 15) == 0) {
         st_cluster_f(rM + entry, owner, M);
         st_cluster_f(rL + entry, owner, L);
+        if constexpr (kStats) {
+          // for the block mass every CTA learns everyone's: it then needs no second barrier
+          for (int q = 0; q < cluster; ++q) {
+            st_cluster_f(rL + kRecv4 + (rank * 2) * kHeads + h, (uint32_t)q, M);
+            st_cluster_f(rL + kRecv4 + (rank * 2 + 1) * kHeads + h, (uint32_t)q, L);
+          }
+        }
       }
       cluster_sync();
       write = owner == rank;
@@ -766,13 +773,7 @@ __global__ void __launch_bounds__(kThreads4, 1) kv4_attn_kernel(const Kv4AttnArg
       }
     }
     if (write) {
-      if constexpr (kStats && kCluster) {
-        if ((t & 15) == 0)                     // every CTA of the cluster learns the head's reference and sum
-          for (int q = 0; q < cluster; ++q) {
-            st_cluster_f(mM + h, (uint32_t)q, M);
-            st_cluster_f(mL + h, (uint32_t)q, L);
-          }
-      } else if constexpr (kStats) {
+      if constexpr (kStats && !kCluster) {
         if ((t & 15) == 0) {
           a.ml[p.bg * 2 * kHeads + h] = M;
           a.ml[p.bg * 2 * kHeads + kHeads + h] = L;
@@ -789,8 +790,10 @@ __global__ void __launch_bounds__(kThreads4, 1) kv4_attn_kernel(const Kv4AttnArg
       const SlotBlocks list = slot_blocks(a.idx ? s_pre : nullptr, n0);
       const int tb = (T0 - 1) / kBlock;
       const int slots = a.idx ? a.kslots : a.nb_cap;
-      cluster_sync();                          // (mM and mL were last read before the first one)
-      const float Mh = mM[lane & 15], Lh = mL[lane & 15];
+      const float* every = mL + kMergeWarps * kHeads + kRecv4 * (kHeadDim + 2) + (lane & 15);
+      float Mh = kLowest, Lh = 0.f;
+      for (int q = 0; q < cluster; ++q) Mh = fmaxf(Mh, every[2 * q * kHeads]);
+      for (int q = 0; q < cluster; ++q) Lh += fast_exp2(every[2 * q * kHeads] - Mh) * every[(2 * q + 1) * kHeads];
       for (int s = p.s0 + warp; s < p.s1; s += kCWarps)
         add_block_mass(a.stats + (size_t)p.bg * slots * (8 / kTiles) * kHeads, 8 / kTiles, a.H, Mh, Lh, list, s, tb,
                        a.mass + (size_t)p.bg * a.nb_cap);
@@ -813,7 +816,7 @@ namespace {
 template <int kW, bool kStats, bool kCluster, bool kEight>
 int launch_form(const Kv4AttnArgs& a, int grid, int cluster, cudaStream_t s) {
   auto kern = kv4_attn_kernel<kW, kStats, kCluster, kEight>;
-  constexpr int smem = kCluster ? kClusterSmem4 : kSmem4;
+  constexpr int smem = !kCluster ? kSmem4 : kStats ? kMassSmem4 : kClusterSmem4;
   static_assert(smem <= 232448, "shared memory of a CTA");
   // the register split needs the registers that it counts on; a build with fewer must not run
   static const bool fits = [&] {
