@@ -5,7 +5,7 @@
 // every head, a reference m and the sum l of exp2(s - m), and for every head the final reference M
 // and sum L over all blocks; the weight of the part is l exp2(m - M) / L. So no score is stored or
 // computed twice: 256 or 512 bytes per block beside the block's 10 to 32 KiB. Where a (sequence,
-// group) is one thread-block cluster, the attention adds the weights itself (its CTAs tell each other
+// group) is one thread-block cluster, the attention adds the weights itself (its CTAs tell each other their
 // partial M and L), which saves this launch (11.4 -> 10.9 us for 34 blocks of each of 16 sequences in 4
 // bits when it was added, 9.8 now).
 // This kernel serves the other forms, one warp per attended block; a block's weights are added in a
