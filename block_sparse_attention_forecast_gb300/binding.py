@@ -199,18 +199,20 @@ class Shape:
     def __setattr__(self, name, value):
         self.__dict__[name] = value
         self.__dict__.pop("_ref", None)
-        self.__dict__.pop("_kv4_sizes", None)
+        self.__dict__.pop("_sizes", None)
 
     def __getstate__(self):
-        return {k: v for k, v in self.__dict__.items() if k not in ("_ref", "_kv4_sizes")}
+        return {k: v for k, v in self.__dict__.items() if k not in ("_ref", "_sizes")}
 
-    def kv4_sizes(self):
-        """(bytes of a LayerKV4's kv, elements of its ck), kept until a field changes."""
-        r = self.__dict__.get("_kv4_sizes")
+    def sizes(self):
+        """(elements of a resident LayerKV's k or v, bytes of a LayerKV4's kv, elements of their ck), kept until
+        a field changes."""
+        r = self.__dict__.get("_sizes")
         if r is None:
             rows = self.max_batch * self.n_groups
-            r = self.__dict__["_kv4_sizes"] = (rows * (self.max_ctx // BLOCK) * KV4_BLOCK_BYTES,
-                                               rows * num_windows(self.max_ctx) * self.head_dim)
+            r = self.__dict__["_sizes"] = (rows * self.max_ctx * self.head_dim,
+                                           rows * (self.max_ctx // BLOCK) * KV4_BLOCK_BYTES,
+                                           rows * num_windows(self.max_ctx) * self.head_dim)
         return r
 
     def ref(self):
@@ -243,6 +245,13 @@ class LayerKV:
     hot_k: torch.Tensor = None
     hot_v: torch.Tensor = None
     on_host: bool = False
+
+    def __setattr__(self, name, value):
+        self.__dict__[name] = value
+        self.__dict__.pop("_args", None)
+
+    def __getstate__(self):
+        return {k: v for k, v in self.__dict__.items() if k != "_args"}
 
     def c(self):
         return c_layer_kv(self.k.data_ptr(), self.v.data_ptr(), self.ck.data_ptr(),
@@ -575,7 +584,7 @@ def _kv4_layer(shape, layer):
     dev = kv.get_device()
     if dev < 0 or dev != _current_device():
         _cache_device(kv)                            # raises
-    n_kv, n_ck = shape.kv4_sizes()
+    _, n_kv, n_ck = shape.sizes()
     args = layer.__dict__.get("_args")
     if (args is not None and args[0] == kv.data_ptr() and args[1] == ck.data_ptr() and kv.numel() >= n_kv and
             ck.numel() >= n_ck):
@@ -642,15 +651,24 @@ def sparda_kv4_decode_attn(shape, layer, q, idx, cnt, seq_len, batch, out, ws, m
 
 
 def _layer_ptrs(shape, layer):
-    """(device, pointer to the C layer) of a resident LayerKV, its tensors checked."""
+    """(device, pointer to the C layer) of a resident LayerKV, its tensors checked. The C struct is kept with the
+    layer until one of its fields is set; the tensors' sizes and addresses are checked in every call."""
     if layer.on_host:
         raise ValueError("a resident layer is wanted")
-    dev = _cache_device(layer.k)
-    rows, d = shape.max_batch * shape.n_groups, shape.head_dim
-    n = rows * shape.max_ctx * d
-    return dev, ctypes.byref(c_layer_kv(
-        _checked("k", layer.k, torch.bfloat16, n, dev), _checked("v", layer.v, torch.bfloat16, n, dev),
-        _checked("ck", layer.ck, torch.bfloat16, rows * num_windows(shape.max_ctx) * d, dev), None, None, 0, 0))
+    k, v, ck = layer.k, layer.v, layer.ck
+    dev = k.get_device()
+    if dev < 0 or dev != _current_device():
+        _cache_device(k)                             # raises
+    n, _, n_ck = shape.sizes()
+    args = layer.__dict__.get("_args")
+    if (args is not None and args[0] == k.data_ptr() and args[1] == v.data_ptr() and args[2] == ck.data_ptr() and
+            k.numel() >= n and v.numel() >= n and ck.numel() >= n_ck):
+        return dev, args[3]
+    c = c_layer_kv(_checked("k", k, torch.bfloat16, n, dev), _checked("v", v, torch.bfloat16, n, dev),
+                   _checked("ck", ck, torch.bfloat16, n_ck, dev), None, None, 0, 0)
+    ref = ctypes.byref(c)
+    layer.__dict__["_args"] = (c.k, c.v, c.ck, ref)
+    return dev, ref
 
 
 def sparda_sparse_decode_attn_mass(shape, layer, q, idx, cnt, seq_len, batch, out, ws, mass, stream=None):
@@ -672,9 +690,8 @@ def _evict(name, fn, ptrs, shape, layer, mass, seq_len, batch, keep, recent, kep
     dev, lc = ptrs(shape, layer)
     B, G = int(batch), shape.n_groups
     ds = dc = pm = pl = None
-    given = [x is not None for x in (dst_shape, dst, dst_mass, dst_seq_len)]
-    if any(given):
-        if not all(given):
+    if dst is not None or dst_shape is not None or dst_mass is not None or dst_seq_len is not None:
+        if dst is None or dst_shape is None or dst_mass is None or dst_seq_len is None:
             raise ValueError("dst_shape, dst, dst_mass and dst_seq_len come together")
         ds, dc = dst_shape.ref(), ptrs(dst_shape, dst)[1]
         pm = _checked("dst_mass", dst_mass, torch.float32, B * G * (dst_shape.max_ctx // BLOCK), dev)

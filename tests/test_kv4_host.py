@@ -181,3 +181,21 @@ def test_eviction_refuses_a_destination_inside_the_source(kv4):
         assert call(**ok, keep=4097) == sb.ERR_UNSUPPORTED_SHAPE
         if not torch.cuda.is_available():
             assert call(**ok) != bad
+
+
+def test_layers_are_checked_again_when_a_field_changes():
+    """The C struct kept with a layer goes when a field is set, and with a pickle or a copy."""
+    import copy
+    import pickle
+    shape = sb.Shape(max_batch=1, n_groups=1, max_ctx=64)
+    for layer, field in ((sb.LayerKV(torch.zeros(1, 1, 64, 128), torch.zeros(1, 1, 64, 128), torch.zeros(1, 1, 3, 128)), "k"),
+                         (sb.LayerKV4.empty(shape, device="cpu"), "kv")):
+        layer.__dict__["_args"] = (1, 2, ctypes.byref(ctypes.c_int(0)))
+        assert "_args" not in pickle.loads(pickle.dumps(layer)).__dict__
+        assert "_args" not in copy.copy(layer).__dict__ and "_args" not in copy.deepcopy(layer).__dict__
+        assert "_args" in layer.__dict__
+        setattr(layer, field, getattr(layer, field).clone())
+        assert "_args" not in layer.__dict__
+    n = shape.sizes()
+    shape.max_batch = 3
+    assert shape.sizes() == tuple(3 * x for x in n) and pickle.loads(pickle.dumps(shape)) == shape
