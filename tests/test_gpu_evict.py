@@ -341,3 +341,33 @@ def test_evict_in_place_of_long_shifts(sb, kv4, lost):
                 assert torch.equal(layer.ck[b, g].view(torch.int16)[:4 * keep - 1].view(-1, 128)[
                     (4 * torch.arange(keep, device="cuda")[:, None] + torch.arange(3, device="cuda")).flatten()].view(keep, 3, 128)
                     [:-1], inner[:-1]), (run, b, g)
+
+
+def test_two_evictions_in_place_at_once(sb):
+    """Two caches on two streams, each cut in place while the other is."""
+    B, G, n, keep = 4, 2, 700, 450
+    shape = sb.Shape(n_groups=G, max_ctx=64 * n, max_batch=B)
+    gen = torch.Generator(device="cuda").manual_seed(41)
+    streams = [torch.cuda.Stream() for _ in range(2)]
+    raw = [torch.randint(0, 256, (B, G, n, 10240), generator=gen, dtype=torch.uint8, device="cuda") for _ in streams]
+    mass0 = [torch.rand((B, G, n), generator=gen, device="cuda") + 1 for _ in streams]
+    layers = [sb.LayerKV4(r.clone(), torch.zeros((B, G, shape.w_cap, 128), dtype=torch.bfloat16, device="cuda")) for r in raw]
+    masses = [m.clone() for m in mass0]
+    seqs = [torch.full((B,), 64 * n, dtype=torch.int32, device="cuda") for _ in streams]
+    kept = [torch.empty((B, G, keep), dtype=torch.int32, device="cuda") for _ in streams]
+    torch.cuda.synchronize()
+    for _ in range(6):
+        for i, s in enumerate(streams):
+            with torch.cuda.stream(s):
+                layers[i].kv.copy_(raw[i])
+                masses[i].copy_(mass0[i])
+                seqs[i].fill_(64 * n)
+                sb.sparda_kv4_evict_blocks(shape, layers[i], masses[i], seqs[i], B, keep, 3, kept[i])
+    torch.cuda.synchronize()
+    assert sb.sparda_device_error(clear=True) == 0
+    for i in range(2):
+        for b in range(B):
+            for g in range(G):
+                want = R.kept_blocks(mass0[i][b, g].cpu().numpy(), n, keep, 3)
+                assert kept[i][b, g].tolist() == want
+                assert torch.equal(layers[i].kv[b, g, :keep], raw[i][b, g][torch.tensor(want, device="cuda")])
