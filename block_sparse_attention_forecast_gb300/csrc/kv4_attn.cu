@@ -7,11 +7,11 @@
 // a warp issues 293 instructions, 32 of them products. A product occupies the tensor pipe for 8.2
 // cycles and its operands' expansion the issue port for 8.7, but the two only half overlap (13.5
 // cycles together), so the instructions bound a long cache, not the memory: batch 16 of 131072 tokens
-// (671 MB) takes 143 us, and 137 us when every copy hits the same block in L2. A tcgen05 form, whose
+// (671 MB) takes 139.6 us, and 137.1 us when every copy hits the same blocks in L2. A tcgen05 form, whose
 // expanded operands go through tensor memory, took 240 us. With at most 8 heads (kEight) the roles
 // change: the cache is the A operand, 16 tokens or 16 channels of it, the heads are the N dimension,
 // and half the products do: the same batch with 8 heads takes 116 us, 0.85 of the memory's rate
-// (147 with the heads as M). A score tile's 8 x 8 weights are transposed between lanes on the way.
+// (147 with the heads as M; 113 without the memory's part). A score tile's 8 x 8 weights are transposed between lanes on the way.
 //
 // Work, three forms chosen by launch_kv4_attn:
 //   - few blocks per (sequence, group): one thread-block cluster each (of one CTA where there are more
@@ -48,9 +48,10 @@ constexpr int kCWarps = 8;
 constexpr int kCThreads = kCWarps * 32;
 // The producer has a warpgroup to itself, of which one warp works: registers are moved from it to the
 // consumers, which would otherwise be held to 168 each and spill (162 us instead of 147 for batch 16 of
-// 131072 tokens; twelve consumer warps of fewer registers also 162).
+// 131072 tokens when it was tried; twelve consumer warps of fewer registers also 162; now 143.0 at 208,
+// with a few spilled, and 139.6 at 232).
 constexpr int kThreads4 = kCThreads + 128;
-constexpr int kLaunchRegs = 168, kProducerRegs = 40, kConsumerRegs = 208;
+constexpr int kLaunchRegs = 168, kProducerRegs = 40, kConsumerRegs = 232;
 static_assert(128 * kProducerRegs + kCThreads * kConsumerRegs <= kThreads4 * kLaunchRegs, "registers the launch holds");
 constexpr int kRing = 16;                                   // at most a warp's lanes
 constexpr int kPlanMax = 1024;
