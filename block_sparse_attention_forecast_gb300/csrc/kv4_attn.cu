@@ -11,7 +11,8 @@
 // expanded operands go through tensor memory, took 240 us. With at most 8 heads (kEight) the roles
 // change: the cache is the A operand, 16 tokens or 16 channels of it, the heads are the N dimension,
 // and half the products do: the same batch with 8 heads takes 116 us, 0.85 of the memory's rate
-// (147 with the heads as M; 113 without the memory's part). A score tile's 8 x 8 weights are transposed between lanes on the way.
+// (147 with the heads as M; 113 without the memory's part). A score tile's 8 x 8 weights are transposed
+// between lanes on the way.
 //
 // Work, three forms chosen by launch_kv4_attn:
 //   - few blocks per (sequence, group): one thread-block cluster each (of one CTA where there are more
