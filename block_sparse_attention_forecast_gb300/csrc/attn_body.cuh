@@ -22,7 +22,8 @@
 // one CTA is written out directly. Otherwise, in the cluster form (kClusterMerge: the standalone
 // launch with a whole number of CTAs per group, each group one thread-block cluster), each CTA
 // pushes its (O, max, sum) of every head into the shared memory of the CTA that owns the head,
-// and after one cluster barrier each combines its share of the heads; in the general form each covering CTA stores (O, max, sum) to the workspace and
+// once all have started (a cluster barrier arrived at on entry), and after a second barrier each
+// combines its share of the heads; in the general form each covering CTA stores (O, max, sum) to the workspace and
 // the last one to arrive (a counter in the workspace, which it resets) merges them with
 // log-sum-exp weights. Because ranges are contiguous, that merge overlaps the producer's loads
 // for the next group.
@@ -99,7 +100,7 @@ __device__ __forceinline__ GroupInfo group_info(const AttnArgs& a, int bg) {
 // The work of CTA c of `grid` CTAs that share the attention units. The tensor maps live in
 // the calling kernel's parameter space. kClusterMerge: CTA c is rank c % seg_per_group of a
 // cluster of seg_per_group CTAs that covers group c / seg_per_group (seg_per_group >= 2), and
-// every thread of the CTA reaches the merge's one cluster barrier. tl_first (timeline
+// every thread of the CTA reaches the start's and the merge's cluster barriers, once each. tl_first (timeline
 // build only): thread 0 stores there the time its first block arrived.
 // kStats: every quarter block's softmax statistics of each head and the final ones are stored
 // too, for the block mass.
@@ -133,6 +134,9 @@ __device__ __forceinline__ void attn_cta(const AttnArgs& a, const CUtensorMap* m
     }
     fence_mbar_init();
   }
+  // Waited for before the first write to another CTA's shared memory: nothing else says that the
+  // cluster's other CTAs have started, and a group without a selected block gets there at once.
+  if constexpr (kClusterMerge) cluster_arrive();
   __syncthreads();
 
   if (warp == kConsumerWarps) {
@@ -213,7 +217,10 @@ __device__ __forceinline__ void attn_cta(const AttnArgs& a, const CUtensorMap* m
         ++it;
       }
     }
-    if constexpr (kClusterMerge) cluster_sync();   // the consumers' merge barrier
+    if constexpr (kClusterMerge) {                 // the consumers' barriers
+      cluster_wait();
+      cluster_sync();
+    }
     return;
   }
 
@@ -396,7 +403,7 @@ __device__ __forceinline__ void attn_cta(const AttnArgs& a, const CUtensorMap* m
     }
     if constexpr (kClusterMerge) {
       // this CTA's (O, max, sum) of head h pushed into the receive area of the CTA that owns
-      // h (rank h % sg); after one cluster barrier each CTA combines its heads' sg partials
+      // h (rank h % sg); after the merge's cluster barrier each CTA combines its heads' sg partials
       // from its own shared memory, and no CTA reads another's, so none has to stay resident
       float* rO = mL + kConsumerWarps * kHeads;            // [kRecvEntries][128 dims]
       float* rM = rO + kRecvEntries * kHeadDim;            // [kRecvEntries]
@@ -404,6 +411,7 @@ __device__ __forceinline__ void attn_cta(const AttnArgs& a, const CUtensorMap* m
       const uint32_t rank = cluster_rank();
       const int entry = (h / sg) * sg + (int)rank;
       const uint32_t owner = (uint32_t)(h % sg);
+      cluster_wait();                          // every CTA of the cluster has started
       st_cluster_f4(rO + entry * kHeadDim + d0, owner, make_float4(Oh[0], Oh[1], Oh[2], Oh[3]));
       st_cluster_f4(rO + entry * kHeadDim + d0 + 4, owner, make_float4(Oh[4], Oh[5], Oh[6], Oh[7]));
       if ((t & 15) == 0) {
