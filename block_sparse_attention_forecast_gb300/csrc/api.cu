@@ -902,8 +902,9 @@ bool overlap(const void* p, size_t n, const void* q, size_t m) {
   return a < b + m && b < a + n;
 }
 
-// Whether a cache of shape d shares memory with the source of shape s (planes and compressed keys), or
-// its weights and lengths with the source's.
+// Whether a cache of shape d shares memory with the source of shape s (planes and compressed keys, all
+// max_batch sequences of them), or its weights and lengths with the source's. Of those two a call reads and
+// writes `batch` sequences, and a caller may hold no more: what lies behind them is somebody else's.
 bool evict_overlap(const EvictArgs& a, const sparda_shape* s, const sparda_shape* d, int32_t batch) {
   const size_t ns = (size_t)s->max_batch * s->n_groups, nd = (size_t)d->max_batch * d->n_groups;
   const void* from[3] = {a.src_ck, a.src[0], a.src[1]};
@@ -914,7 +915,8 @@ bool evict_overlap(const EvictArgs& a, const sparda_shape* s, const sparda_shape
   for (int i = 0; i <= a.planes; ++i)
     for (int j = 0; j <= a.planes; ++j)
       if (overlap(from[i], n_from[i > 0], to[j], n_to[j > 0])) return true;
-  return overlap(a.src_mass, ns * a.src_nb * 4, a.dst_mass, nd * a.dst_nb * 4) ||
+  const size_t rows = (size_t)batch * s->n_groups;
+  return overlap(a.src_mass, rows * a.src_nb * 4, a.dst_mass, rows * a.dst_nb * 4) ||
          overlap(a.src_len, (size_t)batch * 4, a.dst_len, (size_t)batch * 4);
 }
 

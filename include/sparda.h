@@ -657,7 +657,8 @@ int32_t sparda_kv4_decode_attn(const sparda_shape* shape, const sparda_layer_kv4
 /*
  * An extension beyond the pages, for caches that must not grow with the conversation: attention
  * calls add up the weight that each 64-token block receives, and the blocks with the least of it
- * are evicted. mass: float32 [max_batch, G, max_ctx/64], zeroed by the caller at the start.
+ * are evicted. mass: float32 [max_batch, G, max_ctx/64], zeroed by the caller at the start (a call
+ * reads and writes the first `batch` sequences of it only).
  */
 
 /*

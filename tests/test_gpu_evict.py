@@ -371,3 +371,29 @@ def test_two_evictions_in_place_at_once(sb):
                 want = R.kept_blocks(mass0[i][b, g].cpu().numpy(), n, keep, 3)
                 assert kept[i][b, g].tolist() == want
                 assert torch.equal(layers[i].kv[b, g, :keep], raw[i][b, g][torch.tensor(want, device="cuda")])
+
+
+@pytest.mark.parametrize("kv4", [False, True])
+def test_evict_weights_of_the_batch_side_by_side(sb, kv4):
+    """mass and dst_mass of fewer sequences than max_batch, neighbours in one tensor, either one first."""
+    ctx, keep, G = 1024, 5, 2
+    shape, layer, _, mass = _case(sb, kv4, [1000] * 5, G, ctx, "plain", 410)
+    dshape = sb.Shape(n_groups=G, max_ctx=64 * keep, max_batch=5)
+    fn = sb.sparda_kv4_evict_blocks if kv4 else sb.sparda_evict_blocks
+    n_src, n_dst = 2 * G * 16, 2 * G * keep
+    for first in (False, True):
+        both = torch.full((n_src + n_dst + 8,), 3.0, device="cuda")
+        m = both[n_dst:n_dst + n_src] if first else both[:n_src]
+        dm = both[:n_dst] if first else both[n_src:n_src + n_dst]
+        m.copy_(mass[:2].reshape(-1).cuda())
+        kept = torch.zeros((2, G, keep), dtype=torch.int32, device="cuda")
+        fn(shape, layer, m.view(2, G, 16), _i32([1000, 640]), 2, keep, 1, kept, dst_shape=dshape,
+           dst=(sb.LayerKV4 if kv4 else sb.LayerKV).empty(dshape), dst_mass=dm.view(2, G, keep), dst_seq_len=_i32([0, 0]))
+        torch.cuda.synchronize()
+        assert sb.sparda_device_error(clear=True) == 0
+        for b in range(2):
+            for g in range(G):
+                want = R.kept_blocks(mass[b, g].double().numpy(), (16, 10)[b], keep, 1)
+                assert kept[b, g].tolist() == want
+                assert torch.equal(dm.view(2, G, keep)[b, g].cpu(), mass[b, g][want])
+        assert (both[-8:] == 3).all()

@@ -199,3 +199,23 @@ def test_layers_are_checked_again_when_a_field_changes():
     n = shape.sizes()
     shape.max_batch = 3
     assert shape.sizes() == tuple(3 * x for x in n) and pickle.loads(pickle.dumps(shape)) == shape
+
+
+@pytest.mark.parametrize("kv4", [False, True])
+@pytest.mark.parametrize("batch", [1, 3])
+def test_eviction_takes_weights_of_the_batch_alone(kv4, batch):
+    """Weight arrays of `batch` sequences, fewer than max_batch, directly side by side: they are apart, on
+    either side, and one float nearer they are not."""
+    s, d = _shape(max_batch=8, n_groups=2, max_ctx=1024), _shape(max_batch=4, n_groups=2, max_ctx=512)
+    fn = sb.lib.sparda_kv4_evict_blocks if kv4 else sb.lib.sparda_evict_blocks
+    src, dst = (_l4(kv=1 << 34, ck=1 << 33), _l4(kv=1 << 36, ck=1 << 35)) if kv4 else \
+        (_lk(k=1 << 34, v=1 << 37, ck=1 << 33), _lk(k=1 << 36, v=1 << 38, ck=1 << 35))
+    m = 1 << 20
+    n_src, n_dst = batch * 2 * 16 * 4, batch * 2 * 8 * 4           # bytes of the two arrays
+
+    def call(mass, dm):
+        return fn(_ref(s), src, P(mass), P(1 << 22), _ref(d), dst, P(dm), P(1 << 23), batch, 8, 2, P(1 << 25), None)
+    assert call(m, m + n_src - 4) == sb.ERR_INVALID_ARG and call(m, m - n_dst + 4) == sb.ERR_INVALID_ARG
+    if not torch.cuda.is_available():              # (made-up addresses: not where the call could launch)
+        for dm in (m + n_src, m - n_dst):
+            assert call(m, dm) == sb.ERR_CUDA
