@@ -920,6 +920,13 @@ bool evict_overlap(const EvictArgs& a, const sparda_shape* s, const sparda_shape
          overlap(a.src_len, (size_t)batch * 4, a.dst_len, (size_t)batch * 4);
 }
 
+// The status of a call whose launches gave `e`. An error that a launch left for cudaGetLastError() is this
+// call's and is taken from there, so that the next call does not report it.
+int32_t launched(cudaError_t e) {
+  const cudaError_t left = cudaGetLastError();
+  return cuda_status(e != cudaSuccess ? e : left);
+}
+
 // What both evictions check and hand on beside their cache planes, which *a holds already.
 // `in_place`: no dst argument.
 int32_t prepare_evict(const sparda_shape* s, const sparda_shape* d, const void* ck, void* dst_ck, float* mass,
@@ -984,8 +991,7 @@ int32_t sparda_evict_blocks(const sparda_shape* s, const sparda_layer_kv* L, flo
   a.block_bytes = kBlockBytes;
   SPARDA_TRY(prepare_evict(s, d, L->ck, dst ? dst->ck : nullptr, mass, seq_len, dst_mass, dst_seq_len, batch, keep, recent,
                            kept, dst == nullptr, &a));
-  if (!launch_evict(a, static_cast<cudaStream_t>(stream))) return SPARDA_ERR_CUDA;
-  return cuda_status(cudaGetLastError());
+  return launched(launch_evict(a, static_cast<cudaStream_t>(stream)));
 }
 
 int32_t sparda_kv4_evict_blocks(const sparda_shape* s, const sparda_layer_kv4* L, float* mass, int32_t* seq_len,
@@ -1004,8 +1010,7 @@ int32_t sparda_kv4_evict_blocks(const sparda_shape* s, const sparda_layer_kv4* L
   a.kv4 = 1;
   SPARDA_TRY(prepare_evict(s, d, L->ck, dst ? dst->ck : nullptr, mass, seq_len, dst_mass, dst_seq_len, batch, keep, recent,
                            kept, dst == nullptr, &a));
-  if (!launch_evict(a, static_cast<cudaStream_t>(stream))) return SPARDA_ERR_CUDA;
-  return cuda_status(cudaGetLastError());
+  return launched(launch_evict(a, static_cast<cudaStream_t>(stream)));
 }
 
 }  // extern "C"

@@ -15,7 +15,8 @@
 //                         block n's write waits for m's. One cooperative launch, blocks in the order
 //                         of n: the lowest one in flight never waits, so every wait ends.
 //   evict_join_kernel     after the shift: the compressed keys of windows that span two blocks
-//                         which were not neighbours before (the move kernel does its own).
+//                         which were not neighbours before (the move kernel does its own), and the
+//                         weights, which must not move unless the blocks do.
 //   evict_length_kernel   after the shift: the new lengths, once nothing reads the old ones.
 //
 // A moved block's windows 4n .. 4n+2 lie inside it and move with it; window 4n+3 takes its last 16
@@ -124,7 +125,6 @@ __global__ void __launch_bounds__(kSelThreads) evict_select_kernel(const EvictAr
     const int j = tid * kSelPer + i;
     key[i] = j >= 1 && j < n - a.recent ? weight_key(w[i]) : 0u;     // candidates only
   }
-  __syncthreads();                                 // in place: every weight is read before one is written
   uint32_t sel = 0;                                // bit i: block tid * kSelPer + i is kept
   if (n <= a.keep) {
 #pragma unroll
@@ -224,11 +224,11 @@ __global__ void __launch_bounds__(kSelThreads) evict_select_kernel(const EvictAr
     if (sel >> i & 1u) {
       const int j = tid * kSelPer + i;
       kept[at] = a.in_place && j != at ? j | kUnread : j;
-      dst[at] = w[i];
+      if (!a.in_place) dst[at] = w[i];             // in place the weights move when the blocks have
       ++at;
     }
   for (int i = count + tid; i < a.keep; i += kSelThreads) kept[i] = -1;
-  if (valid)
+  if (valid && !a.in_place)
     for (int i = count + tid; i < a.dst_nb; i += kSelThreads) dst[i] = 0.f;
   if (!a.in_place && tid == 0 && bg % a.G == 0) a.dst_len[b] = valid ? kept_len(T, a.keep) : T;
 }
@@ -370,7 +370,8 @@ __global__ void __launch_bounds__(32) evict_shift_kernel(const EvictArgs a) {
   bulk_wait_all();
 }
 
-// Grid: (sequence, group) x groups of kept blocks, 64 threads per kept block.
+// Grid: (sequence, group) x groups of kept blocks, 64 threads per kept block. A group's first CTA also moves
+// its weights, each read before one is written.
 __global__ void __launch_bounds__(kMoveThreads) evict_join_kernel(const EvictArgs a) {
   grid_dep_wait();
   grid_dep_launch();
@@ -378,9 +379,25 @@ __global__ void __launch_bounds__(kMoveThreads) evict_join_kernel(const EvictArg
   const int pieces = (a.keep + per - 1) / per;
   const int bg = blockIdx.x / pieces, n = (blockIdx.x % pieces) * per + (int)threadIdx.x / 64, t = threadIdx.x % 64;
   const int T0 = a.src_len[bg / a.G];
-  if (n + 1 >= a.keep || !valid_len(T0, a.src_nb)) return;
+  if (!valid_len(T0, a.src_nb)) return;
   const int32_t* kept = a.kept + (size_t)bg * a.keep;
-  if (!joins(n, min(blocks_of(T0), a.keep), kept_len(T0, a.keep), kept[n + 1] == kept[n] + 1)) return;
+  const int count = min(blocks_of(T0), a.keep);
+  if (blockIdx.x % pieces == 0) {
+    float* mass = a.dst_mass + (size_t)bg * a.dst_nb;
+    float w[kMaxCtx / kBlock / kMoveThreads];
+#pragma unroll
+    for (int i = 0; i < kMaxCtx / kBlock / kMoveThreads; ++i) {
+      const int at = i * kMoveThreads + (int)threadIdx.x;
+      w[i] = at < count ? mass[kept[at]] : 0.f;
+    }
+    __syncthreads();
+#pragma unroll
+    for (int i = 0; i < kMaxCtx / kBlock / kMoveThreads; ++i) {
+      const int at = i * kMoveThreads + (int)threadIdx.x;
+      if (at < a.dst_nb) mass[at] = w[i];
+    }
+  }
+  if (n + 1 >= a.keep || !joins(n, count, kept_len(T0, a.keep), kept[n + 1] == kept[n] + 1)) return;
   const size_t block = (size_t)bg * a.dst_nb + n;
   reinterpret_cast<uint32_t*>(a.dst_ck + ((size_t)bg * (4 * a.dst_nb - 1) + 4 * n + 3) * kHeadDim)[t] =
       joined_window(a.dst[0], a.kv4, block, block + 1, t);
@@ -395,18 +412,40 @@ __global__ void evict_length_kernel(const EvictArgs a) {
   }
 }
 
-bool launch_evict(const EvictArgs& a, cudaStream_t s) {
+namespace {
+
+// CTAs of the shift that an SM holds at once, found once per device and size of a block.
+int shift_ctas_per_sm(const EvictArgs& a, int smem) {
+  static std::atomic<int> known[64][2] = {};
+  int dev = 0;
+  if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= 64) return 0;
+  std::atomic<int>& n = known[dev][a.kv4 ? 1 : 0];
+  int ctas = n.load(std::memory_order_relaxed);
+  if (ctas == 0 && cudaOccupancyMaxActiveBlocksPerMultiprocessor(&ctas, evict_shift_kernel, 32, smem) == cudaSuccess)
+    n.store(ctas, std::memory_order_relaxed);
+  return ctas;
+}
+
+}  // namespace
+
+cudaError_t launch_evict(const EvictArgs& a, cudaStream_t s) {
   const unsigned bg = (unsigned)a.B * a.G;
-  launch_pdl(evict_select_kernel, dim3(bg), dim3(kSelThreads), 0, s, a);
+  const int smem = 128 + a.planes * a.block_bytes + 4 * kCkRow;       // of the shift
+  long long most = 0;
+  if (a.in_place) {
+    const int fit = shift_ctas_per_sm(a, smem);    // the cooperative launch needs all its CTAs resident
+    if (fit < 1) return cudaErrorCooperativeLaunchTooLarge;
+    most = (long long)min(fit, kShiftBytes / smem) * sm_count();
+  }
+  cudaError_t err = launch_pdl(evict_select_kernel, dim3(bg), dim3(kSelThreads), 0, s, a);
+  if (err != cudaSuccess) return err;
   if (!a.in_place) {
     const int ring = kMoveSlots * a.block_bytes;
     const long long items = (long long)bg * a.keep * a.planes, ctas = (items + kMoveSlots - 1) / kMoveSlots;
-    const int most = kMoveBytes / ring * sm_count(), grid = (int)(ctas < most ? ctas : most);
-    launch_pdl(evict_move_kernel, dim3(grid), dim3(kMoveThreads + 32), (size_t)ring + 128, s, a);
-    return true;
+    const int all = kMoveBytes / ring * sm_count(), grid = (int)(ctas < all ? ctas : all);
+    return launch_pdl(evict_move_kernel, dim3(grid), dim3(kMoveThreads + 32), (size_t)ring + 128, s, a);
   }
-  const int smem = 128 + a.planes * a.block_bytes + 4 * kCkRow;
-  const long long items = (long long)bg * a.keep, most = kShiftBytes / smem * sm_count();
+  const long long items = (long long)bg * a.keep;
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3((unsigned)(items < most ? items : most));
   cfg.blockDim = dim3(32);
@@ -417,10 +456,11 @@ bool launch_evict(const EvictArgs& a, cudaStream_t s) {
   attr[0].val.cooperative = 1;
   cfg.attrs = attr;
   cfg.numAttrs = 1;
-  if (cudaLaunchKernelEx(&cfg, evict_shift_kernel, a) != cudaSuccess) return false;
-  launch_pdl(evict_join_kernel, dim3(bg * (unsigned)((a.keep + 3) / 4)), dim3(kMoveThreads), 0, s, a);
-  launch_pdl(evict_length_kernel, dim3(1), dim3(256), 0, s, a);
-  return true;
+  err = cudaLaunchKernelEx(&cfg, evict_shift_kernel, a);
+  if (err != cudaSuccess) return err;
+  err = launch_pdl(evict_join_kernel, dim3(bg * (unsigned)((a.keep + 3) / 4)), dim3(kMoveThreads), 0, s, a);
+  if (err != cudaSuccess) return err;
+  return launch_pdl(evict_length_kernel, dim3(1), dim3(256), 0, s, a);
 }
 
 }  // namespace sparda

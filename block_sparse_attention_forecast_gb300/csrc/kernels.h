@@ -259,7 +259,9 @@ struct EvictArgs {
   int planes, block_bytes, kv4;  // kv4: one plane in the 4-bit layout; else K and V planes of bf16
   int B, G, src_nb, dst_nb, keep, recent, in_place;
 };
-bool launch_evict(const EvictArgs& a, cudaStream_t s);   // false: a launch could not be prepared
+// Launches nothing behind a launch that failed, whose error it returns. In place, weights and lengths are
+// written by the launches behind the one that moves the blocks: an error leaves them, and the cache, as they were.
+cudaError_t launch_evict(const EvictArgs& a, cudaStream_t s);
 
 // Device address of the library's device error word on the current device (api.cu).
 int* dev_error_word();
@@ -288,7 +290,7 @@ struct SmemOptIn {
 // A launch that may begin while the kernel before it in the stream still runs (programmatic
 // dependent launch); the kernel waits for that one with grid_dep_wait().
 template <typename... P, typename... A>
-inline void launch_pdl(void (*kern)(P...), dim3 grid, dim3 block, size_t smem, cudaStream_t s, A&&... args) {
+inline cudaError_t launch_pdl(void (*kern)(P...), dim3 grid, dim3 block, size_t smem, cudaStream_t s, A&&... args) {
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = grid;
   cfg.blockDim = block;
@@ -299,7 +301,7 @@ inline void launch_pdl(void (*kern)(P...), dim3 grid, dim3 block, size_t smem, c
   attr[0].val.programmaticStreamSerializationAllowed = 1;
   cfg.attrs = attr;
   cfg.numAttrs = 1;
-  cudaLaunchKernelEx(&cfg, kern, static_cast<P>(args)...);
+  return cudaLaunchKernelEx(&cfg, kern, static_cast<P>(args)...);
 }
 
 }  // namespace sparda

@@ -689,7 +689,9 @@ int32_t sparda_sparse_decode_attn_mass(const sparda_shape* shape, const sparda_l
  *
  * In place: dst_shape and dst NULL (dst_mass and dst_seq_len too): layer, mass and seq_len are
  * updated; one of the launches is cooperative (its CTAs wait for one another, at most 175 KiB of them
- * per SM) and starts when all of it fits beside what is running. Otherwise dst is another resident cache of dst_shape (n_groups equal, max_batch >= batch,
+ * per SM) and starts when all of it fits beside what is running. If it is refused the call returns
+ * SPARDA_ERR_CUDA and layer, mass and seq_len stay as they were (kept is undefined).
+ * Otherwise dst is another resident cache of dst_shape (n_groups equal, max_batch >= batch,
  * max_ctx >= 64 keep, smaller or larger than the source's) that shares no memory with the source,
  * dst_mass float32 [max_batch, G, max_ctx/64] of dst_shape, dst_seq_len int32 [B], and the source
  * stays as it was. kept: int32 [B, G, keep], written: the old block numbers, ascending, -1 behind.

@@ -1,0 +1,85 @@
+"""What the library does when a CUDA launch is refused, on the CPU: its host code linked against a stand-in
+for the CUDA runtime that records the launches and refuses the n-th."""
+import ctypes
+import os
+import subprocess
+
+import pytest
+
+from block_sparse_attention_forecast_gb300 import build as _build
+
+_build.build()
+
+import block_sparse_attention_forecast_gb300.binding as sb  # noqa: E402
+
+P = ctypes.c_void_p
+TOO_LARGE = 720                                    # cudaErrorCooperativeLaunchTooLarge
+
+
+def compiled(tmp, sources, fake="fake_cuda_runtime.cpp"):
+    """A shared library of these files of csrc and the stand-in; calls into files left out are never made
+    (their symbols are looked up when they are called)."""
+    here = os.path.dirname(os.path.abspath(__file__))
+    objs = []
+    for src in [os.path.join(_build.CSRC, s) for s in sources] + [os.path.join(here, fake)]:
+        objs.append(os.path.join(tmp, os.path.basename(src) + ".o"))
+        subprocess.run([_build.nvcc()] + _build.ARCH + _build.FLAGS + ["-Xcompiler", "-fno-stack-protector", "-c", src,
+                                                                       "-o", objs[-1]], check=True)
+    lib = os.path.join(tmp, "host.so")
+    subprocess.run([_build.nvcc(), "-shared", "-cudart", "none", "-Xlinker", "-Bsymbolic", "-Xlinker", "-z", "-Xlinker", "lazy",
+                    "-o", lib] + objs, check=True)
+    dl = ctypes.CDLL(None)
+    dl.dlopen.restype, dl.dlopen.argtypes = P, [ctypes.c_char_p, ctypes.c_int]
+    handle = dl.dlopen(lib.encode(), os.RTLD_LAZY | os.RTLD_LOCAL)
+    assert handle
+    lib = ctypes.CDLL(lib, handle=handle)
+    lib.fake_launch.restype = ctypes.c_char_p
+    for name in ("sparda_evict_blocks", "sparda_kv4_evict_blocks", "sparda_kv4_decode_attn"):
+        getattr(lib, name).argtypes = getattr(sb.lib, name).argtypes
+    return lib
+
+
+@pytest.fixture(scope="module")
+def lib(tmp_path_factory):
+    return compiled(str(tmp_path_factory.mktemp("host")), ["api.cu", "evict.cu"])
+
+
+def _names(lib):
+    full = [lib.fake_launch(i).decode() for i in range(lib.fake_launches())]
+    return [n[n.index("evict_"):n.index("_kernel")] for n in full]
+
+
+def _evict(lib, kv4, in_place):
+    s = sb.Shape(max_batch=2, max_ctx=4096)
+    d = sb.Shape(max_batch=2, max_ctx=1024)
+    mk = (lambda at: ctypes.byref(sb.c_layer_kv4(at, at << 1))) if kv4 else \
+        (lambda at: ctypes.byref(sb.c_layer_kv(at, at << 1, at << 2, None, None, 0, 0)))
+    fn = lib.sparda_kv4_evict_blocks if kv4 else lib.sparda_evict_blocks
+    dst = (None,) * 4 if in_place else (ctypes.byref(d.c()), mk(1 << 40), P(1 << 21), P(1 << 23))
+    return fn(ctypes.byref(s.c()), mk(1 << 32), P(1 << 20), P(1 << 22), *dst, 2, 8, 2, P(1 << 25), None)
+
+
+ORDER = {True: ["evict_select", "evict_shift", "evict_join", "evict_length"], False: ["evict_select", "evict_move"]}
+
+
+@pytest.mark.parametrize("in_place", [True, False])
+@pytest.mark.parametrize("kv4", [True, False])
+def test_an_eviction_stops_at_a_refused_launch(lib, kv4, in_place):
+    """Nothing is launched behind the refused one, the call reports it, and no error is left behind."""
+    order = ORDER[in_place]
+    for nth in range(len(order) + 1):
+        lib.fake_reset(nth, TOO_LARGE)
+        status = _evict(lib, kv4, in_place)
+        assert status == (sb.ERR_CUDA if nth < len(order) else sb.OK), nth
+        assert _names(lib) == order[:nth]
+        assert lib.fake_last_error() == 0
+
+
+def test_an_eviction_in_place_that_no_sm_can_hold_launches_nothing(tmp_path):
+    lib = compiled(str(tmp_path), ["api.cu", "evict.cu"])
+    lib.fake_reset(-1, 0)
+    lib.fake_set_ctas_per_sm(0)
+    for kv4 in (True, False):
+        assert _evict(lib, kv4, True) == sb.ERR_CUDA and _names(lib) == [] and lib.fake_last_error() == 0
+    lib.fake_set_ctas_per_sm(1)
+    assert _evict(lib, True, True) == sb.OK and _names(lib) == ORDER[True]
