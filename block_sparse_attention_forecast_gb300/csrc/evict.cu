@@ -42,12 +42,19 @@ constexpr int kMoveThreads = 256;
 constexpr int kMoveSlots = 2;
 constexpr int kMoveBytes = 64 * 1024;
 constexpr uint32_t kMovePolls = 1u << 25;                       // bounds a lane's wait to seconds
-constexpr uint32_t kShiftPolls = 1u << 22;                      // the same, each a round trip to L2
+// The same, each a round trip to L2. (A test builds this file with a limit that runs out.)
+#ifndef SPARDA_SHIFT_POLLS
+#define SPARDA_SHIFT_POLLS (1u << 22)
+#endif
+constexpr uint32_t kShiftPolls = SPARDA_SHIFT_POLLS;
 // Shared memory of the shift's CTAs on an SM, a block each. With the selection, 4 sequences of bf16 blocks to 512:
 // 81 us at 72 KiB, 70 at 140, 68 at 175, 67 at 210; 16 sequences in 4 bits to 512: 129, 112, 110, 108. (A cluster
 // per group that reads a round of blocks before it writes it: 125 and 146; of one sequence 103, this 23.)
 constexpr int kShiftBytes = 175 * 1024;
-constexpr int kUnread = 1 << 30;                                // kept: a block that moves and has not been read
+// In the kept list while a cache is cut in place: a block that moves and has not been read. On the first
+// entry of a sequence's first group, block 0, which never moves: a wait ran out and blocks of the sequence
+// were left.
+constexpr int kUnread = 1 << 30;
 constexpr int kCkRow = kHeadDim * 2;                            // bytes of a compressed key
 
 __device__ __forceinline__ bool valid_len(int T, int nb) { return T >= 1 && T <= nb * kBlock; }
@@ -90,6 +97,10 @@ __device__ __forceinline__ int window_bytes(int n, int count, int T, bool neighb
   const int complete = num_windows(T) - 4 * n;
   const int own = n + 1 < count && neighbour ? 4 : 3;
   return min(max(complete, 0), own) * kCkRow;
+}
+// Whether the shift left blocks of sequence b (of a valid length) where they were.
+__device__ __forceinline__ bool left_blocks(const EvictArgs& a, int b) {
+  return (a.kept[(size_t)b * a.G * a.keep] & kUnread) != 0;
 }
 // Whether window 4n+3 has to be formed anew.
 __device__ __forceinline__ bool joins(int n, int count, int T, bool neighbour) {
@@ -317,15 +328,19 @@ __global__ void __launch_bounds__(32) evict_shift_kernel(const EvictArgs a) {
   uint8_t* slot = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_shift) + 127) & ~static_cast<uintptr_t>(127));
   const int groups = a.B * a.G, items = groups * a.keep;
   uint32_t phase = 0;
-  bool ok = true;                                  // until a wait runs out: then nothing more is moved, but
+  bool ok = true;                                  // until a wait runs out: then nothing more is moved
   for (int item = blockIdx.x; item < items; item += gridDim.x) {
     const int bg = item % groups, n = item / groups;
     int32_t* kept = a.kept + (size_t)bg * a.keep;
-    const int v = kept[n];
-    if (v < 0 || !(v & kUnread)) continue;         // behind the last block, or already in place with its windows
-    const int j = v ^ kUnread;
-    if (!ok) {                                     // the marks go on being cleared, so that nobody waits for them
+    const int v = kept[n], j = v & ~kUnread;
+    if (v < 0 || !(v & kUnread) || j == n) continue;     // behind the last block, or already in place with its windows
+    // a block is left: its sequence is marked, its own mark cleared, so that nobody waits for it
+    const auto leave = [&]() {
+      atomicOr(a.kept + (size_t)(bg / a.G) * a.G * a.keep, kUnread);
       asm volatile("st.release.gpu.global.s32 [%0], %1;" ::"l"(kept + n), "r"(j) : "memory");
+    };
+    if (!ok) {
+      leave();
       continue;
     }
     const int T0 = a.src_len[bg / a.G];
@@ -346,7 +361,7 @@ __global__ void __launch_bounds__(32) evict_shift_kernel(const EvictArgs a) {
     }
     ok = mbar_wait(&full, phase, a.err);
     phase ^= 1;
-    asm volatile("st.release.gpu.global.s32 [%0], %1;" ::"l"(kept + n), "r"(j) : "memory");
+    if (ok) asm volatile("st.release.gpu.global.s32 [%0], %1;" ::"l"(kept + n), "r"(j) : "memory");
     if (ok && lo < n && (kept[lo] & ~kUnread) == n) {
       uint32_t polls = 0;
       for (;;) {
@@ -360,7 +375,10 @@ __global__ void __launch_bounds__(32) evict_shift_kernel(const EvictArgs a) {
         }
       }
     }
-    if (!ok) continue;
+    if (!ok) {
+      leave();
+      continue;
+    }
     for (int p = 0; p < a.planes; ++p)
       bulk_store(a.dst[p] + ((size_t)bg * a.dst_nb + n) * a.block_bytes, slot + p * a.block_bytes, a.block_bytes);
     if (ck) bulk_store(a.dst_ck + (row + 4 * n) * kHeadDim, slot + a.planes * a.block_bytes, ck);
@@ -382,6 +400,7 @@ __global__ void __launch_bounds__(kMoveThreads) evict_join_kernel(const EvictArg
   if (!valid_len(T0, a.src_nb)) return;
   const int32_t* kept = a.kept + (size_t)bg * a.keep;
   const int count = min(blocks_of(T0), a.keep);
+  if (left_blocks(a, bg / a.G)) return;
   if (blockIdx.x % pieces == 0) {
     float* mass = a.dst_mass + (size_t)bg * a.dst_nb;
     float w[kMaxCtx / kBlock / kMoveThreads];
@@ -408,7 +427,11 @@ __global__ void evict_length_kernel(const EvictArgs a) {
   grid_dep_launch();
   for (int b = threadIdx.x; b < a.B; b += blockDim.x) {
     const int T = a.src_len[b];
-    if (valid_len(T, a.src_nb)) a.dst_len[b] = kept_len(T, a.keep);
+    if (!valid_len(T, a.src_nb)) continue;
+    if (left_blocks(a, b))
+      a.kept[(size_t)b * a.G * a.keep] = 0;        // block 0, without the mark
+    else
+      a.dst_len[b] = kept_len(T, a.keep);
   }
 }
 

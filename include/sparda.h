@@ -695,6 +695,8 @@ int32_t sparda_sparse_decode_attn_mass(const sparda_shape* shape, const sparda_l
  * max_ctx >= 64 keep, smaller or larger than the source's) that shares no memory with the source,
  * dst_mass float32 [max_batch, G, max_ctx/64] of dst_shape, dst_seq_len int32 [B], and the source
  * stays as it was. kept: int32 [B, G, keep], written: the old block numbers, ascending, -1 behind.
+ * A wait inside the move that runs out sets SPARDA_DEV_WAIT_TIMEOUT; in place, a sequence with a block that
+ * was not moved then keeps its seq_len and its mass (its cache holds neither the old blocks nor the new).
  * A sequence with a seq_len out of range keeps everything as it is (kept -1; into another cache,
  * its length is copied) and sets SPARDA_DEV_BAD_SEQ_LEN. Sequences at and past batch stay as they were.
  *

@@ -397,3 +397,51 @@ def test_evict_weights_of_the_batch_side_by_side(sb, kv4):
                 assert kept[b, g].tolist() == want
                 assert torch.equal(dm.view(2, G, keep)[b, g].cpu(), mass[b, g][want])
         assert (both[-8:] == 3).all()
+
+
+@pytest.mark.parametrize("kv4", [False, True])
+def test_evict_in_place_whose_waits_run_out(sb, kv4, tmp_path, monkeypatch):
+    """A build of the eviction that gives a wait up at its first look, over shifts by one block, in which nearly
+    every write waits. The call reports it; a sequence of which a block was left keeps its length and
+    weights, any other is cut as it should be."""
+    from tests.test_launch_errors import compiled
+    B, G, n = 5, 2, 700
+    T = [64 * n - 3, 64 * n, 64 * (n - 1), 100, 64 * n - 60]          # two of them have nothing to move
+    keep = n - 1
+    lib = compiled(str(tmp_path), ["api.cu", "evict.cu", "attn.cu"], fake=None, extra=["-DSPARDA_SHIFT_POLLS=0"])
+    shape = sb.Shape(n_groups=G, max_ctx=64 * n, max_batch=B)
+    gen = torch.Generator(device="cuda").manual_seed(43)
+    raw = torch.randint(0, 256, (B, G, n, 10240 if kv4 else 16384), generator=gen, dtype=torch.uint8, device="cuda")
+    ck = torch.zeros((B, G, shape.w_cap, 128), dtype=torch.bfloat16, device="cuda")
+    if kv4:
+        layer = sb.LayerKV4(raw.clone(), ck)
+    else:
+        k = raw.clone().view(torch.bfloat16).view(B, G, 64 * n, 128)
+        layer = sb.LayerKV(k, k.clone(), ck)
+    mass0 = torch.rand((B, G, n), generator=gen, device="cuda") + 1
+    mass0[:, :, 1] = 0                                                # the block to go, where one does
+    mass, seq = mass0.clone(), _i32(T)
+    kept = torch.full((B, G, keep), -7, dtype=torch.int32, device="cuda")
+    monkeypatch.setattr(sb, "lib", lib)
+    (sb.sparda_kv4_evict_blocks if kv4 else sb.sparda_evict_blocks)(shape, layer, mass, seq, B, keep, 1, kept)
+    torch.cuda.synchronize()
+    assert sb.sparda_device_error(clear=True) == sb.DEV_WAIT_TIMEOUT
+    left = 0
+    for b in range(B):
+        cut = T[b] > 64 * keep
+        blocks = [0] + list(range(2, n)) if cut else list(range((T[b] - 1) // 64 + 1))
+        want = torch.tensor(blocks, device="cuda")
+        if cut and int(seq[b]) == T[b]:
+            left += 1
+            assert torch.equal(mass[b], mass0[b])
+        else:
+            assert int(seq[b]) == T[b] - (64 if cut else 0)
+            for g in range(G):
+                m = torch.zeros(n, device="cuda")
+                m[:len(blocks)] = mass0[b, g][want]
+                assert torch.equal(mass[b, g], m)
+                got = layer.kv[b, g] if kv4 else layer.k[b, g].reshape(n, -1).view(torch.uint8)
+                assert torch.equal(got[:len(blocks)], raw[b, g][want])
+        for g in range(G):
+            assert kept[b, g].tolist() == blocks + [-1] * (keep - len(blocks))
+    assert left >= 1

@@ -16,25 +16,27 @@ P = ctypes.c_void_p
 TOO_LARGE = 720                                    # cudaErrorCooperativeLaunchTooLarge
 
 
-def compiled(tmp, sources, fake="fake_cuda_runtime.cpp"):
-    """A shared library of these files of csrc and the stand-in; calls into files left out are never made
-    (their symbols are looked up when they are called)."""
-    here = os.path.dirname(os.path.abspath(__file__))
+def compiled(tmp, sources, fake="fake_cuda_runtime.cpp", extra=()):
+    """A shared library of these files of csrc and the stand-in (fake=None: the CUDA runtime itself); calls
+    into files left out are never made (their symbols are looked up when they are called)."""
+    files = [os.path.join(_build.CSRC, s) for s in sources]
+    if fake:
+        files.append(os.path.join(os.path.dirname(os.path.abspath(__file__)), fake))
     objs = []
-    for src in [os.path.join(_build.CSRC, s) for s in sources] + [os.path.join(here, fake)]:
+    for src in files:
         objs.append(os.path.join(tmp, os.path.basename(src) + ".o"))
-        subprocess.run([_build.nvcc()] + _build.ARCH + _build.FLAGS + ["-Xcompiler", "-fno-stack-protector", "-c", src,
-                                                                       "-o", objs[-1]], check=True)
+        subprocess.run([_build.nvcc()] + _build.ARCH + _build.FLAGS + list(extra) + ["-c", src, "-o", objs[-1]], check=True)
     lib = os.path.join(tmp, "host.so")
-    subprocess.run([_build.nvcc(), "-shared", "-cudart", "none", "-Xlinker", "-Bsymbolic", "-Xlinker", "-z", "-Xlinker", "lazy",
-                    "-o", lib] + objs, check=True)
+    subprocess.run([_build.nvcc()] + _build.ARCH + ["-shared", "-cudart", "none" if fake else "static", "-Xlinker", "-Bsymbolic",
+                                                    "-Xlinker", "-z", "-Xlinker", "lazy", "-o", lib] + objs, check=True)
     dl = ctypes.CDLL(None)
     dl.dlopen.restype, dl.dlopen.argtypes = P, [ctypes.c_char_p, ctypes.c_int]
     handle = dl.dlopen(lib.encode(), os.RTLD_LAZY | os.RTLD_LOCAL)
     assert handle
     lib = ctypes.CDLL(lib, handle=handle)
-    lib.fake_launch.restype = ctypes.c_char_p
-    for name in ("sparda_evict_blocks", "sparda_kv4_evict_blocks", "sparda_kv4_decode_attn"):
+    if fake:
+        lib.fake_launch.restype = ctypes.c_char_p
+    for name in ("sparda_evict_blocks", "sparda_kv4_evict_blocks", "sparda_kv4_decode_attn", "sparda_device_error"):
         getattr(lib, name).argtypes = getattr(sb.lib, name).argtypes
     return lib
 
