@@ -138,6 +138,13 @@ int32_t cuda_status(cudaError_t e) {
   return SPARDA_ERR_CUDA;
 }
 
+// The status of a call whose launches gave `e`. An error that a launch left for cudaGetLastError() is this
+// call's and is taken from there, so that the next call does not report it.
+int32_t launched(cudaError_t e) {
+  const cudaError_t left = cudaGetLastError();
+  return cuda_status(e != cudaSuccess ? e : left);
+}
+
 // ------------------------------------------------------------------ TMA tensor maps
 typedef CUresult (*EncodeTiledFn)(CUtensorMap*, CUtensorMapDataType, cuuint32_t, void*,
                                   const cuuint64_t*, const cuuint64_t*, const cuuint32_t*,
@@ -862,13 +869,13 @@ int32_t sparda_kv4_decode_attn(const sparda_shape* s, const sparda_layer_kv4* L,
     a.stats = reinterpret_cast<float2*>(stats);
     a.ml = reinterpret_cast<float*>(stats + mass_stats_bytes(s, kv4_mass_slots(s)));
   }
-  const int parts = launch_kv4_attn(a, st);
-  if (parts < 0) return SPARDA_ERR_CUDA;
-  if (parts > 0) {
+  int parts = 0;
+  const cudaError_t run = launch_kv4_attn(a, st, &parts);
+  if (run == cudaSuccess && parts > 0) {           // (without the attention the statistics are another call's)
     BlockMassArgs m{a.stats, a.ml, mass, idx, cnt, seq_len, s->n_groups, s->heads_per_group, s->max_ctx, nb_cap(s), slots, parts};
     launch_block_mass(m, batch * s->n_groups, st);
   }
-  return cuda_status(cudaGetLastError());
+  return launched(run);
 }
 
 // ------------------------------------------------------------------ block mass and eviction
@@ -886,11 +893,13 @@ int32_t sparda_sparse_decode_attn_mass(const sparda_shape* s, const sparda_layer
   a.ml = reinterpret_cast<float*>(stats + mass_stats_bytes(s, kslots(s)));
   a.mass = mass;
   const cudaStream_t st = static_cast<cudaStream_t>(stream);
-  if (launch_sparse_attn(a, mk, mv, hk, hv, batch * s->n_groups, st)) {
+  bool mass_left = false;
+  const cudaError_t run = launch_sparse_attn(a, mk, mv, hk, hv, batch * s->n_groups, st, &mass_left);
+  if (run == cudaSuccess && mass_left) {
     BlockMassArgs m{a.stats, a.ml, mass, idx, cnt, seq_len, s->n_groups, kHeads, s->max_ctx, nb_cap(s), kslots(s), 4};
     launch_block_mass(m, batch * s->n_groups, st);
   }
-  return cuda_status(cudaGetLastError());
+  return launched(run);
 }
 
 }  // extern "C"
@@ -918,13 +927,6 @@ bool evict_overlap(const EvictArgs& a, const sparda_shape* s, const sparda_shape
   const size_t rows = (size_t)batch * s->n_groups;
   return overlap(a.src_mass, rows * a.src_nb * 4, a.dst_mass, rows * a.dst_nb * 4) ||
          overlap(a.src_len, (size_t)batch * 4, a.dst_len, (size_t)batch * 4);
-}
-
-// The status of a call whose launches gave `e`. An error that a launch left for cudaGetLastError() is this
-// call's and is taken from there, so that the next call does not report it.
-int32_t launched(cudaError_t e) {
-  const cudaError_t left = cudaGetLastError();
-  return cuda_status(e != cudaSuccess ? e : left);
 }
 
 // What both evictions check and hand on beside their cache planes, which *a holds already.

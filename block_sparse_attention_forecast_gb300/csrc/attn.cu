@@ -51,9 +51,9 @@ int sm_count() {
 }
 
 
-bool launch_sparse_attn(const AttnArgs& a, const CUtensorMap& mk, const CUtensorMap& mv,
-                        const CUtensorMap& hk, const CUtensorMap& hv, int bg_count,
-                        cudaStream_t s) {
+cudaError_t launch_sparse_attn(const AttnArgs& a, const CUtensorMap& mk, const CUtensorMap& mv,
+                               const CUtensorMap& hk, const CUtensorMap& hv, int bg_count,
+                               cudaStream_t s, bool* mass_left) {
   AttnArgs b = a;
   b.n_units = bg_count * a.kslots;
   const int sms = sm_count();
@@ -97,8 +97,8 @@ bool launch_sparse_attn(const AttnArgs& a, const CUtensorMap& mk, const CUtensor
   attr[1].val.clusterDim.z = 1;
   cfg.attrs = attr;
   cfg.numAttrs = cluster ? 2 : 1;
-  cudaLaunchKernelEx(&cfg, kern, b, mk, mv, hk, hv);
-  return !cluster;
+  if (mass_left) *mass_left = !cluster;
+  return cudaLaunchKernelEx(&cfg, kern, b, mk, mv, hk, hv);
 }
 
 }  // namespace sparda

@@ -142,10 +142,10 @@ void launch_compress_keys(const CompressArgs& a, int bg_count, cudaStream_t s);
 void launch_forecast_project(const ProjectArgs& a, cudaStream_t s);
 void launch_forecast_select(const SelectArgs& a, int bg_count, cudaStream_t s);
 // maps: K and V of the resident cache or of the staging buffer, then hot K and V (offload).
-// Returns whether the block mass (where wanted) is still to be added, by launch_block_mass.
-bool launch_sparse_attn(const AttnArgs& a, const CUtensorMap& mk, const CUtensorMap& mv,
-                        const CUtensorMap& hk, const CUtensorMap& hv, int bg_count,
-                        cudaStream_t s);
+// *mass_left: whether the block mass (where wanted) is still to be added, by launch_block_mass.
+cudaError_t launch_sparse_attn(const AttnArgs& a, const CUtensorMap& mk, const CUtensorMap& mv,
+                               const CUtensorMap& hk, const CUtensorMap& hv, int bg_count,
+                               cudaStream_t s, bool* mass_left = nullptr);
 void launch_prefetch(const PrefetchArgs& a, int n_ctas, cudaStream_t s);
 void launch_attend_and_select(const AttnArgs& a, const SelectArgs& s, const CUtensorMap& mk,
                               const CUtensorMap& mv, const CUtensorMap& hk, const CUtensorMap& hv,
@@ -228,9 +228,9 @@ struct Kv4AttnArgs {
   int* err;
   int G, H, max_ctx, nb_cap, kslots, bg_count;
 };
-// The stats' parts per block (2 or 4) where the block mass is still to be added by launch_block_mass,
-// 0 where there is nothing left to do, -1 if nothing was launched.
-int launch_kv4_attn(const Kv4AttnArgs& a, cudaStream_t s);
+// *parts: the stats' parts per block (2 or 4) where the block mass is still to be added by launch_block_mass,
+// else 0.
+cudaError_t launch_kv4_attn(const Kv4AttnArgs& a, cudaStream_t s, int* parts);
 
 // Accumulates the attention weight of each attended block (block_mass.cu).
 struct BlockMassArgs {

@@ -816,18 +816,20 @@ __global__ void __launch_bounds__(kThreads4, 1) kv4_attn_kernel(const Kv4AttnArg
 namespace {
 
 template <int kW, bool kStats, bool kCluster, bool kEight>
-int launch_form(const Kv4AttnArgs& a, int grid, int cluster, cudaStream_t s) {
+cudaError_t launch_form(const Kv4AttnArgs& a, int grid, int cluster, cudaStream_t s, int* parts) {
   auto kern = kv4_attn_kernel<kW, kStats, kCluster, kEight>;
   constexpr int smem = !kCluster ? kSmem4 : kStats ? kMassSmem4 : kClusterSmem4;
   static_assert(smem <= 232448, "shared memory of a CTA");
   // the register split needs the registers that it counts on; a build with fewer must not run
-  static const bool fits = [&] {
+  static std::atomic<bool> fits{false};
+  if (!fits.load(std::memory_order_relaxed)) {
     cudaFuncAttributes at;
-    return cudaFuncGetAttributes(&at, kern) == cudaSuccess &&
-           at.numRegs * kThreads4 >= 128 * kProducerRegs + kCThreads * kConsumerRegs;
-  }();
+    const cudaError_t err = cudaFuncGetAttributes(&at, kern);
+    if (err != cudaSuccess) return err;
+    fits.store(at.numRegs * kThreads4 >= 128 * kProducerRegs + kCThreads * kConsumerRegs, std::memory_order_relaxed);
+  }
   static SmemOptIn opt_in;
-  if (!fits || !opt_in.set(kern, smem)) return -1;
+  if (!fits || !opt_in.set(kern, smem)) return cudaErrorLaunchOutOfResources;
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3(grid);
   cfg.blockDim = dim3(kThreads4);
@@ -842,22 +844,22 @@ int launch_form(const Kv4AttnArgs& a, int grid, int cluster, cudaStream_t s) {
   attr[1].val.clusterDim.z = 1;
   cfg.attrs = attr;
   cfg.numAttrs = kCluster ? 2 : 1;
-  cudaLaunchKernelEx(&cfg, kern, a, cluster);
-  return !kStats || kCluster ? 0 : kW == 4 ? 4 : 2;
+  *parts = !kStats || kCluster ? 0 : kW == 4 ? 4 : 2;
+  return cudaLaunchKernelEx(&cfg, kern, a, cluster);
 }
 
 template <int kW, bool kCluster>
-int launch_form(const Kv4AttnArgs& a, int grid, int cluster, cudaStream_t s) {
+cudaError_t launch_form(const Kv4AttnArgs& a, int grid, int cluster, cudaStream_t s, int* parts) {
   if (a.H <= 8)
-    return a.stats ? launch_form<kW, true, kCluster, true>(a, grid, cluster, s)
-                   : launch_form<kW, false, kCluster, true>(a, grid, cluster, s);
-  return a.stats ? launch_form<kW, true, kCluster, false>(a, grid, cluster, s)
-                 : launch_form<kW, false, kCluster, false>(a, grid, cluster, s);
+    return a.stats ? launch_form<kW, true, kCluster, true>(a, grid, cluster, s, parts)
+                   : launch_form<kW, false, kCluster, true>(a, grid, cluster, s, parts);
+  return a.stats ? launch_form<kW, true, kCluster, false>(a, grid, cluster, s, parts)
+                 : launch_form<kW, false, kCluster, false>(a, grid, cluster, s, parts);
 }
 
 }  // namespace
 
-int launch_kv4_attn(const Kv4AttnArgs& a, cudaStream_t s) {
+cudaError_t launch_kv4_attn(const Kv4AttnArgs& a, cudaStream_t s, int* parts) {
   const int sms = sm_count() < kKv4MaxCtas ? sm_count() : kKv4MaxCtas;
   const int slots = a.idx ? a.kslots : a.nb_cap;
   const long long bound = (long long)a.bg_count * slots;
@@ -873,16 +875,16 @@ int launch_kv4_attn(const Kv4AttnArgs& a, cudaStream_t s) {
   // Without a list, slots is the capacity: sequences may be far shorter, which the plan takes into account.
   if ((a.idx || share <= kClusterBlocks) && waves * (share + kCtaCost) <= planned) {
     const int ctas = cluster * a.bg_count;
-    return share > kWholeBlocks * kCWarps ? launch_form<1, true>(a, ctas, cluster, s)
-           : share > kPairBlocks          ? launch_form<2, true>(a, ctas, cluster, s)
-                                          : launch_form<4, true>(a, ctas, cluster, s);
+    return share > kWholeBlocks * kCWarps ? launch_form<1, true>(a, ctas, cluster, s, parts)
+           : share > kPairBlocks          ? launch_form<2, true>(a, ctas, cluster, s, parts)
+                                          : launch_form<4, true>(a, ctas, cluster, s, parts);
   }
   int grid = sms;
   const long long want = a.bg_count <= kPlanMax ? (bound + kMinUnits - 1) / kMinUnits : a.bg_count;
   if (want < grid) grid = (int)want;
   // whole blocks per warp once a warp has several
-  return bound >= (long long)kWholeBlocks * kCWarps * grid ? launch_form<1, false>(a, grid, 1, s)
-                                                           : launch_form<4, false>(a, grid, 1, s);
+  return bound >= (long long)kWholeBlocks * kCWarps * grid ? launch_form<1, false>(a, grid, 1, s, parts)
+                                                           : launch_form<4, false>(a, grid, 1, s, parts);
 }
 
 }  // namespace sparda

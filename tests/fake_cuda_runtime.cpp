@@ -13,7 +13,7 @@ std::map<const void*, std::string>& names() {
   return n;
 }
 std::vector<std::string> launches;
-int fail_at = -1, fail_code = 0, last_error = 0, ctas_per_sm = 32;
+int fail_at = -1, fail_code = 0, refused_attributes = 0, last_error = 0, ctas_per_sm = 32;
 char memory[64];
 
 int launch(const void* f) {
@@ -34,6 +34,8 @@ void fake_reset(int nth, int code) {
   fail_code = code;
   last_error = 0;
 }
+// the next question for a kernel's attributes fails
+void fake_refuse_attributes(int code) { refused_attributes = code; }
 void fake_set_ctas_per_sm(int n) { ctas_per_sm = n; }
 int fake_launches() { return (int)launches.size(); }
 const char* fake_launch(int i) { return launches[i].c_str(); }
@@ -95,9 +97,29 @@ int cudaMemset(void* p, int v, size_t n) {
 int cudaMemcpyAsync(void*, const void*, size_t, int, void*) { return 0; }
 int cudaDeviceSynchronize() { return 0; }
 int cudaPointerGetAttributes(void*, const void*) { return 1; }
-int cudaGetDriverEntryPointByVersion(...) { return 1; }
+int cudaDeviceGetAttribute(int* v, int, int) {
+  *v = 152;
+  return 0;
+}
+// of the attributes only the registers per thread, behind three sizes and the largest block
+int cudaFuncGetAttributes(void* at, const void*) {
+  if (refused_attributes) {
+    last_error = refused_attributes;
+    refused_attributes = 0;
+    return last_error;
+  }
+  static_cast<int*>(at)[7] = 168;
+  return 0;
+}
+// the one driver function that is looked up: encodes a tensor map
+int fake_encode(...) { return 0; }
+int cudaGetDriverEntryPointByVersion(const char*, void** f, unsigned, unsigned long long, int* found) {
+  *f = reinterpret_cast<void*>(&fake_encode);
+  *found = 0;
+  return 0;
+}
 }
 
 namespace sparda {
-int sm_count() { return 152; }
+__attribute__((weak)) int sm_count() { return 152; }      // (attn.cu's, where that is linked)
 }  // namespace sparda

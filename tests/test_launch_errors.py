@@ -1,5 +1,6 @@
 """What the library does when a CUDA launch is refused, on the CPU: its host code linked against a stand-in
 for the CUDA runtime that records the launches and refuses the n-th."""
+import concurrent.futures as futures
 import ctypes
 import os
 import subprocess
@@ -22,10 +23,10 @@ def compiled(tmp, sources, fake="fake_cuda_runtime.cpp", extra=()):
     files = [os.path.join(_build.CSRC, s) for s in sources]
     if fake:
         files.append(os.path.join(os.path.dirname(os.path.abspath(__file__)), fake))
-    objs = []
-    for src in files:
-        objs.append(os.path.join(tmp, os.path.basename(src) + ".o"))
-        subprocess.run([_build.nvcc()] + _build.ARCH + _build.FLAGS + list(extra) + ["-c", src, "-o", objs[-1]], check=True)
+    objs = [os.path.join(tmp, os.path.basename(src) + ".o") for src in files]
+    cmds = [[_build.nvcc()] + _build.ARCH + _build.FLAGS + list(extra) + ["-c", src, "-o", o] for src, o in zip(files, objs)]
+    with futures.ThreadPoolExecutor() as ex:
+        list(ex.map(lambda c: subprocess.run(c, check=True), cmds))
     lib = os.path.join(tmp, "host.so")
     subprocess.run([_build.nvcc()] + _build.ARCH + ["-shared", "-cudart", "none" if fake else "static", "-Xlinker", "-Bsymbolic",
                                                     "-Xlinker", "-z", "-Xlinker", "lazy", "-o", lib] + objs, check=True)
@@ -36,7 +37,8 @@ def compiled(tmp, sources, fake="fake_cuda_runtime.cpp", extra=()):
     lib = ctypes.CDLL(lib, handle=handle)
     if fake:
         lib.fake_launch.restype = ctypes.c_char_p
-    for name in ("sparda_evict_blocks", "sparda_kv4_evict_blocks", "sparda_kv4_decode_attn", "sparda_device_error"):
+    for name in ("sparda_evict_blocks", "sparda_kv4_evict_blocks", "sparda_kv4_decode_attn", "sparda_sparse_decode_attn_mass",
+                 "sparda_device_error"):
         getattr(lib, name).argtypes = getattr(sb.lib, name).argtypes
     return lib
 
@@ -85,3 +87,39 @@ def test_an_eviction_in_place_that_no_sm_can_hold_launches_nothing(tmp_path):
         assert _evict(lib, kv4, True) == sb.ERR_CUDA and _names(lib) == [] and lib.fake_last_error() == 0
     lib.fake_set_ctas_per_sm(1)
     assert _evict(lib, True, True) == sb.OK and _names(lib) == ORDER[True]
+
+
+@pytest.fixture(scope="module")
+def attn(tmp_path_factory):
+    return compiled(str(tmp_path_factory.mktemp("attn")), ["api.cu", "attn.cu", "kv4_attn.cu", "block_mass.cu"])
+
+
+def _attend(lib, kv4, B, mass, H=16):
+    s = sb.Shape(max_batch=B, max_ctx=4096, topk=62, heads_per_group=H)
+    layer = ctypes.byref(sb.c_layer_kv4(1 << 32, 1 << 33) if kv4 else
+                         sb.c_layer_kv(1 << 32, 1 << 33, 1 << 34, None, None, 0, 0))
+    p = P(1 << 20)
+    args = (ctypes.byref(s.c()), layer, p, p, p, p, B, p) + (P(1 << 22) if mass else None, p, 1 << 40, None)
+    return (lib.sparda_kv4_decode_attn if kv4 else lib.sparda_sparse_decode_attn_mass)(*args)
+
+
+@pytest.mark.parametrize("kv4", [True, False])
+def test_no_block_mass_behind_a_refused_attention(attn, kv4):
+    """The block mass is added from what the attention left: without the attention it must not be. 100
+    sequences take the forms that leave it to a launch of its own."""
+    kinds = lambda: ["mass" if b"block_mass" in attn.fake_launch(i) else "attention" for i in range(attn.fake_launches())]
+    attn.fake_reset(-1, 0)
+    assert _attend(attn, kv4, 100, True) == sb.OK and kinds() == ["attention", "mass"]
+    for nth in (0, 1):
+        attn.fake_reset(nth, 701)
+        assert _attend(attn, kv4, 100, True) == sb.ERR_CUDA and kinds() == ["attention"] * nth
+        assert attn.fake_last_error() == 0
+
+
+def test_a_failed_question_to_the_runtime_is_not_kept(attn):
+    """A call that cannot learn its kernel's registers fails and leaves no error behind; the next goes on."""
+    attn.fake_reset(-1, 0)
+    attn.fake_refuse_attributes(98)
+    assert _attend(attn, True, 2, False, H=4) == sb.ERR_CUDA
+    assert attn.fake_launches() == 0 and attn.fake_last_error() == 0
+    assert _attend(attn, True, 2, False, H=4) == sb.OK and attn.fake_launches() == 1
