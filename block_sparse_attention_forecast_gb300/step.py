@@ -425,11 +425,16 @@ class DecodeStack:
             self.seq_len.add_(1)
 
     def capture(self):
-        """Capture one step into a CUDA graph (after one eager warm-up step)."""
+        """Capture one step into a CUDA graph, after one eager warm-up step: a real step, which stores its
+        tokens and (with advance) moves seq_len. Only the block mass is put back to what it was before, so
+        that the steps that are replayed are the ones that count."""
         s = torch.cuda.Stream(device=self.device)
         s.wait_stream(torch.cuda.current_stream())
         with torch.cuda.stream(s):
+            mass = None if self.mass is None else self.mass.clone()
             self.enqueue()
+            if mass is not None:
+                self.mass.copy_(mass)
         torch.cuda.current_stream().wait_stream(s)
         torch.cuda.synchronize()
         self.graph = torch.cuda.CUDAGraph()

@@ -165,3 +165,29 @@ def test_stack_refuses(sb):
     W = torch.zeros((G * D, 256), dtype=torch.bfloat16, device="cuda")
     with pytest.raises(ValueError):
         DecodeStack(shape, layers, W, [W], 1, block_mass=True)
+
+
+@pytest.mark.parametrize("advance", [False, True])
+def test_capture_adds_nothing_to_the_mass(sb, advance):
+    """Captured and replayed once, a stack holds the mass of one eager step, on top of what it held before;
+    the capture alone leaves the mass as it was."""
+    T_list, seed = [700, 130], 630
+    st = _stack(sb, [True, False], T_list, 4, 1024, seed, block_mass=True, advance=advance)
+    _inputs(st, seed, 0)
+    start = torch.rand(st.mass.shape, generator=torch.Generator().manual_seed(seed)).cuda()
+    st.mass.copy_(start)
+    st.run()                                                      # eager
+    torch.cuda.synchronize()
+    want = st.mass.clone()
+    assert not torch.equal(want, start)
+    again = _stack(sb, [True, False], T_list, 4, 1024, seed, block_mass=True, advance=advance)
+    _inputs(again, seed, 0)
+    again.mass.copy_(start)
+    again.capture()
+    torch.cuda.synchronize()
+    assert torch.equal(again.mass, start)
+    again.seq_len.copy_(torch.tensor(T_list, dtype=torch.int32))  # the same token once more
+    again.run()
+    torch.cuda.synchronize()
+    assert sb.sparda_device_error(clear=True) == 0
+    assert torch.equal(again.mass, want) and torch.equal(again.out, st.out)
