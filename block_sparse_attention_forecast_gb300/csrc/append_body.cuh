@@ -8,8 +8,9 @@
 // [2^-40, 2^11), and zero, converts without loss, and 32 of them cannot overflow. GB300
 // issues float64 arithmetic at a small fraction of its integer rate, so the integer sum keeps
 // the append short. A window holding any other value (a subnormal, a magnitude of 2^11 or
-// more, a non-finite value) is summed in float64 instead, which is exact for bf16 keys of
-// ordinary range, and rounded to bf16 without double rounding.
+// more, a non-finite value) is summed in float64 instead, which is exact while its nonzero keys lie within a
+// factor of 2^40 of one another, and rounded to bf16 without double rounding. (window_mean below, for the
+// 4-bit cache and the eviction, is exact for every window.)
 #pragma once
 
 #include "common.cuh"
@@ -71,6 +72,59 @@ __device__ __forceinline__ uint16_t fixed_mean_to_bf16(long long S) {
   return (uint16_t)(sign + ((uint32_t)(p + 75) << 7) + (m - 128u));
 }
 
+// The mean of 32 bf16 values of any magnitudes, exact, rounded once to bf16 (nearest, ties to even); with an
+// infinity or a NaN among them what their sum is. The sum is an integer of 2^-133, the last bit of the smallest
+// subnormal, in words of 32 bits that take 42 before they are carried. For the rare window: `half` 0 or 1
+// of the 32 pairs at xs, in a loop over local memory.
+inline __device__ __noinline__ uint32_t any_mean(const uint32_t* xs, int half) {
+  constexpr int kWords = 9;                        // 254 + 8 + 5 bits
+  long long acc[kWords] = {};
+  float special = 0.f;
+#pragma unroll 1
+  for (int u = 0; u < kWinKernel; ++u) {
+    const uint32_t h = half ? xs[u] >> 16 : xs[u] & 0xffffu;
+    const int e = (int)((h >> 7) & 0xffu);
+    if (e == 255) special += __uint_as_float(h << 16);
+    const int at = max(e, 1) - 1;                  // x = m * 2^(at - 133)
+    const long long v = (long long)((h & 0x7fu) | (e ? 0x80u : 0u)) << (at & 31);
+    acc[at >> 5] += (h & 0x8000u) ? -v : v;
+  }
+  if (special != 0.f) return __bfloat16_as_ushort(__float2bfloat16_rn(special));
+  // carried: the words are the sum modulo 2^288, whose sign is the last carry's
+  long long carry = 0;
+#pragma unroll 1
+  for (int i = 0; i < kWords; ++i) {
+    acc[i] += carry;
+    carry = acc[i] >> 32;
+    acc[i] &= 0xffffffffll;
+  }
+  const uint32_t sign = carry < 0 ? 0x8000u : 0u;
+  if (sign) {
+    carry = 1;
+#pragma unroll 1
+    for (int i = 0; i < kWords; ++i) {
+      acc[i] = (~acc[i] & 0xffffffffll) + carry;
+      carry = acc[i] >> 32;
+      acc[i] &= 0xffffffffll;
+    }
+  }
+  int top = kWords - 1;
+  while (top > 0 && acc[top] == 0) --top;
+  if (acc[top] == 0) return 0u;                    // an exactly zero mean is +0
+  const int p = 32 * top + 31 - __clz((int)acc[top]);         // the sum is in [2^p, 2^(p+1)) times 2^-133
+  // The mean is the sum times 2^-138. It keeps 8 leading bits, or (subnormal) what lies above 2^-133.
+  const int cut = max(p - 7, 5);
+  const auto bit = [&](int i) { return (uint32_t)(acc[i >> 5] >> (i & 31)) & 1u; };
+  uint32_t m = 0u;
+  for (int i = p; i >= cut; --i) m = 2u * m + bit(i);
+  bool below = false;
+#pragma unroll 1
+  for (int i = 0; i < cut - 1 && !below; ++i) below = bit(i) != 0u;
+  if (bit(cut - 1) && (below || (m & 1u))) ++m;
+  // m = 256 carries into the exponent, and so does the subnormals' m = 128
+  return sign + (p >= 12 ? ((uint32_t)(p - 11) << 7) + m - 128u : m);
+}
+
 // The exact sum of 32 bf16 values, as two float32 numbers hi + lo. amax: their largest magnitude,
 // in [2^-64, 2^64). Each value is cut at u = 2^-12 of amax's power of two (adding and taking off 1.5 * 2^23 u
 // rounds to multiples of u): the upper parts are multiples of u below 2^19 u in sum, the lower parts
@@ -90,7 +144,7 @@ __device__ __forceinline__ float2 exact_sum(const float (&x)[kWinKernel], float 
 
 // The mean of 32 bf16 pairs, per half-word, rounded once to bf16: a compression window's
 // compressed key for two channels. A window of ordinary values is summed in float32 (exact_sum), at
-// 8 instructions per value; any other through the fixed-point or the float64 sum of the append.
+// 8 instructions per value; one of the append's wide range in fixed point; any other by any_mean.
 __device__ __forceinline__ uint32_t window_mean(const uint32_t (&xs)[kWinKernel]) {
   uint32_t top = 0u, low = 0xffffffffu;            // per half: largest magnitude, smallest nonzero one less 1
 #pragma unroll
@@ -131,14 +185,10 @@ __device__ __forceinline__ uint32_t window_mean(const uint32_t (&xs)[kWinKernel]
     S1 += bf16_to_fixed(xs[u] >> 16, in_range);
   }
   if (in_range) return (uint32_t)fixed_mean_to_bf16(S0) | ((uint32_t)fixed_mean_to_bf16(S1) << 16);
-  double s0 = 0.0, s1 = 0.0;
+  uint32_t ys[kWinKernel];                         // a copy, so that xs stays in registers
 #pragma unroll
-  for (int u = 0; u < kWinKernel; ++u) {
-    s0 += bf16_lo(xs[u]);
-    s1 += bf16_hi(xs[u]);
-  }
-  const __nv_bfloat16 b0 = f64_to_bf16_rn(s0 / kWinKernel), b1 = f64_to_bf16_rn(s1 / kWinKernel);
-  return (uint32_t)__bfloat16_as_ushort(b0) | ((uint32_t)__bfloat16_as_ushort(b1) << 16);
+  for (int u = 0; u < kWinKernel; ++u) ys[u] = xs[u];
+  return any_mean(ys, 0) | (any_mean(ys, 1) << 16);
 }
 
 // The append of sequence-group `bg` by 64 threads; thread t (0..63) owns dims 2t and 2t+1.

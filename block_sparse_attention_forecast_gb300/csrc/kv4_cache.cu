@@ -215,8 +215,8 @@ __global__ void __launch_bounds__(kQThreads) kv4_dequantize_kernel(const Kv4Cach
 }
 
 // One decode token: 64 threads per (sequence, group), thread t owns channels 2t and 2t+1 of the
-// key and of the value. When the token completes a compression window the same threads sum the
-// window's 32 stored keys exactly (fixed point, as the bf16 cache's append does).
+// key and of the value. When the token completes a compression window the same threads form the exact
+// mean of the window's 32 stored keys (window_mean).
 constexpr int kAppendPerCta4 = 4;
 
 __global__ void __launch_bounds__(64 * kAppendPerCta4) kv4_append_kernel(const Kv4CacheArgs a, int bg_count) {

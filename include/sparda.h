@@ -181,7 +181,8 @@ int32_t sparda_prefetch_default_ctas(int32_t batch);
  * once to bf16, nearest even. Each dimension's window sum is formed exactly in a 64-bit
  * fixed-point integer (47 fractional bits) when every key of the window is zero or of
  * magnitude in [2^-40, 2^11); otherwise in float64, rounded to bf16 through a round-to-odd
- * float32 so that no double rounding occurs. Both give the same bf16 code as the exact mean.
+ * float32 so that no double rounding occurs. Both give the same bf16 code as the exact mean, the
+ * second as long as the window's nonzero keys lie within a factor of 2^40 of one another.
  * Offloaded layers: the token goes to the hot tail slot; when it fills its block (T % 64
  * == 0) that block is also written to the host cache, so that a later gather finds it.
  */

@@ -445,3 +445,104 @@ def test_evict_in_place_whose_waits_run_out(sb, kv4, tmp_path, monkeypatch):
         for g in range(G):
             assert kept[b, g].tolist() == blocks + [-1] * (keep - len(blocks))
     assert left >= 1
+
+
+def _wide_windows(n, seed):
+    """[n, 32] bf16 values (as floats) whose mean is lost unless all of every value counts: large ones that
+    cancel beside small ones, over all exponents, subnormals, sums at and beside a tie, the largest values."""
+    rng = np.random.default_rng(seed)
+    sig = lambda size: rng.integers(128, 256, size=size).astype(np.float64) * rng.choice([-1.0, 1.0], size=size)
+    x = np.zeros((n, 32))
+    for i in range(n):
+        kind = i % 6
+        if kind == 0:                                    # a small rest behind what cancels
+            pairs = rng.integers(1, 16)
+            big = sig(pairs) * 2.0 ** rng.integers(-133, 121, size=pairs)
+            x[i, :2 * pairs] = np.concatenate([big, -big])
+            x[i, 2 * pairs:] = sig(32 - 2 * pairs) * 2.0 ** rng.integers(-133, 121)
+        elif kind == 1:                                  # any exponents at all
+            x[i] = sig(32) * 2.0 ** rng.integers(-133, 121, size=32)
+        elif kind == 2:                                  # subnormals and a little more
+            x[i] = rng.integers(-255, 256, size=32) * 2.0 ** -133
+        elif kind == 3:                                  # a tie of the mean, and a last bit beside it or not
+            e = rng.integers(-100, 100)
+            x[i, 0], x[i, 1] = rng.integers(128, 256) * 2.0 ** e, 2.0 ** (e - 1)
+            x[i, 2] = rng.integers(-1, 2) * 2.0 ** max(e - rng.integers(2, 60), -133)
+            x[i, 3:5] = (2.0 ** 120, -2.0 ** 120)
+        elif kind == 4:                                  # the largest
+            x[i] = 255 * 2.0 ** 120 * (1 if i % 12 < 6 else rng.choice([-1.0, 1.0], size=32))
+        else:
+            x[i, :3] = (2.0 ** 60, 1.0, -2.0 ** 60)
+        x[i] = rng.permutation(x[i])
+    y = torch.from_numpy(x).to(torch.bfloat16)
+    assert np.array_equal(y.double().numpy(), x)         # bf16 values as they stand
+    return y
+
+
+def test_joined_windows_of_any_magnitudes(sb):
+    """As above for windows beyond every range that has a shorter way; infinities and NaN as a sum has them."""
+    ctx, keep, lost = 64 * 40, 20, 20
+    shape = sb.Shape(n_groups=2, max_ctx=ctx, max_batch=1)
+    blocks = list(range(0, 38, 2)) + [39]
+    rows = _wide_windows(2 * (keep - 1) * 128, 511).view(2, keep - 1, 128, 32)
+    rows[0, 0, :4, 7] = torch.tensor([float("inf"), float("-inf"), float("nan"), float("inf")]).to(torch.bfloat16)
+    rows[0, 0, 3, 8] = float("-inf")
+    K = torch.zeros((1, 2, ctx, 128), dtype=torch.bfloat16)
+    for i in range(keep - 1):
+        a, b = 64 * blocks[i] + 48, 64 * blocks[i + 1]
+        K[0, :, a:a + 16] = rows[:, i, :, :16].transpose(1, 2)
+        K[0, :, b:b + 16] = rows[:, i, :, 16:].transpose(1, 2)
+    mass = torch.zeros((1, 2, 40), device="cuda")
+    mass[:, :, blocks[1:-1]] = 1
+    for in_place in (True, False):
+        layer = sb.LayerKV.empty(shape)
+        layer.k.copy_(K.cuda())
+        layer.v.zero_()
+        kept, seq, m = torch.zeros((1, 2, keep), dtype=torch.int32, device="cuda"), _i32([ctx]), mass.clone()
+        if in_place:
+            sb.sparda_evict_blocks(shape, layer, m, seq, 1, keep, 1, kept)
+            ck = layer.ck
+        else:
+            dshape = sb.Shape(n_groups=2, max_ctx=64 * keep, max_batch=1)
+            dst = sb.LayerKV.empty(dshape)
+            sb.sparda_evict_blocks(shape, layer, m, seq, 1, keep, 1, kept, dst_shape=dshape, dst=dst,
+                                   dst_mass=torch.zeros((1, 2, keep), device="cuda"), dst_seq_len=_i32([0]))
+            ck = dst.ck
+        torch.cuda.synchronize()
+        assert sb.sparda_device_error(clear=True) == 0
+        assert kept[0, 0].tolist() == blocks and kept[0, 1].tolist() == blocks
+        for g in range(2):
+            for i in range(keep - 1):
+                got, w = to64(ck[0, g, 4 * i + 3]), rows[g, i].double().numpy()
+                for c in range(128):
+                    with np.errstate(invalid="ignore"):
+                        s = w[c].sum() if not np.isfinite(w[c]).all() else None
+                    want = _bf16_mean(w[c]) if s is None else s
+                    assert got[c] == want or (np.isnan(got[c]) and np.isnan(want)), (g, i, c, got[c], want)
+                    # (a sum below zero whose mean rounds to nothing is -0, a sum of zero +0)
+                    assert got[c] != 0 or np.signbit(got[c]) == np.signbit(want)
+
+
+def test_append_of_windows_of_any_magnitudes(sb):
+    """The compressed keys of the 4-bit append: groups of equal channels are stored as they stand, so that each
+    window holds any 32 bf16 values."""
+    B, G, n = 6, 4, 10                                    # windows per (sequence, group): every second one counted
+    shape = sb.Shape(n_groups=G, max_ctx=64 * ((32 * n + 63) // 64), max_batch=B, heads_per_group=2)
+    rows = _wide_windows(B * G * 4 * n, 521).view(B, G, 4, n, 32)
+    tokens = rows.flatten(3).permute(3, 0, 1, 2)          # [32 n, B, G, 4]
+    layer = sb.LayerKV4.empty(shape)
+    zero = torch.zeros((B, G, 128), dtype=torch.bfloat16, device="cuda")
+    keys = tokens.repeat_interleave(32, dim=3).contiguous().cuda()
+    for t in range(32 * n):
+        sb.sparda_kv4_append(shape, layer, keys[t], zero, _i32([t + 1] * B), B)
+    torch.cuda.synchronize()
+    assert sb.sparda_device_error(clear=True) == 0
+    k = torch.zeros((B, G, shape.max_ctx, 128), dtype=torch.bfloat16, device="cuda")
+    sb.sparda_kv4_dequantize(shape, layer, _i32([32 * n] * B), B, k, torch.zeros_like(k))
+    assert torch.equal(k[:, :, :32 * n], keys.permute(1, 2, 0, 3))
+    for b in range(B):
+        for g in range(G):
+            for c in range(4):
+                for i in range(n):
+                    want = _bf16_mean(rows[b, g, c, i].double().numpy())
+                    assert to64(layer.ck[b, g, 2 * i, 32 * c:32 * c + 32]).tolist() == [want] * 32, (b, g, c, i)
