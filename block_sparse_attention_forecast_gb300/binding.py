@@ -182,6 +182,7 @@ def num_windows(n_tokens):
 @dataclass
 class Shape:
     """Decode-step geometry (sparda_shape)."""
+    __slots__ = ("_kept", "__dict__", "__weakref__")     # [sizes(), ref()], no field: not among vars(shape)
     n_groups: int = 2
     heads_per_group: int = 16
     head_dim: int = 128
@@ -197,29 +198,31 @@ class Shape:
                        self.win_kernel, self.win_stride, self.topk, self.max_ctx, self.max_batch)
 
     def __setattr__(self, name, value):
-        self.__dict__[name] = value
-        self.__dict__.pop("_ref", None)
-        self.__dict__.pop("_sizes", None)
+        object.__setattr__(self, name, value)
+        object.__setattr__(self, "_kept", [None, None])
 
     def __getstate__(self):
-        return {k: v for k, v in self.__dict__.items() if k not in ("_ref", "_sizes")}
+        return self.__dict__
+
+    def __setstate__(self, state):
+        for name, value in state.items():
+            setattr(self, name, value)
 
     def sizes(self):
         """(elements of a resident LayerKV's k or v, bytes of a LayerKV4's kv, elements of their ck), kept until
         a field changes."""
-        r = self.__dict__.get("_sizes")
+        r = self._kept[0]
         if r is None:
             rows = self.max_batch * self.n_groups
-            r = self.__dict__["_sizes"] = (rows * self.max_ctx * self.head_dim,
-                                           rows * (self.max_ctx // BLOCK) * KV4_BLOCK_BYTES,
-                                           rows * num_windows(self.max_ctx) * self.head_dim)
+            r = self._kept[0] = (rows * self.max_ctx * self.head_dim, rows * (self.max_ctx // BLOCK) * KV4_BLOCK_BYTES,
+                                 rows * num_windows(self.max_ctx) * self.head_dim)
         return r
 
     def ref(self):
         """A pointer to c(), kept until a field changes."""
-        r = self.__dict__.get("_ref")
+        r = self._kept[1]
         if r is None:
-            r = self.__dict__["_ref"] = ctypes.byref(self.c())
+            r = self._kept[1] = ctypes.byref(self.c())
         return r
 
     @property

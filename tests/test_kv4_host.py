@@ -219,3 +219,23 @@ def test_eviction_takes_weights_of_the_batch_alone(kv4, batch):
     if not torch.cuda.is_available():              # (made-up addresses: not where the call could launch)
         for dm in (m + n_src, m - n_dst):
             assert call(m, dm) == sb.ERR_CUDA
+
+
+def test_what_a_shape_keeps_is_no_field():
+    """A shape that calls have used is copied, spread and compared as one that they have not."""
+    import copy
+    import dataclasses
+    import pickle
+    used, fresh = _shape(), _shape()
+    used.ref(), used.sizes()
+    assert vars(used) == vars(fresh) == dataclasses.asdict(fresh) and used == fresh and repr(used) == repr(fresh)
+    for other in (sb.Shape(**vars(used)), sb.Shape(**{**vars(used), "max_batch": 3}), copy.copy(used), copy.deepcopy(used),
+                  pickle.loads(pickle.dumps(used)), dataclasses.replace(used, topk=4)):
+        assert other.sizes()[0] == other.max_batch * 2 * 4096 * 128
+        got = other.ref()._obj
+        assert (got.max_batch, got.topk) == (other.max_batch, other.topk)
+        other.max_batch += 1                       # what it keeps is its own
+        assert other.ref()._obj.max_batch == other.max_batch and other.sizes()[0] == other.max_batch * 2 * 4096 * 128
+    assert used.ref()._obj.max_batch == 2
+    with pytest.raises(AttributeError):
+        used.w_cap = 5                             # follows from the fields
