@@ -546,3 +546,104 @@ def test_append_of_windows_of_any_magnitudes(sb):
                 for i in range(n):
                     want = _bf16_mean(rows[b, g, c, i].double().numpy())
                     assert to64(layer.ck[b, g, 2 * i, 32 * c:32 * c + 32]).tolist() == [want] * 32, (b, g, c, i)
+
+
+def _compressed(sb, kv4, B, G, n, seed):
+    """(shape, make, check) of caches of n full blocks whose compressed keys are the means of the keys as they are
+    stored: make() is a fresh one, check(layer, seq) compares every complete window of it with the
+    means of the keys that it holds now."""
+    shape = sb.Shape(n_groups=G, max_ctx=64 * n, max_batch=B)
+    gen = torch.Generator(device="cuda").manual_seed(seed)
+    bf = sb.LayerKV.empty(shape)
+    bf.k.copy_(torch.randn(bf.k.shape, generator=gen, device="cuda"))
+    bf.v.copy_(torch.randn(bf.v.shape, generator=gen, device="cuda"))
+    full = _i32([64 * n] * B)
+    layer = bf
+    if kv4:
+        layer = sb.LayerKV4.empty(shape)
+        sb.sparda_kv4_quantize(shape, layer, bf.k, bf.v, full, B)
+        sb.sparda_kv4_dequantize(shape, layer, full, B, bf.k, bf.v)
+    sb.sparda_compress_keys(shape, bf, full, B)
+    if kv4:
+        layer.ck.copy_(bf.ck)
+
+    def make():
+        if kv4:
+            return sb.LayerKV4(layer.kv.clone(), layer.ck.clone())
+        return sb.LayerKV(layer.k.clone(), layer.v.clone(), layer.ck.clone())
+
+    def check(got, seq):
+        now = got
+        if kv4:
+            now = sb.LayerKV.empty(shape)
+            sb.sparda_kv4_dequantize(shape, got, seq, B, now.k, now.v)
+        want = sb.LayerKV(now.k, now.v, torch.zeros_like(got.ck))
+        sb.sparda_compress_keys(shape, want, seq, B)
+        torch.cuda.synchronize()
+        for b in range(B):
+            W = O.num_windows(int(seq[b]))
+            assert torch.equal(got.ck[b, :, :W], want.ck[b, :, :W]), b
+    return shape, make, check
+
+
+@pytest.mark.parametrize("kv4", [False, True])
+@pytest.mark.parametrize("lost", [1, 3, 200, 700])
+def test_every_window_after_long_shifts(sb, kv4, lost):
+    """The windows inside the moved blocks, those beside a neighbour that moved along and those formed anew, the
+    last block's too, eager and replayed."""
+    B, G, n = 2, 2, 1100
+    keep = n - lost
+    shape, make, check = _compressed(sb, kv4, B, G, n, 51)
+    gen = torch.Generator(device="cuda").manual_seed(52)
+    mass0 = torch.rand((B, G, n), generator=gen, device="cuda") + 1
+    mass0[0, :, 1:1 + lost] = 0                            # one sequence loses its oldest blocks, one any
+    fn = sb.sparda_kv4_evict_blocks if kv4 else sb.sparda_evict_blocks
+    T = _i32([64 * n - 5, 64 * n])
+    kept = torch.empty((B, G, keep), dtype=torch.int32, device="cuda")
+    layer, mass, seq = make(), mass0.clone(), T.clone()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        fn(shape, layer, mass, seq, B, keep, 2, kept)
+    for run in range(3):
+        fresh = make()
+        for name in ("kv", "ck") if kv4 else ("k", "v", "ck"):
+            getattr(layer, name).copy_(getattr(fresh, name))
+        mass.copy_(mass0)
+        seq.copy_(T)
+        if run:
+            graph.replay()
+        else:
+            fn(shape, layer, mass, seq, B, keep, 2, kept)
+        torch.cuda.synchronize()
+        assert sb.sparda_device_error(clear=True) == 0
+        assert seq.tolist() == [64 * keep - 5, 64 * keep]
+        check(layer, seq)
+
+
+def test_every_window_after_two_evictions_at_once(sb):
+    """Two caches on two streams, one in 4 bits and one in bf16, each cut in place while the other is."""
+    B, G, n, keep = 3, 2, 500, 320
+    parts = []
+    for kv4 in (False, True):
+        shape, make, check = _compressed(sb, kv4, B, G, n, 53 + kv4)
+        gen = torch.Generator(device="cuda").manual_seed(55 + kv4)
+        mass = torch.rand((B, G, n), generator=gen, device="cuda")
+        parts.append(dict(shape=shape, make=make, check=check, mass=mass, stream=torch.cuda.Stream(), runs=[],
+                          fn=sb.sparda_kv4_evict_blocks if kv4 else sb.sparda_evict_blocks))
+    for p in parts:
+        p["runs"] = [dict(layer=p["make"](), mass=p["mass"].clone(), seq=_i32([64 * n, 64 * n - 40, 64 * n - 63]),
+                          kept=torch.empty((B, G, keep), dtype=torch.int32, device="cuda")) for _ in range(4)]
+    torch.cuda.synchronize()
+    for i in range(4):
+        for p in parts:
+            with torch.cuda.stream(p["stream"]):
+                r = p["runs"][i]
+                p["fn"](p["shape"], r["layer"], r["mass"], r["seq"], B, keep, 3, r["kept"])
+    torch.cuda.synchronize()
+    assert sb.sparda_device_error(clear=True) == 0
+    for p in parts:
+        for r in p["runs"]:
+            for b in range(B):
+                for g in range(G):
+                    assert r["kept"][b, g].tolist() == R.kept_blocks(p["mass"][b, g].cpu().numpy(), n, keep, 3)
+            p["check"](r["layer"], r["seq"])
