@@ -936,7 +936,8 @@ int32_t prepare_evict(const sparda_shape* s, const sparda_shape* d, const void* 
                       int32_t recent, int32_t* kept, bool in_place, EvictArgs* a) {
   SPARDA_TRY(batch_status(s, batch));
   if (!mass || !seq_len || !kept || recent < 1 || keep <= recent) return SPARDA_ERR_INVALID_ARG;
-  if (keep > kMaxCtx / kBlock) return SPARDA_ERR_UNSUPPORTED_SHAPE;
+  // (kept entries are counted in 32 bits, once per plane)
+  if (keep > kMaxCtx / kBlock || (int64_t)batch * s->n_groups * keep >= (int64_t)1 << 29) return SPARDA_ERR_UNSUPPORTED_SHAPE;
   if (in_place) {
     if (d || dst_mass || dst_seq_len) return SPARDA_ERR_INVALID_ARG;
     d = s;

@@ -703,7 +703,7 @@ int32_t sparda_sparse_decode_attn_mass(const sparda_shape* shape, const sparda_l
  *
  * SPARDA_ERR_INVALID_ARG: an offloaded layer, recent < 1, keep <= recent, only some of the dst
  * arguments NULL, dst memory that overlaps the source's. SPARDA_ERR_UNSUPPORTED_SHAPE: dst_shape too
- * small, other groups, or keep above 4096. Ordering: as sparda_compress_keys, the call must not be
+ * small, other groups, keep above 4096, or 2^29 or more entries in kept. Ordering: as sparda_compress_keys, the call must not be
  * the kernel just before a selection that scores this cache.
  */
 int32_t sparda_evict_blocks(const sparda_shape* shape, const sparda_layer_kv* layer, float* mass, int32_t* seq_len,

@@ -239,3 +239,18 @@ def test_what_a_shape_keeps_is_no_field():
     assert used.ref()._obj.max_batch == 2
     with pytest.raises(AttributeError):
         used.w_cap = 5                             # follows from the fields
+
+
+@pytest.mark.parametrize("kv4", [False, True])
+def test_eviction_refuses_lists_past_32_bits(kv4):
+    """keep may exceed a cache's blocks, so kept can be larger than any cache: entries are counted in 32 bits."""
+    fn = sb.lib.sparda_kv4_evict_blocks if kv4 else sb.lib.sparda_evict_blocks
+    layer = _l4(kv=1 << 34, ck=1 << 33) if kv4 else _lk(k=1 << 34, v=1 << 37, ck=1 << 33)
+
+    def call(max_batch, G, keep):
+        s = _shape(max_batch=max_batch, n_groups=G, max_ctx=64)
+        return fn(_ref(s), layer, P(1 << 20), P(1 << 22), None, None, None, None, max_batch, keep, 2, P(1 << 25), None)
+    for big in ((1 << 18, 2, 4096), (1 << 17, 1, 4096), ((1 << 18) + 1, 8, 256)):
+        assert call(*big) == sb.ERR_UNSUPPORTED_SHAPE, big
+    if not torch.cuda.is_available():
+        assert call((1 << 17) - 1, 1, 4096) == sb.ERR_CUDA
