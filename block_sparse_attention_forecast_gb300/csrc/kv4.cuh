@@ -12,8 +12,9 @@
 // Why this form: 16 + code is a bit pattern. The upper mantissa bits of 16.0 (bf16 0x4180, fp16
 // 0x4c00) count units, so a code placed there is 16 + code with one AND-OR, and one packed fused
 // multiply-add turns two codes into two values in the type the tensor cores read: 11
-// instructions for 8 values, 5 to 7 of them on the half-rate logic pipe. z carries the rounding of 24 s at most (half of 0.125 s in bf16),
-// which only moves the grid, since codes are taken against the rounded z. Keys are bf16 because
+// instructions for 8 values, 5 to 7 of them on the half-rate logic pipe. z carries one rounding, of at most
+// 2^-8 |z| in bf16 and 2^-11 |z| in fp16 (|z| is about 24 s for a group around zero, and without bound beside
+// s for values with a common offset). It only moves the grid, since codes are taken against the rounded z. Keys are bf16 because
 // the queries are; values are fp16 so that the attention weights, its other operand, keep 11
 // bits instead of 8.
 //

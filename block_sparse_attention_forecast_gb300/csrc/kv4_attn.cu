@@ -3,12 +3,14 @@
 //
 // What bounds it: a token is 160 bytes of cache for 4 * 16 * 128 multiply-adds and 256 codes to
 // expand. The heads are the M dimension of warp-level MMAs (m16n8k16), and the cache is the B operand,
-// expanded in registers straight into B fragments (1.4 instructions per code, kv4.cuh). Per 16 tokens
-// a warp issues 293 instructions, 32 of them products. A product occupies the tensor pipe for 8.2
-// cycles and its operands' expansion the issue port for 8.7, but the two only half overlap (13.5
-// cycles together), so the instructions bound a long cache, not the memory: batch 16 of 131072 tokens
-// (671 MB) takes 139.6 us, and 137.1 us when every copy hits the same blocks in L2. A tcgen05 form, whose
-// expanded operands go through tensor memory, took 240 us. With at most 8 heads (kEight) the roles
+// expanded in registers straight into B fragments (1.4 instructions per code, kv4.cuh). Batch 16 of 131072
+// tokens (671 MB) takes 139.5 us, and 137 us when every copy hits the same blocks in L2, so not the
+// memory bounds a long cache. At the 2070 MHz sampled meanwhile a scheduler spends 670 cycles on 16 tokens
+// of a group. 293 instructions are issued for them, 32 of them products; in a loop of nothing else a product
+// with the expansion of its operands took 13.5 cycles (8.2 and 8.7 apart: the two only half overlap), which
+// makes 430. The other 240 belong to neither: a scheduler has two of these warps, and the rest of a step, the
+// maximum, the vote, the exponentials and their packing, has only the other warp's products to hide
+// behind. A tcgen05 form, whose expanded operands go through tensor memory, took 240 us. With at most 8 heads (kEight) the roles
 // change: the cache is the A operand, 16 tokens or 16 channels of it, the heads are the N dimension,
 // and half the products do: the same batch with 8 heads takes 116 us, 0.85 of the memory's rate
 // (147 with the heads as M; 113 without the memory's part). A score tile's 8 x 8 weights are transposed
@@ -81,14 +83,16 @@ constexpr int kMassSmem4 = kClusterSmem4 + kMaxCluster4 * 2 * kHeads * 4;      /
 //                   faster at (groups, blocks, clusters vs plan in us, 16 heads): (2, 34) 6.8, 12.5; (32, 34)
 //                   8.4, 14.8; (140, 34) 17.5, 26.2; (160, 16) 17.9, 19.0; (160, 34) 30.2, 27.8; (200, 24)
 //                   24.6, 27.5; (200, 34) 31.2, 31.3; (200, 64) 49, 44; (400, 6) 18.7, 20.8; (600, 34) 64, 71;
-//                   (600, 64) 95, 104.
+//                   (600, 64) 95, 104. The rule counts SMs, but a cluster lies inside one GPC, where some
+//                   sizes leave SMs over and take a second wave that it does not expect: 34 blocks of 16 to 21,
+//                   24, 25, 30 or 38 groups take 11.8 to 13.4 us, of 22, 26, 28 or 32 groups 6.9 to 7.7.
 //   kClusterBlocks  blocks per CTA up to which groups get clusters where no list bounds them: above, the
 //                   plan's balance over ragged lengths counts for more.
 //   kMinUnits       blocks per CTA below which fewer CTAs work; 1, 2 and 4 measured alike, and 2 halves
 //                   the CTAs that a small call occupies.
 //   kPiece          what beginning a group costs a CTA of the planned form (its warps drain, join and start
-//                   again), in blocks. 8 x 8 groups of 64 to 128 blocks, 4 heads: 24.5 us at 0, 22.6 at 14,
-//                   23.5 at 28; 200 groups of 34 blocks: 34.5, 30.6, 31.8.
+//                   again), in blocks. 8 x 8 groups of 64 to 128 blocks, 4 heads: 24.5 us at 0, 22.6 at 14
+//                   (22.9 now), 23.5 at 28; 200 groups of 34 blocks: 34.5, 30.6, 31.8.
 //   kJoin           CTAs that join their results at once; those of a longer group join in two levels. One sequence
 //                   of 131072 tokens (76 CTAs per group): 24.3 us at 4, 23.7 at 8, 24.2 at 16, 32.4 at once.
 //   kPlanMax        (sequence, group)s of the balanced plan, held in 4 KiB of shared memory; beyond it there

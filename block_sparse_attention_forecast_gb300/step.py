@@ -24,7 +24,9 @@ and selects its own blocks with a same-layer forecast), three ways to launch the
 A layer may also keep its cache in 4 bits (LayerKV4, resident); its append and attention are then
 sparda_kv4_append and sparda_kv4_decode_attn. With block_mass, every attention also adds up the weight
 each block received, and evict() cuts the caches to the blocks with the most of it, in place (both are
-extensions beyond the pages, and run in "streams" mode).
+extensions beyond the pages, and run in "streams" mode, whatever mode is asked for). That costs time: at 32
+layers, batch 16 and 131072 tokens a step in 4 bits takes 0.915 ms (0.970 with block mass), a bf16 one 0.776
+in "pipelined" and 0.997 in "streams". What 4 bits save is memory: 20 GiB of keys and values instead of 64.
 
 Every mode computes the same results bit for bit. Everything here is host-side orchestration
 of libsparda calls (no arithmetic); the whole step can be captured once into a CUDA graph and

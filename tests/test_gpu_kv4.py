@@ -464,7 +464,7 @@ def test_bf16_attention_with_mass(sb, T_list, topk):
             assert abs(got.sum() - 16) < 1e-3
 
 
-# ------------------------------------------------------------------ many blocks (tensor-memory form)
+# ------------------------------------------------------------------ many blocks
 @pytest.mark.parametrize("T_list,G,H,ctx", [
     ([16384, 1, 64, 65, 8191, 4000, 127, 12345], 2, 16, 16384),
     ([16320] * 5, 3, 3, 16384),
