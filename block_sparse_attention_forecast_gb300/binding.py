@@ -31,6 +31,8 @@ __all__ = [
     "LayerKV4", "sparda_kv4_quantize", "sparda_kv4_dequantize", "sparda_kv4_append", "sparda_kv4_decode_attn",
     "sparda_sparse_decode_attn_mass", "sparda_evict_blocks", "sparda_kv4_evict_blocks", "KV4_BLOCK_BYTES",
     "WS_ATTN_MASS", "WS_KV4_ATTN", "WS_KV4_ATTN_MASS",
+    "sparda_prompt_attn", "sparda_prompt_append", "sparda_tree_attn", "sparda_tree_commit", "WS_PROMPT", "WS_TREE",
+    "TREE_MAX_NODES",
     "OK", "ERR_INVALID_ARG", "ERR_UNSUPPORTED_SHAPE", "ERR_MISALIGNED", "ERR_NOT_MAPPED_HOST",
     "ERR_WORKSPACE_TOO_SMALL", "ERR_CUDA", "ERR_STATIC_SCRATCH_LIMIT", "DEV_WAIT_TIMEOUT", "DEV_BAD_SEQ_LEN", "DEV_BAD_INDEX",
     "WS_SELECT", "WS_ATTN", "WS_MULTIHEAD", "WS_PREFILL", "BLOCK", "WIN_KERNEL", "WIN_STRIDE",
@@ -61,6 +63,10 @@ WS_PREFILL = 4
 WS_ATTN_MASS = 5
 WS_KV4_ATTN = 6
 WS_KV4_ATTN_MASS = 7
+WS_PROMPT = 8
+WS_TREE = 9
+
+TREE_MAX_NODES = 128        # nodes of a tree of drafted tokens
 
 KV4_BLOCK_BYTES = 10240     # one 64-token block of the 4-bit cache, keys and values
 
@@ -97,7 +103,7 @@ def _load():
             "libsparda.so is not built (%s). Build it with "
             "`python -m block_sparse_attention_forecast_gb300.build` (nvcc, CUDA 13)." % LIB_PATH)
     lib = ctypes.CDLL(LIB_PATH)
-    P, I32, SZ = ctypes.c_void_p, ctypes.c_int32, ctypes.c_size_t
+    P, I32, SZ, I64 = ctypes.c_void_p, ctypes.c_int32, ctypes.c_size_t, ctypes.c_int64
     SH, LY = ctypes.POINTER(c_shape), ctypes.POINTER(c_layer_kv)
     L4 = ctypes.POINTER(c_layer_kv4)
     sig = {
@@ -135,6 +141,10 @@ def _load():
         "sparda_sparse_decode_attn_mass": (I32, [SH, LY, P, P, P, P, I32, P, P, P, SZ, P]),
         "sparda_evict_blocks": (I32, [SH, LY, P, P, SH, LY, P, P, I32, I32, I32, P, P]),
         "sparda_kv4_evict_blocks": (I32, [SH, L4, P, P, SH, L4, P, P, I32, I32, I32, P, P]),
+        "sparda_prompt_attn": (I32, [SH, LY, P, P, I64, P, P, I64, P, I32, I32, P, P, SZ, P]),
+        "sparda_prompt_append": (I32, [SH, LY, P, P, I64, P, I32, P, I32, P, P]),
+        "sparda_tree_attn": (I32, [SH, LY, P, I64, P, P, I64, P, P, I32, P, P, P, I32, P, P, SZ, P]),
+        "sparda_tree_commit": (I32, [SH, LY, P, P, I64, I32, P, P, P, I32, P, P]),
     }
     for name, (res, args) in sig.items():
         fn = getattr(lib, name)
@@ -719,3 +729,101 @@ def sparda_kv4_evict_blocks(shape, layer, mass, seq_len, batch, keep, recent, ke
     """sparda_evict_blocks of a LayerKV4."""
     _evict("sparda_kv4_evict_blocks", lib.sparda_kv4_evict_blocks, _kv4_layer, shape, layer, mass, seq_len, batch, keep,
            recent, kept, dst_shape, dst, dst_mass, dst_seq_len, stream)
+
+
+# ------------------------------------------------------------------ packed prompts and drafted tokens
+def _rows(what, t, lead, heads, d, dev):
+    """(address, elements from one row to the next) of new tokens' queries, keys or values: a bf16 tensor
+    [*lead, heads, d] on CUDA device `dev` whose rows hold their heads densely and lie evenly spaced. A leading
+    length of -1 is any."""
+    ok = (t.dtype is torch.bfloat16 and t.get_device() == dev and t.dim() == len(lead) + 2 and
+          all(a < 0 or a == b for a, b in zip(lead + (heads, d), t.shape)))
+    if ok:
+        st, n = t.stride(), t.shape
+        ok = st[-1] == 1 and (heads == 1 or st[-2] == d)
+        row = heads * d                              # the rows' spacing, where there is more than one
+        if len(lead) == 1:
+            row = st[0] if n[0] > 1 else row
+        else:
+            row = st[1] if n[1] > 1 else (st[0] if n[0] > 1 else row)
+            ok = ok and (n[0] == 1 or st[0] == n[1] * row)
+    if not ok:
+        raise ValueError("%s: a torch.bfloat16 tensor [%s] on cuda:%d with dense heads and evenly spaced rows is wanted, "
+                         "got %s %s on %s, strides %s" % (
+                             what, ", ".join("any" if x < 0 else str(x) for x in lead + (heads, d)), dev, t.dtype,
+                             tuple(t.shape), t.device, tuple(t.stride())))
+    return t.data_ptr(), row
+
+
+def _kv_rows(k, v, lead, G, d, dev):
+    pk, sk = _rows("keys", k, lead, G, d, dev)
+    pv, sv = _rows("values", v, tuple(k.shape[: len(lead)]), G, d, dev)
+    if sk != sv:
+        raise ValueError("keys and values need the same spacing of rows, got %d and %d elements" % (sk, sv))
+    return pk, pv, sk
+
+
+def _int_ptr(what, t, n, dev):
+    return None if t is None else _checked(what, t, torch.int32, n, dev)
+
+
+def sparda_prompt_attn(shape, q, k, v, cu_len, batch, out, ws, past=None, past_len=None, stream=None):
+    """Causal attention of packed prompts: sequence b's tokens are rows cu_len[b] .. cu_len[b+1]-1 of q
+    [n_tokens, G*H, d] and of k and v [n_tokens, G, d] (slices of one projection are fine). past, past_len: a
+    resident LayerKV and how many of its tokens come before each prompt. ws: WS_PROMPT."""
+    if past is not None:
+        dev, lc = _layer_ptrs(shape, past)
+    else:
+        dev, lc = _cache_device(q), None
+    B, G, H, d = int(batch), shape.n_groups, shape.heads_per_group, shape.head_dim
+    n = q.shape[0]
+    pq, sq = _rows("q", q, (-1,), G * H, d, dev)
+    pk, pv, skv = _kv_rows(k, v, (n,), G, d, dev)
+    _check("sparda_prompt_attn", lib.sparda_prompt_attn(
+        shape.ref(), lc, _int_ptr("past_len", past_len, B, dev), pq, sq, pk, pv, skv,
+        _checked("cu_len", cu_len, torch.int32, B + 1, dev), n, B,
+        _checked("out", out, torch.bfloat16, n * G * H * d, dev), _checked("ws", ws, torch.uint8, 1, dev), ws.numel(),
+        _stream_handle(stream, dev)))
+
+
+def sparda_prompt_append(shape, layer, k, v, cu_len, seq_len, batch, new_len=None, stream=None):
+    """Packed prompts' keys and values [n_tokens, G, d] into a resident LayerKV behind the seq_len[b] tokens it
+    holds (None: behind none), with the compressed keys they complete; new_len (int32 [B]) receives the lengths."""
+    dev, lc = _layer_ptrs(shape, layer)
+    B = int(batch)
+    pk, pv, skv = _kv_rows(k, v, (-1,), shape.n_groups, shape.head_dim, dev)
+    _check("sparda_prompt_append", lib.sparda_prompt_append(
+        shape.ref(), lc, pk, pv, skv, _checked("cu_len", cu_len, torch.int32, B + 1, dev), k.shape[0],
+        _int_ptr("seq_len", seq_len, B, dev), B, _int_ptr("new_len", new_len, B, dev), _stream_handle(stream, dev)))
+
+
+def sparda_tree_attn(shape, layer, q, k_new, v_new, parent, seq_len, batch, out, ws, n_nodes=None, idx=None, cnt=None,
+                     stream=None):
+    """Attention of trees of drafted tokens (q [B, N, G*H, d], k_new and v_new [B, N, G, d], parent int32 [B, N] or
+    None for chains; slices of one projection are fine) over the seq_len[b] tokens of a resident LayerKV, all of
+    them or those of the blocks idx / cnt. n_nodes: int32 [B], the nodes each sequence uses. ws: WS_TREE."""
+    dev, lc = _layer_ptrs(shape, layer)
+    B, G, H, d = int(batch), shape.n_groups, shape.heads_per_group, shape.head_dim
+    pq, sq = _rows("q", q, (B, -1), G * H, d, dev)
+    N = q.shape[1]
+    pk, pv, skv = _kv_rows(k_new, v_new, (B, N), G, d, dev)
+    pi, pc = _selection_ptrs(shape, idx, cnt, B * G, dev)
+    _check("sparda_tree_attn", lib.sparda_tree_attn(
+        shape.ref(), lc, pq, sq, pk, pv, skv, _int_ptr("parent", parent, B * N, dev), _int_ptr("n_nodes", n_nodes, B, dev),
+        N, pi, pc, _checked("seq_len", seq_len, torch.int32, B, dev), B,
+        _checked("out", out, torch.bfloat16, B * N * G * H * d, dev), _checked("ws", ws, torch.uint8, 1, dev), ws.numel(),
+        _stream_handle(stream, dev)))
+
+
+def sparda_tree_commit(shape, layer, k_new, v_new, path, n_path, seq_len, batch, new_len=None, stream=None):
+    """The accepted nodes path[b, :n_path[b]] (int32 [B, N]) of trees of drafted tokens (k_new, v_new [B, N, G, d])
+    into a resident LayerKV behind its seq_len[b] tokens, with the compressed keys they complete; new_len (int32
+    [B]) receives the lengths."""
+    dev, lc = _layer_ptrs(shape, layer)
+    B = int(batch)
+    pk, pv, skv = _kv_rows(k_new, v_new, (B, -1), shape.n_groups, shape.head_dim, dev)
+    N = k_new.shape[1]
+    _check("sparda_tree_commit", lib.sparda_tree_commit(
+        shape.ref(), lc, pk, pv, skv, N, _checked("path", path, torch.int32, B * N, dev),
+        _checked("n_path", n_path, torch.int32, B, dev), _checked("seq_len", seq_len, torch.int32, B, dev), B,
+        _int_ptr("new_len", new_len, B, dev), _stream_handle(stream, dev)))

@@ -238,6 +238,13 @@ size_t kv4_workspace_bytes(const sparda_shape* s, int32_t batch, int32_t kind) {
   return kind == SPARDA_WS_KV4_ATTN ? base : base + mass_stats_bytes(s, kv4_mass_slots(s)) + mass_ml_bytes(s);
 }
 
+// Two partial results for each CTA of the attention of new tokens (kTokenMaxCtas: the GPU's SMs at most).
+constexpr int kTokenMaxCtas = 160;
+size_t token_workspace_bytes(const sparda_shape* s, int32_t batch) {
+  if (kv4_shape_status(s) != SPARDA_OK || batch < 1 || batch > s->max_batch) return 0;
+  return (size_t)2 * kTokenMaxCtas * kTokenPartFloats * sizeof(float);
+}
+
 #define SPARDA_TRY(x)                     \
   do {                                    \
     const int32_t st_ = (x);              \
@@ -271,6 +278,7 @@ int32_t sparda_check_shape(const sparda_shape* shape) { return shape_status(shap
 
 size_t sparda_workspace_bytes(const sparda_shape* s, int32_t batch, int32_t kind) {
   if (kind == SPARDA_WS_KV4_ATTN || kind == SPARDA_WS_KV4_ATTN_MASS) return kv4_workspace_bytes(s, batch, kind);
+  if (kind == SPARDA_WS_PROMPT || kind == SPARDA_WS_TREE) return token_workspace_bytes(s, batch);
   if (shape_status(s) != SPARDA_OK || batch < 1 || batch > s->max_batch) return 0;
   switch (kind) {
     case SPARDA_WS_SELECT: return kQueueBytes + counters_bytes(s) + select_data_bytes(s);
@@ -1014,6 +1022,194 @@ int32_t sparda_kv4_evict_blocks(const sparda_shape* s, const sparda_layer_kv4* L
   SPARDA_TRY(prepare_evict(s, d, L->ck, dst ? dst->ck : nullptr, mass, seq_len, dst_mass, dst_seq_len, batch, keep, recent,
                            kept, dst == nullptr, &a));
   return launched(launch_evict(a, static_cast<cudaStream_t>(stream)));
+}
+
+}  // extern "C"
+
+// ------------------------------------------------------------------ packed prompts and drafted tokens
+namespace {
+
+// The new tokens' rows: [seqs][rows] rows of `heads` dense heads, `stride` elements apart.
+int32_t rows_status(const void* p, int64_t stride, int64_t heads) {
+  if (!p) return SPARDA_ERR_INVALID_ARG;
+  if (!aligned(p, 16)) return SPARDA_ERR_MISALIGNED;
+  // rows begin on 16 bytes; a tensor map's strides are below 2^40 bytes
+  if (stride < heads * kHeadDim || stride >= (int64_t)1 << 31) return SPARDA_ERR_INVALID_ARG;
+  return stride % 8 == 0 ? SPARDA_OK : SPARDA_ERR_MISALIGNED;
+}
+
+// Queries as (channel, head of the group, group, row, sequence), in boxes of the heads of box_rows rows.
+int32_t make_query_map(CUtensorMap* m, const void* q, int64_t stride, int G, int H, int64_t rows, int64_t seqs, int box_rows) {
+  EncodeTiledFn enc = encoder();
+  if (!enc) return SPARDA_ERR_CUDA;
+  const cuuint64_t dims[5] = {(cuuint64_t)kHeadDim, (cuuint64_t)H, (cuuint64_t)G, (cuuint64_t)rows, (cuuint64_t)seqs};
+  const cuuint64_t strides[4] = {(cuuint64_t)kRowBytes, (cuuint64_t)H * kRowBytes, (cuuint64_t)stride * 2,
+                                 (cuuint64_t)(rows * stride) * 2};
+  const cuuint32_t box[5] = {64, (cuuint32_t)H, 1, (cuuint32_t)box_rows, 1};
+  const cuuint32_t estr[5] = {1, 1, 1, 1, 1};
+  const CUresult r = enc(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 5, const_cast<void*>(q), dims, strides, box, estr,
+                         CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+                         CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+  return r == CUDA_SUCCESS ? SPARDA_OK : SPARDA_ERR_CUDA;
+}
+
+// New keys or values as (channel, group, row, sequence), in boxes of one group's 64 rows.
+int32_t make_new_kv_map(CUtensorMap* m, const void* p, int64_t stride, int G, int64_t rows, int64_t seqs) {
+  EncodeTiledFn enc = encoder();
+  if (!enc) return SPARDA_ERR_CUDA;
+  const cuuint64_t dims[4] = {(cuuint64_t)kHeadDim, (cuuint64_t)G, (cuuint64_t)rows, (cuuint64_t)seqs};
+  const cuuint64_t strides[3] = {(cuuint64_t)kRowBytes, (cuuint64_t)stride * 2, (cuuint64_t)(rows * stride) * 2};
+  const cuuint32_t box[4] = {64, 1, kBlock, 1};
+  const cuuint32_t estr[4] = {1, 1, 1, 1};
+  const CUresult r = enc(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 4, const_cast<void*>(p), dims, strides, box, estr,
+                         CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+                         CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+  return r == CUDA_SUCCESS ? SPARDA_OK : SPARDA_ERR_CUDA;
+}
+
+constexpr int32_t kMaxPromptTokens = 1 << 24;
+
+// What the two attention calls share: the checks behind those of their own arrays, maps and arguments.
+// rows: of each of seqs sequences.
+int32_t run_token_attn(const sparda_shape* s, const sparda_layer_kv* L, const void* q, int64_t q_stride, const void* k,
+                       const void* v, int64_t kv_stride, int64_t rows, int64_t seqs, int32_t batch, void* out, void* ws,
+                       size_t ws_bytes, TokenAttnArgs a, void* stream) {
+  const int G = s->n_groups, H = s->heads_per_group;
+  SPARDA_TRY(rows_status(q, q_stride, (int64_t)G * H));
+  SPARDA_TRY(rows_status(k, kv_stride, G));
+  SPARDA_TRY(rows_status(v, kv_stride, G));
+  if (!out || !ws) return SPARDA_ERR_INVALID_ARG;
+  if (!aligned(out, 16) || !aligned(ws, 16)) return SPARDA_ERR_MISALIGNED;
+  if (ws_bytes < token_workspace_bytes(s, batch)) return SPARDA_ERR_WORKSPACE_TOO_SMALL;
+  // a tensor map's last stride, in bytes, and the entries' count
+  if (rows * (q_stride > kv_stride ? q_stride : kv_stride) >= (int64_t)1 << 39 || (int64_t)batch * G >= (int64_t)1 << 30)
+    return SPARDA_ERR_UNSUPPORTED_SHAPE;
+  a.err = dev_error_ptr();
+  const int sms = sm_count();
+  if (!a.err || sms < 1) return SPARDA_ERR_CUDA;
+  a.out = static_cast<__nv_bfloat16*>(out);
+  a.part = static_cast<float*>(ws);
+  a.n_entries = batch * G;
+  a.G = G;
+  a.H = H;
+  a.max_ctx = s->max_ctx;
+  a.kslots = kslots(s);
+  a.n_rows = (int)rows;
+  a.tp = 128 / H < a.n_rows ? 128 / H : a.n_rows;
+  a.causal = a.parent == nullptr;
+  a.n_ctas = sms < kTokenMaxCtas ? sms : kTokenMaxCtas;
+  CUtensorMap m[5];
+  SPARDA_TRY(make_query_map(&m[0], q, q_stride, G, H, rows, seqs, a.tp));
+  SPARDA_TRY(make_new_kv_map(&m[3], k, kv_stride, G, rows, seqs));
+  SPARDA_TRY(make_new_kv_map(&m[4], v, kv_stride, G, rows, seqs));
+  if (L) {
+    const uint64_t cache_rows = (uint64_t)s->max_batch * G * s->max_ctx;
+    SPARDA_TRY(make_kv_map(&m[1], L->k, cache_rows));
+    SPARDA_TRY(make_kv_map(&m[2], L->v, cache_rows));
+  } else {
+    m[1] = m[3];
+    m[2] = m[4];
+  }
+  return launched(launch_token_attn(a, m, static_cast<cudaStream_t>(stream)));
+}
+
+int32_t resident_status(const sparda_layer_kv* L) {
+  SPARDA_TRY(layer_status(L, true));
+  return L->on_host ? SPARDA_ERR_INVALID_ARG : SPARDA_OK;
+}
+
+int32_t run_token_append(const sparda_shape* s, const sparda_layer_kv* L, const void* k, const void* v, int64_t kv_stride,
+                         int32_t batch, TokenAppendArgs a, void* stream) {
+  SPARDA_TRY(rows_status(k, kv_stride, s->n_groups));
+  SPARDA_TRY(rows_status(v, kv_stride, s->n_groups));
+  if (a.new_len && a.new_len == a.seq_len) return SPARDA_ERR_INVALID_ARG;
+  a.err = dev_error_ptr();
+  if (!a.err) return SPARDA_ERR_CUDA;
+  a.k = static_cast<__nv_bfloat16*>(L->k);
+  a.v = static_cast<__nv_bfloat16*>(L->v);
+  a.ck = static_cast<__nv_bfloat16*>(L->ck);
+  a.k_new = static_cast<const __nv_bfloat16*>(k);
+  a.v_new = static_cast<const __nv_bfloat16*>(v);
+  a.kv_stride = kv_stride;
+  a.B = batch;
+  a.G = s->n_groups;
+  a.max_ctx = s->max_ctx;
+  a.W_cap = w_cap(s);
+  return launched(launch_token_append(a, static_cast<cudaStream_t>(stream)));
+}
+
+}  // namespace
+
+extern "C" {
+
+int32_t sparda_prompt_attn(const sparda_shape* s, const sparda_layer_kv* past, const int32_t* past_len, const void* q,
+                           int64_t q_stride, const void* k, const void* v, int64_t kv_stride, const int32_t* cu_len,
+                           int32_t n_tokens, int32_t batch, void* out, void* ws, size_t ws_bytes, void* stream) {
+  SPARDA_TRY(kv4_shape_status(s));
+  SPARDA_TRY(batch_status(s, batch));
+  if (!cu_len || (past == nullptr) != (past_len == nullptr) || n_tokens < 1) return SPARDA_ERR_INVALID_ARG;
+  if (past) SPARDA_TRY(resident_status(past));
+  if (!aligned(cu_len, 4) || !aligned(past_len, 4)) return SPARDA_ERR_MISALIGNED;
+  if (n_tokens > kMaxPromptTokens) return SPARDA_ERR_UNSUPPORTED_SHAPE;
+  TokenAttnArgs a{};
+  a.ctx_len = past_len;
+  a.cu = cu_len;
+  return run_token_attn(s, past, q, q_stride, k, v, kv_stride, n_tokens, 1, batch, out, ws, ws_bytes, a, stream);
+}
+
+int32_t sparda_tree_attn(const sparda_shape* s, const sparda_layer_kv* L, const void* q, int64_t q_stride,
+                         const void* k_new, const void* v_new, int64_t kv_stride, const int32_t* parent,
+                         const int32_t* n_nodes, int32_t max_nodes, const int32_t* idx, const int32_t* cnt,
+                         const int32_t* seq_len, int32_t batch, void* out, void* ws, size_t ws_bytes, void* stream) {
+  SPARDA_TRY(kv4_shape_status(s));
+  SPARDA_TRY(batch_status(s, batch));
+  SPARDA_TRY(resident_status(L));
+  if (!seq_len || (idx == nullptr) != (cnt == nullptr) || max_nodes < 1) return SPARDA_ERR_INVALID_ARG;
+  if (max_nodes > SPARDA_TREE_MAX_NODES) return SPARDA_ERR_UNSUPPORTED_SHAPE;
+  if (!aligned(parent, 4) || !aligned(n_nodes, 4) || !aligned(idx, 4) || !aligned(cnt, 4) || !aligned(seq_len, 4))
+    return SPARDA_ERR_MISALIGNED;
+  TokenAttnArgs a{};
+  a.ctx_len = seq_len;
+  a.parent = parent;
+  a.n_nodes = n_nodes;
+  a.idx = idx;
+  a.cnt = cnt;
+  return run_token_attn(s, L, q, q_stride, k_new, v_new, kv_stride, max_nodes, batch, batch, out, ws, ws_bytes, a, stream);
+}
+
+int32_t sparda_prompt_append(const sparda_shape* s, const sparda_layer_kv* L, const void* k, const void* v,
+                             int64_t kv_stride, const int32_t* cu_len, int32_t n_tokens, const int32_t* seq_len,
+                             int32_t batch, int32_t* new_len, void* stream) {
+  SPARDA_TRY(kv4_shape_status(s));
+  SPARDA_TRY(batch_status(s, batch));
+  SPARDA_TRY(resident_status(L));
+  if (!cu_len || n_tokens < 1) return SPARDA_ERR_INVALID_ARG;
+  if (!aligned(cu_len, 4) || !aligned(seq_len, 4) || !aligned(new_len, 4)) return SPARDA_ERR_MISALIGNED;
+  if (n_tokens > kMaxPromptTokens) return SPARDA_ERR_UNSUPPORTED_SHAPE;
+  TokenAppendArgs a{};
+  a.cu = cu_len;
+  a.seq_len = seq_len;
+  a.new_len = new_len;
+  a.n_rows = n_tokens;
+  return run_token_append(s, L, k, v, kv_stride, batch, a, stream);
+}
+
+int32_t sparda_tree_commit(const sparda_shape* s, const sparda_layer_kv* L, const void* k_new, const void* v_new,
+                           int64_t kv_stride, int32_t max_nodes, const int32_t* path, const int32_t* n_path,
+                           const int32_t* seq_len, int32_t batch, int32_t* new_len, void* stream) {
+  SPARDA_TRY(kv4_shape_status(s));
+  SPARDA_TRY(batch_status(s, batch));
+  SPARDA_TRY(resident_status(L));
+  if (!path || !n_path || !seq_len || max_nodes < 1) return SPARDA_ERR_INVALID_ARG;
+  if (max_nodes > SPARDA_TREE_MAX_NODES) return SPARDA_ERR_UNSUPPORTED_SHAPE;
+  if (!aligned(path, 4) || !aligned(n_path, 4) || !aligned(seq_len, 4) || !aligned(new_len, 4)) return SPARDA_ERR_MISALIGNED;
+  TokenAppendArgs a{};
+  a.path = path;
+  a.n_path = n_path;
+  a.seq_len = seq_len;
+  a.new_len = new_len;
+  a.n_rows = max_nodes;
+  return run_token_append(s, L, k_new, v_new, kv_stride, batch, a, stream);
 }
 
 }  // extern "C"

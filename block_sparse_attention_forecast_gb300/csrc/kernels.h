@@ -263,6 +263,50 @@ struct EvictArgs {
 // written by the launches behind the one that moves the blocks: an error leaves them, and the cache, as they were.
 cudaError_t launch_evict(const EvictArgs& a, cudaStream_t s);
 
+// Attention of many new tokens per sequence over a cache (token_attn.cu): packed prompts and trees.
+constexpr int kTokenItemRows = 256;               // query rows of an item, at most
+constexpr int kTokenPartFloats = kTokenItemRows * (128 + 2);   // a partial result: O, maximum, sum
+constexpr int kTokenMaxNodes = 128;               // nodes of a tree, at most
+struct TokenAttnArgs {
+  const int32_t* ctx_len;        // [B] tokens in the cache; nullptr: none
+  const int32_t* cu;             // packed prompts: [B+1] first row of each; nullptr: n_rows rows per sequence
+  const int32_t* n_nodes;        // [B] rows that are used (cu == nullptr); nullptr: all
+  const int32_t* parent;         // [B, n_rows], tree; nullptr: each token attends those before it
+  const int32_t* idx;            // [B, G, kslots], the attended blocks of the cache; nullptr: all
+  const int32_t* cnt;
+  __nv_bfloat16* out;            // [rows, G*H, d]
+  float* part;                   // workspace [2 n_ctas][kTokenPartFloats]
+  int* err;
+  int n_entries, G, H, max_ctx, kslots;
+  int n_rows;                    // rows of all prompts, or of each sequence
+  int tp;                        // tokens per 128-row query tile
+  int causal;                    // parent == nullptr
+  int n_ctas;
+  int split_items;               // fewer items than this: key tiles are divided, not items
+  int min_tiles;                 // a CTA's share of key tiles, at least
+};
+// maps: queries (d, head, group, token, sequence); the cache's K and V [rows, 128]; the new tokens' K and V
+// (d, group, token, sequence)
+cudaError_t launch_token_attn(const TokenAttnArgs& a, const CUtensorMap* maps, cudaStream_t s);
+
+// New tokens into the cache with the compressed keys of the windows that they complete (token_append.cu).
+struct TokenAppendArgs {
+  __nv_bfloat16* k;              // [max_batch, G, max_ctx, d]
+  __nv_bfloat16* v;
+  __nv_bfloat16* ck;             // [max_batch, G, W_cap, d]
+  const __nv_bfloat16* k_new;    // rows of G*d, kv_stride apart
+  const __nv_bfloat16* v_new;
+  long long kv_stride;
+  const int32_t* cu;             // packed prompts: [B+1]; nullptr: path
+  const int32_t* path;           // [B, n_rows]: row numbers inside the sequence's n_rows rows
+  const int32_t* n_path;         // [B]
+  const int32_t* seq_len;        // [B]; nullptr: empty caches
+  int32_t* new_len;              // [B]; nullptr: not wanted
+  int* err;
+  int B, G, max_ctx, W_cap, n_rows;
+};
+cudaError_t launch_token_append(const TokenAppendArgs& a, cudaStream_t s);
+
 // Device address of the library's device error word on the current device (api.cu).
 int* dev_error_word();
 

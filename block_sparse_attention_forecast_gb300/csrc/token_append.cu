@@ -1,0 +1,140 @@
+// Many new tokens into a bf16 cache: packed prompts, or the accepted paths of trees of drafted tokens, with
+// the compressed keys of the windows that they complete (the exact mean of 32 keys, rounded once to bf16).
+//
+// A CTA takes the new tokens of one 64-token block of one sequence's cache, for one KV group: their keys
+// go through shared memory together with the up to 31 keys before them that their windows reach back to
+// (from the cache, or from the new rows), values straight through; then 64 threads per window, two
+// channels each, form the four windows that end in the block.
+#include "append_body.cuh"
+
+namespace sparda {
+
+namespace {
+constexpr int kThreads = 256;
+constexpr int kHalo = kWinKernel - 1;
+constexpr int kCommitBlocks = kTokenMaxNodes / kBlock + 1;   // cache blocks that a path reaches into, at most
+
+// What sequence b appends: n rows behind its S cached tokens; false: nothing may be written.
+__device__ __forceinline__ bool append_range(const TokenAppendArgs& a, int b, int& S, int& n, int& row0) {
+  S = a.seq_len ? a.seq_len[b] : 0;
+  bool good = S >= 0 && S <= a.max_ctx;
+  if (a.cu) {
+    const int lo = a.cu[b], hi = a.cu[b + 1];
+    good = good && lo >= 0 && hi >= lo && hi <= a.n_rows && hi - lo <= a.max_ctx - S;
+    row0 = lo;
+    n = hi - lo;
+  } else {
+    n = a.n_path[b];
+    good = good && n >= 0 && n <= a.n_rows && n <= a.max_ctx - S;
+    row0 = b * a.n_rows;
+  }
+  if (!good) n = 0;
+  return good;
+}
+
+__device__ __forceinline__ int blocks_touched(int S, int n) { return n == 0 ? 0 : (S + n - 1) / kBlock - S / kBlock + 1; }
+}  // namespace
+
+// grid (blocks of all sequences, G); prompts: the blocks are counted off sequence by sequence
+__global__ void __launch_bounds__(kThreads) token_append_kernel(const TokenAppendArgs a) {
+  __shared__ __align__(16) uint32_t ks[kHalo + kBlock][kHeadDim / 2];
+  __shared__ int path_sh[kTokenMaxNodes];
+  __shared__ int bad_path;
+  const int tid = threadIdx.x, lane = tid & 31, g = blockIdx.y;
+  int b, blk, S, n, row0;
+  bool good;
+  if (a.cu) {
+    // every warp looks the block up: blocks before 32 sequences at a time
+    int left = blockIdx.x;
+    b = -1;
+    for (int b0 = 0; b0 < a.B; b0 += 32) {
+      int s_ = 0, n_ = 0, r_ = 0;
+      bool good_ = true;
+      if (b0 + lane < a.B) {
+        good_ = append_range(a, b0 + lane, s_, n_, r_);
+        if (blockIdx.x == 0 && g == 0 && tid < 32) {
+          if (!good_) atomicOr(a.err, SPARDA_DEV_BAD_SEQ_LEN);
+          if (a.new_len) a.new_len[b0 + lane] = s_ + n_;
+        }
+      }
+      int incl = blocks_touched(s_, n_);
+#pragma unroll
+      for (int o = 1; o < 32; o <<= 1) {
+        const int up = __shfl_up_sync(0xffffffffu, incl, o);
+        if (lane >= o) incl += up;
+      }
+      const int sum = __shfl_sync(0xffffffffu, incl, 31);
+      if (b < 0 && left < sum) {
+        const int l = __ffs(__ballot_sync(0xffffffffu, incl > left)) - 1;
+        blk = left - (l == 0 ? 0 : __shfl_sync(0xffffffffu, incl, (l + 31) & 31));
+        b = b0 + l;
+        if (blockIdx.x != 0) break;
+      }
+      left -= sum;
+    }
+    if (b < 0) return;
+    good = append_range(a, b, S, n, row0);
+  } else {
+    b = blockIdx.x / kCommitBlocks;
+    blk = blockIdx.x % kCommitBlocks;
+    good = append_range(a, b, S, n, row0);
+    if (tid == 0) bad_path = 0;
+    __syncthreads();
+    for (int i = tid; i < n; i += kThreads) {
+      const int r = a.path[(size_t)b * a.n_rows + i];
+      path_sh[i] = r;
+      if (r < 0 || r >= a.n_rows) bad_path = 1;
+    }
+    __syncthreads();
+    if (bad_path) n = 0;
+    if (blk == 0 && g == 0 && tid == 0) {
+      if (!good) atomicOr(a.err, SPARDA_DEV_BAD_SEQ_LEN);
+      if (bad_path) atomicOr(a.err, SPARDA_DEV_BAD_INDEX);
+      if (a.new_len) a.new_len[b] = S + n;
+    }
+    if (blk >= blocks_touched(S, n)) return;
+  }
+  // cache positions lo .. hi-1 of this block
+  const size_t bg = (size_t)b * a.G + g;
+  const int base = (S / kBlock + blk) * kBlock;
+  const int lo = max(S, base), hi = min(S + n, base + kBlock);
+  const __nv_bfloat16* kc = a.k + bg * a.max_ctx * kHeadDim;
+  auto new_row = [&](int pos) {
+    const int i = pos - S;
+    return (size_t)(row0 + (a.cu ? i : path_sh[i])) * a.kv_stride + g * kHeadDim;
+  };
+  const int from = max(0, lo - kHalo);
+  for (int i = tid; i < (hi - from) * 16; i += kThreads) {
+    const int pos = from + (i >> 4), c = i & 15;
+    if (pos < S) {
+      *reinterpret_cast<uint4*>(&ks[pos - from][4 * c]) = *reinterpret_cast<const uint4*>(kc + (size_t)pos * kHeadDim + 8 * c);
+    } else {
+      const size_t src = new_row(pos) + 8 * c;
+      const uint4 x = *reinterpret_cast<const uint4*>(a.k_new + src);
+      *reinterpret_cast<uint4*>(&ks[pos - from][4 * c]) = x;
+      if (pos >= lo) {
+        const size_t dst = (bg * a.max_ctx + pos) * kHeadDim + 8 * c;
+        *reinterpret_cast<uint4*>(a.k + dst) = x;
+        *reinterpret_cast<uint4*>(a.v + dst) = *reinterpret_cast<const uint4*>(a.v_new + src);
+      }
+    }
+  }
+  __syncthreads();
+  // the windows that end in lo+1 .. hi: window w ends at 16 w + 32
+  const int w = base / kWinStride - 1 + (tid >> 6), end = w * kWinStride + kWinKernel, pair = tid & 63;
+  if (w >= 0 && end > lo && end <= hi) {
+    uint32_t xs[kWinKernel];
+#pragma unroll
+    for (int u = 0; u < kWinKernel; ++u) xs[u] = ks[end - kWinKernel + u - from][pair];
+    reinterpret_cast<uint32_t*>(a.ck + (bg * a.W_cap + w) * kHeadDim)[pair] = window_mean(xs);
+  }
+}
+
+cudaError_t launch_token_append(const TokenAppendArgs& a, cudaStream_t s) {
+  // a prompt of n tokens reaches into at most n / 64 + 2 blocks of its cache
+  const long long blocks = a.cu ? (long long)a.n_rows / kBlock + 2ll * a.B : (long long)a.B * kCommitBlocks;
+  token_append_kernel<<<dim3((unsigned)blocks, a.G), kThreads, 0, s>>>(a);
+  return cudaGetLastError();
+}
+
+}  // namespace sparda

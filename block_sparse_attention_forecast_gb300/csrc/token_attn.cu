@@ -1,0 +1,685 @@
+// Attention of many new tokens per sequence over a bf16 cache, on the fifth-generation tensor cores:
+// packed prompts (causal, on top of what the cache holds) and trees of drafted tokens.
+//
+// For token i of a sequence and head h of group g, over the keys u it attends (cached tokens, and the new
+// tokens up to i, or i's ancestors and itself):
+//   out = sum_u p_u v_u / sum_u p_u,   p_u = 2^((q . k_u - m) log2(e) / sqrt(128)),   m a running maximum
+//
+// A CTA holds the query rows of an item, row (token - first) * H + h of one KV group: two tiles of 128 rows
+// that share every key tile (128 keys: two 64-token blocks) it loads, or, where all rows fit one tile,
+// the one tile twice (kDup), each copy taking every other key tile, joined at the end. That keeps two
+// softmaxes and two accumulators under way for the one tensor pipe:
+//   warp 0, one lane: TMA loads of the query tiles and of each key tile's K and V into a ring of 32 KiB stages;
+//   warp 1: tensor-memory allocation; zeroes the value rows past a sequence's end (0 * NaN is NaN) and
+//       issues S_t = Q_t K^T (M 128, N 128) and O_t += P_t V, P read from tensor memory, where it
+//       overwrites S; one thread's MMAs run in issue order, so S of a tile's next step is issued behind the
+//       O that reads the P it overwrites, and the completion of S tells that of that O;
+//   warps 2-5 (tile 0) and 6-9 (tile 1), one thread per row: online softmax of S in registers. The maximum
+//       only moves, and O is only rescaled, when it grows by more than 2^8; P goes to tensor memory as bf16
+//       (rounded once; the sum is taken before that, in float32) in two halves of 64 keys, so that the
+//       first half's O += P V runs while the second is formed.
+// Every wait is bounded. A phase of a barrier is only followed by the next one after the thread that
+// waits for it has arrived somewhere.
+#include "tc05.cuh"
+#include "token_attn.cuh"
+
+namespace sparda {
+
+namespace {
+using tok::Cursor;
+using tok::Item;
+using tok::Segments;
+using tok::u64;
+
+constexpr int kThreads = 320;
+constexpr int kTileRows = 128;
+constexpr int kQTile = kTileRows * kRowBytes;              // 32 KiB: columns 0..63 of 128 rows, then 64..127
+constexpr int kStage = 2 * kBlockBytes;                    // 32 KiB: the same of 128 keys or values
+constexpr int kStages = 5;
+constexpr int kHalfCols = kStage / 2;
+constexpr int kPage = 1024;                                // barriers
+constexpr uint32_t kCols = 512;                            // per tile: 128 columns of S (then P), 128 of O
+constexpr float kGrow = 8.f;                               // the maximum moves when it grows past 2^8
+constexpr float kScaleLog2 = 1.4426950408889634f * 0.08838834764831845f;   // log2(e) / sqrt(128)
+
+template <bool kDup>
+constexpr int smem_bytes() {
+  return 1024 + kPage + (kDup ? kQTile + 2048 : 2 * kQTile) + kStages * kStage;
+}
+static_assert(smem_bytes<false>() <= 227 * 1024, "the token attention fits shared memory");
+
+__device__ __forceinline__ void bar_arrive(uint64_t* bar) {
+  asm volatile("mbarrier.arrive.shared::cta.b64 _, [%0];" ::"r"(smem_addr(bar)) : "memory");
+}
+__device__ __forceinline__ void tma_load_4d(void* dst, const CUtensorMap* map, int x, int y, int z, int w, uint64_t* bar) {
+  asm volatile(
+      "cp.async.bulk.tensor.4d.shared::cluster.global.tile.mbarrier::complete_tx::bytes"
+      " [%0], [%1, {%2, %3, %4, %5}], [%6];" ::"r"(smem_addr(dst)),
+      "l"(reinterpret_cast<uint64_t>(map)), "r"(x), "r"(y), "r"(z), "r"(w), "r"(smem_addr(bar))
+      : "memory");
+}
+__device__ __forceinline__ void tma_load_5d(void* dst, const CUtensorMap* map, int x, int y, int z, int w, int v,
+                                            uint64_t* bar) {
+  asm volatile(
+      "cp.async.bulk.tensor.5d.shared::cluster.global.tile.mbarrier::complete_tx::bytes"
+      " [%0], [%1, {%2, %3, %4, %5, %6}], [%7];" ::"r"(smem_addr(dst)),
+      "l"(reinterpret_cast<uint64_t>(map)), "r"(x), "r"(y), "r"(z), "r"(w), "r"(v), "r"(smem_addr(bar))
+      : "memory");
+}
+__device__ __forceinline__ float max3(float a, float b, float c) {
+  float r;
+  asm("max.f32 %0, %1, %2, %3;" : "=f"(r) : "f"(a), "f"(b), "f"(c));
+  return r;
+}
+// two float32 operations in one instruction
+__device__ __forceinline__ u64 pack2(float lo, float hi) {
+  u64 r;
+  asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(lo), "f"(hi));
+  return r;
+}
+__device__ __forceinline__ void unpack2(u64 v, float& lo, float& hi) {
+  asm("mov.b64 {%0, %1}, %2;" : "=f"(lo), "=f"(hi) : "l"(v));
+}
+__device__ __forceinline__ u64 fma2(u64 a, u64 b, u64 c) {
+  u64 r;
+  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
+  return r;
+}
+__device__ __forceinline__ u64 add2(u64 a, u64 b) {
+  u64 r;
+  asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+  return r;
+}
+
+// How the key tiles of a segment are stepped through. Step s works on tile t(s) and the segment's key tile
+// p(s); with L tiles under way, step s + L is the tile's next.
+template <bool kDup>
+struct Steps {
+  int n, L, M;       // key tiles, tiles under way, steps
+  __device__ __forceinline__ explicit Steps(int key_tiles, int tiles) : n(key_tiles) {
+    L = kDup ? 2 : tiles;
+    M = kDup ? n : n * L;
+  }
+  __device__ __forceinline__ int tile(int s) const { return kDup ? (s & 1) : (L == 2 ? (s & 1) : 0); }
+  __device__ __forceinline__ int key(int s) const { return kDup ? s : (L == 2 ? (s >> 1) : s); }
+  __device__ __forceinline__ bool last_use(int s) const { return kDup || tile(s) == L - 1; }
+  // place of key tile p's K and V in the order of loading, which is that of their first use
+  __device__ __forceinline__ int place_k(int p) const { return !kDup ? 2 * p : (p < 2 ? p : 2 * p - 1); }
+  __device__ __forceinline__ int place_v(int p) const {
+    return !kDup ? 2 * p + 1 : min(n, 2) + p + min(p, max(n - 2, 0));
+  }
+};
+
+// The blocks of an item. Block s < nctx is a block of the cache, the others are blocks of the new tokens.
+struct Blocks {
+  int j0, j1;        // lane l: the selection's entries l and 32 + l (selected blocks)
+  bool sel;
+  __device__ __forceinline__ void load(const TokenAttnArgs& a, const Item& it, int lane) {
+    sel = a.idx != nullptr;
+    if (sel) {
+      const int32_t* p = a.idx + (size_t)(it.b * a.G + it.g) * a.kslots;
+      j0 = lane < it.en.nctx ? p[lane] : 0;
+      j1 = lane + 32 < it.en.nctx ? p[lane + 32] : 0;
+    }
+  }
+  // the cache's block number (every lane calls); -1: outside the sequence
+  __device__ __forceinline__ int block(const Item& it, int s) const {
+    if (!sel) return s;
+    const int j = __shfl_sync(0xffffffffu, s < 32 ? j0 : j1, s & 31);
+    return j >= 0 && j <= it.en.P / kBlock ? j : -1;
+  }
+  // its rows that hold tokens: 0 .. 64
+  __device__ __forceinline__ int rows(const Item& it, int s) const {
+    if (s >= it.nblk) return 0;
+    if (s >= it.en.nctx) return min(kBlock, it.en.n - (s - it.en.nctx) * kBlock);
+    const int j = block(it, s);
+    return j < 0 ? 0 : max(0, min(kBlock, it.en.P - j * kBlock));
+  }
+};
+
+// The bounded wait of a whole warp: true in every lane or in none.
+__device__ __forceinline__ bool warp_wait(uint64_t* bar, uint32_t parity, int* err) {
+  return __all_sync(0xffffffffu, mbar_wait(bar, parity, err));
+}
+
+// 64-bit mask of the first n keys, 0 <= n <= 64
+__device__ __forceinline__ u64 first_bits(int n) { return n <= 0 ? 0ull : (n >= 64 ? ~0ull : (1ull << n) - 1ull); }
+
+}  // namespace
+
+template <bool kDup>
+__global__ void __launch_bounds__(kThreads, 1) token_attn_kernel(const TokenAttnArgs a, const __grid_constant__ CUtensorMap mq,
+                                                                const __grid_constant__ CUtensorMap mkc,
+                                                                const __grid_constant__ CUtensorMap mvc,
+                                                                const __grid_constant__ CUtensorMap mkn,
+                                                                const __grid_constant__ CUtensorMap mvn) {
+  extern __shared__ uint8_t smem_raw[];
+  uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~static_cast<uintptr_t>(1023));
+  uint64_t* q_full = reinterpret_cast<uint64_t*>(smem);
+  uint64_t* q_empty = q_full + 1;
+  uint64_t* drain = q_empty + 1;
+  uint64_t* kv_full = drain + 1;                             // [stages]
+  uint64_t* kv_empty = kv_full + kStages;                    // [stages]
+  uint64_t* s_full = kv_empty + kStages;                     // [tile]
+  uint64_t* p_full = s_full + 2;                             // [tile][half]
+  uint64_t* o_full = p_full + 4;                             // [tile]
+  uint32_t* tmem_sh = reinterpret_cast<uint32_t*>(o_full + 2);
+  volatile uint32_t* fail_sh = tmem_sh + 1;
+  uint8_t* qs = smem + kPage;
+  uint8_t* ring = qs + (kDup ? kQTile : 2 * kQTile);
+  float* ml_sh = reinterpret_cast<float*>(ring + kStages * kStage);   // [tile][max, sum][128] (kDup)
+
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  const int H = a.H, tp = a.tp, tpi = kDup ? tp : 2 * tp;
+  if (tid == 0) {
+    mbar_init(q_full, 1);
+    mbar_init(q_empty, 1);
+    mbar_init(drain, 1);
+    for (int i = 0; i < kStages; ++i) {
+      mbar_init(&kv_full[i], 1);
+      mbar_init(&kv_empty[i], 1);
+    }
+    for (int t = 0; t < 2; ++t) {
+      mbar_init(&s_full[t], 1);
+      mbar_init(&p_full[2 * t], 4);
+      mbar_init(&p_full[2 * t + 1], 4);
+      mbar_init(&o_full[t], 1);
+    }
+    *fail_sh = 0;
+    fence_mbar_init();
+  }
+  if (warp == 1) {
+    tc05::alloc(tmem_sh, kCols);
+    tc05::relinquish();
+  }
+  // query rows that no load fills: zero, once
+  for (int i = tid; i < (kTileRows - tp * H) * 8; i += kThreads)
+#pragma unroll
+    for (int part = 0; part < (kDup ? 2 : 4); ++part)
+      *reinterpret_cast<uint4*>(qs + part * (kQTile / 2) + tp * H * 128 + i * 16) = make_uint4(0u, 0u, 0u, 0u);
+  fence_proxy_async_shared();
+  tc05::fence_before();
+  __syncthreads();
+  tc05::fence_after();
+  const uint32_t tmem = *tmem_sh;
+  bool ok = true;
+  Segments seg(a, tpi, lane, blockIdx.x);
+  seg.init(blockIdx.x == 0 && warp == 0);
+  Item it;
+  Blocks bl;
+
+  if (warp == 0) {
+    // ------------------------------------------------------------ TMA producer
+    if (lane == 0) {
+      prefetch_tensormap(&mq);
+      prefetch_tensormap(&mkn);
+      prefetch_tensormap(&mvn);
+      if (a.ctx_len) {
+        prefetch_tensormap(&mkc);
+        prefetch_tensormap(&mvc);
+      }
+    }
+    unsigned n_ld = 0, n_item = 0;
+    auto load = [&](const CUtensorMap* mc, const CUtensorMap* mn, int p) {
+      const int s0 = 2 * p, two = s0 + 1 < it.nblk ? 2 : 1;
+      int j[2];
+      for (int h = 0; h < two; ++h) j[h] = s0 + h < it.en.nctx ? bl.block(it, s0 + h) : 0;
+      const int stage = n_ld % kStages;
+      if (lane == 0) {
+        if (n_ld >= (unsigned)kStages) ok = mbar_wait(&kv_empty[stage], ((n_ld / kStages) & 1) ^ 1, a.err);
+        if (ok) {
+          uint8_t* dst = ring + stage * kStage;
+          uint64_t* bar = &kv_full[stage];
+          mbar_arrive_expect_tx(bar, two * kBlockBytes);
+          for (int h = 0; h < two; ++h) {
+            uint8_t* d = dst + h * (kBlockBytes / 2);
+            if (s0 + h < it.en.nctx) {
+              if (j[h] < 0) atomicOr(a.err, SPARDA_DEV_BAD_INDEX);
+              const int rr = (it.b * a.G + it.g) * a.max_ctx + max(j[h], 0) * kBlock;
+              tma_load_2d(d, mc, 0, rr, bar);
+              tma_load_2d(d + kHalfCols, mc, 64, rr, bar);
+            } else {
+              const int t0 = it.en.row0 + (s0 + h - it.en.nctx) * kBlock, bb = a.cu ? 0 : it.b;
+              tma_load_4d(d, mn, 0, it.g, t0, bb, bar);
+              tma_load_4d(d + kHalfCols, mn, 64, it.g, t0, bb, bar);
+            }
+          }
+        }
+      }
+      ok = __shfl_sync(0xffffffffu, ok, 0);
+      if (ok) ++n_ld;
+    };
+    while (ok && seg.next(it)) {
+      bl.load(a, it, lane);
+      const int tiles = (kDup || it.tok0 + tp >= it.en.n) ? 1 : 2;
+      if (lane == 0) {
+        if (n_item > 0) ok = mbar_wait(q_empty, (n_item - 1) & 1, a.err);
+        if (ok) {
+          mbar_arrive_expect_tx(q_full, tiles * tp * H * kRowBytes);
+          for (int t = 0; t < tiles; ++t) {
+            uint8_t* d = qs + t * kQTile;
+            const int t0 = it.en.row0 + it.tok0 + t * tp, bb = a.cu ? 0 : it.b;
+            tma_load_5d(d, &mq, 0, 0, it.g, t0, bb, q_full);
+            tma_load_5d(d + kQTile / 2, &mq, 64, 0, it.g, t0, bb, q_full);
+          }
+        }
+      }
+      ok = __shfl_sync(0xffffffffu, ok, 0);
+      ++n_item;
+      const int n = it.k1 - it.k0;
+      if (!kDup) {
+        for (int p = 0; ok && p < n; ++p) {
+          load(&mkc, &mkn, it.k0 + p);
+          if (ok) load(&mvc, &mvn, it.k0 + p);
+        }
+      } else {
+        load(&mkc, &mkn, it.k0);
+        if (ok && n > 1) load(&mkc, &mkn, it.k0 + 1);
+        for (int p = 0; ok && p < n; ++p) {
+          load(&mvc, &mvn, it.k0 + p);
+          if (ok && p + 2 < n) load(&mkc, &mkn, it.k0 + p + 2);
+        }
+      }
+    }
+    // a wait ran out: no copy may still be under way when the CTA ends
+    if (!ok && lane == 0)
+      for (unsigned i = n_ld > (unsigned)kStages ? n_ld - kStages : 0; i < n_ld; ++i)
+        mbar_wait(&kv_full[i % kStages], (i / kStages) & 1, a.err);
+  } else if (warp == 1) {
+    // ------------------------------------------------------------ MMA issuer
+    constexpr uint32_t id_qk = tc05::idesc_bf16(128, 128, 0, 0);
+    constexpr uint32_t id_pv = tc05::idesc_bf16(128, 128, 0, 1);
+    const u64 dq = tc05::smem_desc(smem_addr(qs), 16, 1024);
+    const u64 dk = tc05::smem_desc(smem_addr(ring), 16, 1024);
+    const u64 dv = tc05::smem_desc(smem_addr(ring), kHalfCols, 1024);
+    unsigned n_ld = 0, n_item = 0, n_p[2] = {0, 0};
+    while (ok && seg.next(it)) {
+      bl.load(a, it, lane);
+      const int tiles = (kDup || it.tok0 + tp >= it.en.n) ? 1 : 2;
+      const Steps<kDup> st(it.k1 - it.k0, tiles);
+      auto issue_qk = [&](int s) {
+        const int t = st.tile(s), p = st.key(s);
+        const unsigned i = n_ld + st.place_k(p);
+        ok = ok && warp_wait(&kv_full[i % kStages], (i / kStages) & 1, a.err);
+        if (!ok) return;
+        tc05::fence_after();
+        if (lane == 0) {
+          const u64 da = dq + (kDup ? 0 : t * (kQTile >> 4)), db = dk + (i % kStages) * (kStage >> 4);
+#pragma unroll
+          for (int kk = 0; kk < 8; ++kk) {
+            const uint32_t off = (kk >> 2) * (kHalfCols >> 4) + (kk & 3) * 2;
+            tc05::mma_bf16_ss(tmem + 256 * t, da + off, db + off, id_qk, kk > 0 ? 1u : 0u);
+          }
+          tc05::commit(&s_full[t]);
+          if (st.last_use(s)) tc05::commit(&kv_empty[i % kStages]);
+          if (s == st.M - 1) tc05::commit(q_empty);
+        }
+        __syncwarp();
+      };
+      ok = warp_wait(q_full, n_item & 1, a.err);
+      ++n_item;
+      for (int s = 0; ok && s < min(st.L, st.M); ++s) issue_qk(s);
+      for (int s = 0; ok && s < st.M; ++s) {
+        const int t = st.tile(s), p = st.key(s);
+        const unsigned i = n_ld + st.place_v(p);
+        uint8_t* vs = ring + (i % kStages) * kStage;
+        const int blk = 2 * (it.k0 + p);
+        const bool two = blk + 1 < it.nblk;
+        ok = warp_wait(&kv_full[i % kStages], (i / kStages) & 1, a.err);
+        if (ok && (kDup || t == 0)) {
+          // value rows without a token
+          const int r0 = bl.rows(it, blk), r1 = two ? bl.rows(it, blk + 1) : kBlock;
+          if (r0 < kBlock || r1 < kBlock) {
+            for (int h = 0; h < 2; ++h)
+              for (int e = (h ? r1 : r0) * 8 + lane; e < kBlock * 8; e += 32) {
+                uint8_t* d = vs + h * (kBlockBytes / 2) + e * 16;
+                *reinterpret_cast<uint4*>(d) = make_uint4(0u, 0u, 0u, 0u);
+                *reinterpret_cast<uint4*>(d + kHalfCols) = make_uint4(0u, 0u, 0u, 0u);
+              }
+            fence_proxy_async_shared();
+            __syncwarp();
+          }
+        }
+        const u64 db = dv + (i % kStages) * (kStage >> 4);
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+          ok = ok && warp_wait(&p_full[2 * t + h], n_p[t] & 1, a.err);
+          if (ok && (h == 0 || two)) {
+            tc05::fence_after();
+            if (lane == 0) {
+#pragma unroll
+              for (int kk = 4 * h; kk < 4 * h + 4; ++kk)
+                tc05::mma_bf16_ts(tmem + 256 * t + 128, tmem + 256 * t + 8 * kk, db + kk * 128, id_pv,
+                                  (s >= st.L || kk > 0) ? 1u : 0u);
+            }
+          }
+        }
+        ++n_p[t];
+        if (!ok) break;
+        if (lane == 0) {
+          if (st.last_use(s)) tc05::commit(&kv_empty[i % kStages]);
+          if (s + st.L >= st.M) tc05::commit(&o_full[t]);
+        }
+        __syncwarp();
+        if (s + st.L < st.M) issue_qk(s + st.L);
+      }
+      n_ld += 2 * st.n;
+    }
+    if (!ok) {                                               // a wait ran out: let the MMAs under way end
+      if (lane == 0) {
+        tc05::commit(drain);
+        mbar_wait(drain, 0, a.err);
+      }
+      __syncwarp();
+    }
+  } else {
+    // ------------------------------------------------------------ softmax, one row per thread
+    const int t = (warp - 2) >> 2;
+    const int quarter = warp & 3;                            // tensor-memory lanes 32q .. 32q+31
+    const int r = quarter * 32 + lane;
+    const int rt = r / H;                                    // the row's token in its tile
+    const uint32_t lane_off = (uint32_t)(quarter * 32) << 16;
+    const uint32_t t_s = tmem + 256 * t + lane_off, t_o = t_s + 128;
+    const u64 scale2 = pack2(kScaleLog2, kScaleLog2);
+    unsigned n_s = 0, n_o[2] = {0, 0};
+    int tree_b = -1;
+    u64 anc0 = 0, anc1 = 0;                                  // tree: this row's ancestors and itself
+    while (ok && seg.next(it)) {
+      const int tiles = (kDup || it.tok0 + tp >= it.en.n) ? 1 : 2;
+      if (!kDup && t >= tiles) continue;
+      bl.load(a, it, lane);
+      const Steps<kDup> st(it.k1 - it.k0, tiles);
+      const int tile_tok = it.tok0 + (kDup ? 0 : t * tp);
+      const int tok = tile_tok + rt;                         // in the sequence
+      if (a.parent && (it.b != tree_b || !kDup)) {
+        // the chain of parents, from a table that the warp holds in registers
+        tree_b = it.b;
+        int par[4];
+        bool bad = false;
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          const int node = 32 * i + lane;
+          par[i] = node < it.en.n ? a.parent[(size_t)it.b * a.n_rows + node] : -1;
+          if (par[i] < -1 || par[i] >= node) {
+            par[i] = -1;
+            bad = true;
+          }
+        }
+        if (bad) atomicOr(a.err, SPARDA_DEV_BAD_INDEX);
+        anc0 = anc1 = 0;
+        int j = rt < tp && tok < it.en.n ? tok : -1;
+        while (__any_sync(0xffffffffu, j >= 0)) {
+          const int src = max(j, 0);
+          const int p0 = __shfl_sync(0xffffffffu, par[0], src & 31), p1 = __shfl_sync(0xffffffffu, par[1], src & 31);
+          const int p2 = __shfl_sync(0xffffffffu, par[2], src & 31), p3 = __shfl_sync(0xffffffffu, par[3], src & 31);
+          if (j >= 0) {
+            if (j < 64) anc0 |= 1ull << j;
+            else anc1 |= 1ull << (j - 64);
+            const int w = j >> 5;
+            j = w == 0 ? p0 : (w == 1 ? p1 : (w == 2 ? p2 : p3));
+          }
+        }
+      }
+      float m_used = -INFINITY, l = 0.f;
+      bool any = false;                                      // this tile has had a step
+      for (int s = (kDup || st.L == 2) ? t : 0; s < st.M; s += st.L) {
+        const int blk = 2 * (it.k0 + st.key(s));
+        const bool two = blk + 1 < it.nblk;
+        // the keys of each block that this row attends
+        u64 see[2] = {~0ull, two ? ~0ull : 0ull};
+        bool masked = false;                                 // warp-uniform
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+          if (h == 1 && !two) break;
+          const int sb = blk + h;
+          if (sb >= it.en.nctx) {
+            const int u0 = (sb - it.en.nctx) * kBlock;
+            if (a.parent) {
+              see[h] = u0 == 0 ? anc0 : anc1;
+              masked = true;
+            } else if (u0 + kBlock - 1 > tile_tok) {
+              see[h] = first_bits(tok + 1 - u0);
+              masked = true;
+            }
+          } else {
+            const int rows = bl.rows(it, sb);
+            if (rows < kBlock) {
+              see[h] = first_bits(rows);
+              masked = true;
+            }
+          }
+        }
+        ok = warp_wait(&s_full[t], n_s & 1, a.err);
+        ++n_s;
+        if (!ok) break;
+        tc05::fence_after();
+        float x[128];
+#pragma unroll
+        for (int i = 0; i < 4; ++i) tc05::ld32(t_s + 32 * i, *reinterpret_cast<float(*)[32]>(x + 32 * i));
+        tc05::wait_ld();
+        if (masked || !two) {
+#pragma unroll
+          for (int h = 0; h < 2; ++h)
+#pragma unroll
+            for (int w = 0; w < 2; ++w) {
+              const uint32_t bits = (uint32_t)(see[h] >> (32 * w));
+#pragma unroll
+              for (int e = 0; e < 32; ++e) {
+                float& v = x[64 * h + 32 * w + e];
+                v = (bits >> e) & 1u ? v : -INFINITY;
+              }
+            }
+        }
+        float m4[4];
+#pragma unroll
+        for (int e = 0; e < 4; ++e) m4[e] = max3(x[e], x[e + 4], x[e + 8]);
+#pragma unroll
+        for (int e = 12; e < 124; e += 8)
+#pragma unroll
+          for (int k = 0; k < 4; ++k) m4[k] = max3(m4[k], x[e + k], x[e + 4 + k]);
+#pragma unroll
+        for (int k = 0; k < 4; ++k) m4[k] = fmaxf(m4[k], x[124 + k]);
+        const float mb = fmaxf(fmaxf(m4[0], m4[1]), fmaxf(m4[2], m4[3])) * kScaleLog2;
+        const bool grow = mb > m_used + kGrow;               // also the first key this row sees
+        if (__any_sync(0xffffffffu, grow)) {
+          const float mn = grow ? mb : m_used;
+          const float alpha = grow ? fast_exp2(m_used - mn) : 1.f;
+          if (any) {                                         // S is there, so the O before it is
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+              float o[32];
+              tc05::ld32(t_o + 32 * i, o);
+              tc05::wait_ld();
+#pragma unroll
+              for (int e = 0; e < 32; ++e) o[e] *= alpha;
+              tc05::st32(t_o + 32 * i, o);
+            }
+          }
+          l *= alpha;
+          m_used = mn;
+        }
+        any = true;
+        const float neg = m_used == -INFINITY ? 0.f : -m_used;
+        const u64 neg2 = pack2(neg, neg);
+        u64 sum2[2] = {0ull, 0ull};
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+          if (h == 0 || two) {
+            float pk[32];
+#pragma unroll
+            for (int e = 0; e < 32; ++e) {
+              float p0, p1;
+              unpack2(fma2(pack2(x[64 * h + 2 * e], x[64 * h + 2 * e + 1]), scale2, neg2), p0, p1);
+              p0 = fast_exp2(p0);
+              p1 = fast_exp2(p1);
+              sum2[e & 1] = add2(sum2[e & 1], pack2(p0, p1));
+              pk[e] = __uint_as_float(pack_bf16(p0, p1));
+            }
+            tc05::st32(t_s + 32 * h, pk);
+            tc05::wait_st();
+          }
+          tc05::fence_before();
+          __syncwarp();
+          if (lane == 0) bar_arrive(&p_full[2 * t + h]);
+        }
+        float s0, s1;
+        unpack2(add2(sum2[0], sum2[1]), s0, s1);
+        l += s0 + s1;
+      }
+      if (!kDup && !ok) break;
+      // ---- the segment's end: O of this tile (kDup: of both copies) is complete
+      float w0 = 1.f, w1 = 0.f;
+      if (!kDup) {
+        ok = warp_wait(&o_full[t], n_o[t] & 1, a.err);
+        ++n_o[t];
+      } else {
+        ml_sh[256 * t + r] = m_used;
+        ml_sh[256 * t + 128 + r] = l;
+#pragma unroll
+        for (int u = 0; u < 2; ++u)
+          if (u < st.M) {
+            ok = ok && warp_wait(&o_full[u], n_o[u] & 1, a.err);
+            ++n_o[u];
+          }
+        // a wait that ran out in one warp ends the loop in all: none waits at a barrier for another that left
+        if (!ok) *fail_sh = 1;
+        asm volatile("bar.sync 1, 256;" ::: "memory");
+        ok = *fail_sh == 0;
+        const float ma = ml_sh[r], la = ml_sh[128 + r], mb = ml_sh[256 + r], lb = ml_sh[256 + 128 + r];
+        const float mm = fmaxf(ma, mb);
+        w0 = ma == -INFINITY ? 0.f : fast_exp2(ma - mm);
+        w1 = mb == -INFINITY ? 0.f : fast_exp2(mb - mm);
+        m_used = mm;
+        l = w0 * la + w1 * lb;
+      }
+      if (ok) {
+        tc05::fence_after();
+        const bool live = rt < tp && tok < it.en.n;
+        const size_t row = a.cu ? (size_t)it.en.row0 + tok : (size_t)it.b * a.n_rows + tok;
+        const float inv = l > 0.f || l != l ? 1.f / l : 0.f;
+        uint4* dst = reinterpret_cast<uint4*>(a.out + ((row * a.G + it.g) * H + (r - rt * H)) * kHeadDim);
+        float4* part = reinterpret_cast<float4*>(a.part + (size_t)max(it.slot, 0) * kTokenPartFloats);
+        const int prow = (kDup ? 0 : t * kTileRows) + r;
+        const int c0 = kDup ? 2 * t : 0, c1 = kDup ? 2 * t + 2 : 4;
+#pragma unroll 1
+        for (int c = c0; c < c1; ++c) {
+          float o[32];
+          __syncwarp();
+          tc05::ld32(tmem + lane_off + (kDup ? 0 : 256 * t) + 128 + 32 * c, o);
+          tc05::wait_ld();
+          if (kDup) {
+            if (st.M > 1) {
+              float o1[32];
+              tc05::ld32(tmem + lane_off + 256 + 128 + 32 * c, o1);
+              tc05::wait_ld();
+#pragma unroll
+              for (int e = 0; e < 32; ++e) o[e] = w0 * o[e] + w1 * o1[e];
+            }
+          }
+          if (live && it.slot < 0) {
+#pragma unroll
+            for (int e = 0; e < 4; ++e)
+              dst[4 * c + e] = make_uint4(pack_bf16(o[8 * e] * inv, o[8 * e + 1] * inv),
+                                          pack_bf16(o[8 * e + 2] * inv, o[8 * e + 3] * inv),
+                                          pack_bf16(o[8 * e + 4] * inv, o[8 * e + 5] * inv),
+                                          pack_bf16(o[8 * e + 6] * inv, o[8 * e + 7] * inv));
+          } else if (live) {
+#pragma unroll
+            for (int e = 0; e < 8; ++e)
+              part[(8 * c + e) * kTokenItemRows + prow] = make_float4(o[4 * e], o[4 * e + 1], o[4 * e + 2], o[4 * e + 3]);
+          }
+        }
+        if (live && it.slot >= 0 && (!kDup || t == 0)) {
+          float* ml = reinterpret_cast<float*>(part + 32 * kTokenItemRows);
+          ml[prow] = m_used;
+          ml[kTokenItemRows + prow] = l;
+        }
+        tc05::fence_before();
+      }
+      if (kDup) asm volatile("bar.sync 1, 256;" ::: "memory");   // both copies' O have been read by both
+    }
+  }
+  // every tensor-memory access of this CTA is done before the allocating warp frees it
+  tc05::fence_before();
+  __syncthreads();
+  if (warp == 1) {
+    tc05::fence_after();
+    tc05::dealloc(tmem, kCols);
+  }
+}
+
+// Joins the partial results of the items that the key-tile division cut: out = sum_i w_i O_i / sum_i w_i l_i
+// with w_i = 2^(m_i - max m). Block c stands for CTA c of the attention; the item that CTA c's range begins in
+// and the one it ends in are each joined by all the CTAs that share them, every one an equal part of
+// the item's rows.
+constexpr int kJoinThreads = 256;
+
+__global__ void __launch_bounds__(kJoinThreads) token_attn_join_kernel(const TokenAttnArgs a, int dup) {
+  grid_dep_wait();
+  const int lane = threadIdx.x & 31, c = blockIdx.x;
+  const int tp = a.tp, tpi = dup ? tp : 2 * tp, H = a.H;
+  Cursor cur(a, tpi, lane);
+  cur.init(false);
+  if (!cur.split || c >= cur.n_ctas) return;
+  const u64 W = cur.total;
+  const int n = cur.n_ctas;
+  const u64 p0 = tok::range_start(W, n, c), p1 = tok::range_start(W, n, c + 1);
+  if (p0 >= p1) return;
+  u64 done = ~0ull;
+  for (int which = 0; which < 2; ++which) {
+    Item it;
+    cur.tile_at(which ? p1 - 1 : p0, it);
+    const u64 s = it.start, e = s + it.nkt;
+    if (s == done) return;
+    done = s;
+    if (p0 <= s && p1 >= e) continue;                        // not cut
+    const int c1 = tok::range_owner(W, n, s), c2 = tok::range_owner(W, n, e - 1), k = c2 - c1 + 1;
+    const int first_slot = 2 * c1 + (tok::range_start(W, n, c1) < s ? 1 : 0);
+    const int rows = min(tpi, it.en.n - it.tok0) * H;
+    const int r0 = (int)((long long)rows * (c - c1) / k), r1 = (int)((long long)rows * (c - c1 + 1) / k);
+    for (int i = threadIdx.x; i < (r1 - r0) * 32; i += kJoinThreads) {
+      const int v = r0 + i % (r1 - r0), quad = i / (r1 - r0);
+      const int tk = v / H, prow = (tk / tp) * kTileRows + (tk % tp) * H + v % H;
+      float m = -INFINITY, l = 0.f;
+      float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
+      for (int q = c1; q <= c2; ++q) {
+        const float* part = a.part + (size_t)(q == c1 ? first_slot : 2 * q) * kTokenPartFloats;
+        const float mi = part[128 * kTokenItemRows + prow], li = part[129 * kTokenItemRows + prow];
+        const float4 oi = reinterpret_cast<const float4*>(part)[quad * kTokenItemRows + prow];
+        if (mi == -INFINITY && !(li != li)) continue;        // no key of that part is attended
+        const float mn = fmaxf(m, mi);
+        const float w = m == -INFINITY ? 0.f : fast_exp2(m - mn), wi = mi == -INFINITY ? 1.f : fast_exp2(mi - mn);
+        o.x = o.x * w + oi.x * wi;
+        o.y = o.y * w + oi.y * wi;
+        o.z = o.z * w + oi.z * wi;
+        o.w = o.w * w + oi.w * wi;
+        l = l * w + li * wi;
+        m = mn;
+      }
+      const float inv = l > 0.f || l != l ? 1.f / l : 0.f;
+      const int tok = it.tok0 + tk;
+      const size_t row = a.cu ? (size_t)it.en.row0 + tok : (size_t)it.b * a.n_rows + tok;
+      uint2* dst = reinterpret_cast<uint2*>(a.out + ((row * a.G + it.g) * H + v % H) * kHeadDim);
+      dst[quad] = make_uint2(pack_bf16(o.x * inv, o.y * inv), pack_bf16(o.z * inv, o.w * inv));
+    }
+  }
+}
+
+template <bool kDup>
+static cudaError_t launch(const TokenAttnArgs& a, const CUtensorMap* m, cudaStream_t s) {
+  static SmemOptIn opt;
+  if (!opt.set(token_attn_kernel<kDup>, smem_bytes<kDup>())) return cudaErrorInvalidValue;
+  token_attn_kernel<kDup><<<a.n_ctas, kThreads, smem_bytes<kDup>(), s>>>(a, m[0], m[1], m[2], m[3], m[4]);
+  const cudaError_t e = cudaGetLastError();
+  if (e != cudaSuccess) return e;
+  return launch_pdl(token_attn_join_kernel, dim3(a.n_ctas), dim3(kJoinThreads), 0, s, a, kDup ? 1 : 0);
+}
+
+cudaError_t launch_token_attn(const TokenAttnArgs& args, const CUtensorMap* maps, cudaStream_t s) {
+  TokenAttnArgs a = args;
+  a.split_items = 4 * a.n_ctas;
+  a.min_tiles = 2;
+  return a.n_rows <= a.tp ? launch<true>(a, maps, s) : launch<false>(a, maps, s);
+}
+
+}  // namespace sparda

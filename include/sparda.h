@@ -18,6 +18,8 @@
  *   sparda_multihead_select    the baseline query-driven selector, for comparison
  *   sparda_kv4_*               a layer's cache held in 4 bits: fill, append, attend, read back
  *   sparda_evict_blocks        eviction of blocks by the attention weight they received
+ *   sparda_prompt_*            whole prompts, packed: dense causal attention, store into the cache
+ *   sparda_tree_*              trees of drafted tokens: attention over the cache, store of the accepted path
  *
  * Conventions shared by every call
  *   - All tensors are caller-owned. The library never allocates, frees or synchronises on
@@ -80,6 +82,8 @@ extern "C" {
 #define SPARDA_WS_ATTN_MASS     5  /* sparda_sparse_decode_attn_mass                       */
 #define SPARDA_WS_KV4_ATTN      6  /* sparda_kv4_decode_attn without mass                  */
 #define SPARDA_WS_KV4_ATTN_MASS 7  /* sparda_kv4_decode_attn with mass                     */
+#define SPARDA_WS_PROMPT        8  /* sparda_prompt_attn                                   */
+#define SPARDA_WS_TREE          9  /* sparda_tree_attn                                     */
 
 /* ---------------------------------------------------------------- shapes */
 /*
@@ -716,6 +720,89 @@ int32_t sparda_kv4_evict_blocks(const sparda_shape* shape, const sparda_layer_kv
                                 int32_t* seq_len, const sparda_shape* dst_shape, const sparda_layer_kv4* dst,
                                 float* dst_mass, int32_t* dst_seq_len, int32_t batch, int32_t keep, int32_t recent,
                                 int32_t* kept, void* stream);
+
+/* ---------------------------------------------------------------- packed prompts and drafted tokens */
+/*
+ * An extension beyond the pages: many new tokens per sequence at once, over the bf16 cache of a resident
+ * layer. Whole prompts come packed, sequence behind sequence without padding: cu_len (DEVICE int32
+ * [B+1]) holds the first row of each and, last, the end; sequence b's tokens are the rows
+ * cu_len[b] .. cu_len[b+1]-1 of n_tokens rows (none is allowed). Drafted tokens come as trees of at
+ * most SPARDA_TREE_MAX_NODES nodes, [B, max_nodes] rows, of which sequence b uses the first n_nodes[b].
+ *
+ * The calls take any heads_per_group from 1 to 16 (the other shape rules are sparda_check_shape's).
+ * Queries, keys and values of the new tokens may be slices of one projection: a row holds its heads
+ * densely ([G*H, d] or [G, d]) and begins q_stride or kv_stride elements behind the row before it (a
+ * multiple of 8, at least the row's own elements; the sequences' max_nodes rows follow one another).
+ * Here seq_len / past_len count the tokens that the cache holds BEFORE the new ones: 0 <= seq_len[b] <=
+ * max_ctx. A sequence with a length out of range, or whose rows in cu_len are not ascending within
+ * n_tokens, sets SPARDA_DEV_BAD_SEQ_LEN and writes nothing. Rows that belong to no sequence are left
+ * as they were. Cache rows at and past seq_len, and rows past a sequence's end, may hold anything. Outputs
+ * must not overlap inputs. All pointers 16-byte aligned, index and length arrays 4-byte.
+ */
+#define SPARDA_TREE_MAX_NODES 128
+
+/*
+ * sparda_prompt_attn -- causal attention of whole prompts: for token i of sequence b (row cu_len[b] + i)
+ * and query head h of group g
+ *   out[row, g*H + h, :] = sum_u softmax_u(q[row, g*H + h] . k_u / sqrt(d)) v_u
+ * over the past_len[b] tokens that `past` (a resident layer) holds of sequence b and the sequence's new
+ * tokens up to i. past and past_len NULL: no past. Prompts may be longer than max_ctx (the cache is read
+ * only up to past_len). q: bf16 rows of [G*H, d]; k, v: bf16 rows of [G, d]; out: bf16
+ * [n_tokens, G*H, d]. 1 <= n_tokens <= 2^24. Tensor cores with bf16 operands and float32 accumulation,
+ * float32 softmax, probabilities rounded to bf16 before they meet the values. A value row that is not finite
+ * reaches, besides the tokens that attend it, those before it in its sequence that are computed beside
+ * them (up to 256). workspace: SPARDA_WS_PROMPT. One or two launches.
+ */
+int32_t sparda_prompt_attn(const sparda_shape* shape, const sparda_layer_kv* past, const int32_t* past_len,
+                           const void* q, int64_t q_stride, const void* k, const void* v, int64_t kv_stride,
+                           const int32_t* cu_len, int32_t n_tokens, int32_t batch, void* out, void* workspace,
+                           size_t workspace_bytes, void* stream);
+
+/*
+ * sparda_prompt_append -- whole prompts into the cache: sequence b's new keys and values at positions
+ * seq_len[b] .. of `layer`, and the compressed key of every window they complete (the exact mean of its 32
+ * keys rounded once to bf16, as sparda_append_kv one by one). seq_len NULL: empty caches. new_len
+ * (optional, int32 [B], another array than seq_len) receives the new lengths; all layers of a stack
+ * append at the same seq_len. A sequence that does not fit max_ctx sets SPARDA_DEV_BAD_SEQ_LEN and stays
+ * as it was. Ordering: as sparda_compress_keys, the call must not be the kernel just before a selection
+ * that scores this cache.
+ */
+int32_t sparda_prompt_append(const sparda_shape* shape, const sparda_layer_kv* layer, const void* k, const void* v,
+                             int64_t kv_stride, const int32_t* cu_len, int32_t n_tokens, const int32_t* seq_len,
+                             int32_t batch, int32_t* new_len, void* stream);
+
+/*
+ * sparda_tree_attn -- attention of drafted tokens over the cache, before any of them is stored: for node i
+ * of sequence b (i < n_nodes[b]) and query head h of group g
+ *   out[b, i, g*H + h, :] = sum_u softmax_u(q[b, i, g*H + h] . k_u / sqrt(d)) v_u
+ * over the cache's tokens t < seq_len[b], or, with idx and cnt, those of the blocks idx[b, g, 0 ..
+ * cnt[b,g]-1] (as the selectors write them; shared by the sequence's nodes), and over node i and its
+ * ancestors. parent: int32 [B, max_nodes], -1 for a node that follows the cached tokens directly, else a
+ * lower node number; one outside -1 .. i-1 sets SPARDA_DEV_BAD_INDEX and counts as -1. parent NULL: a
+ * chain (node i attends all nodes up to i). n_nodes NULL: max_nodes everywhere; 0 is allowed. A block
+ * named twice counts twice; a block outside 0 .. seq_len[b]/64 sets SPARDA_DEV_BAD_INDEX and is skipped
+ * (block seq_len[b]/64, where the next token lands, may hold none yet). One node is the ordinary
+ * decode step, on a token that is not stored yet, over any number of blocks. q, out: bf16
+ * [B, max_nodes, G*H, d]; k_new, v_new: bf16 [B, max_nodes, G, d] (out dense, the others with their
+ * strides). Numerics as sparda_prompt_attn. A value row of a node that is not finite reaches all nodes of its
+ * tree. workspace: SPARDA_WS_TREE. One or two launches.
+ */
+int32_t sparda_tree_attn(const sparda_shape* shape, const sparda_layer_kv* layer, const void* q, int64_t q_stride,
+                         const void* k_new, const void* v_new, int64_t kv_stride, const int32_t* parent,
+                         const int32_t* n_nodes, int32_t max_nodes, const int32_t* idx, const int32_t* cnt,
+                         const int32_t* seq_len, int32_t batch, void* out, void* workspace, size_t workspace_bytes,
+                         void* stream);
+
+/*
+ * sparda_tree_commit -- the accepted nodes into the cache: node path[b, i] (int32 [B, max_nodes], i <
+ * n_path[b]) of sequence b at position seq_len[b] + i, with the compressed keys of the windows they
+ * complete, new_len and the ordering rule as sparda_prompt_append. A node outside 0 .. max_nodes-1 sets
+ * SPARDA_DEV_BAD_INDEX, and its sequence stays as it was.
+ */
+int32_t sparda_tree_commit(const sparda_shape* shape, const sparda_layer_kv* layer, const void* k_new,
+                           const void* v_new, int64_t kv_stride, int32_t max_nodes, const int32_t* path,
+                           const int32_t* n_path, const int32_t* seq_len, int32_t batch, int32_t* new_len,
+                           void* stream);
 
 #ifdef __cplusplus
 }
