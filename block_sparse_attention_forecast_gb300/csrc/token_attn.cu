@@ -14,7 +14,7 @@
 //       issues S_t = Q_t K^T (M 128, N 128) and O_t += P_t V, P read from tensor memory, where it
 //       overwrites S; one thread's MMAs run in issue order, so S of a tile's next step is issued behind the
 //       O that reads the P it overwrites, and the completion of S tells that of that O;
-//   warps 2-5 (tile 0) and 6-9 (tile 1), one thread per row: online softmax of S in registers. The maximum
+//   warps 4-7 (tile 0) and 8-11 (tile 1), one thread per row: online softmax of S in registers. The maximum
 //       only moves, and O is only rescaled, when it grows by more than 2^8; P goes to tensor memory as bf16
 //       (rounded once; the sum is taken before that, in float32) in two halves of 64 keys, so that the
 //       first half's O += P V runs while the second is formed.
@@ -31,7 +31,10 @@ using tok::Item;
 using tok::Segments;
 using tok::u64;
 
-constexpr int kThreads = 320;
+constexpr int kThreads = 384;                              // three warpgroups
+// registers per thread: of 168 at launch, the softmax warps take what the first warpgroup gives
+constexpr int kRegsMain = 88, kRegsSoftmax = 208;
+static_assert(128 * kRegsMain + 256 * kRegsSoftmax <= kThreads * 168, "the registers of the launch");
 constexpr int kTileRows = 128;
 constexpr int kQTile = kTileRows * kRowBytes;              // 32 KiB: columns 0..63 of 128 rows, then 64..127
 constexpr int kStage = 2 * kBlockBytes;                    // 32 KiB: the same of 128 keys or values
@@ -111,29 +114,35 @@ struct Steps {
 };
 
 // The blocks of an item. Block s < nctx is a block of the cache, the others are blocks of the new tokens.
+// A segment as the scheduling warp hands it to the other warps, through a ring in shared memory.
+struct Work {
+  int b, g, n, P, nctx, row0, tok0, nblk, k0, k1, slot, tiles;   // k0 == k1: no more
+};
+constexpr int kWorkRing = 2;
+
 struct Blocks {
   int j0, j1;        // lane l: the selection's entries l and 32 + l (selected blocks)
   bool sel;
-  __device__ __forceinline__ void load(const TokenAttnArgs& a, const Item& it, int lane) {
+  __device__ __forceinline__ void load(const TokenAttnArgs& a, const Work& it, int lane) {
     sel = a.idx != nullptr;
     if (sel) {
       const int32_t* p = a.idx + (size_t)(it.b * a.G + it.g) * a.kslots;
-      j0 = lane < it.en.nctx ? p[lane] : 0;
-      j1 = lane + 32 < it.en.nctx ? p[lane + 32] : 0;
+      j0 = lane < it.nctx ? p[lane] : 0;
+      j1 = lane + 32 < it.nctx ? p[lane + 32] : 0;
     }
   }
   // the cache's block number (every lane calls); -1: outside the sequence
-  __device__ __forceinline__ int block(const Item& it, int s) const {
+  __device__ __forceinline__ int block(const Work& it, int s) const {
     if (!sel) return s;
     const int j = __shfl_sync(0xffffffffu, s < 32 ? j0 : j1, s & 31);
-    return j >= 0 && j <= it.en.P / kBlock ? j : -1;
+    return j >= 0 && j <= it.P / kBlock ? j : -1;
   }
   // its rows that hold tokens: 0 .. 64
-  __device__ __forceinline__ int rows(const Item& it, int s) const {
+  __device__ __forceinline__ int rows(const Work& it, int s) const {
     if (s >= it.nblk) return 0;
-    if (s >= it.en.nctx) return min(kBlock, it.en.n - (s - it.en.nctx) * kBlock);
+    if (s >= it.nctx) return min(kBlock, it.n - (s - it.nctx) * kBlock);
     const int j = block(it, s);
-    return j < 0 ? 0 : max(0, min(kBlock, it.en.P - j * kBlock));
+    return j < 0 ? 0 : max(0, min(kBlock, it.P - j * kBlock));
   }
 };
 
@@ -163,8 +172,12 @@ __global__ void __launch_bounds__(kThreads, 1) token_attn_kernel(const TokenAttn
   uint64_t* s_full = kv_empty + kStages;                     // [tile]
   uint64_t* p_full = s_full + 2;                             // [tile][half]
   uint64_t* o_full = p_full + 4;                             // [tile]
-  uint32_t* tmem_sh = reinterpret_cast<uint32_t*>(o_full + 2);
-  volatile uint32_t* fail_sh = tmem_sh + 1;
+  uint64_t* w_full = o_full + 2;                             // [work ring]
+  uint64_t* w_empty = w_full + kWorkRing;
+  uint64_t* ml_full = w_empty + kWorkRing;                   // the two copies' maxima and sums (kDup)
+  uint64_t* ml_empty = ml_full + 1;
+  uint32_t* tmem_sh = reinterpret_cast<uint32_t*>(ml_empty + 1);
+  volatile Work* work = reinterpret_cast<volatile Work*>(smem + 512);
   uint8_t* qs = smem + kPage;
   uint8_t* ring = qs + (kDup ? kQTile : 2 * kQTile);
   float* ml_sh = reinterpret_cast<float*>(ring + kStages * kStage);   // [tile][max, sum][128] (kDup)
@@ -185,7 +198,12 @@ __global__ void __launch_bounds__(kThreads, 1) token_attn_kernel(const TokenAttn
       mbar_init(&p_full[2 * t + 1], 4);
       mbar_init(&o_full[t], 1);
     }
-    *fail_sh = 0;
+    for (int i = 0; i < kWorkRing; ++i) {
+      mbar_init(&w_full[i], 1);
+      mbar_init(&w_empty[i], 10);                            // producer, issuer, eight softmax warps
+    }
+    mbar_init(ml_full, 8);
+    mbar_init(ml_empty, 8);
     fence_mbar_init();
   }
   if (warp == 1) {
@@ -203,12 +221,68 @@ __global__ void __launch_bounds__(kThreads, 1) token_attn_kernel(const TokenAttn
   tc05::fence_after();
   const uint32_t tmem = *tmem_sh;
   bool ok = true;
-  Segments seg(a, tpi, lane, blockIdx.x);
-  seg.init(blockIdx.x == 0 && warp == 0);
-  Item it;
+  unsigned n_work = 0;
+  Work it;
   Blocks bl;
+  // the next segment; false: none is left
+  auto next = [&]() {
+    const int i = n_work % kWorkRing;
+    ok = warp_wait(&w_full[i], (n_work / kWorkRing) & 1, a.err);
+    if (!ok) return false;
+    it.b = work[i].b;
+    it.g = work[i].g;
+    it.n = work[i].n;
+    it.P = work[i].P;
+    it.nctx = work[i].nctx;
+    it.row0 = work[i].row0;
+    it.tok0 = work[i].tok0;
+    it.nblk = work[i].nblk;
+    it.k0 = work[i].k0;
+    it.k1 = work[i].k1;
+    it.slot = work[i].slot;
+    it.tiles = work[i].tiles;
+    __syncwarp();
+    if (lane == 0) bar_arrive(&w_empty[i]);
+    ++n_work;
+    if (it.k0 == it.k1) return false;
+    bl.load(a, it, lane);
+    return true;
+  };
 
-  if (warp == 0) {
+  if (warp < 4) {
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kRegsMain));
+  if (warp == 2) {
+    // ------------------------------------------------------------ scheduler
+    Segments seg(a, tpi, lane, blockIdx.x);
+    seg.init(blockIdx.x == 0);
+    Item im;
+    for (bool more = true; ok && more;) {
+      more = seg.next(im);
+      const int i = n_work % kWorkRing;
+      if (n_work >= (unsigned)kWorkRing) ok = warp_wait(&w_empty[i], ((n_work / kWorkRing) & 1) ^ 1, a.err);
+      if (ok && lane == 0) {
+        if (more) {
+          work[i].b = im.b;
+          work[i].g = im.g;
+          work[i].n = im.en.n;
+          work[i].P = im.en.P;
+          work[i].nctx = im.en.nctx;
+          work[i].row0 = im.en.row0;
+          work[i].tok0 = im.tok0;
+          work[i].nblk = im.nblk;
+          work[i].k0 = im.k0;
+          work[i].k1 = im.k1;
+          work[i].slot = im.slot;
+          work[i].tiles = (kDup || im.tok0 + tp >= im.en.n) ? 1 : 2;
+        } else {
+          work[i].k0 = work[i].k1 = 0;
+        }
+        bar_arrive(&w_full[i]);
+      }
+      __syncwarp();
+      ++n_work;
+    }
+  } else if (warp == 0) {
     // ------------------------------------------------------------ TMA producer
     if (lane == 0) {
       prefetch_tensormap(&mq);
@@ -223,7 +297,7 @@ __global__ void __launch_bounds__(kThreads, 1) token_attn_kernel(const TokenAttn
     auto load = [&](const CUtensorMap* mc, const CUtensorMap* mn, int p) {
       const int s0 = 2 * p, two = s0 + 1 < it.nblk ? 2 : 1;
       int j[2];
-      for (int h = 0; h < two; ++h) j[h] = s0 + h < it.en.nctx ? bl.block(it, s0 + h) : 0;
+      for (int h = 0; h < two; ++h) j[h] = s0 + h < it.nctx ? bl.block(it, s0 + h) : 0;
       const int stage = n_ld % kStages;
       if (lane == 0) {
         if (n_ld >= (unsigned)kStages) ok = mbar_wait(&kv_empty[stage], ((n_ld / kStages) & 1) ^ 1, a.err);
@@ -233,13 +307,13 @@ __global__ void __launch_bounds__(kThreads, 1) token_attn_kernel(const TokenAttn
           mbar_arrive_expect_tx(bar, two * kBlockBytes);
           for (int h = 0; h < two; ++h) {
             uint8_t* d = dst + h * (kBlockBytes / 2);
-            if (s0 + h < it.en.nctx) {
+            if (s0 + h < it.nctx) {
               if (j[h] < 0) atomicOr(a.err, SPARDA_DEV_BAD_INDEX);
               const int rr = (it.b * a.G + it.g) * a.max_ctx + max(j[h], 0) * kBlock;
               tma_load_2d(d, mc, 0, rr, bar);
               tma_load_2d(d + kHalfCols, mc, 64, rr, bar);
             } else {
-              const int t0 = it.en.row0 + (s0 + h - it.en.nctx) * kBlock, bb = a.cu ? 0 : it.b;
+              const int t0 = it.row0 + (s0 + h - it.nctx) * kBlock, bb = a.cu ? 0 : it.b;
               tma_load_4d(d, mn, 0, it.g, t0, bb, bar);
               tma_load_4d(d + kHalfCols, mn, 64, it.g, t0, bb, bar);
             }
@@ -249,16 +323,14 @@ __global__ void __launch_bounds__(kThreads, 1) token_attn_kernel(const TokenAttn
       ok = __shfl_sync(0xffffffffu, ok, 0);
       if (ok) ++n_ld;
     };
-    while (ok && seg.next(it)) {
-      bl.load(a, it, lane);
-      const int tiles = (kDup || it.tok0 + tp >= it.en.n) ? 1 : 2;
+    while (ok && next()) {
       if (lane == 0) {
         if (n_item > 0) ok = mbar_wait(q_empty, (n_item - 1) & 1, a.err);
         if (ok) {
-          mbar_arrive_expect_tx(q_full, tiles * tp * H * kRowBytes);
-          for (int t = 0; t < tiles; ++t) {
+          mbar_arrive_expect_tx(q_full, it.tiles * tp * H * kRowBytes);
+          for (int t = 0; t < it.tiles; ++t) {
             uint8_t* d = qs + t * kQTile;
-            const int t0 = it.en.row0 + it.tok0 + t * tp, bb = a.cu ? 0 : it.b;
+            const int t0 = it.row0 + it.tok0 + t * tp, bb = a.cu ? 0 : it.b;
             tma_load_5d(d, &mq, 0, 0, it.g, t0, bb, q_full);
             tma_load_5d(d + kQTile / 2, &mq, 64, 0, it.g, t0, bb, q_full);
           }
@@ -293,10 +365,8 @@ __global__ void __launch_bounds__(kThreads, 1) token_attn_kernel(const TokenAttn
     const u64 dk = tc05::smem_desc(smem_addr(ring), 16, 1024);
     const u64 dv = tc05::smem_desc(smem_addr(ring), kHalfCols, 1024);
     unsigned n_ld = 0, n_item = 0, n_p[2] = {0, 0};
-    while (ok && seg.next(it)) {
-      bl.load(a, it, lane);
-      const int tiles = (kDup || it.tok0 + tp >= it.en.n) ? 1 : 2;
-      const Steps<kDup> st(it.k1 - it.k0, tiles);
+    while (ok && next()) {
+      const Steps<kDup> st(it.k1 - it.k0, it.tiles);
       auto issue_qk = [&](int s) {
         const int t = st.tile(s), p = st.key(s);
         const unsigned i = n_ld + st.place_k(p);
@@ -372,23 +442,29 @@ __global__ void __launch_bounds__(kThreads, 1) token_attn_kernel(const TokenAttn
       }
       __syncwarp();
     }
+    }
+    // every tensor-memory access of this CTA is done before the allocating warp frees it
+    asm volatile("bar.sync 2, %0;" ::"n"(kThreads) : "memory");
+    if (warp == 1) {
+      tc05::fence_after();
+      tc05::dealloc(tmem, kCols);
+    }
   } else {
     // ------------------------------------------------------------ softmax, one row per thread
-    const int t = (warp - 2) >> 2;
+    asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kRegsSoftmax));
+    const int t = (warp - 4) >> 2;
     const int quarter = warp & 3;                            // tensor-memory lanes 32q .. 32q+31
     const int r = quarter * 32 + lane;
     const int rt = r / H;                                    // the row's token in its tile
     const uint32_t lane_off = (uint32_t)(quarter * 32) << 16;
     const uint32_t t_s = tmem + 256 * t + lane_off, t_o = t_s + 128;
     const u64 scale2 = pack2(kScaleLog2, kScaleLog2);
-    unsigned n_s = 0, n_o[2] = {0, 0};
+    unsigned n_s = 0, n_seg = 0, n_o[2] = {0, 0};
     int tree_b = -1;
     u64 anc0 = 0, anc1 = 0;                                  // tree: this row's ancestors and itself
-    while (ok && seg.next(it)) {
-      const int tiles = (kDup || it.tok0 + tp >= it.en.n) ? 1 : 2;
-      if (!kDup && t >= tiles) continue;
-      bl.load(a, it, lane);
-      const Steps<kDup> st(it.k1 - it.k0, tiles);
+    while (ok && next()) {
+      if (!kDup && t >= it.tiles) continue;
+      const Steps<kDup> st(it.k1 - it.k0, it.tiles);
       const int tile_tok = it.tok0 + (kDup ? 0 : t * tp);
       const int tok = tile_tok + rt;                         // in the sequence
       if (a.parent && (it.b != tree_b || !kDup)) {
@@ -399,7 +475,7 @@ __global__ void __launch_bounds__(kThreads, 1) token_attn_kernel(const TokenAttn
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
           const int node = 32 * i + lane;
-          par[i] = node < it.en.n ? a.parent[(size_t)it.b * a.n_rows + node] : -1;
+          par[i] = node < it.n ? a.parent[(size_t)it.b * a.n_rows + node] : -1;
           if (par[i] < -1 || par[i] >= node) {
             par[i] = -1;
             bad = true;
@@ -407,7 +483,7 @@ __global__ void __launch_bounds__(kThreads, 1) token_attn_kernel(const TokenAttn
         }
         if (bad) atomicOr(a.err, SPARDA_DEV_BAD_INDEX);
         anc0 = anc1 = 0;
-        int j = rt < tp && tok < it.en.n ? tok : -1;
+        int j = rt < tp && tok < it.n ? tok : -1;
         while (__any_sync(0xffffffffu, j >= 0)) {
           const int src = max(j, 0);
           const int p0 = __shfl_sync(0xffffffffu, par[0], src & 31), p1 = __shfl_sync(0xffffffffu, par[1], src & 31);
@@ -420,6 +496,8 @@ __global__ void __launch_bounds__(kThreads, 1) token_attn_kernel(const TokenAttn
           }
         }
       }
+      // blocks before this one are attended whole by every row of the tile
+      const int plain = bl.sel ? 0 : it.P % kBlock != 0 ? it.nctx - 1 : it.nctx + (a.parent ? 0 : (tile_tok + 1) / kBlock);
       float m_used = -INFINITY, l = 0.f;
       bool any = false;                                      // this tile has had a step
       for (int s = (kDup || st.L == 2) ? t : 0; s < st.M; s += st.L) {
@@ -430,10 +508,10 @@ __global__ void __launch_bounds__(kThreads, 1) token_attn_kernel(const TokenAttn
         bool masked = false;                                 // warp-uniform
 #pragma unroll
         for (int h = 0; h < 2; ++h) {
-          if (h == 1 && !two) break;
+          if (blk + 2 <= plain || (h == 1 && !two)) break;
           const int sb = blk + h;
-          if (sb >= it.en.nctx) {
-            const int u0 = (sb - it.en.nctx) * kBlock;
+          if (sb >= it.nctx) {
+            const int u0 = (sb - it.nctx) * kBlock;
             if (a.parent) {
               see[h] = u0 == 0 ? anc0 : anc1;
               masked = true;
@@ -541,10 +619,9 @@ __global__ void __launch_bounds__(kThreads, 1) token_attn_kernel(const TokenAttn
             ok = ok && warp_wait(&o_full[u], n_o[u] & 1, a.err);
             ++n_o[u];
           }
-        // a wait that ran out in one warp ends the loop in all: none waits at a barrier for another that left
-        if (!ok) *fail_sh = 1;
-        asm volatile("bar.sync 1, 256;" ::: "memory");
-        ok = *fail_sh == 0;
+        __syncwarp();
+        if (lane == 0) bar_arrive(ml_full);
+        ok = warp_wait(ml_full, n_seg & 1, a.err) && ok;
         const float ma = ml_sh[r], la = ml_sh[128 + r], mb = ml_sh[256 + r], lb = ml_sh[256 + 128 + r];
         const float mm = fmaxf(ma, mb);
         w0 = ma == -INFINITY ? 0.f : fast_exp2(ma - mm);
@@ -554,8 +631,8 @@ __global__ void __launch_bounds__(kThreads, 1) token_attn_kernel(const TokenAttn
       }
       if (ok) {
         tc05::fence_after();
-        const bool live = rt < tp && tok < it.en.n;
-        const size_t row = a.cu ? (size_t)it.en.row0 + tok : (size_t)it.b * a.n_rows + tok;
+        const bool live = rt < tp && tok < it.n;
+        const size_t row = a.cu ? (size_t)it.row0 + tok : (size_t)it.b * a.n_rows + tok;
         const float inv = l > 0.f || l != l ? 1.f / l : 0.f;
         uint4* dst = reinterpret_cast<uint4*>(a.out + ((row * a.G + it.g) * H + (r - rt * H)) * kHeadDim);
         float4* part = reinterpret_cast<float4*>(a.part + (size_t)max(it.slot, 0) * kTokenPartFloats);
@@ -596,15 +673,15 @@ __global__ void __launch_bounds__(kThreads, 1) token_attn_kernel(const TokenAttn
         }
         tc05::fence_before();
       }
-      if (kDup) asm volatile("bar.sync 1, 256;" ::: "memory");   // both copies' O have been read by both
+      if (kDup) {                                            // both copies' O have been read by both
+        __syncwarp();
+        if (lane == 0) bar_arrive(ml_empty);
+        ok = warp_wait(ml_empty, n_seg & 1, a.err) && ok;
+        ++n_seg;
+      }
     }
-  }
-  // every tensor-memory access of this CTA is done before the allocating warp frees it
-  tc05::fence_before();
-  __syncthreads();
-  if (warp == 1) {
-    tc05::fence_after();
-    tc05::dealloc(tmem, kCols);
+    tc05::fence_before();
+    asm volatile("bar.sync 2, %0;" ::"n"(kThreads) : "memory");
   }
 }
 
