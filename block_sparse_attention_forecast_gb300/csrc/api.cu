@@ -238,11 +238,10 @@ size_t kv4_workspace_bytes(const sparda_shape* s, int32_t batch, int32_t kind) {
   return kind == SPARDA_WS_KV4_ATTN ? base : base + mass_stats_bytes(s, kv4_mass_slots(s)) + mass_ml_bytes(s);
 }
 
-// Two partial results for each CTA of the attention of new tokens (kTokenMaxCtas: the GPU's SMs at most).
-constexpr int kTokenMaxCtas = 160;
+// Two partial results, and two shares in joining, for each CTA of the attention of new tokens.
 size_t token_workspace_bytes(const sparda_shape* s, int32_t batch) {
   if (kv4_shape_status(s) != SPARDA_OK || batch < 1 || batch > s->max_batch) return 0;
-  return (size_t)2 * kTokenMaxCtas * kTokenPartFloats * sizeof(float);
+  return (size_t)2 * kTokenMaxCtas * (kTokenPartFloats * sizeof(float) + sizeof(TokenJoin));
 }
 
 #define SPARDA_TRY(x)                     \
@@ -1089,6 +1088,7 @@ int32_t run_token_attn(const sparda_shape* s, const sparda_layer_kv* L, const vo
   if (!a.err || sms < 1) return SPARDA_ERR_CUDA;
   a.out = static_cast<__nv_bfloat16*>(out);
   a.part = static_cast<float*>(ws);
+  a.joins = reinterpret_cast<TokenJoin*>(a.part + (size_t)2 * kTokenMaxCtas * kTokenPartFloats);
   a.n_entries = batch * G;
   a.G = G;
   a.H = H;

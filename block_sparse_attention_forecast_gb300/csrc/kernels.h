@@ -266,7 +266,12 @@ cudaError_t launch_evict(const EvictArgs& a, cudaStream_t s);
 // Attention of many new tokens per sequence over a cache (token_attn.cu): packed prompts and trees.
 constexpr int kTokenItemRows = 256;               // query rows of an item, at most
 constexpr int kTokenPartFloats = kTokenItemRows * (128 + 2);   // a partial result: O, maximum, sum
+constexpr int kTokenMaxCtas = 160;                // CTAs of the attention, at most
 constexpr int kTokenMaxNodes = 128;               // nodes of a tree, at most
+// A CTA's share in joining one item that was cut (token_attn.cuh); r0 == r1: none
+struct TokenJoin {
+  int c1, k, first_slot, rows, r0, r1, g, out_row;
+};
 struct TokenAttnArgs {
   const int32_t* ctx_len;        // [B] tokens in the cache; nullptr: none
   const int32_t* cu;             // packed prompts: [B+1] first row of each; nullptr: n_rows rows per sequence
@@ -276,6 +281,7 @@ struct TokenAttnArgs {
   const int32_t* cnt;
   __nv_bfloat16* out;            // [rows, G*H, d]
   float* part;                   // workspace [2 n_ctas][kTokenPartFloats]
+  TokenJoin* joins;              // workspace [n_ctas][2]
   int* err;
   int n_entries, G, H, max_ctx, kslots;
   int n_rows;                    // rows of all prompts, or of each sequence

@@ -26,7 +26,6 @@
 namespace sparda {
 
 namespace {
-using tok::Cursor;
 using tok::Item;
 using tok::Segments;
 using tok::u64;
@@ -113,22 +112,28 @@ struct Steps {
   }
 };
 
-// The blocks of an item. Block s < nctx is a block of the cache, the others are blocks of the new tokens.
 // A segment as the scheduling warp hands it to the other warps, through a ring in shared memory.
 struct Work {
   int b, g, n, P, nctx, row0, tok0, nblk, k0, k1, slot, tiles;   // k0 == k1: no more
 };
 constexpr int kWorkRing = 2;
 
+// The blocks of an item. Block s < nctx is a block of the cache, the others are blocks of the new tokens.
 struct Blocks {
   int j0, j1;        // lane l: the selection's entries l and 32 + l (selected blocks)
+  u64 part;          // selected blocks with fewer than 64 tokens
   bool sel;
+  __device__ __forceinline__ int rows_of(const Work& it, int j) const {
+    return j < 0 || j > it.P / kBlock ? 0 : min(kBlock, it.P - j * kBlock);
+  }
   __device__ __forceinline__ void load(const TokenAttnArgs& a, const Work& it, int lane) {
     sel = a.idx != nullptr;
     if (sel) {
       const int32_t* p = a.idx + (size_t)(it.b * a.G + it.g) * a.kslots;
       j0 = lane < it.nctx ? p[lane] : 0;
       j1 = lane + 32 < it.nctx ? p[lane + 32] : 0;
+      part = __ballot_sync(0xffffffffu, rows_of(it, j0) < kBlock) |
+             (u64)__ballot_sync(0xffffffffu, rows_of(it, j1) < kBlock) << 32;
     }
   }
   // the cache's block number (every lane calls); -1: outside the sequence
@@ -137,12 +142,13 @@ struct Blocks {
     const int j = __shfl_sync(0xffffffffu, s < 32 ? j0 : j1, s & 31);
     return j >= 0 && j <= it.P / kBlock ? j : -1;
   }
-  // its rows that hold tokens: 0 .. 64
+  // rows of block s that hold tokens: 0 .. 64 (every lane calls), and whether it is 64
   __device__ __forceinline__ int rows(const Work& it, int s) const {
-    if (s >= it.nblk) return 0;
-    if (s >= it.nctx) return min(kBlock, it.n - (s - it.nctx) * kBlock);
-    const int j = block(it, s);
-    return j < 0 ? 0 : max(0, min(kBlock, it.P - j * kBlock));
+    return s >= it.nctx ? min(kBlock, it.n - (s - it.nctx) * kBlock) : rows_of(it, block(it, s));
+  }
+  __device__ __forceinline__ bool full(const Work& it, int s) const {
+    if (s >= it.nctx) return (s - it.nctx + 1) * kBlock <= it.n;
+    return sel ? !(part >> s & 1) : (s + 1) * kBlock <= it.P;
   }
 };
 
@@ -184,6 +190,7 @@ __global__ void __launch_bounds__(kThreads, 1) token_attn_kernel(const TokenAttn
 
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const int H = a.H, tp = a.tp, tpi = kDup ? tp : 2 * tp;
+  grid_dep_launch();
   if (tid == 0) {
     mbar_init(q_full, 1);
     mbar_init(q_empty, 1);
@@ -256,14 +263,15 @@ __global__ void __launch_bounds__(kThreads, 1) token_attn_kernel(const TokenAttn
     Segments seg(a, tpi, lane, blockIdx.x);
     seg.init(blockIdx.x == 0);
     Item im;
+    int n_join = 0;
     for (bool more = true; ok && more;) {
       more = seg.next(im);
       const int i = n_work % kWorkRing;
       if (n_work >= (unsigned)kWorkRing) ok = warp_wait(&w_empty[i], ((n_work / kWorkRing) & 1) ^ 1, a.err);
       if (ok && lane == 0) {
         if (more) {
-          work[i].b = im.b;
-          work[i].g = im.g;
+          work[i].b = im.e / a.G;
+          work[i].g = im.e % a.G;
           work[i].n = im.en.n;
           work[i].P = im.en.P;
           work[i].nctx = im.en.nctx;
@@ -281,7 +289,14 @@ __global__ void __launch_bounds__(kThreads, 1) token_attn_kernel(const TokenAttn
       }
       __syncwarp();
       ++n_work;
+      TokenJoin j;
+      if (more && seg.join(im, j)) {
+        if (lane == 0) a.joins[2 * blockIdx.x + n_join] = j;
+        ++n_join;
+      }
     }
+    if (lane == 0)
+      for (; n_join < 2; ++n_join) a.joins[2 * blockIdx.x + n_join].r0 = a.joins[2 * blockIdx.x + n_join].r1 = 0;
   } else if (warp == 0) {
     // ------------------------------------------------------------ TMA producer
     if (lane == 0) {
@@ -361,45 +376,49 @@ __global__ void __launch_bounds__(kThreads, 1) token_attn_kernel(const TokenAttn
     // ------------------------------------------------------------ MMA issuer
     constexpr uint32_t id_qk = tc05::idesc_bf16(128, 128, 0, 0);
     constexpr uint32_t id_pv = tc05::idesc_bf16(128, 128, 0, 1);
-    const u64 dq = tc05::smem_desc(smem_addr(qs), 16, 1024);
-    const u64 dk = tc05::smem_desc(smem_addr(ring), 16, 1024);
-    const u64 dv = tc05::smem_desc(smem_addr(ring), kHalfCols, 1024);
+    const uint32_t tm = __shfl_sync(0xffffffffu, tmem, 0), qs_at = __shfl_sync(0xffffffffu, smem_addr(qs), 0);
+    const uint32_t ring_at = __shfl_sync(0xffffffffu, smem_addr(ring), 0);
+    const u64 dq = tc05::smem_desc(qs_at, 16, 1024);
+    const u64 dk = tc05::smem_desc(ring_at, 16, 1024);
+    const u64 dv = tc05::smem_desc(ring_at, kHalfCols, 1024);
+    const uint32_t leader = tc05::elect_leader();
     unsigned n_ld = 0, n_item = 0, n_p[2] = {0, 0};
     while (ok && next()) {
-      const Steps<kDup> st(it.k1 - it.k0, it.tiles);
+      const Steps<kDup> st(__shfl_sync(0xffffffffu, it.k1 - it.k0, 0), __shfl_sync(0xffffffffu, it.tiles, 0));
       auto issue_qk = [&](int s) {
         const int t = st.tile(s), p = st.key(s);
-        const unsigned i = n_ld + st.place_k(p);
-        ok = ok && warp_wait(&kv_full[i % kStages], (i / kStages) & 1, a.err);
-        if (!ok) return;
-        tc05::fence_after();
-        if (lane == 0) {
-          const u64 da = dq + (kDup ? 0 : t * (kQTile >> 4)), db = dk + (i % kStages) * (kStage >> 4);
-#pragma unroll
-          for (int kk = 0; kk < 8; ++kk) {
-            const uint32_t off = (kk >> 2) * (kHalfCols >> 4) + (kk & 3) * 2;
-            tc05::mma_bf16_ss(tmem + 256 * t, da + off, db + off, id_qk, kk > 0 ? 1u : 0u);
-          }
-          tc05::commit(&s_full[t]);
-          if (st.last_use(s)) tc05::commit(&kv_empty[i % kStages]);
-          if (s == st.M - 1) tc05::commit(q_empty);
+        const unsigned i = n_ld + st.place_k(p), stage = i % kStages;
+        if (kDup || t == 0) {
+          ok = warp_wait(&kv_full[stage], (i / kStages) & 1, a.err);
+          if (!ok) return;
+          tc05::fence_after();
         }
-        __syncwarp();
+        const u64 da = dq + (kDup ? 0 : t * (kQTile >> 4)), db = dk + stage * (kStage >> 4);
+        const uint32_t d = tm + 256 * t;
+#pragma unroll
+        for (int kk = 0; kk < 8; ++kk) {
+          const uint32_t off = (kk >> 2) * (kHalfCols >> 4) + (kk & 3) * 2;
+          tc05::mma_bf16_ss_by(leader, d, da + off, db + off, id_qk, kk > 0 ? 1u : 0u);
+        }
+        tc05::commit_by(leader, &s_full[t]);
+        if (st.last_use(s)) tc05::commit_by(leader, &kv_empty[stage]);
+        if (s == st.M - 1) tc05::commit_by(leader, q_empty);
       };
       ok = warp_wait(q_full, n_item & 1, a.err);
       ++n_item;
       for (int s = 0; ok && s < min(st.L, st.M); ++s) issue_qk(s);
       for (int s = 0; ok && s < st.M; ++s) {
         const int t = st.tile(s), p = st.key(s);
-        const unsigned i = n_ld + st.place_v(p);
-        uint8_t* vs = ring + (i % kStages) * kStage;
+        const unsigned i = n_ld + st.place_v(p), stage = i % kStages;
         const int blk = 2 * (it.k0 + p);
         const bool two = blk + 1 < it.nblk;
-        ok = warp_wait(&kv_full[i % kStages], (i / kStages) & 1, a.err);
-        if (ok && (kDup || t == 0)) {
-          // value rows without a token
-          const int r0 = bl.rows(it, blk), r1 = two ? bl.rows(it, blk + 1) : kBlock;
-          if (r0 < kBlock || r1 < kBlock) {
+        if (kDup || t == 0) {
+          ok = warp_wait(&kv_full[stage], (i / kStages) & 1, a.err);
+          if (!ok) break;
+          if (!bl.full(it, blk) || (two && !bl.full(it, blk + 1))) {
+            // value rows without a token
+            uint8_t* vs = ring + stage * kStage;
+            const int r0 = bl.rows(it, blk), r1 = two ? bl.rows(it, blk + 1) : kBlock;
             for (int h = 0; h < 2; ++h)
               for (int e = (h ? r1 : r0) * 8 + lane; e < kBlock * 8; e += 32) {
                 uint8_t* d = vs + h * (kBlockBytes / 2) + e * 16;
@@ -410,36 +429,29 @@ __global__ void __launch_bounds__(kThreads, 1) token_attn_kernel(const TokenAttn
             __syncwarp();
           }
         }
-        const u64 db = dv + (i % kStages) * (kStage >> 4);
+        const u64 db = dv + stage * (kStage >> 4);
+        const uint32_t d = tm + 256 * t + 128, pa = tm + 256 * t;
 #pragma unroll
         for (int h = 0; h < 2; ++h) {
           ok = ok && warp_wait(&p_full[2 * t + h], n_p[t] & 1, a.err);
           if (ok && (h == 0 || two)) {
             tc05::fence_after();
-            if (lane == 0) {
 #pragma unroll
-              for (int kk = 4 * h; kk < 4 * h + 4; ++kk)
-                tc05::mma_bf16_ts(tmem + 256 * t + 128, tmem + 256 * t + 8 * kk, db + kk * 128, id_pv,
-                                  (s >= st.L || kk > 0) ? 1u : 0u);
-            }
+            for (int kk = 4 * h; kk < 4 * h + 4; ++kk)
+              tc05::mma_bf16_ts_by(leader, d, pa + 8 * kk, db + kk * 128, id_pv, (s >= st.L || kk > 0) ? 1u : 0u);
           }
         }
         ++n_p[t];
         if (!ok) break;
-        if (lane == 0) {
-          if (st.last_use(s)) tc05::commit(&kv_empty[i % kStages]);
-          if (s + st.L >= st.M) tc05::commit(&o_full[t]);
-        }
-        __syncwarp();
+        if (st.last_use(s)) tc05::commit_by(leader, &kv_empty[stage]);
+        if (s + st.L >= st.M) tc05::commit_by(leader, &o_full[t]);
         if (s + st.L < st.M) issue_qk(s + st.L);
       }
       n_ld += 2 * st.n;
     }
     if (!ok) {                                               // a wait ran out: let the MMAs under way end
-      if (lane == 0) {
-        tc05::commit(drain);
-        mbar_wait(drain, 0, a.err);
-      }
+      tc05::commit_by(leader, drain);
+      mbar_wait(drain, 0, a.err);
       __syncwarp();
     }
     }
@@ -496,8 +508,6 @@ __global__ void __launch_bounds__(kThreads, 1) token_attn_kernel(const TokenAttn
           }
         }
       }
-      // blocks before this one are attended whole by every row of the tile
-      const int plain = bl.sel ? 0 : it.P % kBlock != 0 ? it.nctx - 1 : it.nctx + (a.parent ? 0 : (tile_tok + 1) / kBlock);
       float m_used = -INFINITY, l = 0.f;
       bool any = false;                                      // this tile has had a step
       for (int s = (kDup || st.L == 2) ? t : 0; s < st.M; s += st.L) {
@@ -508,7 +518,7 @@ __global__ void __launch_bounds__(kThreads, 1) token_attn_kernel(const TokenAttn
         bool masked = false;                                 // warp-uniform
 #pragma unroll
         for (int h = 0; h < 2; ++h) {
-          if (blk + 2 <= plain || (h == 1 && !two)) break;
+          if (h == 1 && !two) break;
           const int sb = blk + h;
           if (sb >= it.nctx) {
             const int u0 = (sb - it.nctx) * kBlock;
@@ -519,12 +529,9 @@ __global__ void __launch_bounds__(kThreads, 1) token_attn_kernel(const TokenAttn
               see[h] = first_bits(tok + 1 - u0);
               masked = true;
             }
-          } else {
-            const int rows = bl.rows(it, sb);
-            if (rows < kBlock) {
-              see[h] = first_bits(rows);
-              masked = true;
-            }
+          } else if (!bl.full(it, sb)) {
+            see[h] = first_bits(bl.rows(it, sb));
+            masked = true;
           }
         }
         ok = warp_wait(&s_full[t], n_s & 1, a.err);
@@ -686,46 +693,29 @@ __global__ void __launch_bounds__(kThreads, 1) token_attn_kernel(const TokenAttn
 }
 
 // Joins the partial results of the items that the key-tile division cut: out = sum_i w_i O_i / sum_i w_i l_i
-// with w_i = 2^(m_i - max m). Block c stands for CTA c of the attention; the item that CTA c's range begins in
-// and the one it ends in are each joined by all the CTAs that share them, every one an equal part of
-// the item's rows.
+// with w_i = 2^(m_i - max m). Block c joins what CTA c of the attention left in joins[c]: its shares of the rows of
+// at most two items (the one its range began in and the one it ended in).
 constexpr int kJoinThreads = 256;
 
-__global__ void __launch_bounds__(kJoinThreads) token_attn_join_kernel(const TokenAttnArgs a, int dup) {
+__global__ void __launch_bounds__(kJoinThreads) token_attn_join_kernel(const TokenAttnArgs a) {
   grid_dep_wait();
-  const int lane = threadIdx.x & 31, c = blockIdx.x;
-  const int tp = a.tp, tpi = dup ? tp : 2 * tp, H = a.H;
-  Cursor cur(a, tpi, lane);
-  cur.init(false);
-  if (!cur.split || c >= cur.n_ctas) return;
-  const u64 W = cur.total;
-  const int n = cur.n_ctas;
-  const u64 p0 = tok::range_start(W, n, c), p1 = tok::range_start(W, n, c + 1);
-  if (p0 >= p1) return;
-  u64 done = ~0ull;
+  const int tp = a.tp, H = a.H;
   for (int which = 0; which < 2; ++which) {
-    Item it;
-    cur.tile_at(which ? p1 - 1 : p0, it);
-    const u64 s = it.start, e = s + it.nkt;
-    if (s == done) return;
-    done = s;
-    if (p0 <= s && p1 >= e) continue;                        // not cut
-    const int c1 = tok::range_owner(W, n, s), c2 = tok::range_owner(W, n, e - 1), k = c2 - c1 + 1;
-    const int first_slot = 2 * c1 + (tok::range_start(W, n, c1) < s ? 1 : 0);
-    const int rows = min(tpi, it.en.n - it.tok0) * H;
-    const int r0 = (int)((long long)rows * (c - c1) / k), r1 = (int)((long long)rows * (c - c1 + 1) / k);
-    for (int i = threadIdx.x; i < (r1 - r0) * 32; i += kJoinThreads) {
-      const int v = r0 + i % (r1 - r0), quad = i / (r1 - r0);
+    const TokenJoin j = a.joins[2 * blockIdx.x + which];
+    const int n = j.r1 - j.r0;
+    for (int i = threadIdx.x; i < n * 32; i += kJoinThreads) {
+      const int v = j.r0 + i % n, quad = i / n;
       const int tk = v / H, prow = (tk / tp) * kTileRows + (tk % tp) * H + v % H;
       float m = -INFINITY, l = 0.f;
       float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
-      for (int q = c1; q <= c2; ++q) {
-        const float* part = a.part + (size_t)(q == c1 ? first_slot : 2 * q) * kTokenPartFloats;
+#pragma unroll 4
+      for (int q = 0; q < j.k; ++q) {
+        const float* part = a.part + (size_t)(q == 0 ? j.first_slot : 2 * (j.c1 + q)) * kTokenPartFloats;
         const float mi = part[128 * kTokenItemRows + prow], li = part[129 * kTokenItemRows + prow];
         const float4 oi = reinterpret_cast<const float4*>(part)[quad * kTokenItemRows + prow];
-        if (mi == -INFINITY && !(li != li)) continue;        // no key of that part is attended
-        const float mn = fmaxf(m, mi);
-        const float w = m == -INFINITY ? 0.f : fast_exp2(m - mn), wi = mi == -INFINITY ? 1.f : fast_exp2(mi - mn);
+        // mi is -inf where the row attends no key of this part (or every score is NaN: then li is too)
+        const float mn = fmaxf(m, mi), ref = mn == -INFINITY ? 0.f : mn;
+        const float w = fast_exp2(m - ref), wi = mi == -INFINITY ? 1.f : fast_exp2(mi - ref);
         o.x = o.x * w + oi.x * wi;
         o.y = o.y * w + oi.y * wi;
         o.z = o.z * w + oi.z * wi;
@@ -734,9 +724,7 @@ __global__ void __launch_bounds__(kJoinThreads) token_attn_join_kernel(const Tok
         m = mn;
       }
       const float inv = l > 0.f || l != l ? 1.f / l : 0.f;
-      const int tok = it.tok0 + tk;
-      const size_t row = a.cu ? (size_t)it.en.row0 + tok : (size_t)it.b * a.n_rows + tok;
-      uint2* dst = reinterpret_cast<uint2*>(a.out + ((row * a.G + it.g) * H + v % H) * kHeadDim);
+      uint2* dst = reinterpret_cast<uint2*>(a.out + (((size_t)(j.out_row + tk) * a.G + j.g) * H + v % H) * kHeadDim);
       dst[quad] = make_uint2(pack_bf16(o.x * inv, o.y * inv), pack_bf16(o.z * inv, o.w * inv));
     }
   }
@@ -749,7 +737,7 @@ static cudaError_t launch(const TokenAttnArgs& a, const CUtensorMap* m, cudaStre
   token_attn_kernel<kDup><<<a.n_ctas, kThreads, smem_bytes<kDup>(), s>>>(a, m[0], m[1], m[2], m[3], m[4]);
   const cudaError_t e = cudaGetLastError();
   if (e != cudaSuccess) return e;
-  return launch_pdl(token_attn_join_kernel, dim3(a.n_ctas), dim3(kJoinThreads), 0, s, a, kDup ? 1 : 0);
+  return launch_pdl(token_attn_join_kernel, dim3(a.n_ctas), dim3(kJoinThreads), 0, s, a);
 }
 
 cudaError_t launch_token_attn(const TokenAttnArgs& args, const CUtensorMap* maps, cudaStream_t s) {
