@@ -152,9 +152,13 @@ struct Blocks {
   }
 };
 
-// The bounded wait of a whole warp: true in every lane or in none.
+// The bounded wait of a whole warp: true in every lane or in none, and the warp is converged behind it. One look
+// first: a phase that is complete costs no suspended wait (32768-token prompt 7.5 -> 6.3 ms; more looks, 7.0).
 __device__ __forceinline__ bool warp_wait(uint64_t* bar, uint32_t parity, int* err) {
-  return __all_sync(0xffffffffu, mbar_wait(bar, parity, err));
+  if (__all_sync(0xffffffffu, mbar_test_wait(bar, parity))) return true;
+  const bool ok = __all_sync(0xffffffffu, mbar_wait(bar, parity, err));
+  __syncwarp();
+  return ok;
 }
 
 // 64-bit mask of the first n keys, 0 <= n <= 64
