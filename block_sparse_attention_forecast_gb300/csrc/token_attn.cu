@@ -93,25 +93,6 @@ __device__ __forceinline__ u64 add2(u64 a, u64 b) {
   return r;
 }
 
-// How the key tiles of a segment are stepped through. Step s works on tile t(s) and the segment's key tile
-// p(s); with L tiles under way, step s + L is the tile's next.
-template <bool kDup>
-struct Steps {
-  int n, L, M;       // key tiles, tiles under way, steps
-  __device__ __forceinline__ explicit Steps(int key_tiles, int tiles) : n(key_tiles) {
-    L = kDup ? 2 : tiles;
-    M = kDup ? n : n * L;
-  }
-  __device__ __forceinline__ int tile(int s) const { return kDup ? (s & 1) : (L == 2 ? (s & 1) : 0); }
-  __device__ __forceinline__ int key(int s) const { return kDup ? s : (L == 2 ? (s >> 1) : s); }
-  __device__ __forceinline__ bool last_use(int s) const { return kDup || tile(s) == L - 1; }
-  // place of key tile p's K and V in the order of loading, which is that of their first use
-  __device__ __forceinline__ int place_k(int p) const { return !kDup ? 2 * p : (p < 2 ? p : 2 * p - 1); }
-  __device__ __forceinline__ int place_v(int p) const {
-    return !kDup ? 2 * p + 1 : min(n, 2) + p + min(p, max(n - 2, 0));
-  }
-};
-
 // A segment as the scheduling warp hands it to the other warps, through a ring in shared memory.
 struct Work {
   int b, g, n, P, nctx, row0, tok0, nblk, k0, k1, slot, tiles;   // k0 == k1: no more
@@ -378,6 +359,8 @@ __global__ void __launch_bounds__(kThreads, 1) token_attn_kernel(const TokenAttn
         mbar_wait(&kv_full[i % kStages], (i / kStages) & 1, a.err);
   } else if (warp == 1) {
     // ------------------------------------------------------------ MMA issuer
+    // The whole warp stays together (uniform arithmetic), one lane issues. What stands between two MMAs is the
+    // tensor pipe's idle time, so a step's bookkeeping is a few counters: the ring is read in the order of loading.
     constexpr uint32_t id_qk = tc05::idesc_bf16(128, 128, 0, 0);
     constexpr uint32_t id_pv = tc05::idesc_bf16(128, 128, 0, 1);
     const uint32_t tm = __shfl_sync(0xffffffffu, tmem, 0), qs_at = __shfl_sync(0xffffffffu, smem_addr(qs), 0);
@@ -386,72 +369,131 @@ __global__ void __launch_bounds__(kThreads, 1) token_attn_kernel(const TokenAttn
     const u64 dk = tc05::smem_desc(ring_at, 16, 1024);
     const u64 dv = tc05::smem_desc(ring_at, kHalfCols, 1024);
     const uint32_t leader = tc05::elect_leader();
-    unsigned n_ld = 0, n_item = 0, n_p[2] = {0, 0};
-    while (ok && next()) {
-      const Steps<kDup> st(__shfl_sync(0xffffffffu, it.k1 - it.k0, 0), __shfl_sync(0xffffffffu, it.tiles, 0));
-      auto issue_qk = [&](int s) {
-        const int t = st.tile(s), p = st.key(s);
-        const unsigned i = n_ld + st.place_k(p), stage = i % kStages;
-        if (kDup || t == 0) {
-          ok = warp_wait(&kv_full[stage], (i / kStages) & 1, a.err);
-          if (!ok) return;
-          tc05::fence_after();
-        }
-        const u64 da = dq + (kDup ? 0 : t * (kQTile >> 4)), db = dk + stage * (kStage >> 4);
-        const uint32_t d = tm + 256 * t;
-#pragma unroll
-        for (int kk = 0; kk < 8; ++kk) {
-          const uint32_t off = (kk >> 2) * (kHalfCols >> 4) + (kk & 3) * 2;
-          tc05::mma_bf16_ss_by(leader, d, da + off, db + off, id_qk, kk > 0 ? 1u : 0u);
-        }
-        tc05::commit_by(leader, &s_full[t]);
-        if (st.last_use(s)) tc05::commit_by(leader, &kv_empty[stage]);
-        if (s == st.M - 1) tc05::commit_by(leader, q_empty);
-      };
-      ok = warp_wait(q_full, n_item & 1, a.err);
-      ++n_item;
-      for (int s = 0; ok && s < min(st.L, st.M); ++s) issue_qk(s);
-      for (int s = 0; ok && s < st.M; ++s) {
-        const int t = st.tile(s), p = st.key(s);
-        const unsigned i = n_ld + st.place_v(p), stage = i % kStages;
-        const int blk = 2 * (it.k0 + p);
-        const bool two = blk + 1 < it.nblk;
-        if (kDup || t == 0) {
-          ok = warp_wait(&kv_full[stage], (i / kStages) & 1, a.err);
-          if (!ok) break;
-          if (!bl.full(it, blk) || (two && !bl.full(it, blk + 1))) {
-            // value rows without a token
-            uint8_t* vs = ring + stage * kStage;
-            const int r0 = bl.rows(it, blk), r1 = two ? bl.rows(it, blk + 1) : kBlock;
-            for (int h = 0; h < 2; ++h)
-              for (int e = (h ? r1 : r0) * 8 + lane; e < kBlock * 8; e += 32) {
-                uint8_t* d = vs + h * (kBlockBytes / 2) + e * 16;
-                *reinterpret_cast<uint4*>(d) = make_uint4(0u, 0u, 0u, 0u);
-                *reinterpret_cast<uint4*>(d + kHalfCols) = make_uint4(0u, 0u, 0u, 0u);
-              }
-            fence_proxy_async_shared();
-            __syncwarp();
-          }
-        }
-        const u64 db = dv + stage * (kStage >> 4);
-        const uint32_t d = tm + 256 * t + 128, pa = tm + 256 * t;
-#pragma unroll
-        for (int h = 0; h < 2; ++h) {
-          ok = ok && warp_wait(&p_full[2 * t + h], n_p[t] & 1, a.err);
-          if (ok && (h == 0 || two)) {
-            tc05::fence_after();
-#pragma unroll
-            for (int kk = 4 * h; kk < 4 * h + 4; ++kk)
-              tc05::mma_bf16_ts_by(leader, d, pa + 8 * kk, db + kk * 128, id_pv, (s >= st.L || kk > 0) ? 1u : 0u);
-          }
-        }
-        ++n_p[t];
-        if (!ok) break;
-        if (st.last_use(s)) tc05::commit_by(leader, &kv_empty[stage]);
-        if (s + st.L >= st.M) tc05::commit_by(leader, &o_full[t]);
-        if (s + st.L < st.M) issue_qk(s + st.L);
+    unsigned stage = 0, full_parity = 0, q_parity = 0, p_parity[2] = {0, 0};
+    // the next load of the ring, once it is there
+    auto take = [&]() {
+      const unsigned at = stage;
+      ok = ok && warp_wait(&kv_full[at], full_parity, a.err);
+      if (++stage == kStages) {
+        stage = 0;
+        full_parity ^= 1;
       }
-      n_ld += 2 * st.n;
+      tc05::fence_after();
+      return at;
+    };
+    auto issue_qk = [&](int t, unsigned at) {                // S_t = Q_t K^T
+      const u64 da = dq + (kDup ? 0 : t * (kQTile >> 4)), db = dk + at * (kStage >> 4);
+      const uint32_t d = tm + 256 * t;
+#pragma unroll
+      for (int kk = 0; kk < 8; ++kk) {
+        const uint32_t off = (kk >> 2) * (kHalfCols >> 4) + (kk & 3) * 2;
+        tc05::mma_bf16_ss_by(leader, d, da + off, db + off, id_qk, kk > 0 ? 1u : 0u);
+      }
+      tc05::commit_by(leader, &s_full[t]);
+    };
+    auto issue_pv = [&](int t, unsigned at, bool first, bool two) {   // O_t += P_t V
+      const u64 db = dv + at * (kStage >> 4);
+      const uint32_t d = tm + 256 * t + 128, pa = tm + 256 * t;
+#pragma unroll
+      for (int h = 0; h < 2; ++h) {
+        ok = ok && warp_wait(&p_full[2 * t + h], p_parity[t], a.err);
+        if (ok && (h == 0 || two)) {
+          tc05::fence_after();
+#pragma unroll
+          for (int kk = 4 * h; kk < 4 * h + 4; ++kk)
+            tc05::mma_bf16_ts_by(leader, d, pa + 8 * kk, db + kk * 128, id_pv, (kk > 0 || !first) ? 1u : 0u);
+        }
+      }
+      p_parity[t] ^= 1;
+    };
+    // value rows without a token, of a key tile whose blocks hold rows0 and rows1 tokens: zeroed
+    auto clear_rows = [&](unsigned at, int rows0, int rows1) {
+      uint8_t* vs = ring + at * kStage;
+      for (int h = 0; h < 2; ++h)
+        for (int e = (h ? rows1 : rows0) * 8 + lane; e < kBlock * 8; e += 32) {
+          uint8_t* d = vs + h * (kBlockBytes / 2) + e * 16;
+          *reinterpret_cast<uint4*>(d) = make_uint4(0u, 0u, 0u, 0u);
+          *reinterpret_cast<uint4*>(d + kHalfCols) = make_uint4(0u, 0u, 0u, 0u);
+        }
+      fence_proxy_async_shared();
+      __syncwarp();
+    };
+    while (ok && next()) {
+      const int n = __shfl_sync(0xffffffffu, it.k1 - it.k0, 0), tiles = __shfl_sync(0xffffffffu, it.tiles, 0);
+      // the segment's key tiles with fewer than 128 tokens: all before the last new block's tile are whole, but
+      // for the one at the cache's end (and selected blocks)
+      const int nblk = __shfl_sync(0xffffffffu, it.nblk, 0), k0 = __shfl_sync(0xffffffffu, it.k0, 0);
+      const int ragged0 = bl.sel ? 0 : __shfl_sync(0xffffffffu, it.P % kBlock ? (it.nctx - 1) / 2 : it.nblk, 0) - k0;
+      const int ragged1 = __shfl_sync(0xffffffffu, (it.nctx + it.n / kBlock) / 2, 0) - k0;
+      ok = warp_wait(q_full, q_parity, a.err);
+      q_parity ^= 1;
+      unsigned ks = take();
+      if (!ok) break;
+      issue_qk(0, ks);
+      if (!kDup && tiles == 2) issue_qk(1, ks);
+      tc05::commit_by(leader, &kv_empty[ks]);
+      if (kDup && n > 1) {
+        ks = take();
+        if (!ok) break;
+        issue_qk(1, ks);
+        tc05::commit_by(leader, &kv_empty[ks]);
+      }
+      if (n <= (kDup ? 2 : 1)) tc05::commit_by(leader, q_empty);
+      // one step of tile t on key tile p of the segment (V in stage vs); `more`: with S of the tile's next, K in ks
+      for (int p = 0; ok && p < n; ++p) {
+        const bool two = 2 * (k0 + p) + 1 < nblk;
+        const unsigned vs = take();
+        if (!ok) break;
+        if (p == ragged0 || p >= ragged1 || bl.sel) {
+          const int blk = 2 * (k0 + p);
+          const int rows0 = bl.rows(it, blk), rows1 = two ? bl.rows(it, blk + 1) : kBlock;
+          if (rows0 < kBlock || rows1 < kBlock) clear_rows(vs, rows0, rows1);
+        }
+        if (!kDup) {
+          const bool more = p + 1 < n;
+          issue_pv(0, vs, p == 0, two);
+          if (!ok) break;
+          if (more) {
+            ks = take();
+            if (!ok) break;
+            issue_qk(0, ks);
+          } else {
+            tc05::commit_by(leader, &o_full[0]);
+          }
+          if (tiles == 2) {
+            issue_pv(1, vs, p == 0, two);
+            if (!ok) break;
+            tc05::commit_by(leader, &kv_empty[vs]);
+            if (more)
+              issue_qk(1, ks);
+            else
+              tc05::commit_by(leader, &o_full[1]);
+          } else {
+            tc05::commit_by(leader, &kv_empty[vs]);
+          }
+          if (more) tc05::commit_by(leader, &kv_empty[ks]);
+          if (p + 2 == n) tc05::commit_by(leader, q_empty);
+        } else {
+          auto step = [&](int t) {
+            issue_pv(t, vs, p < 2, two);
+            if (!ok) return;
+            tc05::commit_by(leader, &kv_empty[vs]);
+            if (p + 2 < n) {
+              ks = take();
+              if (!ok) return;
+              issue_qk(t, ks);
+              tc05::commit_by(leader, &kv_empty[ks]);
+              if (p + 3 == n) tc05::commit_by(leader, q_empty);
+            } else {
+              tc05::commit_by(leader, &o_full[t]);
+            }
+          };
+          if (p & 1)
+            step(1);
+          else
+            step(0);
+        }
+      }
     }
     if (!ok) {                                               // a wait ran out: let the MMAs under way end
       tc05::commit_by(leader, drain);
@@ -480,7 +522,7 @@ __global__ void __launch_bounds__(kThreads, 1) token_attn_kernel(const TokenAttn
     u64 anc0 = 0, anc1 = 0;                                  // tree: this row's ancestors and itself
     while (ok && next()) {
       if (!kDup && t >= it.tiles) continue;
-      const Steps<kDup> st(it.k1 - it.k0, it.tiles);
+      const int n = it.k1 - it.k0;
       const int tile_tok = it.tok0 + (kDup ? 0 : t * tp);
       const int tok = tile_tok + rt;                         // in the sequence
       if (a.parent && (it.b != tree_b || !kDup)) {
@@ -512,17 +554,19 @@ __global__ void __launch_bounds__(kThreads, 1) token_attn_kernel(const TokenAttn
           }
         }
       }
+      // key tiles before this one are attended whole by every row of the tile (selected blocks: looked at one by one)
+      const int whole = bl.sel ? 0 : (it.P % kBlock ? it.nctx - 1 : it.nctx + (a.parent ? 0 : (tile_tok + 1) / kBlock)) / 2;
       float m_used = -INFINITY, l = 0.f;
       bool any = false;                                      // this tile has had a step
-      for (int s = (kDup || st.L == 2) ? t : 0; s < st.M; s += st.L) {
-        const int blk = 2 * (it.k0 + st.key(s));
+      for (int p = kDup ? t : 0; p < n; p += kDup ? 2 : 1) {
+        const int blk = 2 * (it.k0 + p);
         const bool two = blk + 1 < it.nblk;
         // the keys of each block that this row attends
         u64 see[2] = {~0ull, two ? ~0ull : 0ull};
         bool masked = false;                                 // warp-uniform
 #pragma unroll
         for (int h = 0; h < 2; ++h) {
-          if (h == 1 && !two) break;
+          if (it.k0 + p < whole || (h == 1 && !two)) break;
           const int sb = blk + h;
           if (sb >= it.nctx) {
             const int u0 = (sb - it.nctx) * kBlock;
@@ -626,7 +670,7 @@ __global__ void __launch_bounds__(kThreads, 1) token_attn_kernel(const TokenAttn
         ml_sh[256 * t + 128 + r] = l;
 #pragma unroll
         for (int u = 0; u < 2; ++u)
-          if (u < st.M) {
+          if (u < n) {
             ok = ok && warp_wait(&o_full[u], n_o[u] & 1, a.err);
             ++n_o[u];
           }
@@ -656,7 +700,7 @@ __global__ void __launch_bounds__(kThreads, 1) token_attn_kernel(const TokenAttn
           tc05::ld32(tmem + lane_off + (kDup ? 0 : 256 * t) + 128 + 32 * c, o);
           tc05::wait_ld();
           if (kDup) {
-            if (st.M > 1) {
+            if (n > 1) {
               float o1[32];
               tc05::ld32(tmem + lane_off + 256 + 128 + 32 * c, o1);
               tc05::wait_ld();
