@@ -241,7 +241,7 @@ size_t kv4_workspace_bytes(const sparda_shape* s, int32_t batch, int32_t kind) {
 // Two partial results, and two shares in joining, for each CTA of the attention of new tokens.
 size_t token_workspace_bytes(const sparda_shape* s, int32_t batch) {
   if (kv4_shape_status(s) != SPARDA_OK || batch < 1 || batch > s->max_batch) return 0;
-  return (size_t)2 * kTokenMaxCtas * (kTokenPartFloats * sizeof(float) + sizeof(TokenJoin));
+  return (size_t)2 * kTokenMaxCtas * (kTokenPartFloats * sizeof(float) + sizeof(TokenJoin)) + 16;
 }
 
 #define SPARDA_TRY(x)                     \
@@ -1087,7 +1087,8 @@ int32_t run_token_attn(const sparda_shape* s, const sparda_layer_kv* L, const vo
   const int sms = sm_count();
   if (!a.err || sms < 1) return SPARDA_ERR_CUDA;
   a.out = static_cast<__nv_bfloat16*>(out);
-  a.part = static_cast<float*>(ws);
+  a.wide_out = aligned(out, 32);
+  a.part = reinterpret_cast<float*>((reinterpret_cast<uintptr_t>(ws) + 31) & ~static_cast<uintptr_t>(31));
   a.joins = reinterpret_cast<TokenJoin*>(a.part + (size_t)2 * kTokenMaxCtas * kTokenPartFloats);
   a.n_entries = batch * G;
   a.G = G;

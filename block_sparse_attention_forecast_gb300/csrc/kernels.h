@@ -280,16 +280,18 @@ struct TokenAttnArgs {
   const int32_t* idx;            // [B, G, kslots], the attended blocks of the cache; nullptr: all
   const int32_t* cnt;
   __nv_bfloat16* out;            // [rows, G*H, d]
-  float* part;                   // workspace [2 n_ctas][kTokenPartFloats]
+  float* part;                   // workspace [2 n_ctas][kTokenPartFloats], 32-byte aligned
   TokenJoin* joins;              // workspace [n_ctas][2]
   int* err;
   int n_entries, G, H, max_ctx, kslots;
   int n_rows;                    // rows of all prompts, or of each sequence
   int tp;                        // tokens per 128-row query tile
   int causal;                    // parent == nullptr
+  int wide_out;                  // out is 32-byte aligned
   int n_ctas;
   int split_items;               // fewer items than this: key tiles are divided, not items
   int min_tiles;                 // a CTA's share of key tiles, at least
+  int join_tiles;                // what joining cut items costs, in key tiles
 };
 // maps: queries (d, head, group, token, sequence); the cache's K and V [rows, 128]; the new tokens' K and V
 // (d, group, token, sequence)

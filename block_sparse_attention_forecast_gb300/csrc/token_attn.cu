@@ -93,6 +93,13 @@ __device__ __forceinline__ u64 add2(u64 a, u64 b) {
   return r;
 }
 
+// 32 bytes of global memory (32-byte aligned) in one store: a whole sector, where each thread writes a row of its own
+__device__ __forceinline__ void store32(void* dst, const uint32_t* w) {
+  asm volatile("st.global.v8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(dst), "r"(w[0]), "r"(w[1]), "r"(w[2]),
+               "r"(w[3]), "r"(w[4]), "r"(w[5]), "r"(w[6]), "r"(w[7])
+               : "memory");
+}
+
 // A segment as the scheduling warp hands it to the other warps, through a ring in shared memory.
 struct Work {
   int b, g, n, P, nctx, row0, tok0, nblk, k0, k1, slot, tiles;   // k0 == k1: no more
@@ -202,6 +209,9 @@ __global__ void __launch_bounds__(kThreads, 1) token_attn_kernel(const TokenAttn
     tc05::alloc(tmem_sh, kCols);
     tc05::relinquish();
   }
+  grid_dep_wait();
+  Segments seg(a, tpi, lane, blockIdx.x);
+  if (warp == 2) seg.init(blockIdx.x == 0);
   // query rows that no load fills: zero, once
   for (int i = tid; i < (kTileRows - tp * H) * 8; i += kThreads)
 #pragma unroll
@@ -245,8 +255,6 @@ __global__ void __launch_bounds__(kThreads, 1) token_attn_kernel(const TokenAttn
     asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kRegsMain));
   if (warp == 2) {
     // ------------------------------------------------------------ scheduler
-    Segments seg(a, tpi, lane, blockIdx.x);
-    seg.init(blockIdx.x == 0);
     Item im;
     int n_join = 0;
     for (bool more = true; ok && more;) {
@@ -689,9 +697,9 @@ __global__ void __launch_bounds__(kThreads, 1) token_attn_kernel(const TokenAttn
         const bool live = rt < tp && tok < it.n;
         const size_t row = a.cu ? (size_t)it.row0 + tok : (size_t)it.b * a.n_rows + tok;
         const float inv = l > 0.f || l != l ? 1.f / l : 0.f;
-        uint4* dst = reinterpret_cast<uint4*>(a.out + ((row * a.G + it.g) * H + (r - rt * H)) * kHeadDim);
-        float4* part = reinterpret_cast<float4*>(a.part + (size_t)max(it.slot, 0) * kTokenPartFloats);
+        __nv_bfloat16* dst = a.out + ((row * a.G + it.g) * H + (r - rt * H)) * kHeadDim;
         const int prow = (kDup ? 0 : t * kTileRows) + r;
+        float* part = a.part + (size_t)max(it.slot, 0) * kTokenPartFloats;
         const int c0 = kDup ? 2 * t : 0, c1 = kDup ? 2 * t + 2 : 4;
 #pragma unroll 1
         for (int c = c0; c < c1; ++c) {
@@ -710,19 +718,25 @@ __global__ void __launch_bounds__(kThreads, 1) token_attn_kernel(const TokenAttn
           }
           if (live && it.slot < 0) {
 #pragma unroll
-            for (int e = 0; e < 4; ++e)
-              dst[4 * c + e] = make_uint4(pack_bf16(o[8 * e] * inv, o[8 * e + 1] * inv),
-                                          pack_bf16(o[8 * e + 2] * inv, o[8 * e + 3] * inv),
-                                          pack_bf16(o[8 * e + 4] * inv, o[8 * e + 5] * inv),
-                                          pack_bf16(o[8 * e + 6] * inv, o[8 * e + 7] * inv));
+            for (int e = 0; e < 2; ++e) {
+              uint32_t w[8];
+#pragma unroll
+              for (int i = 0; i < 8; ++i) w[i] = pack_bf16(o[16 * e + 2 * i] * inv, o[16 * e + 2 * i + 1] * inv);
+              if (a.wide_out) {
+                store32(dst + 32 * c + 16 * e, w);
+              } else {
+                reinterpret_cast<uint4*>(dst + 32 * c + 16 * e)[0] = make_uint4(w[0], w[1], w[2], w[3]);
+                reinterpret_cast<uint4*>(dst + 32 * c + 16 * e)[1] = make_uint4(w[4], w[5], w[6], w[7]);
+              }
+            }
           } else if (live) {
 #pragma unroll
-            for (int e = 0; e < 8; ++e)
-              part[(8 * c + e) * kTokenItemRows + prow] = make_float4(o[4 * e], o[4 * e + 1], o[4 * e + 2], o[4 * e + 3]);
+            for (int e = 0; e < 4; ++e)
+              store32(part + prow * kHeadDim + 32 * c + 8 * e, reinterpret_cast<const uint32_t*>(o + 8 * e));
           }
         }
         if (live && it.slot >= 0 && (!kDup || t == 0)) {
-          float* ml = reinterpret_cast<float*>(part + 32 * kTokenItemRows);
+          float* ml = part + kTokenItemRows * kHeadDim;
           ml[prow] = m_used;
           ml[kTokenItemRows + prow] = l;
         }
@@ -741,39 +755,66 @@ __global__ void __launch_bounds__(kThreads, 1) token_attn_kernel(const TokenAttn
 }
 
 // Joins the partial results of the items that the key-tile division cut: out = sum_i w_i O_i / sum_i w_i l_i
-// with w_i = 2^(m_i - max m). Block c joins what CTA c of the attention left in joins[c]: its shares of the rows of
-// at most two items (the one its range began in and the one it ended in).
+// with w_i = 2^(m_i - max m). joins[c] holds what CTA c of the attention is to join: its shares of the rows of at most two
+// items (the one its range began in and the one it ended in). kJoinSplit blocks take a share together: what joining
+// costs is the latency of a few dependent reads, so each thread has as few as may be. A block holds 8 rows of 32
+// column quads at a time or, for items of many parts, one row whose parts are dealt out to the 8 warps.
 constexpr int kJoinThreads = 256;
+constexpr int kJoinWarps = kJoinThreads / 32;
+constexpr int kJoinSplit = 8;
+
+struct JoinSum {
+  float m, l;
+  float4 o;
+  // mi is -inf where a row attends no key of a part (or every score is a NaN: then li is one too)
+  __device__ __forceinline__ void add(float mi, float li, float4 oi) {
+    const float mn = fmaxf(m, mi), ref = mn == -INFINITY ? 0.f : mn;
+    const float w = fast_exp2(m - ref), wi = mi == -INFINITY ? 1.f : fast_exp2(mi - ref);
+    o.x = o.x * w + oi.x * wi;
+    o.y = o.y * w + oi.y * wi;
+    o.z = o.z * w + oi.z * wi;
+    o.w = o.w * w + oi.w * wi;
+    l = l * w + li * wi;
+    m = mn;
+  }
+};
 
 __global__ void __launch_bounds__(kJoinThreads) token_attn_join_kernel(const TokenAttnArgs a) {
+  __shared__ float ml_sh[kJoinWarps][2];
+  __shared__ float4 o_sh[kJoinWarps][32];
   grid_dep_wait();
-  const int tp = a.tp, H = a.H;
+  const int tp = a.tp, H = a.H, warp = threadIdx.x >> 5, quad = threadIdx.x & 31;
   for (int which = 0; which < 2; ++which) {
-    const TokenJoin j = a.joins[2 * blockIdx.x + which];
-    const int n = j.r1 - j.r0;
-    for (int i = threadIdx.x; i < n * 32; i += kJoinThreads) {
-      const int v = j.r0 + i % n, quad = i / n;
+    const TokenJoin j = a.joins[2 * (blockIdx.x / kJoinSplit) + which];
+    const int b = blockIdx.x % kJoinSplit, n = j.r1 - j.r0;
+    const bool many = j.k > 2 * kJoinWarps;                  // the parts of a row to all warps
+    const int r0 = j.r0 + n * b / kJoinSplit, r1 = j.r0 + n * (b + 1) / kJoinSplit;
+    for (int v = r0 + (many ? 0 : warp); v < r1; v += many ? 1 : kJoinWarps) {
       const int tk = v / H, prow = (tk / tp) * kTileRows + (tk % tp) * H + v % H;
-      float m = -INFINITY, l = 0.f;
-      float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
-#pragma unroll 4
-      for (int q = 0; q < j.k; ++q) {
+      JoinSum s{-INFINITY, 0.f, make_float4(0.f, 0.f, 0.f, 0.f)};
+      const int step = many ? kJoinWarps : 1;
+#pragma unroll 8
+      for (int q = many ? warp : 0; q < j.k; q += step) {
         const float* part = a.part + (size_t)(q == 0 ? j.first_slot : 2 * (j.c1 + q)) * kTokenPartFloats;
-        const float mi = part[128 * kTokenItemRows + prow], li = part[129 * kTokenItemRows + prow];
-        const float4 oi = reinterpret_cast<const float4*>(part)[quad * kTokenItemRows + prow];
-        // mi is -inf where the row attends no key of this part (or every score is NaN: then li is too)
-        const float mn = fmaxf(m, mi), ref = mn == -INFINITY ? 0.f : mn;
-        const float w = fast_exp2(m - ref), wi = mi == -INFINITY ? 1.f : fast_exp2(mi - ref);
-        o.x = o.x * w + oi.x * wi;
-        o.y = o.y * w + oi.y * wi;
-        o.z = o.z * w + oi.z * wi;
-        o.w = o.w * w + oi.w * wi;
-        l = l * w + li * wi;
-        m = mn;
+        s.add(part[kTokenItemRows * kHeadDim + prow], part[kTokenItemRows * (kHeadDim + 1) + prow],
+              reinterpret_cast<const float4*>(part + prow * kHeadDim)[quad]);
       }
-      const float inv = l > 0.f || l != l ? 1.f / l : 0.f;
-      uint2* dst = reinterpret_cast<uint2*>(a.out + (((size_t)(j.out_row + tk) * a.G + j.g) * H + v % H) * kHeadDim);
-      dst[quad] = make_uint2(pack_bf16(o.x * inv, o.y * inv), pack_bf16(o.z * inv, o.w * inv));
+      if (many) {
+        o_sh[warp][quad] = s.o;
+        if (quad == 0) {
+          ml_sh[warp][0] = s.m;
+          ml_sh[warp][1] = s.l;
+        }
+        __syncthreads();
+        if (warp == 0)
+          for (int w = 1; w < kJoinWarps; ++w) s.add(ml_sh[w][0], ml_sh[w][1], o_sh[w][quad]);
+        __syncthreads();
+      }
+      if (!many || warp == 0) {
+        const float inv = s.l > 0.f || s.l != s.l ? 1.f / s.l : 0.f;
+        uint2* dst = reinterpret_cast<uint2*>(a.out + (((size_t)(j.out_row + tk) * a.G + j.g) * H + v % H) * kHeadDim);
+        dst[quad] = make_uint2(pack_bf16(s.o.x * inv, s.o.y * inv), pack_bf16(s.o.z * inv, s.o.w * inv));
+      }
     }
   }
 }
@@ -782,16 +823,19 @@ template <bool kDup>
 static cudaError_t launch(const TokenAttnArgs& a, const CUtensorMap* m, cudaStream_t s) {
   static SmemOptIn opt;
   if (!opt.set(token_attn_kernel<kDup>, smem_bytes<kDup>())) return cudaErrorInvalidValue;
-  token_attn_kernel<kDup><<<a.n_ctas, kThreads, smem_bytes<kDup>(), s>>>(a, m[0], m[1], m[2], m[3], m[4]);
-  const cudaError_t e = cudaGetLastError();
+  const cudaError_t e = launch_pdl(token_attn_kernel<kDup>, dim3(a.n_ctas), dim3(kThreads), smem_bytes<kDup>(), s, a, m[0],
+                                   m[1], m[2], m[3], m[4]);
   if (e != cudaSuccess) return e;
-  return launch_pdl(token_attn_join_kernel, dim3(a.n_ctas), dim3(kJoinThreads), 0, s, a);
+  return launch_pdl(token_attn_join_kernel, dim3(a.n_ctas * kJoinSplit), dim3(kJoinThreads), 0, s, a);
 }
 
 cudaError_t launch_token_attn(const TokenAttnArgs& args, const CUtensorMap* maps, cudaStream_t s) {
   TokenAttnArgs a = args;
   a.split_items = 4 * a.n_ctas;
-  a.min_tiles = 2;
+  // where one query tile is taken twice, two key tiles take as long as one
+  const int two = a.n_rows <= a.tp ? 2 : 1;
+  a.min_tiles = 2 * two;
+  a.join_tiles = 4 * two;
   return a.n_rows <= a.tp ? launch<true>(a, maps, s) : launch<false>(a, maps, s);
 }
 

@@ -108,7 +108,7 @@ struct Parts {
   }
 };
 
-// The segments of CTA c, in order, for one warp (every lane calls every function).
+// The segments of CTA c, in order, for one warp (every lane calls every function). Lane l holds entry e0 + l.
 struct Segments {
   const TokenAttnArgs& a;
   const int tpi, lane;
@@ -116,17 +116,19 @@ struct Segments {
   bool split;          // key-tile division
   u32 n_ctas, total;   // CTAs that take part; items or key tiles
   u32 base, incl, sum; // 32 entries at a time: the weight before them, up to this lane's, of all
+  Entry mine;
   int e0;
   u32 pos, end, first, round;
 
   __device__ Segments(const TokenAttnArgs& args, int tokens_per_item, int ln, int cta)
       : a(args), tpi(tokens_per_item), lane(ln), c(cta) {}
 
-  __device__ __forceinline__ u32 weight(const Entry& en) const {
-    return split ? entry_tiles(a, en, tpi) : (u32)n_items(en, tpi);
+  __device__ __forceinline__ void fetch() {
+    mine = Entry{0, 0, 0, 0, false};
+    if (e0 + lane < a.n_entries) mine = load_entry(a, e0 + lane);
   }
-  __device__ __forceinline__ void load() {
-    incl = e0 + lane < a.n_entries ? weight(load_entry(a, e0 + lane)) : 0;
+  __device__ __forceinline__ void weigh() {
+    incl = split ? entry_tiles(a, mine, tpi) : (u32)n_items(mine, tpi);
 #pragma unroll
     for (int o = 1; o < 32; o <<= 1) {
       const u32 up = __shfl_up_sync(0xffffffffu, incl, o);
@@ -134,30 +136,52 @@ struct Segments {
     }
     sum = __shfl_sync(0xffffffffu, incl, 31);
   }
+  __device__ __forceinline__ Entry entry(int l) const {
+    Entry en;
+    en.n = __shfl_sync(0xffffffffu, mine.n, l);
+    en.P = __shfl_sync(0xffffffffu, mine.P, l);
+    en.nctx = __shfl_sync(0xffffffffu, mine.nctx, l);
+    en.row0 = __shfl_sync(0xffffffffu, mine.row0, l);
+    en.bad = false;
+    return en;
+  }
 
   // the division; `report`: sets the error word for bad lengths
   __device__ __forceinline__ void init(bool report) {
-    u32 items = 0;
+    u32 items = 0, longest = 0;
     bool bad = false;
-    for (int e = lane; e < a.n_entries; e += 32) {
-      const Entry en = load_entry(a, e);
-      items += n_items(en, tpi);
-      bad = bad || en.bad;
+    for (e0 = 0; e0 < a.n_entries; e0 += 32) {
+      fetch();
+      const int ni = n_items(mine, tpi);
+      items += ni;
+      if (ni > 0) longest = max(longest, (u32)(item_blocks(a, mine, ni - 1, tpi) + 1) / 2);
+      bad = bad || mine.bad;
     }
     items = __reduce_add_sync(0xffffffffu, items);
+    longest = __reduce_max_sync(0xffffffffu, longest);
     if (report && __any_sync(0xffffffffu, bad) && lane == 0) atomicOr(a.err, SPARDA_DEV_BAD_SEQ_LEN);
-    split = items < (u32)a.split_items;
+    split = false;
     total = items;
     n_ctas = a.n_ctas;
-    if (split) {
+    if (items < (u32)a.split_items) {
       u32 tiles = 0;
-      for (int e = lane; e < a.n_entries; e += 32) tiles += entry_tiles(a, load_entry(a, e), tpi);
-      total = __reduce_add_sync(0xffffffffu, tiles);
-      n_ctas = min(n_ctas, max(1u, total / a.min_tiles));
+      for (e0 = 0; e0 < a.n_entries; e0 += 32) {
+        if (a.n_entries > 32) fetch();
+        tiles += entry_tiles(a, mine, tpi);
+      }
+      tiles = __reduce_add_sync(0xffffffffu, tiles);
+      // Whole items take about as long as the longest one (one round), or half of it more than an even share
+      // (several); joining cut ones takes as long as join_tiles key tiles.
+      split = items <= n_ctas ? longest > tiles / n_ctas + a.join_tiles : longest > 2 * a.join_tiles;
+      if (split) {
+        total = tiles;
+        n_ctas = min(n_ctas, max(1u, total / a.min_tiles));
+      }
     }
     e0 = 0;
     base = 0;
-    load();
+    if (a.n_entries > 32) fetch();
+    weigh();
     round = 0;
     pos = end = first = 0;
     if (split && c < n_ctas) {
@@ -167,21 +191,22 @@ struct Segments {
     }
   }
 
-  // the entry of position p < total (not below one asked for before), and the position inside it
+  // the lane of the entry of position p < total (not below one asked for before), and the position inside it
   __device__ __forceinline__ int seek(u32 p, u32& off) {
     while (p >= base + sum) {
       base += sum;
       e0 += 32;
-      load();
+      fetch();
+      weigh();
     }
     const int l = __ffs(__ballot_sync(0xffffffffu, base + incl > p)) - 1;
     const u32 before = __shfl_sync(0xffffffffu, incl, (l + 31) & 31);
     off = p - base - (l == 0 ? 0 : before);
-    return e0 + l;
+    return l;
   }
 
-  __device__ __forceinline__ void fill(Item& it, int e, const Entry& en, int i) const {
-    it.e = e;
+  __device__ __forceinline__ void fill(Item& it, int l, const Entry& en, int i) const {
+    it.e = e0 + l;
     it.en = en;
     it.tok0 = i * tpi;
     it.nblk = item_blocks(a, en, i, tpi);
@@ -196,15 +221,15 @@ struct Segments {
       const u32 u = round * n_ctas + ((round & 1) ? n_ctas - 1 - c : c);
       ++round;
       if (u >= total) return false;
-      const int e = seek(u, off);
-      const Entry en = load_entry(a, e);
-      fill(it, e, en, n_items(en, tpi) - 1 - (int)off);
+      const int l = seek(u, off);
+      const Entry en = entry(l);
+      fill(it, l, en, n_items(en, tpi) - 1 - (int)off);
       it.k0 = 0;
       return true;
     }
     if (pos >= end) return false;
-    const int e = seek(pos, off);
-    const Entry en = load_entry(a, e);
+    const int at = seek(pos, off);
+    const Entry en = entry(at);
     // the last item with tiles_before <= off, 32 candidates at a time
     int lo = 0, len = n_items(en, tpi);
     while (len > 1) {
@@ -216,7 +241,7 @@ struct Segments {
       lo += l * step;
       len = min(step, stop - lo);
     }
-    fill(it, e, en, lo);
+    fill(it, at, en, lo);
     it.k0 = (int)(off - tiles_before(a, en, lo, tpi));
     it.start = pos - it.k0;
     it.k1 = (int)min((u32)it.k1, it.k0 + (end - pos));
