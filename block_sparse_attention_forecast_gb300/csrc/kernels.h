@@ -268,6 +268,21 @@ constexpr int kTokenItemRows = 256;               // query rows of an item, at m
 constexpr int kTokenPartFloats = kTokenItemRows * (128 + 2);   // a partial result: O, maximum, sum
 constexpr int kTokenMaxCtas = 160;                // CTAs of the attention, at most
 constexpr int kTokenMaxNodes = 128;               // nodes of a tree, at most
+// Division by a number that the host knows, for dividends below 2^31: one product and two shifts where the
+// hardware has no divide (T. Granlund and P. Montgomery, "Division by invariant integers using multiplication",
+// PLDI 1994, figure 4.1).
+struct FastDiv {
+  uint32_t d, mul, shift;
+  FastDiv() = default;
+  explicit FastDiv(uint32_t n) : d(n), mul(0), shift(0) {
+    while ((1ull << shift) < n) ++shift;
+    mul = (uint32_t)(((1ull << 32) * ((1ull << shift) - n)) / n + 1);
+  }
+#ifdef __CUDACC__
+  __device__ __forceinline__ uint32_t div(uint32_t x) const { return (__umulhi(mul, x) + x) >> shift; }
+#endif
+};
+
 // A CTA's share in joining one item that was cut (token_attn.cuh); r0 == r1: none
 struct TokenJoin {
   int c1, k, first_slot, rows, r0, r1, g, out_row;
@@ -292,6 +307,7 @@ struct TokenAttnArgs {
   int split_items;               // fewer items than this: key tiles are divided, not items
   int min_tiles;                 // a CTA's share of key tiles, at least
   int join_tiles;                // what joining cut items costs, in key tiles
+  FastDiv by_G, by_H, by_item;   // by the groups, the heads of a group, the tokens of an item
 };
 // maps: queries (d, head, group, token, sequence); the cache's K and V [rows, 128]; the new tokens' K and V
 // (d, group, token, sequence)

@@ -263,8 +263,9 @@ __global__ void __launch_bounds__(kThreads, 1) token_attn_kernel(const TokenAttn
       if (n_work >= (unsigned)kWorkRing) ok = warp_wait(&w_empty[i], ((n_work / kWorkRing) & 1) ^ 1, a.err);
       if (ok && lane == 0) {
         if (more) {
-          work[i].b = im.e / a.G;
-          work[i].g = im.e % a.G;
+          const int b = a.by_G.div(im.e);
+          work[i].b = b;
+          work[i].g = im.e - b * a.G;
           work[i].n = im.en.n;
           work[i].P = im.en.P;
           work[i].nctx = im.en.nctx;
@@ -521,7 +522,7 @@ __global__ void __launch_bounds__(kThreads, 1) token_attn_kernel(const TokenAttn
     const int t = (warp - 4) >> 2;
     const int quarter = warp & 3;                            // tensor-memory lanes 32q .. 32q+31
     const int r = quarter * 32 + lane;
-    const int rt = r / H;                                    // the row's token in its tile
+    const int rt = a.by_H.div(r);                                 // the row's token in its tile
     const uint32_t lane_off = (uint32_t)(quarter * 32) << 16;
     const uint32_t t_s = tmem + 256 * t + lane_off, t_o = t_s + 128;
     const u64 scale2 = pack2(kScaleLog2, kScaleLog2);
@@ -790,7 +791,8 @@ __global__ void __launch_bounds__(kJoinThreads) token_attn_join_kernel(const Tok
     const bool many = j.k > 2 * kJoinWarps;                  // the parts of a row to all warps
     const int r0 = j.r0 + n * b / kJoinSplit, r1 = j.r0 + n * (b + 1) / kJoinSplit;
     for (int v = r0 + (many ? 0 : warp); v < r1; v += many ? 1 : kJoinWarps) {
-      const int tk = v / H, prow = (tk / tp) * kTileRows + (tk % tp) * H + v % H;
+      const int tk = a.by_H.div(v), h = v - tk * H;
+      const int prow = (tk >= tp ? kTileRows + (tk - tp) * H : tk * H) + h;
       JoinSum s{-INFINITY, 0.f, make_float4(0.f, 0.f, 0.f, 0.f)};
       const int step = many ? kJoinWarps : 1;
 #pragma unroll 8
@@ -812,7 +814,7 @@ __global__ void __launch_bounds__(kJoinThreads) token_attn_join_kernel(const Tok
       }
       if (!many || warp == 0) {
         const float inv = s.l > 0.f || s.l != s.l ? 1.f / s.l : 0.f;
-        uint2* dst = reinterpret_cast<uint2*>(a.out + (((size_t)(j.out_row + tk) * a.G + j.g) * H + v % H) * kHeadDim);
+        uint2* dst = reinterpret_cast<uint2*>(a.out + (((size_t)(j.out_row + tk) * a.G + j.g) * H + h) * kHeadDim);
         dst[quad] = make_uint2(pack_bf16(s.o.x * inv, s.o.y * inv), pack_bf16(s.o.z * inv, s.o.w * inv));
       }
     }
@@ -835,7 +837,10 @@ cudaError_t launch_token_attn(const TokenAttnArgs& args, const CUtensorMap* maps
   // where one query tile is taken twice, two key tiles take as long as one
   const int two = a.n_rows <= a.tp ? 2 : 1;
   a.min_tiles = 2 * two;
-  a.join_tiles = 4 * two;
+  a.join_tiles = two == 2 ? 16 : 4;
+  a.by_G = FastDiv(a.G);
+  a.by_H = FastDiv(a.H);
+  a.by_item = FastDiv(two == 2 ? a.tp : 2 * a.tp);
   return a.n_rows <= a.tp ? launch<true>(a, maps, s) : launch<false>(a, maps, s);
 }
 

@@ -42,7 +42,7 @@ struct Item {
 };
 
 __device__ __forceinline__ Entry load_entry(const TokenAttnArgs& a, int e) {
-  const int b = e / a.G;
+  const int b = a.by_G.div(e);
   Entry en;
   en.P = a.ctx_len ? a.ctx_len[b] : 0;
   const int cnt = a.idx ? a.cnt[e] : 0;
@@ -62,7 +62,7 @@ __device__ __forceinline__ Entry load_entry(const TokenAttnArgs& a, int e) {
   return en;
 }
 
-__device__ __forceinline__ int n_items(const Entry& en, int tpi) { return (en.n + tpi - 1) / tpi; }
+__device__ __forceinline__ int n_items(const TokenAttnArgs& a, const Entry& en) { return a.by_item.div(en.n + a.by_item.d - 1); }
 
 __device__ __forceinline__ int item_blocks(const TokenAttnArgs& a, const Entry& en, int i, int tpi) {
   const int last = (a.causal ? min((i + 1) * tpi, en.n) : en.n) - 1;
@@ -94,7 +94,7 @@ __device__ __forceinline__ u32 tiles_before(const TokenAttnArgs& a, const Entry&
   return floor_sum(i, 2 * kBlock, tpi, kBlock * (en.nctx + 2) + tpi - 1);
 }
 __device__ __forceinline__ u32 entry_tiles(const TokenAttnArgs& a, const Entry& en, int tpi) {
-  const int ni = n_items(en, tpi);
+  const int ni = n_items(a, en);
   return ni == 0 ? 0 : tiles_before(a, en, ni - 1, tpi) + (item_blocks(a, en, ni - 1, tpi) + 1) / 2;
 }
 
@@ -128,7 +128,7 @@ struct Segments {
     if (e0 + lane < a.n_entries) mine = load_entry(a, e0 + lane);
   }
   __device__ __forceinline__ void weigh() {
-    incl = split ? entry_tiles(a, mine, tpi) : (u32)n_items(mine, tpi);
+    incl = split ? entry_tiles(a, mine, tpi) : (u32)n_items(a, mine);
 #pragma unroll
     for (int o = 1; o < 32; o <<= 1) {
       const u32 up = __shfl_up_sync(0xffffffffu, incl, o);
@@ -152,7 +152,7 @@ struct Segments {
     bool bad = false;
     for (e0 = 0; e0 < a.n_entries; e0 += 32) {
       fetch();
-      const int ni = n_items(mine, tpi);
+      const int ni = n_items(a, mine);
       items += ni;
       if (ni > 0) longest = max(longest, (u32)(item_blocks(a, mine, ni - 1, tpi) + 1) / 2);
       bad = bad || mine.bad;
@@ -223,7 +223,7 @@ struct Segments {
       if (u >= total) return false;
       const int l = seek(u, off);
       const Entry en = entry(l);
-      fill(it, l, en, n_items(en, tpi) - 1 - (int)off);
+      fill(it, l, en, n_items(a, en) - 1 - (int)off);
       it.k0 = 0;
       return true;
     }
@@ -231,7 +231,7 @@ struct Segments {
     const int at = seek(pos, off);
     const Entry en = entry(at);
     // the last item with tiles_before <= off, 32 candidates at a time
-    int lo = 0, len = n_items(en, tpi);
+    int lo = 0, len = n_items(a, en);
     while (len > 1) {
       const int step = (len + 31) / 32;
       const int i = lo + lane * step;
@@ -262,8 +262,9 @@ struct Segments {
     j.rows = min(tpi, it.en.n - it.tok0) * a.H;
     j.r0 = (int)((u32)j.rows * (c - c1) / j.k);
     j.r1 = (int)((u32)j.rows * (c - c1 + 1) / j.k);
-    j.g = it.e % a.G;
-    j.out_row = (a.cu ? it.en.row0 : it.e / a.G * a.n_rows) + it.tok0;
+    const int b = a.by_G.div(it.e);
+    j.g = it.e - b * a.G;
+    j.out_row = (a.cu ? it.en.row0 : b * a.n_rows) + it.tok0;
     return true;
   }
 };
