@@ -238,10 +238,11 @@ size_t kv4_workspace_bytes(const sparda_shape* s, int32_t batch, int32_t kind) {
   return kind == SPARDA_WS_KV4_ATTN ? base : base + mass_stats_bytes(s, kv4_mass_slots(s)) + mass_ml_bytes(s);
 }
 
-// Two partial results, and two shares in joining, for each CTA of the attention of new tokens.
+// [the item counter, zero between calls][two partial results, and two shares in joining, for each CTA of the
+// attention of new tokens]
 size_t token_workspace_bytes(const sparda_shape* s, int32_t batch) {
   if (kv4_shape_status(s) != SPARDA_OK || batch < 1 || batch > s->max_batch) return 0;
-  return (size_t)2 * kTokenMaxCtas * (kTokenPartFloats * sizeof(float) + sizeof(TokenJoin)) + 16;
+  return 256 + (size_t)2 * kTokenMaxCtas * (kTokenPartFloats * sizeof(float) + sizeof(TokenJoin)) + 16;
 }
 
 #define SPARDA_TRY(x)                     \
@@ -1088,7 +1089,8 @@ int32_t run_token_attn(const sparda_shape* s, const sparda_layer_kv* L, const vo
   if (!a.err || sms < 1) return SPARDA_ERR_CUDA;
   a.out = static_cast<__nv_bfloat16*>(out);
   a.wide_out = aligned(out, 32);
-  a.part = reinterpret_cast<float*>((reinterpret_cast<uintptr_t>(ws) + 31) & ~static_cast<uintptr_t>(31));
+  a.queue = static_cast<unsigned*>(ws);
+  a.part = reinterpret_cast<float*>((reinterpret_cast<uintptr_t>(ws) + 256 + 31) & ~static_cast<uintptr_t>(31));
   a.joins = reinterpret_cast<TokenJoin*>(a.part + (size_t)2 * kTokenMaxCtas * kTokenPartFloats);
   a.n_entries = batch * G;
   a.G = G;

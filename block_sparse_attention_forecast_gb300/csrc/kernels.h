@@ -297,6 +297,7 @@ struct TokenAttnArgs {
   __nv_bfloat16* out;            // [rows, G*H, d]
   float* part;                   // workspace [2 n_ctas][kTokenPartFloats], 32-byte aligned
   TokenJoin* joins;              // workspace [n_ctas][2]
+  unsigned* queue;               // workspace: items taken from the queue, zero between calls
   int* err;
   int n_entries, G, H, max_ctx, kslots;
   int n_rows;                    // rows of all prompts, or of each sequence

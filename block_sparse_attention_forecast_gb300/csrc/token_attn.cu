@@ -104,7 +104,7 @@ __device__ __forceinline__ void store32(void* dst, const uint32_t* w) {
 struct Work {
   int b, g, n, P, nctx, row0, tok0, nblk, k0, k1, slot, tiles;   // k0 == k1: no more
 };
-constexpr int kWorkRing = 2;
+constexpr int kWorkRing = 1;   // an item is taken when the loads of the one before have been issued, not earlier
 
 // The blocks of an item. Block s < nctx is a block of the cache, the others are blocks of the new tokens.
 struct Blocks {
@@ -244,7 +244,7 @@ __global__ void __launch_bounds__(kThreads, 1) token_attn_kernel(const TokenAttn
     it.slot = work[i].slot;
     it.tiles = work[i].tiles;
     __syncwarp();
-    if (lane == 0) bar_arrive(&w_empty[i]);
+    if (lane == 0 && warp != 0) bar_arrive(&w_empty[i]);     // (the producer's comes behind its loads)
     ++n_work;
     if (it.k0 == it.k1) return false;
     bl.load(a, it, lane);
@@ -361,6 +361,7 @@ __global__ void __launch_bounds__(kThreads, 1) token_attn_kernel(const TokenAttn
           if (ok && p + 2 < n) load(&mkc, &mkn, it.k0 + p + 2);
         }
       }
+      if (lane == 0) bar_arrive(&w_empty[(n_work - 1) % kWorkRing]);
     }
     // a wait ran out: no copy may still be under way when the CTA ends
     if (!ok && lane == 0)
@@ -784,6 +785,7 @@ __global__ void __launch_bounds__(kJoinThreads) token_attn_join_kernel(const Tok
   __shared__ float ml_sh[kJoinWarps][2];
   __shared__ float4 o_sh[kJoinWarps][32];
   grid_dep_wait();
+  if (blockIdx.x == 0 && threadIdx.x == 0) *a.queue = 0;
   const int tp = a.tp, H = a.H, warp = threadIdx.x >> 5, quad = threadIdx.x & 31;
   for (int which = 0; which < 2; ++which) {
     const TokenJoin j = a.joins[2 * (blockIdx.x / kJoinSplit) + which];

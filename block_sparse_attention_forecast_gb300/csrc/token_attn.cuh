@@ -5,9 +5,9 @@
 // (times the group's H query heads: at most 128 or 256 rows); an item attends nctx 64-token blocks of
 // the cache and the new tokens' blocks up to its own last token (causal), or all of them (tree), two
 // blocks (a key tile) at a time. Two ways to share the items out:
-//   whole items   position u of all items, entry by entry, the longest of an entry first, dealt out to the
-//                 CTAs in snake order (0 .. n-1, n-1 .. 0, ...): CTAs that run at one time attend the
-//                 same keys, and the last items are the short ones;
+//   whole items   position u of all items, entry by entry, the longest of an entry first: CTA c takes item c, and
+//                 then whatever item is next, from a counter. CTAs that run at one time attend the same
+//                 keys, and the last items are the short ones;
 //   key tiles     position u of all items' key tiles: each CTA takes an equal range of positions, whatever
 //                 items they belong to. An item cut by a range's border leaves partial results, which
 //                 token_attn_join_kernel joins.
@@ -118,7 +118,8 @@ struct Segments {
   u32 base, incl, sum; // 32 entries at a time: the weight before them, up to this lane's, of all
   Entry mine;
   int e0;
-  u32 pos, end, first, round;
+  u32 pos, end, first;
+  bool started;
 
   __device__ Segments(const TokenAttnArgs& args, int tokens_per_item, int ln, int cta)
       : a(args), tpi(tokens_per_item), lane(ln), c(cta) {}
@@ -182,7 +183,7 @@ struct Segments {
     base = 0;
     if (a.n_entries > 32) fetch();
     weigh();
-    round = 0;
+    started = false;
     pos = end = first = 0;
     if (split && c < n_ctas) {
       const Parts parts(total, n_ctas);
@@ -218,8 +219,12 @@ struct Segments {
   __device__ __forceinline__ bool next(Item& it) {
     u32 off;
     if (!split) {
-      const u32 u = round * n_ctas + ((round & 1) ? n_ctas - 1 - c : c);
-      ++round;
+      u32 u = c;
+      if (started) {
+        if (lane == 0) u = n_ctas + atomicAdd(a.queue, 1u);
+        u = __shfl_sync(0xffffffffu, u, 0);
+      }
+      started = true;
       if (u >= total) return false;
       const int l = seek(u, off);
       const Entry en = entry(l);
