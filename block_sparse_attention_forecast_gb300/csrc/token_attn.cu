@@ -30,10 +30,11 @@ using tok::Item;
 using tok::Segments;
 using tok::u64;
 
-constexpr int kThreads = 384;                              // three warpgroups
-// registers per thread: of 168 at launch, the softmax warps take what the first warpgroup gives
-constexpr int kRegsMain = 88, kRegsSoftmax = 208;
-static_assert(128 * kRegsMain + 256 * kRegsSoftmax <= kThreads * 168, "the registers of the launch");
+constexpr int kSoftmaxWarps = 16;
+constexpr int kThreads = 128 + 32 * kSoftmaxWarps;
+// registers per thread: of 96 at launch, the softmax warps take what the first warpgroup gives
+constexpr int kRegsMain = 64, kRegsSoftmax = 104;
+static_assert(128 * kRegsMain + 32 * kSoftmaxWarps * kRegsSoftmax <= kThreads * 96, "the registers of the launch");
 constexpr int kTileRows = 128;
 constexpr int kQTile = kTileRows * kRowBytes;              // 32 KiB: columns 0..63 of 128 rows, then 64..127
 constexpr int kStage = 2 * kBlockBytes;                    // 32 KiB: the same of 128 keys or values
@@ -46,7 +47,7 @@ constexpr float kScaleLog2 = 1.4426950408889634f * 0.08838834764831845f;   // lo
 
 template <bool kDup>
 constexpr int smem_bytes() {
-  return 1024 + kPage + (kDup ? kQTile + 2048 : 2 * kQTile) + kStages * kStage;
+  return kPage + (kDup ? kQTile + 2048 : 2 * kQTile) + kStages * kStage + 1024;
 }
 static_assert(smem_bytes<false>() <= 227 * 1024, "the token attention fits shared memory");
 
@@ -104,7 +105,7 @@ __device__ __forceinline__ void store32(void* dst, const uint32_t* w) {
 struct Work {
   int b, g, n, P, nctx, row0, tok0, nblk, k0, k1, slot, tiles;   // k0 == k1: no more
 };
-constexpr int kWorkRing = 1;   // an item is taken when the loads of the one before have been issued, not earlier
+constexpr int kWorkRing = 1;   // an item is taken when all warps have begun the one before, not earlier
 
 // The blocks of an item. Block s < nctx is a block of the cache, the others are blocks of the new tokens.
 struct Blocks {
@@ -149,6 +150,25 @@ __device__ __forceinline__ bool warp_wait(uint64_t* bar, uint32_t parity, int* e
   return ok;
 }
 
+// The two warps that share rows: a barrier of their own, and one that tells whether any of their threads says so.
+__device__ __forceinline__ void pair_sync(int id) {
+  __syncwarp();
+  asm volatile("bar.sync %0, 64;" ::"r"(id) : "memory");
+}
+__device__ __forceinline__ bool pair_any(int id, bool v) {
+  uint32_t r;
+  __syncwarp();
+  asm volatile(
+      "{\n\t.reg .pred p, q;\n\t"
+      "setp.ne.u32 p, %1, 0;\n\t"
+      "bar.red.or.pred q, %2, 64, p;\n\t"
+      "selp.u32 %0, 1, 0, q;\n\t}"
+      : "=r"(r)
+      : "r"((uint32_t)v), "r"(id)
+      : "memory");
+  return r != 0;
+}
+
 // 64-bit mask of the first n keys, 0 <= n <= 64
 __device__ __forceinline__ u64 first_bits(int n) { return n <= 0 ? 0ull : (n >= 64 ? ~0ull : (1ull << n) - 1ull); }
 
@@ -160,25 +180,26 @@ __global__ void __launch_bounds__(kThreads, 1) token_attn_kernel(const TokenAttn
                                                                 const __grid_constant__ CUtensorMap mvc,
                                                                 const __grid_constant__ CUtensorMap mkn,
                                                                 const __grid_constant__ CUtensorMap mvn) {
-  extern __shared__ uint8_t smem_raw[];
-  uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~static_cast<uintptr_t>(1023));
+  extern __shared__ __align__(1024) uint8_t smem[];
   uint64_t* q_full = reinterpret_cast<uint64_t*>(smem);
   uint64_t* q_empty = q_full + 1;
   uint64_t* drain = q_empty + 1;
   uint64_t* kv_full = drain + 1;                             // [stages]
   uint64_t* kv_empty = kv_full + kStages;                    // [stages]
   uint64_t* s_full = kv_empty + kStages;                     // [tile]
-  uint64_t* p_full = s_full + 2;                             // [tile][half]
-  uint64_t* o_full = p_full + 4;                             // [tile]
+  uint64_t* p_full = s_full + 2;                             // [tile]
+  uint64_t* o_full = p_full + 2;                             // [tile]
   uint64_t* w_full = o_full + 2;                             // [work ring]
   uint64_t* w_empty = w_full + kWorkRing;
   uint64_t* ml_full = w_empty + kWorkRing;                   // the two copies' maxima and sums (kDup)
   uint64_t* ml_empty = ml_full + 1;
   uint32_t* tmem_sh = reinterpret_cast<uint32_t*>(ml_empty + 1);
+  volatile uint32_t* fail_sh = tmem_sh + 1;                  // [row pairs]: a wait of one of the two warps ran out
   volatile Work* work = reinterpret_cast<volatile Work*>(smem + 512);
   uint8_t* qs = smem + kPage;
   uint8_t* ring = qs + (kDup ? kQTile : 2 * kQTile);
-  float* ml_sh = reinterpret_cast<float*>(ring + kStages * kStage);   // [tile][max, sum][128] (kDup)
+  float* row_sh = reinterpret_cast<float*>(ring + kStages * kStage);  // [tile][128]: between a row's two threads
+  float* ml_sh = row_sh + 256;                               // [tile][max, sum][128] (kDup)
 
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const int H = a.H, tp = a.tp, tpi = kDup ? tp : 2 * tp;
@@ -187,22 +208,22 @@ __global__ void __launch_bounds__(kThreads, 1) token_attn_kernel(const TokenAttn
     mbar_init(q_full, 1);
     mbar_init(q_empty, 1);
     mbar_init(drain, 1);
+    for (int i = 0; i < kSoftmaxWarps / 2; ++i) fail_sh[i] = 0;
     for (int i = 0; i < kStages; ++i) {
       mbar_init(&kv_full[i], 1);
       mbar_init(&kv_empty[i], 1);
     }
     for (int t = 0; t < 2; ++t) {
       mbar_init(&s_full[t], 1);
-      mbar_init(&p_full[2 * t], 4);
-      mbar_init(&p_full[2 * t + 1], 4);
+      mbar_init(&p_full[t], kSoftmaxWarps / 2);
       mbar_init(&o_full[t], 1);
     }
     for (int i = 0; i < kWorkRing; ++i) {
       mbar_init(&w_full[i], 1);
-      mbar_init(&w_empty[i], 10);                            // producer, issuer, eight softmax warps
+      mbar_init(&w_empty[i], 2 + kSoftmaxWarps);             // producer, issuer, softmax warps
     }
-    mbar_init(ml_full, 8);
-    mbar_init(ml_empty, 8);
+    mbar_init(ml_full, kSoftmaxWarps);
+    mbar_init(ml_empty, kSoftmaxWarps);
     fence_mbar_init();
   }
   if (warp == 1) {
@@ -244,7 +265,7 @@ __global__ void __launch_bounds__(kThreads, 1) token_attn_kernel(const TokenAttn
     it.slot = work[i].slot;
     it.tiles = work[i].tiles;
     __syncwarp();
-    if (lane == 0 && warp != 0) bar_arrive(&w_empty[i]);     // (the producer's comes behind its loads)
+    if (lane == 0) bar_arrive(&w_empty[i]);
     ++n_work;
     if (it.k0 == it.k1) return false;
     bl.load(a, it, lane);
@@ -361,7 +382,6 @@ __global__ void __launch_bounds__(kThreads, 1) token_attn_kernel(const TokenAttn
           if (ok && p + 2 < n) load(&mkc, &mkn, it.k0 + p + 2);
         }
       }
-      if (lane == 0) bar_arrive(&w_empty[(n_work - 1) % kWorkRing]);
     }
     // a wait ran out: no copy may still be under way when the CTA ends
     if (!ok && lane == 0)
@@ -404,15 +424,13 @@ __global__ void __launch_bounds__(kThreads, 1) token_attn_kernel(const TokenAttn
     auto issue_pv = [&](int t, unsigned at, bool first, bool two) {   // O_t += P_t V
       const u64 db = dv + at * (kStage >> 4);
       const uint32_t d = tm + 256 * t + 128, pa = tm + 256 * t;
+      ok = ok && warp_wait(&p_full[t], p_parity[t], a.err);
+      if (ok) {
+        tc05::fence_after();
 #pragma unroll
-      for (int h = 0; h < 2; ++h) {
-        ok = ok && warp_wait(&p_full[2 * t + h], p_parity[t], a.err);
-        if (ok && (h == 0 || two)) {
-          tc05::fence_after();
-#pragma unroll
-          for (int kk = 4 * h; kk < 4 * h + 4; ++kk)
-            tc05::mma_bf16_ts_by(leader, d, pa + 8 * kk, db + kk * 128, id_pv, (kk > 0 || !first) ? 1u : 0u);
-        }
+        for (int kk = 0; kk < 8; ++kk)                       // P of the second half lies 64 columns behind the first's
+          if (kk < 4 || two)
+            tc05::mma_bf16_ts_by(leader, d, pa + 8 * kk + (kk < 4 ? 0 : 32), db + kk * 128, id_pv, (kk > 0 || !first) ? 1u : 0u);
       }
       p_parity[t] ^= 1;
     };
@@ -512,21 +530,24 @@ __global__ void __launch_bounds__(kThreads, 1) token_attn_kernel(const TokenAttn
     }
     }
     // every tensor-memory access of this CTA is done before the allocating warp frees it
-    asm volatile("bar.sync 2, %0;" ::"n"(kThreads) : "memory");
+    asm volatile("bar.sync 15, %0;" ::"n"(kThreads) : "memory");
     if (warp == 1) {
       tc05::fence_after();
       tc05::dealloc(tmem, kCols);
     }
   } else {
-    // ------------------------------------------------------------ softmax, one row per thread
+    // ------------------------------------------------------------ softmax, two threads per row
     asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kRegsSoftmax));
-    const int t = (warp - 4) >> 2;
+    const int t = ((warp - 4) >> 2) & 1, h = (warp - 4) >> 3;   // tile, half of the key tile
     const int quarter = warp & 3;                            // tensor-memory lanes 32q .. 32q+31
     const int r = quarter * 32 + lane;
     const int rt = a.by_H.div(r);                                 // the row's token in its tile
     const uint32_t lane_off = (uint32_t)(quarter * 32) << 16;
     const uint32_t t_s = tmem + 256 * t + lane_off, t_o = t_s + 128;
+    const int pair = 1 + 4 * t + quarter;                    // named barrier of the rows' two warps
+    float* other = row_sh + 128 * t + r;
     const u64 scale2 = pack2(kScaleLog2, kScaleLog2);
+    bool met = false;                                        // both warps of the rows know that a wait ran out
     unsigned n_s = 0, n_seg = 0, n_o[2] = {0, 0};
     int tree_b = -1;
     u64 anc0 = 0, anc1 = 0;                                  // tree: this row's ancestors and itself
@@ -569,115 +590,123 @@ __global__ void __launch_bounds__(kThreads, 1) token_attn_kernel(const TokenAttn
       float m_used = -INFINITY, l = 0.f;
       bool any = false;                                      // this tile has had a step
       for (int p = kDup ? t : 0; p < n; p += kDup ? 2 : 1) {
-        const int blk = 2 * (it.k0 + p);
-        const bool two = blk + 1 < it.nblk;
-        // the keys of each block that this row attends
-        u64 see[2] = {~0ull, two ? ~0ull : 0ull};
-        bool masked = false;                                 // warp-uniform
-#pragma unroll
-        for (int h = 0; h < 2; ++h) {
-          if (it.k0 + p < whole || (h == 1 && !two)) break;
-          const int sb = blk + h;
-          if (sb >= it.nctx) {
-            const int u0 = (sb - it.nctx) * kBlock;
-            if (a.parent) {
-              see[h] = u0 == 0 ? anc0 : anc1;
-              masked = true;
-            } else if (u0 + kBlock - 1 > tile_tok) {
-              see[h] = first_bits(tok + 1 - u0);
-              masked = true;
-            }
-          } else if (!bl.full(it, sb)) {
-            see[h] = first_bits(bl.rows(it, sb));
-            masked = true;
-          }
-        }
+        const int blk = 2 * (it.k0 + p) + h;
+        const bool there = blk < it.nblk;                    // an odd number of blocks: the last tile has one
+        u64 see = ~0ull;                                     // the keys of the block that this row attends
+        if (it.k0 + p >= whole && there)
+          see = blk < it.nctx ? first_bits(bl.rows(it, blk))
+                              : a.parent ? (blk == it.nctx ? anc0 : anc1) : first_bits(tok + 1 - (blk - it.nctx) * kBlock);
+        const bool masked = __any_sync(0xffffffffu, see != ~0ull);
         ok = warp_wait(&s_full[t], n_s & 1, a.err);
         ++n_s;
-        if (!ok) break;
-        tc05::fence_after();
-        float x[128];
+        // 32 keys of S, -inf where the row does not attend the key
+        float x[32];
+        auto load = [&](int c) {
+          tc05::ld32(t_s + 64 * h + 32 * c, x);
+          tc05::wait_ld();
+          if (masked) {
+            const uint32_t bits = (uint32_t)(see >> (32 * c));
 #pragma unroll
-        for (int i = 0; i < 4; ++i) tc05::ld32(t_s + 32 * i, *reinterpret_cast<float(*)[32]>(x + 32 * i));
-        tc05::wait_ld();
-        if (masked || !two) {
+            for (int e = 0; e < 32; ++e) x[e] = (bits >> e) & 1u ? x[e] : -INFINITY;
+          }
+        };
+        float mb = -INFINITY;
+        if (ok && there) {
+          tc05::fence_after();
+#pragma unroll 1
+          for (int c = 0; c < 2; ++c) {
+            load(c);
+            float m4[4];
 #pragma unroll
-          for (int h = 0; h < 2; ++h)
+            for (int k = 0; k < 4; ++k) m4[k] = max3(x[k], x[k + 4], x[k + 8]);
 #pragma unroll
-            for (int w = 0; w < 2; ++w) {
-              const uint32_t bits = (uint32_t)(see[h] >> (32 * w));
+            for (int e = 12; e < 28; e += 8)
 #pragma unroll
-              for (int e = 0; e < 32; ++e) {
-                float& v = x[64 * h + 32 * w + e];
-                v = (bits >> e) & 1u ? v : -INFINITY;
-              }
-            }
+              for (int k = 0; k < 4; ++k) m4[k] = max3(m4[k], x[e + k], x[e + 4 + k]);
+#pragma unroll
+            for (int k = 0; k < 4; ++k) m4[k] = fmaxf(m4[k], x[28 + k]);
+            mb = max3(mb, fmaxf(m4[0], m4[1]), fmaxf(m4[2], m4[3]));
+          }
+          mb *= kScaleLog2;
         }
-        float m4[4];
-#pragma unroll
-        for (int e = 0; e < 4; ++e) m4[e] = max3(x[e], x[e + 4], x[e + 8]);
-#pragma unroll
-        for (int e = 12; e < 124; e += 8)
-#pragma unroll
-          for (int k = 0; k < 4; ++k) m4[k] = max3(m4[k], x[e + k], x[e + 4 + k]);
-#pragma unroll
-        for (int k = 0; k < 4; ++k) m4[k] = fmaxf(m4[k], x[124 + k]);
-        const float mb = fmaxf(fmaxf(m4[0], m4[1]), fmaxf(m4[2], m4[3])) * kScaleLog2;
-        const bool grow = mb > m_used + kGrow;               // also the first key this row sees
-        if (__any_sync(0xffffffffu, grow)) {
-          const float mn = grow ? mb : m_used;
-          const float alpha = grow ? fast_exp2(m_used - mn) : 1.f;
+        // does a maximum move (also at the first key a row sees)?
+        if (!ok) fail_sh[pair - 1] = 1;
+        if (pair_any(pair, mb > m_used + kGrow || !ok)) {
+          if (fail_sh[pair - 1]) {                           // in one of the two: both leave
+            ok = false;
+            met = true;
+            break;
+          }
+          if (h == 1) *other = mb;
+          pair_sync(pair);
+          if (h == 0) {
+            mb = fmaxf(mb, *other);
+            *other = mb > m_used + kGrow ? mb : m_used;
+          }
+          pair_sync(pair);
+          const float mn = *other;
+          const float alpha = mn > m_used ? fast_exp2(m_used - mn) : 1.f;
           if (any) {                                         // S is there, so the O before it is
-#pragma unroll
-            for (int i = 0; i < 4; ++i) {
-              float o[32];
-              tc05::ld32(t_o + 32 * i, o);
+#pragma unroll 1
+            for (int i = 0; i < 2; ++i) {
+              tc05::ld32(t_o + 64 * h + 32 * i, x);
               tc05::wait_ld();
 #pragma unroll
-              for (int e = 0; e < 32; ++e) o[e] *= alpha;
-              tc05::st32(t_o + 32 * i, o);
+              for (int e = 0; e < 32; ++e) x[e] *= alpha;
+              tc05::st32(t_o + 64 * h + 32 * i, x);
             }
           }
           l *= alpha;
           m_used = mn;
         }
         any = true;
-        const float neg = m_used == -INFINITY ? 0.f : -m_used;
-        const u64 neg2 = pack2(neg, neg);
-        u64 sum2[2] = {0ull, 0ull};
+        if (there) {
+          const float neg = m_used == -INFINITY ? 0.f : -m_used;
+          const u64 neg2 = pack2(neg, neg);
+          u64 sum2[2] = {0ull, 0ull};
+#pragma unroll 1
+          for (int c = 0; c < 2; ++c) {
+            // P lies over S of this half's first 32 keys, which are read by then
+            load(c);
+            uint32_t pk[16];
 #pragma unroll
-        for (int h = 0; h < 2; ++h) {
-          if (h == 0 || two) {
-            float pk[32];
-#pragma unroll
-            for (int e = 0; e < 32; ++e) {
+            for (int e = 0; e < 16; ++e) {
               float p0, p1;
-              unpack2(fma2(pack2(x[64 * h + 2 * e], x[64 * h + 2 * e + 1]), scale2, neg2), p0, p1);
+              unpack2(fma2(pack2(x[2 * e], x[2 * e + 1]), scale2, neg2), p0, p1);
               p0 = fast_exp2(p0);
               p1 = fast_exp2(p1);
               sum2[e & 1] = add2(sum2[e & 1], pack2(p0, p1));
-              pk[e] = __uint_as_float(pack_bf16(p0, p1));
+              pk[e] = pack_bf16(p0, p1);
             }
-            tc05::st32(t_s + 32 * h, pk);
-            tc05::wait_st();
+            tc05::st16(t_s + 64 * h + 16 * c, pk);
           }
-          tc05::fence_before();
-          __syncwarp();
-          if (lane == 0) bar_arrive(&p_full[2 * t + h]);
+          float s0, s1;
+          unpack2(add2(sum2[0], sum2[1]), s0, s1);
+          l += s0 + s1;
         }
-        float s0, s1;
-        unpack2(add2(sum2[0], sum2[1]), s0, s1);
-        l += s0 + s1;
+        tc05::wait_st();
+        tc05::fence_before();
+        __syncwarp();
+        if (lane == 0) bar_arrive(&p_full[t]);
       }
       if (!kDup && !ok) break;
       // ---- the segment's end: O of this tile (kDup: of both copies) is complete
       float w0 = 1.f, w1 = 0.f;
+      if (ok) {                                              // the row's sum (both warps of the rows are here, or neither)
+        if (h == 1) *other = l;
+        pair_sync(pair);
+        if (h == 0) *other = l += *other;
+        pair_sync(pair);
+        l = *other;
+      }
       if (!kDup) {
         ok = warp_wait(&o_full[t], n_o[t] & 1, a.err);
         ++n_o[t];
       } else {
-        ml_sh[256 * t + r] = m_used;
-        ml_sh[256 * t + 128 + r] = l;
+        if (h == 0) {
+          ml_sh[256 * t + r] = m_used;
+          ml_sh[256 * t + 128 + r] = l;
+        }
 #pragma unroll
         for (int u = 0; u < 2; ++u)
           if (u < n) {
@@ -702,7 +731,8 @@ __global__ void __launch_bounds__(kThreads, 1) token_attn_kernel(const TokenAttn
         __nv_bfloat16* dst = a.out + ((row * a.G + it.g) * H + (r - rt * H)) * kHeadDim;
         const int prow = (kDup ? 0 : t * kTileRows) + r;
         float* part = a.part + (size_t)max(it.slot, 0) * kTokenPartFloats;
-        const int c0 = kDup ? 2 * t : 0, c1 = kDup ? 2 * t + 2 : 4;
+        // a warp's columns: half of its tile's, or (kDup) a quarter of the joined tile's
+        const int c0 = kDup ? 2 * h + t : 2 * h, c1 = kDup ? c0 + 1 : c0 + 2;
 #pragma unroll 1
         for (int c = c0; c < c1; ++c) {
           float o[32];
@@ -737,7 +767,7 @@ __global__ void __launch_bounds__(kThreads, 1) token_attn_kernel(const TokenAttn
               store32(part + prow * kHeadDim + 32 * c + 8 * e, reinterpret_cast<const uint32_t*>(o + 8 * e));
           }
         }
-        if (live && it.slot >= 0 && (!kDup || t == 0)) {
+        if (live && it.slot >= 0 && h == 0 && (!kDup || t == 0)) {
           float* ml = part + kTokenItemRows * kHeadDim;
           ml[prow] = m_used;
           ml[kTokenItemRows + prow] = l;
@@ -751,8 +781,13 @@ __global__ void __launch_bounds__(kThreads, 1) token_attn_kernel(const TokenAttn
         ++n_seg;
       }
     }
+    // a warp whose wait ran out outside of a step leaves by way of the barrier that the other one is at, or comes to
+    if (!met) {
+      if (!ok) fail_sh[pair - 1] = 1;
+      pair_any(pair, !ok);
+    }
     tc05::fence_before();
-    asm volatile("bar.sync 2, %0;" ::"n"(kThreads) : "memory");
+    asm volatile("bar.sync 15, %0;" ::"n"(kThreads) : "memory");
   }
 }
 
