@@ -110,7 +110,6 @@ constexpr int kWorkRing = 1;   // an item is taken when all warps have begun the
 // The blocks of an item. Block s < nctx is a block of the cache, the others are blocks of the new tokens.
 struct Blocks {
   int j0, j1;        // lane l: the selection's entries l and 32 + l (selected blocks)
-  u64 part;          // selected blocks with fewer than 64 tokens
   bool sel;
   __device__ __forceinline__ int rows_of(const Work& it, int j) const {
     return j < 0 || j > it.P / kBlock ? 0 : min(kBlock, it.P - j * kBlock);
@@ -121,8 +120,6 @@ struct Blocks {
       const int32_t* p = a.idx + (size_t)(it.b * a.G + it.g) * a.kslots;
       j0 = lane < it.nctx ? p[lane] : 0;
       j1 = lane + 32 < it.nctx ? p[lane + 32] : 0;
-      part = __ballot_sync(0xffffffffu, rows_of(it, j0) < kBlock) |
-             (u64)__ballot_sync(0xffffffffu, rows_of(it, j1) < kBlock) << 32;
     }
   }
   // the cache's block number (every lane calls); -1: outside the sequence
@@ -131,13 +128,9 @@ struct Blocks {
     const int j = __shfl_sync(0xffffffffu, s < 32 ? j0 : j1, s & 31);
     return j >= 0 && j <= it.P / kBlock ? j : -1;
   }
-  // rows of block s that hold tokens: 0 .. 64 (every lane calls), and whether it is 64
+  // rows of block s that hold tokens: 0 .. 64 (every lane calls)
   __device__ __forceinline__ int rows(const Work& it, int s) const {
     return s >= it.nctx ? min(kBlock, it.n - (s - it.nctx) * kBlock) : rows_of(it, block(it, s));
-  }
-  __device__ __forceinline__ bool full(const Work& it, int s) const {
-    if (s >= it.nctx) return (s - it.nctx + 1) * kBlock <= it.n;
-    return sel ? !(part >> s & 1) : (s + 1) * kBlock <= it.P;
   }
 };
 
@@ -399,7 +392,7 @@ __global__ void __launch_bounds__(kThreads, 1) token_attn_kernel(const TokenAttn
     const u64 dk = tc05::smem_desc(ring_at, 16, 1024);
     const u64 dv = tc05::smem_desc(ring_at, kHalfCols, 1024);
     const uint32_t leader = tc05::elect_leader();
-    unsigned stage = 0, full_parity = 0, q_parity = 0, p_parity[2] = {0, 0};
+    unsigned stage = 0, full_parity = 0, q_parity = 0, p_parity = 0;   // (p_parity: bit t)
     // the next load of the ring, once it is there
     auto take = [&]() {
       const unsigned at = stage;
@@ -411,28 +404,43 @@ __global__ void __launch_bounds__(kThreads, 1) token_attn_kernel(const TokenAttn
       tc05::fence_after();
       return at;
     };
+    // (One tile's two copies wait for memory, and smaller code serves them better than a fast issue: half of the
+    // MMAs in the code, twice around.)
+    constexpr int kAtOnce = kDup ? 4 : 8;
     auto issue_qk = [&](int t, unsigned at) {                // S_t = Q_t K^T
-      const u64 da = dq + (kDup ? 0 : t * (kQTile >> 4)), db = dk + at * (kStage >> 4);
+      u64 da = dq + (kDup ? 0 : t * (kQTile >> 4)), db = dk + at * (kStage >> 4);
       const uint32_t d = tm + 256 * t;
+#pragma unroll 1
+      for (int k0 = 0; k0 < 8; k0 += kAtOnce) {
 #pragma unroll
-      for (int kk = 0; kk < 8; ++kk) {
-        const uint32_t off = (kk >> 2) * (kHalfCols >> 4) + (kk & 3) * 2;
-        tc05::mma_bf16_ss_by(leader, d, da + off, db + off, id_qk, kk > 0 ? 1u : 0u);
+        for (int kk = 0; kk < kAtOnce; ++kk) {
+          const uint32_t off = (kk >> 2) * (kHalfCols >> 4) + (kk & 3) * 2;
+          tc05::mma_bf16_ss_by(leader, d, da + off, db + off, id_qk, kk > 0 ? 1u : k0);
+        }
+        da += kHalfCols >> 4;
+        db += kHalfCols >> 4;
       }
       tc05::commit_by(leader, &s_full[t]);
     };
     auto issue_pv = [&](int t, unsigned at, bool first, bool two) {   // O_t += P_t V
-      const u64 db = dv + at * (kStage >> 4);
-      const uint32_t d = tm + 256 * t + 128, pa = tm + 256 * t;
-      ok = ok && warp_wait(&p_full[t], p_parity[t], a.err);
+      u64 db = dv + at * (kStage >> 4);
+      const uint32_t d = tm + 256 * t + 128;
+      uint32_t pa = tm + 256 * t;
+      ok = ok && warp_wait(&p_full[t], (p_parity >> t) & 1, a.err);
       if (ok) {
         tc05::fence_after();
+#pragma unroll 1
+        for (int k0 = 0; k0 < (two ? 8 : 4); k0 += kAtOnce) {
 #pragma unroll
-        for (int kk = 0; kk < 8; ++kk)                       // P of the second half lies 64 columns behind the first's
-          if (kk < 4 || two)
-            tc05::mma_bf16_ts_by(leader, d, pa + 8 * kk + (kk < 4 ? 0 : 32), db + kk * 128, id_pv, (kk > 0 || !first) ? 1u : 0u);
+          for (int kk = 0; kk < kAtOnce; ++kk)               // P of the second half lies 64 columns behind the first's
+            if (kk < 4 || two)
+              tc05::mma_bf16_ts_by(leader, d, pa + 8 * kk + (kk < 4 ? 0 : 32), db + kk * 128, id_pv,
+                                   kk > 0 || k0 > 0 || !first ? 1u : 0u);
+          pa += 64;
+          db += 512;
+        }
       }
-      p_parity[t] ^= 1;
+      p_parity ^= 1u << t;
     };
     // value rows without a token, of a key tile whose blocks hold rows0 and rows1 tokens: zeroed
     auto clear_rows = [&](unsigned at, int rows0, int rows1) {
@@ -502,24 +510,19 @@ __global__ void __launch_bounds__(kThreads, 1) token_attn_kernel(const TokenAttn
           if (more) tc05::commit_by(leader, &kv_empty[ks]);
           if (p + 2 == n) tc05::commit_by(leader, q_empty);
         } else {
-          auto step = [&](int t) {
-            issue_pv(t, vs, p < 2, two);
-            if (!ok) return;
-            tc05::commit_by(leader, &kv_empty[vs]);
-            if (p + 2 < n) {
-              ks = take();
-              if (!ok) return;
-              issue_qk(t, ks);
-              tc05::commit_by(leader, &kv_empty[ks]);
-              if (p + 3 == n) tc05::commit_by(leader, q_empty);
-            } else {
-              tc05::commit_by(leader, &o_full[t]);
-            }
-          };
-          if (p & 1)
-            step(1);
-          else
-            step(0);
+          const int t = p & 1;
+          issue_pv(t, vs, p < 2, two);
+          if (!ok) break;
+          tc05::commit_by(leader, &kv_empty[vs]);
+          if (p + 2 < n) {
+            ks = take();
+            if (!ok) break;
+            issue_qk(t, ks);
+            tc05::commit_by(leader, &kv_empty[ks]);
+            if (p + 3 == n) tc05::commit_by(leader, q_empty);
+          } else {
+            tc05::commit_by(leader, &o_full[t]);
+          }
         }
       }
     }
@@ -613,7 +616,7 @@ __global__ void __launch_bounds__(kThreads, 1) token_attn_kernel(const TokenAttn
         float mb = -INFINITY;
         if (ok && there) {
           tc05::fence_after();
-#pragma unroll 1
+#pragma unroll(kDup ? 1 : 2)
           for (int c = 0; c < 2; ++c) {
             load(c);
             float m4[4];
