@@ -2,16 +2,17 @@
 // the compressed keys of the windows that they complete (the exact mean of 32 keys, rounded once to bf16).
 //
 // A CTA takes the new tokens of one 64-token block of one sequence's cache, for one KV group: their keys
-// go through shared memory together with the up to 31 keys before them that their windows reach back to
-// (from the cache, or from the new rows), values straight through; then 64 threads per window, two
-// channels each, form the four windows that end in the block.
+// go through shared memory together with the 16 keys before the block and the block's cached ones that their
+// windows reach back to (from the cache, or from the new rows), values straight through; then 64 threads per
+// window, two channels each, form the four windows that end in the block. Every load of a thread is under way
+// before its first store, since a CTA's time is otherwise that of one load behind the other.
 #include "append_body.cuh"
 
 namespace sparda {
 
 namespace {
 constexpr int kThreads = 256;
-constexpr int kHalo = kWinKernel - 1;
+constexpr int kHalo = kWinKernel - kWinStride;               // windows begin at multiples of 16
 constexpr int kCommitBlocks = kTokenMaxNodes / kBlock + 1;   // cache blocks that a path reaches into, at most
 
 // What sequence b appends: n rows behind its S cached tokens; false: nothing may be written.
@@ -103,20 +104,31 @@ __global__ void __launch_bounds__(kThreads) token_append_kernel(const TokenAppen
     const int i = pos - S;
     return (size_t)(row0 + (a.cu ? i : path_sh[i])) * a.kv_stride + g * kHeadDim;
   };
-  const int from = max(0, lo - kHalo);
-  for (int i = tid; i < (hi - from) * 16; i += kThreads) {
-    const int pos = from + (i >> 4), c = i & 15;
-    if (pos < S) {
-      *reinterpret_cast<uint4*>(&ks[pos - from][4 * c]) = *reinterpret_cast<const uint4*>(kc + (size_t)pos * kHeadDim + 8 * c);
-    } else {
+  // thread: 16 bytes of the rows r, r + 16, ..; the first 16 rows are those before the block
+  constexpr int kRows = kThreads / 16, kParts = (kHalo + kBlock) / kRows;
+  static_assert(kHalo == kRows && kBlock % kRows == 0, "the rows before the block are the first part");
+  const int c = tid & 15, r = tid >> 4;
+  uint4 x[kParts], y[kParts];
+#pragma unroll
+  for (int j = 0; j < kParts; ++j) {
+    const int pos = base - kHalo + r + kRows * j;
+    x[j] = make_uint4(0u, 0u, 0u, 0u);
+    if (pos >= S && pos < hi) {
       const size_t src = new_row(pos) + 8 * c;
-      const uint4 x = *reinterpret_cast<const uint4*>(a.k_new + src);
-      *reinterpret_cast<uint4*>(&ks[pos - from][4 * c]) = x;
-      if (pos >= lo) {
-        const size_t dst = (bg * a.max_ctx + pos) * kHeadDim + 8 * c;
-        *reinterpret_cast<uint4*>(a.k + dst) = x;
-        *reinterpret_cast<uint4*>(a.v + dst) = *reinterpret_cast<const uint4*>(a.v_new + src);
-      }
+      x[j] = *reinterpret_cast<const uint4*>(a.k_new + src);
+      if (j > 0) y[j] = *reinterpret_cast<const uint4*>(a.v_new + src);
+    } else if (pos >= 0 && pos < S) {
+      x[j] = *reinterpret_cast<const uint4*>(kc + (size_t)pos * kHeadDim + 8 * c);
+    }
+  }
+#pragma unroll
+  for (int j = 0; j < kParts; ++j) {
+    const int pos = base - kHalo + r + kRows * j;
+    *reinterpret_cast<uint4*>(&ks[r + kRows * j][4 * c]) = x[j];
+    if (j > 0 && pos >= S && pos < hi) {
+      const size_t dst = (bg * a.max_ctx + pos) * kHeadDim + 8 * c;
+      *reinterpret_cast<uint4*>(a.k + dst) = x[j];
+      *reinterpret_cast<uint4*>(a.v + dst) = y[j];
     }
   }
   __syncthreads();
@@ -125,7 +137,7 @@ __global__ void __launch_bounds__(kThreads) token_append_kernel(const TokenAppen
   if (w >= 0 && end > lo && end <= hi) {
     uint32_t xs[kWinKernel];
 #pragma unroll
-    for (int u = 0; u < kWinKernel; ++u) xs[u] = ks[end - kWinKernel + u - from][pair];
+    for (int u = 0; u < kWinKernel; ++u) xs[u] = ks[end - kWinKernel + u - (base - kHalo)][pair];
     reinterpret_cast<uint32_t*>(a.ck + (bg * a.W_cap + w) * kHeadDim)[pair] = window_mean(xs);
   }
 }
