@@ -732,35 +732,34 @@ def sparda_kv4_evict_blocks(shape, layer, mass, seq_len, batch, keep, recent, ke
 
 
 # ------------------------------------------------------------------ packed prompts and drafted tokens
-def _rows(what, t, lead, heads, d, dev):
-    """(address, elements from one row to the next) of new tokens' queries, keys or values: a bf16 tensor
-    [*lead, heads, d] on CUDA device `dev` whose rows hold their heads densely and lie evenly spaced. A leading
-    length of -1 is any."""
-    ok = (t.dtype is torch.bfloat16 and t.get_device() == dev and t.dim() == len(lead) + 2 and
-          all(a < 0 or a == b for a, b in zip(lead + (heads, d), t.shape)))
-    if ok:
-        st, n = t.stride(), t.shape
-        ok = st[-1] == 1 and (heads == 1 or st[-2] == d)
-        row = heads * d                              # the rows' spacing, where there is more than one
-        if len(lead) == 1:
-            row = st[0] if n[0] > 1 else row
-        else:
-            row = st[1] if n[1] > 1 else (st[0] if n[0] > 1 else row)
-            ok = ok and (n[0] == 1 or st[0] == n[1] * row)
-    if not ok:
-        raise ValueError("%s: a torch.bfloat16 tensor [%s] on cuda:%d with dense heads and evenly spaced rows is wanted, "
-                         "got %s %s on %s, strides %s" % (
-                             what, ", ".join("any" if x < 0 else str(x) for x in lead + (heads, d)), dev, t.dtype,
-                             tuple(t.shape), t.device, tuple(t.stride())))
-    return t.data_ptr(), row
+def _rows(what, t, dims, heads, d, dev):
+    """(address, elements from one row to the next) of new tokens' queries, keys or values: a bf16 tensor of `dims`
+    leading dimensions (1: rows, 2: sequences of rows) and [heads, d] on CUDA device `dev`, whose rows hold their
+    heads densely and lie evenly spaced."""
+    n, st = t.shape, t.stride()
+    if (t.dtype is torch.bfloat16 and t.get_device() == dev and len(n) == dims + 2 and n[-1] == d and n[-2] == heads and
+            st[-1] == 1 and (st[-2] == d or heads == 1)):
+        row = st[dims - 1] if n[dims - 1] > 1 else (st[0] if dims == 2 and n[0] > 1 else heads * d)
+        if dims == 1 or n[0] == 1 or st[0] == n[1] * row:
+            return t.data_ptr(), row
+    raise ValueError("%s: a torch.bfloat16 tensor of %d dimensions ending in [%d, %d] on cuda:%d with dense heads and "
+                     "evenly spaced rows is wanted, got %s %s on %s, strides %s" % (
+                         what, dims + 2, heads, d, dev, t.dtype, tuple(n), t.device, tuple(st)))
 
 
-def _kv_rows(k, v, lead, G, d, dev):
-    pk, sk = _rows("keys", k, lead, G, d, dev)
-    pv, sv = _rows("values", v, tuple(k.shape[: len(lead)]), G, d, dev)
+def _kv_rows(k, v, dims, G, d, dev):
+    pk, sk = _rows("keys", k, dims, G, d, dev)
+    if v.shape != k.shape:
+        raise ValueError("keys and values need the same shape, got %s and %s" % (tuple(k.shape), tuple(v.shape)))
+    pv, sv = _rows("values", v, dims, G, d, dev)
     if sk != sv:
         raise ValueError("keys and values need the same spacing of rows, got %d and %d elements" % (sk, sv))
     return pk, pv, sk
+
+
+def _same_rows(q, k, dims):
+    if q.shape[:dims] != k.shape[:dims]:
+        raise ValueError("queries and keys need the same rows, got %s and %s" % (tuple(q.shape), tuple(k.shape)))
 
 
 def _int_ptr(what, t, n, dev):
@@ -777,8 +776,9 @@ def sparda_prompt_attn(shape, q, k, v, cu_len, batch, out, ws, past=None, past_l
         dev, lc = _cache_device(q), None
     B, G, H, d = int(batch), shape.n_groups, shape.heads_per_group, shape.head_dim
     n = q.shape[0]
-    pq, sq = _rows("q", q, (-1,), G * H, d, dev)
-    pk, pv, skv = _kv_rows(k, v, (n,), G, d, dev)
+    pq, sq = _rows("q", q, 1, G * H, d, dev)
+    pk, pv, skv = _kv_rows(k, v, 1, G, d, dev)
+    _same_rows(q, k, 1)
     _check("sparda_prompt_attn", lib.sparda_prompt_attn(
         shape.ref(), lc, _int_ptr("past_len", past_len, B, dev), pq, sq, pk, pv, skv,
         _checked("cu_len", cu_len, torch.int32, B + 1, dev), n, B,
@@ -791,7 +791,7 @@ def sparda_prompt_append(shape, layer, k, v, cu_len, seq_len, batch, new_len=Non
     holds (None: behind none), with the compressed keys they complete; new_len (int32 [B]) receives the lengths."""
     dev, lc = _layer_ptrs(shape, layer)
     B = int(batch)
-    pk, pv, skv = _kv_rows(k, v, (-1,), shape.n_groups, shape.head_dim, dev)
+    pk, pv, skv = _kv_rows(k, v, 1, shape.n_groups, shape.head_dim, dev)
     _check("sparda_prompt_append", lib.sparda_prompt_append(
         shape.ref(), lc, pk, pv, skv, _checked("cu_len", cu_len, torch.int32, B + 1, dev), k.shape[0],
         _int_ptr("seq_len", seq_len, B, dev), B, _int_ptr("new_len", new_len, B, dev), _stream_handle(stream, dev)))
@@ -804,9 +804,12 @@ def sparda_tree_attn(shape, layer, q, k_new, v_new, parent, seq_len, batch, out,
     them or those of the blocks idx / cnt. n_nodes: int32 [B], the nodes each sequence uses. ws: WS_TREE."""
     dev, lc = _layer_ptrs(shape, layer)
     B, G, H, d = int(batch), shape.n_groups, shape.heads_per_group, shape.head_dim
-    pq, sq = _rows("q", q, (B, -1), G * H, d, dev)
+    pq, sq = _rows("q", q, 2, G * H, d, dev)
     N = q.shape[1]
-    pk, pv, skv = _kv_rows(k_new, v_new, (B, N), G, d, dev)
+    pk, pv, skv = _kv_rows(k_new, v_new, 2, G, d, dev)
+    _same_rows(q, k_new, 2)
+    if q.shape[0] < B:
+        raise ValueError("q holds %d sequences, %d are wanted" % (q.shape[0], B))
     pi, pc = _selection_ptrs(shape, idx, cnt, B * G, dev)
     _check("sparda_tree_attn", lib.sparda_tree_attn(
         shape.ref(), lc, pq, sq, pk, pv, skv, _int_ptr("parent", parent, B * N, dev), _int_ptr("n_nodes", n_nodes, B, dev),
@@ -821,8 +824,10 @@ def sparda_tree_commit(shape, layer, k_new, v_new, path, n_path, seq_len, batch,
     [B]) receives the lengths."""
     dev, lc = _layer_ptrs(shape, layer)
     B = int(batch)
-    pk, pv, skv = _kv_rows(k_new, v_new, (B, -1), shape.n_groups, shape.head_dim, dev)
+    pk, pv, skv = _kv_rows(k_new, v_new, 2, shape.n_groups, shape.head_dim, dev)
     N = k_new.shape[1]
+    if k_new.shape[0] < B:
+        raise ValueError("k_new holds %d sequences, %d are wanted" % (k_new.shape[0], B))
     _check("sparda_tree_commit", lib.sparda_tree_commit(
         shape.ref(), lc, pk, pv, skv, N, _checked("path", path, torch.int32, B * N, dev),
         _checked("n_path", n_path, torch.int32, B, dev), _checked("seq_len", seq_len, torch.int32, B, dev), B,
