@@ -180,8 +180,8 @@ __global__ void __launch_bounds__(kThreads, 1) token_attn_kernel(const TokenAttn
   uint64_t* kv_full = drain + 1;                             // [stages]
   uint64_t* kv_empty = kv_full + kStages;                    // [stages]
   uint64_t* s_full = kv_empty + kStages;                     // [tile]
-  uint64_t* p_full = s_full + 2;                             // [tile]
-  uint64_t* o_full = p_full + 2;                             // [tile]
+  uint64_t* p_full = s_full + 2;                             // [tile][32 keys of each half]
+  uint64_t* o_full = p_full + 4;                             // [tile]
   uint64_t* w_full = o_full + 2;                             // [work ring]
   uint64_t* w_empty = w_full + kWorkRing;
   uint64_t* ml_full = w_empty + kWorkRing;                   // the two copies' maxima and sums (kDup)
@@ -208,7 +208,8 @@ __global__ void __launch_bounds__(kThreads, 1) token_attn_kernel(const TokenAttn
     }
     for (int t = 0; t < 2; ++t) {
       mbar_init(&s_full[t], 1);
-      mbar_init(&p_full[t], kSoftmaxWarps / 2);
+      mbar_init(&p_full[2 * t], kSoftmaxWarps / 2);
+      mbar_init(&p_full[2 * t + 1], kSoftmaxWarps / 2);
       mbar_init(&o_full[t], 1);
     }
     for (int i = 0; i < kWorkRing; ++i) {
@@ -404,7 +405,7 @@ __global__ void __launch_bounds__(kThreads, 1) token_attn_kernel(const TokenAttn
       tc05::fence_after();
       return at;
     };
-    // (One tile's two copies wait for memory, and smaller code serves them better than a fast issue: half of the
+    // (One tile's two copies wait for memory, and smaller code serves them better than a fast issue: half of S's
     // MMAs in the code, twice around.)
     constexpr int kAtOnce = kDup ? 4 : 8;
     auto issue_qk = [&](int t, unsigned at) {                // S_t = Q_t K^T
@@ -426,18 +427,18 @@ __global__ void __launch_bounds__(kThreads, 1) token_attn_kernel(const TokenAttn
       u64 db = dv + at * (kStage >> 4);
       const uint32_t d = tm + 256 * t + 128;
       uint32_t pa = tm + 256 * t;
-      ok = ok && warp_wait(&p_full[t], (p_parity >> t) & 1, a.err);
-      if (ok) {
-        tc05::fence_after();
-#pragma unroll 1
-        for (int k0 = 0; k0 < (two ? 8 : 4); k0 += kAtOnce) {
+      // 32 keys of each half at a time: the products of the first run beside the softmax of the others
 #pragma unroll
-          for (int kk = 0; kk < kAtOnce; ++kk)               // P of the second half lies 64 columns behind the first's
-            if (kk < 4 || two)
-              tc05::mma_bf16_ts_by(leader, d, pa + 8 * kk + (kk < 4 ? 0 : 32), db + kk * 128, id_pv,
-                                   kk > 0 || k0 > 0 || !first ? 1u : 0u);
-          pa += 64;
-          db += 512;
+      for (int c = 0; c < 2; ++c) {
+        ok = ok && warp_wait(&p_full[2 * t + c], (p_parity >> t) & 1, a.err);
+        if (ok) {
+          tc05::fence_after();
+#pragma unroll
+          for (int i = 0; i < 4; ++i) {                      // P of the second half lies 64 columns behind the first's
+            const int kk = 2 * c + (i & 1) + (i < 2 ? 0 : 4);
+            if (i < 2 || two)
+              tc05::mma_bf16_ts_by(leader, d, pa + 8 * kk + (i < 2 ? 0 : 32), db + kk * 128, id_pv, c > 0 || i > 0 || !first ? 1u : 0u);
+          }
         }
       }
       p_parity ^= 1u << t;
@@ -682,15 +683,24 @@ __global__ void __launch_bounds__(kThreads, 1) token_attn_kernel(const TokenAttn
               pk[e] = pack_bf16(p0, p1);
             }
             tc05::st16(t_s + 64 * h + 16 * c, pk);
+            tc05::wait_st();
+            tc05::fence_before();
+            __syncwarp();
+            if (lane == 0) bar_arrive(&p_full[2 * t + c]);
           }
           float s0, s1;
           unpack2(add2(sum2[0], sum2[1]), s0, s1);
           l += s0 + s1;
         }
-        tc05::wait_st();
-        tc05::fence_before();
-        __syncwarp();
-        if (lane == 0) bar_arrive(&p_full[t]);
+        if (!there) {
+          tc05::wait_st();                                   // (O that was rescaled)
+          tc05::fence_before();
+          __syncwarp();
+          if (lane == 0) {
+            bar_arrive(&p_full[2 * t]);
+            bar_arrive(&p_full[2 * t + 1]);
+          }
+        }
       }
       if (!kDup && !ok) break;
       // ---- the segment's end: O of this tile (kDup: of both copies) is complete
