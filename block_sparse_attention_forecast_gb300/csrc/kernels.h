@@ -308,6 +308,7 @@ struct TokenAttnArgs {
   int split_items;               // fewer items than this: key tiles are divided, not items
   int min_tiles;                 // a CTA's share of key tiles, at least
   int join_tiles;                // what joining cut items costs, in key tiles
+  int seg_tiles;                 // what another segment costs a CTA, in key tiles
   FastDiv by_G, by_H, by_item;   // by the groups, the heads of a group, the tokens of an item
 };
 // maps: queries (d, head, group, token, sequence); the cache's K and V [rows, 128]; the new tokens' K and V

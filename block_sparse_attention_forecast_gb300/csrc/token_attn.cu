@@ -888,6 +888,7 @@ cudaError_t launch_token_attn(const TokenAttnArgs& args, const CUtensorMap* maps
   const int two = a.n_rows <= a.tp ? 2 : 1;
   a.min_tiles = 2 * two;
   a.join_tiles = two == 2 ? 16 : 4;
+  a.seg_tiles = 3 * two;
   a.by_G = FastDiv(a.G);
   a.by_H = FastDiv(a.H);
   a.by_item = FastDiv(two == 2 ? a.tp : 2 * a.tp);

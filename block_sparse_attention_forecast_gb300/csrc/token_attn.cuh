@@ -9,8 +9,10 @@
 //                 then whatever item is next, from a counter. CTAs that run at one time attend the same
 //                 keys, and the last items are the short ones;
 //   key tiles     position u of all items' key tiles: each CTA takes an equal range of positions, whatever
-//                 items they belong to. An item cut by a range's border leaves partial results, which
-//                 token_attn_join_kernel joins.
+//                 items they belong to;
+//   equal parts   where there are fewer items than CTAs and they are about as long: each item to the same number
+//                 of CTAs, so that no CTA begins and ends more than one.
+// An item that is cut leaves partial results, which token_attn_join_kernel joins.
 #pragma once
 
 #include "common.cuh"
@@ -114,6 +116,7 @@ struct Segments {
   const int tpi, lane;
   const u32 c;
   bool split;          // key-tile division
+  u32 per_item;        // equal parts: CTAs per item; else 0
   u32 n_ctas, total;   // CTAs that take part; items or key tiles
   u32 base, incl, sum; // 32 entries at a time: the weight before them, up to this lane's, of all
   Entry mine;
@@ -162,9 +165,10 @@ struct Segments {
     longest = __reduce_max_sync(0xffffffffu, longest);
     if (report && __any_sync(0xffffffffu, bad) && lane == 0) atomicOr(a.err, SPARDA_DEV_BAD_SEQ_LEN);
     split = false;
+    per_item = 0;
     total = items;
     n_ctas = a.n_ctas;
-    if (items < (u32)a.split_items) {
+    if (items > 0 && items < (u32)a.split_items) {
       u32 tiles = 0;
       for (e0 = 0; e0 < a.n_entries; e0 += 32) {
         if (a.n_entries > 32) fetch();
@@ -175,8 +179,16 @@ struct Segments {
       // (several); joining cut ones takes as long as join_tiles key tiles.
       split = items <= n_ctas ? longest > tiles / n_ctas + a.join_tiles : longest > 2 * a.join_tiles;
       if (split) {
-        total = tiles;
-        n_ctas = min(n_ctas, max(1u, total / a.min_tiles));
+        const u32 ctas = min(n_ctas, max(1u, tiles / a.min_tiles));
+        // a range's second segment costs as much as seg_tiles key tiles (its start, its own partial result)
+        const u32 k = min(n_ctas / items, max(1u, longest / a.min_tiles));
+        if (k > 1 && (longest + k - 1) / k <= tiles / ctas + a.seg_tiles) {
+          split = false;
+          per_item = k;
+        } else {
+          total = tiles;
+          n_ctas = ctas;
+        }
       }
     }
     e0 = 0;
@@ -218,6 +230,21 @@ struct Segments {
 
   __device__ __forceinline__ bool next(Item& it) {
     u32 off;
+    if (per_item > 0) {
+      const u32 i = c / per_item, part = c - i * per_item;
+      if (started || i >= total) return false;
+      started = true;
+      const int l = seek(i, off);
+      const Entry en = entry(l);
+      fill(it, l, en, n_items(a, en) - 1 - (int)off);
+      const u32 k = min(per_item, (u32)it.nkt);
+      if (part >= k) return false;
+      const Parts parts(it.nkt, k);
+      it.k0 = parts.start(part);
+      it.k1 = parts.start(part + 1);
+      if (k > 1) it.slot = 2 * c;
+      return true;
+    }
     if (!split) {
       u32 u = c;
       if (started) {
@@ -259,11 +286,18 @@ struct Segments {
   // of it join an equal share of its rows. CTA q's part is in slot 2q, that of c1 in first_slot.
   __device__ __forceinline__ bool join(const Item& it, TokenJoin& j) const {
     if (it.slot < 0) return false;
-    const Parts parts(total, n_ctas);
-    const u32 c1 = parts.owner(it.start), c2 = parts.owner(it.start + it.nkt - 1);
+    u32 c1;
+    if (per_item > 0) {
+      c1 = c - c % per_item;
+      j.k = min(per_item, (u32)it.nkt);
+      j.first_slot = 2 * c1;
+    } else {
+      const Parts parts(total, n_ctas);
+      c1 = parts.owner(it.start);
+      j.k = parts.owner(it.start + it.nkt - 1) - c1 + 1;
+      j.first_slot = 2 * c1 + (parts.start(c1) < it.start ? 1 : 0);
+    }
     j.c1 = c1;
-    j.k = c2 - c1 + 1;
-    j.first_slot = 2 * c1 + (parts.start(c1) < it.start ? 1 : 0);
     j.rows = min(tpi, it.en.n - it.tok0) * a.H;
     j.r0 = (int)((u32)j.rows * (c - c1) / j.k);
     j.r1 = (int)((u32)j.rows * (c - c1 + 1) / j.k);
