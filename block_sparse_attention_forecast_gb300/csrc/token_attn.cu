@@ -651,6 +651,7 @@ __global__ void __launch_bounds__(kThreads, 1) token_attn_kernel(const TokenAttn
           const float mn = *other;
           const float alpha = mn > m_used ? fast_exp2(m_used - mn) : 1.f;
           if (any) {                                         // S is there, so the O before it is
+            tc05::fence_after();
 #pragma unroll 1
             for (int i = 0; i < 2; ++i) {
               tc05::ld32(t_o + 64 * h + 32 * i, x);

@@ -168,16 +168,16 @@ struct Segments {
     per_item = 0;
     total = items;
     n_ctas = a.n_ctas;
-    if (items > 0 && items < (u32)a.split_items) {
+    // Whole items take about as long as the longest one (one round), or half of it more than an even share
+    // (several); joining cut ones takes as long as join_tiles key tiles.
+    if (items < (u32)a.split_items && longest > a.join_tiles * (items <= n_ctas ? 1u : 2u)) {
       u32 tiles = 0;
       for (e0 = 0; e0 < a.n_entries; e0 += 32) {
         if (a.n_entries > 32) fetch();
         tiles += entry_tiles(a, mine, tpi);
       }
       tiles = __reduce_add_sync(0xffffffffu, tiles);
-      // Whole items take about as long as the longest one (one round), or half of it more than an even share
-      // (several); joining cut ones takes as long as join_tiles key tiles.
-      split = items <= n_ctas ? longest > tiles / n_ctas + a.join_tiles : longest > 2 * a.join_tiles;
+      split = items > n_ctas || longest > tiles / n_ctas + a.join_tiles;
       if (split) {
         const u32 ctas = min(n_ctas, max(1u, tiles / a.min_tiles));
         // a range's second segment costs as much as seg_tiles key tiles (its start, its own partial result)
