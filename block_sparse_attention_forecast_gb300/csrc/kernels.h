@@ -306,9 +306,11 @@ struct TokenAttnArgs {
   int wide_out;                  // out is 32-byte aligned
   int n_ctas;
   int split_items;               // fewer items than this: key tiles are divided, not items
-  uint32_t min_tiles;                 // a CTA's share of key tiles, at least
-  uint32_t join_tiles;                // what joining cut items costs, in key tiles
-  uint32_t seg_tiles;                 // what another segment costs a CTA, in key tiles
+  uint32_t min_tiles;            // a CTA's share of key tiles, at least
+  uint32_t item_tiles;           // what an item costs beside its key tiles, in key tiles
+  uint32_t join_tiles;           // what cutting items costs, in key tiles, where there is at most one per CTA,
+  uint32_t cut_tiles;            //   and where there are more
+  uint32_t seg_tiles;            // what another segment costs a CTA, in key tiles
   FastDiv by_G, by_H, by_item;   // by the groups, the heads of a group, the tokens of an item
 };
 // maps: queries (d, head, group, token, sequence); the cache's K and V [rows, 128]; the new tokens' K and V

@@ -14,10 +14,22 @@
 //       issues S_t = Q_t K^T (M 128, N 128) and O_t += P_t V, P read from tensor memory, where it
 //       overwrites S; one thread's MMAs run in issue order, so S of a tile's next step is issued behind the
 //       O that reads the P it overwrites, and the completion of S tells that of that O;
-//   warps 4-7 (tile 0) and 8-11 (tile 1), one thread per row: online softmax of S in registers. The maximum
-//       only moves, and O is only rescaled, when it grows by more than 2^8; P goes to tensor memory as bf16
-//       (rounded once; the sum is taken before that, in float32) in two halves of 64 keys, so that the
-//       first half's O += P V runs while the second is formed.
+//   warp 2: hands out the segments (token_attn.cuh), through shared memory;
+//   warps 4-19, two threads per row (each 64 of a key tile's 128 keys): online softmax. The two agree on a
+//       reference that only moves, and O is only rescaled, when a score passes it by more than 2^8 (log2); any
+//       reference serves that keeps P in range, since P and its sum are divided by one another. P goes to tensor
+//       memory as bf16 (rounded once; the sum is taken before that, in float32), 32 keys of each half at a
+//       time, so that their O += P V runs while the others are formed.
+// S and P never leave the SM, K and V are read once per item, and nothing is written but the output (or a partial
+// result where an item is cut). A long prompt is bound by the tensor pipe and what stands between its MMAs: 32768
+// tokens, 32 heads over 2 groups, 5.4 ms, 1.63 PFLOP/s (0.85 of the measured GEMM rate; 4.9 ms with a softmax that
+// does nothing). A decode step over 16 x 131072 tokens is bound by memory: 0.32 ms, 6.66 TB/s (0.99 of the measured
+// copy rate). What was measured on the way there, for the 32768-token prompt: one thread per row, all S in registers,
+// MMAs issued from a divergent branch 11.0 ms; the issuing warp kept together (uniform registers) 7.5; a look
+// at each barrier before the suspended wait 6.3; a step's bookkeeping cut to counters 5.65; two threads per row
+// 5.65 (and 0.91 of the time for packed prompts); P handed on in two parts 5.4. Slower: two issuing warps (7.2), a
+// watcher of the loads for the issuer (6.9), waits that poll (7.0), P formed ahead of the reference (6.4), no
+// maximum at all (5.9), S fetched in pieces of 16 keys ahead of their use (5.6).
 // Every wait is bounded. A phase of a barrier is only followed by the next one after the thread that
 // waits for it has arrived somewhere.
 #include "tc05.cuh"
@@ -42,7 +54,7 @@ constexpr int kStages = 5;
 constexpr int kHalfCols = kStage / 2;
 constexpr int kPage = 1024;                                // barriers
 constexpr uint32_t kCols = 512;                            // per tile: 128 columns of S (then P), 128 of O
-constexpr float kGrow = 8.f;                               // the maximum moves when it grows past 2^8
+constexpr float kGrow = 8.f;                               // the reference moves when a score passes it by this (log2)
 constexpr float kScaleLog2 = 1.4426950408889634f * 0.08838834764831845f;   // log2(e) / sqrt(128)
 
 template <bool kDup>
@@ -884,11 +896,21 @@ static cudaError_t launch(const TokenAttnArgs& a, const CUtensorMap* m, cudaStre
 
 cudaError_t launch_token_attn(const TokenAttnArgs& args, const CUtensorMap* maps, cudaStream_t s) {
   TokenAttnArgs a = args;
-  a.split_items = 4 * a.n_ctas;
-  // where one query tile is taken twice, two key tiles take as long as one
+  // Costs in key tiles (about 1.5 us each; where one query tile is taken twice, two take as long as one).
+  //   item_tiles: an item's start, first step and output; without them a causal prompt's ranges of many short items
+  //     end late (heads of 8192 tokens 240 us, with them 226; 4096 tokens, 16 heads a group, 200 and 149);
+  //   join_tiles, cut_tiles: a partial result written and read, and a second kernel that waits for the last CTA
+  //     (337 tokens with every item cut 60 us, with none 21; 4096 tokens, 512 items of up to 32 key tiles, cut 149,
+  //     whole 133; 512 items of up to 64, one head a group, cut 226, whole 303);
+  //   seg_tiles: a range's second segment (16 trees over 34 blocks in ranges 33 us, in equal parts 29);
+  //   split_items: items in 4 rounds are dealt out whole (8192 tokens, 1024 items: cut 417 us, whole 408), which
+  //     keeps CTAs that run at one time on the same keys.
   const int two = a.n_rows <= a.tp ? 2 : 1;
+  a.split_items = 4 * a.n_ctas;
   a.min_tiles = 2 * two;
+  a.item_tiles = 3 * two;
   a.join_tiles = two == 2 ? 16 : 4;
+  a.cut_tiles = 20 * two;
   a.seg_tiles = 3 * two;
   a.by_G = FastDiv(a.G);
   a.by_H = FastDiv(a.H);

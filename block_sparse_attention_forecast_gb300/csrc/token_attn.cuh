@@ -8,8 +8,8 @@
 //   whole items   position u of all items, entry by entry, the longest of an entry first: CTA c takes item c, and
 //                 then whatever item is next, from a counter. CTAs that run at one time attend the same
 //                 keys, and the last items are the short ones;
-//   key tiles     position u of all items' key tiles: each CTA takes an equal range of positions, whatever
-//                 items they belong to;
+//   key tiles     position u of all items' key tiles, each item's behind item_tiles positions that stand for its
+//                 beginning and end: each CTA takes an equal range of positions, whatever items they belong to;
 //   equal parts   where there are fewer items than CTAs and they are about as long: each item to the same number
 //                 of CTAs, so that no CTA begins and ends more than one.
 // An item that is cut leaves partial results, which token_attn_join_kernel joins.
@@ -40,7 +40,7 @@ struct Item {
   int nkt;      // key tiles: ceil(nblk / 2)
   int k0, k1;   // the key tiles of this segment
   int slot;     // partial result it goes to; -1: the whole item
-  u32 start;    // key-tile position of its first key tile (key-tile division)
+  u32 start;    // position of its first key tile (key-tile division)
 };
 
 __device__ __forceinline__ Entry load_entry(const TokenAttnArgs& a, int e) {
@@ -89,15 +89,16 @@ __device__ __forceinline__ u32 floor_sum(u32 n, u32 m, u32 a, u32 b) {
   return s;
 }
 
-// Key tiles of an entry's items before item i (i < its number of items). Key-tile division only, whose few
-// items (kTokenSplitItems at most) of at most 2^24 / 128 + 2^11 key tiles each keep every sum below 2^32.
+// Positions of an entry's items before item i (i < its number of items). Key-tile division only, whose few
+// items (split_items at most) of at most 2^24 / 128 + 2^11 key tiles each keep every sum below 2^32.
 __device__ __forceinline__ u32 tiles_before(const TokenAttnArgs& a, const Entry& en, int i, int tpi) {
-  if (!a.causal) return (u32)i * ((item_blocks(a, en, 0, tpi) + 1) / 2);
-  return floor_sum(i, 2 * kBlock, tpi, kBlock * (en.nctx + 2) + tpi - 1);
+  const u32 own = i * a.item_tiles;
+  if (!a.causal) return own + (u32)i * ((item_blocks(a, en, 0, tpi) + 1) / 2);
+  return own + floor_sum(i, 2 * kBlock, tpi, kBlock * (en.nctx + 2) + tpi - 1);
 }
 __device__ __forceinline__ u32 entry_tiles(const TokenAttnArgs& a, const Entry& en, int tpi) {
   const int ni = n_items(a, en);
-  return ni == 0 ? 0 : tiles_before(a, en, ni - 1, tpi) + (item_blocks(a, en, ni - 1, tpi) + 1) / 2;
+  return ni == 0 ? 0 : tiles_before(a, en, ni - 1, tpi) + a.item_tiles + (item_blocks(a, en, ni - 1, tpi) + 1) / 2;
 }
 
 // W positions in n even parts: the first of part c, and the part of a position.
@@ -121,8 +122,8 @@ struct Segments {
   u32 base, incl, sum; // 32 entries at a time: the weight before them, up to this lane's, of all
   Entry mine;
   int e0;
-  u32 pos, end, first;
-  bool started;
+  u32 pos, end;
+  int segments;        // given out so far
 
   __device__ Segments(const TokenAttnArgs& args, int tokens_per_item, int ln, int cta)
       : a(args), tpi(tokens_per_item), lane(ln), c(cta) {}
@@ -168,16 +169,22 @@ struct Segments {
     per_item = 0;
     total = items;
     n_ctas = a.n_ctas;
-    // Whole items take about as long as the longest one (one round), or half of it more than an even share
-    // (several); joining cut ones takes as long as join_tiles key tiles.
-    if (items < (u32)a.split_items && longest > a.join_tiles * (items <= n_ctas ? 1u : 2u)) {
+    // Whole items in one round take as long as the longest one; in several about as long as an even share, the part
+    // of a round that stays empty, and half of what the longest has over the average. Cutting costs join_tiles or
+    // cut_tiles key tiles beside an even share.
+    if (items < (u32)a.split_items && longest > (items <= n_ctas ? a.join_tiles : a.cut_tiles / 2)) {
       u32 tiles = 0;
       for (e0 = 0; e0 < a.n_entries; e0 += 32) {
         if (a.n_entries > 32) fetch();
         tiles += entry_tiles(a, mine, tpi);
       }
       tiles = __reduce_add_sync(0xffffffffu, tiles);
-      split = items > n_ctas || longest > tiles / n_ctas + a.join_tiles;
+      if (items <= n_ctas) {
+        split = longest > tiles / n_ctas + a.join_tiles;
+      } else {
+        const u32 average = tiles / items, idle = n_ctas - 1 - (items + n_ctas - 1) % n_ctas;   // CTAs in the last round
+        split = average * idle / n_ctas + (max(longest, average) - average) / 2 > a.cut_tiles;
+      }
       if (split) {
         const u32 ctas = min(n_ctas, max(1u, tiles / a.min_tiles));
         // a range's second segment costs as much as seg_tiles key tiles (its start, its own partial result)
@@ -195,11 +202,11 @@ struct Segments {
     base = 0;
     if (a.n_entries > 32) fetch();
     weigh();
-    started = false;
-    pos = end = first = 0;
+    segments = 0;
+    pos = end = 0;
     if (split && c < n_ctas) {
       const Parts parts(total, n_ctas);
-      first = pos = parts.start(c);
+      pos = parts.start(c);
       end = parts.start(c + 1);
     }
   }
@@ -232,8 +239,7 @@ struct Segments {
     u32 off;
     if (per_item > 0) {
       const u32 i = c / per_item, part = c - i * per_item;
-      if (started || i >= total) return false;
-      started = true;
+      if (segments++ > 0 || i >= total) return false;
       const int l = seek(i, off);
       const Entry en = entry(l);
       fill(it, l, en, n_items(a, en) - 1 - (int)off);
@@ -247,11 +253,10 @@ struct Segments {
     }
     if (!split) {
       u32 u = c;
-      if (started) {
+      if (segments++ > 0) {
         if (lane == 0) u = n_ctas + atomicAdd(a.queue, 1u);
         u = __shfl_sync(0xffffffffu, u, 0);
       }
-      started = true;
       if (u >= total) return false;
       const int l = seek(u, off);
       const Entry en = entry(l);
@@ -259,27 +264,32 @@ struct Segments {
       it.k0 = 0;
       return true;
     }
-    if (pos >= end) return false;
-    const int at = seek(pos, off);
-    const Entry en = entry(at);
-    // the last item with tiles_before <= off, 32 candidates at a time
-    int lo = 0, len = n_items(a, en);
-    while (len > 1) {
-      const int step = (len + 31) / 32;
-      const int i = lo + lane * step;
-      const bool below = i < lo + len && tiles_before(a, en, min(i, lo + len - 1), tpi) <= off;
-      const int l = 31 - __clz(__ballot_sync(0xffffffffu, below));
-      const int stop = lo + len;
-      lo += l * step;
-      len = min(step, stop - lo);
+    while (pos < end) {
+      const int at = seek(pos, off);
+      const Entry en = entry(at);
+      // the last item with tiles_before <= off, 32 candidates at a time
+      int lo = 0, len = n_items(a, en);
+      while (len > 1) {
+        const int step = (len + 31) / 32;
+        const int i = lo + lane * step;
+        const bool below = i < lo + len && tiles_before(a, en, min(i, lo + len - 1), tpi) <= off;
+        const int l = 31 - __clz(__ballot_sync(0xffffffffu, below));
+        const int stop = lo + len;
+        lo += l * step;
+        len = min(step, stop - lo);
+      }
+      fill(it, at, en, lo);
+      const u32 in = off - tiles_before(a, en, lo, tpi), left = in + (end - pos);   // positions of the item: first, end
+      it.start = pos - in + a.item_tiles;
+      it.k0 = (int)(max(in, a.item_tiles) - a.item_tiles);
+      it.k1 = (int)min((u32)it.nkt, max(left, a.item_tiles) - a.item_tiles);
+      pos = it.start + it.nkt;                               // (the next item, if the range goes on)
+      if (it.k0 == it.k1) continue;                          // the range ends before its first key tile
+      if (it.k0 > 0 || it.k1 < it.nkt) it.slot = 2 * c + (segments > 0 ? 1 : 0);
+      ++segments;
+      return true;
     }
-    fill(it, at, en, lo);
-    it.k0 = (int)(off - tiles_before(a, en, lo, tpi));
-    it.start = pos - it.k0;
-    it.k1 = (int)min((u32)it.k1, it.k0 + (end - pos));
-    if (it.k0 > 0 || it.k1 < it.nkt) it.slot = 2 * c + (pos == first ? 0 : 1);
-    pos += it.k1 - it.k0;
-    return true;
+    return false;
   }
 
   // Whether the segment's item is cut, and what this CTA does to join it: all CTAs c1 .. c1+k-1 that have a part
@@ -295,7 +305,7 @@ struct Segments {
       const Parts parts(total, n_ctas);
       c1 = parts.owner(it.start);
       j.k = parts.owner(it.start + it.nkt - 1) - c1 + 1;
-      j.first_slot = 2 * c1 + (parts.start(c1) < it.start ? 1 : 0);
+      j.first_slot = 2 * c1 + (parts.start(c1) < it.start - a.item_tiles ? 1 : 0);
     }
     j.c1 = c1;
     j.rows = min(tpi, it.en.n - it.tok0) * a.H;

@@ -119,6 +119,11 @@ def test_prompt_few_long_items_are_cut():
     _prompt_case([5], [12001], 1, 3, seed=5)           # one query tile, taken twice
 
 
+def test_prompt_items_of_two_rounds_are_cut():
+    # 160 items of 1 to 40 key tiles: ranges of several items, some of which end before an item's first key tile
+    _prompt_case([5000], None, 8, 1, seed=6)
+
+
 def test_prompt_scores_that_grow():
     # keys whose scores rise by more than 2^8 from tile to tile: the reference moves again and again
     G, H, n = 1, 4, 700
