@@ -738,6 +738,10 @@ int32_t sparda_kv4_evict_blocks(const sparda_shape* shape, const sparda_layer_kv
  * n_tokens, sets SPARDA_DEV_BAD_SEQ_LEN and writes nothing. Rows that belong to no sequence are left
  * as they were. Cache rows at and past seq_len, and rows past a sequence's end, may hold anything. Outputs
  * must not overlap inputs. All pointers 16-byte aligned, index and length arrays 4-byte.
+ *
+ * The lengths are read on the device, so a captured call serves any batch of the same row counts. The two attention
+ * calls begin while the kernel before them in the stream still runs (programmatic dependent launch) and wait for
+ * it to complete before they read or write anything; the two stores are ordinary launches.
  */
 #define SPARDA_TREE_MAX_NODES 128
 
