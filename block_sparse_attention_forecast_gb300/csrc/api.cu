@@ -238,11 +238,11 @@ size_t kv4_workspace_bytes(const sparda_shape* s, int32_t batch, int32_t kind) {
   return kind == SPARDA_WS_KV4_ATTN ? base : base + mass_stats_bytes(s, kv4_mass_slots(s)) + mass_ml_bytes(s);
 }
 
-// [the item counter, zero between calls][two partial results, and two shares in joining, for each CTA of the
-// attention of new tokens]
+// [the item counter, zero between calls][two partial results of two tiles per SM][two shares in joining per CTA, of
+// which an SM has one or two]
 size_t token_workspace_bytes(const sparda_shape* s, int32_t batch) {
   if (kv4_shape_status(s) != SPARDA_OK || batch < 1 || batch > s->max_batch) return 0;
-  return 256 + (size_t)2 * kTokenMaxCtas * (kTokenPartFloats * sizeof(float) + sizeof(TokenJoin)) + 16;
+  return 256 + (size_t)4 * kTokenMaxSms * (kTokenPartFloats * sizeof(float) + sizeof(TokenJoin)) + 16;
 }
 
 #define SPARDA_TRY(x)                     \
@@ -1091,7 +1091,7 @@ int32_t run_token_attn(const sparda_shape* s, const sparda_layer_kv* L, const vo
   a.wide_out = aligned(out, 32);
   a.queue = static_cast<unsigned*>(ws);
   a.part = reinterpret_cast<float*>((reinterpret_cast<uintptr_t>(ws) + 256 + 31) & ~static_cast<uintptr_t>(31));
-  a.joins = reinterpret_cast<TokenJoin*>(a.part + (size_t)2 * kTokenMaxCtas * kTokenPartFloats);
+  a.joins = reinterpret_cast<TokenJoin*>(a.part + (size_t)4 * kTokenMaxSms * kTokenPartFloats);
   a.n_entries = batch * G;
   a.G = G;
   a.H = H;
@@ -1100,7 +1100,7 @@ int32_t run_token_attn(const sparda_shape* s, const sparda_layer_kv* L, const vo
   a.n_rows = (int)rows;
   a.tp = 128 / H < a.n_rows ? 128 / H : a.n_rows;
   a.causal = a.parent == nullptr;
-  a.n_ctas = sms < kTokenMaxCtas ? sms : kTokenMaxCtas;
+  a.n_ctas = sms < kTokenMaxSms ? sms : kTokenMaxSms;
   CUtensorMap m[5];
   SPARDA_TRY(make_query_map(&m[0], q, q_stride, G, H, rows, seqs, a.tp));
   SPARDA_TRY(make_new_kv_map(&m[3], k, kv_stride, G, rows, seqs));

@@ -264,9 +264,8 @@ struct EvictArgs {
 cudaError_t launch_evict(const EvictArgs& a, cudaStream_t s);
 
 // Attention of many new tokens per sequence over a cache (token_attn.cu): packed prompts and trees.
-constexpr int kTokenItemRows = 256;               // query rows of an item, at most
-constexpr int kTokenPartFloats = kTokenItemRows * (128 + 2);   // a partial result: O, maximum, sum
-constexpr int kTokenMaxCtas = 160;                // CTAs of the attention, at most
+constexpr int kTokenPartFloats = 128 * (128 + 2); // a partial result of a query tile: O, maximum, sum
+constexpr int kTokenMaxSms = 160;                 // SMs that are used, at most: by a CTA of two tiles, or two of one
 constexpr int kTokenMaxNodes = 128;               // nodes of a tree, at most
 // Division by a number that the host knows, for dividends below 2^31: one product and two shifts where the
 // hardware has no divide (T. Granlund and P. Montgomery, "Division by invariant integers using multiplication",
@@ -295,7 +294,7 @@ struct TokenAttnArgs {
   const int32_t* idx;            // [B, G, kslots], the attended blocks of the cache; nullptr: all
   const int32_t* cnt;
   __nv_bfloat16* out;            // [rows, G*H, d]
-  float* part;                   // workspace [2 n_ctas][kTokenPartFloats], 32-byte aligned
+  float* part;                   // workspace [2 n_ctas][tiles of a CTA][kTokenPartFloats], 32-byte aligned
   TokenJoin* joins;              // workspace [n_ctas][2]
   unsigned* queue;               // workspace: items taken from the queue, zero between calls
   int* err;
@@ -304,7 +303,7 @@ struct TokenAttnArgs {
   int tp;                        // tokens per 128-row query tile
   int causal;                    // parent == nullptr
   int wide_out;                  // out is 32-byte aligned
-  int n_ctas;
+  int n_ctas;                    // SMs that are used; the launch makes CTAs of them
   int split_items;               // fewer items than this: key tiles are divided, not items
   uint32_t min_tiles;            // a CTA's share of key tiles, at least
   uint32_t item_tiles;           // what an item costs beside its key tiles, in key tiles

@@ -42,26 +42,34 @@ using tok::Item;
 using tok::Segments;
 using tok::u64;
 
-constexpr int kSoftmaxWarps = 16;
-constexpr int kThreads = 128 + 32 * kSoftmaxWarps;
-// registers per thread: of 96 at launch, the softmax warps take what the first warpgroup gives
-constexpr int kRegsMain = 64, kRegsSoftmax = 104;
-static_assert(128 * kRegsMain + 32 * kSoftmaxWarps * kRegsSoftmax <= kThreads * 96, "the registers of the launch");
+// Two forms: two query tiles per CTA and a CTA per SM, or (kSolo) one tile per CTA and two CTAs per SM.
+template <bool kSolo>
+struct Form {
+  static constexpr int kTiles = kSolo ? 1 : 2;
+  static constexpr int kSoftmaxWarps = 8 * kTiles;
+  static constexpr int kThreads = 128 + 32 * kSoftmaxWarps;
+  static constexpr int kPerSm = kSolo ? 2 : 1;
+  static constexpr int kStages = kSolo ? 2 : 5;              // of the ring
+  // registers per thread: the softmax warps take what the first warpgroup gives of those at launch
+  static constexpr int kRegsLaunch = kSolo ? 80 : 96, kRegsMain = 64, kRegsSoftmax = kSolo ? 88 : 104;
+  static constexpr uint32_t kCols = 256 * kTiles;            // tensor memory: per tile 128 columns of S (then P), 128 of O
+  static_assert(128 * kRegsMain + 32 * kSoftmaxWarps * kRegsSoftmax <= kThreads * kRegsLaunch, "the registers of the launch");
+};
 constexpr int kTileRows = 128;
 constexpr int kQTile = kTileRows * kRowBytes;              // 32 KiB: columns 0..63 of 128 rows, then 64..127
 constexpr int kStage = 2 * kBlockBytes;                    // 32 KiB: the same of 128 keys or values
-constexpr int kStages = 5;
 constexpr int kHalfCols = kStage / 2;
 constexpr int kPage = 1024;                                // barriers
-constexpr uint32_t kCols = 512;                            // per tile: 128 columns of S (then P), 128 of O
 constexpr float kGrow = 8.f;                               // the reference moves when a score passes it by this (log2)
 constexpr float kScaleLog2 = 1.4426950408889634f * 0.08838834764831845f;   // log2(e) / sqrt(128)
 
-template <bool kDup>
+// [barriers][query tiles][ring][a float per row]
+template <bool kSolo>
 constexpr int smem_bytes() {
-  return kPage + (kDup ? kQTile + 2048 : 2 * kQTile) + kStages * kStage + 1024;
+  return kPage + Form<kSolo>::kTiles * (kQTile + 4 * kTileRows) + Form<kSolo>::kStages * kStage;
 }
-static_assert(smem_bytes<false>() <= 227 * 1024, "the token attention fits shared memory");
+static_assert(smem_bytes<false>() <= 227 * 1024 && 2 * (smem_bytes<true>() + 1024) <= 228 * 1024,
+              "the token attention fits shared memory");
 
 __device__ __forceinline__ void bar_arrive(uint64_t* bar) {
   asm volatile("mbarrier.arrive.shared::cta.b64 _, [%0];" ::"r"(smem_addr(bar)) : "memory");
@@ -179,12 +187,14 @@ __device__ __forceinline__ u64 first_bits(int n) { return n <= 0 ? 0ull : (n >= 
 
 }  // namespace
 
-template <bool kDup>
-__global__ void __launch_bounds__(kThreads, 1) token_attn_kernel(const TokenAttnArgs a, const __grid_constant__ CUtensorMap mq,
+template <bool kSolo>
+__global__ void __launch_bounds__(Form<kSolo>::kThreads, Form<kSolo>::kPerSm) token_attn_kernel(const TokenAttnArgs a, const __grid_constant__ CUtensorMap mq,
                                                                 const __grid_constant__ CUtensorMap mkc,
                                                                 const __grid_constant__ CUtensorMap mvc,
                                                                 const __grid_constant__ CUtensorMap mkn,
                                                                 const __grid_constant__ CUtensorMap mvn) {
+  using F = Form<kSolo>;
+  constexpr int kTiles = F::kTiles, kSoftmaxWarps = F::kSoftmaxWarps, kThreads = F::kThreads, kStages = F::kStages;
   extern __shared__ __align__(1024) uint8_t smem[];
   uint64_t* q_full = reinterpret_cast<uint64_t*>(smem);
   uint64_t* q_empty = q_full + 1;
@@ -196,18 +206,15 @@ __global__ void __launch_bounds__(kThreads, 1) token_attn_kernel(const TokenAttn
   uint64_t* o_full = p_full + 4;                             // [tile]
   uint64_t* w_full = o_full + 2;                             // [work ring]
   uint64_t* w_empty = w_full + kWorkRing;
-  uint64_t* ml_full = w_empty + kWorkRing;                   // the two copies' maxima and sums (kDup)
-  uint64_t* ml_empty = ml_full + 1;
-  uint32_t* tmem_sh = reinterpret_cast<uint32_t*>(ml_empty + 1);
+  uint32_t* tmem_sh = reinterpret_cast<uint32_t*>(w_empty + kWorkRing);
   volatile uint32_t* fail_sh = tmem_sh + 1;                  // [row pairs]: a wait of one of the two warps ran out
   volatile Work* work = reinterpret_cast<volatile Work*>(smem + 512);
   uint8_t* qs = smem + kPage;
-  uint8_t* ring = qs + (kDup ? kQTile : 2 * kQTile);
+  uint8_t* ring = qs + kTiles * kQTile;
   float* row_sh = reinterpret_cast<float*>(ring + kStages * kStage);  // [tile][128]: between a row's two threads
-  float* ml_sh = row_sh + 256;                               // [tile][max, sum][128] (kDup)
 
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
-  const int H = a.H, tp = a.tp, tpi = kDup ? tp : 2 * tp;
+  const int H = a.H, tp = a.tp, tpi = kTiles * tp;
   grid_dep_launch();
   if (tid == 0) {
     mbar_init(q_full, 1);
@@ -218,22 +225,20 @@ __global__ void __launch_bounds__(kThreads, 1) token_attn_kernel(const TokenAttn
       mbar_init(&kv_full[i], 1);
       mbar_init(&kv_empty[i], 1);
     }
-    for (int t = 0; t < 2; ++t) {
+    for (int t = 0; t < kTiles; ++t) {
       mbar_init(&s_full[t], 1);
-      mbar_init(&p_full[2 * t], kSoftmaxWarps / 2);
-      mbar_init(&p_full[2 * t + 1], kSoftmaxWarps / 2);
+      mbar_init(&p_full[2 * t], 8);
+      mbar_init(&p_full[2 * t + 1], 8);
       mbar_init(&o_full[t], 1);
     }
     for (int i = 0; i < kWorkRing; ++i) {
       mbar_init(&w_full[i], 1);
       mbar_init(&w_empty[i], 2 + kSoftmaxWarps);             // producer, issuer, softmax warps
     }
-    mbar_init(ml_full, kSoftmaxWarps);
-    mbar_init(ml_empty, kSoftmaxWarps);
     fence_mbar_init();
   }
   if (warp == 1) {
-    tc05::alloc(tmem_sh, kCols);
+    tc05::alloc(tmem_sh, F::kCols);
     tc05::relinquish();
   }
   grid_dep_wait();
@@ -242,7 +247,7 @@ __global__ void __launch_bounds__(kThreads, 1) token_attn_kernel(const TokenAttn
   // query rows that no load fills: zero, once
   for (int i = tid; i < (kTileRows - tp * H) * 8; i += kThreads)
 #pragma unroll
-    for (int part = 0; part < (kDup ? 2 : 4); ++part)
+    for (int part = 0; part < 2 * kTiles; ++part)
       *reinterpret_cast<uint4*>(qs + part * (kQTile / 2) + tp * H * 128 + i * 16) = make_uint4(0u, 0u, 0u, 0u);
   fence_proxy_async_shared();
   tc05::fence_before();
@@ -279,7 +284,7 @@ __global__ void __launch_bounds__(kThreads, 1) token_attn_kernel(const TokenAttn
   };
 
   if (warp < 4) {
-    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kRegsMain));
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(F::kRegsMain));
   if (warp == 2) {
     // ------------------------------------------------------------ scheduler
     Item im;
@@ -302,7 +307,7 @@ __global__ void __launch_bounds__(kThreads, 1) token_attn_kernel(const TokenAttn
           work[i].k0 = im.k0;
           work[i].k1 = im.k1;
           work[i].slot = im.slot;
-          work[i].tiles = (kDup || im.tok0 + tp >= im.en.n) ? 1 : 2;
+          work[i].tiles = kSolo || im.tok0 + tp >= im.en.n ? 1 : 2;
         } else {
           work[i].k0 = work[i].k1 = 0;
         }
@@ -375,18 +380,9 @@ __global__ void __launch_bounds__(kThreads, 1) token_attn_kernel(const TokenAttn
       ok = __shfl_sync(0xffffffffu, ok, 0);
       ++n_item;
       const int n = it.k1 - it.k0;
-      if (!kDup) {
-        for (int p = 0; ok && p < n; ++p) {
-          load(&mkc, &mkn, it.k0 + p);
-          if (ok) load(&mvc, &mvn, it.k0 + p);
-        }
-      } else {
-        load(&mkc, &mkn, it.k0);
-        if (ok && n > 1) load(&mkc, &mkn, it.k0 + 1);
-        for (int p = 0; ok && p < n; ++p) {
-          load(&mvc, &mvn, it.k0 + p);
-          if (ok && p + 2 < n) load(&mkc, &mkn, it.k0 + p + 2);
-        }
+      for (int p = 0; ok && p < n; ++p) {
+        load(&mkc, &mkn, it.k0 + p);
+        if (ok) load(&mvc, &mvn, it.k0 + p);
       }
     }
     // a wait ran out: no copy may still be under way when the CTA ends
@@ -417,21 +413,13 @@ __global__ void __launch_bounds__(kThreads, 1) token_attn_kernel(const TokenAttn
       tc05::fence_after();
       return at;
     };
-    // (One tile's two copies wait for memory, and smaller code serves them better than a fast issue: half of S's
-    // MMAs in the code, twice around.)
-    constexpr int kAtOnce = kDup ? 4 : 8;
     auto issue_qk = [&](int t, unsigned at) {                // S_t = Q_t K^T
-      u64 da = dq + (kDup ? 0 : t * (kQTile >> 4)), db = dk + at * (kStage >> 4);
+      const u64 da = dq + t * (kQTile >> 4), db = dk + at * (kStage >> 4);
       const uint32_t d = tm + 256 * t;
-#pragma unroll 1
-      for (int k0 = 0; k0 < 8; k0 += kAtOnce) {
 #pragma unroll
-        for (int kk = 0; kk < kAtOnce; ++kk) {
-          const uint32_t off = (kk >> 2) * (kHalfCols >> 4) + (kk & 3) * 2;
-          tc05::mma_bf16_ss_by(leader, d, da + off, db + off, id_qk, kk > 0 ? 1u : k0);
-        }
-        da += kHalfCols >> 4;
-        db += kHalfCols >> 4;
+      for (int kk = 0; kk < 8; ++kk) {
+        const uint32_t off = (kk >> 2) * (kHalfCols >> 4) + (kk & 3) * 2;
+        tc05::mma_bf16_ss_by(leader, d, da + off, db + off, id_qk, kk > 0 ? 1u : 0u);
       }
       tc05::commit_by(leader, &s_full[t]);
     };
@@ -468,7 +456,7 @@ __global__ void __launch_bounds__(kThreads, 1) token_attn_kernel(const TokenAttn
       __syncwarp();
     };
     while (ok && next()) {
-      const int n = __shfl_sync(0xffffffffu, it.k1 - it.k0, 0), tiles = __shfl_sync(0xffffffffu, it.tiles, 0);
+      const int n = __shfl_sync(0xffffffffu, it.k1 - it.k0, 0), tiles = kSolo ? 1 : __shfl_sync(0xffffffffu, it.tiles, 0);
       // the segment's key tiles with fewer than 128 tokens: all before the last new block's tile are whole, but
       // for the one at the cache's end (and selected blocks)
       const int nblk = __shfl_sync(0xffffffffu, it.nblk, 0), k0 = __shfl_sync(0xffffffffu, it.k0, 0);
@@ -479,16 +467,10 @@ __global__ void __launch_bounds__(kThreads, 1) token_attn_kernel(const TokenAttn
       unsigned ks = take();
       if (!ok) break;
       issue_qk(0, ks);
-      if (!kDup && tiles == 2) issue_qk(1, ks);
+      if (!kSolo && tiles == 2) issue_qk(1, ks);
       tc05::commit_by(leader, &kv_empty[ks]);
-      if (kDup && n > 1) {
-        ks = take();
-        if (!ok) break;
-        issue_qk(1, ks);
-        tc05::commit_by(leader, &kv_empty[ks]);
-      }
-      if (n <= (kDup ? 2 : 1)) tc05::commit_by(leader, q_empty);
-      // one step of tile t on key tile p of the segment (V in stage vs); `more`: with S of the tile's next, K in ks
+      if (n == 1) tc05::commit_by(leader, q_empty);
+      // per key tile: O += P V (V in stage vs) and S of the next key tile (K in ks), tile by tile
       for (int p = 0; ok && p < n; ++p) {
         const bool two = 2 * (k0 + p) + 1 < nblk;
         const unsigned vs = take();
@@ -498,45 +480,28 @@ __global__ void __launch_bounds__(kThreads, 1) token_attn_kernel(const TokenAttn
           const int rows0 = bl.rows(it, blk), rows1 = two ? bl.rows(it, blk + 1) : kBlock;
           if (rows0 < kBlock || rows1 < kBlock) clear_rows(vs, rows0, rows1);
         }
-        if (!kDup) {
-          const bool more = p + 1 < n;
-          issue_pv(0, vs, p == 0, two);
+        const bool more = p + 1 < n;
+        issue_pv(0, vs, p == 0, two);
+        if (!ok) break;
+        if (kSolo || tiles == 1) tc05::commit_by(leader, &kv_empty[vs]);
+        if (more) {
+          ks = take();
           if (!ok) break;
-          if (more) {
-            ks = take();
-            if (!ok) break;
-            issue_qk(0, ks);
-          } else {
-            tc05::commit_by(leader, &o_full[0]);
-          }
-          if (tiles == 2) {
-            issue_pv(1, vs, p == 0, two);
-            if (!ok) break;
-            tc05::commit_by(leader, &kv_empty[vs]);
-            if (more)
-              issue_qk(1, ks);
-            else
-              tc05::commit_by(leader, &o_full[1]);
-          } else {
-            tc05::commit_by(leader, &kv_empty[vs]);
-          }
-          if (more) tc05::commit_by(leader, &kv_empty[ks]);
-          if (p + 2 == n) tc05::commit_by(leader, q_empty);
+          issue_qk(0, ks);
         } else {
-          const int t = p & 1;
-          issue_pv(t, vs, p < 2, two);
+          tc05::commit_by(leader, &o_full[0]);
+        }
+        if (!kSolo && tiles == 2) {
+          issue_pv(1, vs, p == 0, two);
           if (!ok) break;
           tc05::commit_by(leader, &kv_empty[vs]);
-          if (p + 2 < n) {
-            ks = take();
-            if (!ok) break;
-            issue_qk(t, ks);
-            tc05::commit_by(leader, &kv_empty[ks]);
-            if (p + 3 == n) tc05::commit_by(leader, q_empty);
-          } else {
-            tc05::commit_by(leader, &o_full[t]);
-          }
+          if (more)
+            issue_qk(1, ks);
+          else
+            tc05::commit_by(leader, &o_full[1]);
         }
+        if (more) tc05::commit_by(leader, &kv_empty[ks]);
+        if (p + 2 == n) tc05::commit_by(leader, q_empty);
       }
     }
     if (!ok) {                                               // a wait ran out: let the MMAs under way end
@@ -549,12 +514,12 @@ __global__ void __launch_bounds__(kThreads, 1) token_attn_kernel(const TokenAttn
     asm volatile("bar.sync 15, %0;" ::"n"(kThreads) : "memory");
     if (warp == 1) {
       tc05::fence_after();
-      tc05::dealloc(tmem, kCols);
+      tc05::dealloc(tmem, F::kCols);
     }
   } else {
     // ------------------------------------------------------------ softmax, two threads per row
-    asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kRegsSoftmax));
-    const int t = ((warp - 4) >> 2) & 1, h = (warp - 4) >> 3;   // tile, half of the key tile
+    asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(F::kRegsSoftmax));
+    const int t = kSolo ? 0 : ((warp - 4) >> 2) & 1, h = (warp - 4) >> (kSolo ? 2 : 3);   // tile, half of the key tile
     const int quarter = warp & 3;                            // tensor-memory lanes 32q .. 32q+31
     const int r = quarter * 32 + lane;
     const int rt = a.by_H.div(r);                                 // the row's token in its tile
@@ -564,15 +529,15 @@ __global__ void __launch_bounds__(kThreads, 1) token_attn_kernel(const TokenAttn
     float* other = row_sh + 128 * t + r;
     const u64 scale2 = pack2(kScaleLog2, kScaleLog2);
     bool met = false;                                        // both warps of the rows know that a wait ran out
-    unsigned n_s = 0, n_seg = 0, n_o[2] = {0, 0};
+    unsigned n_s = 0, n_o = 0;
     int tree_b = -1;
     u64 anc0 = 0, anc1 = 0;                                  // tree: this row's ancestors and itself
     while (ok && next()) {
-      if (!kDup && t >= it.tiles) continue;
+      if (t >= it.tiles) continue;
       const int n = it.k1 - it.k0;
-      const int tile_tok = it.tok0 + (kDup ? 0 : t * tp);
+      const int tile_tok = it.tok0 + t * tp;
       const int tok = tile_tok + rt;                         // in the sequence
-      if (a.parent && (it.b != tree_b || !kDup)) {
+      if (a.parent && (it.b != tree_b || !kSolo)) {
         // the chain of parents, from a table that the warp holds in registers
         tree_b = it.b;
         int par[4];
@@ -605,7 +570,7 @@ __global__ void __launch_bounds__(kThreads, 1) token_attn_kernel(const TokenAttn
       const int whole = bl.sel ? 0 : (it.P % kBlock ? it.nctx - 1 : it.nctx + (a.parent ? 0 : (tile_tok + 1) / kBlock)) / 2;
       float m_used = -INFINITY, l = 0.f;
       bool any = false;                                      // this tile has had a step
-      for (int p = kDup ? t : 0; p < n; p += kDup ? 2 : 1) {
+      for (int p = 0; p < n; ++p) {
         const int blk = 2 * (it.k0 + p) + h;
         const bool there = blk < it.nblk;                    // an odd number of blocks: the last tile has one
         u64 see = ~0ull;                                     // the keys of the block that this row attends
@@ -629,7 +594,7 @@ __global__ void __launch_bounds__(kThreads, 1) token_attn_kernel(const TokenAttn
         float mb = -INFINITY;
         if (ok && there) {
           tc05::fence_after();
-#pragma unroll(kDup ? 1 : 2)
+#pragma unroll(kSolo ? 1 : 2)
           for (int c = 0; c < 2; ++c) {
             load(c);
             float m4[4];
@@ -715,65 +680,30 @@ __global__ void __launch_bounds__(kThreads, 1) token_attn_kernel(const TokenAttn
           }
         }
       }
-      if (!kDup && !ok) break;
-      // ---- the segment's end: O of this tile (kDup: of both copies) is complete
-      float w0 = 1.f, w1 = 0.f;
-      if (ok) {                                              // the row's sum (both warps of the rows are here, or neither)
-        if (h == 1) *other = l;
-        pair_sync(pair);
-        if (h == 0) *other = l += *other;
-        pair_sync(pair);
-        l = *other;
-      }
-      if (!kDup) {
-        ok = warp_wait(&o_full[t], n_o[t] & 1, a.err);
-        ++n_o[t];
-      } else {
-        if (h == 0) {
-          ml_sh[256 * t + r] = m_used;
-          ml_sh[256 * t + 128 + r] = l;
-        }
-#pragma unroll
-        for (int u = 0; u < 2; ++u)
-          if (u < n) {
-            ok = ok && warp_wait(&o_full[u], n_o[u] & 1, a.err);
-            ++n_o[u];
-          }
-        __syncwarp();
-        if (lane == 0) bar_arrive(ml_full);
-        ok = warp_wait(ml_full, n_seg & 1, a.err) && ok;
-        const float ma = ml_sh[r], la = ml_sh[128 + r], mb = ml_sh[256 + r], lb = ml_sh[256 + 128 + r];
-        const float mm = fmaxf(ma, mb);
-        w0 = ma == -INFINITY ? 0.f : fast_exp2(ma - mm);
-        w1 = mb == -INFINITY ? 0.f : fast_exp2(mb - mm);
-        m_used = mm;
-        l = w0 * la + w1 * lb;
-      }
+      if (!ok) break;
+      // ---- the segment's end: the row's sum, and O complete
+      if (h == 1) *other = l;
+      pair_sync(pair);
+      if (h == 0) *other = l += *other;
+      pair_sync(pair);
+      l = *other;
+      ok = warp_wait(&o_full[t], n_o & 1, a.err);
+      ++n_o;
       if (ok) {
         tc05::fence_after();
         const bool live = rt < tp && tok < it.n;
         const size_t row = a.cu ? (size_t)it.row0 + tok : (size_t)it.b * a.n_rows + tok;
         const float inv = l > 0.f || l != l ? 1.f / l : 0.f;
         __nv_bfloat16* dst = a.out + ((row * a.G + it.g) * H + (r - rt * H)) * kHeadDim;
-        const int prow = (kDup ? 0 : t * kTileRows) + r;
-        float* part = a.part + (size_t)max(it.slot, 0) * kTokenPartFloats;
-        // a warp's columns: half of its tile's, or (kDup) a quarter of the joined tile's
-        const int c0 = kDup ? 2 * h + t : 2 * h, c1 = kDup ? c0 + 1 : c0 + 2;
+        const int prow = t * kTileRows + r;
+        float* part = a.part + (size_t)max(it.slot, 0) * kTiles * kTokenPartFloats;
+        const int c0 = 2 * h, c1 = c0 + 2;                   // a warp's columns: half of the tile's
 #pragma unroll 1
         for (int c = c0; c < c1; ++c) {
           float o[32];
           __syncwarp();
-          tc05::ld32(tmem + lane_off + (kDup ? 0 : 256 * t) + 128 + 32 * c, o);
+          tc05::ld32(t_o + 32 * c, o);
           tc05::wait_ld();
-          if (kDup) {
-            if (n > 1) {
-              float o1[32];
-              tc05::ld32(tmem + lane_off + 256 + 128 + 32 * c, o1);
-              tc05::wait_ld();
-#pragma unroll
-              for (int e = 0; e < 32; ++e) o[e] = w0 * o[e] + w1 * o1[e];
-            }
-          }
           if (live && it.slot < 0) {
 #pragma unroll
             for (int e = 0; e < 2; ++e) {
@@ -793,18 +723,12 @@ __global__ void __launch_bounds__(kThreads, 1) token_attn_kernel(const TokenAttn
               store32(part + prow * kHeadDim + 32 * c + 8 * e, reinterpret_cast<const uint32_t*>(o + 8 * e));
           }
         }
-        if (live && it.slot >= 0 && h == 0 && (!kDup || t == 0)) {
-          float* ml = part + kTokenItemRows * kHeadDim;
+        if (live && it.slot >= 0 && h == 0) {
+          float* ml = part + kTiles * kTileRows * kHeadDim;
           ml[prow] = m_used;
-          ml[kTokenItemRows + prow] = l;
+          ml[kTiles * kTileRows + prow] = l;
         }
         tc05::fence_before();
-      }
-      if (kDup) {                                            // both copies' O have been read by both
-        __syncwarp();
-        if (lane == 0) bar_arrive(ml_empty);
-        ok = warp_wait(ml_empty, n_seg & 1, a.err) && ok;
-        ++n_seg;
       }
     }
     // a warp whose wait ran out outside of a step leaves by way of the barrier that the other one is at, or comes to
@@ -842,12 +766,12 @@ struct JoinSum {
   }
 };
 
-__global__ void __launch_bounds__(kJoinThreads) token_attn_join_kernel(const TokenAttnArgs a) {
+__global__ void __launch_bounds__(kJoinThreads) token_attn_join_kernel(const TokenAttnArgs a, int tiles) {
   __shared__ float ml_sh[kJoinWarps][2];
   __shared__ float4 o_sh[kJoinWarps][32];
   grid_dep_wait();
   if (blockIdx.x == 0 && threadIdx.x == 0) *a.queue = 0;
-  const int tp = a.tp, H = a.H, warp = threadIdx.x >> 5, quad = threadIdx.x & 31;
+  const int tp = a.tp, H = a.H, warp = threadIdx.x >> 5, quad = threadIdx.x & 31, rows = tiles * kTileRows;
   for (int which = 0; which < 2; ++which) {
     const TokenJoin j = a.joins[2 * (blockIdx.x / kJoinSplit) + which];
     const int b = blockIdx.x % kJoinSplit, n = j.r1 - j.r0;
@@ -860,8 +784,8 @@ __global__ void __launch_bounds__(kJoinThreads) token_attn_join_kernel(const Tok
       const int step = many ? kJoinWarps : 1;
 #pragma unroll 8
       for (int q = many ? warp : 0; q < j.k; q += step) {
-        const float* part = a.part + (size_t)(q == 0 ? j.first_slot : 2 * (j.c1 + q)) * kTokenPartFloats;
-        s.add(part[kTokenItemRows * kHeadDim + prow], part[kTokenItemRows * (kHeadDim + 1) + prow],
+        const float* part = a.part + (size_t)(q == 0 ? j.first_slot : 2 * (j.c1 + q)) * tiles * kTokenPartFloats;
+        s.add(part[rows * kHeadDim + prow], part[rows * (kHeadDim + 1) + prow],
               reinterpret_cast<const float4*>(part + prow * kHeadDim)[quad]);
       }
       if (many) {
@@ -884,19 +808,23 @@ __global__ void __launch_bounds__(kJoinThreads) token_attn_join_kernel(const Tok
   }
 }
 
-template <bool kDup>
+template <bool kSolo>
 static cudaError_t launch(const TokenAttnArgs& a, const CUtensorMap* m, cudaStream_t s) {
+  using F = Form<kSolo>;
   static SmemOptIn opt;
-  if (!opt.set(token_attn_kernel<kDup>, smem_bytes<kDup>())) return cudaErrorInvalidValue;
-  const cudaError_t e = launch_pdl(token_attn_kernel<kDup>, dim3(a.n_ctas), dim3(kThreads), smem_bytes<kDup>(), s, a, m[0],
-                                   m[1], m[2], m[3], m[4]);
+  if (!opt.set(token_attn_kernel<kSolo>, smem_bytes<kSolo>())) return cudaErrorInvalidValue;
+  cudaError_t e = launch_pdl(token_attn_kernel<kSolo>, dim3(a.n_ctas), dim3(F::kThreads), smem_bytes<kSolo>(), s, a, m[0], m[1],
+                             m[2], m[3], m[4]);
   if (e != cudaSuccess) return e;
-  return launch_pdl(token_attn_join_kernel, dim3(a.n_ctas * kJoinSplit), dim3(kJoinThreads), 0, s, a);
+  e = launch_pdl(token_attn_join_kernel, dim3(a.n_ctas * kJoinSplit), dim3(kJoinThreads), 0, s, a, F::kTiles);
+  if (e != cudaSuccess) cudaMemsetAsync(a.queue, 0, sizeof(unsigned), s);   // (what the join leaves behind)
+  return e;
 }
 
 cudaError_t launch_token_attn(const TokenAttnArgs& args, const CUtensorMap* maps, cudaStream_t s) {
   TokenAttnArgs a = args;
-  // Costs in key tiles (about 1.5 us each; where one query tile is taken twice, two take as long as one).
+  const bool solo = a.n_rows <= a.tp;
+  // Costs in key tiles (about 1.5 us each).
   //   item_tiles: an item's start, first step and output; without them a causal prompt's ranges of many short items
   //     end late (heads of 8192 tokens 240 us, with them 226; 4096 tokens, 16 heads a group, 200 and 149);
   //   join_tiles, cut_tiles: a partial result written and read, and a second kernel that waits for the last CTA
@@ -905,17 +833,17 @@ cudaError_t launch_token_attn(const TokenAttnArgs& args, const CUtensorMap* maps
   //   seg_tiles: a range's second segment (16 trees over 34 blocks in ranges 33 us, in equal parts 29);
   //   split_items: items in 4 rounds are dealt out whole (8192 tokens, 1024 items: cut 417 us, whole 408), which
   //     keeps CTAs that run at one time on the same keys.
-  const int two = a.n_rows <= a.tp ? 2 : 1;
+  a.n_ctas *= solo ? 2 : 1;
   a.split_items = 4 * a.n_ctas;
-  a.min_tiles = 2 * two;
-  a.item_tiles = 3 * two;
-  a.join_tiles = two == 2 ? 16 : 4;
-  a.cut_tiles = 20 * two;
-  a.seg_tiles = 3 * two;
+  a.min_tiles = 2;
+  a.item_tiles = 3;
+  a.join_tiles = 4;
+  a.cut_tiles = 20;
+  a.seg_tiles = 3;
   a.by_G = FastDiv(a.G);
   a.by_H = FastDiv(a.H);
-  a.by_item = FastDiv(two == 2 ? a.tp : 2 * a.tp);
-  return a.n_rows <= a.tp ? launch<true>(a, maps, s) : launch<false>(a, maps, s);
+  a.by_item = FastDiv(solo ? a.tp : 2 * a.tp);
+  return solo ? launch<true>(a, maps, s) : launch<false>(a, maps, s);
 }
 
 }  // namespace sparda
