@@ -6,16 +6,16 @@
 //   out = sum_u p_u v_u / sum_u p_u,   p_u = 2^((q . k_u - m) log2(e) / sqrt(128)),   m a running maximum
 //
 // A CTA holds the query rows of an item, row (token - first) * H + h of one KV group: two tiles of 128 rows
-// that share every key tile (128 keys: two 64-token blocks) it loads, or, where all rows fit one tile,
-// the one tile twice (kDup), each copy taking every other key tile, joined at the end. That keeps two
-// softmaxes and two accumulators under way for the one tensor pipe:
+// that share every key tile (128 keys: two 64-token blocks) it loads, or, where all rows of a sequence's group fit one
+// tile, that tile, and two CTAs run on an SM (kSolo). Either keeps two softmaxes and two accumulators under way for
+// the one tensor pipe:
 //   warp 0, one lane: TMA loads of the query tiles and of each key tile's K and V into a ring of 32 KiB stages;
 //   warp 1: tensor-memory allocation; zeroes the value rows past a sequence's end (0 * NaN is NaN) and
 //       issues S_t = Q_t K^T (M 128, N 128) and O_t += P_t V, P read from tensor memory, where it
 //       overwrites S; one thread's MMAs run in issue order, so S of a tile's next step is issued behind the
 //       O that reads the P it overwrites, and the completion of S tells that of that O;
 //   warp 2: hands out the segments (token_attn.cuh), through shared memory;
-//   warps 4-19, two threads per row (each 64 of a key tile's 128 keys): online softmax. The two agree on a
+//   warps 4-19 (kSolo: 4-11), two threads per row (each 64 of a key tile's 128 keys): online softmax. The two agree on a
 //       reference that only moves, and O is only rescaled, when a score passes it by more than 2^8 (log2); any
 //       reference serves that keeps P in range, since P and its sum are divided by one another. P goes to tensor
 //       memory as bf16 (rounded once; the sum is taken before that, in float32), 32 keys of each half at a
@@ -23,7 +23,7 @@
 // S and P never leave the SM, K and V are read once per item, and nothing is written but the output (or a partial
 // result where an item is cut). A long prompt is bound by the tensor pipe and what stands between its MMAs: 32768
 // tokens, 32 heads over 2 groups, 5.4 ms, 1.63 PFLOP/s (0.85 of the measured GEMM rate; 4.9 ms with a softmax that
-// does nothing). A decode step over 16 x 131072 tokens is bound by memory: 0.32 ms, 6.66 TB/s (0.99 of the measured
+// does nothing). A decode step over 16 x 131072 tokens is bound by memory: 0.315 ms, 6.8 TB/s (1.01 of the measured
 // copy rate). What was measured on the way there, for the 32768-token prompt: one thread per row, all S in registers,
 // MMAs issued from a divergent branch 11.0 ms; the issuing warp kept together (uniform registers) 7.5; a look
 // at each barrier before the suspended wait 6.3; a step's bookkeeping cut to counters 5.65; two threads per row
@@ -50,6 +50,9 @@ struct Form {
   static constexpr int kThreads = 128 + 32 * kSoftmaxWarps;
   static constexpr int kPerSm = kSolo ? 2 : 1;
   static constexpr int kStages = kSolo ? 2 : 5;              // of the ring
+  // Blocks of the join per CTA: 256 rows of few parts each to 64 warps (16 trees over 34 blocks 29 us, to 16 warps 33);
+  // 128 rows at most, and twice the CTAs, to 16 (64 trees over 500 tokens 42 us, to 64 warps 45).
+  static constexpr int kJoinSplit = kSolo ? 2 : 8;
   // registers per thread: the softmax warps take what the first warpgroup gives of those at launch
   static constexpr int kRegsLaunch = kSolo ? 80 : 96, kRegsMain = 64, kRegsSoftmax = kSolo ? 88 : 104;
   static constexpr uint32_t kCols = 256 * kTiles;            // tensor memory: per tile 128 columns of S (then P), 128 of O
@@ -743,12 +746,11 @@ __global__ void __launch_bounds__(Form<kSolo>::kThreads, Form<kSolo>::kPerSm) to
 
 // Joins the partial results of the items that the key-tile division cut: out = sum_i w_i O_i / sum_i w_i l_i
 // with w_i = 2^(m_i - max m). joins[c] holds what CTA c of the attention is to join: its shares of the rows of at most two
-// items (the one its range began in and the one it ended in). kJoinSplit blocks take a share together: what joining
-// costs is the latency of a few dependent reads, so each thread has as few as may be. A block holds 8 rows of 32
-// column quads at a time or, for items of many parts, one row whose parts are dealt out to the 8 warps.
+// items (the one its range began in and the one it ended in). Form::kJoinSplit blocks take a share together: what
+// joining costs is the latency of a few dependent reads, so each thread has as few as may be. A block holds 8 rows of
+// 32 column quads at a time or, for items of many parts, one row whose parts are dealt out to the 8 warps.
 constexpr int kJoinThreads = 256;
 constexpr int kJoinWarps = kJoinThreads / 32;
-constexpr int kJoinSplit = 8;
 
 struct JoinSum {
   float m, l;
@@ -766,12 +768,14 @@ struct JoinSum {
   }
 };
 
-__global__ void __launch_bounds__(kJoinThreads) token_attn_join_kernel(const TokenAttnArgs a, int tiles) {
+template <bool kSolo>
+__global__ void __launch_bounds__(kJoinThreads) token_attn_join_kernel(const TokenAttnArgs a) {
+  constexpr int kTiles = Form<kSolo>::kTiles, kJoinSplit = Form<kSolo>::kJoinSplit;
   __shared__ float ml_sh[kJoinWarps][2];
   __shared__ float4 o_sh[kJoinWarps][32];
   grid_dep_wait();
   if (blockIdx.x == 0 && threadIdx.x == 0) *a.queue = 0;
-  const int tp = a.tp, H = a.H, warp = threadIdx.x >> 5, quad = threadIdx.x & 31, rows = tiles * kTileRows;
+  const int tp = a.tp, H = a.H, warp = threadIdx.x >> 5, quad = threadIdx.x & 31, rows = kTiles * kTileRows;
   for (int which = 0; which < 2; ++which) {
     const TokenJoin j = a.joins[2 * (blockIdx.x / kJoinSplit) + which];
     const int b = blockIdx.x % kJoinSplit, n = j.r1 - j.r0;
@@ -784,7 +788,7 @@ __global__ void __launch_bounds__(kJoinThreads) token_attn_join_kernel(const Tok
       const int step = many ? kJoinWarps : 1;
 #pragma unroll 8
       for (int q = many ? warp : 0; q < j.k; q += step) {
-        const float* part = a.part + (size_t)(q == 0 ? j.first_slot : 2 * (j.c1 + q)) * tiles * kTokenPartFloats;
+        const float* part = a.part + (size_t)(q == 0 ? j.first_slot : 2 * (j.c1 + q)) * kTiles * kTokenPartFloats;
         s.add(part[rows * kHeadDim + prow], part[rows * (kHeadDim + 1) + prow],
               reinterpret_cast<const float4*>(part + prow * kHeadDim)[quad]);
       }
@@ -816,13 +820,16 @@ static cudaError_t launch(const TokenAttnArgs& a, const CUtensorMap* m, cudaStre
   cudaError_t e = launch_pdl(token_attn_kernel<kSolo>, dim3(a.n_ctas), dim3(F::kThreads), smem_bytes<kSolo>(), s, a, m[0], m[1],
                              m[2], m[3], m[4]);
   if (e != cudaSuccess) return e;
-  e = launch_pdl(token_attn_join_kernel, dim3(a.n_ctas * kJoinSplit), dim3(kJoinThreads), 0, s, a, F::kTiles);
+  e = launch_pdl(token_attn_join_kernel<kSolo>, dim3(a.n_ctas * F::kJoinSplit), dim3(kJoinThreads), 0, s, a);
   if (e != cudaSuccess) cudaMemsetAsync(a.queue, 0, sizeof(unsigned), s);   // (what the join leaves behind)
   return e;
 }
 
 cudaError_t launch_token_attn(const TokenAttnArgs& args, const CUtensorMap* maps, cudaStream_t s) {
   TokenAttnArgs a = args;
+  // One tile per CTA where all rows fit it: 64 trees of 4 nodes over 500 tokens 44 us, with a second tile that
+  // takes every other key tile for the same rows 54. Items of more rows read each key tile once for two query
+  // tiles: 32768 tokens 5.4 ms (a tile per CTA 6.1), 64 nodes over 16 x 32768 tokens 415 us (646).
   const bool solo = a.n_rows <= a.tp;
   // Costs in key tiles (about 1.5 us each).
   //   item_tiles: an item's start, first step and output; without them a causal prompt's ranges of many short items

@@ -116,7 +116,7 @@ def test_prompt_whole_items_from_the_queue():
 def test_prompt_few_long_items_are_cut():
     # one group and head: 8 items of up to 16 key tiles and a past of 90 more, shared by all SMs
     _prompt_case([2000], [11500], 1, 1, seed=4)
-    _prompt_case([5], [12001], 1, 3, seed=5)           # one query tile, taken twice
+    _prompt_case([5], [12001], 1, 3, seed=5)           # items of many key tiles
 
 
 def test_prompt_items_of_two_rounds_are_cut():
