@@ -32,6 +32,8 @@
 // maximum at all (5.9), S fetched in pieces of 16 keys ahead of their use (5.6).
 // Every wait is bounded. A phase of a barrier is only followed by the next one after the thread that
 // waits for it has arrived somewhere.
+#include <algorithm>
+
 #include "tc05.cuh"
 #include "token_attn.cuh"
 
@@ -292,10 +294,10 @@ __global__ void __launch_bounds__(Form<kSolo>::kThreads, Form<kSolo>::kPerSm) to
     // ------------------------------------------------------------ scheduler
     Item im;
     int n_join = 0;
-    for (bool more = true; ok && more;) {
+    for (bool more = true; more;) {                          // (to the end, though a wait ran out: see take())
       more = seg.next(im);
       const int i = n_work % kWorkRing;
-      if (n_work >= (unsigned)kWorkRing) ok = warp_wait(&w_empty[i], ((n_work / kWorkRing) & 1) ^ 1, a.err);
+      if (ok && n_work >= (unsigned)kWorkRing) ok = warp_wait(&w_empty[i], ((n_work / kWorkRing) & 1) ^ 1, a.err);
       if (ok && lane == 0) {
         if (more) {
           const int b = a.by_G.div(im.e);
@@ -325,7 +327,7 @@ __global__ void __launch_bounds__(Form<kSolo>::kThreads, Form<kSolo>::kPerSm) to
       }
     }
     if (lane == 0)
-      for (; n_join < 2; ++n_join) a.joins[2 * blockIdx.x + n_join].r0 = a.joins[2 * blockIdx.x + n_join].r1 = 0;
+      for (; n_join < 2; ++n_join) a.joins[2 * blockIdx.x + n_join] = TokenJoin{};
   } else if (warp == 0) {
     // ------------------------------------------------------------ TMA producer
     if (lane == 0) {
@@ -747,10 +749,13 @@ __global__ void __launch_bounds__(Form<kSolo>::kThreads, Form<kSolo>::kPerSm) to
 // Joins the partial results of the items that the key-tile division cut: out = sum_i w_i O_i / sum_i w_i l_i
 // with w_i = 2^(m_i - max m). joins[c] holds what CTA c of the attention is to join: its shares of the rows of at most two
 // items (the one its range began in and the one it ended in). Form::kJoinSplit blocks take a share together: what
-// joining costs is the latency of a few dependent reads, so each thread has as few as may be. A block holds 8 rows of
-// 32 column quads at a time or, for items of many parts, one row whose parts are dealt out to the 8 warps.
+// joining costs is the latency of a few dependent reads, so each thread has as few as may be, and kJoinLoads parts are under
+// way at a time (in turn 16 trees over 34 blocks take 29 us, two at a time 27, eight 30: fewer blocks on an SM). A
+// block holds 8 rows of 32 column quads at a time or, for items of many parts, one row whose parts are dealt out to the
+// 8 warps.
 constexpr int kJoinThreads = 256;
 constexpr int kJoinWarps = kJoinThreads / 32;
+constexpr int kJoinLoads = 2;      // parts under way
 
 struct JoinSum {
   float m, l;
@@ -774,55 +779,63 @@ __global__ void __launch_bounds__(kJoinThreads) token_attn_join_kernel(const Tok
   __shared__ float ml_sh[kJoinWarps][2];
   __shared__ float4 o_sh[kJoinWarps][32];
   grid_dep_wait();
-  if (blockIdx.x == 0 && threadIdx.x == 0) *a.queue = 0;
   const int tp = a.tp, H = a.H, warp = threadIdx.x >> 5, quad = threadIdx.x & 31, rows = kTiles * kTileRows;
-  for (int which = 0; which < 2; ++which) {
-    const TokenJoin j = a.joins[2 * (blockIdx.x / kJoinSplit) + which];
-    const int b = blockIdx.x % kJoinSplit, n = j.r1 - j.r0;
-    const bool many = j.k > 2 * kJoinWarps;                  // the parts of a row to all warps
-    const int r0 = j.r0 + n * b / kJoinSplit, r1 = j.r0 + n * (b + 1) / kJoinSplit;
-    for (int v = r0 + (many ? 0 : warp); v < r1; v += many ? 1 : kJoinWarps) {
-      const int tk = a.by_H.div(v), h = v - tk * H;
-      const int prow = (tk >= tp ? kTileRows + (tk - tp) * H : tk * H) + h;
-      JoinSum s{-INFINITY, 0.f, make_float4(0.f, 0.f, 0.f, 0.f)};
-      const int step = many ? kJoinWarps : 1;
-#pragma unroll 8
-      for (int q = many ? warp : 0; q < j.k; q += step) {
+  // the rows of both joins, one after the other
+  const int at = blockIdx.x % kJoinSplit;
+  const TokenJoin* js = a.joins + 2 * (blockIdx.x / kJoinSplit);
+  const TokenJoin j0 = js[0], j1 = js[1];
+  const int n0 = j0.r1 - j0.r0, n = n0 + j1.r1 - j1.r0;
+  const bool many = max(j0.k, j1.k) > 2 * kJoinWarps;        // the parts of a row to all warps
+  const int end = n * (at + 1) / kJoinSplit, step = many ? kJoinWarps : 1;
+  for (int r = n * at / kJoinSplit + (many ? 0 : warp); r < end; r += many ? 1 : kJoinWarps) {
+    const TokenJoin& j = r < n0 ? j0 : j1;
+    const int v = r < n0 ? j0.r0 + r : j1.r0 + r - n0;
+    const int tk = a.by_H.div(v), h = v - tk * H;
+    const int prow = (tk >= tp ? kTileRows + (tk - tp) * H : tk * H) + h;
+    JoinSum s{-INFINITY, 0.f, make_float4(0.f, 0.f, 0.f, 0.f)};
+    for (int q0 = many ? warp : 0; q0 < j.k; q0 += kJoinLoads * step) {
+      float mi[kJoinLoads], li[kJoinLoads];
+      float4 oi[kJoinLoads];
+#pragma unroll
+      for (int i = 0; i < kJoinLoads; ++i) {                 // (the last part again: no branch between the loads)
+        const int q = min(q0 + i * step, j.k - 1);
         const float* part = a.part + (size_t)(q == 0 ? j.first_slot : 2 * (j.c1 + q)) * kTiles * kTokenPartFloats;
-        s.add(part[rows * kHeadDim + prow], part[rows * (kHeadDim + 1) + prow],
-              reinterpret_cast<const float4*>(part + prow * kHeadDim)[quad]);
+        mi[i] = part[rows * kHeadDim + prow];
+        li[i] = part[rows * (kHeadDim + 1) + prow];
+        oi[i] = reinterpret_cast<const float4*>(part + prow * kHeadDim)[quad];
       }
-      if (many) {
-        o_sh[warp][quad] = s.o;
-        if (quad == 0) {
-          ml_sh[warp][0] = s.m;
-          ml_sh[warp][1] = s.l;
-        }
-        __syncthreads();
-        if (warp == 0)
-          for (int w = 1; w < kJoinWarps; ++w) s.add(ml_sh[w][0], ml_sh[w][1], o_sh[w][quad]);
-        __syncthreads();
+#pragma unroll
+      for (int i = 0; i < kJoinLoads; ++i)
+        if (q0 + i * step < j.k) s.add(mi[i], li[i], oi[i]);
+    }
+    if (many) {
+      o_sh[warp][quad] = s.o;
+      if (quad == 0) {
+        ml_sh[warp][0] = s.m;
+        ml_sh[warp][1] = s.l;
       }
-      if (!many || warp == 0) {
-        const float inv = s.l > 0.f || s.l != s.l ? 1.f / s.l : 0.f;
-        uint2* dst = reinterpret_cast<uint2*>(a.out + (((size_t)(j.out_row + tk) * a.G + j.g) * H + h) * kHeadDim);
-        dst[quad] = make_uint2(pack_bf16(s.o.x * inv, s.o.y * inv), pack_bf16(s.o.z * inv, s.o.w * inv));
-      }
+      __syncthreads();
+      if (warp == 0)
+        for (int w = 1; w < kJoinWarps; ++w) s.add(ml_sh[w][0], ml_sh[w][1], o_sh[w][quad]);
+      __syncthreads();
+    }
+    if (!many || warp == 0) {
+      const float inv = s.l > 0.f || s.l != s.l ? 1.f / s.l : 0.f;
+      uint2* dst = reinterpret_cast<uint2*>(a.out + (((size_t)(j.out_row + tk) * a.G + j.g) * H + h) * kHeadDim);
+      dst[quad] = make_uint2(pack_bf16(s.o.x * inv, s.o.y * inv), pack_bf16(s.o.z * inv, s.o.w * inv));
     }
   }
 }
 
 template <bool kSolo>
-static cudaError_t launch(const TokenAttnArgs& a, const CUtensorMap* m, cudaStream_t s) {
+static cudaError_t launch(const TokenAttnArgs& a, const CUtensorMap* m, bool joined, cudaStream_t s) {
   using F = Form<kSolo>;
   static SmemOptIn opt;
   if (!opt.set(token_attn_kernel<kSolo>, smem_bytes<kSolo>())) return cudaErrorInvalidValue;
-  cudaError_t e = launch_pdl(token_attn_kernel<kSolo>, dim3(a.n_ctas), dim3(F::kThreads), smem_bytes<kSolo>(), s, a, m[0], m[1],
+  const cudaError_t e = launch_pdl(token_attn_kernel<kSolo>, dim3(a.n_ctas), dim3(F::kThreads), smem_bytes<kSolo>(), s, a, m[0], m[1],
                              m[2], m[3], m[4]);
-  if (e != cudaSuccess) return e;
-  e = launch_pdl(token_attn_join_kernel<kSolo>, dim3(a.n_ctas * F::kJoinSplit), dim3(kJoinThreads), 0, s, a);
-  if (e != cudaSuccess) cudaMemsetAsync(a.queue, 0, sizeof(unsigned), s);   // (what the join leaves behind)
-  return e;
+  if (e != cudaSuccess || !joined) return e;
+  return launch_pdl(token_attn_join_kernel<kSolo>, dim3(a.n_ctas * F::kJoinSplit), dim3(kJoinThreads), 0, s, a);
 }
 
 cudaError_t launch_token_attn(const TokenAttnArgs& args, const CUtensorMap* maps, cudaStream_t s) {
@@ -850,7 +863,10 @@ cudaError_t launch_token_attn(const TokenAttnArgs& args, const CUtensorMap* maps
   a.by_G = FastDiv(a.G);
   a.by_H = FastDiv(a.H);
   a.by_item = FastDiv(solo ? a.tp : 2 * a.tp);
-  return solo ? launch<true>(a, maps, s) : launch<false>(a, maps, s);
+  // What no call with these arguments can cut needs no second kernel (337 tokens 16.5 us, with it 18.6).
+  const int64_t blocks = (a.idx ? a.kslots : a.ctx_len ? (a.max_ctx + kBlock - 1) / kBlock : 0) + (a.n_rows + kBlock - 1) / kBlock;
+  const bool joined = (blocks + 1) / 2 > std::min(a.join_tiles, a.cut_tiles / 2);
+  return solo ? launch<true>(a, maps, joined, s) : launch<false>(a, maps, joined, s);
 }
 
 }  // namespace sparda

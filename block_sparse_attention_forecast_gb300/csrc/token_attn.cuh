@@ -235,6 +235,14 @@ struct Segments {
     it.slot = -1;
   }
 
+  // The counter of whole items. In a call it is taken from `total` times in all (each CTA that has a first item goes on
+  // until what it takes is past the last one), and the last time leaves it at zero.
+  __device__ __forceinline__ u32 take() const {
+    u32 u = 0;
+    if (lane == 0) u = atomicInc(a.queue, total - 1);
+    return __shfl_sync(0xffffffffu, u, 0);
+  }
+
   __device__ __forceinline__ bool next(Item& it) {
     u32 off;
     if (per_item > 0) {
@@ -253,11 +261,9 @@ struct Segments {
     }
     if (!split) {
       u32 u = c;
-      if (segments++ > 0) {
-        if (lane == 0) u = n_ctas + atomicAdd(a.queue, 1u);
-        u = __shfl_sync(0xffffffffu, u, 0);
-      }
-      if (u >= total) return false;
+      if (segments++ > 0) u = n_ctas + take();
+      if (u >= total || u < pos) return false;               // (the latter: a workspace that was not zeroed)
+      pos = u;
       const int l = seek(u, off);
       const Entry en = entry(l);
       fill(it, l, en, n_items(a, en) - 1 - (int)off);

@@ -113,6 +113,15 @@ def test_prompt_whole_items_from_the_queue():
     _prompt_case([500, 333, 512, 17, 499, 256, 430, 388], None, 4, 16, seed=3)
 
 
+@pytest.mark.parametrize("lens,G,H", [([3, 9, 14] * 19, 8, 16), ([2, 1] * 40, 8, 1), ([600] * 5, 8, 16)], ids=str)
+def test_prompt_queue_is_left_at_zero(lens, G, H):
+    # more items than run at once: without a call for joining and one query tile or two, and with it
+    ws = None
+    for seed in (5, 6):
+        ws = _prompt_case(lens, None, G, H, seed=seed, ws=ws)
+        assert not ws[:256].any()
+
+
 def test_prompt_few_long_items_are_cut():
     # one group and head: 8 items of up to 16 key tiles and a past of 90 more, shared by all SMs
     _prompt_case([2000], [11500], 1, 1, seed=4)
