@@ -6,7 +6,7 @@
 //   out = sum_u p_u v_u / sum_u p_u,   p_u = 2^((q . k_u - m) log2(e) / sqrt(128)),   m a running maximum
 //
 // A CTA holds the query rows of an item, row (token - first) * H + h of one KV group: two tiles of 128 rows
-// that share every key tile (128 keys: two 64-token blocks) it loads, or, where all rows of a sequence's group fit one
+// that share every key tile (128 keys: two 64-token blocks) it loads, or, where the rows of a sequence's group fit one
 // tile, that tile, and two CTAs run on an SM (kSolo). Either keeps two softmaxes and two accumulators under way for
 // the one tensor pipe:
 //   warp 0, one lane: TMA loads of the query tiles and of each key tile's K and V into a ring of 32 KiB stages;
@@ -840,10 +840,12 @@ static cudaError_t launch(const TokenAttnArgs& a, const CUtensorMap* m, bool joi
 
 cudaError_t launch_token_attn(const TokenAttnArgs& args, const CUtensorMap* maps, cudaStream_t s) {
   TokenAttnArgs a = args;
-  // One tile per CTA where all rows fit it: 64 trees of 4 nodes over 500 tokens 44 us, with a second tile that
-  // takes every other key tile for the same rows 54. Items of more rows read each key tile once for two query
-  // tiles: 32768 tokens 5.4 ms (a tile per CTA 6.1), 64 nodes over 16 x 32768 tokens 415 us (646).
-  const bool solo = a.n_rows <= a.tp;
+  // One tile per CTA where the rows of a sequence's group fit it (of packed prompts, whose lengths only the device knows, the
+  // average): 64 trees of 4 nodes over 500 tokens 44 us, with a second tile that takes every other key tile for the
+  // same rows 54; 64 sequences of one packed token over 32768 317 us, 335 with the second tile empty. Items of more
+  // rows read each key tile once for two query tiles: 32768 tokens 5.4 ms (a tile per CTA 6.1), 64 nodes over
+  // 16 x 32768 tokens 415 us (646).
+  const bool solo = a.n_rows <= (a.cu ? (int64_t)a.tp * (a.n_entries / a.G) : a.tp);
   // Costs in key tiles (about 1.5 us each).
   //   item_tiles: an item's start, first step and output; without them a causal prompt's ranges of many short items
   //     end late (heads of 8192 tokens 240 us, with them 226; 4096 tokens, 16 heads a group, 200 and 149);

@@ -122,6 +122,14 @@ def test_prompt_queue_is_left_at_zero(lens, G, H):
         assert not ws[:256].any()
 
 
+@pytest.mark.parametrize("lens,past,G,H", [([100] + [0, 1] * 20, [700] + [65, 128] * 20, 2, 16), ([1] * 9 + [700], None, 3, 1),
+                                           ([2000] + [5] * 300, None, 1, 16), ([1] * 33, [4096, 1, 0] * 11, 4, 5)],
+                         ids=["turn", "heads of one", "long", "single tokens"])
+def test_prompt_short_sequences_on_average(lens, past, G, H):
+    # one query tile at a time, also for a sequence that is longer than the others
+    _prompt_case(lens, past, G, H, seed=len(lens))
+
+
 def test_prompt_few_long_items_are_cut():
     # one group and head: 8 items of up to 16 key tiles and a past of 90 more, shared by all SMs
     _prompt_case([2000], [11500], 1, 1, seed=4)
