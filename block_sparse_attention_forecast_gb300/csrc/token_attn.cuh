@@ -123,7 +123,8 @@ struct Segments {
   Entry mine;
   int e0;
   u32 pos, end;
-  int segments;        // given out so far
+  int segments;        // given out so far (whole items, equal parts)
+  u32 first, rest;     // key-tile division: the range's start; where its first item ends, if that is left for last
 
   __device__ Segments(const TokenAttnArgs& args, int tokens_per_item, int ln, int cta)
       : a(args), tpi(tokens_per_item), lane(ln), c(cta) {}
@@ -203,10 +204,10 @@ struct Segments {
     if (a.n_entries > 32) fetch();
     weigh();
     segments = 0;
-    pos = end = 0;
+    pos = end = first = rest = 0;
     if (split && c < n_ctas) {
       const Parts parts(total, n_ctas);
-      pos = parts.start(c);
+      pos = first = parts.start(c);
       end = parts.start(c + 1);
     }
   }
@@ -270,7 +271,19 @@ struct Segments {
       it.k0 = 0;
       return true;
     }
-    while (pos < end) {
+    for (;;) {
+      if (pos >= end) {
+        if (rest <= first) return false;
+        pos = first;
+        end = rest;
+        rest = 0;
+        if (e0 > 0) {
+          e0 = 0;
+          base = 0;
+          fetch();
+          weigh();
+        }
+      }
       const int at = seek(pos, off);
       const Entry en = entry(at);
       // the last item with tiles_before <= off, 32 candidates at a time
@@ -291,11 +304,13 @@ struct Segments {
       it.k1 = (int)min((u32)it.nkt, max(left, a.item_tiles) - a.item_tiles);
       pos = it.start + it.nkt;                               // (the next item, if the range goes on)
       if (it.k0 == it.k1) continue;                          // the range ends before its first key tile
-      if (it.k0 > 0 || it.k1 < it.nkt) it.slot = 2 * c + (segments > 0 ? 1 : 0);
-      ++segments;
+      if (it.k0 > 0 && pos < end) {
+        rest = pos;
+        continue;
+      }
+      if (it.k0 > 0 || it.k1 < it.nkt) it.slot = 2 * c + (it.start - a.item_tiles > first ? 1 : 0);
       return true;
     }
-    return false;
   }
 
   // Whether the segment's item is cut, and what this CTA does to join it: all CTAs c1 .. c1+k-1 that have a part
