@@ -1081,8 +1081,9 @@ int32_t run_token_attn(const sparda_shape* s, const sparda_layer_kv* L, const vo
   if (!out || !ws) return SPARDA_ERR_INVALID_ARG;
   if (!aligned(out, 16) || !aligned(ws, 16)) return SPARDA_ERR_MISALIGNED;
   if (ws_bytes < token_workspace_bytes(s, batch)) return SPARDA_ERR_WORKSPACE_TOO_SMALL;
-  // a tensor map's last stride, in bytes, and the entries' count
-  if (rows * (q_stride > kv_stride ? q_stride : kv_stride) >= (int64_t)1 << 39 || (int64_t)batch * G >= (int64_t)1 << 30)
+  // a tensor map's last stride, in bytes, and what lengths on the device can add up to: entries, items in 32 bits
+  if (rows * (q_stride > kv_stride ? q_stride : kv_stride) >= (int64_t)1 << 39 || (int64_t)batch * G >= (int64_t)1 << 30 ||
+      (int64_t)batch * G * (rows / (128 / H) + 1) >= (int64_t)1 << 32)
     return SPARDA_ERR_UNSUPPORTED_SHAPE;
   a.err = dev_error_ptr();
   const int sms = sm_count();

@@ -220,7 +220,6 @@ __global__ void __launch_bounds__(Form<kSolo>::kThreads, Form<kSolo>::kPerSm) to
 
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const int H = a.H, tp = a.tp, tpi = kTiles * tp;
-  grid_dep_launch();
   if (tid == 0) {
     mbar_init(q_full, 1);
     mbar_init(q_empty, 1);
@@ -247,6 +246,7 @@ __global__ void __launch_bounds__(Form<kSolo>::kThreads, Form<kSolo>::kPerSm) to
     tc05::relinquish();
   }
   grid_dep_wait();
+  grid_dep_launch();                                         // (only now: what runs next may not wait for the launch before)
   Segments seg(a, tpi, lane, blockIdx.x);
   if (warp == 2) seg.init(blockIdx.x == 0);
   // query rows that no load fills: zero, once

@@ -107,6 +107,12 @@ def test_layers_lengths_and_paths():
     assert _prompt(n=1 << 24, qs=1 << 30) == sb.ERR_UNSUPPORTED_SHAPE
 
 
+def test_lengths_that_no_counter_holds():
+    # every second sequence may claim all tokens: 2^16 sequences, 2 groups, 41944 items of 25 tokens
+    s = _shape(max_batch=1 << 16)
+    assert _prompt(shape=s, n=1 << 20, batch=1 << 16) == sb.ERR_UNSUPPORTED_SHAPE
+
+
 def test_workspaces():
     s = _shape()
     for kind in (sb.WS_PROMPT, sb.WS_TREE):
