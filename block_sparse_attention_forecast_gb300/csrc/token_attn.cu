@@ -703,7 +703,7 @@ __global__ void __launch_bounds__(Form<kSolo>::kThreads, Form<kSolo>::kPerSm) to
         const int prow = t * kTileRows + r;
         float* part = a.part + (size_t)max(it.slot, 0) * kTiles * kTokenPartFloats;
         const int c0 = 2 * h, c1 = c0 + 2;                   // a warp's columns: half of the tile's
-#pragma unroll 1
+#pragma unroll
         for (int c = c0; c < c1; ++c) {
           float o[32];
           __syncwarp();
