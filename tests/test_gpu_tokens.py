@@ -539,6 +539,35 @@ def test_a_conversation(H):
         assert torch.equal(layer.ck[b, :, :w], full.ck[b, :, :w])
 
 
+def test_store_prompt_and_selection_back_to_back():
+    # a selection reads compressed keys ahead of its wait: what the store before a one-launch prompt wrote is there by then
+    G, H, B, T = 2, 16, 2, 4000
+    g = _gen(77)
+    shape = sb.Shape(n_groups=G, heads_per_group=H, topk=16, max_ctx=4096, max_batch=B)
+    layer = sb.LayerKV.empty(shape)
+    q, k, v = _projection((2 * T,), G, H, g)
+    forecasts = _randn((B, G, D), g)
+    cu, cu_q, seq = _i32([0, T, 2 * T]), _i32([0, 40, 90]), _i32([T, T])
+    out = torch.empty((90, G * H, D), dtype=torch.bfloat16, device=DEV)
+    ws, ws_s = sb.workspace(shape, B, sb.WS_PROMPT), sb.workspace(shape, B, sb.WS_SELECT)
+
+    def run(idx, cnt, between):
+        sb.sparda_prompt_append(shape, layer, k, v, cu, None, B)
+        between()
+        sb.sparda_prompt_attn(shape, q[:90], k[:90], v[:90], cu_q, B, out, ws)
+        between()
+        sb.sparda_forecast_select(shape, layer.ck, forecasts, seq, B, idx, cnt, ws_s)
+
+    want = torch.full((B, G, 18), -7, dtype=torch.int32, device=DEV), torch.zeros((B, G), dtype=torch.int32, device=DEV)
+    run(*want, torch.cuda.synchronize)
+    for _ in range(20):
+        got = torch.full_like(want[0], -7), torch.zeros_like(want[1])
+        layer.ck.fill_(NAN)
+        run(*got, lambda: None)
+        assert torch.equal(got[0], want[0]) and torch.equal(got[1], want[1])
+    assert sb.sparda_device_error() == 0
+
+
 def test_captured_and_replayed_with_other_lengths():
     G, H, B, N = 2, 16, 4, 10
     g = _gen(50)
