@@ -68,10 +68,10 @@ constexpr int kPage = 1024;                                // barriers
 constexpr float kGrow = 8.f;                               // the reference moves when a score passes it by this (log2)
 constexpr float kScaleLog2 = 1.4426950408889634f * 0.08838834764831845f;   // log2(e) / sqrt(128)
 
-// [barriers][query tiles][ring][a float per row]
+// [barriers][query tiles][ring][two floats per row]
 template <bool kSolo>
 constexpr int smem_bytes() {
-  return kPage + Form<kSolo>::kTiles * (kQTile + 4 * kTileRows) + Form<kSolo>::kStages * kStage;
+  return kPage + Form<kSolo>::kTiles * (kQTile + 8 * kTileRows) + Form<kSolo>::kStages * kStage;
 }
 static_assert(smem_bytes<false>() <= 227 * 1024 && 2 * (smem_bytes<true>() + 1024) <= 228 * 1024,
               "the token attention fits shared memory");
@@ -216,7 +216,7 @@ __global__ void __launch_bounds__(Form<kSolo>::kThreads, Form<kSolo>::kPerSm) to
   volatile Work* work = reinterpret_cast<volatile Work*>(smem + 512);
   uint8_t* qs = smem + kPage;
   uint8_t* ring = qs + kTiles * kQTile;
-  float* row_sh = reinterpret_cast<float*>(ring + kStages * kStage);  // [tile][128]: between a row's two threads
+  float* row_sh = reinterpret_cast<float*>(ring + kStages * kStage);  // [tile][2][128]: between a row's two threads
 
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const int H = a.H, tp = a.tp, tpi = kTiles * tp;
@@ -531,7 +531,11 @@ __global__ void __launch_bounds__(Form<kSolo>::kThreads, Form<kSolo>::kPerSm) to
     const uint32_t lane_off = (uint32_t)(quarter * 32) << 16;
     const uint32_t t_s = tmem + 256 * t + lane_off, t_o = t_s + 128;
     const int pair = 1 + 4 * t + quarter;                    // named barrier of the rows' two warps
-    float* other = row_sh + 128 * t + r;
+    // Between the row's two threads: the maximum that moves a reference, and the row's sum. A word each: the reference is
+    // read behind the last barrier of a step, and the segment's end may follow at once with no barrier before its sum.
+    // (Every word is written behind a barrier that follows its last read: the vote of a later step.)
+    float* other = row_sh + 256 * t + r;
+    float* row_sum = other + 128;
     const u64 scale2 = pack2(kScaleLog2, kScaleLog2);
     bool met = false;                                        // both warps of the rows know that a wait ran out
     unsigned n_s = 0, n_o = 0;
@@ -687,11 +691,11 @@ __global__ void __launch_bounds__(Form<kSolo>::kThreads, Form<kSolo>::kPerSm) to
       }
       if (!ok) break;
       // ---- the segment's end: the row's sum, and O complete
-      if (h == 1) *other = l;
+      if (h == 1) *row_sum = l;
       pair_sync(pair);
-      if (h == 0) *other = l += *other;
+      if (h == 0) *row_sum = l += *row_sum;
       pair_sync(pair);
-      l = *other;
+      l = *row_sum;
       ok = warp_wait(&o_full[t], n_o & 1, a.err);
       ++n_o;
       if (ok) {
