@@ -3,7 +3,8 @@ the ordinary, values that are not finite, and rows that two sequences claim."""
 import pytest
 import torch
 
-from tests.test_gpu_tokens import _check, _clean_error_word, _gen, _i32, _layer, _projection, _shape  # noqa: F401
+from tests.test_gpu_tokens import (_check, _clean_error_word, _copy, _gen, _i32, _layer, _projection, _randn, _shape,  # noqa: F401
+                                   _store_check)
 from tests.token_reference import D, ancestors, attend
 
 pytestmark = pytest.mark.gpu
@@ -78,3 +79,27 @@ def test_tree_references_that_move_in_the_last_key_tile(ctx, N, H):
         call(again)
         assert torch.equal(again, out)
     assert sb.sparda_device_error() == 0
+
+
+# ------------------------------------------------------------------------------- stores
+@pytest.mark.parametrize("cu,start", [([0, 4096, 0, 4096], [0, 7, 45]),                      # one refused between two that hold all rows
+                                      ([0, 2000, 100, 2000, 1, 1900, 1900], [64, 0, 1, 0, 31, 5]),
+                                      ([0] + [1000, 3] * 40 + [1000], [b % 70 for b in range(81)])], ids=["two", "three", "forty-one"])
+def test_rows_that_several_sequences_claim(cu, start):
+    """Behind a sequence whose rows do not ascend, later ones may name rows again: every sequence that is not refused is
+    stored whole, however many blocks of the cache that makes, and new_len says so."""
+    G, B, n = 2, len(start), max(cu)
+    g = _gen(B)
+    shape = _shape(G, 3, max(start) + n, B)
+    layer = _layer(shape, g, start)
+    layer.ck.copy_(_randn(layer.ck.shape, g))
+    _, k, v = _projection((n,), G, 3, g)
+    before, new = _copy(layer), _i32([-5] * B)
+    sb.sparda_prompt_append(shape, layer, k, v, _i32(cu), _i32(start), B, new_len=new)
+    assert sb.sparda_device_error() == sb.DEV_BAD_SEQ_LEN
+    good = [cu[b + 1] >= cu[b] for b in range(B)]
+    assert sum(cu[b + 1] - cu[b] for b in range(B) if good[b]) > n
+    for b in range(B):
+        rows = slice(cu[b], cu[b + 1] if good[b] else cu[b])
+        _store_check(layer, before, start[b], k[rows], v[rows], b)
+        assert int(new[b]) == start[b] + rows.stop - rows.start
