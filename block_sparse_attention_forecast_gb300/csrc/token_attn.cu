@@ -702,7 +702,7 @@ __global__ void __launch_bounds__(Form<kSolo>::kThreads, Form<kSolo>::kPerSm) to
         tc05::fence_after();
         const bool live = rt < tp && tok < it.n;
         const size_t row = a.cu ? (size_t)it.row0 + tok : (size_t)it.b * a.n_rows + tok;
-        const float inv = l > 0.f || l != l ? 1.f / l : 0.f;
+        const float inv = 1.f / l;                           // (every token attends itself; l is 0 if all its scores are -inf: NaN)
         __nv_bfloat16* dst = a.out + ((row * a.G + it.g) * H + (r - rt * H)) * kHeadDim;
         const int prow = t * kTileRows + r;
         float* part = a.part + (size_t)max(it.slot, 0) * kTiles * kTokenPartFloats;
@@ -824,7 +824,7 @@ __global__ void __launch_bounds__(kJoinThreads) token_attn_join_kernel(const Tok
       __syncthreads();
     }
     if (!many || warp == 0) {
-      const float inv = s.l > 0.f || s.l != s.l ? 1.f / s.l : 0.f;
+      const float inv = 1.f / s.l;
       uint2* dst = reinterpret_cast<uint2*>(a.out + (((size_t)(j.out_row + tk) * a.G + j.g) * H + h) * kHeadDim);
       dst[quad] = make_uint2(pack_bf16(s.o.x * inv, s.o.y * inv), pack_bf16(s.o.z * inv, s.o.w * inv));
     }

@@ -753,7 +753,8 @@ int32_t sparda_kv4_evict_blocks(const sparda_shape* shape, const sparda_layer_kv
  * tokens up to i. past and past_len NULL: no past. Prompts may be longer than max_ctx (the cache is read
  * only up to past_len). q: bf16 rows of [G*H, d]; k, v: bf16 rows of [G, d]; out: bf16
  * [n_tokens, G*H, d]. 1 <= n_tokens <= 2^24. Tensor cores with bf16 operands and float32 accumulation,
- * float32 softmax, probabilities rounded to bf16 before they meet the values. A value row that is not finite
+ * float32 softmax, probabilities rounded to bf16 before they meet the values. A token with a score of +inf, or none
+ * but -inf, gives NaN, as the formula does. A value row that is not finite
  * reaches, besides the tokens that attend it, those before it in its sequence that are computed beside
  * them (up to 256). workspace: SPARDA_WS_PROMPT. One or two launches.
  */

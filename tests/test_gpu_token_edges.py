@@ -13,6 +13,7 @@ if torch.cuda.is_available():
     import block_sparse_attention_forecast_gb300.binding as sb
 
 DEV = "cuda"
+NAN, INF = float("nan"), float("inf")
 
 
 # ------------------------------------------------------------------------------- references
@@ -103,3 +104,100 @@ def test_rows_that_several_sequences_claim(cu, start):
         rows = slice(cu[b], cu[b + 1] if good[b] else cu[b])
         _store_check(layer, before, start[b], k[rows], v[rows], b)
         assert int(new[b]) == start[b] + rows.stop - rows.start
+
+
+# ------------------------------------------------------------------------------- values that are not finite
+def _formula(q, k, v, on, out, what):
+    """out [n, D] against softmax(q k / sqrt(d)) v where keys may have one infinite channel: a score of -inf leaves its key
+    out, and a row that has a score of +inf, or none but -inf, is NaN."""
+    z = q @ k.T
+    drop = torch.isinf(z)
+    nan = (on & (z == INF)).any(dim=1) | ~(on & ~drop).any(dim=1)
+    finite = torch.isfinite(k).all(dim=1, keepdim=True)
+    want, bound = attend(q, torch.where(finite, k, torch.zeros_like(k)), v, on & ~drop)
+    assert bool(torch.isnan(out[nan]).all()), what
+    _check(out[~nan], want[~nan], bound[~nan], what)
+    return int(nan.sum()), int((~nan).sum())
+
+
+@pytest.mark.parametrize("lens,past,H", [([1, 1], None, 4), ([200, 31, 64], None, 16), ([400], [300], 2), ([5, 3], [6000, 6001], 3)], ids=str)
+@pytest.mark.parametrize("every", [False, True])
+def test_infinite_scores(lens, past, H, every):
+    """Keys with an infinite channel, many in a row, and queries of either sign in it. every: all cached keys, and the new
+    ones but every 50th."""
+    G, B, rows = 1, len(lens), sum(lens)
+    g = _gen(300 + rows)
+    P = past or [0] * B
+    shape = _shape(G, H, max(P + [64]), B)
+    q, k, v = _projection((rows,), G, H, g)
+    q[..., 0] = torch.where(torch.rand(q.shape[:-1], generator=g, device=DEV) < 0.1, 1.0, -1.0).to(torch.bfloat16)
+    q[0, :, 0] = 1.0
+    at = torch.arange(rows, device=DEV)
+    k[(at % 50 != 49) if every else (at % 64 < 40), 0, 0] = INF
+    layer, kw = None, {}
+    if past:
+        layer = _layer(shape, g, past)
+        for b, n in enumerate(past):
+            layer.k[b, :, : n if every else n // 2, 0] = INF
+        kw = dict(past=layer, past_len=_i32(past))
+    cu = [sum(lens[:i]) for i in range(B + 1)]
+    out = torch.full((rows, G * H, D), 7.0, dtype=torch.bfloat16, device=DEV)
+    sb.sparda_prompt_attn(shape, q, k, v, _i32(cu), B, out, sb.workspace(shape, B, sb.WS_PROMPT), **kw)
+    seen = [0, 0]
+    for b, n in enumerate(lens):
+        part = slice(cu[b], cu[b + 1])
+        kk, vv = k[part, 0].double(), v[part, 0].double()
+        if past:
+            kk, vv = torch.cat((layer.k[b, 0, : P[b]].double(), kk)), torch.cat((layer.v[b, 0, : P[b]].double(), vv))
+        on = torch.ones((n, P[b] + n), dtype=torch.bool, device=DEV).tril(P[b])
+        for h in range(H):
+            for i, c in enumerate(_formula(q[part, h].double(), kk, vv, on, out[part, h], "sequence %d head %d" % (b, h))):
+                seen[i] += c
+    assert seen[0] > 0 and (seen[1] > 0 or rows < 10)
+    assert sb.sparda_device_error() == 0
+
+
+def test_tree_of_infinite_scores():
+    G, H, N, ctx = 1, 4, 6, [0, 200]
+    g = _gen(31)
+    shape = _shape(G, H, 256, 2)
+    layer = _layer(shape, g, ctx)
+    layer.k[:, :, :200, 0] = INF
+    q, k, v = _projection((2, N), G, H, g)
+    q[..., 0] = -1.0
+    k[:, [0, 1, 4], :, 0] = INF                                 # the root and two more: node 1 sees none but -inf
+    parent = [-1, 0, 0, 1, 3, -1]
+    out = torch.full((2, N, G * H, D), 7.0, dtype=torch.bfloat16, device=DEV)
+    sb.sparda_tree_attn(shape, layer, q, k, v, _i32([parent] * 2), _i32(ctx), 2, out, sb.workspace(shape, 2, sb.WS_TREE))
+    for b, S in enumerate(ctx):
+        kk, vv = (torch.cat((c[b, 0, :S], x[b, :, 0])).double() for c, x in ((layer.k, k), (layer.v, v)))
+        on = torch.cat((torch.ones((N, S), dtype=torch.bool), ancestors(parent, N)), dim=1).to(DEV)
+        for h in range(H):
+            nan, _ = _formula(q[b, :, h].double(), kk, vv, on, out[b, :, h], "sequence %d head %d" % (b, h))
+            assert nan == 2
+    assert sb.sparda_device_error() == 0
+
+
+def test_attended_nan_and_infinite_values():
+    """A NaN key reaches the rows that attend it, a NaN query its own row, a value its own channel."""
+    G, H, n = 1, 3, 300
+    g = _gen(32)
+    shape = _shape(G, H, 64, 1)
+    q, k, v = _projection((n,), G, H, g)
+    ws = sb.workspace(shape, 1, sb.WS_PROMPT)
+    want, out = (torch.empty((n, G * H, D), dtype=torch.bfloat16, device=DEV) for _ in range(2))
+    call = lambda o: sb.sparda_prompt_attn(shape, q, k, v, _i32([0, n]), 1, o, ws)
+    call(want)
+    k[150, 0, 7], q[80, 1, 9] = NAN, NAN
+    call(out)
+    assert bool(torch.isnan(out[150:]).all()) and bool(torch.isnan(out[80, 1]).all())
+    out[80, 1] = want[80, 1]
+    assert torch.equal(out[:150], want[:150])
+    k[150, 0, 7], q[80, 1, 9] = 0.0, 0.0
+    call(want)
+    v[20, 0, 3], v[90, 0, 4] = INF, NAN
+    call(out)
+    assert bool((out[20:, :, 3] == INF).all()) and bool(torch.isnan(out[90:, :, 4]).all())
+    keep = [c for c in range(D) if c not in (3, 4)]
+    assert torch.equal(out[..., keep], want[..., keep])
+    assert sb.sparda_device_error() == 0
