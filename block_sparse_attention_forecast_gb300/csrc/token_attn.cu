@@ -67,6 +67,11 @@ constexpr int kHalfCols = kStage / 2;
 constexpr int kPage = 1024;                                // barriers
 constexpr float kGrow = 8.f;                               // the reference moves when a score passes it by this (log2)
 constexpr float kScaleLog2 = 1.4426950408889634f * 0.08838834764831845f;   // log2(e) / sqrt(128)
+// The exponent of a probability is one fused operation, score * kScaleLog2 - reference, so it carries the rounding of the
+// reference: the same factor for all keys of a row, which the division by the sum takes out while it is in range (2^16 at
+// most for references below 2^29; twice the exponent with every bit more). Beyond, float32 scores are equal or 2^8 and
+// more apart (2^32 and more as probabilities), and any scale tells which: a power of two, with which the product is exact.
+constexpr float kFar = 536870912.f, kScaleFar = 0.125f;
 
 // [barriers][query tiles][ring][two floats per row]
 template <bool kSolo>
@@ -536,7 +541,6 @@ __global__ void __launch_bounds__(Form<kSolo>::kThreads, Form<kSolo>::kPerSm) to
     // (Every word is written behind a barrier that follows its last read: the vote of a later step.)
     float* other = row_sh + 256 * t + r;
     float* row_sum = other + 128;
-    const u64 scale2 = pack2(kScaleLog2, kScaleLog2);
     bool met = false;                                        // both warps of the rows know that a wait ran out
     unsigned n_s = 0, n_o = 0;
     int tree_b = -1;
@@ -577,7 +581,8 @@ __global__ void __launch_bounds__(Form<kSolo>::kThreads, Form<kSolo>::kPerSm) to
       }
       // key tiles before this one are attended whole by every row of the tile (selected blocks: looked at one by one)
       const int whole = bl.sel ? 0 : (it.P % kBlock ? it.nctx - 1 : it.nctx + (a.parent ? 0 : (tile_tok + 1) / kBlock)) / 2;
-      float m_used = -INFINITY, l = 0.f;
+      float m_used = -INFINITY, l = 0.f;                     // the reference (log2), the sum
+      float scale = kScaleLog2, neg = 0.f;                   // a score's exponent: score * scale + neg
       bool any = false;                                      // this tile has had a step
       for (int p = 0; p < n; ++p) {
         const int blk = 2 * (it.k0 + p) + h;
@@ -617,11 +622,10 @@ __global__ void __launch_bounds__(Form<kSolo>::kThreads, Form<kSolo>::kPerSm) to
             for (int k = 0; k < 4; ++k) m4[k] = fmaxf(m4[k], x[28 + k]);
             mb = max3(mb, fmaxf(m4[0], m4[1]), fmaxf(m4[2], m4[3]));
           }
-          mb *= kScaleLog2;
         }
         // does a maximum move (also at the first key a row sees)?
         if (!ok) fail_sh[pair - 1] = 1;
-        if (pair_any(pair, mb > m_used + kGrow || !ok)) {
+        if (pair_any(pair, mb * kScaleLog2 > m_used + kGrow || !ok)) {
           if (fail_sh[pair - 1]) {                           // in one of the two: both leave
             ok = false;
             met = true;
@@ -631,11 +635,19 @@ __global__ void __launch_bounds__(Form<kSolo>::kThreads, Form<kSolo>::kPerSm) to
           pair_sync(pair);
           if (h == 0) {
             mb = fmaxf(mb, *other);
-            *other = mb > m_used + kGrow ? mb : m_used;
+            *other = mb * kScaleLog2 > m_used + kGrow ? mb : -INFINITY;   // (the latter: it stays)
           }
           pair_sync(pair);
-          const float mn = *other;
-          const float alpha = mn > m_used ? fast_exp2(m_used - mn) : 1.f;
+          const float top = *other;
+          float alpha = 1.f;
+          if (top > -INFINITY) {
+            const float mn = __fmul_rn(top, kScaleLog2);     // (rounded, as neg is: alpha is their quotient)
+            alpha = fast_exp2(m_used - mn);
+            m_used = mn;
+            const bool far = fabsf(mn) >= kFar;
+            scale = far ? kScaleFar : kScaleLog2;
+            neg = far ? -(top * kScaleFar) : -mn;
+          }
           if (any) {                                         // S is there, so the O before it is
             tc05::fence_after();
 #pragma unroll 1
@@ -648,12 +660,10 @@ __global__ void __launch_bounds__(Form<kSolo>::kThreads, Form<kSolo>::kPerSm) to
             }
           }
           l *= alpha;
-          m_used = mn;
         }
         any = true;
         if (there) {
-          const float neg = m_used == -INFINITY ? 0.f : -m_used;
-          const u64 neg2 = pack2(neg, neg);
+          const u64 scale2 = pack2(scale, scale), neg2 = pack2(neg, neg);
           u64 sum2[2] = {0ull, 0ull};
 #pragma unroll 1
           for (int c = 0; c < 2; ++c) {

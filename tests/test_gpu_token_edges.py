@@ -201,3 +201,43 @@ def test_attended_nan_and_infinite_values():
     keep = [c for c in range(D) if c not in (3, 4)]
     assert torch.equal(out[..., keep], want[..., keep])
     assert sb.sparda_device_error() == 0
+
+
+# ------------------------------------------------------------------------------- very large scores
+@pytest.mark.parametrize("sign", [1, -1])
+@pytest.mark.parametrize("size", [2.0**14, 2.0**17, 2.0**38])
+@pytest.mark.parametrize("n,past,H", [(70, 0, 16), (700, 0, 3), (6, 6000, 1)], ids=str)
+def test_scores_far_beyond_the_exponents_of_probabilities(n, past, H, size, sign):
+    """One channel is not zero, so that every score is exact: size^2 (1 + m/128) 2^e. Any two differ by far more than
+    the exponents of float32: a row is the value of its largest key, exactly, or the mean of two values where two keys tie."""
+    G = 1
+    g = _gen(400 + n + past)
+    shape = _shape(G, H, max(64, past), 1)
+    q, k, v = _projection((n,), G, H, g)
+    q.zero_()
+    q[..., 5] = size
+    # distinct keys in a random order (values of bf16); the last one of the whole once more
+    m = torch.arange(past + n, device=DEV)
+    m = m[torch.randperm(past + n, generator=g, device=DEV)]
+    key = (size * (1 + (m % 128) / 128.0) * 2.0 ** (m // 128)).to(torch.bfloat16) * sign
+    k.zero_()
+    layer, kw = None, {}
+    vv = v[:, 0]
+    if past:
+        layer = _layer(shape, g, [past])
+        layer.k.zero_()
+        layer.k[0, 0, :past, 5] = key[:past]
+        kw = dict(past=layer, past_len=_i32([past]))
+        vv = torch.cat((layer.v[0, 0, :past], vv))
+    key[-1] = key[-2]
+    k[:, 0, 5] = key[past:]
+    out = torch.full((n, G * H, D), 7.0, dtype=torch.bfloat16, device=DEV)
+    sb.sparda_prompt_attn(shape, q, k, v, _i32([0, n]), 1, out, sb.workspace(shape, 1, sb.WS_PROMPT), **kw)
+    for i in range(n):
+        seen = key[: past + i + 1].double()
+        top = seen == seen.max()
+        assert 1 <= int(top.sum()) <= 2
+        want = vv[: past + i + 1][top].double().mean(dim=0)
+        # the mean of two bf16 values: their sum in float32 rounds to 2^-24, then one rounding to bf16
+        assert bool(((out[i].double() - want).abs() <= (2.0**-8 + 2.0**-20) * want.abs() * (int(top.sum()) - 1)).all()), i
+    assert sb.sparda_device_error() == 0
