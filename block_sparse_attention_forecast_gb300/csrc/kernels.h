@@ -284,7 +284,7 @@ struct FastDiv {
 
 // A CTA's share in joining one item that was cut (token_attn.cuh); r0 == r1: none
 struct TokenJoin {
-  int c1, k, first_slot, rows, r0, r1, g, out_row;
+  int c1, k, first_slot, r0, r1, g, out_row;
 };
 struct TokenAttnArgs {
   const int32_t* ctx_len;        // [B] tokens in the cache; nullptr: none

@@ -23,7 +23,7 @@
 // S and P never leave the SM, K and V are read once per item, and nothing is written but the output (or a partial
 // result where an item is cut). A long prompt is bound by the tensor pipe and what stands between its MMAs: 32768
 // tokens, 32 heads over 2 groups, 5.4 ms, 1.63 PFLOP/s (0.85 of the measured GEMM rate; 4.9 ms with a softmax that
-// does nothing). A decode step over 16 x 131072 tokens is bound by memory: 0.315 ms, 6.8 TB/s (1.01 of the measured
+// does nothing). A decode step over 16 x 131072 tokens is bound by memory: 0.317 ms, 6.8 TB/s (1.01 of the measured
 // copy rate). What was measured on the way there, for the 32768-token prompt: one thread per row, all S in registers,
 // MMAs issued from a divergent branch 11.0 ms; the issuing warp kept together (uniform registers) 7.5; a look
 // at each barrier before the suspended wait 6.3; a step's bookkeeping cut to counters 5.65; two threads per row
@@ -52,8 +52,8 @@ struct Form {
   static constexpr int kThreads = 128 + 32 * kSoftmaxWarps;
   static constexpr int kPerSm = kSolo ? 2 : 1;
   static constexpr int kStages = kSolo ? 2 : 5;              // of the ring
-  // Blocks of the join per CTA: 256 rows of few parts each to 64 warps (16 trees over 34 blocks 29 us, to 16 warps 33);
-  // 128 rows at most, and twice the CTAs, to 16 (64 trees over 500 tokens 42 us, to 64 warps 45).
+  // Blocks of the join per CTA: 256 rows of few parts each to 64 warps (16 trees over 34 blocks 27 us, to 16 warps 31);
+  // 128 rows at most, and twice the CTAs, to 16 (64 trees over 500 tokens 41 us, to 64 warps 43).
   static constexpr int kJoinSplit = kSolo ? 2 : 8;
   // registers per thread: the softmax warps take what the first warpgroup gives of those at launch
   static constexpr int kRegsLaunch = kSolo ? 80 : 96, kRegsMain = 64, kRegsSoftmax = kSolo ? 88 : 104;
@@ -764,7 +764,7 @@ __global__ void __launch_bounds__(Form<kSolo>::kThreads, Form<kSolo>::kPerSm) to
 // with w_i = 2^(m_i - max m). joins[c] holds what CTA c of the attention is to join: its shares of the rows of at most two
 // items (the one its range began in and the one it ended in). Form::kJoinSplit blocks take a share together: what
 // joining costs is the latency of a few dependent reads, so each thread has as few as may be, and kJoinLoads parts are under
-// way at a time (in turn 16 trees over 34 blocks take 29 us, two at a time 27, eight 30: fewer blocks on an SM). A
+// way at a time (in turn 16 trees over 34 blocks take 29 us, two at a time 27, eight 31: fewer blocks on an SM). A
 // block holds 8 rows of 32 column quads at a time or, for items of many parts, one row whose parts are dealt out to the
 // 8 warps.
 constexpr int kJoinThreads = 256;
@@ -855,20 +855,21 @@ static cudaError_t launch(const TokenAttnArgs& a, const CUtensorMap* m, bool joi
 cudaError_t launch_token_attn(const TokenAttnArgs& args, const CUtensorMap* maps, cudaStream_t s) {
   TokenAttnArgs a = args;
   // One tile per CTA where the rows of a sequence's group fit it (of packed prompts, whose lengths only the device knows, the
-  // average): 64 trees of 4 nodes over 500 tokens 44 us, with a second tile that takes every other key tile for the
-  // same rows 54; 64 sequences of one packed token over 32768 317 us, 335 with the second tile empty. Items of more
-  // rows read each key tile once for two query tiles: 32768 tokens 5.4 ms (a tile per CTA 6.1), 64 nodes over
-  // 16 x 32768 tokens 415 us (646).
+  // average): 64 trees of 4 nodes over 500 tokens 41 us, in the two-tile form, with its second tile empty, 48; 64
+  // sequences of one packed token over 32768 317 us and 331. Items of more rows read each key tile once for two
+  // query tiles: 32768 tokens 5.4 ms (a tile per CTA 6.3), 64 nodes over 16 x 32768 tokens 379 us (480). The average is
+  // that of the rows the call is given: a captured call whose buffers its batches do not fill may take the two-tile form
+  // for short sequences, the second of those times.
   const bool solo = a.n_rows <= (a.cu ? (int64_t)a.tp * (a.n_entries / a.G) : a.tp);
   // Costs in key tiles (about 1.5 us each).
   //   item_tiles: an item's start, first step and output; without them a causal prompt's ranges of many short items
-  //     end late (heads of 8192 tokens 240 us, with them 226; 4096 tokens, 16 heads a group, 200 and 149);
+  //     end late (8192 tokens of 16 single heads 241 us, with them 224);
   //   join_tiles, cut_tiles: a partial result written and read, and a second kernel that waits for the last CTA
-  //     (337 tokens with every item cut 60 us, with none 21; 4096 tokens, 512 items of up to 32 key tiles, cut 149,
-  //     whole 133; 512 items of up to 64, one head a group, cut 226, whole 303);
-  //   seg_tiles: a range's second segment (16 trees over 34 blocks in ranges 33 us, in equal parts 29);
-  //   split_items: items in 4 rounds are dealt out whole (8192 tokens, 1024 items: cut 417 us, whole 408), which
-  //     keeps CTAs that run at one time on the same keys.
+  //     (337 tokens with every item cut 22.6 us, with none 16.4; 4096 tokens, 512 items of up to 32 key tiles, cut 142,
+  //     whole 134; 512 items of up to 64, one head a group, cut 224, whole 300);
+  //   seg_tiles: a range's second segment (16 trees over 34 blocks in ranges 29 us, in equal parts 27);
+  //   split_items: items in 4 rounds are dealt out whole, which leaves no partial results (8192 tokens, 1024 items: whole
+  //     408 to 430 us from run to run, cut 404).
   a.n_ctas *= solo ? 2 : 1;
   a.split_items = 4 * a.n_ctas;
   a.min_tiles = 2;
@@ -879,7 +880,7 @@ cudaError_t launch_token_attn(const TokenAttnArgs& args, const CUtensorMap* maps
   a.by_G = FastDiv(a.G);
   a.by_H = FastDiv(a.H);
   a.by_item = FastDiv(solo ? a.tp : 2 * a.tp);
-  // What no call with these arguments can cut needs no second kernel (337 tokens 16.5 us, with it 18.6).
+  // What no call with these arguments can cut needs no second kernel (337 tokens 16.4 us, with it 18.6).
   const int64_t blocks = (a.idx ? a.kslots : a.ctx_len ? (a.max_ctx + kBlock - 1) / kBlock : 0) + (a.n_rows + kBlock - 1) / kBlock;
   const bool joined = (blocks + 1) / 2 > std::min(a.join_tiles, a.cut_tiles / 2);
   return solo ? launch<true>(a, maps, joined, s) : launch<false>(a, maps, joined, s);

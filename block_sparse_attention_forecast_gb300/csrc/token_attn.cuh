@@ -332,9 +332,9 @@ struct Segments {
       j.first_slot = 2 * c1 + (parts.start(c1) < it.start - a.item_tiles ? 1 : 0);
     }
     j.c1 = c1;
-    j.rows = min(tpi, it.en.n - it.tok0) * a.H;
-    j.r0 = (int)((u32)j.rows * (c - c1) / j.k);
-    j.r1 = (int)((u32)j.rows * (c - c1 + 1) / j.k);
+    const u32 rows = min(tpi, it.en.n - it.tok0) * a.H;
+    j.r0 = (int)(rows * (c - c1) / j.k);
+    j.r1 = (int)(rows * (c - c1 + 1) / j.k);
     const int b = a.by_G.div(it.e);
     j.g = it.e - b * a.G;
     j.out_row = (a.cu ? it.en.row0 : b * a.n_rows) + it.tok0;

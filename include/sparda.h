@@ -71,7 +71,8 @@ extern "C" {
 
 /* bits of the device error word (sparda_device_error) */
 #define SPARDA_DEV_WAIT_TIMEOUT   1   /* a bounded wait on a copy's completion ran out      */
-#define SPARDA_DEV_BAD_SEQ_LEN    2   /* seq_len[b] outside [1, max_ctx]                    */
+#define SPARDA_DEV_BAD_SEQ_LEN    2   /* seq_len[b] outside [1, max_ctx]; of the calls for packed prompts and drafted
+                                       * tokens also a past, a number of rows, nodes or accepted nodes out of range   */
 #define SPARDA_DEV_BAD_INDEX      4   /* a block index outside the sequence's blocks        */
 
 /* workspace kinds for sparda_workspace_bytes */
@@ -735,7 +736,9 @@ int32_t sparda_kv4_evict_blocks(const sparda_shape* shape, const sparda_layer_kv
  * multiple of 8, at least the row's own elements; the sequences' max_nodes rows follow one another).
  * Here seq_len / past_len count the tokens that the cache holds BEFORE the new ones: 0 <= seq_len[b] <=
  * max_ctx. A sequence with a length out of range, or whose rows in cu_len are not ascending within
- * n_tokens, sets SPARDA_DEV_BAD_SEQ_LEN and writes nothing. Rows that belong to no sequence are left
+ * n_tokens, sets SPARDA_DEV_BAD_SEQ_LEN and writes nothing, but for a store's new_len[b], which receives seq_len[b]
+ * as it came. The other sequences are served; where one behind it names rows that an earlier one has, both are,
+ * and those rows of an attention's output may come from either. Rows that belong to no sequence are left
  * as they were. Cache rows at and past seq_len, and rows past a sequence's end, may hold anything. Outputs
  * must not overlap inputs. All pointers 16-byte aligned, index and length arrays 4-byte.
  *
@@ -769,7 +772,7 @@ int32_t sparda_prompt_attn(const sparda_shape* shape, const sparda_layer_kv* pas
  * keys rounded once to bf16, as sparda_append_kv one by one). seq_len NULL: empty caches. new_len
  * (optional, int32 [B], another array than seq_len) receives the new lengths; all layers of a stack
  * append at the same seq_len. A sequence that does not fit max_ctx sets SPARDA_DEV_BAD_SEQ_LEN and stays
- * as it was. Ordering: as sparda_compress_keys, the call must not be the kernel just before a selection
+ * as it was (new_len[b] is then seq_len[b], in range or not). Ordering: as sparda_compress_keys, the call must not be the kernel just before a selection
  * that scores this cache.
  */
 int32_t sparda_prompt_append(const sparda_shape* shape, const sparda_layer_kv* layer, const void* k, const void* v,
