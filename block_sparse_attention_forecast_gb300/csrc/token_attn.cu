@@ -16,7 +16,7 @@
 //       O that reads the P it overwrites, and the completion of S tells that of that O;
 //   warp 2: hands out the segments (token_attn.cuh), through shared memory;
 //   warps 4-19 (kSolo: 4-11), two threads per row (each 64 of a key tile's 128 keys): online softmax. The two agree on a
-//       reference that only moves, and O is only rescaled, when a score passes it by more than 2^8 (log2); any
+//       reference that only moves, and O is only rescaled, when a score passes it by more than 8 (log2); any
 //       reference serves that keeps P in range, since P and its sum are divided by one another. P goes to tensor
 //       memory as bf16 (rounded once; the sum is taken before that, in float32), 32 keys of each half at a
 //       time, so that their O += P V runs while the others are formed.
@@ -69,9 +69,15 @@ constexpr float kGrow = 8.f;                               // the reference move
 constexpr float kScaleLog2 = 1.4426950408889634f * 0.08838834764831845f;   // log2(e) / sqrt(128)
 // The exponent of a probability is one fused operation, score * kScaleLog2 - reference, so it carries the rounding of the
 // reference: the same factor for all keys of a row, which the division by the sum takes out while it is in range (2^16 at
-// most for references below 2^29; twice the exponent with every bit more). Beyond, float32 scores are equal or 2^8 and
-// more apart (2^32 and more as probabilities), and any scale tells which: a power of two, with which the product is exact.
-constexpr float kFar = 536870912.f, kScaleFar = 0.125f;
+// most below 2^29; twice the exponent with every bit more). Beyond, float32 scores are equal or 2^8 and more apart (2^32 as
+// probabilities), and any scale tells which: a power of two, with which products and references are exact. This one
+// keeps the references in the order of the scores. (8 packed prompts 583 us, with one scale for all rows 575; the scale chosen
+// again in every step 581, and the 32768-token prompt 1 % slower; far rows in a loop of their own 613.)
+constexpr float kFar = 536870912.f, kScaleFar = 0.25f;
+__device__ __forceinline__ float reference(float score) {
+  const float r = __fmul_rn(score, kScaleLog2);
+  return fabsf(r) < kFar ? r : score * kScaleFar;
+}
 
 // [barriers][query tiles][ring][two floats per row]
 template <bool kSolo>
@@ -582,7 +588,7 @@ __global__ void __launch_bounds__(Form<kSolo>::kThreads, Form<kSolo>::kPerSm) to
       // key tiles before this one are attended whole by every row of the tile (selected blocks: looked at one by one)
       const int whole = bl.sel ? 0 : (it.P % kBlock ? it.nctx - 1 : it.nctx + (a.parent ? 0 : (tile_tok + 1) / kBlock)) / 2;
       float m_used = -INFINITY, l = 0.f;                     // the reference (log2), the sum
-      float scale = kScaleLog2, neg = 0.f;                   // a score's exponent: score * scale + neg
+      float scale = kScaleFar;                               // the reference's (that of -inf is far)
       bool any = false;                                      // this tile has had a step
       for (int p = 0; p < n; ++p) {
         const int blk = 2 * (it.k0 + p) + h;
@@ -625,7 +631,7 @@ __global__ void __launch_bounds__(Form<kSolo>::kThreads, Form<kSolo>::kPerSm) to
         }
         // does a maximum move (also at the first key a row sees)?
         if (!ok) fail_sh[pair - 1] = 1;
-        if (pair_any(pair, mb * kScaleLog2 > m_used + kGrow || !ok)) {
+        if (pair_any(pair, mb * scale > m_used + kGrow || !ok)) {
           if (fail_sh[pair - 1]) {                           // in one of the two: both leave
             ok = false;
             met = true;
@@ -635,19 +641,11 @@ __global__ void __launch_bounds__(Form<kSolo>::kThreads, Form<kSolo>::kPerSm) to
           pair_sync(pair);
           if (h == 0) {
             mb = fmaxf(mb, *other);
-            *other = mb * kScaleLog2 > m_used + kGrow ? mb : -INFINITY;   // (the latter: it stays)
+            *other = mb * scale > m_used + kGrow ? reference(mb) : m_used;
           }
           pair_sync(pair);
-          const float top = *other;
-          float alpha = 1.f;
-          if (top > -INFINITY) {
-            const float mn = __fmul_rn(top, kScaleLog2);     // (rounded, as neg is: alpha is their quotient)
-            alpha = fast_exp2(m_used - mn);
-            m_used = mn;
-            const bool far = fabsf(mn) >= kFar;
-            scale = far ? kScaleFar : kScaleLog2;
-            neg = far ? -(top * kScaleFar) : -mn;
-          }
+          const float mn = *other;
+          const float alpha = mn > m_used ? fast_exp2(m_used - mn) : 1.f;
           if (any) {                                         // S is there, so the O before it is
             tc05::fence_after();
 #pragma unroll 1
@@ -660,9 +658,12 @@ __global__ void __launch_bounds__(Form<kSolo>::kThreads, Form<kSolo>::kPerSm) to
             }
           }
           l *= alpha;
+          m_used = mn;
+          scale = fabsf(mn) < kFar ? kScaleLog2 : kScaleFar;
         }
         any = true;
         if (there) {
+          const float neg = m_used == -INFINITY ? 0.f : -m_used;
           const u64 scale2 = pack2(scale, scale), neg2 = pack2(neg, neg);
           u64 sum2[2] = {0ull, 0ull};
 #pragma unroll 1

@@ -241,3 +241,44 @@ def test_scores_far_beyond_the_exponents_of_probabilities(n, past, H, size, sign
         # the mean of two bf16 values: their sum in float32 rounds to 2^-24, then one rounding to bf16
         assert bool(((out[i].double() - want).abs() <= (2.0**-8 + 2.0**-20) * want.abs() * (int(top.sum()) - 1)).all()), i
     assert sb.sparda_device_error() == 0
+
+
+@pytest.mark.parametrize("order", ["rising", "falling", "mixed"])
+@pytest.mark.parametrize("exponent", [31, 34, 36, 61])
+@pytest.mark.parametrize("n,past,H", [(200, 0, 3), (4, 9000, 1)], ids=str)
+def test_scores_one_step_of_float32_apart(n, past, H, exponent, order):
+    """Exact scores 2^exponent (1.984375 + j 2^-23), j distinct: their products with log2(e) / sqrt(128) lie in the binade
+    above, where neighbours round to one number. A step is 2^5 and more in log2 (exponent 31), so that a row is the value of
+    its largest key to 2^-30."""
+    G = 1
+    g = _gen(500 + n)
+    shape = _shape(G, H, max(64, past), 1)
+    q, k, v = _projection((n,), G, H, g)
+    total = past + n
+    j = torch.arange(total, device=DEV)
+    if order == "falling":
+        j = j.flip(0)
+    elif order == "mixed":
+        j = j[torch.randperm(total, generator=g, device=DEV)]
+    keys = torch.zeros((total, D), dtype=torch.bfloat16, device=DEV)
+    keys[:, 0] = 1.984375 * 2.0 ** (exponent - 17)
+    keys[:, 1] = (j % 256).float() * 2.0 ** (exponent - 40)
+    keys[:, 2] = (j // 256).float() * 2.0 ** (exponent - 32)
+    q.zero_()
+    q[..., :3] = 2.0**17
+    kw, vv = {}, v[:, 0]
+    if past:
+        layer = _layer(shape, g, [past])
+        layer.k[0, 0, :past] = keys[:past]
+        kw = dict(past=layer, past_len=_i32([past]))
+        vv = torch.cat((layer.v[0, 0, :past], vv))
+    k[:, 0] = keys[past:]
+    score = (keys[:, :3].double() * 2.0**17).sum(dim=1)
+    assert torch.equal(score.float().double(), score) and len(torch.unique(score)) == total
+    out = torch.full((n, G * H, D), 7.0, dtype=torch.bfloat16, device=DEV)
+    sb.sparda_prompt_attn(shape, q, k, v, _i32([0, n]), 1, out, sb.workspace(shape, 1, sb.WS_PROMPT), **kw)
+    for i in range(n):
+        want = vv[int(score[: past + i + 1].argmax())].double()
+        # the other keys together: total * 2^-32 of their values, all below 8; then one rounding to bf16
+        assert bool(((out[i].double() - want).abs() <= (2.0**-8) * want.abs() + total * 2.0**-32 * 16).all()), i
+    assert sb.sparda_device_error() == 0
